@@ -32,6 +32,11 @@
  *    returns TP_OK (0) or a negative tp_status; nothing aborts, prints or
  *    falls back to the CPU. tp_last_error() gives a message for the last
  *    failing call on the calling thread.
+ *  - "Packed" calls take a batch of sequences of different lengths: token rows
+ *    of all sequences back to back, sequence b at rows cu[b]..cu[b+1]-1
+ *    (cu: DEVICE int32 [B + 1], cu[0] = 0, nondecreasing, cu[B] <= T; empty
+ *    sequences are allowed). Lengths and positions stay on the device, so a
+ *    captured CUDA graph replays with other lengths.
  *  - Launching calls require the current device to be compute capability
  *    10.3 (sm_103a); otherwise they return TP_ERR_UNSUPPORTED.
  */
@@ -435,6 +440,112 @@ tp_status tp_stack_decode(tp_stack_t stack, const float* x, float* y, const int3
 tp_status tp_lm_head_forward(tp_plan_t plan, const void* const* head_shards, const float* gamma,
                              const float* x, int32_t T, float* logits, int32_t* device_status,
                              void* stream);
+
+/* Per-row controls of a batch's logits. Every array is DEVICE memory; a NULL
+ * array leaves its control out. */
+typedef struct tp_logit_controls {
+    const int32_t* tokens;      /* the rows' token histories back to back: row t's at
+                                 * cu_tokens[t]..cu_tokens[t+1]-1, prompt first; ids outside
+                                 * 0..org_vocab-1 are passed over */
+    const int32_t* cu_tokens;   /* [T + 1] */
+    const int32_t* n_prompt;    /* [T]: leading prompt tokens of each history (NULL: none); the
+                                 * others are generated ones */
+    const float* repetition;    /* [T]: factor r of tokens in the history (NULL: 1) */
+    const float* presence;      /* [T]: subtracted once from generated tokens (NULL: 0) */
+    const float* frequency;     /* [T]: subtracted per occurrence among the generated (NULL: 0) */
+    const int32_t* bias_ids;    /* the rows' biased tokens back to back */
+    const float* bias_values;   /* added to them; of a token listed twice the last counts */
+    const int32_t* cu_bias;     /* [T + 1] */
+    const uint32_t* mask;       /* [mask_rows][ceil(org_vocab / 32)]: bit v % 32 of word v / 32 is
+                                 * 1 where token v is allowed */
+    const int32_t* mask_row;    /* [T]: the mask row of each row, -1 for none (NULL: row t); a row
+                                 * outside -1..mask_rows-1 counts as none */
+    int32_t mask_rows;
+    int32_t reserved0;          /* must be 0 */
+} tp_logit_controls;
+
+/* Applies a batch's penalties, biases and grammar masks to its logits, as
+ * tp_lm_head_forward writes them (float32 [T, org_vocab]), in this order:
+ *   y = x > 0 ? x / r : x * r         for tokens of the row's history,
+ *   y = y - frequency * c - presence  for tokens with c > 0 generated
+ *                                     occurrences,
+ *   y = y + bias                      for biased tokens,
+ *   y = -inf                          for tokens the row's mask forbids.
+ * out is float32 [T, org_vocab]; out may be the same buffer as logits (only
+ * the entries that a control changes are then written), but must not overlap
+ * it otherwise. Both 4-byte aligned (16 bytes are faster). A cu that decreases
+ * gives an empty list for that row. Deterministic; one launch, no allocation,
+ * no synchronisation.
+ * Errors: TP_ERR_NULL (also a list without its cu or its values),
+ * TP_ERR_INVALID_ARG (no head in the plan, overlap, reserved0), TP_ERR_SHAPE
+ * (T < 1, mask_rows < 0, mask without mask_row and mask_rows < T),
+ * TP_ERR_ALIGN, TP_ERR_UNSUPPORTED, TP_ERR_CUDA. */
+tp_status tp_logits_process(tp_plan_t plan, const float* logits, int32_t T, const tp_logit_controls* c,
+                            float* out, void* stream);
+
+/* ------------------------------------- attention of a packed batch */
+
+/* Causal attention of a packed batch over the shards' KV caches, the form of
+ * step 2 of [MG] How tensor parallelism works for prompts of different
+ * lengths: token row t of sequence b (i = t - cu[b]) is at position
+ * p = pos[b] + i, and for shard r, query head h of its Hq' and KV head h / G
+ * (G = Hq' / Hkv')
+ *   out[r][t][h] = sum_{j <= p} w_j v_j / sum_{j <= p} w_j,
+ *   w_j = exp(q[r][t][h] . k_j / sqrt(d)),
+ * with k_j, v_j row j of kv->k[r], kv->v[r] at [b][h / G]. The caches hold
+ * the rows 0..p already (keys rotated), those of the new tokens included;
+ * rows past a sequence's last token are not used, whatever they hold, and a
+ * row whose position is below 0 or at or past max_kv is written as zeros and
+ * recorded as TP_ERR_CAPACITY in the workspace status word. One new token per
+ * sequence (a decode step of any batch) and whole prompts may be mixed.
+ * q and out are bf16 [tp][T][Hq'][d], 16-byte aligned, not overlapping; pos is
+ * DEVICE int32 [B]. Rows cu[B]..T-1 of out are left as they are. A cu that is
+ * not as described above records TP_ERR_SHAPE in the status word, and out is
+ * left as it is. `workspace` is a tp_workspace_init'ed workspace of the plan
+ * (workspace_bytes or more); calls on one workspace must not overlap on the
+ * GPU. Scores, softmax sums and outputs accumulate in float32; the weights w_j
+ * are rounded to bf16 for the product with v, and out once from float32.
+ * Results are deterministic. No allocation and no synchronisation: the call
+ * may be captured in a CUDA graph.
+ * Errors: TP_ERR_NULL, TP_ERR_INVALID_ARG (no attention block, out overlaps
+ * q), TP_ERR_UNSUPPORTED (not a bf16 plan), TP_ERR_SHAPE (B outside
+ * 1..max_batch, T outside 1..max_tokens), TP_ERR_CAPACITY (workspace too
+ * small), TP_ERR_ALIGN, TP_ERR_CUDA. */
+tp_status tp_attn_packed(tp_plan_t plan, const void* q, const tp_kv_set* kv, const int32_t* cu,
+                         const int32_t* pos, int32_t B, int32_t T, void* out,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* As tp_attn_packed for a batch whose sequences share a prefix: every token
+ * attends to all prefix_len rows of the prefix, then to its own sequence's
+ * cache rows 0..p (so pos counts rows of the sequence's own cache, without the
+ * prefix; keys of both are stored already rotated). prefix->k[r] and
+ * prefix->v[r] are [Hkv'][prefix_rows][d] in the plan dtype, one copy for the
+ * batch, of which rows 0..prefix_len-1 are used. prefix_len = 0 is
+ * tp_attn_packed (prefix may then be NULL). Where the batch's sequences bring
+ * few new tokens each, the prefix's keys and values are read once for all of
+ * them.
+ * Errors: as tp_attn_packed, and TP_ERR_SHAPE (prefix_len < 0, prefix_len +
+ * max_kv beyond int32), TP_ERR_CAPACITY (prefix_len > prefix_rows). */
+tp_status tp_attn_prefix(tp_plan_t plan, const void* q, const tp_kv_set* prefix, int64_t prefix_len,
+                         int64_t prefix_rows, const tp_kv_set* kv, const int32_t* cu, const int32_t* pos,
+                         int32_t B, int32_t T, void* out, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* The block of tp_block_forward (PREFILL) over a packed batch, with an
+ * optional shared prefix: x and y are float32 [T, H] packed rows, K/V of the
+ * new tokens are appended to sequence b's cache at rows pos[b].., and the
+ * attention is tp_attn_prefix's (tp_attn_packed's with prefix_len = 0, prefix
+ * NULL). The rotary position of cache row p is prefix_len + p; prefix keys are
+ * stored rotated at positions 0..prefix_len-1. Rows cu[B]..T-1 of y are left
+ * as they are. Rows at positions outside 0..max_kv-1 append nothing, take no
+ * attention output, and are recorded as TP_ERR_CAPACITY; a malformed cu
+ * records TP_ERR_SHAPE and writes neither y nor the caches.
+ * Errors: as tp_attn_prefix, and TP_ERR_INVALID_ARG (y == x). */
+tp_status tp_block_forward_packed(tp_plan_t plan, const tp_shard_set* w, const tp_kv_set* kv,
+                                  const tp_kv_set* prefix, int64_t prefix_len, int64_t prefix_rows,
+                                  const float* x, float* y, const int32_t* cu, const int32_t* pos,
+                                  int32_t B, int32_t T, void* workspace, size_t workspace_bytes,
+                                  void* stream);
 
 /* Standalone rank-order reduction ([RT] Collective backend abstraction,
  * copy-and-reduce; [MG] Local TP: the add after the copies):

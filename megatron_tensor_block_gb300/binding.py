@@ -71,6 +71,12 @@ class tp_kv_set(C.Structure):
     _fields_ = [("k", _P8), ("v", _P8)]
 
 
+class tp_logit_controls(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "tokens", "cu_tokens", "n_prompt", "repetition", "presence", "frequency", "bias_ids", "bias_values", "cu_bias",
+        "mask", "mask_row")] + [("mask_rows", C.c_int32), ("reserved0", C.c_int32)]
+
+
 class TpError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -113,6 +119,12 @@ def load(path: str | None = None) -> C.CDLL:
         "tp_stack_decode": (I32, [P, VP, VP, VP, I32, VP, C.c_size_t, VP]),
         "tp_lm_head_forward": (I32, [P, C.POINTER(VP), VP, VP, I32, VP, VP, VP]),
         "tp_reduce_partials": (I32, [P, VP, VP, VP, VP, I64, VP]),
+        "tp_attn_packed": (I32, [P, VP, C.POINTER(tp_kv_set), VP, VP, I32, I32, VP, VP, C.c_size_t, VP]),
+        "tp_attn_prefix": (I32, [P, VP, C.POINTER(tp_kv_set), I64, I64, C.POINTER(tp_kv_set), VP, VP, I32, I32, VP, VP,
+                                 C.c_size_t, VP]),
+        "tp_block_forward_packed": (I32, [P, C.POINTER(tp_shard_set), C.POINTER(tp_kv_set), C.POINTER(tp_kv_set), I64,
+                                          I64, VP, VP, VP, VP, I32, I32, VP, C.c_size_t, VP]),
+        "tp_logits_process": (I32, [P, VP, I32, C.POINTER(tp_logit_controls), VP, VP]),
         "tp_get_device_status": (I32, [VP, C.POINTER(I32), VP]),
         "tp_gemm_bf16": (I32, [VP, VP, VP, I64, I64, I64, VP, VP]),
         "tp_gemm_bf16_kn": (I32, [VP, VP, VP, I64, I64, I64, VP, VP]),
@@ -154,10 +166,14 @@ def _stream(s) -> int | None:
 
 
 class Plan:
-    """Owns a ``tp_plan_t``; destroyed with the object."""
+    """Owns a ``tp_plan_t``; destroyed with the object. Keeps the sizes that
+    the packed calls check their tensors against."""
 
-    def __init__(self, handle: int):
+    def __init__(self, handle: int, desc: tp_model_desc):
         self.handle = handle
+        self.info = tp_plan_get_info(self)
+        for n in ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab"):
+            setattr(self, n, int(getattr(desc, n)))
 
     def __del__(self):
         if self.handle and _lib is not None:
@@ -171,7 +187,7 @@ def tp_plan(desc, tp: int) -> Plan:
         desc = tp_model_desc(**desc)
     h = C.c_void_p()
     _check(lib.tp_plan(C.byref(desc), int(tp), C.byref(h)))
-    return Plan(h.value)
+    return Plan(h.value, desc)
 
 
 def tp_plan_get_info(plan: Plan) -> dict:
@@ -305,6 +321,91 @@ def tp_lm_head_forward(plan: Plan, head_shards: list, gamma, x, T: int, logits, 
     arr = (C.c_void_p * len(head_shards))(*[_ptr(t) for t in head_shards])
     _check(load().tp_lm_head_forward(plan.handle, arr, _ptr(gamma), _ptr(x), T, _ptr(logits),
                                      _ptr(device_status), _stream(stream)))
+
+
+def _checked(t, name: str, dtype: str, numel: int) -> int | None:
+    """Address of a tensor argument after the checks that an address alone
+    does not allow: type, contiguity, size, device. Integers pass as they are."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype is not getattr(torch, dtype):
+        raise TypeError(f"{name}: {t.dtype}, expected torch.{dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, expected at least {numel}")
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{t.get_device()}, current device is cuda:{torch.cuda.current_device()}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: not a CUDA tensor")
+    return t.data_ptr()
+
+
+def _kv_checked(plan: Plan, kv, name: str, rows: int) -> tp_kv_set:
+    """``kv = (k list, v list)``; every tensor holds at least ``rows`` rows per KV head."""
+    n = rows * plan.info["hkv_shard"] * plan.head_dim
+    tp = plan.info["tp"]
+    if len(kv[0]) != tp or len(kv[1]) != tp:
+        raise ValueError(f"{name}: expected a K and a V cache for each of {tp} shards")
+    return _kv_set([_checked(t, name, "bfloat16", n) for t in kv[0]], [_checked(t, name, "bfloat16", n) for t in kv[1]])
+
+
+def tp_attn_packed(plan: Plan, q, kv: tuple, cu, pos, B: int, T: int, out, workspace, nbytes: int, stream=None) -> None:
+    """Causal attention of a packed batch: ``q``, ``out`` bf16 ``[tp, T, Hq', d]``, sequence b the rows
+    ``cu[b]..cu[b+1]-1`` at positions ``pos[b]..`` of the caches ``kv = (k list, v list)``."""
+    n = T * plan.n_heads * plan.head_dim
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
+    _check(load().tp_attn_packed(plan.handle, _checked(q, "q", "bfloat16", n), C.byref(kvs),
+                                 _checked(cu, "cu", "int32", B + 1), _checked(pos, "pos", "int32", B), B, T,
+                                 _checked(out, "out", "bfloat16", n), _checked(workspace, "workspace", "uint8", nbytes),
+                                 nbytes, _stream(stream)))
+
+
+def tp_attn_prefix(plan: Plan, q, prefix: tuple, prefix_len: int, prefix_rows: int, kv: tuple, cu, pos, B: int, T: int,
+                   out, workspace, nbytes: int, stream=None) -> None:
+    """``tp_attn_packed`` with a shared prefix ``(k list, v list)`` of ``[Hkv', prefix_rows, d]``, rows
+    ``0..prefix_len-1`` of which every token attends to before its own cache."""
+    n = T * plan.n_heads * plan.head_dim
+    pre = _kv_checked(plan, prefix, "prefix", prefix_rows) if prefix_len else None
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
+    _check(load().tp_attn_prefix(plan.handle, _checked(q, "q", "bfloat16", n), C.byref(pre) if pre is not None else None,
+                                 prefix_len, prefix_rows, C.byref(kvs), _checked(cu, "cu", "int32", B + 1),
+                                 _checked(pos, "pos", "int32", B), B, T, _checked(out, "out", "bfloat16", n),
+                                 _checked(workspace, "workspace", "uint8", nbytes), nbytes, _stream(stream)))
+
+
+def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, B: int, T: int, workspace, nbytes: int,
+                            prefix: tuple | None = None, prefix_len: int = 0, prefix_rows: int = 0, stream=None) -> None:
+    """The PREFILL block over a packed batch (``x``, ``y`` float32 ``[T, H]``), with an optional shared prefix."""
+    pre = _kv_checked(plan, prefix, "prefix", prefix_rows) if prefix_len and prefix is not None else None
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
+    n = T * plan.hidden
+    _check(load().tp_block_forward_packed(plan.handle, C.byref(_shard_set(shards)), C.byref(kvs),
+                                          C.byref(pre) if pre is not None else None, prefix_len, prefix_rows,
+                                          _checked(x, "x", "float32", n), _checked(y, "y", "float32", n),
+                                          _checked(cu, "cu", "int32", B + 1), _checked(pos, "pos", "int32", B), B, T,
+                                          _checked(workspace, "workspace", "uint8", nbytes), nbytes, _stream(stream)))
+
+
+def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=None, n_prompt=None, repetition=None,
+                      presence=None, frequency=None, bias_ids=None, bias_values=None, cu_bias=None, mask=None,
+                      mask_row=None, mask_rows: int | None = None, stream=None) -> None:
+    """Penalties, biases and grammar masks of ``logits`` (float32 ``[T, org_vocab]``) into ``out`` (which may be
+    ``logits``). ``mask`` is int32 ``[mask_rows, ceil(org_vocab / 32)]``, bit 1 = allowed; ``mask_rows`` is taken from a
+    tensor's size where not given."""
+    words = (plan.org_vocab + 31) // 32
+    if mask_rows is None:
+        mask_rows = 0 if mask is None or isinstance(mask, int) else mask.numel() // max(words, 1)
+    c = tp_logit_controls(
+        _checked(tokens, "tokens", "int32", 0), _checked(cu_tokens, "cu_tokens", "int32", T + 1),
+        _checked(n_prompt, "n_prompt", "int32", T), _checked(repetition, "repetition", "float32", T),
+        _checked(presence, "presence", "float32", T), _checked(frequency, "frequency", "float32", T),
+        _checked(bias_ids, "bias_ids", "int32", 0), _checked(bias_values, "bias_values", "float32", 0),
+        _checked(cu_bias, "cu_bias", "int32", T + 1), _checked(mask, "mask", "int32", mask_rows * words),
+        _checked(mask_row, "mask_row", "int32", T), mask_rows, 0)
+    _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", "float32", T * plan.org_vocab), T, C.byref(c),
+                                    _checked(out, "out", "float32", T * plan.org_vocab), _stream(stream)))
 
 
 def tp_reduce_partials(plan: Plan, partials, residual, bias, out, M: int, stream=None) -> None:

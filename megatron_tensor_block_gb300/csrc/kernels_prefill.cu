@@ -224,7 +224,8 @@ __device__ __forceinline__ float fbits(uint32_t u) { return __uint_as_float(u); 
 // next are issued, and the TMA producer runs ahead across tile boundaries.
 // ---------------------------------------------------------------------------
 
-enum TcMode : int { TC_QKV = 0, TC_GATEUP = 1 };
+// TC_QKV_PACKED: as TC_QKV for sequences of different lengths (cu, n_tok)
+enum TcMode : int { TC_QKV = 0, TC_GATEUP = 1, TC_QKV_PACKED = 2 };
 
 struct TcColArgs {
     CUtensorMap ta;                       // normalised activations [copies * T, K], boxes 64 x 128
@@ -236,6 +237,9 @@ struct TcColArgs {
     int hq_s, hkv_s, d, max_kv, ffn_s;
     const float* bias[TP_MAX_SHARDS];
     const int* pos;                       // [B] first new position of each sequence
+    const int* cu;                        // packed: [B + 1] first token row of each sequence
+    const int* n_tok;                     // packed: token rows in use (device)
+    int B;
     const float2* rope;                   // [max_kv][d/2] (cos, sin)
     bf16* q_out;                          // [N][T][hq_s * d]
     void* kcache[TP_MAX_SHARDS];
@@ -263,7 +267,7 @@ template <int MODE>
 __device__ __forceinline__ void col_epilogue(const TcColArgs& g, uint32_t acc, int mt, int nt, int r, int q, int lane,
                                              bool ok) {
     const int t = mt * kTcBM + 32 * q + lane;
-    const bool live = ok && t < g.T;
+    const bool live = ok && t < (MODE == TC_QKV_PACKED ? *g.n_tok : g.T);
     const uint32_t lane_off = (uint32_t)(32 * q) << 16;
     if (MODE == TC_GATEUP) {
         for (int c = 0; c < 4; ++c) {
@@ -292,7 +296,20 @@ __device__ __forceinline__ void col_epilogue(const TcColArgs& g, uint32_t acc, i
         return;
     }
     const int d = g.d, half = d >> 1;
-    const int b = t / g.S, sidx = t - b * g.S;
+    int b, sidx;
+    if (MODE == TC_QKV_PACKED) {
+        b = 0;
+        if (live)
+            for (int lo = 0, hi = g.B - 1; lo <= hi;) {   // the last sequence that begins at or before row t
+                const int m = (lo + hi) >> 1;
+                if (g.cu[m] <= t) b = m, lo = m + 1;
+                else hi = m - 1;
+            }
+        sidx = live ? t - g.cu[b] : 0;
+    } else {
+        b = t / g.S;
+        sidx = t - b * g.S;
+    }
     const int p = live ? g.pos[b] + sidx : 0;
     const bool in_cache = p >= 0 && p < g.max_kv;
     if (live && !in_cache) set_status(g.status, TP_ERR_CAPACITY);
@@ -390,7 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tc_col_kernel(const __grid_cons
                     mbar_arrive_expect_tx(&full[s], kTcStageBytes);
                     unsigned char* st = stages + s * kTcStageBytes;
                     tma_load_2d_keep(st, &g.ta, kb * kTcBK, arow, &full[s]);
-                    if (MODE == TC_QKV) {
+                    if (MODE != TC_GATEUP) {
                         tma_load_2d_keep(st + kTcABytes, &g.tb[r], kb * kTcBK, nt * kTcBN, &full[s]);
                     } else {   // 128 gate rows, then the matching 128 up rows
                         tma_load_2d_keep(st + kTcABytes, &g.tb[r], kb * kTcBK, nt * 128, &full[s]);
@@ -487,6 +504,7 @@ struct TcRowArgs {
     int gn;                               // output-column tiles per group (tile order, below)
     const float* resid;                   // [T][H]
     float* out;                           // [T][H]
+    const int* n_tok;                     // packed batch: token rows in use (device)
     int* status;
 };
 
@@ -506,6 +524,7 @@ __device__ __forceinline__ void row_tile(const TcRowArgs& g, int tile, int& m0, 
     n0 = (c0 + local % gn) * kRowBN;
 }
 
+template <bool PACKED>
 __global__ void __launch_bounds__(kRowThreads, 1) tc_row_kernel(const __grid_constant__ TcRowArgs g) {
     extern __shared__ __align__(1024) unsigned char smem[];
     uint64_t *full, *empty, *extra;
@@ -616,10 +635,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) tc_row_kernel(const __grid_con
             }
             const int t = m0 + 32 * q + lane;
             const int n = n0 + 128 * hf;
-            if (ok && t < g.T && n < g.H) {
+            if (ok && t < (PACKED ? *g.n_tok : g.T) && n < g.H) {
                 const size_t o = (size_t)t * g.H + n;
 #pragma unroll
                 for (int i = 0; i < 128; i += 4) {
+                    if (n + i >= g.H) break;            // H is a multiple of 64: the last half tile may be half full
                     const float4 rv = *reinterpret_cast<const float4*>(g.resid + o + i);
                     *reinterpret_cast<float4*>(g.out + o + i) =
                         make_float4(rv.x + sum[i], rv.y + sum[i + 1], rv.z + sum[i + 2], rv.w + sum[i + 3]);
@@ -683,6 +703,19 @@ __global__ void rope_table_kernel(float2* tab, int max_pos, int half, int d, flo
     const int p = i / half, j = i - p * half;
     float sn, cs;
     sincosf((float)p * exp2f(-(2.0f * j / d) * log2_theta), &sn, &cs);
+    tab[i] = make_float2(cs, sn);
+}
+
+// The table of a packed batch: rows first .. first + n - 1, positions that a
+// shared prefix moves far out. The angle is reduced to one turn in 64 bits: in
+// 32, its error would grow with the position (6e-3 at position 1e5).
+__global__ void rope_table_at_kernel(float2* tab, int n, int half, int d, double log2_theta, int first) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n * half) return;
+    const int p = i / half, j = i - p * half;
+    const double turns = ((double)first + p) * exp2(-(2.0 * j / d) * log2_theta) * 0.15915494309189533577;
+    float sn, cs;
+    sincospif((float)(2.0 * (turns - rint(turns))), &sn, &cs);
     tab[i] = make_float2(cs, sn);
 }
 
@@ -1050,6 +1083,12 @@ cudaError_t launch_rope_table(float2* tab, int max_pos, int d, double log2_theta
     return cudaGetLastError();
 }
 
+cudaError_t launch_rope_table_at(float2* tab, int n, int d, double log2_theta, int first, cudaStream_t s) {
+    const int m = n * (d / 2);
+    rope_table_at_kernel<<<(m + 255) / 256, 256, 0, s>>>(tab, n, d / 2, d, log2_theta, first);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_tc_col(int mode, const PrefillColParams& p, cudaStream_t s) {
     if (p.T <= 0) return cudaSuccess;
     TcColArgs g;
@@ -1057,7 +1096,7 @@ cudaError_t launch_tc_col(int mode, const PrefillColParams& p, cudaStream_t s) {
     const int copies = p.a_copies > 1 ? p.N : 1;
     cudaError_t e = tensor_map_2d(p.A, p.K, (long)copies * p.T, kTcBK, kTcBM, 1, &g.ta);
     for (int r = 0; r < p.N && e == cudaSuccess; ++r)
-        e = tensor_map_2d(p.W[r], p.K, p.rows, kTcBK, mode == TC_QKV ? kTcBN : 128, 1, &g.tb[r]);
+        e = tensor_map_2d(p.W[r], p.K, p.rows, kTcBK, mode == TC_GATEUP ? 128 : kTcBN, 1, &g.tb[r]);
     if (e != cudaSuccess) return e;
     g.a_row_stride = copies > 1 ? p.T : 0;
     g.T = p.T;
@@ -1074,20 +1113,24 @@ cudaError_t launch_tc_col(int mode, const PrefillColParams& p, cudaStream_t s) {
         g.vcache[r] = p.vcache[r];
     }
     g.pos = p.pos;
+    g.cu = p.cu;
+    g.n_tok = p.n_tok;
+    g.B = p.B;
     g.rope = p.rope;
     g.q_out = static_cast<bf16*>(p.q_out);
     g.act = static_cast<bf16*>(p.act);
     g.status = p.status;
-    static bool set[2] = {false, false};
-    const void* fn = mode == TC_QKV ? reinterpret_cast<const void*>(tc_col_kernel<TC_QKV>)
-                                    : reinterpret_cast<const void*>(tc_col_kernel<TC_GATEUP>);
+    static bool set[3] = {false, false, false};
+    const void* fn = mode == TC_QKV          ? reinterpret_cast<const void*>(tc_col_kernel<TC_QKV>)
+                     : mode == TC_QKV_PACKED ? reinterpret_cast<const void*>(tc_col_kernel<TC_QKV_PACKED>)
+                                             : reinterpret_cast<const void*>(tc_col_kernel<TC_GATEUP>);
     if (!set[mode]) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
         if (e != cudaSuccess) return e;
         set[mode] = true;
     }
     g.n_mt = (p.T + kTcBM - 1) / kTcBM;
-    g.n_nt = mode == TC_QKV ? (p.rows + kTcBN - 1) / kTcBN : (p.ffn_s + 127) / 128;
+    g.n_nt = mode == TC_GATEUP ? (p.ffn_s + 127) / 128 : (p.rows + kTcBN - 1) / kTcBN;
     g.N = p.N;
     // token tiles per group: about kColGroupMB of activations per group, every copy counted
     const long tile_bytes = (long)kTcBM * p.K * 2 * copies;
@@ -1114,11 +1157,14 @@ cudaError_t launch_tc_row(const PrefillRowParams& p, cudaStream_t s) {
     g.resid = p.resid;
     g.out = p.out;
     g.status = p.status;
-    static bool set = false;
-    if (!set) {
-        e = cudaFuncSetAttribute(tc_row_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
+    g.n_tok = p.n_tok;
+    static bool set[2] = {false, false};
+    const int packed = p.n_tok != nullptr;
+    if (!set[packed]) {
+        e = cudaFuncSetAttribute(packed ? tc_row_kernel<true> : tc_row_kernel<false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kRowSmem);
         if (e != cudaSuccess) return e;
-        set = true;
+        set[packed] = true;
     }
     g.n_mt = (p.T + kTcBM - 1) / kTcBM;
     g.n_nt = (p.H + kRowBN - 1) / kRowBN;
@@ -1128,7 +1174,8 @@ cudaError_t launch_tc_row(const PrefillRowParams& p, cudaStream_t s) {
     const long tiles = (long)g.n_mt * g.n_nt;
     if (tiles > INT32_MAX) return cudaErrorInvalidConfiguration;
     const int grid = tiles < kSMs ? (int)tiles : kSMs;
-    tc_row_kernel<<<grid, kRowThreads, kRowSmem, s>>>(g);
+    if (packed) tc_row_kernel<true><<<grid, kRowThreads, kRowSmem, s>>>(g);
+    else tc_row_kernel<false><<<grid, kRowThreads, kRowSmem, s>>>(g);
     return cudaGetLastError();
 }
 

@@ -182,6 +182,9 @@ struct PrefillColParams {
     int hq_s, hkv_s, d, max_kv, ffn_s;
     const float* bias[TP_MAX_SHARDS];
     const int* pos;
+    const int* cu;                        // packed batch (mode 2): [B + 1], and the token rows in use (device)
+    const int* n_tok;
+    int B;
     const float2* rope;
     void* q_out;                          // [N][T][hq_s d] bf16
     void* kcache[TP_MAX_SHARDS];
@@ -195,6 +198,7 @@ struct PrefillRowParams {
     int N, T, Kr, H;
     const float* resid;
     float* out;
+    const int* n_tok;                     // packed batch: token rows in use (device); NULL: all T
     int* status;
 };
 struct FlashParams {
@@ -212,7 +216,10 @@ struct FlashParams {
 cudaError_t launch_prefill_norm(const float* x, const float* const* gammas, int n_copies, void* out, int T, int H,
                                 float eps, cudaStream_t s);
 cudaError_t launch_rope_table(float2* tab, int max_pos, int d, double log2_theta, cudaStream_t s);
-cudaError_t launch_tc_col(int mode, const PrefillColParams& p, cudaStream_t s);   // 0: QKV, 1: gate/up
+// Row i: the rotation of position first + i, of which a packed batch may have far ones.
+cudaError_t launch_rope_table_at(float2* tab, int n, int d, double log2_theta, int first, cudaStream_t s);
+// mode 0: QKV, 1: gate/up, 2: QKV of a packed batch
+cudaError_t launch_tc_col(int mode, const PrefillColParams& p, cudaStream_t s);
 cudaError_t launch_tc_row(const PrefillRowParams& p, cudaStream_t s);
 cudaError_t launch_flash_prefill(const FlashParams& p, cudaStream_t s);
 
@@ -317,6 +324,52 @@ struct HeadArgs {
 // Picks the stage geometry of `a` (H set) for smem_max bytes; returns the launch's shared-memory bytes.
 size_t head_smem(HeadArgs& a, int smem_max);
 cudaError_t launch_lm_head(const HeadArgs& a, size_t smem, cudaStream_t s);
+
+// Attention of a packed batch (kernels_attn.cu).
+struct AttnCtl {
+    int n_tokens;                         // cu[B], or 0 where cu is malformed
+    int reserved[15];
+};
+struct RaggedAttnParams {
+    const void* q;                        // [N][T][hq_s d] bf16
+    void* out;                            // as q
+    const void* kc[TP_MAX_SHARDS];        // caches [max_batch][hkv_s][max_kv][d]
+    const void* vc[TP_MAX_SHARDS];
+    const void* pk[TP_MAX_SHARDS];        // shared prefix [hkv_s][prefix_rows][d] (prefix_len > 0)
+    const void* pv[TP_MAX_SHARDS];
+    int prefix_len;
+    int64_t prefix_rows;
+    const int* cu;                        // [B + 1]
+    const int* pos;                       // [B] row of each sequence's first new token
+    int N, B, T, hq_s, hkv_s, d, max_kv, max_batch;
+    float scale_log2;                     // log2(e) / sqrt(d)
+    int* status;
+    AttnCtl* ctl;                         // workspace
+};
+// Checks cu and pos and fills ctl; every other kernel of a packed batch reads ctl.
+cudaError_t launch_attn_check(const RaggedAttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s);
+
+// Per-row controls of a batch's logits (kernels_logits.cu).
+struct LogitArgs {
+    const float* x;                       // [T][V]
+    float* y;                             // [T][V], x itself or apart from it
+    int T, V, slices;
+    int vec;                              // x and y are 16-byte aligned
+    const int* tokens;
+    const int* cu_tokens;
+    const int* n_prompt;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int* bias_ids;
+    const float* bias_values;
+    const int* cu_bias;
+    const uint32_t* mask;
+    const int* mask_row;
+    int mask_rows, mask_words;
+};
+cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
 // launchers (return the launch's cudaError_t)
 cudaError_t launch_gemv(const GemvParams& p, int epi, int dtype, cudaStream_t s);

@@ -169,6 +169,23 @@ class Model:
         B.tp_stack_decode(self.stack(), x, y, self.pos, self.w.batch, self.ws.buf, self.ws.nbytes, stream)
         return y
 
+    def forward_packed(self, x, y, cu, pos, prefix=None, prefix_len=0, prefix_rows=0, stream=None):
+        """Runs every layer over a packed batch (rows ``cu[b]..cu[b+1]-1`` of
+        ``x`` are sequence b's, at positions ``pos[b]..`` of its cache);
+        ``prefix``: per layer a shared prefix's (k list, v list), or None."""
+        n, cur, B_ = len(self.layers), x, pos.numel()
+        tmp = _torch().empty_like(y) if n > 1 else None
+        if tmp is not None and stream is not None:      # freed on return: not before the kernels on `stream` are done
+            cuda = _torch().cuda
+            tmp.record_stream(cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        for i, L in enumerate(self.layers):
+            out = y if (n - 1 - i) % 2 == 0 else tmp
+            B.tp_block_forward_packed(self.plan, L.shards, (self.caches[i].k, self.caches[i].v), cur, out, cu, pos, B_,
+                                      x.shape[0], self.ws.buf, self.ws.nbytes, prefix[i] if prefix else None,
+                                      prefix_len, prefix_rows, stream)
+            cur = out
+        return y
+
     def forward(self, x=None, y=None, stream=None):
         """Runs every layer; returns the output tensor."""
         x = self.x if x is None else x
