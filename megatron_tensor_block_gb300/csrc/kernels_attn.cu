@@ -1,99 +1,915 @@
 // Attention of a packed batch over the shards' KV caches, with an optional
 // prefix that the batch shares.
+//
+//   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
+//
+// in one pass over the keys with a running m and sum, three launches:
+//   attn_plan_kernel     one CTA turns the offsets and lengths into a list of
+//                        items, longest first, and cuts long items into parts
+//                        where the batch has too few of them for the machine;
+//   attn_items_kernel    persistent, one CTA per SM, on the tensor cores;
+//   attn_combine_kernel  joins the parts of a row.
+// A call whose sequences bring few tokens each treats a shared prefix as items
+// of its own, whose rows are the batch's tokens whatever their sequence: its
+// keys are read once for the batch. Otherwise the prefix's blocks precede the
+// sequence's own in the item's list of key blocks.
 #include <climits>
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "stream.cuh"
+#include "tcgen05.cuh"
 #include "tp_internal.h"
 
 namespace tpk {
 
-// Checks the batch's offsets and positions: ctl->n_tokens = cu[B], or 0 with
-// TP_ERR_SHAPE in the status word where cu is malformed; TP_ERR_CAPACITY where
-// a token's position is outside the cache.
-__global__ void __launch_bounds__(256) attn_check_kernel(const RaggedAttnParams p) {
+constexpr int kAtM = 128;               // query rows per tile: 128 / G tokens of the G heads of a KV head
+constexpr int kAtK = 128;               // keys per block
+constexpr int kAtBuckets = 512;         // item lengths told apart when sorting
+constexpr int kAtMinPart = 2;           // blocks of the shortest part worth its join
+
+enum AttnKind : int { AT_PREFIX = 1, AT_OWN = 2 };   // key blocks of an item: the prefix's, the sequence's own
+
+// blocks of a sequence's own cache that a tile ending at position `end` (exclusive) needs
+__device__ __forceinline__ int own_blocks(int64_t end, int max_kv) {
+    const int64_t e = end < 0 ? 0 : (end > max_kv ? max_kv : end);
+    return (int)((e + kAtK - 1) / kAtK);
+}
+
+// Splits `nb` blocks into parts of at most `len` blocks each when nb exceeds it by half.
+__device__ __forceinline__ void part_split(int nb, int target, int& parts, int& len) {
+    parts = 1;
+    len = nb;
+    if (nb > target + target / 2) {
+        parts = (nb + target - 1) / target;
+        len = (nb + parts - 1) / parts;
+        parts = (nb + len - 1) / len;
+    }
+}
+
+// One CTA. Three passes over the tiles: count the blocks, count the items of
+// each length, place them. Every lane takes a sequence; a warp takes the tiles
+// of a long sequence together. Integer atomics place items and rows of
+// partial results: their order decides where a partial lies, not what is
+// added to what.
+__global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams p) {
+    __shared__ int s_hist[kAtBuckets];
+    __shared__ unsigned long long s_work;
+    __shared__ int s_rows, s_groups, s_chunks, s_warp[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();
+    for (int i = tid; i < kAtBuckets; i += 1024) s_hist[i] = 0;
+    if (tid == 0) {
+        s_work = 0;
+        s_rows = s_groups = s_chunks = 0;
+    }
     pdl_wait();
+    const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G);            // tokens per item
+    const int heads = p.N * p.hkv_s;
+    const int n_prefix = (p.prefix_len + kAtK - 1) / kAtK;           // prefix blocks
+    const int in_item = p.shared ? 0 : n_prefix;
     int bad = 0, out = 0;
-    for (int b = threadIdx.x; b < p.B; b += 256) {
+    __syncthreads();
+
+    auto visit = [&](auto&& tile) {
+        for (int b0 = warp * 32; b0 < p.B; b0 += 1024) {
+            const int b = b0 + lane;
+            int c0 = 0, n = 0, pos = 0;
+            if (b < p.B) {
+                c0 = p.cu[b];
+                n = p.cu[b + 1] - c0;
+                pos = p.pos[b];
+            }
+            if (n > 0 && n <= per) tile(b, c0, n, pos);
+            for (unsigned m = __ballot_sync(0xffffffffu, n > per); m; m &= m - 1) {
+                const int l = __ffs(m) - 1;
+                const int bl = b0 + l, cl = __shfl_sync(0xffffffffu, c0, l), nl = __shfl_sync(0xffffffffu, n, l),
+                          pl = __shfl_sync(0xffffffffu, pos, l);
+                for (int64_t i = (int64_t)lane * per; i < nl; i += 32 * per)
+                    tile(bl, cl + (int)i, min(per, nl - (int)i), pl + (int)i);
+            }
+        }
+    };
+
+    for (int b = tid; b < p.B; b += 1024) {
         const int c0 = p.cu[b], c1 = p.cu[b + 1];
         if (c1 < c0 || c0 < 0 || c1 > p.T || (b == 0 && c0 != 0)) bad = 1;
         else if (c1 > c0 && (p.pos[b] < 0 || (int64_t)p.pos[b] + (c1 - c0) > p.max_kv)) out = 1;
     }
     bad = __syncthreads_or(bad);
     out = __syncthreads_or(out);
-    if (threadIdx.x == 0) {
-        p.ctl->n_tokens = bad ? 0 : p.cu[p.B];
-        if (bad) set_status(p.status, TP_ERR_SHAPE);
-        else if (out) set_status(p.status, TP_ERR_CAPACITY);
+    if (bad) {
+        if (tid == 0) {
+            AttnCtl c = {};
+            *p.ctl = c;
+            set_status(p.status, TP_ERR_SHAPE);
+        }
+        return;
     }
-}
+    const int n_tok = p.cu[p.B];
+    const int prefix_tiles = p.shared ? (n_tok + per - 1) / per : 0;
 
-// One warp per (shard, token, query head); a lane takes one key of 32 for the
-// scores and D / 32 output elements for the sums.
-template <int D>
-__global__ void __launch_bounds__(256) attn_rows_kernel(const RaggedAttnParams p) {
-    __shared__ float sq[8][D];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * 8 + w;
-    const int h = (int)(unit % p.hq_s);
-    const int t = (int)(unit / p.hq_s % p.T), r = (int)(unit / p.hq_s / p.T);
-    pdl_wait();
-    if (r >= p.N || t >= p.ctl->n_tokens) return;
-    int b = 0;
-    for (int lo = 0, hi = p.B - 1; lo <= hi;) {          // the last b with cu[b] <= t
-        const int m = (lo + hi) >> 1;
-        if (p.cu[m] <= t) b = m, lo = m + 1;
-        else hi = m - 1;
+    unsigned long long work = 0;
+    visit([&](int, int, int n, int pos) { work += in_item + own_blocks((int64_t)pos + n, p.max_kv); });
+    if (tid == 0) work += (unsigned long long)prefix_tiles * n_prefix;
+    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+    if (lane == 0 && work) atomicAdd(&s_work, work);
+    __syncthreads();
+    // parts of an even share of all blocks or shorter: between one and two rounds of the SMs
+    const long long share = (long long)((s_work * heads * 2 + 3 * kSMs - 1) / (3 * kSMs));
+    const int target = (int)min((long long)INT_MAX / 4, max((long long)kAtMinPart, share));
+
+    auto bucket = [&](int nb) { return kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
+    auto count = [&](int nb) {
+        int parts, len;
+        part_split(nb, target, parts, len);
+        if (parts > 1) atomicAdd(&s_hist[bucket(len)], parts - 1);
+        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len)], 1);
+    };
+    visit([&](int, int, int n, int pos) { count(in_item + own_blocks((int64_t)pos + n, p.max_kv)); });
+    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix);
+    __syncthreads();
+    // exclusive scan of the buckets (16 warps of 32)
+    int mine = tid < kAtBuckets ? s_hist[tid] : 0, incl = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
     }
-    const int64_t pos = (int64_t)p.pos[b] + (t - p.cu[b]);
-    const bool in = pos >= 0 && pos < p.max_kv;
-    const int kvh = h / (p.hq_s / p.hkv_s);
-    const bf16* q = static_cast<const bf16*>(p.q) + (((int64_t)r * p.T + t) * p.hq_s + h) * D;
-    for (int i = lane; i < D; i += 32) sq[w][i] = __bfloat162float(q[i]) * p.scale_log2;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    auto run = [&](const bf16* k, const bf16* v, int64_t n) {
-        for (int64_t j0 = 0; j0 < n; j0 += 32) {
-            float s = -INFINITY;
-            if (j0 + lane < n) {
-                s = 0.f;
-                for (int i = 0; i < D; ++i) s = fmaf(sq[w][i], __bfloat162float(k[(j0 + lane) * D + i]), s);
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < kAtBuckets / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    if (tid < kAtBuckets) s_hist[tid] = before + incl - mine;
+    __syncthreads();
+
+    auto place = [&](int kind, int b, int t0, int n, int pos, int nb, int group) {
+        int parts, len;
+        part_split(nb, target, parts, len);
+        int row = -1;
+        if (parts > 1 || p.shared) {
+            row = atomicAdd(&s_rows, parts * heads * n * G);
+            if (kind & AT_OWN) {
+                const int g = atomicAdd(&s_groups, 1), chunks = (n * G + 7) / 8, c = atomicAdd(&s_chunks, chunks);
+                p.groups[g] = AttnGroup{t0, n, pos, row, parts, 0, 0, 0};
+                for (int i = 0; i < chunks; ++i) p.chunks[c + i] = g * 32 + i;
+            } else {
+                p.prefix_groups[group] = make_int2(row, parts);
             }
-            const float mn = fmaxf(m, warp_max(s)), alpha = exp2f(m - mn), e = j0 + lane < n ? exp2f(s - mn) : 0.f;
-            m = mn;
-            l = l * alpha + warp_sum(e);
-            for (int i = 0; i < D / 32; ++i) o[i] *= alpha;
-            for (int j = 0; j < 32 && j0 + j < n; ++j) {
-                const float pj = __shfl_sync(0xffffffffu, e, j);
-                for (int i = 0; i < D / 32; ++i) o[i] = fmaf(pj, __bfloat162float(v[(j0 + j) * D + lane + 32 * i]), o[i]);
-            }
+        }
+        for (int i = 0; i < parts; ++i) {
+            const int k0 = i * len, k1 = min(nb, k0 + len);
+            const int e = atomicAdd(&s_hist[bucket(k1 - k0)], 1);
+            p.items[e] = AttnItem{t0, n, b, pos, k0, k1, kind, row < 0 ? -1 : row + i * heads * n * G};
         }
     };
-    if (in) {
-        if (p.prefix_len) {
-            const int64_t off = (int64_t)kvh * p.prefix_rows * D;
-            run(static_cast<const bf16*>(p.pk[r]) + off, static_cast<const bf16*>(p.pv[r]) + off, p.prefix_len);
-        }
-        const int64_t off = ((int64_t)b * p.hkv_s + kvh) * p.max_kv * D;
-        run(static_cast<const bf16*>(p.kc[r]) + off, static_cast<const bf16*>(p.vc[r]) + off, pos + 1);
+    visit([&](int b, int t0, int n, int pos) {
+        place(p.shared ? AT_OWN : AT_OWN | AT_PREFIX, b, t0, n, pos, in_item + own_blocks((int64_t)pos + n, p.max_kv), 0);
+    });
+    for (int i = tid; i < prefix_tiles; i += 1024)
+        place(AT_PREFIX, 0, i * per, min(per, n_tok - i * per), 0, n_prefix, i);
+    __syncthreads();
+    if (tid == 0) {
+        AttnCtl c = {};
+        c.n_tokens = n_tok;
+        c.n_items = total;
+        c.n_groups = s_groups;
+        c.n_chunks = s_chunks;
+        *p.ctl = c;
+        if (out) set_status(p.status, TP_ERR_CAPACITY);
     }
-    bf16* out = static_cast<bf16*>(p.out) + (((int64_t)r * p.T + t) * p.hq_s + h) * D;
-    for (int i = 0; i < D / 32; ++i) out[lane + 32 * i] = __float2bfloat16_rn(in ? o[i] / l : 0.f);
 }
 
-cudaError_t launch_attn_check(const RaggedAttnParams& p, cudaStream_t s) {
+// ---------------------------------------------------------------------------
+// The items on the tensor cores. An item is two tiles of 128 query rows (the
+// G heads of a KV head for 128 / G consecutive tokens each) over a range of
+// key blocks; both tiles use every block that is loaded.
+//   warp 0        TMA: the Q tiles, then K and V blocks of 128 keys, in the
+//                 order in which they are used, into a ring of slots;
+//   warp 1        tensor memory (S_0, S_1, O_0, O_1) and the MMAs: S_t = Q_t K^T;
+//                 O_t += P_t V with P_t read from tensor memory (bf16, over
+//                 S_t). While one tile's softmax runs, the other's products do,
+//                 and the next item's S_t is issued behind this item's last O_t;
+//   warps 4-7,    softmax of tile 0 and 1, one row per thread: masked maximum,
+//   8-11          P = 2^(S - m) rounded to bf16 (its sum is taken before), m
+//                 moving only when a row's maximum grows by more than 2^8
+//                 (O is then rescaled; a weight of 2^8 is as exact in bf16 and
+//                 float32 as one of 1);
+//   warps 12-15   V blocks that some row of the item does not see to their end
+//                 are made finite before their product (0 * inf is not 0), and
+//                 the results O / l (or O, m and l of a part) are written while
+//                 the next item is under way.
+// The items' ranges of blocks are walked in the same order by every role; all
+// waits are bounded.
+// ---------------------------------------------------------------------------
+
+constexpr int kAtThreads = 512;
+constexpr float kAtRescale = 8.0f;
+constexpr int kAtRegsIo = 64, kAtRegsSoftmax = 184, kAtRegsOut = 80;
+static_assert(kAtRegsIo + 2 * kAtRegsSoftmax + kAtRegsOut <= 4 * 128, "the launch's registers");
+
+template <int D>
+struct AtShape {
+    static constexpr int NKB = D / 64;
+    static constexpr int QB = kAtM * D * 2;             // one Q tile
+    static constexpr int KB = kAtK * D * 2;             // one K or V block
+    static constexpr int RING = D == 128 ? 5 : 10;
+    static constexpr int HEAD = 1024;                   // barriers
+    static constexpr int STAT = 2 * kAtM * 8;           // (m, l) of the tiles' rows
+    static constexpr int SMEM = HEAD + 2 * QB + RING * KB + STAT;
+};
+
+struct AtArgs {
+    CUtensorMap tq;                       // q as [N T][hq_s][D], boxes of 128 / G tokens x G heads x 64
+    CUtensorMap tk[TP_MAX_SHARDS];        // caches as [max_batch hkv_s][max_kv][D], boxes of 128 rows x 64
+    CUtensorMap tv[TP_MAX_SHARDS];
+    CUtensorMap pk[TP_MAX_SHARDS];        // prefix as [hkv_s][prefix_len][D] (rows past it read as zeros)
+    CUtensorMap pv[TP_MAX_SHARDS];
+    const bf16* v[TP_MAX_SHARDS];
+    bf16* out;                            // [N][T][hq_s][D]
+    float* part_o;                        // [rows][D]
+    float2* part_ml;                      // [rows] (m, l)
+    const AttnItem* items;
+    const AttnCtl* ctl;
+    int N, T, hq_s, hkv_s, G, tpt, max_kv, prefix_len;
+    float scale_log2;
+    int* status;
+};
+
+__device__ __forceinline__ uint64_t at_desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
+
+// One item for one KV head of one shard. nb[t]: key blocks of tile t.
+struct AtWork {
+    int r, kvh, h;                        // shard, KV head of the shard, KV head of all
+    int t0, ntok, b, qpos, blk0, part;
+    int nP, nt, nb0, nb1, nb;             // prefix blocks in the list, tiles, blocks of the tiles and of both
+};
+
+// The CTA's k-th item: rounds of the grid run alternately up and down the
+// sorted list, which evens out what the CTAs get.
+__device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWork& w) {
+    const int P = gridDim.x, c = blockIdx.x;
+    const int64_t idx64 = (int64_t)k * P + ((k & 1) ? P - 1 - c : c);
+    if ((int64_t)k * P >= total) return false;
+    if (idx64 >= total) {
+        w.nb = w.nt = w.nb0 = w.nb1 = w.ntok = w.qpos = 0;
+        return true;                                     // nothing in this round
+    }
+    const int idx = (int)idx64, heads = a.N * a.hkv_s, e = idx / heads;
+    const int4 x = __ldg(reinterpret_cast<const int4*>(a.items + e)), y = __ldg(reinterpret_cast<const int4*>(a.items + e) + 1);
+    w.h = idx - e * heads;
+    w.r = w.h / a.hkv_s;
+    w.kvh = w.h - w.r * a.hkv_s;
+    w.t0 = x.x;
+    w.ntok = x.y;
+    w.b = x.z;
+    w.qpos = x.w;
+    w.blk0 = y.x;
+    const int blk1 = y.y, kind = y.z;
+    w.part = y.w;
+    w.nP = (kind & AT_PREFIX) ? (a.prefix_len + kAtK - 1) / kAtK : 0;
+    w.nt = w.ntok > a.tpt ? 2 : 1;
+    const int n0 = min(w.ntok, a.tpt);
+    const int e0 = w.nP + ((kind & AT_OWN) ? own_blocks((int64_t)w.qpos + n0, a.max_kv) : 0);
+    const int e1 = w.nP + ((kind & AT_OWN) ? own_blocks((int64_t)w.qpos + w.ntok, a.max_kv) : 0);
+    w.nb0 = max(0, min(blk1, e0) - w.blk0);
+    w.nb1 = w.nt > 1 ? max(0, min(blk1, e1) - w.blk0) : 0;
+    w.nb = max(w.nb0, w.nb1);
+    return true;
+}
+
+// Block j of an item: its first key in the prefix (own = false) or in the sequence's own cache.
+__device__ __forceinline__ int at_block(const AtWork& w, int j, bool& own) {
+    const int k = w.blk0 + j;
+    own = k >= w.nP;
+    return (own ? k - w.nP : k) * kAtK;
+}
+// end of an item's own keys
+__device__ __forceinline__ int at_kend(const AtArgs& a, const AtWork& w) {
+    const int64_t e = (int64_t)w.qpos + w.ntok;
+    return (int)(e < 0 ? 0 : (e > a.max_kv ? a.max_kv : e));
+}
+// whether the V block at own key `key0` has rows that some row of the item does not see
+__device__ __forceinline__ bool at_ragged(const AtWork& w, int key0) { return (int64_t)key0 + kAtK > (int64_t)w.qpos + 1; }
+
+template <int D>
+__global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_constant__ AtArgs a) {
+    using Sh = AtShape<D>;
+    constexpr int R = Sh::RING;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* q_full = bars;              // [2] per tile
+    uint64_t* q_empty = q_full + 2;       // [2]
+    uint64_t* s_full = q_empty + 2;       // [2]
+    uint64_t* p_full = s_full + 2;        // [2]
+    uint64_t* o_full = p_full + 2;        // [2] an item's last product of the tile
+    uint64_t* o_empty = o_full + 2;       // [2] O has been read
+    uint64_t* st_full = o_empty + 2;      // [2] (m, l)
+    uint64_t* st_empty = st_full + 2;     // [2]
+    uint64_t* kv_full = st_empty + 2;     // [R]
+    uint64_t* kv_empty = kv_full + R;     // [R]
+    uint64_t* v_ragged = kv_empty + R;    // a ragged V block has arrived ...
+    uint64_t* v_clean = v_ragged + 1;     // ... and is finite
+    uint64_t* done = v_clean + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
+    unsigned char* sq = smem + Sh::HEAD;
+    unsigned char* ring = sq + 2 * Sh::QB;
+    float2* stat = reinterpret_cast<float2*>(ring + R * Sh::KB);     // [2][kAtM]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&o_empty[i], 4);
+            mbar_init(&st_full[i], 4);
+            mbar_init(&st_empty[i], 4);
+        }
+        for (int i = 0; i < R; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(v_ragged, 1);
+        mbar_init(v_clean, 4);
+        mbar_init(done, 1);
+        *abort_flag = (smem_u32(sq) & 1023u) ? 1 : 0;
+        s_poison[0] = s_poison[1] = 0;
+        if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_trigger();
+    pdl_wait();
+    const int total = *abort_flag ? 0 : a.ctl->n_items * (a.N * a.hkv_s);
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsIo));
+        if (warp == 0 && lane == 0) {
+            // ---------------------------------------------------------------- loads
+            uint32_t it = 0, nq[2] = {0, 0};
+            const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * 128 * Sh::NKB);
+            bool ok = true;
+            AtWork w;
+            for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+                const int grp = w.b * a.hkv_s + w.kvh;
+                auto load = [&](int j, bool v) {
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    const CUtensorMap* m = own ? (v ? &a.tv[w.r] : &a.tk[w.r]) : (v ? &a.pv[w.r] : &a.pk[w.r]);
+                    const int s = it % R;
+                    if (!(ok = mbar_wait(&kv_empty[s], ((it / R) & 1) ^ 1, abort_flag, a.status))) return;
+                    mbar_arrive_expect_tx(&kv_full[s], Sh::KB);
+#pragma unroll
+                    for (int kb = 0; kb < Sh::NKB; ++kb)
+                        tma_load_3d_keep(ring + s * Sh::KB + kb * (kAtK * 128), m, kb * 64, key0, own ? grp : w.kvh, &kv_full[s]);
+                    ++it;
+                };
+                for (int j = 0; j < w.nb && ok; ++j) {
+                    load(j, false);
+                    if (j == 0)
+                        for (int t = 0; t < w.nt && ok; ++t) {
+                            if ((t ? w.nb1 : w.nb0) == 0) continue;
+                            if (!(ok = mbar_wait(&q_empty[t], (nq[t] & 1) ^ 1, abort_flag, a.status))) break;
+                            mbar_arrive_expect_tx(&q_full[t], q_bytes);
+#pragma unroll
+                            for (int kb = 0; kb < Sh::NKB; ++kb)
+                                tma_load_3d_keep(sq + t * Sh::QB + kb * (kAtM * 128), &a.tq, kb * 64, w.kvh * a.G,
+                                                 w.r * a.T + w.t0 + t * a.tpt, &q_full[t]);
+                            ++nq[t];
+                        }
+                    if (ok) load(j, true);
+                }
+            }
+            volatile int no_abort = 0;      // no copy may still be landing when the CTA exits
+            for (int t = 0; t < 2; ++t)
+                if (nq[t]) mbar_wait(&q_full[t], (nq[t] - 1) & 1, &no_abort, nullptr);
+            for (uint32_t k = it > (uint32_t)R ? it - R : 0; k < it; ++k)
+                mbar_wait(&kv_full[k % R], (k / R) & 1, &no_abort, nullptr);
+        } else if (warp == 1) {
+            // ---------------------------------------------------------------- products
+            // the whole warp runs the loop (warp-uniform operands); one elected lane issues
+            const uint32_t id_s = idesc_bf16(kAtM, kAtK), id_o = idesc_bf16_bmn(kAtM, D);
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring));
+            const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
+            uint32_t base = 0, ph = 0;      // phase bits: q_full 0, 1; p_full 2, 3; o_empty 4, 5; v_clean 6
+            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
+            };
+            auto try_all = [&](uint64_t* bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); };
+            auto flip = [&](int bit) {
+                const uint32_t v = (ph >> bit) & 1;
+                ph ^= 1u << bit;
+                return v;
+            };
+            auto issue_s = [&](int t, uint32_t slot, bool last) {          // S_t = Q_t K^T
+                const uint64_t dq = at_desc_add(dq0, t * Sh::QB), dk = at_desc_add(dk0, slot * Sh::KB);
+#pragma unroll
+                for (int kb = 0; kb < Sh::NKB; ++kb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_w(tmem + kAtK * t, at_desc_add(dq, kb * (kAtM * 128) + k * 32),
+                                 at_desc_add(dk, kb * (kAtK * 128) + k * 32), id_s, (kb | k) != 0);
+                tc_commit_w(smem_u32(&s_full[t]));
+                if (last) tc_commit_w(smem_u32(&q_empty[t]));
+            };
+            auto next = [&](int& k, AtWork& w) {            // the next item with key blocks
+                while (at_item(a, total, k, w)) {
+                    ++k;
+                    if (w.nb) return true;
+                }
+                w.nb = 0;
+                return false;
+            };
+            int k = 0;
+            AtWork cur, nxt;
+            bool have = next(k, cur);
+            bool ok = true;
+            if (have) {
+                ok = wait_all(&kv_full[0], 0);
+                for (int t = 0; t < cur.nt && ok; ++t) {
+                    const int n = t ? cur.nb1 : cur.nb0;
+                    if (!n) continue;
+                    if (!(ok = wait_all(&q_full[t], flip(t)))) break;
+                    tc_fence_after();
+                    issue_s(t, 0, n == 1);
+                }
+                tc_commit_w(smem_u32(&kv_empty[0]));
+            }
+            while (have && ok) {
+                const bool more = next(k, nxt);
+                for (int j = 0; j < cur.nb && ok; ++j) {
+                    const uint32_t iv = base + 2 * j + 1, sv = iv % R, in = iv + 1, sn = in % R;   // V of j, the K behind it
+                    const bool last = j + 1 == cur.nb;
+                    const bool follow = !last || more;      // some S is issued behind this block's products
+                    bool own;
+                    const int key0 = at_block(cur, j, own);
+                    const int valid = min(kAtK, (own ? at_kend(a, cur) : a.prefix_len) - key0);
+                    const int steps = (valid + 15) >> 4;
+                    if (!(ok = wait_all(&kv_full[sv], (iv / R) & 1))) break;
+                    bool ragged = own && at_ragged(cur, key0);
+                    if (ragged && lane == 0) mbar_arrive(v_ragged);
+                    __syncwarp();
+                    const uint64_t dv = at_desc_add(dv0, sv * Sh::KB);
+                    bool k_ready = false;
+                    unsigned issued = 0;
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        const int n = t ? cur.nb1 : cur.nb0;
+                        if (j < n) {
+                            if (!(ok = wait_all(&p_full[t], flip(2 + t)))) break;
+                            if (j == 0 && !(ok = wait_all(&o_empty[t], flip(4 + t) ^ 1))) break;
+                            if (ragged && !(ok = wait_all(v_clean, flip(6)))) break;
+                            ragged = false;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int kk = 0; kk < steps; ++kk)
+                                tc_mma_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 8 * kk, at_desc_add(dv, kk * 16 * 128),
+                                            id_o, (j | kk) != 0);
+                            if (j + 1 == n) tc_commit_w(smem_u32(&o_full[t]));
+                        }
+                        if (!last) {
+                            if (j + 1 < n) {
+                                if (!k_ready && !(ok = wait_all(&kv_full[sn], (in / R) & 1))) break;
+                                if (!k_ready) tc_fence_after();
+                                k_ready = true;
+                                issue_s(t, sn, j + 2 == n);
+                            }
+                        } else if (more && (t ? nxt.nb1 : nxt.nb0) && t == 0) {
+                            // the next item's first S behind this tile's last product, if its operands are there
+                            if (try_all(&kv_full[sn], (in / R) & 1) && try_all(&q_full[t], (ph >> t) & 1)) {
+                                flip(t);
+                                tc_fence_after();
+                                issue_s(t, sn, (t ? nxt.nb1 : nxt.nb0) == 1);
+                                issued |= 1u << t;
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit_w(smem_u32(&kv_empty[sv]));   // every MMA reading V has been issued
+                    if (last && more) {
+                        if (!(ok = wait_all(&kv_full[sn], (in / R) & 1))) break;
+                        for (int t = 0; t < nxt.nt && ok; ++t) {
+                            const int n = t ? nxt.nb1 : nxt.nb0;
+                            if (!n || (issued >> t & 1)) continue;
+                            if (!(ok = wait_all(&q_full[t], flip(t)))) break;
+                            tc_fence_after();
+                            issue_s(t, sn, n == 1);
+                        }
+                    }
+                    if (follow && ok) tc_commit_w(smem_u32(&kv_empty[sn]));
+                }
+                base += 2 * cur.nb;
+                cur = nxt;
+                have = more;
+            }
+            tc_commit_w(smem_u32(done));
+        }
+    } else if (warp < 12) {
+        // -------------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAtRegsSoftmax));
+        const int t = (warp - 4) >> 2;                      // tile
+        const int qd = warp & 3;                            // tensor-memory lane quarter
+        const int m = 32 * qd + lane;                       // row of the tile
+        const int tok = m / a.G + t * a.tpt;                // the row's token in the item
+        const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
+        const uint32_t s_col = tmem + lane_off + kAtK * t, o_col = tmem + lane_off + 2 * kAtK + D * t;
+        uint32_t sp = 0, ip = 0;                            // blocks, items of the tile so far
+        bool ok = true;
+        AtWork w;
+        for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+            const int n = t ? w.nb1 : w.nb0;
+            if (!n) continue;
+            const int rows = min(a.tpt, w.ntok - t * a.tpt) * a.G;
+            const bool idle = 32 * qd >= rows;              // a warp without rows only keeps the barriers' pace
+            const int kend = at_kend(a, w);
+            const int own_max = min((int64_t)kend - 1, (int64_t)w.qpos + tok);       // last own key the row sees
+            const int warp_max = w.qpos + (32 * qd) / a.G + t * a.tpt;               // ... its warp's first row sees
+            float m_use = -INFINITY, l_run = 0.f;
+            for (int j = 0; j < n; ++j, ++sp) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], sp & 1, abort_flag, a.status));
+                if (!ok) break;
+                if (!idle) {
+                    tc_fence_after();
+                    uint32_t v[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
+                    tmem_wait_ld();
+                    float* e = reinterpret_cast<float*>(&v[0][0]);
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    // a block that every row of the warp sees whole needs no mask
+                    const bool whole = own ? key0 + kAtK - 1 <= min(warp_max, kend - 1) : key0 + kAtK <= a.prefix_len;
+                    if (!whole) {
+                        const int hi = (own ? own_max : a.prefix_len - 1) - key0;
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) e[i] = i <= hi ? e[i] : -INFINITY;
+                    }
+                    float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // independent chains
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) mq[i & 3] = fmaxf(mq[i & 3], e[i]);
+                    const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * a.scale_log2;
+                    const bool grow = m_blk > m_use + kAtRescale;
+                    const float alpha = grow ? ex2_approx(m_use - m_blk) : 1.f;   // 0 when m_use is -inf
+                    if (grow) m_use = m_blk;
+                    const float m_sub = m_use == -INFINITY ? 0.f : m_use;         // nothing seen yet: every weight is 0
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) e[i] = fmaf(e[i], a.scale_log2, -m_sub);
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) e[i] = ex2_approx(e[i]);
+                    float sq[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) sq[i & 7] += e[i];
+                    l_run = l_run * alpha + (((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])));
+                    uint32_t pk[2][32];
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) pk[i >> 5][i & 31] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+                    tmem_st32(s_col, pk[0]);
+                    tmem_st32(s_col + 32, pk[1]);
+                    // O holds the blocks before this one (their products precede this S in the
+                    // order of issue); rescale it where the row's m moved
+                    if (j > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o_col + 32 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(o_col + 32 * c, o);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&st_empty[t], (ip & 1) ^ 1, abort_flag, a.status));
+            if (!ok) break;
+            stat[t * kAtM + m] = make_float2(m_use, l_run);
+            ++ip;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_full[t]);
+        }
+    } else {
+        // -------------------------------------------------------------------- ragged V blocks, results
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsOut));
+        const int qd = warp & 3, m = 32 * qd + lane;
+        const int tok0 = m / a.G, g = m - tok0 * a.G;
+        const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
+        uint32_t base = 0, ip[2] = {0, 0}, rp = 0;
+        int np = 0;
+        bool ok = true;
+        AtWork w;
+        for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+            const int kend = at_kend(a, w);
+            int first_ragged = INT_MAX;                     // first own key of the ragged blocks
+            int poison = 0;
+            for (int j = 0; j < w.nb && ok; ++j) {
+                bool own;
+                const int key0 = at_block(w, j, own);
+                if (!own || !at_ragged(w, key0)) continue;
+                const uint32_t sv = (base + 2 * j + 1) % R;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_ragged, rp & 1, abort_flag, a.status)))) break;
+                ++rp;
+                first_ragged = min(first_ragged, key0);
+                // row m of the block: zeros behind the last key, and no infinities or NaN
+                unsigned char* row = ring + sv * Sh::KB + m * 128;
+                const bool past = key0 + m >= kend;
+#pragma unroll
+                for (int c = 0; c < Sh::NKB; ++c)
+#pragma unroll 1
+                    for (int u = 0; u < 8; ++u) {
+                        uint4* q = reinterpret_cast<uint4*>(row + c * (kAtK * 128) + ((u ^ (m & 7)) << 4));
+                        if (past) {
+                            *q = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 x = *q;
+                        uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+                        bool hit = false;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((y[i] & 0x7F80u) == 0x7F80u) y[i] &= 0xFFFF0000u, hit = true;
+                            if ((y[i] & 0x7F800000u) == 0x7F800000u) y[i] &= 0xFFFFu, hit = true;
+                        }
+                        if (hit) {
+                            *q = x;
+                            poison = 1;
+                        }
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                const bool any = __any_sync(0xffffffffu, poison);
+                __syncwarp();
+                if (lane == 0) {
+                    if (any) s_poison[np & 1] = np + 1;
+                    mbar_arrive(v_clean);
+                }
+            }
+            if (!ok) break;
+            base += 2 * w.nb;
+            if (first_ragged != INT_MAX) {
+                // did any of the four warps find one? Their last arrival is behind their notes; a note holds the number
+                // of its item, in turns in two places, as a warp is at most one such item ahead of another
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_clean, (rp - 1) & 1, abort_flag, a.status)))) break;
+                poison = s_poison[np & 1] == np + 1;
+                ++np;
+            }
+            for (int t = 0; t < w.nt && ok; ++t) {
+                const int n = t ? w.nb1 : w.nb0, tok = tok0 + t * a.tpt;
+                const bool live = tok0 < a.tpt && tok < w.ntok;
+                const int64_t pos = (int64_t)w.qpos + tok;
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (n) {
+                    ok = __all_sync(0xffffffffu, mbar_wait(&st_full[t], ip[t] & 1, abort_flag, a.status) &&
+                                                     mbar_wait(&o_full[t], ip[t] & 1, abort_flag, a.status));
+                    if (!ok) break;
+                    ++ip[t];
+                    tc_fence_after();
+                    ml = stat[t * kAtM + m];
+                }
+                const bool in = pos >= 0 && pos < a.max_kv && ml.y != 0.f;
+                const float inv = w.part >= 0 ? 1.f : 1.f / ml.y;
+                bf16* dst = a.out + (((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + g) * D;
+                const int64_t prow = (int64_t)w.part + (int64_t)w.h * w.ntok * a.G + tok * a.G + g;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    if (n) {
+                        tmem_ld32(tmem + 2 * kAtK + D * t + lane_off + 32 * c, o);
+                        tmem_wait_ld();
+                    }
+                    if (!live) continue;
+                    if (!n || (w.part < 0 && !in)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    } else if (poison) {                    // what the row does see of them
+                        const int end = (int)min((int64_t)kend - 1, pos);
+                        const bf16* v = a.v[w.r] + ((int64_t)w.b * a.hkv_s + w.kvh) * a.max_kv * D + 32 * c;
+                        for (int key = first_ragged; key <= end; ++key)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const float x = __bfloat162float(v[(int64_t)key * D + i]);
+                                if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                            }
+                    }
+                    if (w.part >= 0) {
+                        float* po = a.part_o + prow * D + 32 * c;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4*>(po + i) =
+                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                            __uint_as_float(o[i + 3]));
+                    } else {
+                        const float f = in && n ? inv : 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(
+                                pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
+                                pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
+                                pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
+                                pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
+                    }
+                }
+                if (w.part >= 0 && live) a.part_ml[prow] = ml;
+                if (n) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&o_empty[t]);
+                        mbar_arrive(&st_empty[t]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        volatile int no_abort = 0;                   // every MMA has retired before the columns are freed
+        mbar_wait(done, 0, &no_abort, nullptr);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+        tmem_relinquish();
+    }
+}
+
+// One warp per output row: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
+// over the row's own parts, then its prefix tile's, in their order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParams p) {
+    constexpr int E = D / 32;                        // elements per lane
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G), heads = p.N * p.hkv_s;
+    pdl_wait();
+    const int64_t units = (int64_t)p.ctl->n_chunks * heads;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int c = p.chunks[u / heads], h = (int)(u % heads), r = h / p.hkv_s;
+        const AttnGroup gr = p.groups[c >> 5];
+        const int row = (c & 31) * 8 + warp;
+        if (row >= gr.ntok * G) continue;
+        const int tok = row / G, t = gr.t0 + tok;
+        const int64_t pos = (int64_t)gr.qpos + tok;
+        const int64_t stride = (int64_t)heads * gr.ntok * G, first = gr.row + (int64_t)h * gr.ntok * G + row;
+        int n2 = 0;
+        int64_t first2 = 0, stride2 = 0;
+        if (p.shared) {
+            const int i = t / per, ntok = min(per, p.ctl->n_tokens - i * per);
+            const int2 g = p.prefix_groups[i];
+            n2 = g.y;
+            stride2 = (int64_t)heads * ntok * G;
+            first2 = g.x + (int64_t)h * ntok * G + (t - i * per) * G + (row - tok * G);
+        }
+        const int n = gr.parts + n2;
+        auto at = [&](int i) { return i < gr.parts ? first + i * stride : first2 + (i - gr.parts) * stride2; };
+        float mx = -INFINITY;
+        for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.part_ml[at(i)].x);
+        mx = warp_max(mx);
+        float l = 0.f, o[E] = {};
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = p.part_ml[at(i)];
+            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+            l = fmaf(f, ml.y, l);
+            const float* src = p.part_o + at(i) * D + lane * E;
+            float x[E];
+            if (E == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[0] = y.x, x[1] = y.y, x[E - 2] = y.z, x[E - 1] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[0] = y.x, x[1] = y.y;
+            }
+            if (f != 0.f)
+#pragma unroll
+                for (int k = 0; k < E; ++k) o[k] = fmaf(f, x[k], o[k]);
+        }
+        const bool in = pos >= 0 && pos < p.max_kv && l != 0.f;
+        const float inv = 1.f / l;
+        uint32_t y[E / 2];
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) y[k] = in ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
+        bf16* dst = static_cast<bf16*>(p.out) + (((int64_t)r * p.T + t) * p.hq_s + (h - r * p.hkv_s) * G + (row - tok * G)) * D + lane * E;
+        if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[E / 2 - 1]);
+        else *reinterpret_cast<uint32_t*>(dst) = y[0];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------
+
+namespace {
+// 3-D bf16 map [d2][d1][d0], rows of d1 `stride1` elements apart and of d2 `stride2`; boxes b0 x b1 x b2, 128-byte swizzled.
+cudaError_t attn_map(const void* base, int64_t d0, int64_t d1, int64_t d2, int64_t stride1, int64_t stride2, int b1, int b2,
+                     CUtensorMap* out) {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!encode) {
+            cudaDriverEntryPointQueryResult q;
+            cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&encode),
+                                                             12000, cudaEnableDefault, &q);
+            if (e != cudaSuccess || !encode) return e != cudaSuccess ? e : cudaErrorNotSupported;
+        }
+    }
+    cuuint64_t gdim[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+    cuuint64_t gstride[2] = {(cuuint64_t)stride1 * 2, (cuuint64_t)stride2 * 2};
+    cuuint32_t box[3] = {64u, (cuuint32_t)b1, (cuuint32_t)b2};
+    cuuint32_t estride[3] = {1u, 1u, 1u};
+    CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estride,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+}  // namespace
+
+AttnSizes attn_sizes(int64_t B, int64_t T, int hq, int hkv, int d) {
+    const int64_t G = hq / hkv, per = 2 * (kAtM / G);
+    const int64_t tiles = T / per + B + 1, prefix = T / per + 2, extra = 2 * kSMs / hkv + 2;
+    AttnSizes s;
+    s.items = (size_t)(tiles + prefix + extra) * sizeof(AttnItem);
+    s.groups = (size_t)tiles * sizeof(AttnGroup);
+    s.prefix_groups = (size_t)prefix * sizeof(int2);
+    s.chunks = (size_t)(T * G / 8 + tiles) * sizeof(int);
+    // every row once as a sequence's own and once as the prefix's, and the extra parts' rows
+    const int64_t most = T < per ? T : per;
+    s.rows = 2 * T * hq + extra * hkv * most * G;
+    s.part_ml = (size_t)s.rows * sizeof(float2);
+    s.part_o = (size_t)s.rows * d * sizeof(float);
+    return s;
+}
+
+cudaError_t launch_attn_plan(const RaggedAttnParams& p, cudaStream_t s) {
     RaggedAttnParams a = p;
     void* args[] = {&a};
-    return launch_pdl(reinterpret_cast<const void*>(attn_check_kernel), args, 1, 0, s, 256);
+    return launch_pdl(reinterpret_cast<const void*>(attn_plan_kernel), args, 1, 0, s, 1024);
 }
 
 cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
-    const int64_t grid = ((int64_t)p.N * p.T * p.hq_s + 7) / 8;
-    if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    const void* fn = p.d == 128 ? reinterpret_cast<const void*>(attn_rows_kernel<128>)
-                                : reinterpret_cast<const void*>(attn_rows_kernel<64>);
-    RaggedAttnParams a = p;
+    AtArgs a;
+    memset(&a, 0, sizeof a);
+    const int G = p.hq_s / p.hkv_s;
+    a.N = p.N;
+    a.T = p.T;
+    a.hq_s = p.hq_s;
+    a.hkv_s = p.hkv_s;
+    a.G = G;
+    a.tpt = kAtM / G;
+    a.max_kv = p.max_kv;
+    a.prefix_len = p.prefix_len;
+    a.scale_log2 = p.scale_log2;
+    a.status = p.status;
+    a.out = static_cast<bf16*>(p.out);
+    a.part_o = p.part_o;
+    a.part_ml = p.part_ml;
+    a.items = p.items;
+    a.ctl = p.ctl;
+    const int64_t D = p.d;
+    cudaError_t e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, a.tpt, &a.tq);
+    for (int r = 0; r < p.N && e == cudaSuccess; ++r) {
+        a.v[r] = static_cast<const bf16*>(p.vc[r]);
+        const int64_t groups = (int64_t)p.max_batch * p.hkv_s, rows = p.max_kv;
+        e = attn_map(p.kc[r], D, rows, groups, D, rows * D, kAtK, 1, &a.tk[r]);
+        if (e == cudaSuccess) e = attn_map(p.vc[r], D, rows, groups, D, rows * D, kAtK, 1, &a.tv[r]);
+        if (p.prefix_len && e == cudaSuccess) {
+            e = attn_map(p.pk[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, kAtK, 1, &a.pk[r]);
+            if (e == cudaSuccess) e = attn_map(p.pv[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, kAtK, 1, &a.pv[r]);
+        }
+    }
+    if (e != cudaSuccess) return e;
+    const bool wide = p.d == 128;
+    const void* fn = wide ? reinterpret_cast<const void*>(attn_items_kernel<128>)
+                          : reinterpret_cast<const void*>(attn_items_kernel<64>);
+    const int smem = wide ? AtShape<128>::SMEM : AtShape<64>::SMEM;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
     void* args[] = {&a};
-    return launch_pdl(fn, args, (int)grid, 0, s, 256);
+    e = launch_pdl(fn, args, kSMs, smem, s, kAtThreads);
+    if (e != cudaSuccess) return e;
+    RaggedAttnParams c = p;
+    void* cargs[] = {&c};
+    const int64_t units = ((int64_t)p.T * G / 8 + p.B) * p.N * p.hkv_s;
+    return launch_pdl(wide ? reinterpret_cast<const void*>(attn_combine_kernel<128>)
+                           : reinterpret_cast<const void*>(attn_combine_kernel<64>),
+                      cargs, (int)(units < 8 * kSMs ? units : 8 * kSMs), 0, s, 256);
 }
 
 }  // namespace tpk

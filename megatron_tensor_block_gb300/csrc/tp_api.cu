@@ -68,7 +68,9 @@ struct tp_plan_s {
            off_m_xs = 0, off_m_act = 0, off_m_o = 0, ws_moe_end = 0;
     // prefill buffers (share the data region with the decode and MoE buffers)
     size_t off_p_xn = 0, off_p_q = 0, off_p_ao = 0, off_p_h = 0, off_p_act = 0, off_p_rope = 0, ws_prefill_end = 0;
-    size_t off_a_ctl = 0;               // packed batches: counts, after the prefill buffers
+    // packed batches: counts and lists after the prefill buffers; the partial results share
+    // the region of the normalised activations, which an attention stage does not need
+    size_t off_a_ctl = 0, off_a_items = 0, off_a_groups = 0, off_a_prefix = 0, off_a_chunks = 0, off_a_ml = 0, off_a_o = 0;
     size_t ws_bytes = 0;
     size_t ws_decode_end = 0;           // end of the decode buffers (control words included)
     // multi-layer decode (tp_stack_decode): control words, then its own pair buffers
@@ -304,13 +306,19 @@ extern "C" tp_status tp_plan(const tp_model_desc* d, int32_t tp, tp_plan_t* out)
     if (dense && d->dtype == TP_BF16) {
         off = P->ctrl_bytes;
         const int64_t Tm = d->max_tokens, hd = d->head_dim;
-        P->off_p_xn = take((size_t)N * Tm * H * 2);              // one bf16 copy per distinct gamma
+        const AttnSizes as = attn_sizes(d->max_batch, Tm, (int)d->n_heads, (int)d->n_kv_heads, (int)hd);
+        P->off_p_xn = P->off_a_o = take(std::max((size_t)N * Tm * H * 2, as.part_o));   // one bf16 copy per distinct gamma
         P->off_p_q = take((size_t)Tm * d->n_heads * hd * 2);     // [N][T][Hq' d]
         P->off_p_ao = take((size_t)Tm * d->n_heads * hd * 2);
         P->off_p_h = take((size_t)Tm * H * 4);
         P->off_p_act = take((size_t)Tm * d->ffn * 2);            // [N][T][F']
         P->off_p_rope = take((size_t)d->max_kv * (hd / 2) * 8);  // (cos, sin) per position and pair
         P->off_a_ctl = take(sizeof(AttnCtl));
+        P->off_a_items = take(as.items);
+        P->off_a_groups = take(as.groups);
+        P->off_a_prefix = take(as.prefix_groups);
+        P->off_a_chunks = take(as.chunks);
+        P->off_a_ml = take(as.part_ml);
         P->ws_prefill_end = off;
     }
     if (moe) {
@@ -1047,7 +1055,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
     cudaError_t e;
     const double log2_theta = std::log2(d.rope_theta);
     stage_mark(P, 0, s);
-    e = pk ? launch_attn_check(*pk, s) : cudaSuccess;
+    e = pk ? launch_attn_plan(*pk, s) : cudaSuccess;
     if (e == cudaSuccess)
         e = pk ? launch_rope_table_at(rope, (int)d.max_kv, hd, log2_theta, pk->prefix_len, s)
                : launch_rope_table(rope, (int)d.max_kv, hd, log2_theta, s);
@@ -1255,6 +1263,15 @@ static tp_status packed_args(const char* who, tp_plan_t plan, const tp_kv_set* p
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)d.head_dim));
     a.status = reinterpret_cast<int*>(ws + plan->off_status);
     a.ctl = reinterpret_cast<AttnCtl*>(ws + plan->off_a_ctl);
+    a.items = reinterpret_cast<AttnItem*>(ws + plan->off_a_items);
+    a.groups = reinterpret_cast<AttnGroup*>(ws + plan->off_a_groups);
+    a.prefix_groups = reinterpret_cast<int2*>(ws + plan->off_a_prefix);
+    a.chunks = reinterpret_cast<int*>(ws + plan->off_a_chunks);
+    a.part_ml = reinterpret_cast<float2*>(ws + plan->off_a_ml);
+    a.part_o = reinterpret_cast<float*>(ws + plan->off_a_o);
+    // A prefix that the batch shares is read once for tiles of tokens of any sequence where the sequences bring less
+    // than half a tile of rows each; longer ones fill their own tiles, which then take the prefix before their own keys.
+    a.shared = prefix_len > 0 && (int64_t)T * (a.hq_s / a.hkv_s) < (int64_t)B * 128;
     return TP_OK;
 }
 
@@ -1273,7 +1290,7 @@ static tp_status attn_packed(const char* who, tp_plan_t plan, const void* q, con
     a.q = q;
     a.out = out;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_attn_check(a, s);
+    cudaError_t e = launch_attn_plan(a, s);
     if (e == cudaSuccess) e = launch_attn_ragged(a, s);
     if (e != cudaSuccess) return cuda_fail(e, who);
     return ok();

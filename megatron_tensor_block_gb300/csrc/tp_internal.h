@@ -328,7 +328,18 @@ cudaError_t launch_lm_head(const HeadArgs& a, size_t smem, cudaStream_t s);
 // Attention of a packed batch (kernels_attn.cu).
 struct AttnCtl {
     int n_tokens;                         // cu[B], or 0 where cu is malformed
-    int reserved[15];
+    int n_items, n_groups, n_chunks;
+    int reserved[12];
+};
+struct AttnItem {                         // for every KV head of every shard:
+    int t0, ntok;                         // token rows
+    int b, qpos;                          // sequence, cache row of the first of them
+    int blk0, blk1;                       // part of its list of key blocks
+    int kind;                             // which blocks the list has
+    int row;                              // first row of its partial results, or -1: final
+};
+struct AttnGroup {                        // tokens whose results are joined from parts
+    int t0, ntok, qpos, row, parts, reserved[3];
 };
 struct RaggedAttnParams {
     const void* q;                        // [N][T][hq_s d] bf16
@@ -338,16 +349,30 @@ struct RaggedAttnParams {
     const void* pk[TP_MAX_SHARDS];        // shared prefix [hkv_s][prefix_rows][d] (prefix_len > 0)
     const void* pv[TP_MAX_SHARDS];
     int prefix_len;
+    int shared;                           // 1: the prefix is attended to by tiles of the batch's tokens
     int64_t prefix_rows;
     const int* cu;                        // [B + 1]
     const int* pos;                       // [B] row of each sequence's first new token
     int N, B, T, hq_s, hkv_s, d, max_kv, max_batch;
     float scale_log2;                     // log2(e) / sqrt(d)
     int* status;
-    AttnCtl* ctl;                         // workspace
+    // workspace
+    AttnCtl* ctl;
+    AttnItem* items;
+    AttnGroup* groups;
+    int2* prefix_groups;                  // per prefix tile: first row of its partial results, parts
+    int* chunks;                          // group * 32 + eighth-rows chunk
+    float2* part_ml;
+    float* part_o;
 };
-// Checks cu and pos and fills ctl; every other kernel of a packed batch reads ctl.
-cudaError_t launch_attn_check(const RaggedAttnParams& p, cudaStream_t s);
+// Workspace of a plan's packed batches; `rows` of partial results.
+struct AttnSizes {
+    size_t items, groups, prefix_groups, chunks, part_ml, part_o;
+    int64_t rows;
+};
+AttnSizes attn_sizes(int64_t max_batch, int64_t max_tokens, int hq, int hkv, int d);
+// Checks cu and pos, fills ctl and the lists; every other kernel of a packed batch reads ctl.
+cudaError_t launch_attn_plan(const RaggedAttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s);
 
 // Per-row controls of a batch's logits (kernels_logits.cu).
