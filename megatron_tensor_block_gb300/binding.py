@@ -171,7 +171,8 @@ class Plan:
 
     def __init__(self, handle: int, desc: tp_model_desc):
         self.handle = handle
-        self.info = tp_plan_get_info(self)
+        info = tp_plan_get_info(self)
+        self.tp, self.hkv_shard, self.workspace_bytes = info["tp"], info["hkv_shard"], info["workspace_bytes"]
         for n in ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab"):
             setattr(self, n, int(getattr(desc, n)))
 
@@ -323,42 +324,54 @@ def tp_lm_head_forward(plan: Plan, head_shards: list, gamma, x, T: int, logits, 
                                      _ptr(device_status), _stream(stream)))
 
 
-def _checked(t, name: str, dtype: str, numel: int) -> int | None:
+class _Torch:
+    """torch's types and current device, looked up once."""
+    types = None
+
+    @classmethod
+    def device(cls) -> int:
+        """The current device; -1 (no tensor's device) where there is none."""
+        import torch
+        if cls.types is None:
+            cls.types = {n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")}
+            cls.current = staticmethod(torch.cuda.current_device if torch.cuda.is_available() else lambda: -2)
+        return cls.current()
+
+
+def _checked(t, name: str, dtype: str, numel: int, device: int) -> int | None:
     """Address of a tensor argument after the checks that an address alone
     does not allow: type, contiguity, size, device. Integers pass as they are."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    import torch
-    if t.dtype is not getattr(torch, dtype):
+    if (t.dtype is _Torch.types[dtype] and t.numel() >= numel and t.get_device() == device and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype is not _Torch.types[dtype]:
         raise TypeError(f"{name}: {t.dtype}, expected torch.{dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     if t.numel() < numel:
         raise ValueError(f"{name}: {t.numel()} elements, expected at least {numel}")
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on cuda:{t.get_device()}, current device is cuda:{torch.cuda.current_device()}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: not a CUDA tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
 
 
-def _kv_checked(plan: Plan, kv, name: str, rows: int) -> tp_kv_set:
+def _kv_checked(plan: Plan, kv, name: str, rows: int, device: int) -> tp_kv_set:
     """``kv = (k list, v list)``; every tensor holds at least ``rows`` rows per KV head."""
-    n = rows * plan.info["hkv_shard"] * plan.head_dim
-    tp = plan.info["tp"]
-    if len(kv[0]) != tp or len(kv[1]) != tp:
-        raise ValueError(f"{name}: expected a K and a V cache for each of {tp} shards")
-    return _kv_set([_checked(t, name, "bfloat16", n) for t in kv[0]], [_checked(t, name, "bfloat16", n) for t in kv[1]])
+    n = rows * plan.hkv_shard * plan.head_dim
+    k, v = kv
+    if len(k) != plan.tp or len(v) != plan.tp:
+        raise ValueError(f"{name}: expected a K and a V cache for each of {plan.tp} shards")
+    return tp_kv_set(_P8(*[_checked(t, name, "bfloat16", n, device) for t in k]),
+                     _P8(*[_checked(t, name, "bfloat16", n, device) for t in v]))
 
 
 def tp_attn_packed(plan: Plan, q, kv: tuple, cu, pos, B: int, T: int, out, workspace, nbytes: int, stream=None) -> None:
     """Causal attention of a packed batch: ``q``, ``out`` bf16 ``[tp, T, Hq', d]``, sequence b the rows
     ``cu[b]..cu[b+1]-1`` at positions ``pos[b]..`` of the caches ``kv = (k list, v list)``."""
-    n = T * plan.n_heads * plan.head_dim
-    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
-    _check(load().tp_attn_packed(plan.handle, _checked(q, "q", "bfloat16", n), C.byref(kvs),
-                                 _checked(cu, "cu", "int32", B + 1), _checked(pos, "pos", "int32", B), B, T,
-                                 _checked(out, "out", "bfloat16", n), _checked(workspace, "workspace", "uint8", nbytes),
+    n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv, dev)
+    _check(load().tp_attn_packed(plan.handle, _checked(q, "q", "bfloat16", n, dev), C.byref(kvs),
+                                 _checked(cu, "cu", "int32", B + 1, dev), _checked(pos, "pos", "int32", B, dev), B, T,
+                                 _checked(out, "out", "bfloat16", n, dev), _checked(workspace, "workspace", "uint8", nbytes, dev),
                                  nbytes, _stream(stream)))
 
 
@@ -366,26 +379,27 @@ def tp_attn_prefix(plan: Plan, q, prefix: tuple, prefix_len: int, prefix_rows: i
                    out, workspace, nbytes: int, stream=None) -> None:
     """``tp_attn_packed`` with a shared prefix ``(k list, v list)`` of ``[Hkv', prefix_rows, d]``, rows
     ``0..prefix_len-1`` of which every token attends to before its own cache."""
-    n = T * plan.n_heads * plan.head_dim
-    pre = _kv_checked(plan, prefix, "prefix", prefix_rows) if prefix_len else None
-    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
-    _check(load().tp_attn_prefix(plan.handle, _checked(q, "q", "bfloat16", n), C.byref(pre) if pre is not None else None,
-                                 prefix_len, prefix_rows, C.byref(kvs), _checked(cu, "cu", "int32", B + 1),
-                                 _checked(pos, "pos", "int32", B), B, T, _checked(out, "out", "bfloat16", n),
-                                 _checked(workspace, "workspace", "uint8", nbytes), nbytes, _stream(stream)))
+    n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
+    pre = _kv_checked(plan, prefix, "prefix", prefix_rows, dev) if prefix_len else None
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv, dev)
+    _check(load().tp_attn_prefix(plan.handle, _checked(q, "q", "bfloat16", n, dev), C.byref(pre) if pre is not None else None,
+                                 prefix_len, prefix_rows, C.byref(kvs), _checked(cu, "cu", "int32", B + 1, dev),
+                                 _checked(pos, "pos", "int32", B, dev), B, T, _checked(out, "out", "bfloat16", n, dev),
+                                 _checked(workspace, "workspace", "uint8", nbytes, dev), nbytes, _stream(stream)))
 
 
 def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, B: int, T: int, workspace, nbytes: int,
                             prefix: tuple | None = None, prefix_len: int = 0, prefix_rows: int = 0, stream=None) -> None:
     """The PREFILL block over a packed batch (``x``, ``y`` float32 ``[T, H]``), with an optional shared prefix."""
-    pre = _kv_checked(plan, prefix, "prefix", prefix_rows) if prefix_len and prefix is not None else None
-    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv)
+    dev = _Torch.device()
+    pre = _kv_checked(plan, prefix, "prefix", prefix_rows, dev) if prefix_len and prefix is not None else None
+    kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv, dev)
     n = T * plan.hidden
     _check(load().tp_block_forward_packed(plan.handle, C.byref(_shard_set(shards)), C.byref(kvs),
                                           C.byref(pre) if pre is not None else None, prefix_len, prefix_rows,
-                                          _checked(x, "x", "float32", n), _checked(y, "y", "float32", n),
-                                          _checked(cu, "cu", "int32", B + 1), _checked(pos, "pos", "int32", B), B, T,
-                                          _checked(workspace, "workspace", "uint8", nbytes), nbytes, _stream(stream)))
+                                          _checked(x, "x", "float32", n, dev), _checked(y, "y", "float32", n, dev),
+                                          _checked(cu, "cu", "int32", B + 1, dev), _checked(pos, "pos", "int32", B, dev), B, T,
+                                          _checked(workspace, "workspace", "uint8", nbytes, dev), nbytes, _stream(stream)))
 
 
 def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=None, n_prompt=None, repetition=None,
@@ -394,18 +408,18 @@ def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=No
     """Penalties, biases and grammar masks of ``logits`` (float32 ``[T, org_vocab]``) into ``out`` (which may be
     ``logits``). ``mask`` is int32 ``[mask_rows, ceil(org_vocab / 32)]``, bit 1 = allowed; ``mask_rows`` is taken from a
     tensor's size where not given."""
-    words = (plan.org_vocab + 31) // 32
+    words, dev = (plan.org_vocab + 31) // 32, _Torch.device()
     if mask_rows is None:
         mask_rows = 0 if mask is None or isinstance(mask, int) else mask.numel() // max(words, 1)
     c = tp_logit_controls(
-        _checked(tokens, "tokens", "int32", 0), _checked(cu_tokens, "cu_tokens", "int32", T + 1),
-        _checked(n_prompt, "n_prompt", "int32", T), _checked(repetition, "repetition", "float32", T),
-        _checked(presence, "presence", "float32", T), _checked(frequency, "frequency", "float32", T),
-        _checked(bias_ids, "bias_ids", "int32", 0), _checked(bias_values, "bias_values", "float32", 0),
-        _checked(cu_bias, "cu_bias", "int32", T + 1), _checked(mask, "mask", "int32", mask_rows * words),
-        _checked(mask_row, "mask_row", "int32", T), mask_rows, 0)
-    _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", "float32", T * plan.org_vocab), T, C.byref(c),
-                                    _checked(out, "out", "float32", T * plan.org_vocab), _stream(stream)))
+        _checked(tokens, "tokens", "int32", 0, dev), _checked(cu_tokens, "cu_tokens", "int32", T + 1, dev),
+        _checked(n_prompt, "n_prompt", "int32", T, dev), _checked(repetition, "repetition", "float32", T, dev),
+        _checked(presence, "presence", "float32", T, dev), _checked(frequency, "frequency", "float32", T, dev),
+        _checked(bias_ids, "bias_ids", "int32", 0, dev), _checked(bias_values, "bias_values", "float32", 0, dev),
+        _checked(cu_bias, "cu_bias", "int32", T + 1, dev), _checked(mask, "mask", "int32", mask_rows * words, dev),
+        _checked(mask_row, "mask_row", "int32", T, dev), mask_rows, 0)
+    _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", "float32", T * plan.org_vocab, dev), T, C.byref(c),
+                                    _checked(out, "out", "float32", T * plan.org_vocab, dev), _stream(stream)))
 
 
 def tp_reduce_partials(plan: Plan, partials, residual, bias, out, M: int, stream=None) -> None:

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
 
 constexpr int kAtThreads = 512;
 constexpr float kAtRescale = 8.0f;
-constexpr int kAtRegsIo = 64, kAtRegsSoftmax = 184, kAtRegsOut = 80;
+constexpr int kAtRegsIo = 80, kAtRegsSoftmax = 168, kAtRegsOut = 96;
 static_assert(kAtRegsIo + 2 * kAtRegsSoftmax + kAtRegsOut <= 4 * 128, "the launch's registers");
 
 template <int D>
@@ -241,6 +241,31 @@ struct AtArgs {
     float scale_log2;
     int* status;
 };
+
+// Two float32 operations per instruction, and a maximum of three.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 __device__ __forceinline__ uint64_t at_desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
@@ -560,25 +585,31 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                     }
                     float mq[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // independent chains
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) mq[i & 3] = fmaxf(mq[i & 3], e[i]);
+                    for (int i = 0; i < 128; i += 2) mq[(i >> 1) & 3] = max3(mq[(i >> 1) & 3], e[i], e[i + 1]);
                     const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3])) * a.scale_log2;
                     const bool grow = m_blk > m_use + kAtRescale;
                     const float alpha = grow ? ex2_approx(m_use - m_blk) : 1.f;   // 0 when m_use is -inf
                     if (grow) m_use = m_blk;
                     const float m_sub = m_use == -INFINITY ? 0.f : m_use;         // nothing seen yet: every weight is 0
+                    const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2), neg2 = f2_pack(-m_sub, -m_sub);
+                    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) e[i] = fmaf(e[i], a.scale_log2, -m_sub);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int i = 0; i < 128; ++i) e[i] = ex2_approx(e[i]);
-                    float sq[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 128; ++i) sq[i & 7] += e[i];
-                    l_run = l_run * alpha + (((sq[0] + sq[1]) + (sq[2] + sq[3])) + ((sq[4] + sq[5]) + (sq[6] + sq[7])));
-                    uint32_t pk[2][32];
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) pk[i >> 5][i & 31] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
-                    tmem_st32(s_col, pk[0]);
-                    tmem_st32(s_col + 32, pk[1]);
+                        for (int i = 0; i < 16; ++i) {
+                            float x, y;
+                            f2_unpack(f2_fma(f2_pack(e[32 * c + 2 * i], e[32 * c + 2 * i + 1]), scale2, neg2), x, y);
+                            x = ex2_approx(x);
+                            y = ex2_approx(y);
+                            sum[i & 3] = f2_add(sum[i & 3], f2_pack(x, y));
+                            pk[i] = pack_bf16x2(x, y);
+                        }
+                        tmem_st16(s_col + 16 * c, pk);
+                    }
+                    float sx, sy;
+                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), sx, sy);
+                    l_run = l_run * alpha + (sx + sy);
                     // O holds the blocks before this one (their products precede this S in the
                     // order of issue); rescale it where the row's m moved
                     if (j > 0 && __any_sync(0xffffffffu, grow)) {

@@ -9,10 +9,10 @@
 // what a control changes), plus an eighth of a byte of mask. A CTA takes one
 // slice of one row's vocabulary. It counts the row's whole history into one
 // shared-memory word per token of its slice (bit 0: seen in the prompt, bits
-// 1..: generated occurrences) and the last bias entry per token into another;
-// integer atomics, so their order does not change a result. One sweep then
-// reads, changes and writes each logit once. The logits of the sweep are
-// loaded into registers before the history is counted.
+// 1..: generated occurrences); integer atomics, so their order does not change
+// a result. One sweep then reads, changes and writes each logit once; its
+// logits are loaded into registers before the history is counted. The few
+// biased entries follow.
 #include <climits>
 
 #include "common.cuh"
@@ -30,9 +30,8 @@ template <int SLICE>
 __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const LogitArgs a) {
     constexpr int PER = SLICE / 4 / kLogitThreads;          // groups of four per thread
     static_assert(PER >= 1 && SLICE % (4 * kLogitThreads) == 0, "a slice is whole groups of every thread");
-    extern __shared__ __align__(16) unsigned s_words[];
-    unsigned* cnt = s_words;
-    unsigned* last = s_words + SLICE;
+    __shared__ __align__(16) unsigned cnt[SLICE];
+    __shared__ int s_ids[kLogitThreads];
     const int tid = threadIdx.x;
     const int t = blockIdx.x / a.slices, slice = blockIdx.x - t * a.slices;
     const int64_t row0 = (int64_t)t * a.V;
@@ -81,51 +80,65 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
 #pragma unroll
         for (int i = 0; i < PER; ++i) load(v0 + 4 * (tid + i * kLogitThreads), x[i]);
 
-    if (hn)
+    const int lo = max(v0, 0), hi = (int)min((int64_t)v0 + SLICE, (int64_t)a.V);
+    int id = -1;                                            // the thread's entry of a short bias list
+    if (bn && bn <= kLogitThreads && tid < bn) s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
+    if (hn) {
         for (int i = tid; i < SLICE / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
-    if (bn)
-        for (int i = tid; i < SLICE / 4; i += kLogitThreads) reinterpret_cast<uint4*>(last)[i] = make_uint4(0, 0, 0, 0);
-    if (hn || bn) __syncthreads();
-    const int lo = max(v0, 0), hi = min((int64_t)v0 + SLICE, (int64_t)a.V);
-    for (int i = tid; i < hn; i += kLogitThreads) {
-        const int tok = a.tokens[(int64_t)h0 + i];
-        if (tok < lo || tok >= hi) continue;
-        if (i < np) atomicOr(&cnt[tok - v0], 1u);
-        else atomicAdd(&cnt[tok - v0], 2u);
+        __syncthreads();
+        auto hit = [&](int tok, int i) {
+            if (tok < lo || tok >= hi) return;
+            if (i < np) atomicOr(&cnt[tok - v0], 1u);
+            else atomicAdd(&cnt[tok - v0], 2u);
+        };
+        // four tokens per load, four loads in flight
+        const int* h = a.tokens + h0;
+        const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2) & 3), hn), nv = (hn - head) >> 2;
+        if (tid < head) hit(h[tid], tid);
+        const int4* h4 = reinterpret_cast<const int4*>(h + head);
+        for (int j = tid; j < nv; j += 4 * kLogitThreads) {
+            int4 w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = j + k * kLogitThreads < nv ? h4[j + k * kLogitThreads] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = head + 4 * (j + k * kLogitThreads);
+                hit(w[k].x, i);
+                hit(w[k].y, i + 1);
+                hit(w[k].z, i + 2);
+                hit(w[k].w, i + 3);
+            }
+        }
+        for (int i = head + 4 * nv + tid; i < hn; i += kLogitThreads) hit(h[i], i);
+        __syncthreads();
     }
-    for (int i = tid; i < bn; i += kLogitThreads) {
-        const int tok = a.bias_ids[(int64_t)b0 + i];
-        if (tok >= lo && tok < hi) atomicMax(&last[tok - v0], (unsigned)i + 1u);
-    }
-    if (hn || bn) __syncthreads();
+    auto allowed4 = [&](int v) -> unsigned {                // mask bits of entries v .. v + 3
+        if (!mask) return 15u;
+        const int va = max(v, 0), vb = min(v + 3, a.V - 1);
+        const uint32_t w0 = mask[va >> 5], w1 = mask[vb >> 5];
+        return (v >= 0 ? __funnelshift_r(w0, w1, v & 31) : w0 << -v) & 15u;
+    };
 
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int g = tid + i * kLogitThreads, v = v0 + 4 * g;
         if (v >= a.V || v + 3 < 0) continue;
         const uint4 c4 = hn ? reinterpret_cast<const uint4*>(cnt)[g] : make_uint4(0, 0, 0, 0);
-        const uint4 l4 = bn ? reinterpret_cast<const uint4*>(last)[g] : make_uint4(0, 0, 0, 0);
-        unsigned allowed = 15u;
-        if (mask) {
-            const int va = max(v, 0), vb = min(v + 3, a.V - 1);
-            const uint32_t w0 = mask[va >> 5], w1 = mask[vb >> 5];
-            allowed = (v >= 0 ? __funnelshift_r(w0, w1, v & 31) : w0 << -v) & 15u;
-        }
-        const bool touched = (c4.x | c4.y | c4.z | c4.w | l4.x | l4.y | l4.z | l4.w) || allowed != 15u;
+        const unsigned allowed = allowed4(v);
+        const bool touched = (c4.x | c4.y | c4.z | c4.w) || allowed != 15u;
         if (in_place) {
             if (!touched) continue;
             load(v, x[i]);
         }
         float e[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
         if (touched) {
-            const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
+            const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (c[k]) {
                     e[k] = e[k] > 0.f ? e[k] / rep : e[k] * rep;
                     if (c[k] > 1u) e[k] = e[k] - freq * (float)(c[k] >> 1) - pres;
                 }
-                if (l[k]) e[k] += a.bias_values[(int64_t)b0 + l[k] - 1];
                 if (!((allowed >> k) & 1u)) e[k] = -INFINITY;
             }
         }
@@ -138,6 +151,30 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
                 if (v + k >= 0 && v + k < a.V) p[k] = e[k];
         }
     }
+
+    // Biases go onto the penalised logits that the sweep has written; a masked one stays -inf.
+    if (!bn) return;
+    __syncthreads();
+    auto add = [&](int v, int entry) {
+        if (allowed4(v) & 1u) a.y[row0 + v] += a.bias_values[(int64_t)b0 + entry];
+    };
+    if (bn <= kLogitThreads) {
+        if (id >= lo && id < hi) {
+            bool last = true;
+            for (int j = tid + 1; j < bn; ++j) last &= s_ids[j] != id;
+            if (last) add(id, tid);
+        }
+        return;
+    }
+    for (int i = tid; i < SLICE / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < bn; i += kLogitThreads) {
+        const int tok = a.bias_ids[(int64_t)b0 + i];
+        if (tok >= lo && tok < hi) atomicMax(&cnt[tok - v0], (unsigned)i + 1u);
+    }
+    __syncthreads();
+    for (int u = tid; u < SLICE; u += kLogitThreads)
+        if (cnt[u]) add(v0 + u, (int)cnt[u] - 1);
 }
 
 template <int SLICE>
@@ -145,14 +182,8 @@ static cudaError_t launch_slices(LogitArgs a, cudaStream_t s) {
     a.slices = (int)(((int64_t)a.V + 3 + SLICE - 1) / SLICE);
     const int64_t grid = (int64_t)a.T * a.slices;
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    const size_t smem = (a.bias_ids ? 2 : 1) * SLICE * sizeof(unsigned);
-    const void* fn = reinterpret_cast<const void*>(logits_process_kernel<SLICE>);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
     void* args[] = {&a};
-    return launch_pdl(fn, args, (int)grid, smem, s, kLogitThreads);
+    return launch_pdl(reinterpret_cast<const void*>(logits_process_kernel<SLICE>), args, (int)grid, 0, s, kLogitThreads);
 }
 
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s) {

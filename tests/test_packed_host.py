@@ -17,7 +17,7 @@ def plan(**kw):
 
 def packed(p, q=A, kv=([A, A], [A, A]), cu=A, pos=A, Bn=4, T=64, out=A + (1 << 20), ws=A, nbytes=None, prefix=None,
            prefix_len=0, prefix_rows=0):
-    nbytes = p.info["workspace_bytes"] if nbytes is None else nbytes
+    nbytes = p.workspace_bytes if nbytes is None else nbytes
     if prefix is None and not prefix_len:
         tb.tp_attn_packed(p, q, kv, cu, pos, Bn, T, out, ws, nbytes, stream=0)
     else:
@@ -54,7 +54,7 @@ def test_packed_calls_need_a_bf16_attention_plan():
                           n_experts=4, top_k=2, expert_ffn=256, hidden=256), 2)
     with pytest.raises(tb.TpError) as e:
         B._check(tb.load().tp_attn_packed(moe.handle, A, B.C.byref(B._kv_set([A, A], [A, A])), A, A, 1, 1, 2 * A, A,
-                                          moe.info["workspace_bytes"], None))
+                                          moe.workspace_bytes, None))
     assert e.value.status == B.TP_ERR_INVALID_ARG
 
 
@@ -62,7 +62,7 @@ def test_prefix_pointer_is_needed_when_it_has_rows():
     p = plan()
     with pytest.raises(tb.TpError) as e:
         B._check(tb.load().tp_attn_prefix(p.handle, A, None, 8, 8, B.C.byref(B._kv_set([A, A], [A, A])), A, A, 1, 1, 2 * A, A,
-                                          p.info["workspace_bytes"], None))
+                                          p.workspace_bytes, None))
     assert e.value.status == B.TP_ERR_NULL
 
 
@@ -71,7 +71,7 @@ def test_prefix_pointer_is_needed_when_it_has_rows():
     (dict(T=65), B.TP_ERR_SHAPE), (dict(Bn=0), B.TP_ERR_SHAPE), (dict(nbytes=100), B.TP_ERR_CAPACITY)])
 def test_packed_block_refuses(kw, status):
     p = plan()
-    a = dict(x=A, y=A + (1 << 20), T=64, Bn=4, nbytes=p.info["workspace_bytes"])
+    a = dict(x=A, y=A + (1 << 20), T=64, Bn=4, nbytes=p.workspace_bytes)
     a.update(kw)
     with pytest.raises(tb.TpError) as e:
         tb.tp_block_forward_packed(p, {}, ([A, A], [A, A]), a["x"], a["y"], A, A, a["Bn"], a["T"], A, a["nbytes"], stream=0)
