@@ -3,11 +3,12 @@
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
 //
-// in one pass over the keys with a running m and sum, three launches:
+// in one pass over the keys with a running m and sum, in up to four launches:
 //   attn_plan_kernel     one CTA turns the offsets and lengths into a list of
 //                        items, longest first, and cuts long items into parts
 //                        where the batch has too few of them for the machine;
-//   attn_items_kernel    persistent, one CTA per SM, on the tensor cores;
+//   attn_items_kernel    persistent, one CTA per SM: items of many query rows;
+//   attn_narrow_kernel   two CTAs per SM: items of few query rows;
 //   attn_combine_kernel  joins the parts of a row.
 // A call whose sequences bring few tokens each treats a shared prefix as items
 // of its own, whose rows are the batch's tokens whatever their sequence: its
@@ -31,6 +32,7 @@ constexpr int kAtM = 128;               // query rows per tile: 128 / G tokens o
 constexpr int kAtK = 128;               // keys per block
 constexpr int kAtBuckets = 512;         // item lengths told apart when sorting
 constexpr int kAtMinPart = 2;           // blocks of the shortest part worth its join
+constexpr int kAtNarrow = 32;           // rows of an item at most that the narrow kernel takes
 
 enum AttnKind : int { AT_PREFIX = 1, AT_OWN = 2 };   // key blocks of an item: the prefix's, the sequence's own
 
@@ -57,14 +59,14 @@ __device__ __forceinline__ void part_split(int nb, int target, int& parts, int& 
 // partial results: their order decides where a partial lies, not what is
 // added to what.
 __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams p) {
-    __shared__ int s_hist[kAtBuckets];
-    __shared__ unsigned long long s_work;
+    __shared__ int s_hist[2 * kAtBuckets];                           // wide items, narrow items
+    __shared__ unsigned long long s_work[2];
     __shared__ int s_rows, s_groups, s_chunks, s_warp[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
-    for (int i = tid; i < kAtBuckets; i += 1024) s_hist[i] = 0;
+    for (int i = tid; i < 2 * kAtBuckets; i += 1024) s_hist[i] = 0;
     if (tid == 0) {
-        s_work = 0;
+        s_work[0] = s_work[1] = 0;
         s_rows = s_groups = s_chunks = 0;
     }
     pdl_wait();
@@ -75,11 +77,12 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     int bad = 0, out = 0;
     __syncthreads();
 
+    const int lanes = min(32, (p.B + 31) / 32);                      // sequences per warp and round
     auto visit = [&](auto&& tile) {
-        for (int b0 = warp * 32; b0 < p.B; b0 += 1024) {
+        for (int b0 = warp * lanes; b0 < p.B; b0 += 32 * lanes) {
             const int b = b0 + lane;
             int c0 = 0, n = 0, pos = 0;
-            if (b < p.B) {
+            if (lane < lanes && b < p.B) {
                 c0 = p.cu[b];
                 n = p.cu[b + 1] - c0;
                 pos = p.pos[b];
@@ -113,45 +116,56 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     const int n_tok = p.cu[p.B];
     const int prefix_tiles = p.shared ? (n_tok + per - 1) / per : 0;
 
-    unsigned long long work = 0;
-    visit([&](int, int, int n, int pos) { work += in_item + own_blocks((int64_t)pos + n, p.max_kv); });
-    if (tid == 0) work += (unsigned long long)prefix_tiles * n_prefix;
-    for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
-    if (lane == 0 && work) atomicAdd(&s_work, work);
+    unsigned long long work[2] = {0, 0};
+    visit([&](int, int, int n, int pos) {
+        work[n * G <= kAtNarrow] += in_item + own_blocks((int64_t)pos + n, p.max_kv);
+    });
+    for (int i = tid; i < prefix_tiles; i += 1024) work[min(per, n_tok - i * per) * G <= kAtNarrow] += n_prefix;
+    for (int k = 0; k < 2; ++k) {
+        for (int o = 16; o; o >>= 1) work[k] += __shfl_xor_sync(0xffffffffu, work[k], o);
+        if (lane == 0 && work[k]) atomicAdd(&s_work[k], work[k]);
+    }
     __syncthreads();
-    // parts of an even share of all blocks or shorter: between one and two rounds of the SMs
-    const long long share = (long long)((s_work * heads * 2 + 3 * kSMs - 1) / (3 * kSMs));
-    const int target = (int)min((long long)INT_MAX / 4, max((long long)kAtMinPart, share));
+    // Parts are an even share of all blocks or shorter: between one and two rounds of the wide kernel's CTAs, and two
+    // of the narrow kernel's, which has two per SM.
+    int target[2];
+    for (int k = 0; k < 2; ++k) {
+        const long long share = (long long)((s_work[k] * heads * 2 + (k ? 8 : 3) * kSMs - 1) / ((k ? 8 : 3) * kSMs));
+        target[k] = (int)min((long long)INT_MAX / 4, max((long long)kAtMinPart, share));
+    }
 
-    auto bucket = [&](int nb) { return kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
-    auto count = [&](int nb) {
+    auto bucket = [&](int nb, bool narrow) { return (narrow ? 2 : 1) * kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
+    auto count = [&](int nb, bool narrow) {
         int parts, len;
-        part_split(nb, target, parts, len);
-        if (parts > 1) atomicAdd(&s_hist[bucket(len)], parts - 1);
-        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len)], 1);
+        part_split(nb, target[narrow], parts, len);
+        if (parts > 1) atomicAdd(&s_hist[bucket(len, narrow)], parts - 1);
+        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len, narrow)], 1);
     };
-    visit([&](int, int, int n, int pos) { count(in_item + own_blocks((int64_t)pos + n, p.max_kv)); });
-    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix);
+    visit([&](int, int, int n, int pos) { count(in_item + own_blocks((int64_t)pos + n, p.max_kv), n * G <= kAtNarrow); });
+    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix, min(per, n_tok - i * per) * G <= kAtNarrow);
     __syncthreads();
-    // exclusive scan of the buckets (16 warps of 32)
-    int mine = tid < kAtBuckets ? s_hist[tid] : 0, incl = mine;
+    // exclusive scan of the buckets, one per thread
+    const int mine = s_hist[tid];
+    int incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kAtBuckets / 32; ++w) {
+    int before = 0, n_wide = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
         if (w < warp) before += s_warp[w];
+        if (w < kAtBuckets / 32) n_wide += s_warp[w];
         total += s_warp[w];
     }
-    if (tid < kAtBuckets) s_hist[tid] = before + incl - mine;
+    s_hist[tid] = before + incl - mine;
     __syncthreads();
 
     auto place = [&](int kind, int b, int t0, int n, int pos, int nb, int group) {
+        const bool narrow = n * G <= kAtNarrow;
         int parts, len;
-        part_split(nb, target, parts, len);
+        part_split(nb, target[narrow], parts, len);
         int row = -1;
         if (parts > 1 || p.shared) {
             row = atomicAdd(&s_rows, parts * heads * n * G);
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
         }
         for (int i = 0; i < parts; ++i) {
             const int k0 = i * len, k1 = min(nb, k0 + len);
-            const int e = atomicAdd(&s_hist[bucket(k1 - k0)], 1);
+            const int e = atomicAdd(&s_hist[bucket(k1 - k0, narrow)], 1);
             p.items[e] = AttnItem{t0, n, b, pos, k0, k1, kind, row < 0 ? -1 : row + i * heads * n * G};
         }
     };
@@ -178,6 +192,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     if (tid == 0) {
         AttnCtl c = {};
         c.n_tokens = n_tok;
+        c.n_wide = n_wide;
         c.n_items = total;
         c.n_groups = s_groups;
         c.n_chunks = s_chunks;
@@ -227,6 +242,7 @@ struct AtShape {
 
 struct AtArgs {
     CUtensorMap tq;                       // q as [N T][hq_s][D], boxes of 128 / G tokens x G heads x 64
+    CUtensorMap tqn;                      // the same with boxes of kAtNarrow / G tokens
     CUtensorMap tk[TP_MAX_SHARDS];        // caches as [max_batch hkv_s][max_kv][D], boxes of 128 rows x 64
     CUtensorMap tv[TP_MAX_SHARDS];
     CUtensorMap pk[TP_MAX_SHARDS];        // prefix as [hkv_s][prefix_len][D] (rows past it read as zeros)
@@ -236,7 +252,8 @@ struct AtArgs {
     float* part_o;                        // [rows][D]
     float2* part_ml;                      // [rows] (m, l)
     const AttnItem* items;
-    const AttnCtl* ctl;
+    AttnCtl* ctl;
+    int after_wide;                       // narrow kernel: the wide one is launched before it
     int N, T, hq_s, hkv_s, G, tpt, max_kv, prefix_len;
     float scale_log2;
     int* status;
@@ -276,21 +293,11 @@ struct AtWork {
     int nP, nt, nb0, nb1, nb;             // prefix blocks in the list, tiles, blocks of the tiles and of both
 };
 
-// The CTA's k-th item: rounds of the grid run alternately up and down the
-// sorted list, which evens out what the CTAs get.
-__device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWork& w) {
-    const int P = gridDim.x, c = blockIdx.x;
-    const int64_t idx64 = (int64_t)k * P + ((k & 1) ? P - 1 - c : c);
-    if ((int64_t)k * P >= total) return false;
-    if (idx64 >= total) {
-        w.nb = w.nt = w.nb0 = w.nb1 = w.ntok = w.qpos = 0;
-        return true;                                     // nothing in this round
-    }
-    const int idx = (int)idx64, heads = a.N * a.hkv_s, e = idx / heads;
-    const int4 x = __ldg(reinterpret_cast<const int4*>(a.items + e)), y = __ldg(reinterpret_cast<const int4*>(a.items + e) + 1);
-    w.h = idx - e * heads;
-    w.r = w.h / a.hkv_s;
-    w.kvh = w.h - w.r * a.hkv_s;
+__device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork& w) {
+    const int4 x = __ldcg(reinterpret_cast<const int4*>(a.items + e)), y = __ldcg(reinterpret_cast<const int4*>(a.items + e) + 1);
+    w.h = h;
+    w.r = h / a.hkv_s;
+    w.kvh = h - w.r * a.hkv_s;
     w.t0 = x.x;
     w.ntok = x.y;
     w.b = x.z;
@@ -306,6 +313,20 @@ __device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWor
     w.nb0 = max(0, min(blk1, e0) - w.blk0);
     w.nb1 = w.nt > 1 ? max(0, min(blk1, e1) - w.blk0) : 0;
     w.nb = max(w.nb0, w.nb1);
+}
+
+// The CTA's k-th item: rounds of the grid run alternately up and down the
+// sorted list, which evens out what the CTAs get.
+__device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWork& w) {
+    const int P = gridDim.x, c = blockIdx.x;
+    const int64_t idx64 = (int64_t)k * P + ((k & 1) ? P - 1 - c : c);
+    if ((int64_t)k * P >= total) return false;
+    if (idx64 >= total) {
+        w.nb = w.nt = w.nb0 = w.nb1 = w.ntok = w.qpos = 0;
+        return true;                                     // nothing in this round
+    }
+    const int idx = (int)idx64, heads = a.N * a.hkv_s, e = idx / heads;
+    at_decode(a, e, idx - e * heads, w);
     return true;
 }
 
@@ -322,6 +343,36 @@ __device__ __forceinline__ int at_kend(const AtArgs& a, const AtWork& w) {
 }
 // whether the V block at own key `key0` has rows that some row of the item does not see
 __device__ __forceinline__ bool at_ragged(const AtWork& w, int key0) { return (int64_t)key0 + kAtK > (int64_t)w.qpos + 1; }
+
+// Row `m` of a V block: zeros where it lies behind the last key, and no
+// infinities or NaN. Whether it held one.
+template <int D>
+__device__ __forceinline__ int v_row_finite(unsigned char* block, int m, bool past) {
+    int found = 0;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll 1
+        for (int u = 0; u < 8; ++u) {
+            uint4* q = reinterpret_cast<uint4*>(block + m * 128 + c * (kAtK * 128) + ((u ^ (m & 7)) << 4));
+            if (past) {
+                *q = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            uint4 x = *q;
+            uint32_t* y = reinterpret_cast<uint32_t*>(&x);
+            bool hit = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if ((y[i] & 0x7F80u) == 0x7F80u) y[i] &= 0xFFFF0000u, hit = true;
+                if ((y[i] & 0x7F800000u) == 0x7F800000u) y[i] &= 0xFFFFu, hit = true;
+            }
+            if (hit) {
+                *q = x;
+                found = 1;
+            }
+        }
+    return found;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_constant__ AtArgs a) {
@@ -378,9 +429,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_trigger();
     pdl_wait();
-    const int total = *abort_flag ? 0 : a.ctl->n_items * (a.N * a.hkv_s);
+    pdl_trigger();                        // only now: the narrow kernel relies on the lists being there when it starts
+    const int total = *abort_flag ? 0 : a.ctl->n_wide * (a.N * a.hkv_s);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsIo));
@@ -659,31 +710,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_ragged, rp & 1, abort_flag, a.status)))) break;
                 ++rp;
                 first_ragged = min(first_ragged, key0);
-                // row m of the block: zeros behind the last key, and no infinities or NaN
-                unsigned char* row = ring + sv * Sh::KB + m * 128;
-                const bool past = key0 + m >= kend;
-#pragma unroll
-                for (int c = 0; c < Sh::NKB; ++c)
-#pragma unroll 1
-                    for (int u = 0; u < 8; ++u) {
-                        uint4* q = reinterpret_cast<uint4*>(row + c * (kAtK * 128) + ((u ^ (m & 7)) << 4));
-                        if (past) {
-                            *q = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 x = *q;
-                        uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-                        bool hit = false;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if ((y[i] & 0x7F80u) == 0x7F80u) y[i] &= 0xFFFF0000u, hit = true;
-                            if ((y[i] & 0x7F800000u) == 0x7F800000u) y[i] &= 0xFFFFu, hit = true;
-                        }
-                        if (hit) {
-                            *q = x;
-                            poison = 1;
-                        }
-                    }
+                poison |= v_row_finite<D>(ring + sv * Sh::KB, m, key0 + m >= kend);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 const bool any = __any_sync(0xffffffffu, poison);
                 __syncwarp();
@@ -781,6 +808,441 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     }
 }
 
+// ---------------------------------------------------------------------------
+// Items of at most 32 query rows (single tokens, most of a decode step): bound
+// by the bytes of K and V. With the queries as the rows of a tile, a product
+// would be mostly padding and a row's softmax the work of one thread; so the
+// keys are the rows: S^T = K Q^T (128 keys x 16 or 32 rows), and O^T = V^T P^T
+// (d x rows) with V read as the M-major operand and P^T from shared memory. A
+// thread has one key: its scores of every row are one column each. Two CTAs per
+// SM, each with its own ring, cover one another's waits; items are taken from
+// the list as CTAs become free.
+//   warps 0-3   the softmax of a block, one key per thread: maxima over the
+//               keys by redux and one exchange between the warps; P^T to shared
+//               memory in bf16; the previous block's O^T (one element of d per
+//               thread) from tensor memory to registers. m moves as in the wide
+//               kernel. The V rows that some row does not see are made finite
+//               by the thread of the key.
+//   warp 4      takes the items, TMA
+//   warp 5      products
+// ---------------------------------------------------------------------------
+
+constexpr int kAnThreads = 192;
+constexpr int kAnQueue = 4;               // items taken ahead
+
+template <int D>
+struct AnShape {
+    static constexpr int NKB = D / 64;
+    static constexpr int KB = kAtK * D * 2;
+    static constexpr int RING = D == 128 ? 3 : 6;
+    static constexpr int HEAD = 1024;                   // barriers, the queue, the warps' maxima
+    static constexpr int QB = kAtNarrow * D * 2;
+    static constexpr int PB = kAtNarrow * kAtK * 2;
+    // a block of 64-element V rows is read as if it had 128: the other half is whatever follows, up to KB bytes on
+    static constexpr int PAD = D == 64 ? KB - QB - PB : 0;
+    static constexpr int SMEM = RING * KB + QB + PB + PAD + HEAD;
+};
+static_assert(2 * (AnShape<128>::SMEM + 1024) <= 228 * 1024 && 2 * (AnShape<64>::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+
+__device__ __forceinline__ float redux_max(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+template <int D>
+struct AnCtx {
+    const AtArgs* a;
+    unsigned char *ring, *p;
+    uint64_t *s_full, *p_full, *o_full, *x_full, *x_empty, *v_ragged;
+    float* wmax;                          // [4][kAtNarrow]
+    volatile int *abort_flag, *s_poison;
+    uint32_t tmem, base, blocks, ragged, exchanges;   // base: ring index of the item's first block
+    int np;
+};
+
+// An item's softmax and results for NR = 16 or 32 rows; false: a wait gave up.
+template <int D, int NR>
+__device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
+    using Sh = AnShape<D>;
+    const AtArgs& a = *c.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = w.ntok * a.G, kend = at_kend(a, w);
+    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    float o[NR], l[NR];
+#pragma unroll
+    for (int n = 0; n < NR; ++n) o[n] = l[n] = 0.f;
+    float m_lane = -INFINITY, alpha_prev = 1.f;          // lane n: row n's m, and what it changed by in the last block
+    bool moved_prev = false;
+    int first_ragged = INT_MAX, poison = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, c.abort_flag, a.status));
+    };
+    // every warp's value of row n to lane n of all
+    auto exchange = [&](float mine, float (&x)[4]) {
+        if (!wait(c.x_empty, (c.exchanges & 1) ^ 1)) return false;
+        if (lane < NR) c.wmax[warp * kAtNarrow + lane] = mine;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.x_full);
+        if (!wait(c.x_full, c.exchanges & 1)) return false;
+        ++c.exchanges;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *const_cast<volatile float*>(&c.wmax[i * kAtNarrow + (lane & (NR - 1))]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.x_empty);
+        return true;
+    };
+    auto take_o = [&]() {                                // the last block's product onto the running sums
+        uint32_t x[NR];
+        if constexpr (NR == 32) tmem_ld32(c.tmem + 64 + lane_off, x);
+        else tmem_ld16(c.tmem + 64 + lane_off, x);
+        tmem_wait_ld();
+        if (moved_prev) {
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                o[n] = fmaf(o[n], __shfl_sync(0xffffffffu, alpha_prev, n), __uint_as_float(x[n]));
+        } else {
+#pragma unroll
+            for (int n = 0; n < NR; ++n) o[n] += __uint_as_float(x[n]);
+        }
+    };
+    for (int j = 0; j < w.nb; ++j, ++c.blocks) {
+        if (!wait(&c.s_full[c.blocks & 1], (c.blocks >> 1) & 1)) return false;
+        tc_fence_after();
+        uint32_t v[NR];
+        if constexpr (NR == 32) tmem_ld32(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
+        else tmem_ld16(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
+        tmem_wait_ld();
+        bool own;
+        const int key0 = at_block(w, j, own), key = key0 + tid;
+        // the first row that sees the thread's key
+        int first = 0;
+        if (own) first = key >= kend ? NR : (int)max((int64_t)0, min((int64_t)NR, ((int64_t)key - w.qpos) * a.G));
+        else if (key >= a.prefix_len) first = NR;
+        float mine = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float s = n >= first ? __uint_as_float(v[n]) : -INFINITY;
+            v[n] = __float_as_uint(s);
+            const float r = redux_max(s);
+            if (lane == n) mine = r;
+        }
+        float x[4];
+        if (!exchange(mine, x)) return false;
+        const float m_blk = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * a.scale_log2;
+        const bool grow = m_blk > m_lane + kAtRescale;
+        const float alpha = grow ? ex2_approx(m_lane - m_blk) : 1.f;
+        if (grow) m_lane = m_blk;
+        const bool moved = __any_sync(0xffffffffu, grow);
+        const float m_sub = m_lane == -INFINITY ? 0.f : m_lane;
+        if (moved)
+#pragma unroll
+            for (int n = 0; n < NR; ++n) l[n] *= __shfl_sync(0xffffffffu, alpha, n);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float e = ex2_approx(fmaf(__uint_as_float(v[n]), a.scale_log2, -__shfl_sync(0xffffffffu, m_sub, n)));
+            l[n] += e;
+            v[n] = __float_as_uint(e);
+        }
+        if (j > 0) {                                     // also: the products no longer read P^T
+            if (!wait(c.o_full, (c.blocks - 1) & 1)) return false;
+            tc_fence_after();
+            take_o();
+        }
+        alpha_prev = alpha;
+        moved_prev = moved;
+        // P^T: 64 keys per 128-byte row of one query row, rows in atoms of 8, 16-byte units swizzled
+        unsigned char* pr = c.p + (tid >> 6) * (kAtNarrow * 128) + (tid & 7) * 2;
+        const int unit = (tid & 63) >> 3;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+            *reinterpret_cast<bf16*>(pr + n * 128 + ((unit ^ (n & 7)) << 4)) = __float2bfloat16_rn(__uint_as_float(v[n]));
+        if (own && at_ragged(w, key0)) {
+            if (!wait(c.v_ragged, c.ragged & 1)) return false;
+            ++c.ragged;
+            first_ragged = min(first_ragged, key0);
+            // K and V of a block: K_0 K_1 V_0 K_2 V_1 ... V_last
+            const uint32_t iv = c.base + (j + 1 < w.nb ? 2 * j + 2 : 2 * j + 1);
+            const int hit = v_row_finite<D>(c.ring + (iv % Sh::RING) * Sh::KB, tid, key >= kend);
+            if (__any_sync(0xffffffffu, hit) && lane == 0) c.s_poison[c.np & 1] = c.np + 1;
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(c.p_full);
+    }
+    c.base += 2 * w.nb;
+    float l_lane = 0.f;
+    if (w.nb) {
+        if (!wait(c.o_full, (c.blocks - 1) & 1)) return false;
+        tc_fence_after();
+        take_o();
+        tc_fence_before();
+        // sums over the keys: each step halves the rows a lane holds; lane n ends with row n's
+#pragma unroll
+        for (int off = NR / 2; off; off >>= 1) {
+            const bool up = lane & off;
+#pragma unroll
+            for (int n = 0; n < off; ++n) {
+                const float keep = up ? l[n + off] : l[n], give = up ? l[n] : l[n + off];
+                l[n] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        }
+        if (NR == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+        float x[4];
+        if (!exchange(l[0], x)) return false;
+        l_lane = (x[0] + x[1]) + (x[2] + x[3]);
+        if (first_ragged != INT_MAX) {
+            poison = c.s_poison[c.np & 1] == c.np + 1;
+            ++c.np;
+        }
+        if (poison && tid < D) {                         // what the rows do see of the values that are not finite
+            const bf16* v = a.v[w.r] + ((int64_t)w.b * a.hkv_s + w.kvh) * a.max_kv * D + tid;
+            for (int key = first_ragged; key < kend; ++key) {
+                const float x = __bfloat162float(v[(int64_t)key * D]);
+                if (fabsf(x) < INFINITY) continue;
+                const int64_t first = ((int64_t)key - w.qpos) * a.G;
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (n >= first) o[n] += x;
+            }
+        }
+    }
+    if (w.part >= 0) {
+        const int64_t row0 = (int64_t)w.part + (int64_t)w.h * rows;
+        if (warp == 0 && lane < rows) a.part_ml[row0 + lane] = make_float2(m_lane, l_lane);
+        if (tid < D) {
+            float* dst = a.part_o + row0 * D + tid;
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+                if (n < rows) dst[n * D] = o[n];
+        }
+        return true;
+    }
+    const int64_t pos = (int64_t)w.qpos + lane / a.G;    // lane n: row n's
+    const float inv = pos >= 0 && pos < a.max_kv && l_lane != 0.f ? 1.f / l_lane : 0.f;
+    const unsigned zero = __ballot_sync(0xffffffffu, pos < 0 || pos >= a.max_kv || l_lane == 0.f);
+    bf16* dst = a.out + (((int64_t)w.r * a.T + w.t0) * a.hq_s + w.kvh * a.G) * D + tid;
+    int g = 0;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        const float f = __shfl_sync(0xffffffffu, inv, n);
+        if (n < rows && tid < D) dst[(int64_t)g * D] = __float2bfloat16_rn((zero >> n & 1) ? 0.f : o[n] * f);
+        if (++g == a.G) {
+            g = 0;
+            dst += (int64_t)a.hq_s * D;
+        }
+    }
+    return true;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid_constant__ AtArgs a) {
+    using Sh = AnShape<D>;
+    constexpr int R = Sh::RING;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    unsigned char* ring = smem;
+    unsigned char* sq = ring + R * Sh::KB;
+    unsigned char* sp = sq + Sh::QB;
+    unsigned char* head = sp + Sh::PB + Sh::PAD;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(head);
+    uint64_t* kv_full = bars;             // [R]
+    uint64_t* kv_empty = kv_full + R;     // [R]
+    uint64_t* q_full = kv_empty + R;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;       // [2]
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 1;
+    uint64_t* x_full = o_full + 1;        // the warps' maxima or sums are there
+    uint64_t* x_empty = x_full + 1;       // ... and read
+    uint64_t* v_ragged = x_empty + 1;
+    uint64_t* item_full = v_ragged + 1;   // [kAnQueue]
+    uint64_t* item_empty = item_full + kAnQueue;
+    uint64_t* done = item_empty + kAnQueue;
+    int* queue = reinterpret_cast<int*>(done + 1);                   // [kAnQueue]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(queue + kAnQueue);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
+    float* wmax = reinterpret_cast<float*>(head + Sh::HEAD - 4 * kAtNarrow * 4);
+    static_assert((2 * R + 9 + 2 * kAnQueue + 1) * 8 + (kAnQueue + 4) * 4 <= Sh::HEAD - 4 * kAtNarrow * 4, "the head's words");
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(&s_full[0], 1);
+        mbar_init(&s_full[1], 1);
+        mbar_init(p_full, 4);
+        mbar_init(o_full, 1);
+        mbar_init(x_full, 4);
+        mbar_init(x_empty, 4);
+        mbar_init(v_ragged, 1);
+        for (int i = 0; i < kAnQueue; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 5);
+        }
+        mbar_init(done, 1);
+        *abort_flag = (smem_u32(ring) & 1023u) ? 1 : 0;
+        s_poison[0] = s_poison[1] = 0;
+        if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
+        fence_mbar_init();
+    }
+    if (warp == 5) tmem_alloc(smem_u32(tmem_slot), 128);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // Behind the wide kernel the lists are there: it lets this one start only after its own wait. This kernel waits for
+    // the wide one at its end, so that what follows it follows both.
+    if (!a.after_wide) pdl_wait();
+    const int heads = a.N * a.hkv_s;
+    const int n_wide = __ldcg(&a.ctl->n_wide);
+    const int total = *abort_flag ? 0 : (__ldcg(&a.ctl->n_items) - n_wide) * heads;
+
+    // the i-th item of this CTA, -1 when there are no more
+    auto item = [&](int i, AtWork& w, bool& more) {
+        const int s = i % kAnQueue;
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&item_full[s], (i / kAnQueue) & 1, abort_flag, a.status));
+        if (!ok) return false;
+        const int idx = *reinterpret_cast<volatile int*>(&queue[s]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[s]);
+        more = idx >= 0;
+        if (more) at_decode(a, n_wide + idx / heads, idx % heads, w);
+        return true;
+    };
+
+    if (warp == 4) {
+        if (lane == 0) {
+            uint32_t it = 0, nq = 0;
+            const uint32_t q_bytes = (uint32_t)(kAtNarrow / a.G * a.G * 128 * Sh::NKB);
+            bool ok = !*abort_flag;
+            AtWork w;
+            for (int i = 0; ok; ++i) {
+                const int s = i % kAnQueue;
+                int idx = total ? atomicAdd(&a.ctl->next, 1) : 0;
+                if (idx >= total) idx = -1;
+                if (!(ok = mbar_wait(&item_empty[s], ((i / kAnQueue) & 1) ^ 1, abort_flag, a.status))) break;
+                *reinterpret_cast<volatile int*>(&queue[s]) = idx;
+                mbar_arrive(&item_full[s]);
+                if (idx < 0) break;
+                at_decode(a, n_wide + idx / heads, idx % heads, w);
+                const int grp = w.b * a.hkv_s + w.kvh;
+                auto load = [&](int j, bool v) {
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    const CUtensorMap* m = own ? (v ? &a.tv[w.r] : &a.tk[w.r]) : (v ? &a.pv[w.r] : &a.pk[w.r]);
+                    const int sl = it % R;
+                    if (!(ok = mbar_wait(&kv_empty[sl], ((it / R) & 1) ^ 1, abort_flag, a.status))) return;
+                    mbar_arrive_expect_tx(&kv_full[sl], Sh::KB);
+#pragma unroll
+                    for (int kb = 0; kb < Sh::NKB; ++kb)
+                        tma_load_3d_keep(ring + sl * Sh::KB + kb * (kAtK * 128), m, kb * 64, key0, own ? grp : w.kvh, &kv_full[sl]);
+                    ++it;
+                };
+                if (w.nb) {
+                    load(0, false);
+                    if (ok && (ok = mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag, a.status))) {
+                        mbar_arrive_expect_tx(q_full, q_bytes);
+#pragma unroll
+                        for (int kb = 0; kb < Sh::NKB; ++kb)
+                            tma_load_3d_keep(sq + kb * (kAtNarrow * 128), &a.tqn, kb * 64, w.kvh * a.G, w.r * a.T + w.t0, q_full);
+                        ++nq;
+                    }
+                }
+                for (int j = 0; j < w.nb && ok; ++j) {
+                    if (j + 1 < w.nb) load(j + 1, false);
+                    if (ok) load(j, true);
+                }
+            }
+            volatile int no_abort = 0;      // no copy may still be landing when the CTA exits
+            if (nq) mbar_wait(q_full, (nq - 1) & 1, &no_abort, nullptr);
+            for (uint32_t k = it > (uint32_t)R ? it - R : 0; k < it; ++k)
+                mbar_wait(&kv_full[k % R], (k / R) & 1, &no_abort, nullptr);
+        }
+    } else if (warp == 5) {
+        const uint64_t dq = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring)), dp = smem_desc_sw128(smem_u32(sp));
+        const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
+        uint32_t it = 0, blocks = 0, nq = 0;
+        bool ok = !*abort_flag, more = true;
+        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+            return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
+        };
+        AtWork w;
+        for (int i = 0; ok; ++i) {
+            if (!(ok = item(i, w, more)) || !more) break;
+            if (!w.nb) continue;
+            const int nr = w.ntok * a.G <= 16 ? 16 : 32;
+            const uint32_t id_s = idesc_bf16(kAtK, nr), id_o = idesc_bf16_amn(128, nr);
+            auto issue_s = [&](int j) {                  // S^T of block j into the buffer of its turn
+                const uint32_t s = it % R;
+                if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) return;
+                ++it;
+                tc_fence_after();
+                const uint64_t dk = at_desc_add(dk0, s * Sh::KB);
+#pragma unroll
+                for (int kb = 0; kb < Sh::NKB; ++kb)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_w(tmem + 32 * ((blocks + j) & 1), at_desc_add(dk, kb * (kAtK * 128) + k * 32),
+                                 at_desc_add(dq, kb * (kAtNarrow * 128) + k * 32), id_s, (kb | k) != 0);
+                tc_commit_w(smem_u32(&s_full[(blocks + j) & 1]));
+                tc_commit_w(smem_u32(&kv_empty[s]));
+                if (j + 1 == w.nb) tc_commit_w(smem_u32(q_empty));
+            };
+            if (!(ok = wait_all(q_full, nq & 1))) break;
+            ++nq;
+            issue_s(0);
+            for (int j = 0; j < w.nb && ok; ++j) {
+                if (j + 1 < w.nb) issue_s(j + 1);
+                if (!ok) break;
+                const uint32_t s = it % R;
+                if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) break;
+                ++it;
+                bool own;
+                const int key0 = at_block(w, j, own);
+                if (own && at_ragged(w, key0) && lane == 0) mbar_arrive(v_ragged);
+                __syncwarp();
+                if (!(ok = wait_all(p_full, (blocks + j) & 1))) break;
+                tc_fence_after();
+                const int valid = min(kAtK, (own ? at_kend(a, w) : a.prefix_len) - key0), steps = (valid + 15) >> 4;
+                const uint64_t dv = at_desc_add(dv0, s * Sh::KB);
+#pragma unroll 1
+                for (int kk = 0; kk < steps; ++kk)       // O^T of the block alone
+                    tc_mma_w(tmem + 64, at_desc_add(dv, kk * 16 * 128),
+                             at_desc_add(dp, (kk >> 2) * (kAtNarrow * 128) + (kk & 3) * 32), id_o, kk != 0);
+                tc_commit_w(smem_u32(o_full));
+                tc_commit_w(smem_u32(&kv_empty[s]));
+            }
+            blocks += w.nb;
+        }
+        tc_commit_w(smem_u32(done));
+    } else {
+        AnCtx<D> c{&a, ring, sp, s_full, p_full, o_full, x_full, x_empty, v_ragged, wmax, abort_flag, s_poison, tmem, 0, 0, 0, 0, 0};
+        bool ok = !*abort_flag, more = true;
+        AtWork w;
+        for (int i = 0; ok; ++i) {
+            if (!(ok = item(i, w, more)) || !more) break;
+            ok = w.ntok * a.G <= 16 ? an_item<D, 16>(c, w) : an_item<D, 32>(c, w);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        volatile int no_abort = 0;                   // every MMA has retired before the columns are freed
+        mbar_wait(done, 0, &no_abort, nullptr);
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 128);
+        tmem_relinquish();
+    }
+    pdl_wait();
+}
+
 // One warp per output row: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
 // over the row's own parts, then its prefix tile's, in their order.
 template <int D>
@@ -874,15 +1336,16 @@ cudaError_t attn_map(const void* base, int64_t d0, int64_t d1, int64_t d2, int64
 
 AttnSizes attn_sizes(int64_t B, int64_t T, int hq, int hkv, int d) {
     const int64_t G = hq / hkv, per = 2 * (kAtM / G);
-    const int64_t tiles = T / per + B + 1, prefix = T / per + 2, extra = 2 * kSMs / hkv + 2;
+    // extra parts: their number times the target is at most all blocks
+    const int64_t tiles = T / per + B + 1, prefix = T / per + 2, extra = 2 * kSMs / hkv + 2, extra_n = 5 * kSMs / hkv + 2;
     AttnSizes s;
-    s.items = (size_t)(tiles + prefix + extra) * sizeof(AttnItem);
+    s.items = (size_t)(tiles + prefix + extra + extra_n) * sizeof(AttnItem);
     s.groups = (size_t)tiles * sizeof(AttnGroup);
     s.prefix_groups = (size_t)prefix * sizeof(int2);
     s.chunks = (size_t)(T * G / 8 + tiles) * sizeof(int);
     // every row once as a sequence's own and once as the prefix's, and the extra parts' rows
     const int64_t most = T < per ? T : per;
-    s.rows = 2 * T * hq + extra * hkv * most * G;
+    s.rows = 2 * T * hq + extra * hkv * most * G + extra_n * hkv * (most * G < kAtNarrow ? most * G : kAtNarrow);
     s.part_ml = (size_t)s.rows * sizeof(float2);
     s.part_o = (size_t)s.rows * d * sizeof(float);
     return s;
@@ -915,6 +1378,7 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     a.ctl = p.ctl;
     const int64_t D = p.d;
     cudaError_t e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, a.tpt, &a.tq);
+    if (e == cudaSuccess) e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, kAtNarrow / G, &a.tqn);
     for (int r = 0; r < p.N && e == cudaSuccess; ++r) {
         a.v[r] = static_cast<const bf16*>(p.vc[r]);
         const int64_t groups = (int64_t)p.max_batch * p.hkv_s, rows = p.max_kv;
@@ -926,19 +1390,27 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
         }
     }
     if (e != cudaSuccess) return e;
-    const bool wide = p.d == 128;
-    const void* fn = wide ? reinterpret_cast<const void*>(attn_items_kernel<128>)
-                          : reinterpret_cast<const void*>(attn_items_kernel<64>);
-    const int smem = wide ? AtShape<128>::SMEM : AtShape<64>::SMEM;
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    const bool d128 = p.d == 128;
     void* args[] = {&a};
-    e = launch_pdl(fn, args, kSMs, smem, s, kAtThreads);
+    a.after_wide = p.T * (int64_t)G > kAtNarrow;         // else no item can have more rows
+    if (a.after_wide) {
+        const void* fn = d128 ? reinterpret_cast<const void*>(attn_items_kernel<128>)
+                              : reinterpret_cast<const void*>(attn_items_kernel<64>);
+        const int smem = d128 ? AtShape<128>::SMEM : AtShape<64>::SMEM;
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kAtThreads);
+        if (e != cudaSuccess) return e;
+    }
+    const void* fn = d128 ? reinterpret_cast<const void*>(attn_narrow_kernel<128>)
+                          : reinterpret_cast<const void*>(attn_narrow_kernel<64>);
+    const int smem = d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM;
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(fn, args, 2 * kSMs, smem, s, kAnThreads);
     if (e != cudaSuccess) return e;
     RaggedAttnParams c = p;
     void* cargs[] = {&c};
     const int64_t units = ((int64_t)p.T * G / 8 + p.B) * p.N * p.hkv_s;
-    return launch_pdl(wide ? reinterpret_cast<const void*>(attn_combine_kernel<128>)
+    return launch_pdl(d128 ? reinterpret_cast<const void*>(attn_combine_kernel<128>)
                            : reinterpret_cast<const void*>(attn_combine_kernel<64>),
                       cargs, (int)(units < 8 * kSMs ? units : 8 * kSMs), 0, s, 256);
 }

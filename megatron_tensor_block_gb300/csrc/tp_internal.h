@@ -328,8 +328,9 @@ cudaError_t launch_lm_head(const HeadArgs& a, size_t smem, cudaStream_t s);
 // Attention of a packed batch (kernels_attn.cu).
 struct AttnCtl {
     int n_tokens;                         // cu[B], or 0 where cu is malformed
-    int n_items, n_groups, n_chunks;
-    int reserved[12];
+    int n_wide, n_items, n_groups, n_chunks;   // items: n_wide wide ones, then the narrow ones
+    int next;                             // narrow items taken
+    int reserved[10];
 };
 struct AttnItem {                         // for every KV head of every shard:
     int t0, ntok;                         // token rows
