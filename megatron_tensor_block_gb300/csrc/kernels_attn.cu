@@ -284,6 +284,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// mbar_wait in two halves: a try in line, and the bounded wait out of line, which keeps the loops' code short.
+__device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+    const uint64_t t0 = global_ns();
+    while (true) {
+        if (mbar_try_at(bar, parity)) return true;
+        if (*abort) return false;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            *abort = 1;
+            set_status(status, TP_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 __device__ __forceinline__ uint64_t at_desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
 // One item for one KV head of one shard. nb[t]: key blocks of tile t.
@@ -328,6 +351,19 @@ __device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWor
     const int idx = (int)idx64, heads = a.N * a.hkv_s, e = idx / heads;
     at_decode(a, e, idx - e * heads, w);
     return true;
+}
+
+// A value that is the same in every lane, in a form that lets the compiler know.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ void uniform(AtWork& w) {
+    w.qpos = uniform(w.qpos);
+    w.ntok = uniform(w.ntok);
+    w.blk0 = uniform(w.blk0);
+    w.nP = uniform(w.nP);
+    w.nt = uniform(w.nt);
+    w.nb0 = uniform(w.nb0);
+    w.nb1 = uniform(w.nb1);
+    w.nb = uniform(w.nb);
 }
 
 // Block j of an item: its first key in the prefix (own = false) or in the sequence's own cache.
@@ -400,7 +436,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     unsigned char* ring = sq + 2 * Sh::QB;
     float2* stat = reinterpret_cast<float2*>(ring + R * Sh::KB);     // [2][kAtM]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
@@ -428,10 +464,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*tmem_slot);
     pdl_wait();
     pdl_trigger();                        // only now: the narrow kernel relies on the lists being there when it starts
-    const int total = *abort_flag ? 0 : a.ctl->n_wide * (a.N * a.hkv_s);
+    const int total = uniform(*abort_flag ? 0 : a.ctl->n_wide * (a.N * a.hkv_s));
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsIo));
@@ -478,34 +514,43 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 mbar_wait(&kv_full[k % R], (k / R) & 1, &no_abort, nullptr);
         } else if (warp == 1) {
             // ---------------------------------------------------------------- products
-            // the whole warp runs the loop (warp-uniform operands); one elected lane issues
+            // The whole warp runs the loop on warp-uniform values and one elected lane issues. What runs between two
+            // blocks' products costs the tensor cores' time (instructions come in at tens of cycles per 128 bytes of
+            // code when four roles share the caches), so the common block has a short path of its own.
             const uint32_t id_s = idesc_bf16(kAtM, kAtK), id_o = idesc_bf16_bmn(kAtM, D);
             const uint64_t dq0 = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring));
             const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
-            uint32_t base = 0, ph = 0;      // phase bits: q_full 0, 1; p_full 2, 3; o_empty 4, 5; v_clean 6
-            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
+            const uint32_t bar0 = smem_u32(kv_full), emp0 = smem_u32(kv_empty), sf0 = smem_u32(s_full), pf0 = smem_u32(p_full);
+            uint32_t ph = 0;                // phase bits: q_full 0, 1; p_full 2, 3; o_empty 4, 5; v_clean 6
+            uint32_t slot = 0, sph = 0;     // the ring's next slot and its phase
+            auto wait_at = [&](uint32_t bar, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, mbar_try_at(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, a.status));
             };
-            auto try_all = [&](uint64_t* bar, uint32_t parity) { return (bool)__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); };
             auto flip = [&](int bit) {
                 const uint32_t v = (ph >> bit) & 1;
                 ph ^= 1u << bit;
                 return v;
             };
-            auto issue_s = [&](int t, uint32_t slot, bool last) {          // S_t = Q_t K^T
-                const uint64_t dq = at_desc_add(dq0, t * Sh::QB), dk = at_desc_add(dk0, slot * Sh::KB);
+            auto step = [&]() {
+                if (++slot == R) slot = 0, sph ^= 1;
+            };
+            auto issue_s = [&](int t, uint32_t sl, bool last) {            // S_t = Q_t K^T
+                const uint64_t dq = at_desc_add(dq0, t * Sh::QB), dk = at_desc_add(dk0, sl * Sh::KB);
 #pragma unroll
                 for (int kb = 0; kb < Sh::NKB; ++kb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_w(tmem + kAtK * t, at_desc_add(dq, kb * (kAtM * 128) + k * 32),
-                                 at_desc_add(dk, kb * (kAtK * 128) + k * 32), id_s, (kb | k) != 0);
-                tc_commit_w(smem_u32(&s_full[t]));
+                    tc_mma4_w(tmem + kAtK * t, at_desc_add(dq, kb * (kAtM * 128)), at_desc_add(dk, kb * (kAtK * 128)), 2, 2,
+                              id_s, kb != 0);
+                tc_commit_w(sf0 + 8 * t);
                 if (last) tc_commit_w(smem_u32(&q_empty[t]));
+            };
+            auto issue_o = [&](int t, uint64_t dv, bool first) {           // O_t += P_t V, all 128 keys
+                tc_mma4_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t, dv, 8, 128, id_o, !first);
+                tc_mma4_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 32, at_desc_add(dv, 8192), 8, 128, id_o, 1);
             };
             auto next = [&](int& k, AtWork& w) {            // the next item with key blocks
                 while (at_item(a, total, k, w)) {
                     ++k;
+                    uniform(w);
                     if (w.nb) return true;
                 }
                 w.nb = 0;
@@ -516,79 +561,114 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
             bool have = next(k, cur);
             bool ok = true;
             if (have) {
-                ok = wait_all(&kv_full[0], 0);
+                ok = wait_at(bar0, 0);
                 for (int t = 0; t < cur.nt && ok; ++t) {
                     const int n = t ? cur.nb1 : cur.nb0;
                     if (!n) continue;
-                    if (!(ok = wait_all(&q_full[t], flip(t)))) break;
+                    if (!(ok = wait_at(smem_u32(&q_full[t]), flip(t)))) break;
                     tc_fence_after();
                     issue_s(t, 0, n == 1);
                 }
-                tc_commit_w(smem_u32(&kv_empty[0]));
+                tc_commit_w(emp0);
+                step();
             }
             while (have && ok) {
                 const bool more = next(k, nxt);
+                const int kend = at_kend(a, cur);
+                // blocks 1 .. plain - 1 are whole, seen by every row, and followed by one of both tiles; the prefix's last
+                // block may be cut short
+                int plain = min(cur.nb0, cur.nb1) - 1;
+                const int own0 = cur.nP - cur.blk0;         // the item's first own block
+                plain = min(plain, own0 + max(0, (cur.qpos + 1) / kAtK));
+                const int cut = a.prefix_len % kAtK ? own0 - 1 : -1;
                 for (int j = 0; j < cur.nb && ok; ++j) {
-                    const uint32_t iv = base + 2 * j + 1, sv = iv % R, in = iv + 1, sn = in % R;   // V of j, the K behind it
+                    if (j >= 1 && j < plain && j != cut) {
+                        const uint32_t sv = slot, pv = sph;
+                        step();
+                        if (!(ok = wait_at(bar0 + 8 * sv, pv) && wait_at(pf0, (ph >> 2) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t dv = at_desc_add(dv0, sv * Sh::KB);
+                        issue_o(0, dv, false);
+                        if (!(ok = wait_at(bar0 + 8 * slot, sph))) break;
+                        tc_fence_after();
+                        issue_s(0, slot, j + 2 == cur.nb0);
+                        if (!(ok = wait_at(pf0 + 8, (ph >> 3) & 1))) break;
+                        tc_fence_after();
+                        issue_o(1, dv, false);
+                        issue_s(1, slot, j + 2 == cur.nb1);
+                        ph ^= 12;
+                        tc_commit_w(emp0 + 8 * sv);
+                        tc_commit_w(emp0 + 8 * slot);
+                        step();
+                        continue;
+                    }
+                    const uint32_t sv = slot, pv = sph;     // V of block j; the K behind it is the slot after
+                    step();
                     const bool last = j + 1 == cur.nb;
-                    const bool follow = !last || more;      // some S is issued behind this block's products
                     bool own;
                     const int key0 = at_block(cur, j, own);
-                    const int valid = min(kAtK, (own ? at_kend(a, cur) : a.prefix_len) - key0);
+                    const int valid = min(kAtK, (own ? kend : a.prefix_len) - key0);
                     const int steps = (valid + 15) >> 4;
-                    if (!(ok = wait_all(&kv_full[sv], (iv / R) & 1))) break;
+                    if (!(ok = wait_at(bar0 + 8 * sv, pv))) break;
                     bool ragged = own && at_ragged(cur, key0);
                     if (ragged && lane == 0) mbar_arrive(v_ragged);
                     __syncwarp();
                     const uint64_t dv = at_desc_add(dv0, sv * Sh::KB);
                     bool k_ready = false;
                     unsigned issued = 0;
+#pragma unroll 1
                     for (int t = 0; t < 2 && ok; ++t) {
                         const int n = t ? cur.nb1 : cur.nb0;
                         if (j < n) {
-                            if (!(ok = wait_all(&p_full[t], flip(2 + t)))) break;
-                            if (j == 0 && !(ok = wait_all(&o_empty[t], flip(4 + t) ^ 1))) break;
-                            if (ragged && !(ok = wait_all(v_clean, flip(6)))) break;
+                            if (!(ok = wait_at(pf0 + 8 * t, flip(2 + t)))) break;
+                            if (j == 0 && !(ok = wait_at(smem_u32(&o_empty[t]), flip(4 + t) ^ 1))) break;
+                            if (ragged && !(ok = wait_at(smem_u32(v_clean), flip(6)))) break;
                             ragged = false;
                             tc_fence_after();
+                            if (steps == kAtK / 16) {
+                                issue_o(t, dv, j == 0);
+                            } else {
 #pragma unroll 1
-                            for (int kk = 0; kk < steps; ++kk)
-                                tc_mma_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 8 * kk, at_desc_add(dv, kk * 16 * 128),
-                                            id_o, (j | kk) != 0);
+                                for (int kk = 0; kk < steps; ++kk)
+                                    tc_mma_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 8 * kk, at_desc_add(dv, kk * 16 * 128),
+                                                id_o, (j | kk) != 0);
+                            }
                             if (j + 1 == n) tc_commit_w(smem_u32(&o_full[t]));
                         }
                         if (!last) {
                             if (j + 1 < n) {
-                                if (!k_ready && !(ok = wait_all(&kv_full[sn], (in / R) & 1))) break;
-                                if (!k_ready) tc_fence_after();
-                                k_ready = true;
-                                issue_s(t, sn, j + 2 == n);
-                            }
-                        } else if (more && (t ? nxt.nb1 : nxt.nb0) && t == 0) {
-                            // the next item's first S behind this tile's last product, if its operands are there
-                            if (try_all(&kv_full[sn], (in / R) & 1) && try_all(&q_full[t], (ph >> t) & 1)) {
-                                flip(t);
+                                if (!k_ready && !(ok = wait_at(bar0 + 8 * slot, sph))) break;
                                 tc_fence_after();
-                                issue_s(t, sn, (t ? nxt.nb1 : nxt.nb0) == 1);
-                                issued |= 1u << t;
+                                k_ready = true;
+                                issue_s(t, slot, j + 2 == n);
+                            }
+                        } else if (more && t == 0 && nxt.nb0) {
+                            // the next item's first S behind this tile's last product, if its operands are there
+                            if (__all_sync(0xffffffffu, mbar_try_at(bar0 + 8 * slot, sph) && mbar_try_at(smem_u32(&q_full[0]), ph & 1))) {
+                                flip(0);
+                                tc_fence_after();
+                                issue_s(0, slot, nxt.nb0 == 1);
+                                issued = 1;
                             }
                         }
                     }
                     if (!ok) break;
-                    tc_commit_w(smem_u32(&kv_empty[sv]));   // every MMA reading V has been issued
+                    tc_commit_w(emp0 + 8 * sv);             // every MMA reading V has been issued
                     if (last && more) {
-                        if (!(ok = wait_all(&kv_full[sn], (in / R) & 1))) break;
+                        if (!(ok = wait_at(bar0 + 8 * slot, sph))) break;
                         for (int t = 0; t < nxt.nt && ok; ++t) {
                             const int n = t ? nxt.nb1 : nxt.nb0;
                             if (!n || (issued >> t & 1)) continue;
-                            if (!(ok = wait_all(&q_full[t], flip(t)))) break;
+                            if (!(ok = wait_at(smem_u32(&q_full[t]), flip(t)))) break;
                             tc_fence_after();
-                            issue_s(t, sn, n == 1);
+                            issue_s(t, slot, n == 1);
                         }
                     }
-                    if (follow && ok) tc_commit_w(smem_u32(&kv_empty[sn]));
+                    if ((!last || more) && ok) {
+                        tc_commit_w(emp0 + 8 * slot);
+                        step();
+                    }
                 }
-                base += 2 * cur.nb;
                 cur = nxt;
                 have = more;
             }

@@ -105,6 +105,32 @@ __device__ __forceinline__ void tc_mma_ts_w(uint32_t d_tmem, uint32_t a_tmem, ui
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Four products in a row with one election: K steps `astep` and `bstep`
+// (descriptor units of 16 bytes, or tensor-memory columns) apart.
+__device__ __forceinline__ void tc_mma4_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint64_t astep, uint64_t bstep,
+                                          uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\tsetp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %10, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %4, %10, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %6, %10, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %8, %10, t;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "l"(a + astep), "l"(b + bstep), "l"(a + 2 * astep), "l"(b + 2 * bstep), "l"(a + 3 * astep),
+        "l"(b + 3 * bstep), "r"(accumulate), "r"(idesc)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma4_ts_w(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t astep, uint64_t bstep,
+                                             uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\tsetp.ne.b32 p, %9, 0;\n\tsetp.eq.b32 t, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %10, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%3], %4, %10, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%5], %6, %10, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%7], %8, %10, t;\n\t}" ::"r"(d_tmem),
+        "r"(a), "l"(b), "r"(a + astep), "l"(b + bstep), "r"(a + 2 * astep), "l"(b + 2 * bstep), "r"(a + 3 * astep),
+        "l"(b + 3 * bstep), "r"(accumulate), "r"(idesc)
+        : "memory");
+}
 __device__ __forceinline__ void tc_commit_w(uint32_t mbar_smem) {
     asm volatile(
         "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
