@@ -207,10 +207,11 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
 // key blocks; both tiles use every block that is loaded.
 //   warp 0        TMA: the Q tiles, then K and V blocks of 128 keys, in the
 //                 order in which they are used, into a ring of slots;
-//   warp 1        tensor memory (S_0, S_1, O_0, O_1) and the MMAs: S_t = Q_t K^T;
-//                 O_t += P_t V with P_t read from tensor memory (bf16, over
-//                 S_t). While one tile's softmax runs, the other's products do,
-//                 and the next item's S_t is issued behind this item's last O_t;
+//   warps 1, 2    the products of tile 0 and 1 in tensor memory (S_0, S_1, O_0,
+//                 O_1): S_t = Q_t K^T; O_t += P_t V with P_t read from tensor
+//                 memory (bf16, over S_t), in halves as the softmax writes it.
+//                 While one tile's softmax runs, the other's products do, and
+//                 the next item's S_t is issued behind this item's last O_t;
 //   warps 4-7,    softmax of tile 0 and 1, one row per thread: masked maximum,
 //   8-11          P = 2^(S - m) rounded to bf16 (its sum is taken before), m
 //                 moving only when a row's maximum grows by more than 2^8
@@ -419,7 +420,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     uint64_t* q_full = bars;              // [2] per tile
     uint64_t* q_empty = q_full + 2;       // [2]
     uint64_t* s_full = q_empty + 2;       // [2]
-    uint64_t* p_full = s_full + 2;        // [2]
+    uint64_t* p_half = s_full + 2;        // [2] P of the first 64 keys
+    uint64_t* p_full = p_half + 2;        // [2]
     uint64_t* o_full = p_full + 2;        // [2] an item's last product of the tile
     uint64_t* o_empty = o_full + 2;       // [2] O has been read
     uint64_t* st_full = o_empty + 2;      // [2] (m, l)
@@ -428,7 +430,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     uint64_t* kv_empty = kv_full + R;     // [R]
     uint64_t* v_ragged = kv_empty + R;    // a ragged V block has arrived ...
     uint64_t* v_clean = v_ragged + 1;     // ... and is finite
-    uint64_t* done = v_clean + 1;
+    uint64_t* turn = v_clean + 1;         // [2] whose products are next
+    uint64_t* done = turn + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
@@ -442,6 +445,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
+            mbar_init(&p_half[i], 4);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&o_empty[i], 4);
@@ -450,11 +454,13 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
         }
         for (int i = 0; i < R; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_empty[i], 2);
         }
-        mbar_init(v_ragged, 1);
+        mbar_init(v_ragged, 2);
         mbar_init(v_clean, 4);
-        mbar_init(done, 1);
+        mbar_init(&turn[0], 1);
+        mbar_init(&turn[1], 1);
+        mbar_init(done, 2);
         *abort_flag = (smem_u32(sq) & 1023u) ? 1 : 0;
         s_poison[0] = s_poison[1] = 0;
         if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
@@ -512,165 +518,129 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 if (nq[t]) mbar_wait(&q_full[t], (nq[t] - 1) & 1, &no_abort, nullptr);
             for (uint32_t k = it > (uint32_t)R ? it - R : 0; k < it; ++k)
                 mbar_wait(&kv_full[k % R], (k / R) & 1, &no_abort, nullptr);
-        } else if (warp == 1) {
+        } else if (warp == 1 || warp == 2) {
             // ---------------------------------------------------------------- products
-            // The whole warp runs the loop on warp-uniform values and one elected lane issues. What runs between two
-            // blocks' products costs the tensor cores' time (instructions come in at tens of cycles per 128 bytes of
-            // code when four roles share the caches), so the common block has a short path of its own.
+            // A warp for each tile. The products queue only a few deep, so what a warp does between them is lost to the
+            // tensor cores unless the other's are under way. They take turns, a block's products each: mixed with the
+            // other's, a tile's would take twice as long, and both softmaxes would then wait and run together. The whole warp runs the loop on warp-uniform values and one
+            // elected lane issues; the common block has a short path of its own.
+            const int t = warp - 1;
             const uint32_t id_s = idesc_bf16(kAtM, kAtK), id_o = idesc_bf16_bmn(kAtM, D);
-            const uint64_t dq0 = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring));
+            const uint64_t dq = smem_desc_sw128(smem_u32(sq) + t * Sh::QB), dk0 = smem_desc_sw128(smem_u32(ring));
             const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
-            const uint32_t bar0 = smem_u32(kv_full), emp0 = smem_u32(kv_empty), sf0 = smem_u32(s_full), pf0 = smem_u32(p_full);
-            uint32_t ph = 0;                // phase bits: q_full 0, 1; p_full 2, 3; o_empty 4, 5; v_clean 6
+            const uint32_t full0 = smem_u32(kv_full), empty0 = smem_u32(kv_empty), sf = smem_u32(&s_full[t]),
+                           ph = smem_u32(&p_half[t]), pf = smem_u32(&p_full[t]);
+            const uint32_t ts = tmem + kAtK * t, to = tmem + 2 * kAtK + D * t;
             uint32_t slot = 0, sph = 0;     // the ring's next slot and its phase
+            uint32_t pp = 0, ip = 0, rp = 0, tp = 0;        // phases: blocks and items of the tile, ragged blocks, turns
+            bool ok = true;
             auto wait_at = [&](uint32_t bar, uint32_t parity) {
                 return (bool)__all_sync(0xffffffffu, mbar_try_at(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, a.status));
             };
-            auto flip = [&](int bit) {
-                const uint32_t v = (ph >> bit) & 1;
-                ph ^= 1u << bit;
-                return v;
+            const uint32_t mine = smem_u32(&turn[t]), other = smem_u32(&turn[1 - t]);
+            auto take = [&]() { return wait_at(mine, (tp++ & 1) ^ (t == 0)); };
+            auto pass = [&]() {
+                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(other) : "memory");
+                __syncwarp();
             };
-            auto step = [&]() {
+            auto release = [&]() {                          // once the products so far are done
+                tc_commit_w(empty0 + 8 * slot);
                 if (++slot == R) slot = 0, sph ^= 1;
             };
-            auto issue_s = [&](int t, uint32_t sl, bool last) {            // S_t = Q_t K^T
-                const uint64_t dq = at_desc_add(dq0, t * Sh::QB), dk = at_desc_add(dk0, sl * Sh::KB);
+            auto issue_s = [&](bool last) {                 // S = Q K^T
+                const uint64_t dk = at_desc_add(dk0, slot * Sh::KB);
 #pragma unroll
                 for (int kb = 0; kb < Sh::NKB; ++kb)
-                    tc_mma4_w(tmem + kAtK * t, at_desc_add(dq, kb * (kAtM * 128)), at_desc_add(dk, kb * (kAtK * 128)), 2, 2,
-                              id_s, kb != 0);
-                tc_commit_w(sf0 + 8 * t);
+                    tc_mma4_w(ts, at_desc_add(dq, kb * (kAtM * 128)), at_desc_add(dk, kb * (kAtK * 128)), 2, 2, id_s, kb != 0);
+                tc_commit_w(sf);
                 if (last) tc_commit_w(smem_u32(&q_empty[t]));
             };
-            auto issue_o = [&](int t, uint64_t dv, bool first) {           // O_t += P_t V, all 128 keys
-                tc_mma4_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t, dv, 8, 128, id_o, !first);
-                tc_mma4_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 32, at_desc_add(dv, 8192), 8, 128, id_o, 1);
+            auto issue_o = [&](bool first, int half) {      // O += P V, 64 of the 128 keys
+                tc_mma4_ts_w(to, ts + 32 * half, at_desc_add(dv0, slot * Sh::KB + 8192 * half), 8, 128, id_o, !first);
             };
-            auto next = [&](int& k, AtWork& w) {            // the next item with key blocks
-                while (at_item(a, total, k, w)) {
-                    ++k;
-                    uniform(w);
-                    if (w.nb) return true;
-                }
-                w.nb = 0;
-                return false;
-            };
-            int k = 0;
-            AtWork cur, nxt;
-            bool have = next(k, cur);
-            bool ok = true;
-            if (have) {
-                ok = wait_at(bar0, 0);
-                for (int t = 0; t < cur.nt && ok; ++t) {
-                    const int n = t ? cur.nb1 : cur.nb0;
-                    if (!n) continue;
-                    if (!(ok = wait_at(smem_u32(&q_full[t]), flip(t)))) break;
-                    tc_fence_after();
-                    issue_s(t, 0, n == 1);
-                }
-                tc_commit_w(emp0);
-                step();
-            }
-            while (have && ok) {
-                const bool more = next(k, nxt);
-                const int kend = at_kend(a, cur);
-                // blocks 1 .. plain - 1 are whole, seen by every row, and followed by one of both tiles; the prefix's last
-                // block may be cut short
-                int plain = min(cur.nb0, cur.nb1) - 1;
-                const int own0 = cur.nP - cur.blk0;         // the item's first own block
-                plain = min(plain, own0 + max(0, (cur.qpos + 1) / kAtK));
+            AtWork w;
+            for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+                uniform(w);
+                if (!w.nb) continue;
+                const int n = t ? w.nb1 : w.nb0, kend = at_kend(a, w);
+                // blocks 1 .. plain - 1 are whole, seen by every row and followed by one of the tile; the prefix's last one
+                // may be cut short
+                const int own0 = w.nP - w.blk0;             // the item's first own block
+                const int plain = min(n - 1, own0 + max(0, (w.qpos + 1) / kAtK));
                 const int cut = a.prefix_len % kAtK ? own0 - 1 : -1;
-                for (int j = 0; j < cur.nb && ok; ++j) {
+                if (!(ok = wait_at(full0 + 8 * slot, sph))) break;
+                if (n && !(ok = wait_at(smem_u32(&q_full[t]), ip & 1))) break;
+                if (!(ok = take())) break;
+                if (n) {
+                    tc_fence_after();
+                    issue_s(n == 1);
+                }
+                pass();
+                release();
+                for (int j = 0; j < w.nb; ++j) {
                     if (j >= 1 && j < plain && j != cut) {
-                        const uint32_t sv = slot, pv = sph;
-                        step();
-                        if (!(ok = wait_at(bar0 + 8 * sv, pv) && wait_at(pf0, (ph >> 2) & 1))) break;
-                        tc_fence_after();
-                        const uint64_t dv = at_desc_add(dv0, sv * Sh::KB);
-                        issue_o(0, dv, false);
-                        if (!(ok = wait_at(bar0 + 8 * slot, sph))) break;
-                        tc_fence_after();
-                        issue_s(0, slot, j + 2 == cur.nb0);
-                        if (!(ok = wait_at(pf0 + 8, (ph >> 3) & 1))) break;
-                        tc_fence_after();
-                        issue_o(1, dv, false);
-                        issue_s(1, slot, j + 2 == cur.nb1);
-                        ph ^= 12;
-                        tc_commit_w(emp0 + 8 * sv);
-                        tc_commit_w(emp0 + 8 * slot);
-                        step();
+                        const int stop = cut > j && cut < plain ? cut : plain;
+                        while (true) {
+                            const uint32_t sk = slot + 1 == R ? 0 : slot + 1;
+                            if (!(ok = wait_at(full0 + 8 * slot, sph) && wait_at(full0 + 8 * sk, sk ? sph : sph ^ 1) &&
+                                       wait_at(ph, pp & 1) && take())) break;
+                            tc_fence_after();
+                            issue_o(false, 0);
+                            if (!(ok = wait_at(pf, pp & 1))) break;
+                            tc_fence_after();
+                            issue_o(false, 1);
+                            ++pp;
+                            release();
+                            issue_s(j + 2 == n);
+                            pass();
+                            release();
+                            if (++j == stop) break;
+                        }
+                        if (!ok) break;
+                        --j;
                         continue;
                     }
-                    const uint32_t sv = slot, pv = sph;     // V of block j; the K behind it is the slot after
-                    step();
-                    const bool last = j + 1 == cur.nb;
                     bool own;
-                    const int key0 = at_block(cur, j, own);
-                    const int valid = min(kAtK, (own ? kend : a.prefix_len) - key0);
-                    const int steps = (valid + 15) >> 4;
-                    if (!(ok = wait_at(bar0 + 8 * sv, pv))) break;
-                    bool ragged = own && at_ragged(cur, key0);
-                    if (ragged && lane == 0) mbar_arrive(v_ragged);
-                    __syncwarp();
-                    const uint64_t dv = at_desc_add(dv0, sv * Sh::KB);
-                    bool k_ready = false;
-                    unsigned issued = 0;
+                    const int key0 = at_block(w, j, own);
+                    if (!(ok = wait_at(full0 + 8 * slot, sph))) break;
+                    const bool ragged = own && at_ragged(w, key0);
+                    if (ragged) {                           // both warps, for every ragged block: no phase is passed over
+                        if (lane == 0) mbar_arrive(v_ragged);
+                        __syncwarp();
+                        if (!(ok = wait_at(smem_u32(v_clean), rp & 1))) break;
+                        ++rp;
+                    }
+                    if (j < n) {
+                        if (!(ok = wait_at(ph, pp & 1) && wait_at(pf, pp & 1))) break;
+                        ++pp;
+                        if (j == 0 && !(ok = wait_at(smem_u32(&o_empty[t]), (ip & 1) ^ 1))) break;
+                    }
+                    if (!(ok = take())) break;
+                    if (j < n) {
+                        tc_fence_after();
+                        const int steps = (min(kAtK, (own ? kend : a.prefix_len) - key0) + 15) >> 4;
+                        if (steps == kAtK / 16) {
+                            issue_o(j == 0, 0);
+                            issue_o(false, 1);
+                        } else {
 #pragma unroll 1
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        const int n = t ? cur.nb1 : cur.nb0;
-                        if (j < n) {
-                            if (!(ok = wait_at(pf0 + 8 * t, flip(2 + t)))) break;
-                            if (j == 0 && !(ok = wait_at(smem_u32(&o_empty[t]), flip(4 + t) ^ 1))) break;
-                            if (ragged && !(ok = wait_at(smem_u32(v_clean), flip(6)))) break;
-                            ragged = false;
+                            for (int kk = 0; kk < steps; ++kk)
+                                tc_mma_ts_w(to, ts + 8 * kk, at_desc_add(dv0, slot * Sh::KB + kk * 16 * 128), id_o, (j | kk) != 0);
+                        }
+                        if (j + 1 == n) tc_commit_w(smem_u32(&o_full[t]));
+                    }
+                    release();
+                    if (j + 1 < w.nb) {
+                        if (!(ok = wait_at(full0 + 8 * slot, sph))) break;
+                        if (j + 1 < n) {
                             tc_fence_after();
-                            if (steps == kAtK / 16) {
-                                issue_o(t, dv, j == 0);
-                            } else {
-#pragma unroll 1
-                                for (int kk = 0; kk < steps; ++kk)
-                                    tc_mma_ts_w(tmem + 2 * kAtK + D * t, tmem + kAtK * t + 8 * kk, at_desc_add(dv, kk * 16 * 128),
-                                                id_o, (j | kk) != 0);
-                            }
-                            if (j + 1 == n) tc_commit_w(smem_u32(&o_full[t]));
+                            issue_s(j + 2 == n);
                         }
-                        if (!last) {
-                            if (j + 1 < n) {
-                                if (!k_ready && !(ok = wait_at(bar0 + 8 * slot, sph))) break;
-                                tc_fence_after();
-                                k_ready = true;
-                                issue_s(t, slot, j + 2 == n);
-                            }
-                        } else if (more && t == 0 && nxt.nb0) {
-                            // the next item's first S behind this tile's last product, if its operands are there
-                            if (__all_sync(0xffffffffu, mbar_try_at(bar0 + 8 * slot, sph) && mbar_try_at(smem_u32(&q_full[0]), ph & 1))) {
-                                flip(0);
-                                tc_fence_after();
-                                issue_s(0, slot, nxt.nb0 == 1);
-                                issued = 1;
-                            }
-                        }
+                        release();
                     }
-                    if (!ok) break;
-                    tc_commit_w(emp0 + 8 * sv);             // every MMA reading V has been issued
-                    if (last && more) {
-                        if (!(ok = wait_at(bar0 + 8 * slot, sph))) break;
-                        for (int t = 0; t < nxt.nt && ok; ++t) {
-                            const int n = t ? nxt.nb1 : nxt.nb0;
-                            if (!n || (issued >> t & 1)) continue;
-                            if (!(ok = wait_at(smem_u32(&q_full[t]), flip(t)))) break;
-                            tc_fence_after();
-                            issue_s(t, slot, n == 1);
-                        }
-                    }
-                    if ((!last || more) && ok) {
-                        tc_commit_w(emp0 + 8 * slot);
-                        step();
-                    }
+                    pass();
                 }
-                cur = nxt;
-                have = more;
+                if (n) ++ip;
             }
             tc_commit_w(smem_u32(done));
         }
@@ -721,6 +691,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                     const bool grow = m_blk > m_use + kAtRescale;
                     const float alpha = grow ? ex2_approx(m_use - m_blk) : 1.f;   // 0 when m_use is -inf
                     if (grow) m_use = m_blk;
+                    // O holds the blocks before this one (their products precede this S in the
+                    // order of issue); rescale it where the row's m moved
+                    if (j > 0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + 16 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st16(o_col + 16 * c, o);
+                        }
+                    }
                     const float m_sub = m_use == -INFINITY ? 0.f : m_use;         // nothing seen yet: every weight is 0
                     const uint64_t scale2 = f2_pack(a.scale_log2, a.scale_log2), neg2 = f2_pack(-m_sub, -m_sub);
                     uint64_t sum[4] = {0, 0, 0, 0};
@@ -736,26 +719,22 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                             sum[i & 3] = f2_add(sum[i & 3], f2_pack(x, y));
                             pk[i] = pack_bf16x2(x, y);
                         }
+                        if (c == 2) {                       // the first 64 keys' products may begin
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&p_half[t]);
+                        }
                         tmem_st16(s_col + 16 * c, pk);
                     }
                     float sx, sy;
                     f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), sx, sy);
                     l_run = l_run * alpha + (sx + sy);
-                    // O holds the blocks before this one (their products precede this S in the
-                    // order of issue); rescale it where the row's m moved
-                    if (j > 0 && __any_sync(0xffffffffu, grow)) {
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32(o_col + 32 * c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                            tmem_st32(o_col + 32 * c, o);
-                        }
-                    }
                     tmem_wait_st();
                     tc_fence_before();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_half[t]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[t]);
