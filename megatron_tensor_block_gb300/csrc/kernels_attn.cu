@@ -31,7 +31,9 @@ namespace tpk {
 constexpr int kAtM = 128;               // query rows per tile: 128 / G tokens of the G heads of a KV head
 constexpr int kAtK = 128;               // keys per block
 constexpr int kAtBuckets = 512;         // item lengths told apart when sorting
-constexpr int kAtMinPart = 2;           // blocks of the shortest part worth its join
+constexpr int kAtMinPart = 2;           // blocks of the shortest part of a narrow item worth its join
+constexpr int kAtMinCut = 4;            // ... and of a wide one, which has more rows to join
+constexpr int kAtMaxParts = 16;
 constexpr int kAtNarrow = 32;           // rows of an item at most that the narrow kernel takes
 
 enum AttnKind : int { AT_PREFIX = 1, AT_OWN = 2 };   // key blocks of an item: the prefix's, the sequence's own
@@ -53,151 +55,228 @@ __device__ __forceinline__ void part_split(int nb, int target, int& parts, int& 
     }
 }
 
-// One CTA. Three passes over the tiles: count the blocks, count the items of
-// each length, place them. Every lane takes a sequence; a warp takes the tiles
-// of a long sequence together. Integer atomics place items and rows of
-// partial results: their order decides where a partial lies, not what is
-// added to what.
+// One CTA. Three passes over the tiles: check and sum up, count the items of
+// each length, place them. A lane takes a sequence (the first of them stay in
+// its registers), a warp the tiles of a long sequence together. The items are
+// sorted by length; CTAs take them from the front.
+//
+// An item is cut into parts, which are joined at the end, where whole items
+// would leave SMs without work: all long ones, when there are fewer than SMs; one
+// that is longer than an even share of all; and those of a last round that has
+// few (two rounds of equal items for 160 on 152 SMs end almost twice as late as
+// one). Parts cost their partial results' way to memory and back.
+//
+// Integer atomics place the items of a length and the rows of partial results:
+// their order decides where a partial lies, not what is added to what.
 __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams p) {
     __shared__ int s_hist[2 * kAtBuckets];                           // wide items, narrow items
-    __shared__ unsigned long long s_work[2];
-    __shared__ int s_rows, s_groups, s_chunks, s_warp[32];
+    __shared__ unsigned long long s_blocks[2][32];                   // per warp: blocks of wide and narrow tiles
+    __shared__ int s_tiles[32], s_longest[32], s_warp[32];           // wide tiles
+    __shared__ int s_rows, s_chunks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr unsigned kAll = 0xffffffffu;
     pdl_trigger();
-    for (int i = tid; i < 2 * kAtBuckets; i += 1024) s_hist[i] = 0;
-    if (tid == 0) {
-        s_work[0] = s_work[1] = 0;
-        s_rows = s_groups = s_chunks = 0;
-    }
-    pdl_wait();
+    s_hist[tid] = 0;
+    if (tid == 0) s_rows = s_chunks = 0;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G);            // tokens per item
     const int heads = p.N * p.hkv_s;
     const int n_prefix = (p.prefix_len + kAtK - 1) / kAtK;           // prefix blocks
     const int in_item = p.shared ? 0 : n_prefix;
-    int bad = 0, out = 0;
-    __syncthreads();
-
     const int lanes = min(32, (p.B + 31) / 32);                      // sequences per warp and round
-    auto visit = [&](auto&& tile) {
+    pdl_wait();
+
+    int bad = 0, out = 0;
+    int c0 = 0, n = 0, pos = 0;                                      // the lane's sequence of the first round
+    auto load = [&](int b0, int& c0, int& n, int& pos) {
+        const int b = b0 + lane;
+        c0 = n = pos = 0;
+        if (lane < lanes && b < p.B) {
+            c0 = p.cu[b];
+            const int c1 = p.cu[b + 1];
+            pos = p.pos[b];
+            if (c1 < c0 || c0 < 0 || c1 > p.T || (b == 0 && c0 != 0)) bad = 1;
+            else if (c1 > c0 && (pos < 0 || (int64_t)pos + (c1 - c0) > p.max_kv)) out = 1;
+            if (!bad) n = c1 - c0;
+        }
+    };
+    // f(sequence, first token, tokens, position) for every tile, lanes apart
+    auto visit = [&](auto&& f) {
         for (int b0 = warp * lanes; b0 < p.B; b0 += 32 * lanes) {
-            const int b = b0 + lane;
-            int c0 = 0, n = 0, pos = 0;
-            if (lane < lanes && b < p.B) {
-                c0 = p.cu[b];
-                n = p.cu[b + 1] - c0;
-                pos = p.pos[b];
-            }
-            if (n > 0 && n <= per) tile(b, c0, n, pos);
-            for (unsigned m = __ballot_sync(0xffffffffu, n > per); m; m &= m - 1) {
-                const int l = __ffs(m) - 1;
-                const int bl = b0 + l, cl = __shfl_sync(0xffffffffu, c0, l), nl = __shfl_sync(0xffffffffu, n, l),
-                          pl = __shfl_sync(0xffffffffu, pos, l);
-                for (int64_t i = (int64_t)lane * per; i < nl; i += 32 * per)
-                    tile(bl, cl + (int)i, min(per, nl - (int)i), pl + (int)i);
+            int c = c0, m = n, q = pos;
+            if (b0 != warp * lanes) load(b0, c, m, q);
+            if (m > 0 && m <= per) f(b0 + lane, c, m, q);
+            for (unsigned w = __ballot_sync(kAll, m > per); w; w &= w - 1) {
+                const int l = __ffs(w) - 1;
+                const int cl = __shfl_sync(kAll, c, l), nl = __shfl_sync(kAll, m, l), ql = __shfl_sync(kAll, q, l);
+                for (int64_t at = (int64_t)lane * per; at < nl; at += 32 * per)
+                    f(b0 + l, cl + (int)at, min(per, nl - (int)at), (int)((int64_t)ql + at));
             }
         }
     };
+    auto blocks = [&](int n, int pos) { return in_item + own_blocks((int64_t)pos + n, p.max_kv); };
+    auto is_narrow = [&](int n) { return n * G <= kAtNarrow; };
 
-    for (int b = tid; b < p.B; b += 1024) {
-        const int c0 = p.cu[b], c1 = p.cu[b + 1];
-        if (c1 < c0 || c0 < 0 || c1 > p.T || (b == 0 && c0 != 0)) bad = 1;
-        else if (c1 > c0 && (p.pos[b] < 0 || (int64_t)p.pos[b] + (c1 - c0) > p.max_kv)) out = 1;
+    // ---- check and sum up
+    load(warp * lanes, c0, n, pos);
+    unsigned long long wide_blocks = 0, narrow_blocks = 0;
+    int wide_tiles = 0, longest = 0;
+    auto sum_up = [&](int k, int nb) {
+        if (is_narrow(k)) {
+            narrow_blocks += nb;
+        } else {
+            wide_blocks += nb;
+            ++wide_tiles;
+            longest = max(longest, nb);
+        }
+    };
+    visit([&](int, int, int k, int q) { sum_up(k, blocks(k, q)); });
+    for (int o = 16; o; o >>= 1) {
+        wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
+        narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
+        wide_tiles += __shfl_xor_sync(kAll, wide_tiles, o);
+        longest = max(longest, __shfl_xor_sync(kAll, longest, o));
+    }
+    if (lane == 0) {
+        s_tiles[warp] = wide_tiles;
+        s_longest[warp] = longest;
+        s_blocks[0][warp] = wide_blocks;
+        s_blocks[1][warp] = narrow_blocks;
     }
     bad = __syncthreads_or(bad);
-    out = __syncthreads_or(out);
     if (bad) {
-        if (tid == 0) {
-            AttnCtl c = {};
-            *p.ctl = c;
-            set_status(p.status, TP_ERR_SHAPE);
-        }
+        if (tid < (int)(sizeof(AttnCtl) / sizeof(int))) reinterpret_cast<int*>(p.ctl)[tid] = 0;
+        if (tid == 0) set_status(p.status, TP_ERR_SHAPE);
         return;
     }
+    if (out) set_status(p.status, TP_ERR_CAPACITY);
     const int n_tok = p.cu[p.B];
+    wide_blocks = s_blocks[0][lane];
+    narrow_blocks = s_blocks[1][lane];
+    wide_tiles = s_tiles[lane];
+    longest = s_longest[lane];
+    for (int o = 16; o; o >>= 1) {
+        wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
+        narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
+        wide_tiles += __shfl_xor_sync(kAll, wide_tiles, o);
+        longest = max(longest, __shfl_xor_sync(kAll, longest, o));
+    }
     const int prefix_tiles = p.shared ? (n_tok + per - 1) / per : 0;
-
-    unsigned long long work[2] = {0, 0};
-    visit([&](int, int, int n, int pos) {
-        work[n * G <= kAtNarrow] += in_item + own_blocks((int64_t)pos + n, p.max_kv);
-    });
-    for (int i = tid; i < prefix_tiles; i += 1024) work[min(per, n_tok - i * per) * G <= kAtNarrow] += n_prefix;
-    for (int k = 0; k < 2; ++k) {
-        for (int o = 16; o; o >>= 1) work[k] += __shfl_xor_sync(0xffffffffu, work[k], o);
-        if (lane == 0 && work[k]) atomicAdd(&s_work[k], work[k]);
-    }
-    __syncthreads();
-    // Parts are an even share of all blocks or shorter: between one and two rounds of the wide kernel's CTAs, and two
-    // of the narrow kernel's, which has two per SM.
-    int target[2];
-    for (int k = 0; k < 2; ++k) {
-        const long long share = (long long)((s_work[k] * heads * 2 + (k ? 8 : 3) * kSMs - 1) / ((k ? 8 : 3) * kSMs));
-        target[k] = (int)min((long long)INT_MAX / 4, max((long long)kAtMinPart, share));
+    auto prefix_n = [&](int i) { return min(per, n_tok - i * per); };
+    if (prefix_tiles) {
+        const int small = is_narrow(prefix_n(prefix_tiles - 1));
+        wide_tiles += prefix_tiles - small;
+        wide_blocks += (unsigned long long)(prefix_tiles - small) * n_prefix;
+        if (small) narrow_blocks += n_prefix;
+        if (prefix_tiles > small) longest = max(longest, n_prefix);
     }
 
-    auto bucket = [&](int nb, bool narrow) { return (narrow ? 2 : 1) * kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
-    auto count = [&](int nb, bool narrow) {
-        int parts, len;
-        part_split(nb, target[narrow], parts, len);
-        if (parts > 1) atomicAdd(&s_hist[bucket(len, narrow)], parts - 1);
-        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len, narrow)], 1);
+    // ---- the longest parts
+    const long long items = (long long)wide_tiles * heads;
+    auto share = [&](unsigned long long sum, unsigned parts) {      // of the blocks of all KV heads
+        const unsigned long long all = sum * heads;
+        const unsigned long long q = all < (1ull << 32) ? (unsigned)all / parts + 1 : all / parts + 1;
+        return (int)min((unsigned long long)INT_MAX / 4, max((unsigned long long)kAtMinPart, q));
     };
-    visit([&](int, int, int n, int pos) { count(in_item + own_blocks((int64_t)pos + n, p.max_kv), n * G <= kAtNarrow); });
-    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix, min(per, n_tok - i * per) * G <= kAtNarrow);
+    // narrow: two parts per CTA, of which there are two per SM (time goes by the bytes: parts cost little)
+    const int target_n = share(narrow_blocks, 4 * kSMs);
+    int target_w = max(kAtMinCut, share(wide_blocks, kSMs));
+    if (items && items <= kSMs) {
+        // The parts per item that are done first, in blocks' time: rounds of parts, each two blocks' longer than its blocks,
+        // and the joining, a block's time for about 4.8 MB of float32 results there and back.
+        const float join = (float)(items * 2 * kAtM) * p.d * 8 / 4.8e6f;
+        float best = 1e30f;
+        int parts = 1;
+        for (int k = 1; k <= kAtMaxParts && k * items <= 3 * kSMs; ++k) {
+            const int len = (longest + k - 1) / k;
+            if (k > 1 && len < kAtMinCut) break;
+            const float t = (float)((int)(k * items + kSMs - 1) / kSMs) * (len + 2) + (k > 1 ? k * join : 0.f);
+            if (t < best) best = t, parts = k;
+        }
+        target_w = (longest + parts - 1) / parts;
+    }
+    // a last round of few items, if nothing else is cut: parts for its items
+    const int rounds = items <= 3 * kSMs ? (int)items / kSMs : 0;
+    int last_from = INT_MAX, last_parts = 1;
+    if (rounds && longest <= target_w + target_w / 2) {
+        last_from = (rounds * kSMs + heads - 1) / heads;
+        const int rest = wide_tiles - last_from;
+        last_parts = rest > 0 ? min(kAtMaxParts, kSMs / (rest * heads)) : 1;
+        if (last_parts < 2) last_from = INT_MAX, last_parts = 1;
+    }
+
+    // ---- count
+    auto bucket = [&](int nb, bool nar) { return (nar ? 2 : 1) * kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
+    auto count = [&](int nb, bool nar) {
+        int parts, len;
+        part_split(nb, nar ? target_n : target_w, parts, len);
+        if (parts > 1) atomicAdd(&s_hist[bucket(len, nar)], parts - 1);
+        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len, nar)], 1);
+    };
+    visit([&](int, int, int k, int q) { count(blocks(k, q), is_narrow(k)); });
+    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix, is_narrow(prefix_n(i)));
     __syncthreads();
     // exclusive scan of the buckets, one per thread
     const int mine = s_hist[tid];
     int incl = mine;
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        const int v = __shfl_up_sync(kAll, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int before = 0, n_wide = 0, total = 0;
-    for (int w = 0; w < 32; ++w) {
-        if (w < warp) before += s_warp[w];
-        if (w < kAtBuckets / 32) n_wide += s_warp[w];
-        total += s_warp[w];
+    int of_warp = s_warp[lane];
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(kAll, of_warp, o);
+        if (lane >= o) of_warp += v;
     }
-    s_hist[tid] = before + incl - mine;
+    const int sorted = __shfl_sync(kAll, of_warp, kAtBuckets / 32 - 1);
+    const int more = last_parts > 1 ? (sorted - last_from) * (last_parts - 1) : 0;      // places of the last round's parts
+    s_hist[tid] = (warp ? __shfl_sync(kAll, of_warp, warp - 1) : 0) + incl - mine + (tid >= kAtBuckets ? more : 0);
+    const int total = __shfl_sync(kAll, of_warp, 31) + more;
     __syncthreads();
 
-    auto place = [&](int kind, int b, int t0, int n, int pos, int nb, int group) {
-        const bool narrow = n * G <= kAtNarrow;
-        int parts, len;
-        part_split(nb, target[narrow], parts, len);
-        int row = -1;
-        if (parts > 1 || p.shared) {
-            row = atomicAdd(&s_rows, parts * heads * n * G);
-            if (kind & AT_OWN) {
-                const int g = atomicAdd(&s_groups, 1), chunks = (n * G + 7) / 8, c = atomicAdd(&s_chunks, chunks);
-                p.groups[g] = AttnGroup{t0, n, pos, row, parts, 0, 0, 0};
-                for (int i = 0; i < chunks; ++i) p.chunks[c + i] = g * 32 + i;
-            } else {
-                p.prefix_groups[group] = make_int2(row, parts);
+    // ---- place
+    auto place = [&](int kind, int b, int t0, int k, int q, int nb, int i) {
+        const bool nar = is_narrow(k);
+        int parts, len, from = -1;
+        part_split(nb, nar ? target_n : target_w, parts, len);
+        if (parts == 1) {
+            from = atomicAdd(&s_hist[bucket(nb, nar)], 1);
+            if (!nar && from >= last_from) {
+                from = last_from + (from - last_from) * last_parts;
+                parts = max(1, min(last_parts, nb / kAtMinPart));
+                len = (nb + parts - 1) / parts;
+                parts = max(1, (nb + len - 1) / max(len, 1));
+                for (int j = parts; j < last_parts; ++j) p.items[from + j] = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};   // no rows
             }
         }
-        for (int i = 0; i < parts; ++i) {
-            const int k0 = i * len, k1 = min(nb, k0 + len);
-            const int e = atomicAdd(&s_hist[bucket(k1 - k0, narrow)], 1);
-            p.items[e] = AttnItem{t0, n, b, pos, k0, k1, kind, row < 0 ? -1 : row + i * heads * n * G};
+        int row = -1;
+        if (parts > 1 || p.shared) {
+            row = atomicAdd(&s_rows, parts * heads * k * G);
+            if (kind & AT_OWN) {
+                const int chunks = (k * G + 7) / 8, c = atomicAdd(&s_chunks, chunks);
+                for (int j = 0; j < chunks; ++j) p.chunks[c + j] = AttnChunk{t0, k, q, row, parts, j, 0, 0};
+            } else {
+                p.prefix_groups[i] = make_int2(row, parts);
+            }
+        }
+        for (int j = 0; j < parts; ++j) {
+            const int k0 = j * len, k1 = min(nb, k0 + len);
+            const int e = from >= 0 ? from + j : atomicAdd(&s_hist[bucket(k1 - k0, nar)], 1);
+            p.items[e] = AttnItem{t0, k, b, q, k0, k1, kind, row < 0 ? -1 : row + j * heads * k * G};
         }
     };
-    visit([&](int b, int t0, int n, int pos) {
-        place(p.shared ? AT_OWN : AT_OWN | AT_PREFIX, b, t0, n, pos, in_item + own_blocks((int64_t)pos + n, p.max_kv), 0);
-    });
-    for (int i = tid; i < prefix_tiles; i += 1024)
-        place(AT_PREFIX, 0, i * per, min(per, n_tok - i * per), 0, n_prefix, i);
+    const int kind = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
+    visit([&](int b, int t0, int k, int q) { place(kind, b, t0, k, q, blocks(k, q), 0); });
+    for (int i = tid; i < prefix_tiles; i += 1024) place(AT_PREFIX, 0, i * per, prefix_n(i), 0, n_prefix, i);
     __syncthreads();
     if (tid == 0) {
         AttnCtl c = {};
         c.n_tokens = n_tok;
-        c.n_wide = n_wide;
+        c.n_wide = sorted + more;
         c.n_items = total;
-        c.n_groups = s_groups;
         c.n_chunks = s_chunks;
         *p.ctl = c;
-        if (out) set_status(p.status, TP_ERR_CAPACITY);
     }
 }
 
@@ -217,17 +296,18 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
 //                 moving only when a row's maximum grows by more than 2^8
 //                 (O is then rescaled; a weight of 2^8 is as exact in bf16 and
 //                 float32 as one of 1);
-//   warps 12-15   V blocks that some row of the item does not see to their end
-//                 are made finite before their product (0 * inf is not 0), and
-//                 the results O / l (or O, m and l of a part) are written while
+//   warp 3        V blocks that some row of the item does not see to their end
+//                 are made finite before their product (0 * inf is not 0);
+//   warps 12-15   the results O / l (or O, m and l of a part) are written while
 //                 the next item is under way.
 // The items' ranges of blocks are walked in the same order by every role; all
 // waits are bounded.
 // ---------------------------------------------------------------------------
 
 constexpr int kAtThreads = 512;
+constexpr int kAtQueue = 4;               // items read ahead
 constexpr float kAtRescale = 8.0f;
-constexpr int kAtRegsIo = 80, kAtRegsSoftmax = 168, kAtRegsOut = 96;
+constexpr int kAtRegsIo = 88, kAtRegsSoftmax = 160, kAtRegsOut = 104;
 static_assert(kAtRegsIo + 2 * kAtRegsSoftmax + kAtRegsOut <= 4 * 128, "the launch's registers");
 
 template <int D>
@@ -308,14 +388,21 @@ __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volat
     }
 }
 
+__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+    const uint32_t b = smem_u32(bar);
+    return mbar_try_at(b, parity) || mbar_wait_slow(b, parity, abort, status);
+}
+
 __device__ __forceinline__ uint64_t at_desc_add(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 
-// One item for one KV head of one shard. nb[t]: key blocks of tile t.
-struct AtWork {
+// One item for one KV head of one shard. nb0, nb1: key blocks of its tiles.
+struct __align__(16) AtWork {
     int r, kvh, h;                        // shard, KV head of the shard, KV head of all
     int t0, ntok, b, qpos, blk0, part;
     int nP, nt, nb0, nb1, nb;             // prefix blocks in the list, tiles, blocks of the tiles and of both
+    int end, reserved;                    // 1: there are no more items
 };
+static_assert(sizeof(AtWork) == 64, "four 16-byte words of the queue");
 
 __device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork& w) {
     const int4 x = __ldcg(reinterpret_cast<const int4*>(a.items + e)), y = __ldcg(reinterpret_cast<const int4*>(a.items + e) + 1);
@@ -337,35 +424,11 @@ __device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork&
     w.nb0 = max(0, min(blk1, e0) - w.blk0);
     w.nb1 = w.nt > 1 ? max(0, min(blk1, e1) - w.blk0) : 0;
     w.nb = max(w.nb0, w.nb1);
-}
-
-// The CTA's k-th item: rounds of the grid run alternately up and down the
-// sorted list, which evens out what the CTAs get.
-__device__ __forceinline__ bool at_item(const AtArgs& a, int total, int k, AtWork& w) {
-    const int P = gridDim.x, c = blockIdx.x;
-    const int64_t idx64 = (int64_t)k * P + ((k & 1) ? P - 1 - c : c);
-    if ((int64_t)k * P >= total) return false;
-    if (idx64 >= total) {
-        w.nb = w.nt = w.nb0 = w.nb1 = w.ntok = w.qpos = 0;
-        return true;                                     // nothing in this round
-    }
-    const int idx = (int)idx64, heads = a.N * a.hkv_s, e = idx / heads;
-    at_decode(a, e, idx - e * heads, w);
-    return true;
+    w.end = w.reserved = 0;
 }
 
 // A value that is the same in every lane, in a form that lets the compiler know.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __forceinline__ void uniform(AtWork& w) {
-    w.qpos = uniform(w.qpos);
-    w.ntok = uniform(w.ntok);
-    w.blk0 = uniform(w.blk0);
-    w.nP = uniform(w.nP);
-    w.nt = uniform(w.nt);
-    w.nb0 = uniform(w.nb0);
-    w.nb1 = uniform(w.nb1);
-    w.nb = uniform(w.nb);
-}
 
 // Block j of an item: its first key in the prefix (own = false) or in the sequence's own cache.
 __device__ __forceinline__ int at_block(const AtWork& w, int j, bool& own) {
@@ -380,6 +443,46 @@ __device__ __forceinline__ int at_kend(const AtArgs& a, const AtWork& w) {
 }
 // whether the V block at own key `key0` has rows that some row of the item does not see
 __device__ __forceinline__ bool at_ragged(const AtWork& w, int key0) { return (int64_t)key0 + kAtK > (int64_t)w.qpos + 1; }
+
+// Whether a bf16 of the word is infinite or NaN: adding one to a full exponent carries out of it.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t only_finite(uint32_t x) {
+    if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
+    if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
+    return x;
+}
+
+// One warp: rows 0 .. valid - 1 of a V block without infinities and NaN, the
+// rows behind them zeros as far as a product of 16 keys reads. Whether the lane
+// found one. A step is four rows of 128 bytes; the swizzle moves 16-byte units
+// within a row only.
+template <int D>
+__device__ __forceinline__ int v_block_finite(unsigned char* block, int lane, int valid) {
+    int found = 0;
+    const int rows = (valid + 15) & ~15;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        uint4* base = reinterpret_cast<uint4*>(block + c * (kAtK * 128)) + lane;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 16) {
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = base[(r0 / 4 + i) * 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = r0 + 4 * i + (lane >> 3);
+                if (row >= valid) {
+                    base[(r0 / 4 + i) * 32] = make_uint4(0, 0, 0, 0);
+                } else if (not_finite(x[i].x) | not_finite(x[i].y) | not_finite(x[i].z) | not_finite(x[i].w)) {
+                    base[(r0 / 4 + i) * 32] =
+                        make_uint4(only_finite(x[i].x), only_finite(x[i].y), only_finite(x[i].z), only_finite(x[i].w));
+                    found = 1;
+                }
+            }
+        }
+    }
+    return found;
+}
 
 // Row `m` of a V block: zeros where it lies behind the last key, and no
 // infinities or NaN. Whether it held one.
@@ -397,18 +500,32 @@ __device__ __forceinline__ int v_row_finite(unsigned char* block, int m, bool pa
             }
             uint4 x = *q;
             uint32_t* y = reinterpret_cast<uint32_t*>(&x);
-            bool hit = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if ((y[i] & 0x7F80u) == 0x7F80u) y[i] &= 0xFFFF0000u, hit = true;
-                if ((y[i] & 0x7F800000u) == 0x7F800000u) y[i] &= 0xFFFFu, hit = true;
-            }
-            if (hit) {
-                *q = x;
+            if (not_finite(y[0]) | not_finite(y[1]) | not_finite(y[2]) | not_finite(y[3])) {
+                *q = make_uint4(only_finite(y[0]), only_finite(y[1]), only_finite(y[2]), only_finite(y[3]));
                 found = 1;
             }
         }
     return found;
+}
+
+// 16-byte units of four lanes' rows, transposed: lane i of four gets unit i of the rows of all four, so that a store of the
+// warp writes eight runs of 64 bytes and not 32 of 16.
+__device__ __forceinline__ void transpose4(uint4 (&u)[4], int lane) {
+    auto swap = [&](uint4& a, uint4& b, int off) {       // b of the lower lane for a of the upper
+        const bool up = lane & off;
+        uint4 give = up ? a : b;
+        give.x = __shfl_xor_sync(0xffffffffu, give.x, off);
+        give.y = __shfl_xor_sync(0xffffffffu, give.y, off);
+        give.z = __shfl_xor_sync(0xffffffffu, give.z, off);
+        give.w = __shfl_xor_sync(0xffffffffu, give.w, off);
+        if (up) a = give;
+        else b = give;
+    };
+    __syncwarp();
+    swap(u[0], u[1], 1);
+    swap(u[2], u[3], 1);
+    swap(u[0], u[2], 2);
+    swap(u[1], u[3], 2);
 }
 
 template <int D>
@@ -428,13 +545,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     uint64_t* st_empty = st_full + 2;     // [2]
     uint64_t* kv_full = st_empty + 2;     // [R]
     uint64_t* kv_empty = kv_full + R;     // [R]
-    uint64_t* v_ragged = kv_empty + R;    // a ragged V block has arrived ...
-    uint64_t* v_clean = v_ragged + 1;     // ... and is finite
-    uint64_t* turn = v_clean + 1;         // [2] whose products are next
-    uint64_t* done = turn + 2;
+    uint64_t* v_clean = kv_empty + R;     // [R] the slot's ragged V block is finite
+    uint64_t* note = v_clean + R;         // [kAtQueue] the item's notes are written
+    uint64_t* turn = note + kAtQueue;     // [2] whose products are next
+    uint64_t* item_full = turn + 2;       // [kAtQueue]
+    uint64_t* item_empty = item_full + kAtQueue;
+    uint64_t* done = item_empty + kAtQueue;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
+    volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [kAtQueue] an item's V had infinities or NaN
+    AtWork* queue = reinterpret_cast<AtWork*>(smem + Sh::HEAD - kAtQueue * sizeof(AtWork));
+    static_assert((18 + 3 * R + 2 + 3 * kAtQueue + 1) * 8 + 8 + 4 * kAtQueue <= Sh::HEAD - kAtQueue * sizeof(AtWork), "the head's words");
     unsigned char* sq = smem + Sh::HEAD;
     unsigned char* ring = sq + 2 * Sh::QB;
     float2* stat = reinterpret_cast<float2*>(ring + R * Sh::KB);     // [2][kAtM]
@@ -454,15 +575,18 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
         }
         for (int i = 0; i < R; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 2);
+            mbar_init(&kv_empty[i], 3);
+            mbar_init(&v_clean[i], 1);
         }
-        mbar_init(v_ragged, 2);
-        mbar_init(v_clean, 4);
         mbar_init(&turn[0], 1);
         mbar_init(&turn[1], 1);
+        for (int i = 0; i < kAtQueue; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 15);
+            mbar_init(&note[i], 1);
+        }
         mbar_init(done, 2);
         *abort_flag = (smem_u32(sq) & 1023u) ? 1 : 0;
-        s_poison[0] = s_poison[1] = 0;
         if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
         fence_mbar_init();
     }
@@ -473,7 +597,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
     const uint32_t tmem = uniform(*tmem_slot);
     pdl_wait();
     pdl_trigger();                        // only now: the narrow kernel relies on the lists being there when it starts
-    const int total = uniform(*abort_flag ? 0 : a.ctl->n_wide * (a.N * a.hkv_s));
+    // The copying thread reads the list ahead of the other roles and leaves the items in a queue in shared memory; this
+    // gives the k-th of them to a warp.
+    auto item_done = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_empty[k % kAtQueue]);
+    };
+    auto item = [&](int k, AtWork& w, bool hold = false) {  // hold: the warp calls item_done itself
+        const int q = k % kAtQueue;
+        if (!__all_sync(0xffffffffu, mbar_wait(&item_full[q], (k / kAtQueue) & 1, abort_flag, a.status))) return false;
+        const int4* x = reinterpret_cast<const int4*>(&queue[q]);
+        const int4 x0 = x[0], x1 = x[1], x2 = x[2], x3 = x[3];
+        if (!hold) item_done(k);
+        w.r = x0.x, w.kvh = x0.y, w.h = x0.z, w.t0 = x0.w;
+        w.ntok = uniform(x1.x), w.b = x1.y, w.qpos = uniform(x1.z), w.blk0 = uniform(x1.w);
+        w.part = x2.x, w.nP = uniform(x2.y), w.nt = uniform(x2.z), w.nb0 = uniform(x2.w);
+        w.nb1 = uniform(x3.x), w.nb = uniform(x3.y), w.end = uniform(x3.z);
+        return w.end == 0;
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsIo));
@@ -481,28 +622,56 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
             // ---------------------------------------------------------------- loads
             uint32_t it = 0, nq[2] = {0, 0};
             const uint32_t q_bytes = (uint32_t)(a.tpt * a.G * 128 * Sh::NKB);
-            bool ok = true;
-            AtWork w;
-            for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+            bool ok = !*abort_flag;
+            const int heads = a.N * a.hkv_s, total = __ldcg(&a.ctl->n_wide) * heads;
+            // The sorted list is taken from as CTAs become free, but for the first round; a few blocks before an item's
+            // end, so that the next one's loads follow on.
+            auto take = [&]() { return total > (int)gridDim.x ? (int)gridDim.x + atomicAdd(&a.ctl->next_wide, 1) : total; };
+            auto publish = [&](int k, int& idx) {
+                const int q = k % kAtQueue;
+                if (idx >= total) idx = -1;
+                AtWork w = {};
+                w.end = 1;
+                if (idx >= 0) {
+                    const int e = idx / heads;
+                    at_decode(a, e, idx - e * heads, w);
+                }
+                if (!(ok = at_wait(&item_empty[q], ((k / kAtQueue) & 1) ^ 1, abort_flag, a.status))) return;
+                const int4* x = reinterpret_cast<const int4*>(&w);
+                int4* y = reinterpret_cast<int4*>(&queue[q]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[i] = x[i];
+                mbar_arrive(&item_full[q]);
+            };
+            int idx = blockIdx.x;
+            if (ok) publish(0, idx);
+            for (int k = 0; ok && idx >= 0; ++k) {
+                const AtWork w = queue[k % kAtQueue];
                 const int grp = w.b * a.hkv_s + w.kvh;
                 auto load = [&](int j, bool v) {
                     bool own;
                     const int key0 = at_block(w, j, own);
                     const CUtensorMap* m = own ? (v ? &a.tv[w.r] : &a.tk[w.r]) : (v ? &a.pv[w.r] : &a.pk[w.r]);
                     const int s = it % R;
-                    if (!(ok = mbar_wait(&kv_empty[s], ((it / R) & 1) ^ 1, abort_flag, a.status))) return;
+                    if (!(ok = at_wait(&kv_empty[s], ((it / R) & 1) ^ 1, abort_flag, a.status))) return;
                     mbar_arrive_expect_tx(&kv_full[s], Sh::KB);
 #pragma unroll
                     for (int kb = 0; kb < Sh::NKB; ++kb)
                         tma_load_3d_keep(ring + s * Sh::KB + kb * (kAtK * 128), m, kb * 64, key0, own ? grp : w.kvh, &kv_full[s]);
                     ++it;
                 };
+                int in = 0;
+                if (w.nb == 0) {
+                    in = take();
+                    publish(k + 1, in);
+                }
                 for (int j = 0; j < w.nb && ok; ++j) {
                     load(j, false);
-                    if (j == 0)
+                    if (j == max(0, w.nb - 4)) in = take();
+                    if (j == 0) {
                         for (int t = 0; t < w.nt && ok; ++t) {
                             if ((t ? w.nb1 : w.nb0) == 0) continue;
-                            if (!(ok = mbar_wait(&q_empty[t], (nq[t] & 1) ^ 1, abort_flag, a.status))) break;
+                            if (!(ok = at_wait(&q_empty[t], (nq[t] & 1) ^ 1, abort_flag, a.status))) break;
                             mbar_arrive_expect_tx(&q_full[t], q_bytes);
 #pragma unroll
                             for (int kb = 0; kb < Sh::NKB; ++kb)
@@ -510,8 +679,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                                                  w.r * a.T + w.t0 + t * a.tpt, &q_full[t]);
                             ++nq[t];
                         }
+                    }
                     if (ok) load(j, true);
+                    if (ok && j == max(0, w.nb - 2)) publish(k + 1, in);
                 }
+                idx = in;
             }
             volatile int no_abort = 0;      // no copy may still be landing when the CTA exits
             for (int t = 0; t < 2; ++t)
@@ -532,7 +704,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                            ph = smem_u32(&p_half[t]), pf = smem_u32(&p_full[t]);
             const uint32_t ts = tmem + kAtK * t, to = tmem + 2 * kAtK + D * t;
             uint32_t slot = 0, sph = 0;     // the ring's next slot and its phase
-            uint32_t pp = 0, ip = 0, rp = 0, tp = 0;        // phases: blocks and items of the tile, ragged blocks, turns
+            uint32_t pp = 0, ip = 0, tp = 0, clean = 0;     // phases: blocks and items of the tile, turns, each slot's v_clean
             bool ok = true;
             auto wait_at = [&](uint32_t bar, uint32_t parity) {
                 return (bool)__all_sync(0xffffffffu, mbar_try_at(bar, parity) || mbar_wait_slow(bar, parity, abort_flag, a.status));
@@ -559,8 +731,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 tc_mma4_ts_w(to, ts + 32 * half, at_desc_add(dv0, slot * Sh::KB + 8192 * half), 8, 128, id_o, !first);
             };
             AtWork w;
-            for (int k = 0; ok && at_item(a, total, k, w); ++k) {
-                uniform(w);
+            for (int k = 0; ok && item(k, w); ++k) {
                 if (!w.nb) continue;
                 const int n = t ? w.nb1 : w.nb0, kend = at_kend(a, w);
                 // blocks 1 .. plain - 1 are whole, seen by every row and followed by one of the tile; the prefix's last one
@@ -603,12 +774,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                     bool own;
                     const int key0 = at_block(w, j, own);
                     if (!(ok = wait_at(full0 + 8 * slot, sph))) break;
-                    const bool ragged = own && at_ragged(w, key0);
-                    if (ragged) {                           // both warps, for every ragged block: no phase is passed over
-                        if (lane == 0) mbar_arrive(v_ragged);
-                        __syncwarp();
-                        if (!(ok = wait_at(smem_u32(v_clean), rp & 1))) break;
-                        ++rp;
+                    if (own && at_ragged(w, key0)) {
+                        if (!(ok = wait_at(smem_u32(&v_clean[slot]), clean >> slot & 1))) break;
+                        clean ^= 1u << slot;
                     }
                     if (j < n) {
                         if (!(ok = wait_at(ph, pp & 1) && wait_at(pf, pp & 1))) break;
@@ -643,6 +811,43 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 if (n) ++ip;
             }
             tc_commit_w(smem_u32(done));
+        } else if (warp == 3) {
+            // ---------------------------------------------------------------- ragged V blocks
+            // A consumer of every slot, so that it works as soon as a block has arrived and is never a round behind.
+            uint32_t slot = 0, sph = 0;
+            bool ok = true;
+            auto next_slot = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&kv_empty[slot]);
+                if (++slot == R) slot = 0, sph ^= 1;
+            };
+            AtWork w;
+            int k = 0;
+            for (; ok && item(k, w, true); ++k) {
+                const int kend = at_kend(a, w);
+                int found = 0;
+                for (int j = 0; j < w.nb; ++j) {
+                    if (!(ok = __all_sync(0xffffffffu, at_wait(&kv_full[slot], sph, abort_flag, a.status)))) break;
+                    next_slot();
+                    if (!(ok = __all_sync(0xffffffffu, at_wait(&kv_full[slot], sph, abort_flag, a.status)))) break;
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    if (own && at_ragged(w, key0)) {
+                        found |= v_block_finite<D>(ring + slot * Sh::KB, lane, min(kAtK, kend - key0));
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&v_clean[slot]);
+                    }
+                    next_slot();
+                }
+                if (!ok) break;
+                found = __any_sync(0xffffffffu, found);
+                if (lane == 0) {
+                    s_poison[k % kAtQueue] = found;
+                    mbar_arrive(&note[k % kAtQueue]);
+                }
+                item_done(k);
+            }
         }
     } else if (warp < 12) {
         // -------------------------------------------------------------------- softmax
@@ -656,7 +861,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
         uint32_t sp = 0, ip = 0;                            // blocks, items of the tile so far
         bool ok = true;
         AtWork w;
-        for (int k = 0; ok && at_item(a, total, k, w); ++k) {
+        for (int k = 0; ok && item(k, w); ++k) {
             const int n = t ? w.nb1 : w.nb0;
             if (!n) continue;
             const int rows = min(a.tpt, w.ntok - t * a.tpt) * a.G;
@@ -670,17 +875,17 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                 if (!ok) break;
                 if (!idle) {
                     tc_fence_after();
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    // a block that every row of the warp sees whole needs no mask
+                    const bool whole = own ? key0 + kAtK - 1 <= min(warp_max, kend - 1) : key0 + kAtK <= a.prefix_len;
+                    const int hi = whole ? kAtK : (own ? own_max : a.prefix_len - 1) - key0;   // last key of the block the row sees
                     uint32_t v[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
                     tmem_wait_ld();
                     float* e = reinterpret_cast<float*>(&v[0][0]);
-                    bool own;
-                    const int key0 = at_block(w, j, own);
-                    // a block that every row of the warp sees whole needs no mask
-                    const bool whole = own ? key0 + kAtK - 1 <= min(warp_max, kend - 1) : key0 + kAtK <= a.prefix_len;
                     if (!whole) {
-                        const int hi = (own ? own_max : a.prefix_len - 1) - key0;
 #pragma unroll
                         for (int i = 0; i < 128; ++i) e[i] = i <= hi ? e[i] : -INFINITY;
                     }
@@ -748,102 +953,96 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
             if (lane == 0) mbar_arrive(&st_full[t]);
         }
     } else {
-        // -------------------------------------------------------------------- ragged V blocks, results
+        // -------------------------------------------------------------------- results
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAtRegsOut));
         const int qd = warp & 3, m = 32 * qd + lane;
         const int tok0 = m / a.G, g = m - tok0 * a.G;
-        const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
-        uint32_t base = 0, ip[2] = {0, 0}, rp = 0;
-        int np = 0;
+        const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + 2 * kAtK;
+        uint32_t ip0 = 0, ip1 = 0;
         bool ok = true;
-        AtWork w;
-        for (int k = 0; ok && at_item(a, total, k, w); ++k) {
-            const int kend = at_kend(a, w);
-            int first_ragged = INT_MAX;                     // first own key of the ragged blocks
+        for (int k = 0; ok; ++k) {
+            AtWork w;
+            if (!item(k, w, true)) break;
+            const int ntok = w.ntok, qpos = w.qpos;
+            const bool part = w.part >= 0;
+            const int rows = ntok * a.G;
+            // the item's first row of results, moved to the unit that the lane stores
+            const int64_t prow = (int64_t)w.part + (int64_t)w.h * rows;
+            char* base = part ? reinterpret_cast<char*>(a.part_o + prow * D)
+                              : reinterpret_cast<char*>(a.out + (((int64_t)w.r * a.T + w.t0) * a.hq_s + w.kvh * a.G) * D);
+            base += (lane & 3) * 16;
+            const int row_bytes = part ? D * 4 : D * 2, tok_rows = part ? a.G : a.hq_s;
             int poison = 0;
-            for (int j = 0; j < w.nb && ok; ++j) {
-                bool own;
-                const int key0 = at_block(w, j, own);
-                if (!own || !at_ragged(w, key0)) continue;
-                const uint32_t sv = (base + 2 * j + 1) % R;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_ragged, rp & 1, abort_flag, a.status)))) break;
-                ++rp;
-                first_ragged = min(first_ragged, key0);
-                poison |= v_row_finite<D>(ring + sv * Sh::KB, m, key0 + m >= kend);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                const bool any = __any_sync(0xffffffffu, poison);
-                __syncwarp();
-                if (lane == 0) {
-                    if (any) s_poison[np & 1] = np + 1;
-                    mbar_arrive(v_clean);
-                }
-            }
-            if (!ok) break;
-            base += 2 * w.nb;
-            if (first_ragged != INT_MAX) {
-                // did any of the four warps find one? Their last arrival is behind their notes; a note holds the number
-                // of its item, in turns in two places, as a warp is at most one such item ahead of another
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(v_clean, (rp - 1) & 1, abort_flag, a.status)))) break;
-                poison = s_poison[np & 1] == np + 1;
-                ++np;
-            }
+#pragma unroll 1
             for (int t = 0; t < w.nt && ok; ++t) {
                 const int n = t ? w.nb1 : w.nb0, tok = tok0 + t * a.tpt;
-                const bool live = tok0 < a.tpt && tok < w.ntok;
-                const int64_t pos = (int64_t)w.qpos + tok;
+                const bool live = tok0 < a.tpt && tok < ntok;
+                const int64_t pos = (int64_t)qpos + tok;
                 float2 ml = make_float2(-INFINITY, 0.f);
                 if (n) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&st_full[t], ip[t] & 1, abort_flag, a.status) &&
-                                                     mbar_wait(&o_full[t], ip[t] & 1, abort_flag, a.status));
+                    const uint32_t ph = (t ? ip1 : ip0) & 1;
+                    // the item's notes are there by then: a product waits for them
+                    ok = __all_sync(0xffffffffu, mbar_wait(&st_full[t], ph, abort_flag, a.status) &&
+                                                     mbar_wait(&o_full[t], ph, abort_flag, a.status) &&
+                                                     mbar_wait(&note[k % kAtQueue], (k / kAtQueue) & 1, abort_flag, a.status));
                     if (!ok) break;
-                    ++ip[t];
+                    if (t) ++ip1;
+                    else ++ip0;
                     tc_fence_after();
                     ml = stat[t * kAtM + m];
+                    poison |= s_poison[k % kAtQueue];
                 }
-                const bool in = pos >= 0 && pos < a.max_kv && ml.y != 0.f;
-                const float inv = w.part >= 0 ? 1.f : 1.f / ml.y;
-                bf16* dst = a.out + (((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + g) * D;
-                const int64_t prow = (int64_t)w.part + (int64_t)w.h * w.ntok * a.G + tok * a.G + g;
+                const bool zero = !n || (!part && (pos < 0 || pos >= a.max_kv || ml.y == 0.f));
+                const float f = zero ? 0.f : part ? 1.f : 1.f / ml.y;
+                if (part && live) a.part_ml[prow + tok * a.G + g] = ml;
+                const unsigned store = __ballot_sync(0xffffffffu, live) >> (lane & 28);
+                const int row = (tok * tok_rows + g) * row_bytes;
+                int to[4];                                  // the four rows whose units the lane stores
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xffffffffu, row, (lane & 28) | i);
+                const uint32_t col = o_col + D * t;
+                // 64 bytes of a row at a time, as four units; the next columns are read while these are written
+                if (part) {
+                    uint32_t o[16];
+                    if (n) tmem_ld16(col, o);
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4 u[4] = {};
+                        if (n) {
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) u[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            if (c + 1 < D / 16) tmem_ld16(col + 16 * c + 16, o);
+                            transpose4(u, lane);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (store >> i & 1) *reinterpret_cast<uint4*>(base + to[i] + 64 * c) = u[i];
+                    }
+                } else {
                     uint32_t o[32];
-                    if (n) {
-                        tmem_ld32(tmem + 2 * kAtK + D * t + lane_off + 32 * c, o);
-                        tmem_wait_ld();
-                    }
-                    if (!live) continue;
-                    if (!n || (w.part < 0 && !in)) {
+                    if (n) tmem_ld32(col, o);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint4 u[4] = {};
+                        if (n) {
+                            tmem_wait_ld();
+                            if (!zero) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = 0;
-                    } else if (poison) {                    // what the row does see of them
-                        const int end = (int)min((int64_t)kend - 1, pos);
-                        const bf16* v = a.v[w.r] + ((int64_t)w.b * a.hkv_s + w.kvh) * a.max_kv * D + 32 * c;
-                        for (int key = first_ragged; key <= end; ++key)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float x = __bfloat162float(v[(int64_t)key * D + i]);
-                                if (!(fabsf(x) < INFINITY)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                                for (int i = 0; i < 4; ++i)
+                                    u[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f),
+                                                      pack_bf16x2(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f),
+                                                      pack_bf16x2(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f),
+                                                      pack_bf16x2(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f));
                             }
-                    }
-                    if (w.part >= 0) {
-                        float* po = a.part_o + prow * D + 32 * c;
+                            if (c + 1 < D / 32) tmem_ld32(col + 32 * c + 32, o);
+                            transpose4(u, lane);
+                        }
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4*>(po + i) =
-                                make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                            __uint_as_float(o[i + 3]));
-                    } else {
-                        const float f = in && n ? inv : 0.f;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4*>(dst + 32 * c + i) = make_uint4(
-                                pack_bf16x2(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f),
-                                pack_bf16x2(__uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f),
-                                pack_bf16x2(__uint_as_float(o[i + 4]) * f, __uint_as_float(o[i + 5]) * f),
-                                pack_bf16x2(__uint_as_float(o[i + 6]) * f, __uint_as_float(o[i + 7]) * f));
+                        for (int i = 0; i < 4; ++i)
+                            if (store >> i & 1) *reinterpret_cast<uint4*>(base + to[i] + 64 * c) = u[i];
                     }
                 }
-                if (w.part >= 0 && live) a.part_ml[prow] = ml;
                 if (n) {
                     tc_fence_before();
                     __syncwarp();
@@ -853,6 +1052,30 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                     }
                 }
             }
+            if (ok && poison) {                             // what the rows do see of the values that are not finite
+                __syncwarp();
+                const AtWork* q = &queue[k % kAtQueue];
+                for (int t = 0; t < q->nt; ++t) {
+                    const int tok = tok0 + t * a.tpt;
+                    const int64_t pos = (int64_t)q->qpos + tok;
+                    if (tok0 >= a.tpt || tok >= q->ntok || pos >= a.max_kv) continue;
+                    const int end = (int)min((int64_t)at_kend(a, *q) - 1, pos);
+                    const int ragged = max(0, (q->qpos + 1) / kAtK) * kAtK, first = max(0, q->blk0 - q->nP) * kAtK;
+                    const bf16* v = a.v[q->r] + ((int64_t)q->b * a.hkv_s + q->kvh) * a.max_kv * D;
+                    float* po = a.part_o + ((int64_t)q->part + (int64_t)q->h * q->ntok * a.G + tok * a.G + g) * D;
+                    bf16* out = a.out + (((int64_t)q->r * a.T + q->t0 + tok) * a.hq_s + q->kvh * a.G + g) * D;
+#pragma unroll 1
+                    for (int key = max(ragged, first); key <= end; ++key)
+#pragma unroll 1
+                        for (int i = 0; i < D; ++i) {
+                            const float x = __bfloat162float(v[(int64_t)key * D + i]);
+                            if (fabsf(x) < INFINITY) continue;
+                            if (q->part >= 0) po[i] += x;
+                            else out[i] = __float2bfloat16_rn(__bfloat162float(out[i]) + x);
+                        }
+                }
+            }
+            if (ok) item_done(k);
         }
     }
     tc_fence_before();
@@ -1177,19 +1400,23 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
 
     if (warp == 4) {
         if (lane == 0) {
-            uint32_t it = 0, nq = 0;
+            uint32_t it = 0, nq = 0;        // loads, Q tiles
             const uint32_t q_bytes = (uint32_t)(kAtNarrow / a.G * a.G * 128 * Sh::NKB);
             bool ok = !*abort_flag;
-            AtWork w;
-            for (int i = 0; ok; ++i) {
+            // As the wide kernel's.
+            auto take = [&]() { return total > (int)gridDim.x ? (int)gridDim.x + atomicAdd(&a.ctl->next, 1) : total; };
+            auto publish = [&](int i, int& idx, AtWork& w) {
                 const int s = i % kAnQueue;
-                int idx = total ? atomicAdd(&a.ctl->next, 1) : 0;
                 if (idx >= total) idx = -1;
-                if (!(ok = mbar_wait(&item_empty[s], ((i / kAnQueue) & 1) ^ 1, abort_flag, a.status))) break;
+                if (!(ok = mbar_wait(&item_empty[s], ((i / kAnQueue) & 1) ^ 1, abort_flag, a.status))) return;
                 *reinterpret_cast<volatile int*>(&queue[s]) = idx;
                 mbar_arrive(&item_full[s]);
-                if (idx < 0) break;
-                at_decode(a, n_wide + idx / heads, idx % heads, w);
+                if (idx >= 0) at_decode(a, n_wide + idx / heads, idx % heads, w);
+            };
+            AtWork w, wn;
+            int idx = blockIdx.x, in = 0;
+            if (ok) publish(0, idx, w);
+            for (int i = 0; ok && idx >= 0; ++i) {
                 const int grp = w.b * a.hkv_s + w.kvh;
                 auto load = [&](int j, bool v) {
                     bool own;
@@ -1213,10 +1440,19 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
                         ++nq;
                     }
                 }
+                if (!ok) break;
+                if (w.nb == 0) {
+                    in = take();
+                    publish(i + 1, in, wn);
+                }
                 for (int j = 0; j < w.nb && ok; ++j) {
+                    if (j == max(0, w.nb - 3)) in = take();
                     if (j + 1 < w.nb) load(j + 1, false);
+                    if (ok && j == max(0, w.nb - 2)) publish(i + 1, in, wn);
                     if (ok) load(j, true);
                 }
+                w = wn;
+                idx = in;
             }
             volatile int no_abort = 0;      // no copy may still be landing when the CTA exits
             if (nq) mbar_wait(q_full, (nq - 1) & 1, &no_abort, nullptr);
@@ -1303,62 +1539,84 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
 }
 
 // One warp per output row: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
-// over the row's own parts, then its prefix tile's, in their order.
+// over the row's own parts, then its prefix tile's, in their order. Bound by
+// the latency of its loads: lane i takes part i's m and l, and the first eight
+// parts' outputs are under way before these are there.
 template <int D>
 __global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParams p) {
-    constexpr int E = D / 32;                        // elements per lane
+    constexpr int E = D / 32, AHEAD = 8;             // elements per lane, parts loaded together
+    constexpr unsigned kAll = 0xffffffffu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G), heads = p.N * p.hkv_s;
     pdl_wait();
-    const int64_t units = (int64_t)p.ctl->n_chunks * heads;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int c = p.chunks[u / heads], h = (int)(u % heads), r = h / p.hkv_s;
-        const AttnGroup gr = p.groups[c >> 5];
-        const int row = (c & 31) * 8 + warp;
-        if (row >= gr.ntok * G) continue;
-        const int tok = row / G, t = gr.t0 + tok;
-        const int64_t pos = (int64_t)gr.qpos + tok;
-        const int64_t stride = (int64_t)heads * gr.ntok * G, first = gr.row + (int64_t)h * gr.ntok * G + row;
+    const unsigned units = (unsigned)p.ctl->n_chunks * heads;
+    const int n_tok = p.ctl->n_tokens;
+    for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
+        const unsigned c = u / heads;
+        const int h = u - c * heads, r = h / p.hkv_s;
+        const int4 x0 = __ldcg(reinterpret_cast<const int4*>(p.chunks + c)), x1 = __ldcg(reinterpret_cast<const int4*>(p.chunks + c) + 1);
+        const int t0 = x0.x, ntok = x0.y, qpos = x0.z, parts = x1.x;
+        const int row = x1.y * 8 + warp;
+        if (row >= ntok * G) continue;
+        const int tok = row / G, g = row - tok * G, t = t0 + tok;
+        const int64_t pos = (int64_t)qpos + tok;
+        const int64_t stride = (int64_t)heads * ntok * G, first = x0.w + (int64_t)h * ntok * G + row;
         int n2 = 0;
         int64_t first2 = 0, stride2 = 0;
         if (p.shared) {
-            const int i = t / per, ntok = min(per, p.ctl->n_tokens - i * per);
-            const int2 g = p.prefix_groups[i];
-            n2 = g.y;
-            stride2 = (int64_t)heads * ntok * G;
-            first2 = g.x + (int64_t)h * ntok * G + (t - i * per) * G + (row - tok * G);
+            const int i = t / per, k = min(per, n_tok - i * per);
+            const int2 q = __ldcg(&p.prefix_groups[i]);
+            n2 = q.y;
+            stride2 = (int64_t)heads * k * G;
+            first2 = q.x + (int64_t)h * k * G + (t - i * per) * G + g;
         }
-        const int n = gr.parts + n2;
-        auto at = [&](int i) { return i < gr.parts ? first + i * stride : first2 + (i - gr.parts) * stride2; };
-        float mx = -INFINITY;
-        for (int i = lane; i < n; i += 32) mx = fmaxf(mx, p.part_ml[at(i)].x);
-        mx = warp_max(mx);
-        float l = 0.f, o[E] = {};
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float2 ml = p.part_ml[at(i)];
-            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-            l = fmaf(f, ml.y, l);
-            const float* src = p.part_o + at(i) * D + lane * E;
-            float x[E];
-            if (E == 4) {
-                const float4 y = *reinterpret_cast<const float4*>(src);
-                x[0] = y.x, x[1] = y.y, x[E - 2] = y.z, x[E - 1] = y.w;
-            } else {
-                const float2 y = *reinterpret_cast<const float2*>(src);
-                x[0] = y.x, x[1] = y.y;
-            }
-            if (f != 0.f)
+        const int n = parts + n2;
+        auto at = [&](int i) { return i < parts ? first + i * stride : first2 + (i - parts) * stride2; };
+        float x[AHEAD][E];
+        auto load = [&](int i0) {
 #pragma unroll
-                for (int k = 0; k < E; ++k) o[k] = fmaf(f, x[k], o[k]);
+            for (int i = 0; i < AHEAD; ++i) {
+                if (i0 + i >= n) break;
+                const float* src = p.part_o + at(i0 + i) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
+                    x[i][0] = y.x, x[i][1] = y.y, x[i][2] = y.z, x[i][3] = y.w;
+                } else {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(src));
+                    x[i][0] = y.x, x[i][1] = y.y;
+                }
+            }
+        };
+        load(0);
+        float mx = -INFINITY;
+        float2 ml = make_float2(-INFINITY, 0.f);     // lane's part of the first 32
+        if (lane < n) ml = __ldcg(&p.part_ml[at(lane)]);
+        mx = ml.x;
+        for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, p.part_ml[at(i)].x);
+        mx = warp_max(mx);
+        float f = 0.f, l = 0.f, o[E] = {};
+        for (int i0 = 0; i0 < n; i0 += AHEAD) {
+            if ((i0 & 31) == 0) {                    // weights of the next 32 parts
+                if (i0) ml = i0 + lane < n ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
+                f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+                l += warp_sum(f == 0.f ? 0.f : f * ml.y);
+            }
+            if (i0) load(i0);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const float w = __shfl_sync(kAll, f, (i0 + i) & 31);
+                if (i0 + i < n && w != 0.f)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) o[k] = fmaf(w, x[i][k], o[k]);
+            }
         }
         const bool in = pos >= 0 && pos < p.max_kv && l != 0.f;
         const float inv = 1.f / l;
         uint32_t y[E / 2];
 #pragma unroll
         for (int k = 0; k < E / 2; ++k) y[k] = in ? pack_bf16x2(o[2 * k] * inv, o[2 * k + 1] * inv) : 0u;
-        bf16* dst = static_cast<bf16*>(p.out) + (((int64_t)r * p.T + t) * p.hq_s + (h - r * p.hkv_s) * G + (row - tok * G)) * D + lane * E;
-        if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[E / 2 - 1]);
+        bf16* dst = static_cast<bf16*>(p.out) + (((int64_t)r * p.T + t) * p.hq_s + (h - r * p.hkv_s) * G + g) * D + lane * E;
+        if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
         else *reinterpret_cast<uint32_t*>(dst) = y[0];
     }
 }
@@ -1396,12 +1654,11 @@ cudaError_t attn_map(const void* base, int64_t d0, int64_t d1, int64_t d2, int64
 AttnSizes attn_sizes(int64_t B, int64_t T, int hq, int hkv, int d) {
     const int64_t G = hq / hkv, per = 2 * (kAtM / G);
     // extra parts: their number times the target is at most all blocks
-    const int64_t tiles = T / per + B + 1, prefix = T / per + 2, extra = 2 * kSMs / hkv + 2, extra_n = 5 * kSMs / hkv + 2;
+    const int64_t tiles = T / per + B + 1, prefix = T / per + 2, extra = 3 * kSMs / hkv + 2, extra_n = 5 * kSMs / hkv + 2;
     AttnSizes s;
-    s.items = (size_t)(tiles + prefix + extra + extra_n) * sizeof(AttnItem);
-    s.groups = (size_t)tiles * sizeof(AttnGroup);
+    s.items = (size_t)(tiles + prefix + extra + extra_n + kSMs) * sizeof(AttnItem);
     s.prefix_groups = (size_t)prefix * sizeof(int2);
-    s.chunks = (size_t)(T * G / 8 + tiles) * sizeof(int);
+    s.chunks = (size_t)(T * G / 8 + tiles) * sizeof(AttnChunk);
     // every row once as a sequence's own and once as the prefix's, and the extra parts' rows
     const int64_t most = T < per ? T : per;
     s.rows = 2 * T * hq + extra * hkv * most * G + extra_n * hkv * (most * G < kAtNarrow ? most * G : kAtNarrow);

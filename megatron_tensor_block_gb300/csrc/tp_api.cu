@@ -70,7 +70,7 @@ struct tp_plan_s {
     size_t off_p_xn = 0, off_p_q = 0, off_p_ao = 0, off_p_h = 0, off_p_act = 0, off_p_rope = 0, ws_prefill_end = 0;
     // packed batches: counts and lists after the prefill buffers; the partial results share
     // the region of the normalised activations, which an attention stage does not need
-    size_t off_a_ctl = 0, off_a_items = 0, off_a_groups = 0, off_a_prefix = 0, off_a_chunks = 0, off_a_ml = 0, off_a_o = 0;
+    size_t off_a_ctl = 0, off_a_items = 0, off_a_prefix = 0, off_a_chunks = 0, off_a_ml = 0, off_a_o = 0;
     size_t ws_bytes = 0;
     size_t ws_decode_end = 0;           // end of the decode buffers (control words included)
     // multi-layer decode (tp_stack_decode): control words, then its own pair buffers
@@ -315,7 +315,6 @@ extern "C" tp_status tp_plan(const tp_model_desc* d, int32_t tp, tp_plan_t* out)
         P->off_p_rope = take((size_t)d->max_kv * (hd / 2) * 8);  // (cos, sin) per position and pair
         P->off_a_ctl = take(sizeof(AttnCtl));
         P->off_a_items = take(as.items);
-        P->off_a_groups = take(as.groups);
         P->off_a_prefix = take(as.prefix_groups);
         P->off_a_chunks = take(as.chunks);
         P->off_a_ml = take(as.part_ml);
@@ -1264,9 +1263,8 @@ static tp_status packed_args(const char* who, tp_plan_t plan, const tp_kv_set* p
     a.status = reinterpret_cast<int*>(ws + plan->off_status);
     a.ctl = reinterpret_cast<AttnCtl*>(ws + plan->off_a_ctl);
     a.items = reinterpret_cast<AttnItem*>(ws + plan->off_a_items);
-    a.groups = reinterpret_cast<AttnGroup*>(ws + plan->off_a_groups);
     a.prefix_groups = reinterpret_cast<int2*>(ws + plan->off_a_prefix);
-    a.chunks = reinterpret_cast<int*>(ws + plan->off_a_chunks);
+    a.chunks = reinterpret_cast<AttnChunk*>(ws + plan->off_a_chunks);
     a.part_ml = reinterpret_cast<float2*>(ws + plan->off_a_ml);
     a.part_o = reinterpret_cast<float*>(ws + plan->off_a_o);
     // A prefix that the batch shares is read once for tiles of tokens of any sequence where the sequences bring less

@@ -328,9 +328,10 @@ cudaError_t launch_lm_head(const HeadArgs& a, size_t smem, cudaStream_t s);
 // Attention of a packed batch (kernels_attn.cu).
 struct AttnCtl {
     int n_tokens;                         // cu[B], or 0 where cu is malformed
-    int n_wide, n_items, n_groups, n_chunks;   // items: n_wide wide ones, then the narrow ones
-    int next;                             // narrow items taken
-    int reserved[10];
+    int n_wide, n_items;                  // items: n_wide wide ones (or places for them), then the narrow ones
+    int n_chunks;
+    int next, next_wide;                  // narrow items taken, wide ones
+    int reserved[2];
 };
 struct AttnItem {                         // for every KV head of every shard:
     int t0, ntok;                         // token rows
@@ -339,8 +340,8 @@ struct AttnItem {                         // for every KV head of every shard:
     int kind;                             // which blocks the list has
     int row;                              // first row of its partial results, or -1: final
 };
-struct AttnGroup {                        // tokens whose results are joined from parts
-    int t0, ntok, qpos, row, parts, reserved[3];
+struct AttnChunk {                        // eight rows of a tile whose results are joined from parts
+    int t0, ntok, qpos, row, parts, chunk, reserved[2];
 };
 struct RaggedAttnParams {
     const void* q;                        // [N][T][hq_s d] bf16
@@ -360,15 +361,14 @@ struct RaggedAttnParams {
     // workspace
     AttnCtl* ctl;
     AttnItem* items;
-    AttnGroup* groups;
     int2* prefix_groups;                  // per prefix tile: first row of its partial results, parts
-    int* chunks;                          // group * 32 + eighth-rows chunk
+    AttnChunk* chunks;
     float2* part_ml;
     float* part_o;
 };
 // Workspace of a plan's packed batches; `rows` of partial results.
 struct AttnSizes {
-    size_t items, groups, prefix_groups, chunks, part_ml, part_o;
+    size_t items, prefix_groups, chunks, part_ml, part_o;
     int64_t rows;
 };
 AttnSizes attn_sizes(int64_t max_batch, int64_t max_tokens, int hq, int hkv, int d);
