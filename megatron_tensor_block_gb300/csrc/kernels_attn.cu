@@ -8,7 +8,7 @@
 //                        items, longest first, and cuts long items into parts
 //                        where the batch has too few of them for the machine;
 //   attn_items_kernel    persistent, one CTA per SM: items of many query rows;
-//   attn_narrow_kernel   two CTAs per SM: items of few query rows;
+//   attn_narrow_kernel   the same for items of few query rows;
 //   attn_combine_kernel  joins the parts of a row.
 // A call whose sequences bring few tokens each treats a shared prefix as items
 // of its own, whose rows are the batch's tokens whatever their sequence: its
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
         const unsigned long long q = all < (1ull << 32) ? (unsigned)all / parts + 1 : all / parts + 1;
         return (int)min((unsigned long long)INT_MAX / 4, max((unsigned long long)kAtMinPart, q));
     };
-    // narrow: two parts per CTA, of which there are two per SM (time goes by the bytes: parts cost little)
+    // narrow: two parts per half of a CTA (time goes by the bytes: parts cost little)
     const int target_n = share(narrow_blocks, 4 * kSMs);
     int target_w = max(kAtMinCut, share(wide_blocks, kSMs));
     if (items && items <= kSMs) {
@@ -1096,20 +1096,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
 // would be mostly padding and a row's softmax the work of one thread; so the
 // keys are the rows: S^T = K Q^T (128 keys x 16 or 32 rows), and O^T = V^T P^T
 // (d x rows) with V read as the M-major operand and P^T from shared memory. A
-// thread has one key: its scores of every row are one column each. Two CTAs per
-// SM, each with its own ring, cover one another's waits; items are taken from
-// the list as CTAs become free.
+// thread has one key: its scores of every row are one column each. A CTA works
+// at two items at a time, in two halves with a ring each that cover one
+// another's waits (a kernel that allocates tensor memory gets one CTA per SM).
+// Of each half's eight warps
 //   warps 0-3   the softmax of a block, one key per thread: maxima over the
 //               keys by redux and one exchange between the warps; P^T to shared
 //               memory in bf16; the previous block's O^T (one element of d per
 //               thread) from tensor memory to registers. m moves as in the wide
 //               kernel. The V rows that some row does not see are made finite
 //               by the thread of the key.
-//   warp 4      takes the items, TMA
+//   warp 4      takes the items from the list as the half becomes free, TMA
 //   warp 5      products
+//   warps 6, 7  nothing (registers are dealt out to groups of four warps)
 // ---------------------------------------------------------------------------
 
-constexpr int kAnThreads = 192;
+constexpr int kAnThreads = 512, kAnHalf = 256;   // of a half's two warpgroups the second gives registers to the first
+constexpr int kAnRegsIo = 80, kAnRegsSoftmax = 176;
+static_assert(kAnRegsIo + kAnRegsSoftmax <= 2 * 128, "the launch's registers");
 constexpr int kAnQueue = 4;               // items taken ahead
 
 template <int D>
@@ -1124,7 +1128,8 @@ struct AnShape {
     static constexpr int PAD = D == 64 ? KB - QB - PB : 0;
     static constexpr int SMEM = RING * KB + QB + PB + PAD + HEAD;
 };
-static_assert(2 * (AnShape<128>::SMEM + 1024) <= 228 * 1024 && 2 * (AnShape<64>::SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(2 * AnShape<128>::SMEM <= 227 * 1024 && 2 * AnShape<64>::SMEM <= 227 * 1024, "two halves");
+static_assert(AnShape<128>::SMEM % 1024 == 0 && AnShape<64>::SMEM % 1024 == 0, "alignment of the second");
 
 __device__ __forceinline__ float redux_max(float v) {
     float r;
@@ -1135,6 +1140,7 @@ __device__ __forceinline__ float redux_max(float v) {
 template <int D>
 struct AnCtx {
     const AtArgs* a;
+    int tid;                              // thread of the half's softmax
     unsigned char *ring, *p;
     uint64_t *s_full, *p_full, *o_full, *x_full, *x_empty, *v_ragged;
     float* wmax;                          // [4][kAtNarrow]
@@ -1148,7 +1154,7 @@ template <int D, int NR>
 __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
     using Sh = AnShape<D>;
     const AtArgs& a = *c.a;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = c.tid, warp = tid >> 5, lane = tid & 31;
     const int rows = w.ntok * a.G, kend = at_kend(a, w);
     const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
     float o[NR], l[NR];
@@ -1319,11 +1325,12 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid_constant__ AtArgs a) {
+__global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid_constant__ AtArgs a) {
     using Sh = AnShape<D>;
     constexpr int R = Sh::RING;
     extern __shared__ __align__(1024) unsigned char smem[];
-    unsigned char* ring = smem;
+    const int half = uniform(threadIdx.x / kAnHalf);
+    unsigned char* ring = smem + half * Sh::SMEM;
     unsigned char* sq = ring + R * Sh::KB;
     unsigned char* sp = sq + Sh::QB;
     unsigned char* head = sp + Sh::PB + Sh::PAD;
@@ -1348,8 +1355,8 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
     float* wmax = reinterpret_cast<float*>(head + Sh::HEAD - 4 * kAtNarrow * 4);
     static_assert((2 * R + 9 + 2 * kAnQueue + 1) * 8 + (kAnQueue + 4) * 4 <= Sh::HEAD - 4 * kAtNarrow * 4, "the head's words");
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
+    const int tid = threadIdx.x % kAnHalf, warp = uniform(tid >> 5), lane = tid & 31;
+    if (tid == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
@@ -1373,14 +1380,15 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
         if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
         fence_mbar_init();
     }
-    if (warp == 5) tmem_alloc(smem_u32(tmem_slot), 128);
+    if (warp == 5 && half == 0) tmem_alloc(smem_u32(tmem_slot), 256);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(*reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(tmem_slot) - half * Sh::SMEM)) + 128 * half;
     // Behind the wide kernel the lists are there: it lets this one start only after its own wait. This kernel waits for
     // the wide one at its end, so that what follows it follows both.
     if (!a.after_wide) pdl_wait();
+    pdl_trigger();
     const int heads = a.N * a.hkv_s;
     const int n_wide = __ldcg(&a.ctl->n_wide);
     const int total = *abort_flag ? 0 : (__ldcg(&a.ctl->n_items) - n_wide) * heads;
@@ -1398,13 +1406,14 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
         return true;
     };
 
-    if (warp == 4) {
-        if (lane == 0) {
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAnRegsIo));
+        if (warp == 4 && lane == 0) {
             uint32_t it = 0, nq = 0;        // loads, Q tiles
             const uint32_t q_bytes = (uint32_t)(kAtNarrow / a.G * a.G * 128 * Sh::NKB);
             bool ok = !*abort_flag;
-            // As the wide kernel's.
-            auto take = [&]() { return total > (int)gridDim.x ? (int)gridDim.x + atomicAdd(&a.ctl->next, 1) : total; };
+            // As the wide kernel's, the first one too: behind that kernel the CTAs start as its CTAs end.
+            auto take = [&]() { return total ? atomicAdd(&a.ctl->next, 1) : 0; };
             auto publish = [&](int i, int& idx, AtWork& w) {
                 const int s = i % kAnQueue;
                 if (idx >= total) idx = -1;
@@ -1414,8 +1423,11 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
                 if (idx >= 0) at_decode(a, n_wide + idx / heads, idx % heads, w);
             };
             AtWork w, wn;
-            int idx = blockIdx.x, in = 0;
-            if (ok) publish(0, idx, w);
+            int idx = -1, in = 0;
+            if (ok) {
+                idx = take();
+                publish(0, idx, w);
+            }
             for (int i = 0; ok && idx >= 0; ++i) {
                 const int grp = w.b * a.hkv_s + w.kvh;
                 auto load = [&](int j, bool v) {
@@ -1458,66 +1470,67 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
             if (nq) mbar_wait(q_full, (nq - 1) & 1, &no_abort, nullptr);
             for (uint32_t k = it > (uint32_t)R ? it - R : 0; k < it; ++k)
                 mbar_wait(&kv_full[k % R], (k / R) & 1, &no_abort, nullptr);
-        }
-    } else if (warp == 5) {
-        const uint64_t dq = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring)), dp = smem_desc_sw128(smem_u32(sp));
-        const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
-        uint32_t it = 0, blocks = 0, nq = 0;
-        bool ok = !*abort_flag, more = true;
-        auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-            return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
-        };
-        AtWork w;
-        for (int i = 0; ok; ++i) {
-            if (!(ok = item(i, w, more)) || !more) break;
-            if (!w.nb) continue;
-            const int nr = w.ntok * a.G <= 16 ? 16 : 32;
-            const uint32_t id_s = idesc_bf16(kAtK, nr), id_o = idesc_bf16_amn(128, nr);
-            auto issue_s = [&](int j) {                  // S^T of block j into the buffer of its turn
-                const uint32_t s = it % R;
-                if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) return;
-                ++it;
-                tc_fence_after();
-                const uint64_t dk = at_desc_add(dk0, s * Sh::KB);
-#pragma unroll
-                for (int kb = 0; kb < Sh::NKB; ++kb)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_w(tmem + 32 * ((blocks + j) & 1), at_desc_add(dk, kb * (kAtK * 128) + k * 32),
-                                 at_desc_add(dq, kb * (kAtNarrow * 128) + k * 32), id_s, (kb | k) != 0);
-                tc_commit_w(smem_u32(&s_full[(blocks + j) & 1]));
-                tc_commit_w(smem_u32(&kv_empty[s]));
-                if (j + 1 == w.nb) tc_commit_w(smem_u32(q_empty));
+        } else if (warp == 5) {
+            const uint64_t dq = smem_desc_sw128(smem_u32(sq)), dk0 = smem_desc_sw128(smem_u32(ring)), dp = smem_desc_sw128(smem_u32(sp));
+            const uint64_t dv0 = smem_desc_mn_sw128(smem_u32(ring), kAtK * 128, 1024);
+            uint32_t it = 0, blocks = 0, nq = 0;
+            bool ok = !*abort_flag, more = true;
+            auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, a.status));
             };
-            if (!(ok = wait_all(q_full, nq & 1))) break;
-            ++nq;
-            issue_s(0);
-            for (int j = 0; j < w.nb && ok; ++j) {
-                if (j + 1 < w.nb) issue_s(j + 1);
-                if (!ok) break;
-                const uint32_t s = it % R;
-                if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) break;
-                ++it;
-                bool own;
-                const int key0 = at_block(w, j, own);
-                if (own && at_ragged(w, key0) && lane == 0) mbar_arrive(v_ragged);
-                __syncwarp();
-                if (!(ok = wait_all(p_full, (blocks + j) & 1))) break;
-                tc_fence_after();
-                const int valid = min(kAtK, (own ? at_kend(a, w) : a.prefix_len) - key0), steps = (valid + 15) >> 4;
-                const uint64_t dv = at_desc_add(dv0, s * Sh::KB);
-#pragma unroll 1
-                for (int kk = 0; kk < steps; ++kk)       // O^T of the block alone
-                    tc_mma_w(tmem + 64, at_desc_add(dv, kk * 16 * 128),
-                             at_desc_add(dp, (kk >> 2) * (kAtNarrow * 128) + (kk & 3) * 32), id_o, kk != 0);
-                tc_commit_w(smem_u32(o_full));
-                tc_commit_w(smem_u32(&kv_empty[s]));
+            AtWork w;
+            for (int i = 0; ok; ++i) {
+                if (!(ok = item(i, w, more)) || !more) break;
+                if (!w.nb) continue;
+                const int nr = w.ntok * a.G <= 16 ? 16 : 32;
+                const uint32_t id_s = idesc_bf16(kAtK, nr), id_o = idesc_bf16_amn(128, nr);
+                auto issue_s = [&](int j) {                  // S^T of block j into the buffer of its turn
+                    const uint32_t s = it % R;
+                    if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) return;
+                    ++it;
+                    tc_fence_after();
+                    const uint64_t dk = at_desc_add(dk0, s * Sh::KB);
+    #pragma unroll
+                    for (int kb = 0; kb < Sh::NKB; ++kb)
+    #pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_w(tmem + 32 * ((blocks + j) & 1), at_desc_add(dk, kb * (kAtK * 128) + k * 32),
+                                     at_desc_add(dq, kb * (kAtNarrow * 128) + k * 32), id_s, (kb | k) != 0);
+                    tc_commit_w(smem_u32(&s_full[(blocks + j) & 1]));
+                    tc_commit_w(smem_u32(&kv_empty[s]));
+                    if (j + 1 == w.nb) tc_commit_w(smem_u32(q_empty));
+                };
+                if (!(ok = wait_all(q_full, nq & 1))) break;
+                ++nq;
+                issue_s(0);
+                for (int j = 0; j < w.nb && ok; ++j) {
+                    if (j + 1 < w.nb) issue_s(j + 1);
+                    if (!ok) break;
+                    const uint32_t s = it % R;
+                    if (!(ok = wait_all(&kv_full[s], (it / R) & 1))) break;
+                    ++it;
+                    bool own;
+                    const int key0 = at_block(w, j, own);
+                    if (own && at_ragged(w, key0) && lane == 0) mbar_arrive(v_ragged);
+                    __syncwarp();
+                    if (!(ok = wait_all(p_full, (blocks + j) & 1))) break;
+                    tc_fence_after();
+                    const int valid = min(kAtK, (own ? at_kend(a, w) : a.prefix_len) - key0), steps = (valid + 15) >> 4;
+                    const uint64_t dv = at_desc_add(dv0, s * Sh::KB);
+    #pragma unroll 1
+                    for (int kk = 0; kk < steps; ++kk)       // O^T of the block alone
+                        tc_mma_w(tmem + 64, at_desc_add(dv, kk * 16 * 128),
+                                 at_desc_add(dp, (kk >> 2) * (kAtNarrow * 128) + (kk & 3) * 32), id_o, kk != 0);
+                    tc_commit_w(smem_u32(o_full));
+                    tc_commit_w(smem_u32(&kv_empty[s]));
+                }
+                blocks += w.nb;
             }
-            blocks += w.nb;
+            tc_commit_w(smem_u32(done));
         }
-        tc_commit_w(smem_u32(done));
     } else {
-        AnCtx<D> c{&a, ring, sp, s_full, p_full, o_full, x_full, x_empty, v_ragged, wmax, abort_flag, s_poison, tmem, 0, 0, 0, 0, 0};
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAnRegsSoftmax));
+        AnCtx<D> c{&a, tid, ring, sp, s_full, p_full, o_full, x_full, x_empty, v_ragged, wmax, abort_flag, s_poison, tmem, 0, 0, 0, 0, 0};
         bool ok = !*abort_flag, more = true;
         AtWork w;
         for (int i = 0; ok; ++i) {
@@ -1527,12 +1540,13 @@ __global__ void __launch_bounds__(kAnThreads, 2) attn_narrow_kernel(const __grid
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
-        volatile int no_abort = 0;                   // every MMA has retired before the columns are freed
+    if (warp == 5 && half == 0) {
+        volatile int no_abort = 0;                   // every MMA of both halves has retired before the columns are freed
         mbar_wait(done, 0, &no_abort, nullptr);
+        mbar_wait(reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(done) + Sh::SMEM), 0, &no_abort, nullptr);
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc(tmem, 128);
+        tmem_dealloc(tmem, 256);
         tmem_relinquish();
     }
     pdl_wait();
@@ -1719,9 +1733,9 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     }
     const void* fn = d128 ? reinterpret_cast<const void*>(attn_narrow_kernel<128>)
                           : reinterpret_cast<const void*>(attn_narrow_kernel<64>);
-    const int smem = d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM;
+    const int smem = 2 * (d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM);
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess) e = launch_pdl(fn, args, 2 * kSMs, smem, s, kAnThreads);
+    if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kAnThreads);
     if (e != cudaSuccess) return e;
     RaggedAttnParams c = p;
     void* cargs[] = {&c};
