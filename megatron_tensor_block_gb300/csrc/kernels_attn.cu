@@ -77,9 +77,12 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     constexpr unsigned kAll = 0xffffffffu;
     pdl_trigger();
     s_hist[tid] = 0;
-    if (tid == 0) s_rows = s_chunks = 0;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G);            // tokens per item
     const int heads = p.N * p.hkv_s;
+    if (tid == 0) {
+        s_rows = 2 * p.T * heads * G;                                // behind the places of part 0
+        s_chunks = 0;
+    }
     const int n_prefix = (p.prefix_len + kAtK - 1) / kAtK;           // prefix blocks
     const int in_item = p.shared ? 0 : n_prefix;
     const int lanes = min(32, (p.B + 31) / 32);                      // sequences per warp and round
@@ -183,15 +186,13 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     if (items && items <= kSMs) {
         // The parts per item that are done first, in blocks' time: rounds of parts, each two blocks' longer than its blocks,
         // and the joining, a block's time for about 4.8 MB of float32 results there and back.
-        const float join = (float)(items * 2 * kAtM) * p.d * 8 / 4.8e6f;
-        float best = 1e30f;
-        int parts = 1;
-        for (int k = 1; k <= kAtMaxParts && k * items <= 3 * kSMs; ++k) {
-            const int len = (longest + k - 1) / k;
-            if (k > 1 && len < kAtMinCut) break;
-            const float t = (float)((int)(k * items + kSMs - 1) / kSMs) * (len + 2) + (k > 1 ? k * join : 0.f);
-            if (t < best) best = t, parts = k;
-        }
+        // Lane k - 1 takes k parts.
+        const int all = (int)items, k = lane + 1, len = (longest + k - 1) / k;
+        const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.8e6f;
+        float t = (float)((k * all + kSMs - 1) / kSMs * (len + 2)) + (k > 1 ? k * join : 0.f);
+        if (k > 1 && (k > kAtMaxParts || k * all > 3 * kSMs || len < kAtMinCut)) t = INFINITY;
+        const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));           // positive: ordered as their bits
+        const int parts = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best));
         target_w = (longest + parts - 1) / parts;
     }
     // a last round of few items, if nothing else is cut: parts for its items
@@ -250,20 +251,35 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
                 for (int j = parts; j < last_parts; ++j) p.items[from + j] = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};   // no rows
             }
         }
-        int row = -1;
+        // partial results: part 0 of a tile at the place of its tokens, the others where there is room
+        const int rows = heads * k * G;
+        int row0 = -1, row1 = 0;
         if (parts > 1 || p.shared) {
-            row = atomicAdd(&s_rows, parts * heads * k * G);
+            row0 = heads * G * ((kind & AT_OWN ? 0 : p.T) + t0);
+            if (parts > 1) row1 = atomicAdd(&s_rows, (parts - 1) * rows);
             if (kind & AT_OWN) {
-                const int chunks = (k * G + 7) / 8, c = atomicAdd(&s_chunks, chunks);
-                for (int j = 0; j < chunks; ++j) p.chunks[c + j] = AttnChunk{t0, k, q, row, parts, j, 0, 0};
+                // the lanes' chunks, added up in one atomic: ranks by the bits of their counts
+                const int chunks = (k * G + 7) / 8;
+                const unsigned with = __activemask(), below = with & ((1u << lane) - 1);
+                int before = 0, sum = 0;
+#pragma unroll
+                for (int b = 0; b < 6; ++b) {
+                    const unsigned v = __ballot_sync(with, chunks >> b & 1);
+                    before += __popc(v & below) << b;
+                    sum += __popc(v) << b;
+                }
+                int c = 0;
+                if (!below) c = atomicAdd(&s_chunks, sum);
+                c = __shfl_sync(with, c, __ffs(with) - 1) + before;
+                for (int j = 0; j < chunks; ++j) p.chunks[c + j] = AttnChunk{t0, k, q, row1, parts, j, 0, 0};
             } else {
-                p.prefix_groups[i] = make_int2(row, parts);
+                p.prefix_groups[i] = make_int2(row1, parts);
             }
         }
         for (int j = 0; j < parts; ++j) {
             const int k0 = j * len, k1 = min(nb, k0 + len);
             const int e = from >= 0 ? from + j : atomicAdd(&s_hist[bucket(k1 - k0, nar)], 1);
-            p.items[e] = AttnItem{t0, k, b, q, k0, k1, kind, row < 0 ? -1 : row + j * heads * k * G};
+            p.items[e] = AttnItem{t0, k, b, q, k0, k1, kind, j && row0 >= 0 ? row1 + (j - 1) * rows : row0};
         }
     };
     const int kind = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
@@ -1562,9 +1578,11 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParam
     constexpr unsigned kAll = 0xffffffffu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G), heads = p.N * p.hkv_s;
-    pdl_wait();
-    const unsigned units = (unsigned)p.ctl->n_chunks * heads;
-    const int n_tok = p.ctl->n_tokens;
+    // the lists are there when this kernel is launched (the kernels before it let it start once they have them), and are
+    // read while those work
+    const unsigned units = (unsigned)__ldcg(&p.ctl->n_chunks) * heads;
+    const int n_tok = __ldcg(&p.ctl->n_tokens);
+    bool waited = false;
     for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
         const unsigned c = u / heads;
         const int h = u - c * heads, r = h / p.hkv_s;
@@ -1573,19 +1591,29 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParam
         const int row = x1.y * 8 + warp;
         if (row >= ntok * G) continue;
         const int tok = row / G, g = row - tok * G, t = t0 + tok;
+        const int64_t row0 = (int64_t)heads * G * t0 + (int64_t)h * ntok * G + row;
         const int64_t pos = (int64_t)qpos + tok;
-        const int64_t stride = (int64_t)heads * ntok * G, first = x0.w + (int64_t)h * ntok * G + row;
+        const int64_t stride = (int64_t)heads * ntok * G, first = x0.w + (int64_t)h * ntok * G + row - stride;
         int n2 = 0;
-        int64_t first2 = 0, stride2 = 0;
+        int64_t row2 = 0, first2 = 0, stride2 = 0;
         if (p.shared) {
             const int i = t / per, k = min(per, n_tok - i * per);
             const int2 q = __ldcg(&p.prefix_groups[i]);
             n2 = q.y;
             stride2 = (int64_t)heads * k * G;
-            first2 = q.x + (int64_t)h * k * G + (t - i * per) * G + g;
+            const int64_t in_tile = (int64_t)h * k * G + (t - i * per) * G + g;
+            row2 = (int64_t)heads * G * ((int64_t)p.T + i * per) + in_tile;
+            first2 = q.x + in_tile - stride2;
         }
         const int n = parts + n2;
-        auto at = [&](int i) { return i < parts ? first + i * stride : first2 + (i - parts) * stride2; };
+        auto at = [&](int i) {
+            const int j = i - parts;
+            return j < 0 ? (i ? first + i * stride : row0) : (j ? first2 + j * stride2 : row2);
+        };
+        if (!waited) {
+            pdl_wait();
+            waited = true;
+        }
         float x[AHEAD][E];
         auto load = [&](int i0) {
 #pragma unroll
@@ -1633,6 +1661,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParam
         if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
         else *reinterpret_cast<uint32_t*>(dst) = y[0];
     }
+    if (!waited) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------

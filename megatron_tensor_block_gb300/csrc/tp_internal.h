@@ -341,7 +341,7 @@ struct AttnItem {                         // for every KV head of every shard:
     int row;                              // first row of its partial results, or -1: final
 };
 struct AttnChunk {                        // eight rows of a tile whose results are joined from parts
-    int t0, ntok, qpos, row, parts, chunk, reserved[2];
+    int t0, ntok, qpos, row, parts, chunk, reserved[2];   // row: first of part 1's
 };
 struct RaggedAttnParams {
     const void* q;                        // [N][T][hq_s d] bf16
@@ -361,7 +361,7 @@ struct RaggedAttnParams {
     // workspace
     AttnCtl* ctl;
     AttnItem* items;
-    int2* prefix_groups;                  // per prefix tile: first row of its partial results, parts
+    int2* prefix_groups;                  // per prefix tile: first row of part 1's results, parts
     AttnChunk* chunks;
     float2* part_ml;
     float* part_o;
