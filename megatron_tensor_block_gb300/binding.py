@@ -325,28 +325,35 @@ def tp_lm_head_forward(plan: Plan, head_shards: list, gamma, x, T: int, logits, 
 
 
 class _Torch:
-    """torch's types and current device, looked up once."""
-    types = None
+    """torch's types, current device and raw current stream, looked up once."""
+    bf16 = f32 = i32 = u8 = None
 
     @classmethod
     def device(cls) -> int:
-        """The current device; -1 (no tensor's device) where there is none."""
-        import torch
-        if cls.types is None:
-            cls.types = {n: getattr(torch, n) for n in ("bfloat16", "float32", "int32", "uint8")}
-            cls.current = staticmethod(torch.cuda.current_device if torch.cuda.is_available() else lambda: -2)
+        """The current device; one that no tensor is on where there is none."""
+        if cls.bf16 is None:
+            import torch
+            cls.bf16, cls.f32, cls.i32, cls.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+            there = torch.cuda.is_available()
+            cls.current = staticmethod(torch.cuda.current_device if there else lambda: -2)
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            cls.raw = staticmethod(raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
         return cls.current()
 
+    @classmethod
+    def stream(cls, s, device: int):
+        return cls.raw(device) if s is None else _stream(s)
 
-def _checked(t, name: str, dtype: str, numel: int, device: int) -> int | None:
+
+def _checked(t, name: str, dtype, numel: int, device: int) -> int | None:
     """Address of a tensor argument after the checks that an address alone
     does not allow: type, contiguity, size, device. Integers pass as they are."""
     if t is None or type(t) is int:
         return t
-    if (t.dtype is _Torch.types[dtype] and t.numel() >= numel and t.get_device() == device and t.is_contiguous()):
+    if t.dtype is dtype and t.get_device() == device and t.numel() >= numel and t.is_contiguous():
         return t.data_ptr()
-    if t.dtype is not _Torch.types[dtype]:
-        raise TypeError(f"{name}: {t.dtype}, expected torch.{dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
     if t.numel() < numel:
@@ -356,12 +363,12 @@ def _checked(t, name: str, dtype: str, numel: int, device: int) -> int | None:
 
 def _kv_checked(plan: Plan, kv, name: str, rows: int, device: int) -> tp_kv_set:
     """``kv = (k list, v list)``; every tensor holds at least ``rows`` rows per KV head."""
-    n = rows * plan.hkv_shard * plan.head_dim
+    n, bf16 = rows * plan.hkv_shard * plan.head_dim, _Torch.bf16
     k, v = kv
     if len(k) != plan.tp or len(v) != plan.tp:
         raise ValueError(f"{name}: expected a K and a V cache for each of {plan.tp} shards")
-    return tp_kv_set(_P8(*[_checked(t, name, "bfloat16", n, device) for t in k]),
-                     _P8(*[_checked(t, name, "bfloat16", n, device) for t in v]))
+    return tp_kv_set(_P8(*[_checked(t, name, bf16, n, device) for t in k]),
+                     _P8(*[_checked(t, name, bf16, n, device) for t in v]))
 
 
 def tp_attn_packed(plan: Plan, q, kv: tuple, cu, pos, B: int, T: int, out, workspace, nbytes: int, stream=None) -> None:
@@ -369,10 +376,10 @@ def tp_attn_packed(plan: Plan, q, kv: tuple, cu, pos, B: int, T: int, out, works
     ``cu[b]..cu[b+1]-1`` at positions ``pos[b]..`` of the caches ``kv = (k list, v list)``."""
     n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
     kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv, dev)
-    _check(load().tp_attn_packed(plan.handle, _checked(q, "q", "bfloat16", n, dev), C.byref(kvs),
-                                 _checked(cu, "cu", "int32", B + 1, dev), _checked(pos, "pos", "int32", B, dev), B, T,
-                                 _checked(out, "out", "bfloat16", n, dev), _checked(workspace, "workspace", "uint8", nbytes, dev),
-                                 nbytes, _stream(stream)))
+    _check(load().tp_attn_packed(plan.handle, _checked(q, "q", _Torch.bf16, n, dev), C.byref(kvs),
+                                 _checked(cu, "cu", _Torch.i32, B + 1, dev), _checked(pos, "pos", _Torch.i32, B, dev), B, T,
+                                 _checked(out, "out", _Torch.bf16, n, dev), _checked(workspace, "workspace", _Torch.u8, nbytes, dev),
+                                 nbytes, _Torch.stream(stream, dev)))
 
 
 def tp_attn_prefix(plan: Plan, q, prefix: tuple, prefix_len: int, prefix_rows: int, kv: tuple, cu, pos, B: int, T: int,
@@ -382,10 +389,10 @@ def tp_attn_prefix(plan: Plan, q, prefix: tuple, prefix_len: int, prefix_rows: i
     n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
     pre = _kv_checked(plan, prefix, "prefix", prefix_rows, dev) if prefix_len else None
     kvs = _kv_checked(plan, kv, "kv", plan.max_batch * plan.max_kv, dev)
-    _check(load().tp_attn_prefix(plan.handle, _checked(q, "q", "bfloat16", n, dev), C.byref(pre) if pre is not None else None,
-                                 prefix_len, prefix_rows, C.byref(kvs), _checked(cu, "cu", "int32", B + 1, dev),
-                                 _checked(pos, "pos", "int32", B, dev), B, T, _checked(out, "out", "bfloat16", n, dev),
-                                 _checked(workspace, "workspace", "uint8", nbytes, dev), nbytes, _stream(stream)))
+    _check(load().tp_attn_prefix(plan.handle, _checked(q, "q", _Torch.bf16, n, dev), C.byref(pre) if pre is not None else None,
+                                 prefix_len, prefix_rows, C.byref(kvs), _checked(cu, "cu", _Torch.i32, B + 1, dev),
+                                 _checked(pos, "pos", _Torch.i32, B, dev), B, T, _checked(out, "out", _Torch.bf16, n, dev),
+                                 _checked(workspace, "workspace", _Torch.u8, nbytes, dev), nbytes, _Torch.stream(stream, dev)))
 
 
 def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, B: int, T: int, workspace, nbytes: int,
@@ -397,9 +404,9 @@ def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, 
     n = T * plan.hidden
     _check(load().tp_block_forward_packed(plan.handle, C.byref(_shard_set(shards)), C.byref(kvs),
                                           C.byref(pre) if pre is not None else None, prefix_len, prefix_rows,
-                                          _checked(x, "x", "float32", n, dev), _checked(y, "y", "float32", n, dev),
-                                          _checked(cu, "cu", "int32", B + 1, dev), _checked(pos, "pos", "int32", B, dev), B, T,
-                                          _checked(workspace, "workspace", "uint8", nbytes, dev), nbytes, _stream(stream)))
+                                          _checked(x, "x", _Torch.f32, n, dev), _checked(y, "y", _Torch.f32, n, dev),
+                                          _checked(cu, "cu", _Torch.i32, B + 1, dev), _checked(pos, "pos", _Torch.i32, B, dev), B, T,
+                                          _checked(workspace, "workspace", _Torch.u8, nbytes, dev), nbytes, _Torch.stream(stream, dev)))
 
 
 def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=None, n_prompt=None, repetition=None,
@@ -412,14 +419,14 @@ def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=No
     if mask_rows is None:
         mask_rows = 0 if mask is None or isinstance(mask, int) else mask.numel() // max(words, 1)
     c = tp_logit_controls(
-        _checked(tokens, "tokens", "int32", 0, dev), _checked(cu_tokens, "cu_tokens", "int32", T + 1, dev),
-        _checked(n_prompt, "n_prompt", "int32", T, dev), _checked(repetition, "repetition", "float32", T, dev),
-        _checked(presence, "presence", "float32", T, dev), _checked(frequency, "frequency", "float32", T, dev),
-        _checked(bias_ids, "bias_ids", "int32", 0, dev), _checked(bias_values, "bias_values", "float32", 0, dev),
-        _checked(cu_bias, "cu_bias", "int32", T + 1, dev), _checked(mask, "mask", "int32", mask_rows * words, dev),
-        _checked(mask_row, "mask_row", "int32", T, dev), mask_rows, 0)
-    _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", "float32", T * plan.org_vocab, dev), T, C.byref(c),
-                                    _checked(out, "out", "float32", T * plan.org_vocab, dev), _stream(stream)))
+        _checked(tokens, "tokens", _Torch.i32, 0, dev), _checked(cu_tokens, "cu_tokens", _Torch.i32, T + 1, dev),
+        _checked(n_prompt, "n_prompt", _Torch.i32, T, dev), _checked(repetition, "repetition", _Torch.f32, T, dev),
+        _checked(presence, "presence", _Torch.f32, T, dev), _checked(frequency, "frequency", _Torch.f32, T, dev),
+        _checked(bias_ids, "bias_ids", _Torch.i32, 0, dev), _checked(bias_values, "bias_values", _Torch.f32, 0, dev),
+        _checked(cu_bias, "cu_bias", _Torch.i32, T + 1, dev), _checked(mask, "mask", _Torch.i32, mask_rows * words, dev),
+        _checked(mask_row, "mask_row", _Torch.i32, T, dev), mask_rows, 0)
+    _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", _Torch.f32, T * plan.org_vocab, dev), T, C.byref(c),
+                                    _checked(out, "out", _Torch.f32, T * plan.org_vocab, dev), _Torch.stream(stream, dev)))
 
 
 def tp_reduce_partials(plan: Plan, partials, residual, bias, out, M: int, stream=None) -> None:

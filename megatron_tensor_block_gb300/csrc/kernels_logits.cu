@@ -20,18 +20,18 @@
 
 namespace tpk {
 
-constexpr int kLogitThreads = 256;
-
 // V < 2^31 and a row's slice starts at most 3 entries before a multiple of
 // SLICE, so that a group of four logits is 16-byte aligned in memory: group
 // position 0 of slice s is vocabulary entry s * SLICE - shift, shift = (t * V)
-// mod 4 entries.
-template <int SLICE>
-__global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const LogitArgs a) {
-    constexpr int PER = SLICE / 4 / kLogitThreads;          // groups of four per thread
-    static_assert(PER >= 1 && SLICE % (4 * kLogitThreads) == 0, "a slice is whole groups of every thread");
-    __shared__ __align__(16) unsigned cnt[SLICE];
-    __shared__ int s_ids[kLogitThreads];
+// mod 4 entries. The groups are taken AHEAD per thread at a time, the first
+// before the history is read.
+template <int SLICE, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel(const LogitArgs a) {
+    constexpr int PER = SLICE / 4 / THREADS;                // groups of four per thread
+    constexpr int AHEAD = PER < 2 ? PER : 2;
+    static_assert(PER % AHEAD == 0 && SLICE % (4 * THREADS) == 0, "a slice is whole rounds of every thread");
+    extern __shared__ __align__(16) unsigned cnt[];         // [SLICE], a word per lane, the ids of a short bias list
+    int* s_ids = reinterpret_cast<int*>(cnt + SLICE + 32);
     const int tid = threadIdx.x;
     const int t = blockIdx.x / a.slices, slice = blockIdx.x - t * a.slices;
     const int64_t row0 = (int64_t)t * a.V;
@@ -39,6 +39,23 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
     const int v0 = slice * SLICE - shift;
     const bool in_place = a.x == a.y;
     pdl_wait();
+
+    float4 x[AHEAD];
+    auto load = [&](int v, float4& r) {
+        const float* p = a.x + row0 + v;
+        if (a.vec && v >= 0 && v + 3 < a.V) {
+            r = __ldcs(reinterpret_cast<const float4*>(p));
+        } else {
+            r.x = v >= 0 && v < a.V ? p[0] : 0.f;
+            r.y = v + 1 >= 0 && v + 1 < a.V ? p[1] : 0.f;
+            r.z = v + 2 >= 0 && v + 2 < a.V ? p[2] : 0.f;
+            r.w = v + 3 >= 0 && v + 3 < a.V ? p[3] : 0.f;
+        }
+    };
+    auto group = [&](int i) { return v0 + 4 * (tid + i * THREADS); };
+    if (!in_place && a.vec && v0 >= 0 && v0 + SLICE <= a.V)
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) load(group(i), x[i]);
 
     int h0 = 0, hn = 0, b0 = 0, bn = 0, np = 0;
     float rep = 1.f, pres = 0.f, freq = 0.f;
@@ -62,93 +79,117 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
     }
     if (in_place && !hn && !bn && !mask) return;
 
-    // the thread's logits: groups tid, tid + 256, ... of the slice
-    float4 x[PER];
-    const bool ahead = !in_place;
-    auto load = [&](int v, float4& r) {
-        const float* p = a.x + row0 + v;
-        if (a.vec && v >= 0 && v + 3 < a.V) {
-            r = *reinterpret_cast<const float4*>(p);
-        } else {
-            r.x = v >= 0 && v < a.V ? p[0] : 0.f;
-            r.y = v + 1 >= 0 && v + 1 < a.V ? p[1] : 0.f;
-            r.z = v + 2 >= 0 && v + 2 < a.V ? p[2] : 0.f;
-            r.w = v + 3 >= 0 && v + 3 < a.V ? p[3] : 0.f;
-        }
-    };
-    if (ahead)
-#pragma unroll
-        for (int i = 0; i < PER; ++i) load(v0 + 4 * (tid + i * kLogitThreads), x[i]);
-
     const int lo = max(v0, 0), hi = (int)min((int64_t)v0 + SLICE, (int64_t)a.V);
+    const unsigned span = (unsigned)max(hi - lo, 0);
     int id = -1;                                            // the thread's entry of a short bias list
-    if (bn && bn <= kLogitThreads && tid < bn) s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
+    if (bn && bn <= THREADS && tid < bn) s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
     if (hn) {
-        for (int i = tid; i < SLICE / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < SLICE / 4; i += THREADS) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        auto hit = [&](int tok, int i) {
-            if (tok < lo || tok >= hi) return;
-            if (i < np) atomicOr(&cnt[tok - v0], 1u);
-            else atomicAdd(&cnt[tok - v0], 2u);
-        };
-        // four tokens per load, four loads in flight
-        const int* h = a.tokens + h0;
-        const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2) & 3), hn), nv = (hn - head) >> 2;
-        if (tid < head) hit(h[tid], tid);
-        const int4* h4 = reinterpret_cast<const int4*>(h + head);
-        for (int j = tid; j < nv; j += 4 * kLogitThreads) {
-            int4 w[4];
+        // Every token counts somewhere, one outside the slice in a word of its lane behind it: no branch, which would
+        // cost more than the count. Four tokens per load, four loads in flight.
+        const int out = SLICE + (tid & 31) - lo + v0;
+        auto scan = [&](const int* h, int n, auto&& count) {
+            auto one = [&](int tok) {
+                const unsigned u = (unsigned)tok - (unsigned)lo;
+                count(&cnt[(int)(u < span ? u : (unsigned)out) + (lo - v0)]);
+            };
+            auto four = [&](const int4& w) {
+                one(w.x);
+                one(w.y);
+                one(w.z);
+                one(w.w);
+            };
+            const int head = min((int)(((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2) & 3), n), nv = (n - head) >> 2;
+            if (tid < head) one(h[tid]);
+            const int4* h4 = reinterpret_cast<const int4*>(h + head);
+            int j = tid;
+            for (; j + 3 * THREADS < nv; j += 4 * THREADS) {
+                int4 w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = j + k * kLogitThreads < nv ? h4[j + k * kLogitThreads] : make_int4(-1, -1, -1, -1);
+                for (int k = 0; k < 4; ++k) w[k] = h4[j + k * THREADS];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = head + 4 * (j + k * kLogitThreads);
-                hit(w[k].x, i);
-                hit(w[k].y, i + 1);
-                hit(w[k].z, i + 2);
-                hit(w[k].w, i + 3);
+                for (int k = 0; k < 4; ++k) four(w[k]);
             }
-        }
-        for (int i = head + 4 * nv + tid; i < hn; i += kLogitThreads) hit(h[i], i);
+            for (; j < nv; j += THREADS) four(h4[j]);
+            if (head + 4 * nv + tid < n) one(h[head + 4 * nv + tid]);
+        };
+        const int n0 = min(max(np, 0), hn);
+        scan(a.tokens + h0, n0, [](unsigned* w) { atomicOr(w, 1u); });
+        scan(a.tokens + h0 + n0, hn - n0, [](unsigned* w) { atomicAdd(w, 2u); });
         __syncthreads();
     }
-    auto allowed4 = [&](int v) -> unsigned {                // mask bits of entries v .. v + 3
-        if (!mask) return 15u;
-        const int va = max(v, 0), vb = min(v + 3, a.V - 1);
+
+    // mask bits of the entries v .. v + 3, some of which may be out of range
+    auto allowed4 = [&](int v) -> unsigned {
+        const int va = min(max(v, 0), a.V - 1), vb = min(max(v + 3, 0), a.V - 1);
         const uint32_t w0 = mask[va >> 5], w1 = mask[vb >> 5];
         return (v >= 0 ? __funnelshift_r(w0, w1, v & 31) : w0 << -v) & 15u;
     };
-
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int g = tid + i * kLogitThreads, v = v0 + 4 * g;
-        if (v >= a.V || v + 3 < 0) continue;
-        const uint4 c4 = hn ? reinterpret_cast<const uint4*>(cnt)[g] : make_uint4(0, 0, 0, 0);
-        const unsigned allowed = allowed4(v);
-        const bool touched = (c4.x | c4.y | c4.z | c4.w) || allowed != 15u;
-        if (in_place) {
-            if (!touched) continue;
-            load(v, x[i]);
-        }
-        float e[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        if (touched) {
-            const unsigned c[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (c[k]) {
-                    e[k] = e[k] > 0.f ? e[k] / rep : e[k] * rep;
-                    if (c[k] > 1u) e[k] = e[k] - freq * (float)(c[k] >> 1) - pres;
-                }
-                if (!((allowed >> k) & 1u)) e[k] = -INFINITY;
-            }
-        }
-        float* p = a.y + row0 + v;
-        if (a.vec && v >= 0 && v + 3 < a.V) {
-            *reinterpret_cast<float4*>(p) = make_float4(e[0], e[1], e[2], e[3]);
-        } else {
+    auto change = [&](float4& x, const uint4& c, unsigned ok) {
+        float e[4] = {x.x, x.y, x.z, x.w};
+        const unsigned n[4] = {c.x, c.y, c.z, c.w};
+        if (n[0] | n[1] | n[2] | n[3]) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (v + k >= 0 && v + k < a.V) p[k] = e[k];
+                if (n[k]) {
+                    e[k] = e[k] > 0.f ? e[k] / rep : e[k] * rep;
+                    if (n[k] > 1u) e[k] = e[k] - freq * (float)(n[k] >> 1) - pres;
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!(ok >> k & 1u)) e[k] = -INFINITY;
+        x = make_float4(e[0], e[1], e[2], e[3]);
+    };
+    if (!in_place && a.vec && v0 >= 0 && v0 + SLICE <= a.V) {
+        // A slice inside its row, the common case: every address is the thread's first and a constant, and the thread's
+        // groups have their mask bits at the same place of words a constant apart.
+        const int first = group(0), sh = first & 31;
+        const float4* px = reinterpret_cast<const float4*>(a.x + row0 + first);
+        float4* py = reinterpret_cast<float4*>(a.y + row0 + first);
+        const uint32_t* pm = mask ? mask + (first >> 5) : nullptr;
+        const uint4* pc = reinterpret_cast<const uint4*>(cnt) + tid;
+#pragma unroll
+        for (int c = 0; c < PER; c += AHEAD) {
+            if (c)
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) x[i] = __ldcs(px + (c + i) * THREADS);
+            unsigned ok[AHEAD];
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                ok[i] = 15u;
+                if (mask) {
+                    const uint32_t* w = pm + (c + i) * (THREADS / 8);
+                    ok[i] = __funnelshift_r(w[0], sh > 28 ? w[1] : 0u, sh);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                change(x[i], hn ? pc[(c + i) * THREADS] : make_uint4(0, 0, 0, 0), ok[i]);
+                __stcs(py + (c + i) * THREADS, x[i]);
+            }
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < PER; ++i) {
+            const int v = group(i);
+            if (v >= a.V || v + 3 < 0) continue;
+            const uint4 c = hn ? reinterpret_cast<const uint4*>(cnt)[tid + i * THREADS] : make_uint4(0, 0, 0, 0);
+            const unsigned ok = mask ? allowed4(v) : 15u;
+            if (in_place && !(c.x | c.y | c.z | c.w) && ok == 15u) continue;
+            float4 z;
+            load(v, z);
+            change(z, c, ok);
+            float* p = a.y + row0 + v;
+            if (a.vec && v >= 0 && v + 3 < a.V) {
+                *reinterpret_cast<float4*>(p) = z;
+            } else {
+                if (v >= 0) p[0] = z.x;
+                if (v + 1 >= 0 && v + 1 < a.V) p[1] = z.y;
+                if (v + 2 >= 0 && v + 2 < a.V) p[2] = z.z;
+                if (v + 3 < a.V) p[3] = z.w;
+            }
         }
     }
 
@@ -156,9 +197,9 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
     if (!bn) return;
     __syncthreads();
     auto add = [&](int v, int entry) {
-        if (allowed4(v) & 1u) a.y[row0 + v] += a.bias_values[(int64_t)b0 + entry];
+        if (!mask || mask[v >> 5] >> (v & 31) & 1u) a.y[row0 + v] += a.bias_values[(int64_t)b0 + entry];
     };
-    if (bn <= kLogitThreads) {
+    if (bn <= THREADS) {
         if (id >= lo && id < hi) {
             bool last = true;
             for (int j = tid + 1; j < bn; ++j) last &= s_ids[j] != id;
@@ -166,28 +207,34 @@ __global__ void __launch_bounds__(kLogitThreads) logits_process_kernel(const Log
         }
         return;
     }
-    for (int i = tid; i < SLICE / 4; i += kLogitThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < SLICE / 4; i += THREADS) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < bn; i += kLogitThreads) {
+    for (int i = tid; i < bn; i += THREADS) {
         const int tok = a.bias_ids[(int64_t)b0 + i];
         if (tok >= lo && tok < hi) atomicMax(&cnt[tok - v0], (unsigned)i + 1u);
     }
     __syncthreads();
-    for (int u = tid; u < SLICE; u += kLogitThreads)
+    for (int u = tid; u < SLICE; u += THREADS)
         if (cnt[u]) add(v0 + u, (int)cnt[u] - 1);
 }
 
-template <int SLICE>
+template <int SLICE, int THREADS>
 static cudaError_t launch_slices(LogitArgs a, cudaStream_t s) {
     a.slices = (int)(((int64_t)a.V + 3 + SLICE - 1) / SLICE);
     const int64_t grid = (int64_t)a.T * a.slices;
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+    const size_t smem = (SLICE + 32 + THREADS) * sizeof(unsigned);
+    const void* fn = reinterpret_cast<const void*>(logits_process_kernel<SLICE, THREADS>);
+    if (smem > 48 * 1024) {
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     void* args[] = {&a};
-    return launch_pdl(reinterpret_cast<const void*>(logits_process_kernel<SLICE>), args, (int)grid, 0, s, kLogitThreads);
+    return launch_pdl(fn, args, (int)grid, smem, s, THREADS);
 }
 
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s) {
-    return launch_slices<8192>(a, s);
+    return launch_slices<8192, 256>(a, s);
 }
 
 }  // namespace tpk
