@@ -471,11 +471,13 @@ __device__ __forceinline__ uint32_t only_finite(uint32_t x) {
 // One warp: rows 0 .. valid - 1 of a V block without infinities and NaN, the
 // rows behind them zeros as far as a product of 16 keys reads. Whether the lane
 // found one. A step is four rows of 128 bytes; the swizzle moves 16-byte units
-// within a row only.
+// within a row only. The common block is only looked at: x * 0 summed up is NaN
+// if any x is not finite, one instruction for two values.
 template <int D>
 __device__ __forceinline__ int v_block_finite(unsigned char* block, int lane, int valid) {
-    int found = 0;
     const int rows = (valid + 15) & ~15;
+    uint32_t sum[4] = {0, 0, 0, 0};
+    auto look = [&](uint32_t& s, uint32_t x) { asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(s) : "r"(x), "r"(0u)); };
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
         uint4* base = reinterpret_cast<uint4*>(block + c * (kAtK * 128)) + lane;
@@ -484,19 +486,33 @@ __device__ __forceinline__ int v_block_finite(unsigned char* block, int lane, in
             uint4 x[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = base[(r0 / 4 + i) * 32];
+            if (r0 + 16 > valid) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r0 + 4 * i + (lane >> 3) >= valid) x[i] = base[(r0 / 4 + i) * 32] = make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int row = r0 + 4 * i + (lane >> 3);
-                if (row >= valid) {
-                    base[(r0 / 4 + i) * 32] = make_uint4(0, 0, 0, 0);
-                } else if (not_finite(x[i].x) | not_finite(x[i].y) | not_finite(x[i].z) | not_finite(x[i].w)) {
-                    base[(r0 / 4 + i) * 32] =
-                        make_uint4(only_finite(x[i].x), only_finite(x[i].y), only_finite(x[i].z), only_finite(x[i].w));
-                    found = 1;
-                }
+                look(sum[0], x[i].x);
+                look(sum[1], x[i].y);
+                look(sum[2], x[i].z);
+                look(sum[3], x[i].w);
             }
         }
     }
+    if (!__any_sync(0xffffffffu, not_finite(sum[0]) | not_finite(sum[1]) | not_finite(sum[2]) | not_finite(sum[3]))) return 0;
+    int found = 0;
+#pragma unroll 1
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll 1
+        for (int i = 0; i < rows / 4; ++i) {
+            uint4* q = reinterpret_cast<uint4*>(block + c * (kAtK * 128)) + lane + i * 32;
+            const uint4 x = *q;
+            if (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) {
+                *q = make_uint4(only_finite(x.x), only_finite(x.y), only_finite(x.z), only_finite(x.w));
+                found = 1;
+            }
+        }
     return found;
 }
 
