@@ -51,6 +51,14 @@ CASES = {
     "prefix_long_split": (L(8, 2, 128, 1), [1, 2], [10, 1000], 6000, {}),
     "prefix_rows_behind": (QWEN, [1, 2, 1], [3, 0, 50], 200, dict(extra_rows=40)),
     "prefix_empty_sequences_first": (QWEN, [0, 0, 1], [3, 0, 50], 100, {}),
+    "prefix_all_empty": (QWEN, [0, 0], [3, 0], 100, dict(extra_rows=9)),
+    # how items are cut and dealt out: one row over very many parts, a few items over one round of the SMs, sequences
+    # for more than one round of the planning CTA
+    "one_token_many_parts": (L(8, 1, 128, 1), [1], [20000], 0, {}),
+    "items_just_over_a_round": (LLAMA, [64] * 20, [0] * 20, 640, {}),
+    "few_items_of_many_blocks": (L(8, 2, 64, 1), [128, 90], [2500, 1800], 0, {}),
+    "many_sequences": (QWEN, [1] * 1100, [(37 * i) % 150 for i in range(1100)], 0, {}),
+    "many_sequences_prefix": (L(4, 1, 64, 1), [i % 3 for i in range(1300)], [(11 * i) % 40 for i in range(1300)], 70, {}),
 }
 
 
