@@ -34,7 +34,7 @@ constexpr int kAtBuckets = 512;         // item lengths told apart when sorting
 constexpr int kAtMinPart = 2;           // blocks of the shortest part of a narrow item worth its join
 constexpr int kAtMinCut = 4;            // ... and of a wide one, which has more rows to join
 constexpr int kAtMaxParts = 16;
-constexpr int kAtNarrow = 32;           // rows of an item at most that the narrow kernel takes
+constexpr int kAtNarrow = 32;           // rows of an item at most that the narrow kernel can take
 
 enum AttnKind : int { AT_PREFIX = 1, AT_OWN = 2 };   // key blocks of an item: the prefix's, the sequence's own
 
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
         }
     };
     auto blocks = [&](int n, int pos) { return in_item + own_blocks((int64_t)pos + n, p.max_kv); };
-    auto is_narrow = [&](int n) { return n * G <= kAtNarrow; };
+    auto is_narrow = [&](int n) { return n * G <= p.narrow; };
 
     // ---- check and sum up
     load(warp * lanes, c0, n, pos);
@@ -1767,7 +1767,7 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const bool d128 = p.d == 128;
     void* args[] = {&a};
-    a.after_wide = p.T * (int64_t)G > kAtNarrow;         // else no item can have more rows
+    a.after_wide = p.T * (int64_t)G > p.narrow;          // else no item can have more rows
     if (a.after_wide) {
         const void* fn = d128 ? reinterpret_cast<const void*>(attn_items_kernel<128>)
                               : reinterpret_cast<const void*>(attn_items_kernel<64>);

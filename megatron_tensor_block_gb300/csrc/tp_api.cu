@@ -1267,9 +1267,15 @@ static tp_status packed_args(const char* who, tp_plan_t plan, const tp_kv_set* p
     a.chunks = reinterpret_cast<AttnChunk*>(ws + plan->off_a_chunks);
     a.part_ml = reinterpret_cast<float2*>(ws + plan->off_a_ml);
     a.part_o = reinterpret_cast<float*>(ws + plan->off_a_o);
-    // A prefix that the batch shares is read once for tiles of tokens of any sequence where the sequences bring less
-    // than half a tile of rows each; longer ones fill their own tiles, which then take the prefix before their own keys.
-    a.shared = prefix_len > 0 && (int64_t)T * (a.hq_s / a.hkv_s) < (int64_t)B * 128;
+    const int64_t rows = (int64_t)T * (a.hq_s / a.hkv_s);
+    // A prefix that the batch shares is read once for tiles of tokens of any sequence where the sequences bring little more
+    // than a tile of 128 rows each or less; longer ones fill their own tiles, which then take the prefix before their own
+    // keys and need no joining. 32 sequences behind 4096 rows, rows per sequence: shared and not, 8: 36 and 70 us,
+    // 64: 59 and 102, 128: 95 and 105, 256: 177 and 111; 16 unlike ones of 206 behind 2048: 63 and 58.
+    a.shared = prefix_len > 0 && rows < (int64_t)B * 160;
+    // Items of up to 16 rows go to the kernel for few rows, of up to 32 where most of the batch is such: among longer prompts
+    // their tails are better off beside those (ragged prompts 59 and 52 us with 32 and 16).
+    a.narrow = rows <= (int64_t)B * 32 ? 32 : 16;
     return TP_OK;
 }
 

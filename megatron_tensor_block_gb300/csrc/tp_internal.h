@@ -352,6 +352,7 @@ struct RaggedAttnParams {
     const void* pv[TP_MAX_SHARDS];
     int prefix_len;
     int shared;                           // 1: the prefix is attended to by tiles of the batch's tokens
+    int narrow;                           // most rows of an item that the narrow kernel takes, 16 or 32
     int64_t prefix_rows;
     const int* cu;                        // [B + 1]
     const int* pos;                       // [B] row of each sequence's first new token
