@@ -184,12 +184,18 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     const int target_n = share(narrow_blocks, 4 * kSMs);
     int target_w = max(kAtMinCut, share(wide_blocks, kSMs));
     if (items && items <= kSMs) {
-        // The parts per item that are done first, in blocks' time: rounds of parts, each two blocks' longer than its blocks,
-        // and the joining, a block's time for about 4.8 MB of float32 results there and back.
-        // Lane k - 1 takes k parts.
-        const int all = (int)items, k = lane + 1, len = (longest + k - 1) / k;
-        const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.8e6f;
-        float t = (float)((k * all + kSMs - 1) / kSMs * (len + 2)) + (k > 1 ? k * join : 0.f);
+        // The parts per item that are done first, in microseconds, k of them in lane k - 1: rounds of parts, each two
+        // blocks' time longer than its blocks and the first seven more (half as long again beside narrow items, which keep
+        // the memory busy); what the SMs that are left do not read of the narrow items meanwhile; and the joining, 4.4 MB of
+        // float32 results a microsecond there and back. Both sides, 8 KV heads: 256 tokens behind 16384, k = 1/2/3/4/6:
+        // 252/209/225/238/248 us; 64 behind 4096, k = 1/2/3/4/6/8: 93/73/65/62/56/58 us; a chunk of 512 behind 30001,
+        // k = 1/2/3/4/6/8: 331/195/249/202/210/217 us.
+        const int all = (int)items, k = lane + 1, len = (longest + k - 1) / k, sms = min(k * all, kSMs);
+        const float bytes = (float)narrow_blocks * heads * (kAtK * 4) * p.d;
+        const float wide_us = (float)((k * all + kSMs - 1) / kSMs * (len + 2) + 7) * (narrow_blocks ? 1.6f : 1.1f);
+        const float left = fmaxf(0.f, bytes - wide_us * fminf(6.5e6f, (kSMs - sms) * 6e4f));
+        const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.4e6f;
+        float t = wide_us + left / 6.5e6f + (k > 1 ? k * join : 0.f);
         if (k > 1 && (k > kAtMaxParts || k * all > 3 * kSMs || len < kAtMinCut)) t = INFINITY;
         const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));           // positive: ordered as their bits
         const int parts = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best));
