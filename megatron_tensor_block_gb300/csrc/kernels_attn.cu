@@ -49,9 +49,9 @@ __device__ __forceinline__ void part_split(int nb, int target, int& parts, int& 
     parts = 1;
     len = nb;
     if (nb > target + target / 2) {
-        parts = (nb + target - 1) / target;
-        len = (nb + parts - 1) / parts;
-        parts = (nb + len - 1) / len;
+        parts = (unsigned)(nb + target - 1) / (unsigned)target;
+        len = (unsigned)(nb + parts - 1) / (unsigned)parts;
+        parts = (unsigned)(nb + len - 1) / (unsigned)len;
     }
 }
 
@@ -68,16 +68,40 @@ __device__ __forceinline__ void part_split(int nb, int target, int& parts, int& 
 //
 // Integer atomics place the items of a length and the rows of partial results:
 // their order decides where a partial lies, not what is added to what.
-__global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams p) {
-    __shared__ int s_hist[2 * kAtBuckets];                           // wide items, narrow items
-    __shared__ unsigned long long s_blocks[2][32];                   // per warp: blocks of wide and narrow tiles
-    __shared__ int s_tiles[32], s_longest[32], s_warp[32];           // wide tiles
+//
+// Bound by latency, 3 to 5 us of it: instructions that run once come from
+// memory, and what every warp computes for itself takes its turn. So the three
+// passes are one loop, their tiles come from one place, and the warps are eight
+// (32 warps and the passes written out: decode of 64 behind 4096 rows 59 us, of
+// 256 behind 16384 rows 220; now 53 and 207. 16 warps: 55 and 208).
+constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
+static_assert(2 * kAtBuckets == 4 * kPlanThreads, "four buckets per thread");
+
+__device__ __forceinline__ int warp_scan(int x, int lane) {          // inclusive
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += v;
+    }
+    return x;
+}
+// the lane whose range [before, before + its number) holds i, before ascending
+__device__ __forceinline__ int warp_owner(int before, int i) {
+    int at = 0;
+    for (int o = 16; o; o >>= 1)
+        if (__shfl_sync(0xffffffffu, before, at + o) <= i) at += o;
+    return at;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAttnParams p) {
+    __shared__ __align__(16) int s_hist[2 * kAtBuckets];             // wide items, narrow items
+    __shared__ unsigned long long s_blocks[2][kPlanWarps];           // per warp: blocks of wide and narrow tiles
+    __shared__ int s_tiles[kPlanWarps], s_longest[kPlanWarps], s_warp[kPlanWarps];       // wide tiles
     __shared__ int s_rows, s_chunks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr unsigned kAll = 0xffffffffu;
     pdl_trigger();
-    s_hist[tid] = 0;
-    const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G);            // tokens per item
+    reinterpret_cast<int4*>(s_hist)[tid] = make_int4(0, 0, 0, 0);
+    const int G = (unsigned)p.hq_s / (unsigned)p.hkv_s, per = 2 * ((unsigned)kAtM / (unsigned)G);      // tokens per item
     const int heads = p.N * p.hkv_s;
     if (tid == 0) {
         s_rows = 2 * p.T * heads * G;                                // behind the places of part 0
@@ -85,218 +109,240 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const RaggedAttnParams 
     }
     const int n_prefix = (p.prefix_len + kAtK - 1) / kAtK;           // prefix blocks
     const int in_item = p.shared ? 0 : n_prefix;
-    const int lanes = min(32, (p.B + 31) / 32);                      // sequences per warp and round
+    const int lanes = min(32, (p.B + kPlanWarps - 1) / kPlanWarps);  // sequences per warp and round
     pdl_wait();
 
     int bad = 0, out = 0;
-    int c0 = 0, n = 0, pos = 0;                                      // the lane's sequence of the first round
-    auto load = [&](int b0, int& c0, int& n, int& pos) {
+    const int n_tok = p.cu[p.B];
+    auto load = [&](int b0, int& c, int& n, int& pos) {
         const int b = b0 + lane;
-        c0 = n = pos = 0;
+        c = n = pos = 0;
         if (lane < lanes && b < p.B) {
-            c0 = p.cu[b];
+            c = p.cu[b];
             const int c1 = p.cu[b + 1];
             pos = p.pos[b];
-            if (c1 < c0 || c0 < 0 || c1 > p.T || (b == 0 && c0 != 0)) bad = 1;
-            else if (c1 > c0 && (pos < 0 || (int64_t)pos + (c1 - c0) > p.max_kv)) out = 1;
-            if (!bad) n = c1 - c0;
+            if (c1 < c || c < 0 || c1 > p.T || (b == 0 && c != 0)) bad = 1;
+            else if (c1 > c && (pos < 0 || (int64_t)pos + (c1 - c) > p.max_kv)) out = 1;
+            if (!bad) n = c1 - c;
         }
     };
-    // f(sequence, first token, tokens, position) for every tile, lanes apart
-    auto visit = [&](auto&& f) {
-        for (int b0 = warp * lanes; b0 < p.B; b0 += 32 * lanes) {
-            int c = c0, m = n, q = pos;
-            if (b0 != warp * lanes) load(b0, c, m, q);
-            if (m > 0 && m <= per) f(b0 + lane, c, m, q);
-            for (unsigned w = __ballot_sync(kAll, m > per); w; w &= w - 1) {
-                const int l = __ffs(w) - 1;
-                const int cl = __shfl_sync(kAll, c, l), nl = __shfl_sync(kAll, m, l), ql = __shfl_sync(kAll, q, l);
-                for (int64_t at = (int64_t)lane * per; at < nl; at += 32 * per)
-                    f(b0 + l, cl + (int)at, min(per, nl - (int)at), (int)((int64_t)ql + at));
-            }
-        }
-    };
-    auto blocks = [&](int n, int pos) { return in_item + own_blocks((int64_t)pos + n, p.max_kv); };
-    auto is_narrow = [&](int n) { return n * G <= p.narrow; };
+    int c0, n0, q0;                                                  // the lane's sequence of the first round
+    load(warp * lanes, c0, n0, q0);
 
-    // ---- check and sum up
-    load(warp * lanes, c0, n, pos);
     unsigned long long wide_blocks = 0, narrow_blocks = 0;
     int wide_tiles = 0, longest = 0;
-    auto sum_up = [&](int k, int nb) {
-        if (is_narrow(k)) {
-            narrow_blocks += nb;
-        } else {
-            wide_blocks += nb;
-            ++wide_tiles;
-            longest = max(longest, nb);
-        }
-    };
-    visit([&](int, int, int k, int q) { sum_up(k, blocks(k, q)); });
-    for (int o = 16; o; o >>= 1) {
-        wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
-        narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
-        wide_tiles += __shfl_xor_sync(kAll, wide_tiles, o);
-        longest = max(longest, __shfl_xor_sync(kAll, longest, o));
-    }
-    if (lane == 0) {
-        s_tiles[warp] = wide_tiles;
-        s_longest[warp] = longest;
-        s_blocks[0][warp] = wide_blocks;
-        s_blocks[1][warp] = narrow_blocks;
-    }
-    bad = __syncthreads_or(bad);
-    if (bad) {
-        if (tid < (int)(sizeof(AttnCtl) / sizeof(int))) reinterpret_cast<int*>(p.ctl)[tid] = 0;
-        if (tid == 0) set_status(p.status, TP_ERR_SHAPE);
-        return;
-    }
-    if (out) set_status(p.status, TP_ERR_CAPACITY);
-    const int n_tok = p.cu[p.B];
-    wide_blocks = s_blocks[0][lane];
-    narrow_blocks = s_blocks[1][lane];
-    wide_tiles = s_tiles[lane];
-    longest = s_longest[lane];
-    for (int o = 16; o; o >>= 1) {
-        wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
-        narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
-        wide_tiles += __shfl_xor_sync(kAll, wide_tiles, o);
-        longest = max(longest, __shfl_xor_sync(kAll, longest, o));
-    }
-    const int prefix_tiles = p.shared ? (n_tok + per - 1) / per : 0;
-    auto prefix_n = [&](int i) { return min(per, n_tok - i * per); };
-    if (prefix_tiles) {
-        const int small = is_narrow(prefix_n(prefix_tiles - 1));
-        wide_tiles += prefix_tiles - small;
-        wide_blocks += (unsigned long long)(prefix_tiles - small) * n_prefix;
-        if (small) narrow_blocks += n_prefix;
-        if (prefix_tiles > small) longest = max(longest, n_prefix);
-    }
+    int target_w = 0, target_n = 0;                                  // the longest parts
+    int last_from = INT_MAX, last_parts = 1;                         // a last round's items and their parts
+    int n_wide = 0, n_items = 0;
+    const int own = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
 
-    // ---- the longest parts
-    const long long items = (long long)wide_tiles * heads;
-    auto share = [&](unsigned long long sum, unsigned parts) {      // of the blocks of all KV heads
-        const unsigned long long all = sum * heads;
-        const unsigned long long q = all < (1ull << 32) ? (unsigned)all / parts + 1 : all / parts + 1;
-        return (int)min((unsigned long long)INT_MAX / 4, max((unsigned long long)kAtMinPart, q));
-    };
-    // narrow: two parts per half of a CTA (time goes by the bytes: parts cost little)
-    const int target_n = share(narrow_blocks, 4 * kSMs);
-    int target_w = max(kAtMinCut, share(wide_blocks, kSMs));
-    if (items && items <= kSMs) {
-        // The parts per item that are done first, in microseconds, k of them in lane k - 1: rounds of parts, each two
-        // blocks' time longer than its blocks and the first seven more (half as long again beside narrow items, which keep
-        // the memory busy); what the SMs that are left do not read of the narrow items meanwhile; and the joining, 4.4 MB of
-        // float32 results a microsecond there and back. Both sides, 8 KV heads: 256 tokens behind 16384, k = 1/2/3/4/6:
-        // 252/209/225/238/248 us; 64 behind 4096, k = 1/2/3/4/6/8: 93/73/65/62/56/58 us; a chunk of 512 behind 30001,
-        // k = 1/2/3/4/6/8: 331/195/249/202/210/217 us.
-        const int all = (int)items, k = lane + 1, len = (longest + k - 1) / k, sms = min(k * all, kSMs);
-        const float bytes = (float)narrow_blocks * heads * (kAtK * 4) * p.d;
-        const float wide_us = (float)((k * all + kSMs - 1) / kSMs * (len + 2) + 7) * (narrow_blocks ? 1.6f : 1.1f);
-        const float left = fmaxf(0.f, bytes - wide_us * fminf(6.5e6f, (kSMs - sms) * 6e4f));
-        const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.4e6f;
-        float t = wide_us + left / 6.5e6f + (k > 1 ? k * join : 0.f);
-        if (k > 1 && (k > kAtMaxParts || k * all > 3 * kSMs || len < kAtMinCut)) t = INFINITY;
-        const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));           // positive: ordered as their bits
-        const int parts = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best));
-        target_w = (longest + parts - 1) / parts;
-    }
-    // a last round of few items, if nothing else is cut: parts for its items
-    const int rounds = items <= 3 * kSMs ? (int)items / kSMs : 0;
-    int last_from = INT_MAX, last_parts = 1;
-    if (rounds && longest <= target_w + target_w / 2) {
-        last_from = (rounds * kSMs + heads - 1) / heads;
-        const int rest = wide_tiles - last_from;
-        last_parts = rest > 0 ? min(kAtMaxParts, kSMs / (rest * heads)) : 1;
-        if (last_parts < 2) last_from = INT_MAX, last_parts = 1;
-    }
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        // The warp's tiles, 32 at a time: those of a round of its sequences back to back, then its share of a shared prefix's.
+        int next = warp * lanes, c = c0, n = n0, q = q0;             // the lane's sequence of the round
+        int b0 = 0, before = 0, total = 0, i0 = 0, step = 32;
+        bool shared = pass && p.shared;
+        int kind = own;
+#pragma unroll 1
+        while (true) {
+            if (i0 >= total) {
+                if (next < p.B) {
+                    if (next != warp * lanes) load(next, c, n, q);
+                    const int tiles = (unsigned)(n + per - 1) / (unsigned)per;
+                    before = warp_scan(tiles, lane);
+                    total = __shfl_sync(kAll, before, 31);
+                    before -= tiles;
+                    b0 = next;
+                    i0 = 0;
+                    next += kPlanWarps * lanes;
+                } else if (shared) {                                 // as one sequence of all tokens
+                    shared = false;
+                    kind = AT_PREFIX;
+                    c = q = b0 = 0;
+                    n = n_tok;
+                    before = lane ? INT_MAX : 0;
+                    total = (unsigned)(n_tok + per - 1) / (unsigned)per;
+                    i0 = 32 * warp;
+                    step = 32 * kPlanWarps;
+                } else {
+                    break;
+                }
+                continue;
+            }
+            const int tile = i0 + lane, owner = warp_owner(before, tile);
+            const int at = (tile - __shfl_sync(kAll, before, owner)) * per;
+            const int b = b0 + owner, t0 = __shfl_sync(kAll, c, owner) + at;
+            const int qpos = (int)((int64_t)__shfl_sync(kAll, q, owner) + at);
+            const int left = __shfl_sync(kAll, n, owner) - at, k = tile < total ? min(per, left) : 0;     // tokens
+            i0 += step;
+            const bool live = k > 0, nar = k * G <= p.narrow;
+            const int nb = kind == AT_PREFIX ? n_prefix : in_item + own_blocks((int64_t)qpos + k, p.max_kv);
+            if (pass == 0) {
+                if (live && nar) narrow_blocks += nb;
+                if (live && !nar) {
+                    wide_blocks += nb;
+                    ++wide_tiles;
+                    longest = max(longest, nb);
+                }
+                continue;
+            }
+            int parts, len;
+            part_split(nb, nar ? target_n : target_w, parts, len);
+            int* rest = &s_hist[(nar ? 2 : 1) * kAtBuckets - 1 - min(nb - (parts - 1) * len, kAtBuckets - 1)];
+            int* full = &s_hist[(nar ? 2 : 1) * kAtBuckets - 1 - min(len, kAtBuckets - 1)];
+            int e0 = 0, e1 = 0;                                      // places of the parts but the last, and of the last
+            if (live) {
+                if (parts > 1) e0 = atomicAdd(full, parts - 1);
+                e1 = atomicAdd(rest, 1);
+            }
+            if (pass == 1) continue;
 
-    // ---- count
-    auto bucket = [&](int nb, bool nar) { return (nar ? 2 : 1) * kAtBuckets - 1 - min(nb, kAtBuckets - 1); };
-    auto count = [&](int nb, bool nar) {
-        int parts, len;
-        part_split(nb, nar ? target_n : target_w, parts, len);
-        if (parts > 1) atomicAdd(&s_hist[bucket(len, nar)], parts - 1);
-        atomicAdd(&s_hist[bucket(nb - (parts - 1) * len, nar)], 1);
-    };
-    visit([&](int, int, int k, int q) { count(blocks(k, q), is_narrow(k)); });
-    for (int i = tid; i < prefix_tiles; i += 1024) count(n_prefix, is_narrow(prefix_n(i)));
-    __syncthreads();
-    // exclusive scan of the buckets, one per thread
-    const int mine = s_hist[tid];
-    int incl = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int of_warp = s_warp[lane];
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kAll, of_warp, o);
-        if (lane >= o) of_warp += v;
-    }
-    const int sorted = __shfl_sync(kAll, of_warp, kAtBuckets / 32 - 1);
-    const int more = last_parts > 1 ? (sorted - last_from) * (last_parts - 1) : 0;      // places of the last round's parts
-    s_hist[tid] = (warp ? __shfl_sync(kAll, of_warp, warp - 1) : 0) + incl - mine + (tid >= kAtBuckets ? more : 0);
-    const int total = __shfl_sync(kAll, of_warp, 31) + more;
-    __syncthreads();
-
-    // ---- place
-    auto place = [&](int kind, int b, int t0, int k, int q, int nb, int i) {
-        const bool nar = is_narrow(k);
-        int parts, len, from = -1;
-        part_split(nb, nar ? target_n : target_w, parts, len);
-        if (parts == 1) {
-            from = atomicAdd(&s_hist[bucket(nb, nar)], 1);
-            if (!nar && from >= last_from) {
-                from = last_from + (from - last_from) * last_parts;
+            int entries = live ? parts : 0;
+            if (live && parts == 1 && !nar && e1 >= last_from) {
+                e0 = last_from + (e1 - last_from) * last_parts;
                 parts = max(1, min(last_parts, nb / kAtMinPart));
                 len = (nb + parts - 1) / parts;
                 parts = max(1, (nb + len - 1) / max(len, 1));
-                for (int j = parts; j < last_parts; ++j) p.items[from + j] = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};   // no rows
+                e1 = e0 + parts - 1;
+                entries = last_parts;                                // those behind the parts: no rows
             }
-        }
-        // partial results: part 0 of a tile at the place of its tokens, the others where there is room
-        const int rows = heads * k * G;
-        int row0 = -1, row1 = 0;
-        if (parts > 1 || p.shared) {
-            row0 = heads * G * ((kind & AT_OWN ? 0 : p.T) + t0);
-            if (parts > 1) row1 = atomicAdd(&s_rows, (parts - 1) * rows);
-            if (kind & AT_OWN) {
-                // the lanes' chunks, added up in one atomic: ranks by the bits of their counts
-                const int chunks = (k * G + 7) / 8;
-                const unsigned with = __activemask(), below = with & ((1u << lane) - 1);
-                int before = 0, sum = 0;
-#pragma unroll
-                for (int b = 0; b < 6; ++b) {
-                    const unsigned v = __ballot_sync(with, chunks >> b & 1);
-                    before += __popc(v & below) << b;
-                    sum += __popc(v) << b;
+            // partial results: part 0 of a tile at the place of its tokens, the others where there is room
+            const int rows = heads * k * G;
+            int row0 = -1, row1 = 0, chunks = 0;
+            if (live && (parts > 1 || p.shared)) {
+                row0 = heads * G * ((kind & AT_OWN ? 0 : p.T) + t0);
+                if (parts > 1) row1 = atomicAdd(&s_rows, (parts - 1) * rows);
+                if (kind & AT_OWN) chunks = (k * G + 7) / 8;
+                else p.prefix_groups[(unsigned)t0 / (unsigned)per] = make_int2(row1, parts);
+            }
+            // the lanes' chunks and items, written by the warp together
+            int first = warp_scan(chunks, lane);
+            int sum = __shfl_sync(kAll, first, 31);
+            if (sum) {
+                first -= chunks;
+                int to = 0;
+                if (lane == 0) to = atomicAdd(&s_chunks, sum);
+                to = __shfl_sync(kAll, to, 0);
+#pragma unroll 1
+                for (int i = lane; i < ((sum + 31) & ~31); i += 32) {
+                    const int l = warp_owner(first, i), j = i - __shfl_sync(kAll, first, l);
+                    const AttnChunk x = {__shfl_sync(kAll, t0, l),   __shfl_sync(kAll, k, l),     __shfl_sync(kAll, qpos, l),
+                                         __shfl_sync(kAll, row1, l), __shfl_sync(kAll, parts, l), j, 0, 0};
+                    if (i < sum) p.chunks[to + i] = x;
                 }
-                int c = 0;
-                if (!below) c = atomicAdd(&s_chunks, sum);
-                c = __shfl_sync(with, c, __ffs(with) - 1) + before;
-                for (int j = 0; j < chunks; ++j) p.chunks[c + j] = AttnChunk{t0, k, q, row1, parts, j, 0, 0};
-            } else {
-                p.prefix_groups[i] = make_int2(row1, parts);
+            }
+            first = warp_scan(entries, lane);
+            sum = __shfl_sync(kAll, first, 31);
+            first -= entries;
+#pragma unroll 1
+            for (int i = lane; i < ((sum + 31) & ~31); i += 32) {
+                const int l = warp_owner(first, i), j = i - __shfl_sync(kAll, first, l);
+                const int np = __shfl_sync(kAll, parts, l), nl = __shfl_sync(kAll, len, l), r0 = __shfl_sync(kAll, row0, l);
+                const int r1 = __shfl_sync(kAll, row1, l) + (j - 1) * __shfl_sync(kAll, rows, l);
+                const int f0 = __shfl_sync(kAll, e0, l), f1 = __shfl_sync(kAll, e1, l), all = __shfl_sync(kAll, nb, l);
+                AttnItem x = {__shfl_sync(kAll, t0, l), __shfl_sync(kAll, k, l),
+                              __shfl_sync(kAll, b, l),  __shfl_sync(kAll, qpos, l),
+                              j * nl, min(all, (j + 1) * nl), kind, j && r0 >= 0 ? r1 : r0};
+                if (j >= np) x = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};
+                if (i < sum) p.items[j == np - 1 ? f1 : f0 + j] = x;
             }
         }
-        for (int j = 0; j < parts; ++j) {
-            const int k0 = j * len, k1 = min(nb, k0 + len);
-            const int e = from >= 0 ? from + j : atomicAdd(&s_hist[bucket(k1 - k0, nar)], 1);
-            p.items[e] = AttnItem{t0, k, b, q, k0, k1, kind, j && row0 >= 0 ? row1 + (j - 1) * rows : row0};
+
+        if (pass == 0) {
+            // ---- the sums over the warps; the longest parts
+            for (int o = 16; o; o >>= 1) {
+                wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
+                narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
+            }
+            wide_tiles = __reduce_add_sync(kAll, wide_tiles);
+            longest = __reduce_max_sync(kAll, longest);
+            if (lane == 0) {
+                s_tiles[warp] = wide_tiles;
+                s_longest[warp] = longest;
+                s_blocks[0][warp] = wide_blocks;
+                s_blocks[1][warp] = narrow_blocks;
+            }
+            if (__syncthreads_or(bad)) {
+                if (tid < (int)(sizeof(AttnCtl) / sizeof(int))) reinterpret_cast<int*>(p.ctl)[tid] = 0;
+                if (tid == 0) set_status(p.status, TP_ERR_SHAPE);
+                return;
+            }
+            if (out) set_status(p.status, TP_ERR_CAPACITY);
+            constexpr int kMask = kPlanWarps - 1;
+            wide_blocks = s_blocks[0][lane & kMask];
+            narrow_blocks = s_blocks[1][lane & kMask];
+            for (int o = kPlanWarps / 2; o; o >>= 1) {
+                wide_blocks += __shfl_xor_sync(kAll, wide_blocks, o);
+                narrow_blocks += __shfl_xor_sync(kAll, narrow_blocks, o);
+            }
+            wide_tiles = __reduce_add_sync(kAll, lane < kPlanWarps ? s_tiles[lane & kMask] : 0);
+            longest = __reduce_max_sync(kAll, s_longest[lane & kMask]);
+            if (p.shared) {
+                const int tiles = (unsigned)(n_tok + per - 1) / (unsigned)per;
+                const int small = tiles && (n_tok - (tiles - 1) * per) * G <= p.narrow;
+                wide_tiles += tiles - small;
+                wide_blocks += (unsigned long long)(tiles - small) * n_prefix;
+                if (small) narrow_blocks += n_prefix;
+                if (tiles > small) longest = max(longest, n_prefix);
+            }
+            const long long items = (long long)wide_tiles * heads;
+            // an even share of the blocks of all KV heads, rounded up (2^-22 for the product's and quotient's roundings)
+            auto share = [&](unsigned long long sum, float parts) {
+                return max(kAtMinPart, (int)fminf((float)sum * (float)heads * (1.f / parts) * (1.f + 0x1p-21f) + 1.f, 0x1p29f));
+            };
+            // narrow: two parts per half of a CTA (time goes by the bytes: parts cost little)
+            target_n = share(narrow_blocks, 4.f * kSMs);
+            target_w = max(kAtMinCut, share(wide_blocks, kSMs));
+            if (items && items <= kSMs) {
+                // The parts per item that are done first, in microseconds, k of them in lane k - 1: rounds of parts, each two
+                // blocks' time longer than its blocks and the first seven more (half as long again beside narrow items,
+                // which keep the memory busy); what the SMs that are left do not read of the narrow items meanwhile; and
+                // the joining, 4.4 MB of float32 results a microsecond there and back. Both sides, 8 KV heads: 256 tokens
+                // behind 16384, k = 1/2/3/4/6: 252/209/225/238/248 us; 64 behind 4096, k = 1/2/3/4/6/8: 93/73/65/62/56/58
+                // us; a chunk of 512 behind 30001, k = 1/2/3/4/6/8: 331/195/249/202/210/217 us.
+                const int all = (int)items, k = lane + 1, len = (unsigned)(longest + k - 1) / (unsigned)k;
+                const int sms = min(k * all, kSMs);
+                const float bytes = (float)narrow_blocks * heads * (kAtK * 4) * p.d;
+                const float wide_us = (float)((k * all + kSMs - 1) / kSMs * (len + 2) + 7) * (narrow_blocks ? 1.6f : 1.1f);
+                const float left = fmaxf(0.f, bytes - wide_us * fminf(6.5e6f, (kSMs - sms) * 6e4f));
+                const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.4e6f;
+                float t = wide_us + left / 6.5e6f + (k > 1 ? k * join : 0.f);
+                if (k > 1 && (k > kAtMaxParts || k * all > 3 * kSMs || len < kAtMinCut)) t = INFINITY;
+                const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));           // positive: ordered as their bits
+                const int parts = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best));
+                target_w = (unsigned)(longest + parts - 1) / (unsigned)parts;
+            }
+            // a last round of few items, if nothing else is cut: parts for its items
+            const int rounds = items <= 3 * kSMs ? (int)items / kSMs : 0;
+            if (rounds && longest <= target_w + target_w / 2) {
+                last_from = (unsigned)(rounds * kSMs + heads - 1) / (unsigned)heads;
+                const int rest = wide_tiles - last_from;
+                last_parts = rest > 0 ? min(kAtMaxParts, (int)((unsigned)kSMs / (unsigned)(rest * heads))) : 1;
+                if (last_parts < 2) last_from = INT_MAX, last_parts = 1;
+            }
+        } else if (pass == 1) {
+            // ---- where the items of each length begin: exclusive sums over the buckets, four per thread
+            __syncthreads();
+            const int4 x = reinterpret_cast<const int4*>(s_hist)[tid];
+            const int mine = x.x + x.y + x.z + x.w, incl = warp_scan(mine, lane);
+            if (lane == 31) s_warp[warp] = incl;
+            __syncthreads();
+            const int of_warp = s_warp[lane & (kPlanWarps - 1)];
+            const int sorted = __reduce_add_sync(kAll, lane < kPlanWarps / 2 ? of_warp : 0);           // wide items
+            const int more = last_parts > 1 ? (sorted - last_from) * (last_parts - 1) : 0;      // the last round's parts
+            n_wide = sorted + more;
+            n_items = __reduce_add_sync(kAll, lane < kPlanWarps ? of_warp : 0) + more;
+            int e = __reduce_add_sync(kAll, lane < warp ? of_warp : 0) + incl - mine + (warp >= kPlanWarps / 2 ? more : 0);
+            reinterpret_cast<int4*>(s_hist)[tid] = make_int4(e, e + x.x, e + x.x + x.y, e + x.x + x.y + x.z);
+            __syncthreads();
         }
-    };
-    const int kind = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
-    visit([&](int b, int t0, int k, int q) { place(kind, b, t0, k, q, blocks(k, q), 0); });
-    for (int i = tid; i < prefix_tiles; i += 1024) place(AT_PREFIX, 0, i * per, prefix_n(i), 0, n_prefix, i);
+    }
     __syncthreads();
     if (tid == 0) {
         AttnCtl c = {};
         c.n_tokens = n_tok;
-        c.n_wide = sorted + more;
-        c.n_items = total;
+        c.n_wide = n_wide;
+        c.n_items = n_items;
         c.n_chunks = s_chunks;
         *p.ctl = c;
     }
@@ -1735,7 +1781,7 @@ AttnSizes attn_sizes(int64_t B, int64_t T, int hq, int hkv, int d) {
 cudaError_t launch_attn_plan(const RaggedAttnParams& p, cudaStream_t s) {
     RaggedAttnParams a = p;
     void* args[] = {&a};
-    return launch_pdl(reinterpret_cast<const void*>(attn_plan_kernel), args, 1, 0, s, 1024);
+    return launch_pdl(reinterpret_cast<const void*>(attn_plan_kernel), args, 1, 0, s, kPlanThreads);
 }
 
 cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {

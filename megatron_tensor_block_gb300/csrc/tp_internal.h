@@ -333,14 +333,14 @@ struct AttnCtl {
     int next, next_wide;                  // narrow items taken, wide ones
     int reserved[2];
 };
-struct AttnItem {                         // for every KV head of every shard:
+struct alignas(16) AttnItem {                         // for every KV head of every shard:
     int t0, ntok;                         // token rows
     int b, qpos;                          // sequence, cache row of the first of them
     int blk0, blk1;                       // part of its list of key blocks
     int kind;                             // which blocks the list has
     int row;                              // first row of its partial results, or -1: final
 };
-struct AttnChunk {                        // eight rows of a tile whose results are joined from parts
+struct alignas(16) AttnChunk {                        // eight rows of a tile whose results are joined from parts
     int t0, ntok, qpos, row, parts, chunk, reserved[2];   // row: first of part 1's
 };
 struct RaggedAttnParams {
