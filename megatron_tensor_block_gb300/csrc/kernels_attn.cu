@@ -6,7 +6,8 @@
 // in one pass over the keys with a running m and sum, in up to four launches:
 //   attn_plan_kernel     one CTA turns the offsets and lengths into a list of
 //                        items, longest first, and cuts long items into parts
-//                        where the batch has too few of them for the machine;
+//                        where the batch has too few of them for the machine
+//                        (a call of very few rows does without it);
 //   attn_items_kernel    persistent, one CTA per SM: items of many query rows;
 //   attn_narrow_kernel   the same for items of few query rows;
 //   attn_combine_kernel  joins the parts of a row.
@@ -76,6 +77,14 @@ __device__ __forceinline__ void part_split(int nb, int target, int& parts, int& 
 // 256 behind 16384 rows 220; now 53 and 207. 16 warps: 55 and 208).
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
 static_assert(2 * kAtBuckets == 4 * kPlanThreads, "four buckets per thread");
+
+// an even share of the blocks of all KV heads, rounded up (2^-21 for the roundings of the product and the quotient)
+__device__ __forceinline__ int even_share(unsigned long long blocks, int heads, float parts) {
+    const float q = (float)blocks * (float)heads * (1.f / parts) * (1.f + 0x1p-21f) + 1.f;
+    return max(kAtMinPart, (int)fminf(q, 0x1p29f));
+}
+// narrow items: two parts per half of a CTA (time goes by the bytes: parts cost little)
+__device__ __forceinline__ int narrow_share(unsigned long long blocks, int heads) { return even_share(blocks, heads, 4.f * kSMs); }
 
 __device__ __forceinline__ int warp_scan(int x, int lane) {          // inclusive
     for (int o = 1; o < 32; o <<= 1) {
@@ -286,13 +295,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
                 if (tiles > small) longest = max(longest, n_prefix);
             }
             const long long items = (long long)wide_tiles * heads;
-            // an even share of the blocks of all KV heads, rounded up (2^-22 for the product's and quotient's roundings)
-            auto share = [&](unsigned long long sum, float parts) {
-                return max(kAtMinPart, (int)fminf((float)sum * (float)heads * (1.f / parts) * (1.f + 0x1p-21f) + 1.f, 0x1p29f));
-            };
-            // narrow: two parts per half of a CTA (time goes by the bytes: parts cost little)
-            target_n = share(narrow_blocks, 4.f * kSMs);
-            target_w = max(kAtMinCut, share(wide_blocks, kSMs));
+            target_n = narrow_share(narrow_blocks, heads);
+            target_w = max(kAtMinCut, even_share(wide_blocks, heads, kSMs));
             if (items && items <= kSMs) {
                 // The parts per item that are done first, in microseconds, k of them in lane k - 1: rounds of parts, each two
                 // blocks' time longer than its blocks and the first seven more (half as long again beside narrow items,
@@ -403,6 +407,12 @@ struct AtArgs {
     const AttnItem* items;
     AttnCtl* ctl;
     int after_wide;                       // narrow kernel: the wide one is launched before it
+    int few;                              // narrow kernel: no plan kernel ran
+    int B;                                // (few) as below to prefix_groups
+    const int* cu;
+    const int* pos;
+    AttnChunk* chunks;
+    int2* prefix_groups;
     int N, T, hq_s, hkv_s, G, tpt, max_kv, prefix_len;
     float scale_log2;
     int* status;
@@ -472,8 +482,7 @@ struct __align__(16) AtWork {
 };
 static_assert(sizeof(AtWork) == 64, "four 16-byte words of the queue");
 
-__device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork& w) {
-    const int4 x = __ldcg(reinterpret_cast<const int4*>(a.items + e)), y = __ldcg(reinterpret_cast<const int4*>(a.items + e) + 1);
+__device__ __forceinline__ void at_fill(const AtArgs& a, const int4& x, const int4& y, int h, AtWork& w) {
     w.h = h;
     w.r = h / a.hkv_s;
     w.kvh = h - w.r * a.hkv_s;
@@ -493,6 +502,15 @@ __device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork&
     w.nb1 = w.nt > 1 ? max(0, min(blk1, e1) - w.blk0) : 0;
     w.nb = max(w.nb0, w.nb1);
     w.end = w.reserved = 0;
+}
+__device__ __forceinline__ void at_load(const AtArgs& a, int e, int4& x, int4& y) {
+    x = __ldcg(reinterpret_cast<const int4*>(a.items + e));
+    y = __ldcg(reinterpret_cast<const int4*>(a.items + e) + 1);
+}
+__device__ __forceinline__ void at_decode(const AtArgs& a, int e, int h, AtWork& w) {
+    int4 x, y;
+    at_load(a, e, x, y);
+    at_fill(a, x, y, h, w);
 }
 
 // A value that is the same in every lane, in a form that lets the compiler know.
@@ -1212,7 +1230,7 @@ struct AnShape {
     static constexpr int PAD = D == 64 ? KB - QB - PB : 0;
     static constexpr int SMEM = RING * KB + QB + PB + PAD + HEAD;
 };
-static_assert(2 * AnShape<128>::SMEM <= 227 * 1024 && 2 * AnShape<64>::SMEM <= 227 * 1024, "two halves");
+static_assert(2 * AnShape<128>::SMEM + 1024 <= 227 * 1024 && 2 * AnShape<64>::SMEM + 1024 <= 227 * 1024, "two halves");
 static_assert(AnShape<128>::SMEM % 1024 == 0 && AnShape<64>::SMEM % 1024 == 0, "alignment of the second");
 
 __device__ __forceinline__ float redux_max(float v) {
@@ -1408,6 +1426,83 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
     return true;
 }
 
+// The plan of a call of so few rows that all items are narrow and its fewer than
+// 32 sequences have one tile each: a lane per sequence, the lane behind them for
+// the tile of a shared prefix. Every CTA makes it for itself, without the
+// plan kernel and the way from it to here: 4 tokens behind 777 shared rows take
+// 13 us from the first kernel's start to the last one's end, and took 22. The
+// items are dealt out in turn.
+struct AnFew {
+    int before[32];                       // items in front of the lane's
+    int t0[32], ntok[32], qpos[32], nb[32], len[32], row1[32];
+    int total, reserved[31];
+};
+static_assert(sizeof(AnFew) == 1024, "behind the two halves");
+
+// One warp. record: this CTA's also writes what the joining kernel reads, and the status.
+__device__ __noinline__ void an_few_plan(const AtArgs& a, AnFew* f, int lane, bool record) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int heads = a.N * a.hkv_s;
+    int c = 0, c1 = 0, n = 0, q = 0;
+    bool bad = false, out = false;
+    if (lane < a.B) {
+        c = a.cu[lane];
+        c1 = a.cu[lane + 1];
+        q = a.pos[lane];
+        bad = c1 < c || c < 0 || c1 > a.T || (lane == 0 && c != 0);
+        n = c1 - c;
+        out = n > 0 && (q < 0 || (int64_t)q + n > a.max_kv);
+    }
+    bad = __any_sync(kAll, bad);
+    out = __any_sync(kAll, out);
+    const int n_tok = __shfl_sync(kAll, c1, a.B - 1);
+    const bool prefix = lane == a.B && a.prefix_len;
+    if (prefix) n = n_tok;
+    if (bad) n = 0;
+    const int nb = !n ? 0 : prefix ? (a.prefix_len + kAtK - 1) / kAtK : own_blocks((int64_t)q + n, a.max_kv);
+    int parts, len;
+    part_split(nb, narrow_share((unsigned)__reduce_add_sync(kAll, nb), heads), parts, len);
+    if (!n) parts = 0;
+    const int items = warp_scan(parts, lane), more = max(parts - 1, 0) * heads * n * a.G;
+    const int row1 = 2 * a.T * heads * a.G + warp_scan(more, lane) - more;
+    f->before[lane] = items - parts;
+    f->t0[lane] = c;
+    f->ntok[lane] = n;
+    f->qpos[lane] = q;
+    f->nb[lane] = nb;
+    f->len[lane] = len;
+    f->row1[lane] = row1;
+    if (lane == 31) f->total = items;
+    if (!record) return;
+    const int chunks = n && !prefix && (parts > 1 || a.prefix_len) ? (n * a.G + 7) / 8 : 0;
+    const int upto = warp_scan(chunks, lane), sum = __shfl_sync(kAll, upto, 31);
+    for (int j = 0; j < chunks; ++j) a.chunks[upto - chunks + j] = AttnChunk{c, n, q, row1, parts, j, 0, 0};
+    if (prefix) a.prefix_groups[0] = make_int2(row1, parts);
+    if (lane == 0) {
+        AttnCtl x = {};
+        x.n_tokens = bad ? 0 : n_tok;
+        x.n_chunks = sum;
+        *a.ctl = x;
+        if (bad) set_status(a.status, TP_ERR_SHAPE);
+        else if (out) set_status(a.status, TP_ERR_CAPACITY);
+    }
+}
+
+// item e of the few
+__device__ __forceinline__ void an_few_item(const AtArgs& a, const AnFew* f, int e, int4& x, int4& y) {
+    int l = 0;
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1)
+        if (f->before[l + o] <= e) l += o;
+    const int j = e - f->before[l], end = l < 31 ? f->before[l + 1] : f->total, parts = end - f->before[l], len = f->len[l];
+    const bool prefix = l == a.B;
+    const int rows = a.N * a.hkv_s * a.G;
+    int row = -1;
+    if (parts > 1 || a.prefix_len) row = j ? f->row1[l] + (j - 1) * rows * f->ntok[l] : rows * ((prefix ? a.T : 0) + f->t0[l]);
+    x = make_int4(f->t0[l], f->ntok[l], l, f->qpos[l]);
+    y = make_int4(j * len, min(f->nb[l], (j + 1) * len), prefix ? AT_PREFIX : AT_OWN, row);
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid_constant__ AtArgs a) {
     using Sh = AnShape<D>;
@@ -1474,8 +1569,24 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
     if (!a.after_wide) pdl_wait();
     pdl_trigger();
     const int heads = a.N * a.hkv_s;
-    const int n_wide = __ldcg(&a.ctl->n_wide);
-    const int total = *abort_flag ? 0 : (__ldcg(&a.ctl->n_items) - n_wide) * heads;
+    AnFew* few = reinterpret_cast<AnFew*>(smem + 2 * Sh::SMEM);
+    int n_wide = 0, total;
+    if (a.few) {
+        if (threadIdx.x < 32) an_few_plan(a, few, lane, blockIdx.x == gridDim.x - 1);
+        __syncthreads();
+        total = few->total * heads;
+    } else {
+        n_wide = __ldcg(&a.ctl->n_wide);
+        total = (__ldcg(&a.ctl->n_items) - n_wide) * heads;
+    }
+    if (*abort_flag) total = 0;
+    auto decode = [&](int idx, AtWork& w) {
+        const int e = idx / heads;
+        int4 x, y;
+        if (a.few) an_few_item(a, few, e, x, y);
+        else at_load(a, n_wide + e, x, y);
+        at_fill(a, x, y, idx - e * heads, w);
+    };
 
     // the i-th item of this CTA, -1 when there are no more
     auto item = [&](int i, AtWork& w, bool& more) {
@@ -1486,7 +1597,7 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[s]);
         more = idx >= 0;
-        if (more) at_decode(a, n_wide + idx / heads, idx % heads, w);
+        if (more) decode(idx, w);
         return true;
     };
 
@@ -1497,14 +1608,20 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
             const uint32_t q_bytes = (uint32_t)(kAtNarrow / a.G * a.G * 128 * Sh::NKB);
             bool ok = !*abort_flag;
             // As the wide kernel's, the first one too: behind that kernel the CTAs start as its CTAs end.
-            auto take = [&]() { return total ? atomicAdd(&a.ctl->next, 1) : 0; };
+            int turn = blockIdx.x + half * gridDim.x;
+            auto take = [&]() {
+                if (!a.few) return total ? atomicAdd(&a.ctl->next, 1) : 0;
+                const int idx = turn;
+                if (turn < total) turn += 2 * gridDim.x;
+                return idx;
+            };
             auto publish = [&](int i, int& idx, AtWork& w) {
                 const int s = i % kAnQueue;
                 if (idx >= total) idx = -1;
                 if (!(ok = mbar_wait(&item_empty[s], ((i / kAnQueue) & 1) ^ 1, abort_flag, a.status))) return;
                 *reinterpret_cast<volatile int*>(&queue[s]) = idx;
                 mbar_arrive(&item_full[s]);
-                if (idx >= 0) at_decode(a, n_wide + idx / heads, idx % heads, w);
+                if (idx >= 0) decode(idx, w);
             };
             AtWork w, wn;
             int idx = -1, in = 0;
@@ -1647,10 +1764,11 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParam
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G), heads = p.N * p.hkv_s;
     // the lists are there when this kernel is launched (the kernels before it let it start once they have them), and are
-    // read while those work
+    // read while those work; or the narrow kernel writes them
+    if (p.few) pdl_wait();
     const unsigned units = (unsigned)__ldcg(&p.ctl->n_chunks) * heads;
     const int n_tok = __ldcg(&p.ctl->n_tokens);
-    bool waited = false;
+    bool waited = p.few;
     for (unsigned u = blockIdx.x; u < units; u += gridDim.x) {
         const unsigned c = u / heads;
         const int h = u - c * heads, r = h / p.hkv_s;
@@ -1803,6 +1921,12 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     a.part_ml = p.part_ml;
     a.items = p.items;
     a.ctl = p.ctl;
+    a.few = p.few;
+    a.B = p.B;
+    a.cu = p.cu;
+    a.pos = p.pos;
+    a.chunks = p.chunks;
+    a.prefix_groups = p.prefix_groups;
     const int64_t D = p.d;
     cudaError_t e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, a.tpt, &a.tq);
     if (e == cudaSuccess) e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, kAtNarrow / G, &a.tqn);
@@ -1830,7 +1954,7 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     }
     const void* fn = d128 ? reinterpret_cast<const void*>(attn_narrow_kernel<128>)
                           : reinterpret_cast<const void*>(attn_narrow_kernel<64>);
-    const int smem = 2 * (d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM);
+    const int smem = 2 * (d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM) + (int)sizeof(AnFew);
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kAnThreads);
     if (e != cudaSuccess) return e;

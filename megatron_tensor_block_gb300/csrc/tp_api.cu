@@ -1294,7 +1294,9 @@ static tp_status attn_packed(const char* who, tp_plan_t plan, const void* q, con
     a.q = q;
     a.out = out;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_attn_plan(a, s);
+    // so few rows that no item can have more than the narrow kernel takes (a prefix is shared then)
+    a.few = B < 32 && (int64_t)T * (a.hq_s / a.hkv_s) <= a.narrow;
+    cudaError_t e = a.few ? cudaSuccess : launch_attn_plan(a, s);
     if (e == cudaSuccess) e = launch_attn_ragged(a, s);
     if (e != cudaSuccess) return cuda_fail(e, who);
     return ok();

@@ -353,6 +353,7 @@ struct RaggedAttnParams {
     int prefix_len;
     int shared;                           // 1: the prefix is attended to by tiles of the batch's tokens
     int narrow;                           // most rows of an item that the narrow kernel takes, 16 or 32
+    int few;                              // 1: no plan kernel, at most `narrow` rows of fewer than 32 sequences
     int64_t prefix_rows;
     const int* cu;                        // [B + 1]
     const int* pos;                       // [B] row of each sequence's first new token
@@ -373,7 +374,8 @@ struct AttnSizes {
     int64_t rows;
 };
 AttnSizes attn_sizes(int64_t max_batch, int64_t max_tokens, int hq, int hkv, int d);
-// Checks cu and pos, fills ctl and the lists; every other kernel of a packed batch reads ctl.
+// Checks cu and pos, fills ctl and the lists; every other kernel of a packed batch reads ctl. Not with `few`: the
+// attention's kernel does it then.
 cudaError_t launch_attn_plan(const RaggedAttnParams& p, cudaStream_t s);
 cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s);
 

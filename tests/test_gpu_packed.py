@@ -57,6 +57,15 @@ CASES = {
     "one_token_many_parts": (L(8, 1, 128, 1), [1], [20000], 0, {}),
     "items_just_over_a_round": (LLAMA, [64] * 20, [0] * 20, 640, {}),
     "few_items_of_many_blocks": (L(8, 2, 64, 1), [128, 90], [2500, 1800], 0, {}),
+    # few rows in all: up to 31 sequences and one more, empty ones between, several tokens, parts
+    "few_rows_31": (L(4, 4, 64, 1), [1] * 31, [(67 * i) % 300 for i in range(31)], 0, {}),
+    "few_rows_32": (L(4, 4, 64, 1), [1] * 32, [(67 * i) % 300 for i in range(32)], 0, {}),
+    "few_rows_31_prefix": (L(2, 2, 128, 2), [1, 0] * 15 + [1], [(67 * i) % 300 for i in range(31)], 390, {}),
+    "few_rows_32_prefix": (L(2, 2, 128, 2), [1, 0] * 16, [(67 * i) % 300 for i in range(32)], 390, {}),
+    "few_rows_several_tokens": (L(8, 2, 128, 2), [2, 0, 1, 0, 4], [500, 3, 0, 9, 1126], 0, {}),
+    "few_rows_several_tokens_prefix": (L(8, 2, 128, 2), [2, 0, 1, 0, 4], [500, 3, 0, 9, 1126], 257, {}),
+    "few_rows_group8_parts": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 0, {}),
+    "few_rows_group8_parts_prefix": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 5000, {}),
     "many_sequences": (QWEN, [1] * 1100, [(37 * i) % 150 for i in range(1100)], 0, {}),
     "many_sequences_prefix": (L(4, 1, 64, 1), [i % 3 for i in range(1300)], [(11 * i) % 40 for i in range(1300)], 70, {}),
 }
@@ -77,7 +86,8 @@ def test_attention_matches_float64(gpu_lib, name):
     print(f"{name}: largest error {share:.2f} of the bound")
 
 
-@pytest.mark.parametrize("name", ["mixed_step", "prefix_decode", "prefix_prompts"])
+@pytest.mark.parametrize("name", ["mixed_step", "prefix_decode", "prefix_prompts", "few_rows_several_tokens",
+                                  "few_rows_group8_parts_prefix"])
 def test_attention_is_deterministic_and_repeats_on_one_workspace(gpu_lib, name):
     import torch
     d = K.OnDevice(gpu_lib, make(name))
@@ -154,6 +164,62 @@ def test_malformed_offsets_write_nothing_and_are_recorded(gpu_lib, cu, prefix):
     d.run()
     assert d.status() == tb.binding.TP_ERR_SHAPE
     assert (d.got() == 7.0).all()
+
+
+@pytest.mark.parametrize("what", ["inf", "nan", "lowest"])
+@pytest.mark.parametrize("prefix", [0, 200])
+def test_few_rows_what_lies_behind_a_sequence_does_not_reach_it(gpu_lib, what, prefix):
+    stale = {"inf": np.inf, "nan": np.nan, "lowest": -3.3895e38}[what]
+    b = K.Batch(QWEN, [1, 0, 2, 1], [3, 5, 130, 700], prefix=prefix, seed=3, stale=stale, extra_kv=200)
+    d = K.OnDevice(gpu_lib, b)
+    d.run()
+    K.check(d.got(), b)
+
+
+@pytest.mark.parametrize("prefix", [0, 70])
+def test_few_rows_positions_outside_the_cache_give_zeros_and_a_status(gpu_lib, prefix):
+    tb = gpu_lib
+    b = K.Batch(L(8, 2, 128, 1), [3, 2, 1, 1], [98, -1, 99, 200], prefix=prefix, seed=5, max_kv=100)
+    d = K.OnDevice(tb, b)
+    d.run()
+    assert d.status() == tb.binding.TP_ERR_CAPACITY
+    K.check(d.got(), b)
+
+
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("cu", [[1, 2, 3], [0, 4, 3], [0, 3, 8], [-1, 2, 3], [0, 9, 3], [0, 2147483647, 3]])
+def test_few_rows_malformed_offsets_write_nothing_and_are_recorded(gpu_lib, cu, prefix):
+    import torch
+    tb = gpu_lib
+    b = K.Batch(QWEN, [1, 2], [4, 300], prefix=prefix, seed=6)
+    d = K.OnDevice(tb, b)
+    d.cu.copy_(torch.tensor(cu, dtype=torch.int32))
+    d.run()
+    assert d.status() == tb.binding.TP_ERR_SHAPE
+    assert (d.got() == 7.0).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 150])
+def test_few_rows_captured_call_replays_with_other_lengths(gpu_lib, prefix):
+    import torch
+    tb = gpu_lib
+    full = K.Batch(QWEN, [2, 1, 1], [900, 900, 900], prefix=prefix, seed=7)
+    d = K.OnDevice(tb, full)
+    want = d.run().clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d.run()
+    for new, cached in (([1, 0, 1], [5, 0, 640]), ([0, 0, 4], [1, 1, 127]), ([2, 1, 1], [900, 900, 900])):
+        d.cu.copy_(torch.tensor(np.cumsum([0] + new), dtype=torch.int32))
+        d.pos.copy_(torch.tensor(cached, dtype=torch.int32))
+        d.out.fill_(7.0)
+        g.replay()
+        replayed = d.out.clone()
+        d.out.fill_(7.0)
+        assert torch.equal(d.run(), replayed)
+        assert (replayed[:, sum(new):] == 7.0).all()
+    assert torch.equal(replayed, want)
 
 
 @pytest.mark.parametrize("prefix", [0, 150])
