@@ -374,6 +374,22 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
 //                 the next item is under way.
 // The items' ranges of blocks are walked in the same order by every role; all
 // waits are bounded.
+//
+// Bound by the tensor cores: 256 rows x 128 keys are 2048 cycles of products for
+// d = 128 (2053 measured, products alone) and 1024 for d = 64, where the 32768
+// exponentials, at 4 cycles for 32 of a quarter of the SM, take as long. Causal
+// prompts of 32 heads: 8192 tokens 342 us, 1.61 PFLOP/s (d = 64: 286 us, 0.96),
+// 16384 tokens 1350 us, 1.63 PFLOP/s of 1.96 measured for a library product; the
+// block takes about 2500 cycles, and the power limit takes its share of the
+// clock. For short prompts an item's beginning and end count: the first 10 to 14
+// us with cold code, each later one 3 to 6 (16 prompts behind 2048 keys: 56 us
+// for 15 us of products).
+//
+// Taken against (8192 tokens): the scores read twice, once for the maximum, once
+// for the weights, so that they need no registers: 400 for 357 us; the products
+// of both tiles without turns: 479 for 359; spilled registers or longer loops
+// cost more than any of their instructions, which the split of registers and the
+// waits out of line come from.
 // ---------------------------------------------------------------------------
 
 constexpr int kAtThreads = 512;
@@ -1211,6 +1227,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
 //   warp 4      takes the items from the list as the half becomes free, TMA
 //   warp 5      products
 //   warps 6, 7  nothing (registers are dealt out to groups of four warps)
+// Decode of 256 sequences of 0 to 2047 keys behind 16384 shared ones, 32 heads:
+// 1.15 GB in 204 to 210 us, 5.5 to 5.7 TB/s, the shared keys on the wide kernel
+// beside it and the joining included. Taking the items out of tiles of 128 query
+// rows took that call from 473 to 305 us, the two halves from 271 to 242.
 // ---------------------------------------------------------------------------
 
 constexpr int kAnThreads = 512, kAnHalf = 256;   // of a half's two warpgroups the second gives registers to the first
@@ -1755,11 +1775,16 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
 
 // One warp per output row: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
 // over the row's own parts, then its prefix tile's, in their order. Bound by
-// the latency of its loads: lane i takes part i's m and l, and the first eight
-// parts' outputs are under way before these are there.
+// the latency of its loads and by its own start, since no CTA of it fits beside
+// those before it: lane i takes part i's m and l, and the first four parts'
+// outputs are under way before these are there. Four CTAs per SM: decode of 64
+// and of 256 behind a prefix 53 and 204 us; with three 55 and 205, with five 56
+// and 212 (211 beside it), with eight 61 and 218. It ends 5 to 12 us after the
+// kernel before it, for 5 to 17 MB read.
+constexpr int kAtJoinCtas = 4;            // per SM
 template <int D>
-__global__ void __launch_bounds__(256) attn_combine_kernel(const RaggedAttnParams p) {
-    constexpr int E = D / 32, AHEAD = 8;             // elements per lane, parts loaded together
+__global__ void __launch_bounds__(256, kAtJoinCtas) attn_combine_kernel(const RaggedAttnParams p) {
+    constexpr int E = D / 32, AHEAD = 4;             // elements per lane, parts loaded together
     constexpr unsigned kAll = 0xffffffffu;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.hq_s / p.hkv_s, per = 2 * (kAtM / G), heads = p.N * p.hkv_s;
@@ -1963,7 +1988,7 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     const int64_t units = ((int64_t)p.T * G / 8 + p.B) * p.N * p.hkv_s;
     return launch_pdl(d128 ? reinterpret_cast<const void*>(attn_combine_kernel<128>)
                            : reinterpret_cast<const void*>(attn_combine_kernel<64>),
-                      cargs, (int)(units < 8 * kSMs ? units : 8 * kSMs), 0, s, 256);
+                      cargs, (int)(units < kAtJoinCtas * kSMs ? units : kAtJoinCtas * kSMs), 0, s, 256);
 }
 
 }  // namespace tpk
