@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
 // d = 128 (2053 measured, products alone) and 1024 for d = 64, where the 32768
 // exponentials, at 4 cycles for 32 of a quarter of the SM, take as long. Causal
 // prompts of 32 heads: 8192 tokens 342 us, 1.61 PFLOP/s (d = 64: 286 us, 0.96),
-// 16384 tokens 1350 us, 1.63 PFLOP/s of 1.96 measured for a library product; the
+// 16384 tokens 1350 us, 1.63 PFLOP/s of 1.88 measured for a library product; the
 // block takes about 2500 cycles, and the power limit takes its share of the
 // clock. For short prompts an item's beginning and end count: the first 10 to 14
 // us with cold code, each later one 3 to 6 (16 prompts behind 2048 keys: 56 us
