@@ -1223,7 +1223,7 @@ static tp_status packed_args(const char* who, tp_plan_t plan, const tp_kv_set* p
     if (d.dtype != TP_BF16) return fail(TP_ERR_UNSUPPORTED, "%s runs on bf16 plans", who);
     if (B < 1 || B > d.max_batch || T < 1 || T > d.max_tokens)
         return fail(TP_ERR_SHAPE, "%s: B=%d or T=%d outside 1..max_batch, 1..max_tokens of the plan", who, B, T);
-    if (prefix_len < 0 || prefix_len + d.max_kv > INT32_MAX - 1024)
+    if (prefix_len < 0 || d.max_kv > INT32_MAX - 1024 || prefix_len > INT32_MAX - 1024 - d.max_kv)
         return fail(TP_ERR_SHAPE, "%s: prefix_len=%lld out of range", who, (long long)prefix_len);
     if (prefix_len > 0 && !prefix) return fail(TP_ERR_NULL, "%s: prefix is NULL", who);
     if (prefix_len > prefix_rows && prefix_len > 0)

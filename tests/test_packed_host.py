@@ -35,6 +35,7 @@ REFUSALS = [
     (dict(prefix=([A, A], [A, A]), prefix_len=9, prefix_rows=8), B.TP_ERR_CAPACITY),
     (dict(prefix=([A, A], [A, A]), prefix_len=-1, prefix_rows=8), B.TP_ERR_SHAPE),
     (dict(prefix=([A, A], [A, A]), prefix_len=2 ** 31 - 50, prefix_rows=2 ** 31), B.TP_ERR_SHAPE),
+    (dict(prefix=([A, A], [A, A]), prefix_len=2 ** 63 - 1, prefix_rows=2 ** 63 - 1), B.TP_ERR_SHAPE),
     (dict(prefix=([A, A], [0, A]), prefix_len=8, prefix_rows=8), B.TP_ERR_NULL),
 ]
 
