@@ -542,7 +542,7 @@ tp_status tp_attn_prefix(tp_plan_t plan, const void* q, const tp_kv_set* prefix,
  * as they are. Rows at positions outside 0..max_kv-1 append nothing, take no
  * attention output, and are recorded as TP_ERR_CAPACITY; a malformed cu
  * records TP_ERR_SHAPE and writes neither y nor the caches.
- * Errors: as tp_attn_prefix, and TP_ERR_INVALID_ARG (y == x). */
+ * Errors: as tp_attn_prefix, and TP_ERR_INVALID_ARG (y overlaps x). */
 tp_status tp_block_forward_packed(tp_plan_t plan, const tp_shard_set* w, const tp_kv_set* kv,
                                   const tp_kv_set* prefix, int64_t prefix_len, int64_t prefix_rows,
                                   const float* x, float* y, const int32_t* cu, const int32_t* pos,

@@ -1327,6 +1327,9 @@ extern "C" tp_status tp_block_forward_packed(tp_plan_t plan, const tp_shard_set*
     tp_status st = packed_args(who, plan, prefix, prefix_len, prefix_rows, kv, cu, pos, B, T, workspace, workspace_bytes, a);
     if (st) return st;
     if (!aligned16(x) || !aligned16(y)) return fail(TP_ERR_ALIGN, "%s: x and y must be 16-byte aligned", who);
+    const uintptr_t bytes = (uintptr_t)T * plan->d.hidden * 4;
+    const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+    if (xa < ya + bytes && ya < xa + bytes) return fail(TP_ERR_INVALID_ARG, "%s: y must not overlap x", who);
     if ((st = check_device())) return st;
     return forward_prefill(plan, w, kv, x, y, pos, B, 0, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream), &a);
 }

@@ -79,6 +79,15 @@ def test_packed_block_refuses(kw, status):
     assert e.value.status == status, str(e.value)
 
 
+@pytest.mark.parametrize("apart", [16, 64 * K.plan_desc(tb, LAY, 4, 64, 100)["hidden"] * 4 - 16])
+def test_packed_block_refuses_an_output_over_its_input(apart):
+    p = plan()
+    for x, y in ((A, A + apart), (A + apart, A)):
+        with pytest.raises(tb.TpError) as e:
+            tb.tp_block_forward_packed(p, {}, ([A, A], [A, A]), x, y, A, A, 4, 64, A, p.workspace_bytes, stream=0)
+        assert e.value.status == B.TP_ERR_INVALID_ARG
+
+
 LOGITS = [
     (dict(logits=None), B.TP_ERR_NULL), (dict(out=None), B.TP_ERR_NULL), (dict(T=0), B.TP_ERR_SHAPE),
     (dict(tokens=A), B.TP_ERR_NULL), (dict(cu_tokens=A), B.TP_ERR_NULL), (dict(repetition=A), B.TP_ERR_NULL),
