@@ -224,36 +224,20 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
                 if (kind & AT_OWN) chunks = (k * G + 7) / 8;
                 else p.prefix_groups[(unsigned)t0 / (unsigned)per] = make_int2(row1, parts);
             }
-            // the lanes' chunks and items, written by the warp together
-            int first = warp_scan(chunks, lane);
-            int sum = __shfl_sync(kAll, first, 31);
+            const int upto = warp_scan(chunks, lane), sum = __shfl_sync(kAll, upto, 31);
             if (sum) {
-                first -= chunks;
                 int to = 0;
                 if (lane == 0) to = atomicAdd(&s_chunks, sum);
-                to = __shfl_sync(kAll, to, 0);
+                to = __shfl_sync(kAll, to, 0) + upto - chunks;
 #pragma unroll 1
-                for (int i = lane; i < ((sum + 31) & ~31); i += 32) {
-                    const int l = warp_owner(first, i), j = i - __shfl_sync(kAll, first, l);
-                    const AttnChunk x = {__shfl_sync(kAll, t0, l),   __shfl_sync(kAll, k, l),     __shfl_sync(kAll, qpos, l),
-                                         __shfl_sync(kAll, row1, l), __shfl_sync(kAll, parts, l), j, 0, 0};
-                    if (i < sum) p.chunks[to + i] = x;
-                }
+                for (int j = 0; j < chunks; ++j) p.chunks[to + j] = AttnChunk{t0, k, qpos, row1, parts, j, 0, 0};
             }
-            first = warp_scan(entries, lane);
-            sum = __shfl_sync(kAll, first, 31);
-            first -= entries;
 #pragma unroll 1
-            for (int i = lane; i < ((sum + 31) & ~31); i += 32) {
-                const int l = warp_owner(first, i), j = i - __shfl_sync(kAll, first, l);
-                const int np = __shfl_sync(kAll, parts, l), nl = __shfl_sync(kAll, len, l), r0 = __shfl_sync(kAll, row0, l);
-                const int r1 = __shfl_sync(kAll, row1, l) + (j - 1) * __shfl_sync(kAll, rows, l);
-                const int f0 = __shfl_sync(kAll, e0, l), f1 = __shfl_sync(kAll, e1, l), all = __shfl_sync(kAll, nb, l);
-                AttnItem x = {__shfl_sync(kAll, t0, l), __shfl_sync(kAll, k, l),
-                              __shfl_sync(kAll, b, l),  __shfl_sync(kAll, qpos, l),
-                              j * nl, min(all, (j + 1) * nl), kind, j && r0 >= 0 ? r1 : r0};
-                if (j >= np) x = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};
-                if (i < sum) p.items[j == np - 1 ? f1 : f0 + j] = x;
+            for (int j = 0; j < entries; ++j) {
+                const int row = j && row0 >= 0 ? row1 + (j - 1) * rows : row0;
+                AttnItem x = {t0, k, b, qpos, j * len, min(nb, (j + 1) * len), kind, row};
+                if (j >= parts) x = AttnItem{0, 0, 0, 0, 0, 0, kind, -1};
+                p.items[j == parts - 1 ? e1 : e0 + j] = x;
             }
         }
 
