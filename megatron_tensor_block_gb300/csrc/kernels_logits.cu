@@ -15,11 +15,13 @@
 // biased entries follow.
 //
 // 256 rows x 151936 with histories of up to 8192 tokens, masks and biases take
-// 76 us, 4.2 TB/s; the bare copy by the same kernel 47, masks and biases 3 each.
-// The rest is the counting, which every slice of a row does for the whole
-// history: that is why slices are not shorter, and longer ones leave fewer CTAs
-// to cover one another's phases. Entries per slice and time: 2048 106, 4096 85,
-// 8192 76, 16384 78, 24576 88, 49152 98 us.
+// 72 to 75 us, 4.3 TB/s; without histories 60, the bare copy 47. The history's
+// loads, its atomics and the penalties are about 5 us each: a CTA spends them
+// one after the other, and only the six on an SM cover one another. Every slice
+// of a row counts its whole history: that is why slices are not shorter, and
+// longer ones leave fewer CTAs. Entries per slice and time: 2048 106, 4096 85,
+// 8192 76, 16384 78, 24576 88, 49152 98 us. Slower too: copies to shared memory
+// ahead (95, fewer CTAs), prefetches to L2 (75 for 73).
 #include <climits>
 
 #include "common.cuh"
@@ -89,7 +91,14 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
     const int lo = max(v0, 0), hi = (int)min((int64_t)v0 + SLICE, (int64_t)a.V);
     const unsigned span = (unsigned)max(hi - lo, 0);
     int id = -1;                                            // the thread's entry of a short bias list
-    if (bn && bn <= THREADS && tid < bn) s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
+    float bias = 0.f, biased = 0.f;                         // its bias and its logit, read ahead of the counting
+    if (bn && bn <= THREADS && tid < bn) {
+        s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
+        if (id >= lo && id < hi) {
+            bias = a.bias_values[(int64_t)b0 + tid];
+            biased = a.x[row0 + id];
+        }
+    }
     if (hn) {
         for (int i = tid; i < SLICE / 4; i += THREADS) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
@@ -133,16 +142,25 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         const uint32_t w0 = mask[va >> 5], w1 = mask[vb >> 5];
         return (v >= 0 ? __funnelshift_r(w0, w1, v & 31) : w0 << -v) & 15u;
     };
+    auto penalise = [&](float e, unsigned n) {
+        e = e > 0.f ? e / rep : e * rep;
+        return n > 1u ? e - freq * (float)(n >> 1) - pres : e;
+    };
     auto change = [&](float4& x, const uint4& c, unsigned ok) {
         float e[4] = {x.x, x.y, x.z, x.w};
         const unsigned n[4] = {c.x, c.y, c.z, c.w};
-        if (n[0] | n[1] | n[2] | n[3]) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (n[k]) {
-                    e[k] = e[k] > 0.f ? e[k] / rep : e[k] * rep;
-                    if (n[k] > 1u) e[k] = e[k] - freq * (float)(n[k] >> 1) - pres;
-                }
+        // one at a time: most groups have none, but most warps have one in a lane, and four of them in turn would cost
+        // the warp four divisions
+        unsigned any = (n[0] ? 1u : 0u) | (n[1] ? 2u : 0u) | (n[2] ? 4u : 0u) | (n[3] ? 8u : 0u);
+#pragma unroll 1
+        for (; any; any &= any - 1) {
+            const unsigned k = any & -any;
+            const float z = penalise(k == 1 ? e[0] : k == 2 ? e[1] : k == 4 ? e[2] : e[3],
+                                     k == 1 ? n[0] : k == 2 ? n[1] : k == 4 ? n[2] : n[3]);
+            e[0] = k == 1 ? z : e[0];
+            e[1] = k == 2 ? z : e[1];
+            e[2] = k == 4 ? z : e[2];
+            e[3] = k == 8 ? z : e[3];
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -200,7 +218,8 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         }
     }
 
-    // Biases go onto the penalised logits that the sweep has written; a masked one stays -inf.
+    // Biases go onto the penalised logits; a masked one stays -inf. The results of a short list are formed from what was read
+    // ahead and replace what the sweep has written, those of a long one are added to it.
     if (!bn) return;
     __syncthreads();
     auto add = [&](int v, int entry) {
@@ -210,7 +229,9 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         if (id >= lo && id < hi) {
             bool last = true;
             for (int j = tid + 1; j < bn; ++j) last &= s_ids[j] != id;
-            if (last) add(id, tid);
+            const unsigned n = hn ? cnt[id - v0] : 0u;
+            if (n) biased = penalise(biased, n);
+            if (last && (!mask || mask[id >> 5] >> (id & 31) & 1u)) a.y[row0 + id] = biased + bias;
         }
         return;
     }
