@@ -1215,6 +1215,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
 // 1.15 GB in 204 to 210 us, 5.5 to 5.7 TB/s, the shared keys on the wide kernel
 // beside it and the joining included. Taking the items out of tiles of 128 query
 // rows took that call from 473 to 305 us, the two halves from 271 to 242.
+// This kernel's own reading goes at the measured copy rate (6.8 TB/s in 171 us).
 // ---------------------------------------------------------------------------
 
 constexpr int kAnThreads = 512, kAnHalf = 256;   // of a half's two warpgroups the second gives registers to the first
