@@ -104,7 +104,9 @@ __device__ __forceinline__ int warp_owner(int before, int i) {
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAttnParams p) {
     __shared__ __align__(16) int s_hist[2 * kAtBuckets];             // wide items, narrow items
     __shared__ unsigned long long s_blocks[2][kPlanWarps];           // per warp: blocks of wide and narrow tiles
-    __shared__ int s_tiles[kPlanWarps], s_longest[kPlanWarps], s_warp[kPlanWarps];       // wide tiles
+    __shared__ int s_tiles[kPlanWarps], s_longest[kPlanWarps];       // wide tiles
+    __shared__ int s_few[kPlanWarps], s_few_longest[kPlanWarps];     // narrow tiles
+    __shared__ int s_warp[kPlanWarps];
     __shared__ int s_rows, s_chunks;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr unsigned kAll = 0xffffffffu;
@@ -139,7 +141,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
     load(warp * lanes, c0, n0, q0);
 
     unsigned long long wide_blocks = 0, narrow_blocks = 0;
-    int wide_tiles = 0, longest = 0;
+    int wide_tiles = 0, longest = 0, few_tiles = 0, few_longest = 0;
+    int narrow = p.narrow;                                           // most rows of a narrow item
     int target_w = 0, target_n = 0;                                  // the longest parts
     int last_from = INT_MAX, last_parts = 1;                         // a last round's items and their parts
     int n_wide = 0, n_items = 0;
@@ -184,10 +187,14 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
             const int qpos = (int)((int64_t)__shfl_sync(kAll, q, owner) + at);
             const int left = __shfl_sync(kAll, n, owner) - at, k = tile < total ? min(per, left) : 0;     // tokens
             i0 += step;
-            const bool live = k > 0, nar = k * G <= p.narrow;
+            const bool live = k > 0, nar = k * G <= narrow;
             const int nb = kind == AT_PREFIX ? n_prefix : in_item + own_blocks((int64_t)qpos + k, p.max_kv);
             if (pass == 0) {
-                if (live && nar) narrow_blocks += nb;
+                if (live && nar) {
+                    narrow_blocks += nb;
+                    ++few_tiles;
+                    few_longest = max(few_longest, nb);
+                }
                 if (live && !nar) {
                     wide_blocks += nb;
                     ++wide_tiles;
@@ -249,7 +256,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
             }
             wide_tiles = __reduce_add_sync(kAll, wide_tiles);
             longest = __reduce_max_sync(kAll, longest);
+            few_tiles = __reduce_add_sync(kAll, few_tiles);
+            few_longest = __reduce_max_sync(kAll, few_longest);
             if (lane == 0) {
+                s_few[warp] = few_tiles;
+                s_few_longest[warp] = few_longest;
                 s_tiles[warp] = wide_tiles;
                 s_longest[warp] = longest;
                 s_blocks[0][warp] = wide_blocks;
@@ -270,9 +281,21 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
             }
             wide_tiles = __reduce_add_sync(kAll, lane < kPlanWarps ? s_tiles[lane & kMask] : 0);
             longest = __reduce_max_sync(kAll, s_longest[lane & kMask]);
+            few_tiles = __reduce_add_sync(kAll, lane < kPlanWarps ? s_few[lane & kMask] : 0);
+            // A few narrow items beside many wide ones are done as such: their own kernel gets an SM only when the wide one
+            // leaves it, and its chain of an item's blocks then follows. Tiles of one prompt and of single tokens over 2000
+            // keys, 8 KV heads, apart and together: 32 and 4 52 and 48 us, 64 and 16 132 and 125, 64 and 32 153 and 152, 64
+            // and 64 187 and 193. Not where the wide ones hardly fill the SMs once: 20 and 5 58 and 60, 8 and 2 28 and 37.
+            if (few_tiles <= wide_tiles / 4 && wide_tiles * (int64_t)heads >= kSMs + kSMs / 2) {
+                narrow = 0;
+                wide_tiles += few_tiles;
+                wide_blocks += narrow_blocks;
+                narrow_blocks = 0;
+                longest = max(longest, __reduce_max_sync(kAll, s_few_longest[lane & kMask]));
+            }
             if (p.shared) {
                 const int tiles = (unsigned)(n_tok + per - 1) / (unsigned)per;
-                const int small = tiles && (n_tok - (tiles - 1) * per) * G <= p.narrow;
+                const int small = tiles && (n_tok - (tiles - 1) * per) * G <= narrow;
                 wide_tiles += tiles - small;
                 wide_blocks += (unsigned long long)(tiles - small) * n_prefix;
                 if (small) narrow_blocks += n_prefix;

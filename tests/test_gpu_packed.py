@@ -57,6 +57,10 @@ CASES = {
     "one_token_many_parts": (L(8, 1, 128, 1), [1], [20000], 0, {}),
     "items_just_over_a_round": (LLAMA, [64] * 20, [0] * 20, 640, {}),
     "few_items_of_many_blocks": (L(8, 2, 64, 1), [128, 90], [2500, 1800], 0, {}),
+    # single tokens beside a prompt of so many items that they are done as its are, or not quite
+    "few_rows_beside_a_prompt": (L(32, 8, 64, 2), [1, 1856, 2, 0, 4, 1], [700, 5, 129, 3, 1000, 0], 0, {}),
+    "few_rows_beside_a_prompt_and_a_prefix": (L(32, 8, 64, 2), [1, 1856, 2, 0, 4, 1], [700, 5, 129, 3, 1000, 0], 70, {}),
+    "few_rows_beside_a_shorter_prompt": (L(32, 8, 64, 2), [1, 1792, 2, 0, 4, 1], [700, 5, 129, 3, 1000, 0], 0, {}),
     # few rows in all: up to 31 sequences and one more, empty ones between, several tokens, parts
     "few_rows_31": (L(4, 4, 64, 1), [1] * 31, [(67 * i) % 300 for i in range(31)], 0, {}),
     "few_rows_32": (L(4, 4, 64, 1), [1] * 32, [(67 * i) % 300 for i in range(32)], 0, {}),
