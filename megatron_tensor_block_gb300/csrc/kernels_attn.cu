@@ -45,11 +45,15 @@ __device__ __forceinline__ int own_blocks(int64_t end, int max_kv) {
     return (int)((e + kAtK - 1) / kAtK);
 }
 
-// Splits `nb` blocks into parts of at most `len` blocks each when nb exceeds it by half.
-__device__ __forceinline__ void part_split(int nb, int target, int& parts, int& len) {
+// Splits `nb` blocks into parts of about `target` blocks each: equal ones when nb exceeds it by half, or, where `rest` is
+// set, parts of `target` and a shorter last one, of at least kAtMinCut blocks.
+__device__ __forceinline__ void part_split(int nb, int target, bool rest, int& parts, int& len) {
     parts = 1;
     len = nb;
-    if (nb > target + target / 2) {
+    if (rest) {
+        parts = max(1, (int)((unsigned)(nb - kAtMinCut + target) / (unsigned)target));
+        len = parts > 1 ? max(target, (int)((unsigned)(nb + parts - 1) / (unsigned)parts)) : nb;
+    } else if (nb > target + target / 2) {
         parts = (unsigned)(nb + target - 1) / (unsigned)target;
         len = (unsigned)(nb + parts - 1) / (unsigned)parts;
         parts = (unsigned)(nb + len - 1) / (unsigned)len;
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
     int wide_tiles = 0, longest = 0, few_tiles = 0, few_longest = 0;
     int narrow = p.narrow;                                           // most rows of a narrow item
     int target_w = 0, target_n = 0;                                  // the longest parts
+    bool rests = false;                                              // wide items: of that length but the last
     int last_from = INT_MAX, last_parts = 1;                         // a last round's items and their parts
     int n_wide = 0, n_items = 0;
     const int own = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
                 continue;
             }
             int parts, len;
-            part_split(nb, nar ? target_n : target_w, parts, len);
+            part_split(nb, nar ? target_n : target_w, rests && !nar, parts, len);
             int* rest = &s_hist[(nar ? 2 : 1) * kAtBuckets - 1 - min(nb - (parts - 1) * len, kAtBuckets - 1)];
             int* full = &s_hist[(nar ? 2 : 1) * kAtBuckets - 1 - min(len, kAtBuckets - 1)];
             int e0 = 0, e1 = 0;                                      // places of the parts but the last, and of the last
@@ -311,21 +316,35 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
                 // the joining, 4.4 MB of float32 results a microsecond there and back. Both sides, 8 KV heads: 256 tokens
                 // behind 16384, k = 1/2/3/4/6: 252/209/225/238/248 us; 64 behind 4096, k = 1/2/3/4/6/8: 93/73/65/62/56/58
                 // us; a chunk of 512 behind 30001, k = 1/2/3/4/6/8: 331/195/249/202/210/217 us.
-                const int all = (int)items, k = lane + 1, len = (unsigned)(longest + k - 1) / (unsigned)k;
-                const int sms = min(k * all, kSMs);
+                // Lanes 16 and up take k parts of one length on an SM each and a shorter last one for the SMs that are left,
+                // which do one after the other: the chunk in two equal parts uses 128 SMs and takes 188 us, in two and a
+                // rest 176; one of 1024 331 and 321, of 256 107 and 101.
+                const int all = (int)items, k = (lane & 15) + 1;
+                int len = (unsigned)(longest + k - 1) / (unsigned)k, sms = min(k * all, kSMs), time = len, parts = k;
+                bool ok = k == 1 || (k * all <= 3 * kSMs && len >= kAtMinCut);
+                if (lane & 16) {
+                    const int turns = (unsigned)(all + kSMs - k * all - 1) / (unsigned)max(kSMs - k * all, 1);
+                    len = (unsigned)(turns * (longest + 4)) / (unsigned)(turns * k + 1) + 1;
+                    ok = k * all < kSMs && longest - k * len >= kAtMinCut;
+                    sms = kSMs;
+                    parts = k + 1;
+                    time = len;
+                } else {
+                    time = (k * all + kSMs - 1) / kSMs * (len + 2) - 2;
+                }
                 const float bytes = (float)narrow_blocks * heads * (kAtK * 4) * p.d;
-                const float wide_us = (float)((k * all + kSMs - 1) / kSMs * (len + 2) + 7) * (narrow_blocks ? 1.6f : 1.1f);
+                const float wide_us = (float)(time + 9) * (narrow_blocks ? 1.6f : 1.1f);
                 const float left = fmaxf(0.f, bytes - wide_us * fminf(6.5e6f, (kSMs - sms) * 6e4f));
                 const float join = (float)(all * 2 * kAtM) * p.d * 8 / 4.4e6f;
-                float t = wide_us + left / 6.5e6f + (k > 1 ? k * join : 0.f);
-                if (k > 1 && (k > kAtMaxParts || k * all > 3 * kSMs || len < kAtMinCut)) t = INFINITY;
-                const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));           // positive: ordered as their bits
-                const int parts = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best));
-                target_w = (unsigned)(longest + parts - 1) / (unsigned)parts;
+                const float t = ok ? wide_us + left / 6.5e6f + (parts > 1 ? parts * join : 0.f) : INFINITY;
+                const unsigned best = __reduce_min_sync(kAll, __float_as_uint(t));       // positive: ordered as their bits
+                const int lane_of = __ffs(__ballot_sync(kAll, __float_as_uint(t) == best)) - 1;
+                target_w = __shfl_sync(kAll, len, lane_of);
+                rests = lane_of & 16;
             }
             // a last round of few items, if nothing else is cut: parts for its items
             const int rounds = items <= 3 * kSMs ? (int)items / kSMs : 0;
-            if (rounds && longest <= target_w + target_w / 2) {
+            if (rounds && !rests && longest <= target_w + target_w / 2) {
                 last_from = (unsigned)(rounds * kSMs + heads - 1) / (unsigned)heads;
                 const int rest = wide_tiles - last_from;
                 last_parts = rest > 0 ? min(kAtMaxParts, (int)((unsigned)kSMs / (unsigned)(rest * heads))) : 1;
@@ -1489,7 +1508,7 @@ __device__ __noinline__ void an_few_plan(const AtArgs& a, AnFew* f, int lane, bo
     if (bad) n = 0;
     const int nb = !n ? 0 : prefix ? (a.prefix_len + kAtK - 1) / kAtK : own_blocks((int64_t)q + n, a.max_kv);
     int parts, len;
-    part_split(nb, narrow_share((unsigned)__reduce_add_sync(kAll, nb), heads), parts, len);
+    part_split(nb, narrow_share((unsigned)__reduce_add_sync(kAll, nb), heads), false, parts, len);
     if (!n) parts = 0;
     const int items = warp_scan(parts, lane), more = max(parts - 1, 0) * heads * n * a.G;
     const int row1 = 2 * a.T * heads * a.G + warp_scan(more, lane) - more;

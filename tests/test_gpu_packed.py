@@ -70,6 +70,7 @@ CASES = {
     "few_rows_several_tokens_prefix": (L(8, 2, 128, 2), [2, 0, 1, 0, 4], [500, 3, 0, 9, 1126], 257, {}),
     "few_rows_group8_parts": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 0, {}),
     "few_rows_group8_parts_prefix": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 5000, {}),
+    "parts_and_a_rest": (L(32, 32, 64, 1), [512, 3], [8000, 100], 0, {}),
     "many_sequences": (QWEN, [1] * 1100, [(37 * i) % 150 for i in range(1100)], 0, {}),
     "many_sequences_prefix": (L(4, 1, 64, 1), [i % 3 for i in range(1300)], [(11 * i) % 40 for i in range(1300)], 70, {}),
 }
