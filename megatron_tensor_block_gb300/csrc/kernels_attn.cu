@@ -1582,6 +1582,13 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
     static_assert((2 * R + 9 + 2 * kAnQueue + 1) * 8 + (kAnQueue + 4) * 4 <= Sh::HEAD - 4 * kAtNarrow * 4, "the head's words");
 
     const int tid = threadIdx.x % kAnHalf, warp = uniform(tid >> 5), lane = tid & 31;
+    // Behind the wide kernel the lists are there: it lets this one start only after its own wait. This kernel waits for
+    // the wide one at its end, so that what follows it follows both. Often there is nothing left for it.
+    int n_wide = 0, n_items = 0;
+    if (a.after_wide) {
+        n_wide = __ldcg(&a.ctl->n_wide);
+        n_items = __ldcg(&a.ctl->n_items);
+    }
     if (tid == 0) {
         for (int i = 0; i < R; ++i) {
             mbar_init(&kv_full[i], 1);
@@ -1606,25 +1613,28 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
         if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
         fence_mbar_init();
     }
+    if (a.after_wide && n_items == n_wide) {
+        pdl_trigger();
+        pdl_wait();
+        return;
+    }
     if (warp == 5 && half == 0) tmem_alloc(smem_u32(tmem_slot), 256);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uniform(*reinterpret_cast<uint32_t*>(reinterpret_cast<unsigned char*>(tmem_slot) - half * Sh::SMEM)) + 128 * half;
-    // Behind the wide kernel the lists are there: it lets this one start only after its own wait. This kernel waits for
-    // the wide one at its end, so that what follows it follows both.
     if (!a.after_wide) pdl_wait();
     pdl_trigger();
     const int heads = a.N * a.hkv_s;
     AnFew* few = reinterpret_cast<AnFew*>(smem + 2 * Sh::SMEM);
-    int n_wide = 0, total;
+    int total;
     if (a.few) {
         if (threadIdx.x < 32) an_few_plan(a, few, lane, blockIdx.x == gridDim.x - 1);
         __syncthreads();
         total = few->total * heads;
     } else {
-        n_wide = __ldcg(&a.ctl->n_wide);
-        total = (__ldcg(&a.ctl->n_items) - n_wide) * heads;
+        if (!a.after_wide) n_items = __ldcg(&a.ctl->n_items);         // none is wide
+        total = (n_items - n_wide) * heads;
     }
     if (*abort_flag) total = 0;
     auto decode = [&](int idx, AtWork& w) {
