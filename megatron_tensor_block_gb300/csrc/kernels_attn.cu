@@ -838,8 +838,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
             // ---------------------------------------------------------------- products
             // A warp for each tile. The products queue only a few deep, so what a warp does between them is lost to the
             // tensor cores unless the other's are under way. They take turns, a block's products each: mixed with the
-            // other's, a tile's would take twice as long, and both softmaxes would then wait and run together. The whole warp runs the loop on warp-uniform values and one
-            // elected lane issues; the common block has a short path of its own.
+            // other's, a tile's would take twice as long, and both softmaxes would then wait and run together. The whole warp
+            // runs the loop on warp-uniform values and one elected lane issues; the common block has a short path of its own.
             const int t = warp - 1;
             const uint32_t id_s = idesc_bf16(kAtM, kAtK), id_o = idesc_bf16_bmn(kAtM, D);
             const uint64_t dq = smem_desc_sw128(smem_u32(sq) + t * Sh::QB), dk0 = smem_desc_sw128(smem_u32(ring));
