@@ -438,7 +438,7 @@ struct AtShape {
 struct AtArgs {
     CUtensorMap tq;                       // q as [N T][hq_s][D], boxes of 128 / G tokens x G heads x 64
     CUtensorMap tqn;                      // the same with boxes of kAtNarrow / G tokens
-    CUtensorMap tk[TP_MAX_SHARDS];        // caches as [max_batch hkv_s][max_kv][D], boxes of 128 rows x 64
+    CUtensorMap tk[TP_MAX_SHARDS];        // caches as [max_batch hkv_s][max_kv][D], boxes of 128 (narrow: kAnBox) rows x 64
     CUtensorMap tv[TP_MAX_SHARDS];
     CUtensorMap pk[TP_MAX_SHARDS];        // prefix as [hkv_s][prefix_len][D] (rows past it read as zeros)
     CUtensorMap pv[TP_MAX_SHARDS];
@@ -1254,7 +1254,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
 //   warp 5      products
 //   warps 6, 7  nothing (registers are dealt out to groups of four warps)
 // Decode of 256 sequences of 0 to 2047 keys behind 16384 shared ones, 32 heads:
-// 1.15 GB in 204 to 210 us, 5.5 to 5.7 TB/s, the shared keys on the wide kernel
+// 1.15 GB in 198 to 203 us, 5.7 to 5.8 TB/s, the shared keys on the wide kernel
 // beside it and the joining included. Taking the items out of tiles of 128 query
 // rows took that call from 473 to 305 us, the two halves from 271 to 242.
 // This kernel's own reading goes at the measured copy rate (6.8 TB/s in 171 us).
@@ -1264,6 +1264,10 @@ constexpr int kAnThreads = 512, kAnHalf = 256;   // of a half's two warpgroups t
 constexpr int kAnRegsIo = 80, kAnRegsSoftmax = 176;
 static_assert(kAnRegsIo + kAnRegsSoftmax <= 2 * 128, "the launch's registers");
 constexpr int kAnQueue = 4;               // items taken ahead
+// Keys per TMA box: a sequence's last block brings no more of them than it must. Decode of 256 sequences of 0 to 2047 keys
+// of their own 205 us with boxes of 128, 201 with 32, 202 with 64, 206 with 16; of 64 of 1000 each, whose last block is
+// nearly full, 55.6, 56.9, 56.3 and 58.0.
+constexpr int kAnBox = 32;
 
 template <int D>
 struct AnShape {
@@ -1298,7 +1302,7 @@ struct AnCtx {
     int np;
 };
 
-// An item's softmax and results for NR = 16 or 32 rows; false: a wait gave up.
+// An item's softmax and results for NR = 4, 8, 16 or 32 rows (of the 16 or 32 of the products); false: a wait gave up.
 template <int D, int NR>
 __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
     using Sh = AnShape<D>;
@@ -1332,7 +1336,9 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
     auto take_o = [&]() {                                // the last block's product onto the running sums
         uint32_t x[NR];
         if constexpr (NR == 32) tmem_ld32(c.tmem + 64 + lane_off, x);
-        else tmem_ld16(c.tmem + 64 + lane_off, x);
+        else if constexpr (NR == 16) tmem_ld16(c.tmem + 64 + lane_off, x);
+        else if constexpr (NR == 8) tmem_ld8(c.tmem + 64 + lane_off, x);
+        else tmem_ld4(c.tmem + 64 + lane_off, x);
         tmem_wait_ld();
         if (moved_prev) {
 #pragma unroll
@@ -1348,7 +1354,9 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
         tc_fence_after();
         uint32_t v[NR];
         if constexpr (NR == 32) tmem_ld32(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
-        else tmem_ld16(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
+        else if constexpr (NR == 16) tmem_ld16(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
+        else if constexpr (NR == 8) tmem_ld8(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
+        else tmem_ld4(c.tmem + 32 * (c.blocks & 1) + lane_off, v);
         tmem_wait_ld();
         bool own;
         const int key0 = at_block(w, j, own), key = key0 + tid;
@@ -1425,7 +1433,8 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
                 l[n] = keep + __shfl_xor_sync(0xffffffffu, give, off);
             }
         }
-        if (NR == 16) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+#pragma unroll
+        for (int off = NR; off < 32; off *= 2) l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
         float x[4];
         if (!exchange(l[0], x)) return false;
         l_lane = (x[0] + x[1]) + (x[2] + x[3]);
@@ -1687,17 +1696,23 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
                 publish(0, idx, w);
             }
             for (int i = 0; ok && idx >= 0; ++i) {
-                const int grp = w.b * a.hkv_s + w.kvh;
+                const int grp = w.b * a.hkv_s + w.kvh, kend = at_kend(a, w);
                 auto load = [&](int j, bool v) {
                     bool own;
                     const int key0 = at_block(w, j, own);
                     const CUtensorMap* m = own ? (v ? &a.tv[w.r] : &a.tk[w.r]) : (v ? &a.pv[w.r] : &a.pk[w.r]);
                     const int sl = it % R;
                     if (!(ok = mbar_wait(&kv_empty[sl], ((it / R) & 1) ^ 1, abort_flag, a.status))) return;
-                    mbar_arrive_expect_tx(&kv_full[sl], Sh::KB);
+                    // the rows behind the last box are not read: their scores are masked, and the products with V end with
+                    // the last 16 keys in use
+                    const int boxes = (min(kAtK, (own ? kend : a.prefix_len) - key0) + kAnBox - 1) / kAnBox;
+                    mbar_arrive_expect_tx(&kv_full[sl], boxes * kAnBox * D * 2);
+#pragma unroll 1
+                    for (int i = 0; i < boxes; ++i)
 #pragma unroll
-                    for (int kb = 0; kb < Sh::NKB; ++kb)
-                        tma_load_3d_keep(ring + sl * Sh::KB + kb * (kAtK * 128), m, kb * 64, key0, own ? grp : w.kvh, &kv_full[sl]);
+                        for (int kb = 0; kb < Sh::NKB; ++kb)
+                            tma_load_3d_keep(ring + sl * Sh::KB + kb * (kAtK * 128) + i * (kAnBox * 128), m, kb * 64,
+                                             key0 + i * kAnBox, own ? grp : w.kvh, &kv_full[sl]);
                     ++it;
                 };
                 if (w.nb) {
@@ -1793,7 +1808,13 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
         AtWork w;
         for (int i = 0; ok; ++i) {
             if (!(ok = item(i, w, more)) || !more) break;
-            ok = w.ntok * a.G <= 16 ? an_item<D, 16>(c, w) : an_item<D, 32>(c, w);
+            const int rows = w.ntok * a.G;
+            // The work on a block goes by the rows: 64 sequences of 3 tokens, 12 rows, over 600 keys take 47 us as 16 and 56
+            // as 32; 512 single tokens of 4 rows over 200 keys 90 as 4, 94 as 8 and 102 as 16.
+            ok = rows <= 4    ? an_item<D, 4>(c, w)
+                 : rows <= 8  ? an_item<D, 8>(c, w)
+                 : rows <= 16 ? an_item<D, 16>(c, w)
+                              : an_item<D, 32>(c, w);
         }
     }
     tc_fence_before();
@@ -1992,16 +2013,18 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
     const int64_t D = p.d;
     cudaError_t e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, a.tpt, &a.tq);
     if (e == cudaSuccess) e = attn_map(p.q, D, p.hq_s, (int64_t)p.N * p.T, D, p.hq_s * D, G, kAtNarrow / G, &a.tqn);
-    for (int r = 0; r < p.N && e == cudaSuccess; ++r) {
-        a.v[r] = static_cast<const bf16*>(p.vc[r]);
-        const int64_t groups = (int64_t)p.max_batch * p.hkv_s, rows = p.max_kv;
-        e = attn_map(p.kc[r], D, rows, groups, D, rows * D, kAtK, 1, &a.tk[r]);
-        if (e == cudaSuccess) e = attn_map(p.vc[r], D, rows, groups, D, rows * D, kAtK, 1, &a.tv[r]);
-        if (p.prefix_len && e == cudaSuccess) {
-            e = attn_map(p.pk[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, kAtK, 1, &a.pk[r]);
-            if (e == cudaSuccess) e = attn_map(p.pv[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, kAtK, 1, &a.pv[r]);
+    auto kv_maps = [&](int box) {                        // of both kernels, one after the other
+        for (int r = 0; r < p.N && e == cudaSuccess; ++r) {
+            a.v[r] = static_cast<const bf16*>(p.vc[r]);
+            const int64_t groups = (int64_t)p.max_batch * p.hkv_s, rows = p.max_kv;
+            e = attn_map(p.kc[r], D, rows, groups, D, rows * D, box, 1, &a.tk[r]);
+            if (e == cudaSuccess) e = attn_map(p.vc[r], D, rows, groups, D, rows * D, box, 1, &a.tv[r]);
+            if (p.prefix_len && e == cudaSuccess) {
+                e = attn_map(p.pk[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, box, 1, &a.pk[r]);
+                if (e == cudaSuccess) e = attn_map(p.pv[r], D, p.prefix_len, p.hkv_s, D, p.prefix_rows * D, box, 1, &a.pv[r]);
+            }
         }
-    }
+    };
     if (e != cudaSuccess) return e;
     const bool d128 = p.d == 128;
     void* args[] = {&a};
@@ -2010,14 +2033,16 @@ cudaError_t launch_attn_ragged(const RaggedAttnParams& p, cudaStream_t s) {
         const void* fn = d128 ? reinterpret_cast<const void*>(attn_items_kernel<128>)
                               : reinterpret_cast<const void*>(attn_items_kernel<64>);
         const int smem = d128 ? AtShape<128>::SMEM : AtShape<64>::SMEM;
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        kv_maps(kAtK);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kAtThreads);
         if (e != cudaSuccess) return e;
     }
     const void* fn = d128 ? reinterpret_cast<const void*>(attn_narrow_kernel<128>)
                           : reinterpret_cast<const void*>(attn_narrow_kernel<64>);
     const int smem = 2 * (d128 ? AnShape<128>::SMEM : AnShape<64>::SMEM) + (int)sizeof(AnFew);
-    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    kv_maps(kAnBox);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kAnThreads);
     if (e != cudaSuccess) return e;
     RaggedAttnParams c = p;

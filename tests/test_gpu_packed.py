@@ -70,6 +70,12 @@ CASES = {
     "few_rows_several_tokens_prefix": (L(8, 2, 128, 2), [2, 0, 1, 0, 4], [500, 3, 0, 9, 1126], 257, {}),
     "few_rows_group8_parts": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 0, {}),
     "few_rows_group8_parts_prefix": (L(8, 1, 64, 1), [1, 0, 3], [9000, 5, 3100], 5000, {}),
+    # every number of rows that an item of few rows can have, beside one another; the last blocks end around TMA boxes
+    "rows_of_few_rows_group1": (L(2, 2, 64, 1), list(range(1, 33)) + [3] * 12,
+                                [(i * 31 + 1) % 270 for i in range(44)], 0, {}),
+    "rows_of_few_rows_group3": (L(6, 2, 128, 2), [1, 2, 3, 4, 5, 6, 7, 8, 9, 10] + [1] * 50,
+                                [95, 31, 29, 124, 123, 122, 250, 0, 64, 7] + [16 * i + (i % 3) for i in range(50)], 0, {}),
+    "rows_of_few_rows_prefix_edges": (L(4, 1, 128, 1), [1] * 3, [30, 31, 32], 161, {}),
     "parts_and_a_rest": (L(32, 32, 64, 1), [512, 3], [8000, 100], 0, {}),
     "many_sequences": (QWEN, [1] * 1100, [(37 * i) % 150 for i in range(1100)], 0, {}),
     "many_sequences_prefix": (L(4, 1, 64, 1), [i % 3 for i in range(1300)], [(11 * i) % 40 for i in range(1300)], 70, {}),
