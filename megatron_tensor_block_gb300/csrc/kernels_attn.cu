@@ -1588,7 +1588,9 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* s_poison = reinterpret_cast<volatile int*>(tmem_slot + 2);   // [2]
     float* wmax = reinterpret_cast<float*>(head + Sh::HEAD - 4 * kAtNarrow * 4);
-    static_assert((2 * R + 9 + 2 * kAnQueue + 1) * 8 + (kAnQueue + 4) * 4 <= Sh::HEAD - 4 * kAtNarrow * 4, "the head's words");
+    int4* entry = reinterpret_cast<int4*>(wmax) - 2 * kAnQueue;      // [kAnQueue][2]: the queue's items as they are listed
+    static_assert((2 * R + 9 + 2 * kAnQueue + 1) * 8 + (kAnQueue + 4) * 4 <= Sh::HEAD - 4 * kAtNarrow * 4 - 32 * kAnQueue,
+                  "the head's words");
 
     const int tid = threadIdx.x % kAnHalf, warp = uniform(tid >> 5), lane = tid & 31;
     // Behind the wide kernel the lists are there: it lets this one start only after its own wait. This kernel waits for
@@ -1646,24 +1648,17 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
         total = (n_items - n_wide) * heads;
     }
     if (*abort_flag) total = 0;
-    auto decode = [&](int idx, AtWork& w) {
-        const int e = idx / heads;
-        int4 x, y;
-        if (a.few) an_few_item(a, few, e, x, y);
-        else at_load(a, n_wide + e, x, y);
-        at_fill(a, x, y, idx - e * heads, w);
-    };
-
     // the i-th item of this CTA, -1 when there are no more
     auto item = [&](int i, AtWork& w, bool& more) {
         const int s = i % kAnQueue;
         bool ok = __all_sync(0xffffffffu, mbar_wait(&item_full[s], (i / kAnQueue) & 1, abort_flag, a.status));
         if (!ok) return false;
         const int idx = *reinterpret_cast<volatile int*>(&queue[s]);
+        const int4 x = entry[2 * s], y = entry[2 * s + 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[s]);
         more = idx >= 0;
-        if (more) decode(idx, w);
+        if (more) at_fill(a, x, y, idx % heads, w);
         return true;
     };
 
@@ -1684,10 +1679,18 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
             auto publish = [&](int i, int& idx, AtWork& w) {
                 const int s = i % kAnQueue;
                 if (idx >= total) idx = -1;
+                const int e = idx / heads;
+                int4 x = {}, y = {};
+                if (idx >= 0) {
+                    if (a.few) an_few_item(a, few, e, x, y);
+                    else at_load(a, n_wide + e, x, y);
+                }
                 if (!(ok = mbar_wait(&item_empty[s], ((i / kAnQueue) & 1) ^ 1, abort_flag, a.status))) return;
                 *reinterpret_cast<volatile int*>(&queue[s]) = idx;
+                entry[2 * s] = x;
+                entry[2 * s + 1] = y;
                 mbar_arrive(&item_full[s]);
-                if (idx >= 0) decode(idx, w);
+                if (idx >= 0) at_fill(a, x, y, idx - e * heads, w);
             };
             AtWork w, wn;
             int idx = -1, in = 0;
