@@ -72,7 +72,10 @@ __device__ __forceinline__ void part_split(int nb, int target, bool rest, int& p
 // one). Parts cost their partial results' way to memory and back.
 //
 // Integer atomics place the items of a length and the rows of partial results:
-// their order decides where a partial lies, not what is added to what.
+// their order decides who does an item when and where a partial lies, not what
+// is added to what. Which of several items of a length belong to the last round
+// must not depend on it, since a cut item is summed up in another order: those
+// are ranked by warp and, within one, in the order in which it comes to them.
 //
 // Bound by latency, 3 to 5 us of it: instructions that run once come from
 // memory, and what every warp computes for itself takes its turn. So the three
@@ -111,16 +114,20 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
     __shared__ int s_tiles[kPlanWarps], s_longest[kPlanWarps];       // wide tiles
     __shared__ int s_few[kPlanWarps], s_few_longest[kPlanWarps];     // narrow tiles
     __shared__ int s_warp[kPlanWarps];
-    __shared__ int s_rows, s_chunks;
+    __shared__ __align__(16) int s_ties[kPlanWarps * kAtBuckets];    // per warp: wide items of each length
+    __shared__ int s_rows, s_chunks, s_edge, s_edge_at;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr unsigned kAll = 0xffffffffu;
     pdl_trigger();
     reinterpret_cast<int4*>(s_hist)[tid] = make_int4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kPlanWarps * kAtBuckets / 4; i += kPlanThreads) reinterpret_cast<int4*>(s_ties)[i + tid] = make_int4(0, 0, 0, 0);
     const int G = (unsigned)p.hq_s / (unsigned)p.hkv_s, per = 2 * ((unsigned)kAtM / (unsigned)G);      // tokens per item
     const int heads = p.N * p.hkv_s;
     if (tid == 0) {
         s_rows = 2 * p.T * heads * G;                                // behind the places of part 0
         s_chunks = 0;
+        s_edge = s_edge_at = 0;
     }
     const int n_prefix = (p.prefix_len + kAtK - 1) / kAtK;           // prefix blocks
     const int in_item = p.shared ? 0 : n_prefix;
@@ -150,6 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
     int target_w = 0, target_n = 0;                                  // the longest parts
     bool rests = false;                                              // wide items: of that length but the last
     int last_from = INT_MAX, last_parts = 1;                         // a last round's items and their parts
+    int edge = -1, edge_at = 0;                                      // the bucket in which it begins, the warp's next place there
     int n_wide = 0, n_items = 0;
     const int own = p.shared ? AT_OWN : AT_OWN | AT_PREFIX;
 
@@ -216,7 +224,15 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
                 if (parts > 1) e0 = atomicAdd(full, parts - 1);
                 e1 = atomicAdd(rest, 1);
             }
-            if (pass == 1) continue;
+            if (pass == 1) {                                         // (nothing else is cut where a last round is)
+                if (last_parts > 1 && live && !nar) atomicAdd(&s_ties[warp * kAtBuckets + (int)(rest - s_hist)], 1);
+                continue;
+            }
+            if (edge >= 0) {
+                const unsigned tied = __ballot_sync(kAll, live && !nar && rest - s_hist == edge);
+                if (tied >> lane & 1) e1 = edge_at + __popc(tied & ((1u << lane) - 1u));
+                edge_at += __popc(tied);
+            }
 
             int entries = live ? parts : 0;
             if (live && parts == 1 && !nar && e1 >= last_from) {
@@ -363,8 +379,18 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
             n_wide = sorted + more;
             n_items = __reduce_add_sync(kAll, lane < kPlanWarps ? of_warp : 0) + more;
             int e = __reduce_add_sync(kAll, lane < warp ? of_warp : 0) + incl - mine + (warp >= kPlanWarps / 2 ? more : 0);
-            reinterpret_cast<int4*>(s_hist)[tid] = make_int4(e, e + x.x, e + x.x + x.y, e + x.x + x.y + x.z);
+            const int4 begin = make_int4(e, e + x.x, e + x.x + x.y, e + x.x + x.y + x.z);
+            reinterpret_cast<int4*>(s_hist)[tid] = begin;
+            if (warp < kPlanWarps / 2 && e <= last_from && last_from < e + mine) {
+                const int i = (last_from >= begin.y) + (last_from >= begin.z) + (last_from >= begin.w);
+                s_edge = 4 * tid + i;
+                s_edge_at = i == 0 ? begin.x : i == 1 ? begin.y : i == 2 ? begin.z : begin.w;
+            }
             __syncthreads();
+            if (last_parts > 1) {
+                edge = s_edge;
+                edge_at = s_edge_at + __reduce_add_sync(kAll, lane < warp ? s_ties[lane * kAtBuckets + edge] : 0);
+            }
         }
     }
     __syncthreads();
