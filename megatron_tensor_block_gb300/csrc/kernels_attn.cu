@@ -1861,7 +1861,10 @@ __global__ void __launch_bounds__(kAnThreads, 1) attn_narrow_kernel(const __grid
 }
 
 // One warp per output row: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i
-// over the row's own parts, then its prefix tile's, in their order. Bound by
+// over the row's own parts, then its prefix tile's, in their order. A part
+// whose scores are all NaN has m = -inf as one that sees no key has, but a NaN
+// in l; no part is left out of the sums, so that its NaN, or one that a weight
+// of 0 meets in O, stays. Bound by
 // the latency of its loads and by its own start, since no CTA of it fits beside
 // those before it: lane i takes part i's m and l, and the first four parts'
 // outputs are under way before these are there. Four CTAs per SM: decode of 64
@@ -1939,13 +1942,13 @@ __global__ void __launch_bounds__(256, kAtJoinCtas) attn_combine_kernel(const Ra
             if ((i0 & 31) == 0) {                    // weights of the next 32 parts
                 if (i0) ml = i0 + lane < n ? p.part_ml[at(i0 + lane)] : make_float2(-INFINITY, 0.f);
                 f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-                l += warp_sum(f == 0.f ? 0.f : f * ml.y);
+                l += warp_sum(f * ml.y);
             }
             if (i0) load(i0);
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 const float w = __shfl_sync(kAll, f, (i0 + i) & 31);
-                if (i0 + i < n && w != 0.f)
+                if (i0 + i < n)
 #pragma unroll
                     for (int k = 0; k < E; ++k) o[k] = fmaf(w, x[i][k], o[k]);
             }
