@@ -505,6 +505,8 @@ tp_status tp_logits_process(tp_plan_t plan, const float* logits, int32_t T, cons
  * (workspace_bytes or more); calls on one workspace must not overlap on the
  * GPU. Scores, softmax sums and outputs accumulate in float32; the weights w_j
  * are rounded to bf16 for the product with v, and out once from float32.
+ * Infinities and NaN that a row sees go the way of this formula (a row whose
+ * scores are all -inf is NaN); those that it does not see never reach it.
  * Every wait on the device is bounded; one that runs out records
  * TP_ERR_TIMEOUT, and out is then undefined.
  * Results are deterministic. No allocation and no synchronisation: the call

@@ -3,7 +3,9 @@
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
 //
-// in one pass over the keys with a running m and sum, in up to four launches:
+// (0 / 0 where every s_j is -inf: such a row is NaN, and zeros are written only
+// to rows whose position lies outside the cache) in one pass over the keys with
+// a running m and sum, in up to four launches:
 //   attn_plan_kernel     one CTA turns the offsets and lengths into a list of
 //                        items, longest first, and cuts long items into parts
 //                        where the batch has too few of them for the machine
@@ -1162,7 +1164,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) attn_items_kernel(const __grid_
                     ml = stat[t * kAtM + m];
                     poison |= s_poison[k % kAtQueue];
                 }
-                const bool zero = !n || (!part && (pos < 0 || pos >= a.max_kv || ml.y == 0.f));
+                const bool zero = !n || (!part && (pos < 0 || pos >= a.max_kv));
                 const float f = zero ? 0.f : part ? 1.f : 1.f / ml.y;
                 if (part && live) a.part_ml[prow + tok * a.G + g] = ml;
                 const unsigned store = __ballot_sync(0xffffffffu, live) >> (lane & 28);
@@ -1492,8 +1494,8 @@ __device__ __forceinline__ bool an_item(AnCtx<D>& c, const AtWork& w) {
         return true;
     }
     const int64_t pos = (int64_t)w.qpos + lane / a.G;    // lane n: row n's
-    const float inv = pos >= 0 && pos < a.max_kv && l_lane != 0.f ? 1.f / l_lane : 0.f;
-    const unsigned zero = __ballot_sync(0xffffffffu, pos < 0 || pos >= a.max_kv || l_lane == 0.f);
+    const float inv = pos >= 0 && pos < a.max_kv ? 1.f / l_lane : 0.f;
+    const unsigned zero = __ballot_sync(0xffffffffu, pos < 0 || pos >= a.max_kv);
     bf16* dst = a.out + (((int64_t)w.r * a.T + w.t0) * a.hq_s + w.kvh * a.G) * D + tid;
     int g = 0;
 #pragma unroll
@@ -1953,7 +1955,7 @@ __global__ void __launch_bounds__(256, kAtJoinCtas) attn_combine_kernel(const Ra
                     for (int k = 0; k < E; ++k) o[k] = fmaf(w, x[i][k], o[k]);
             }
         }
-        const bool in = pos >= 0 && pos < p.max_kv && l != 0.f;
+        const bool in = pos >= 0 && pos < p.max_kv;
         const float inv = 1.f / l;
         uint32_t y[E / 2];
 #pragma unroll

@@ -117,3 +117,36 @@ def test_a_value_of_nan_reaches_a_row_that_hardly_weighs_it(gpu_lib, form):
     rows = slice(0, b.used) if prefix else slice(int(b.cu[s]), int(b.cu[s + 1]))
     nan[0, rows, :lay.group, 7] = True
     compare(b, run(gpu_lib, b, spoil), nan)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+def test_a_row_whose_scores_are_all_minus_infinity_is_nan(gpu_lib, form):
+    # the weights' sum is 0 then, and 0 / 0 no number; zeros would pass for a result
+    lay, new, cached, prefix = FORMS[form]
+    b = K.Batch(lay, new, cached, prefix=prefix, seed=36)
+    b.k[..., 0] = np.where(np.isnan(b.k[..., 0]), np.nan, -1.0)
+    b.pk[..., 0] = -1.0
+    t, r, h = b.used - 1, lay.tp - 1, lay.hq - 1
+
+    def spoil(d):
+        d.q[r, t, h, 0] = float("inf")
+        d.q[0, 0, 0, 0] = float("inf")
+    nan = np.zeros((lay.tp, b.used, lay.hq, lay.d), bool)
+    nan[r, t, h] = nan[0, 0, 0] = True
+    compare(b, run(gpu_lib, b, spoil), nan)
+
+
+@pytest.mark.parametrize("form", ["whole_wide", "wide_parts", "narrow_parts", "few_rows", "few_rows_prefix", "shared_prefix"])
+def test_keys_with_scores_of_minus_infinity_weigh_nothing(gpu_lib, form):
+    # the first 256 keys of the longest cache, but not its last; the reference's have a score of -2^11 / sqrt(d), whose
+    # weight is 0 beside the others' in every one of the bound's figures
+    lay, new, cached, prefix = FORMS[form]
+    b = K.Batch(lay, new, cached, prefix=prefix, seed=37)
+    b.q[..., 0] = 1.0
+    s = max(range(b.B), key=lambda i: cached[i])
+    n = min(256, cached[s])
+    b.k[0, s, 0, :n, 0] = -2048.0
+
+    def spoil(d):
+        d.k[0][s, 0, :n, 0] = -float("inf")
+    compare(b, run(gpu_lib, b, spoil), np.zeros((lay.tp, b.used, lay.hq, lay.d), bool))
