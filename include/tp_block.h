@@ -447,7 +447,7 @@ typedef struct tp_logit_controls {
     const int32_t* tokens;      /* the rows' token histories back to back: row t's at
                                  * cu_tokens[t]..cu_tokens[t+1]-1, prompt first; ids outside
                                  * 0..org_vocab-1 are passed over */
-    const int32_t* cu_tokens;   /* [T + 1] */
+    const int32_t* cu_tokens;   /* [T + 1], values in 0..n_tokens */
     const int32_t* n_prompt;    /* [T]: leading prompt tokens of each history (NULL: none); the
                                  * others are generated ones */
     const float* repetition;    /* [T]: factor r of tokens in the history (NULL: 1) */
@@ -455,13 +455,15 @@ typedef struct tp_logit_controls {
     const float* frequency;     /* [T]: subtracted per occurrence among the generated (NULL: 0) */
     const int32_t* bias_ids;    /* the rows' biased tokens back to back */
     const float* bias_values;   /* added to them; of a token listed twice the last counts */
-    const int32_t* cu_bias;     /* [T + 1] */
+    const int32_t* cu_bias;     /* [T + 1], values in 0..n_bias */
     const uint32_t* mask;       /* [mask_rows][ceil(org_vocab / 32)]: bit v % 32 of word v / 32 is
                                  * 1 where token v is allowed */
     const int32_t* mask_row;    /* [T]: the mask row of each row, -1 for none (NULL: row t); a row
                                  * outside -1..mask_rows-1 counts as none */
     int32_t mask_rows;
     int32_t reserved0;          /* must be 0 */
+    int64_t n_tokens;           /* entries of tokens; at least 1 where tokens is not NULL */
+    int64_t n_bias;             /* entries of bias_ids and of bias_values, likewise */
 } tp_logit_controls;
 
 /* Applies a batch's penalties, biases and grammar masks to its logits, as
@@ -473,12 +475,14 @@ typedef struct tp_logit_controls {
  *   y = -inf                          for tokens the row's mask forbids.
  * out is float32 [T, org_vocab]; out may be the same buffer as logits (only
  * the entries that a control changes are then written), but must not overlap
- * it otherwise. Both 4-byte aligned (16 bytes are faster). A cu that decreases
- * gives an empty list for that row. Deterministic; one launch, no allocation,
- * no synchronisation.
+ * it otherwise. Both 4-byte aligned (16 bytes are faster). A row whose two
+ * values of a cu decrease, begin below 0 or end behind the list has an empty
+ * list: nothing outside the lists is read. Deterministic; one launch, no
+ * allocation, no synchronisation.
  * Errors: TP_ERR_NULL (also a list without its cu or its values),
  * TP_ERR_INVALID_ARG (no head in the plan, overlap, reserved0), TP_ERR_SHAPE
- * (T < 1, mask_rows < 0, mask without mask_row and mask_rows < T),
+ * (T < 1, mask_rows < 0, mask without mask_row and mask_rows < T, a list
+ * with n_tokens or n_bias < 1),
  * TP_ERR_ALIGN, TP_ERR_UNSUPPORTED, TP_ERR_CUDA. */
 tp_status tp_logits_process(tp_plan_t plan, const float* logits, int32_t T, const tp_logit_controls* c,
                             float* out, void* stream);

@@ -74,7 +74,7 @@ class tp_kv_set(C.Structure):
 class tp_logit_controls(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in (
         "tokens", "cu_tokens", "n_prompt", "repetition", "presence", "frequency", "bias_ids", "bias_values", "cu_bias",
-        "mask", "mask_row")] + [("mask_rows", C.c_int32), ("reserved0", C.c_int32)]
+        "mask", "mask_row")] + [("mask_rows", C.c_int32), ("reserved0", C.c_int32), ("n_tokens", C.c_int64), ("n_bias", C.c_int64)]
 
 
 class TpError(RuntimeError):
@@ -411,20 +411,25 @@ def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, 
 
 def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=None, n_prompt=None, repetition=None,
                       presence=None, frequency=None, bias_ids=None, bias_values=None, cu_bias=None, mask=None,
-                      mask_row=None, mask_rows: int | None = None, stream=None) -> None:
+                      mask_row=None, mask_rows: int | None = None, stream=None, n_tokens: int | None = None,
+                      n_bias: int | None = None) -> None:
     """Penalties, biases and grammar masks of ``logits`` (float32 ``[T, org_vocab]``) into ``out`` (which may be
-    ``logits``). ``mask`` is int32 ``[mask_rows, ceil(org_vocab / 32)]``, bit 1 = allowed; ``mask_rows`` is taken from a
-    tensor's size where not given."""
+    ``logits``). ``mask`` is int32 ``[mask_rows, ceil(org_vocab / 32)]``, bit 1 = allowed; ``mask_rows`` and the lists'
+    lengths ``n_tokens`` and ``n_bias`` are taken from a tensor's size where not given."""
     words, dev = (plan.org_vocab + 31) // 32, _Torch.device()
+    if n_tokens is None:
+        n_tokens = 0 if tokens is None or isinstance(tokens, int) else tokens.numel()
+    if n_bias is None:
+        n_bias = 0 if bias_ids is None or isinstance(bias_ids, int) else bias_ids.numel()
     if mask_rows is None:
         mask_rows = 0 if mask is None or isinstance(mask, int) else mask.numel() // max(words, 1)
     c = tp_logit_controls(
-        _checked(tokens, "tokens", _Torch.i32, 0, dev), _checked(cu_tokens, "cu_tokens", _Torch.i32, T + 1, dev),
+        _checked(tokens, "tokens", _Torch.i32, n_tokens, dev), _checked(cu_tokens, "cu_tokens", _Torch.i32, T + 1, dev),
         _checked(n_prompt, "n_prompt", _Torch.i32, T, dev), _checked(repetition, "repetition", _Torch.f32, T, dev),
         _checked(presence, "presence", _Torch.f32, T, dev), _checked(frequency, "frequency", _Torch.f32, T, dev),
-        _checked(bias_ids, "bias_ids", _Torch.i32, 0, dev), _checked(bias_values, "bias_values", _Torch.f32, 0, dev),
+        _checked(bias_ids, "bias_ids", _Torch.i32, n_bias, dev), _checked(bias_values, "bias_values", _Torch.f32, n_bias, dev),
         _checked(cu_bias, "cu_bias", _Torch.i32, T + 1, dev), _checked(mask, "mask", _Torch.i32, mask_rows * words, dev),
-        _checked(mask_row, "mask_row", _Torch.i32, T, dev), mask_rows, 0)
+        _checked(mask_row, "mask_row", _Torch.i32, T, dev), mask_rows, 0, n_tokens, n_bias)
     _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", _Torch.f32, T * plan.org_vocab, dev), T, C.byref(c),
                                     _checked(out, "out", _Torch.f32, T * plan.org_vocab, dev), _Torch.stream(stream, dev)))
 

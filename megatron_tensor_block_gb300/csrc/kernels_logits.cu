@@ -67,20 +67,21 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         for (int i = 0; i < AHEAD; ++i) load(group(i), x[i]);
 
     int h0 = 0, hn = 0, b0 = 0, bn = 0, np = 0;
+    auto list = [&](const int* cu, int64_t n, int& begin) {  // the row's entries, none where they do not lie in the list
+        begin = cu[t];
+        const int end = cu[t + 1];
+        return begin >= 0 && end > begin && end <= n ? end - begin : 0;
+    };
     float rep = 1.f, pres = 0.f, freq = 0.f;
     if (a.tokens) {
-        h0 = a.cu_tokens[t];
-        hn = max(a.cu_tokens[t + 1] - h0, 0);
+        hn = list(a.cu_tokens, a.n_tokens, h0);
         np = a.n_prompt ? a.n_prompt[t] : 0;
         if (a.repetition) rep = a.repetition[t];
         if (a.presence) pres = a.presence[t];
         if (a.frequency) freq = a.frequency[t];
         if (rep == 1.f && pres == 0.f && freq == 0.f) hn = 0;
     }
-    if (a.bias_ids) {
-        b0 = a.cu_bias[t];
-        bn = max(a.cu_bias[t + 1] - b0, 0);
-    }
+    if (a.bias_ids) bn = list(a.cu_bias, a.n_bias, b0);
     const uint32_t* mask = nullptr;
     if (a.mask) {
         const int m = a.mask_row ? a.mask_row[t] : t;

@@ -1357,6 +1357,9 @@ extern "C" tp_status tp_logits_process(tp_plan_t plan, const float* logits, int3
                        c->bias_ids, c->bias_values, c->cu_bias, c->mask, c->mask_row};
     for (const void* q : p)
         if (reinterpret_cast<uintptr_t>(q) & 3) return fail(TP_ERR_ALIGN, "%s: pointers must be 4-byte aligned", who);
+    if ((c->tokens && c->n_tokens < 1) || (c->bias_ids && c->n_bias < 1))
+        return fail(TP_ERR_SHAPE, "%s: a list with n_tokens=%lld or n_bias=%lld entries", who, (long long)c->n_tokens,
+                    (long long)c->n_bias);
     const uintptr_t bytes = (uintptr_t)T * V * 4;
     const uintptr_t xa = reinterpret_cast<uintptr_t>(logits), ya = reinterpret_cast<uintptr_t>(out);
     if (xa != ya && xa < ya + bytes && ya < xa + bytes)
@@ -1382,6 +1385,8 @@ extern "C" tp_status tp_logits_process(tp_plan_t plan, const float* logits, int3
     a.mask_row = c->mask_row;
     a.mask_rows = c->mask_rows;
     a.mask_words = (int)((V + 31) / 32);
+    a.n_tokens = c->n_tokens;
+    a.n_bias = c->n_bias;
     TP_CUDA(launch_logits(a, static_cast<cudaStream_t>(stream)), who);
     return ok();
 }
