@@ -415,7 +415,8 @@ def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=No
                       n_bias: int | None = None) -> None:
     """Penalties, biases and grammar masks of ``logits`` (float32 ``[T, org_vocab]``) into ``out`` (which may be
     ``logits``). ``mask`` is int32 ``[mask_rows, ceil(org_vocab / 32)]``, bit 1 = allowed; ``mask_rows`` and the lists'
-    lengths ``n_tokens`` and ``n_bias`` are taken from a tensor's size where not given."""
+    lengths ``n_tokens`` and ``n_bias`` are taken from a tensor's size where not given. A tensor without elements leaves its
+    control out."""
     words, dev = (plan.org_vocab + 31) // 32, _Torch.device()
     if n_tokens is None:
         n_tokens = 0 if tokens is None or isinstance(tokens, int) else tokens.numel()
@@ -430,6 +431,12 @@ def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=No
         _checked(bias_ids, "bias_ids", _Torch.i32, n_bias, dev), _checked(bias_values, "bias_values", _Torch.f32, n_bias, dev),
         _checked(cu_bias, "cu_bias", _Torch.i32, T + 1, dev), _checked(mask, "mask", _Torch.i32, mask_rows * words, dev),
         _checked(mask_row, "mask_row", _Torch.i32, T, dev), mask_rows, 0, n_tokens, n_bias)
+    if n_tokens == 0 and tokens is not None and not isinstance(tokens, int):
+        c.tokens = c.cu_tokens = c.n_prompt = c.repetition = c.presence = c.frequency = None
+    if n_bias == 0 and bias_ids is not None and not isinstance(bias_ids, int):
+        c.bias_ids = c.bias_values = c.cu_bias = None
+    if mask_rows == 0 and mask is not None and not isinstance(mask, int) and mask_row is not None:
+        c.mask = c.mask_row = None
     _check(load().tp_logits_process(plan.handle, _checked(logits, "logits", _Torch.f32, T * plan.org_vocab, dev), T, C.byref(c),
                                     _checked(out, "out", _Torch.f32, T * plan.org_vocab, dev), _Torch.stream(stream, dev)))
 

@@ -66,3 +66,31 @@ def test_fewer_values_than_biased_tokens_are_refused(gpu_lib):
     x = torch.from_numpy(c.x).cuda()
     with pytest.raises(ValueError, match="bias_values"):
         gpu_lib.tp_logits_process(plan_of(gpu_lib, 500), x, 2, torch.empty_like(x), **kw)
+
+
+@pytest.mark.parametrize("which", ["tokens", "bias", "both"])
+def test_a_batch_without_any_entries(gpu_lib, which):
+    # the first step of requests without a history: empty tensors, whose address is NULL
+    import torch
+    c = Case(T=3, V=700, seed=75, masks=3)
+    if which in ("tokens", "both"):
+        c.hist = [[], [], []]
+        c.n_prompt = np.zeros(3, np.int32)
+    if which in ("bias", "both"):
+        c.bias = [[], [], []]
+    kw = c.args(torch)
+    if which in ("tokens", "both"):
+        kw["tokens"] = torch.empty(0, dtype=torch.int32, device="cuda")
+    if which in ("bias", "both"):
+        kw["bias_ids"] = torch.empty(0, dtype=torch.int32, device="cuda")
+        kw["bias_values"] = torch.empty(0, device="cuda")
+    if which == "both":                          # nor a row with a grammar
+        kw["mask"] = torch.empty(0, 22, dtype=torch.int32, device="cuda")
+        kw["mask_row"] = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+        c.mask = None
+    x = torch.from_numpy(c.x).cuda()
+    out = torch.empty_like(x)
+    gpu_lib.tp_logits_process(plan_of(gpu_lib, 700), x, 3, out, **kw)
+    c.check(out.cpu().numpy())
+    with pytest.raises(TypeError):               # what goes with an empty list is checked all the same
+        gpu_lib.tp_logits_process(plan_of(gpu_lib, 700), x, 3, out, **{**kw, "repetition": kw["repetition"].double()})
