@@ -423,7 +423,9 @@ def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=No
     if n_bias is None:
         n_bias = 0 if bias_ids is None or isinstance(bias_ids, int) else bias_ids.numel()
     if mask_rows is None:
-        mask_rows = 0 if mask is None or isinstance(mask, int) else mask.numel() // max(words, 1)
+        if isinstance(mask, int):
+            raise ValueError("mask: mask_rows is needed where mask is an address")
+        mask_rows = 0 if mask is None else mask.numel() // max(words, 1)
     c = tp_logit_controls(
         _checked(tokens, "tokens", _Torch.i32, n_tokens, dev), _checked(cu_tokens, "cu_tokens", _Torch.i32, T + 1, dev),
         _checked(n_prompt, "n_prompt", _Torch.i32, T, dev), _checked(repetition, "repetition", _Torch.f32, T, dev),

@@ -21,3 +21,10 @@ def test_a_list_without_its_length_is_refused(kw):
     with pytest.raises(tb.TpError) as e:
         tb.tp_logits_process(plan(), A, 2, 2 * A, stream=0, **kw)
     assert e.value.status == B.TP_ERR_SHAPE, str(e.value)
+
+
+@pytest.mark.parametrize("mask_row", [None, A])
+def test_the_address_of_a_mask_needs_its_rows(mask_row):
+    # with 0 rows every mask_row would lie outside, and no grammar apply
+    with pytest.raises(ValueError, match="mask_rows"):
+        tb.tp_logits_process(plan(), A, 2, 2 * A, stream=0, mask=A, mask_row=mask_row)
