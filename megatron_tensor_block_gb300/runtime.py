@@ -172,12 +172,11 @@ class Model:
     def forward_packed(self, x, y, cu, pos, prefix=None, prefix_len=0, prefix_rows=0, stream=None):
         """Runs every layer over a packed batch (rows ``cu[b]..cu[b+1]-1`` of
         ``x`` are sequence b's, at positions ``pos[b]..`` of its cache);
-        ``prefix``: per layer a shared prefix's (k list, v list), or None."""
+        ``prefix``: per layer a shared prefix's (k list, v list), or None.
+        As the workspace, the buffer between the layers is the model's: its
+        calls must not overlap on the GPU."""
         n, cur, B_ = len(self.layers), x, pos.numel()
-        tmp = _torch().empty_like(y) if n > 1 else None
-        if tmp is not None and stream is not None:      # freed on return: not before the kernels on `stream` are done
-            cuda = _torch().cuda
-            tmp.record_stream(cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        tmp = self.tmp[:x.shape[0]] if n > 1 else None
         for i, L in enumerate(self.layers):
             out = y if (n - 1 - i) % 2 == 0 else tmp
             B.tp_block_forward_packed(self.plan, L.shards, (self.caches[i].k, self.caches[i].v), cur, out, cu, pos, B_,

@@ -1,0 +1,74 @@
+"""A packed batch through several layers, on the current and on another
+stream, against the float64 oracle layer by layer."""
+import numpy as np
+import pytest
+
+import synth
+from tests import _oracle_runs as R
+from tests import _packed as K
+from tests import _parity as P
+from tests.test_gpu_packed import BLOCKS, TOL, block_oracle
+
+pytestmark = pytest.mark.gpu
+
+NEW, CACHED = [40, 0, 1, 23], [20, 5, 17, 0]
+
+
+def setup(layers, prefix):
+    import torch
+    from megatron_tensor_block_gb300.runtime import Model
+    w = synth.scaled(BLOCKS["llama_tp2"], n_layers=layers, seed=44)
+    inputs = synth.make_inputs(w, with_head=False)
+    m = Model(inputs)
+    rng = np.random.default_rng(45)
+    up = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.float32)).to("cuda").to(torch.bfloat16)  # noqa: E731
+    per, pre, host = w.n_kv_heads // w.tp, [], []
+    for _ in range(layers):
+        pk, pv = (K.bf16(rng.standard_normal((w.n_kv_heads, prefix, w.head_dim))) for _ in range(2))
+        host.append((pk, pv))
+        pre.append(tuple([up(p[r * per:(r + 1) * per]) for r in range(w.tp)] for p in (pk, pv)))
+    ref = np.asarray(inputs["x"])[:sum(NEW)]
+    for i in range(layers):
+        k0, v0 = (R.full_cache(inputs[n][i], m.max_kv) for n in ("k_cache", "v_cache"))
+        one = dict(inputs, layers=[inputs["layers"][i]])
+        ref, _, _ = block_oracle(one, ref, NEW, CACHED, prefix, *host[i], k0, v0, m.max_kv)
+    return w, inputs, m, pre if prefix else None, ref
+
+
+def batch(inputs):
+    import torch
+    x = torch.from_numpy(np.ascontiguousarray(np.asarray(inputs["x"])[:sum(NEW)])).to("cuda")
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(NEW)]), dtype=torch.int32, device="cuda")
+    return x, cu, torch.tensor(CACHED, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+@pytest.mark.parametrize("layers", [2, 3])
+def test_layers_match_the_oracle(gpu_lib, layers, prefix):
+    import torch
+    w, inputs, m, pre, ref = setup(layers, prefix)
+    x, cu, pos = batch(inputs)
+    y = m.forward_packed(x, torch.empty_like(x), cu, pos, pre, prefix, prefix)
+    assert m.ws.status() == 0
+    assert P.err(y.double().cpu().numpy(), ref) <= TOL
+
+
+@pytest.mark.parametrize("as_address", [False, True])
+def test_layers_on_another_stream_beside_work_of_the_current_one(gpu_lib, as_address):
+    # the current stream still writes a block of the output's size that its owner has given back
+    import torch
+    w, inputs, m, pre, ref = setup(2, 0)
+    x, cu, pos = batch(inputs)
+    y = torch.empty_like(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    big = torch.ones(1 << 28, device="cuda")
+    given_back = torch.empty_like(x)
+    for _ in range(20):
+        big.mul_(1.0)                            # some milliseconds
+    given_back.fill_(float("nan"))
+    del given_back
+    m.forward_packed(x, y, cu, pos, stream=s.cuda_stream if as_address else s)
+    torch.cuda.synchronize()
+    assert m.ws.status() == 0
+    assert P.err(y.double().cpu().numpy(), ref) <= TOL
