@@ -275,7 +275,8 @@ tp_status tp_shard_kv(tp_plan_t plan, const void* k_full, const void* v_full, in
 /* Zeroes the control words (completion counters, status) at the start of a
  * workspace. Call once after allocating a workspace and before its first
  * tp_block_forward; the kernels leave the counters at zero after each
- * call. `bytes` >= tp_plan_info.workspace_bytes. */
+ * call. `bytes` >= tp_plan_info.workspace_bytes; a workspace without the packed
+ * calls' scratch, which lies at the end, serves every other call. */
 tp_status tp_workspace_init(tp_plan_t plan, void* workspace, size_t bytes, void* stream);
 
 /* One tensor-parallel block over all tp logical shards ([MG] How tensor

@@ -68,10 +68,12 @@ struct tp_plan_s {
            off_m_xs = 0, off_m_act = 0, off_m_o = 0, ws_moe_end = 0;
     // prefill buffers (share the data region with the decode and MoE buffers)
     size_t off_p_xn = 0, off_p_q = 0, off_p_ao = 0, off_p_h = 0, off_p_act = 0, off_p_rope = 0, ws_prefill_end = 0;
-    // packed batches: counts and lists after the prefill buffers; the partial results share
-    // the region of the normalised activations, which an attention stage does not need
+    // packed batches: counts and lists at the workspace's end, behind all that the other calls
+    // use; the partial results share the prefill buffers that no attention stage needs
+    // (normalised activations, h, SwiGLU output), or follow where these are smaller
     size_t off_a_ctl = 0, off_a_items = 0, off_a_prefix = 0, off_a_chunks = 0, off_a_ml = 0, off_a_o = 0;
     size_t ws_bytes = 0;
+    size_t ws_base = 0;                 // what every call but the packed ones needs
     size_t ws_decode_end = 0;           // end of the decode buffers (control words included)
     // multi-layer decode (tp_stack_decode): control words, then its own pair buffers
     // at the end of the workspace (no other mode writes them, so no stale epoch matches)
@@ -306,18 +308,12 @@ extern "C" tp_status tp_plan(const tp_model_desc* d, int32_t tp, tp_plan_t* out)
     if (dense && d->dtype == TP_BF16) {
         off = P->ctrl_bytes;
         const int64_t Tm = d->max_tokens, hd = d->head_dim;
-        const AttnSizes as = attn_sizes(d->max_batch, Tm, (int)d->n_heads, (int)d->n_kv_heads, (int)hd);
-        P->off_p_xn = P->off_a_o = take(std::max((size_t)N * Tm * H * 2, as.part_o));   // one bf16 copy per distinct gamma
         P->off_p_q = take((size_t)Tm * d->n_heads * hd * 2);     // [N][T][Hq' d]
         P->off_p_ao = take((size_t)Tm * d->n_heads * hd * 2);
+        P->off_p_rope = take((size_t)d->max_kv * (hd / 2) * 8);  // (cos, sin) per position and pair
+        P->off_p_xn = take((size_t)N * Tm * H * 2);              // one bf16 copy per distinct gamma
         P->off_p_h = take((size_t)Tm * H * 4);
         P->off_p_act = take((size_t)Tm * d->ffn * 2);            // [N][T][F']
-        P->off_p_rope = take((size_t)d->max_kv * (hd / 2) * 8);  // (cos, sin) per position and pair
-        P->off_a_ctl = take(sizeof(AttnCtl));
-        P->off_a_items = take(as.items);
-        P->off_a_prefix = take(as.prefix_groups);
-        P->off_a_chunks = take(as.chunks);
-        P->off_a_ml = take(as.part_ml);
         P->ws_prefill_end = off;
     }
     if (moe) {
@@ -359,6 +355,18 @@ extern "C" tp_status tp_plan(const tp_model_desc* d, int32_t tp, tp_plan_t* out)
         P->off_c_h = take((size_t)MB * H * 8);
         P->off_c_a = take((size_t)N * MB * I.ffn_shard * 8);
         P->off_c_end = off;
+        P->ws_bytes = off;
+    }
+    P->ws_base = P->ws_bytes;
+    if (dense && d->dtype == TP_BF16) {
+        off = P->ws_base;
+        const AttnSizes as = attn_sizes(d->max_batch, d->max_tokens, (int)d->n_heads, (int)d->n_kv_heads, (int)d->head_dim);
+        P->off_a_ctl = take(sizeof(AttnCtl));
+        P->off_a_items = take(as.items);
+        P->off_a_prefix = take(as.prefix_groups);
+        P->off_a_chunks = take(as.chunks);
+        P->off_a_ml = take(as.part_ml);
+        P->off_a_o = as.part_o <= P->ws_prefill_end - P->off_p_xn ? P->off_p_xn : take(as.part_o);
         P->ws_bytes = off;
     }
     I.workspace_bytes = (int64_t)P->ws_bytes;
@@ -677,8 +685,8 @@ extern "C" tp_status tp_shard_kv(tp_plan_t plan, const void* k_full, const void*
 
 extern "C" tp_status tp_workspace_init(tp_plan_t plan, void* workspace, size_t bytes, void* stream) {
     if (!plan || !workspace) return fail(TP_ERR_NULL, "tp_workspace_init: NULL argument");
-    if (bytes < plan->ws_bytes)
-        return fail(TP_ERR_CAPACITY, "tp_workspace_init: workspace %zu bytes < required %zu", bytes, plan->ws_bytes);
+    if (bytes < plan->ws_base)
+        return fail(TP_ERR_CAPACITY, "tp_workspace_init: workspace %zu bytes < required %zu", bytes, plan->ws_base);
     if (!aligned16(workspace)) return fail(TP_ERR_ALIGN, "tp_workspace_init: workspace must be 16-byte aligned");
     tp_status st = check_device();
     if (st) return st;
@@ -1173,9 +1181,9 @@ extern "C" tp_status tp_block_forward(tp_plan_t plan, const tp_shard_set* w, con
     if (B < 1 || T_per_seq < 1) return fail(TP_ERR_SHAPE, "tp_block_forward: B and T_per_seq must be >= 1");
     if (B > plan->d.max_batch || (int64_t)B * T_per_seq > plan->d.max_tokens)
         return fail(TP_ERR_SHAPE, "tp_block_forward: B=%d x T=%d exceeds the plan's max_batch/max_tokens", B, T_per_seq);
-    if (workspace_bytes < plan->ws_bytes)
+    if (workspace_bytes < plan->ws_base)
         return fail(TP_ERR_CAPACITY, "tp_block_forward: workspace %zu bytes < required %zu", workspace_bytes,
-                    plan->ws_bytes);
+                    plan->ws_base);
     if (!aligned16(workspace) || !aligned16(x) || !aligned16(y))
         return fail(TP_ERR_ALIGN, "tp_block_forward: x, y and workspace must be 16-byte aligned");
     tp_status st = check_device();
@@ -1814,8 +1822,8 @@ extern "C" tp_status tp_stack_decode(tp_stack_t stack, const float* x, float* y,
     if (x == y) return fail(TP_ERR_INVALID_ARG, "tp_stack_decode: y must not alias x");
     if (B < 1 || B > P->d.max_batch || B > tpk::kTMax)
         return fail(TP_ERR_SHAPE, "tp_stack_decode: B=%d outside 1..min(max_batch, %d)", B, tpk::kTMax);
-    if (workspace_bytes < P->ws_bytes)
-        return fail(TP_ERR_CAPACITY, "tp_stack_decode: workspace %zu bytes < required %zu", workspace_bytes, P->ws_bytes);
+    if (workspace_bytes < P->ws_base)
+        return fail(TP_ERR_CAPACITY, "tp_stack_decode: workspace %zu bytes < required %zu", workspace_bytes, P->ws_base);
     if (!aligned16(workspace) || !aligned16(x) || !aligned16(y))
         return fail(TP_ERR_ALIGN, "tp_stack_decode: x, y and workspace must be 16-byte aligned");
     char* ws = static_cast<char*>(workspace);
