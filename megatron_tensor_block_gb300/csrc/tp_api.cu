@@ -1034,15 +1034,22 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
     const tp_model_desc& d = P->d;
     const tp_plan_info& I = P->info;
     const int N = P->N, T = pk ? pk->T : B * S, H = (int)d.hidden, hd = (int)d.head_dim;
+    const char* who = pk ? "tp_block_forward_packed" : "tp_block_forward";
+    cudaError_t e;
+    auto launch_fail = [&](const char* what) {
+        char s[96];
+        snprintf(s, sizeof s, "%s: %s", who, what);
+        return cuda_fail(e, s);
+    };
     for (int r = 0; r < N; ++r) {
         if (!w->wqkv[r] || !w->wo[r] || !w->wgu[r] || !w->wd[r] || !w->gamma_attn[r] || !w->gamma_ffn[r])
-            return fail(TP_ERR_NULL, "tp_block_forward: shard %d weight pointer is NULL", r);
-        if (d.has_qkv_bias && !w->bqkv[r]) return fail(TP_ERR_NULL, "tp_block_forward: shard %d bias is NULL", r);
-        if (!kv->k[r] || !kv->v[r]) return fail(TP_ERR_NULL, "tp_block_forward: shard %d KV cache is NULL", r);
+            return fail(TP_ERR_NULL, "%s: shard %d weight pointer is NULL", who, r);
+        if (d.has_qkv_bias && !w->bqkv[r]) return fail(TP_ERR_NULL, "%s: shard %d bias is NULL", who, r);
+        if (!kv->k[r] || !kv->v[r]) return fail(TP_ERR_NULL, "%s: shard %d KV cache is NULL", who, r);
         const void* al[] = {w->wqkv[r], w->wo[r], w->wgu[r], w->wd[r], w->gamma_attn[r], w->gamma_ffn[r],
                             kv->k[r], kv->v[r]};
         for (const void* p : al)
-            if (!aligned16(p)) return fail(TP_ERR_ALIGN, "tp_block_forward: shard %d pointer not 16-byte aligned", r);
+            if (!aligned16(p)) return fail(TP_ERR_ALIGN, "%s: shard %d pointer not 16-byte aligned", who, r);
     }
     int* status = reinterpret_cast<int*>(ws + P->off_status);
     void* xn = ws + P->off_p_xn;
@@ -1059,7 +1066,6 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
         return 1;
     };
     const int na = distinct(w->gamma_attn), nf = distinct(w->gamma_ffn);
-    cudaError_t e;
     const double log2_theta = std::log2(d.rope_theta);
     stage_mark(P, 0, s);
     e = pk ? launch_attn_plan(*pk, s) : cudaSuccess;
@@ -1067,7 +1073,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
         e = pk ? launch_rope_table_at(rope, (int)d.max_kv, hd, log2_theta, pk->prefix_len, s)
                : launch_rope_table(rope, (int)d.max_kv, hd, log2_theta, s);
     if (e == cudaSuccess) e = launch_prefill_norm(x, w->gamma_attn, na, xn, T, H, (float)d.eps, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill norm launch");
+    if (e != cudaSuccess) return launch_fail("prefill norm launch");
 
     PrefillColParams c{};
     c.A = xn;
@@ -1097,7 +1103,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
     c.act = act;
     c.status = status;
     e = launch_tc_col(pk ? 2 : 0, c, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill QKV launch");
+    if (e != cudaSuccess) return launch_fail("prefill QKV launch");
     stage_mark(P, 1, s);
 
     if (pk) {
@@ -1105,7 +1111,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
         ra.q = q;
         ra.out = ao;
         e = launch_attn_ragged(ra, s);
-        if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward_packed: attention launch");
+        if (e != cudaSuccess) return launch_fail("attention launch");
     } else {
         FlashParams f{};
         f.q = q;
@@ -1127,7 +1133,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
         f.scale = (float)(1.0 / std::sqrt((double)hd));
         f.status = status;
         e = launch_flash_prefill(f, s);
-        if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill attention launch");
+        if (e != cudaSuccess) return launch_fail("prefill attention launch");
     }
     stage_mark(P, 2, s);
 
@@ -1143,16 +1149,16 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
     o.n_tok = c.n_tok;
     o.status = status;
     e = launch_tc_row(o, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill o_proj launch");
+    if (e != cudaSuccess) return launch_fail("prefill o_proj launch");
     stage_mark(P, 3, s);
 
     e = launch_prefill_norm(h, w->gamma_ffn, nf, xn, T, H, (float)d.eps, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill norm launch");
+    if (e != cudaSuccess) return launch_fail("prefill norm launch");
     c.a_copies = nf;
     c.rows = (int)(2 * I.ffn_shard);
     for (int r = 0; r < N; ++r) c.W[r] = w->wgu[r];
     e = launch_tc_col(1, c, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill gate/up launch");
+    if (e != cudaSuccess) return launch_fail("prefill gate/up launch");
     stage_mark(P, 4, s);
 
     PrefillRowParams dn{};
@@ -1167,7 +1173,7 @@ static tp_status forward_prefill(tp_plan_t P, const tp_shard_set* w, const tp_kv
     dn.n_tok = c.n_tok;
     dn.status = status;
     e = launch_tc_row(dn, s);
-    if (e != cudaSuccess) return cuda_fail(e, "tp_block_forward: prefill down launch");
+    if (e != cudaSuccess) return launch_fail("prefill down launch");
     stage_mark(P, 5, s);
     return ok();
 }
