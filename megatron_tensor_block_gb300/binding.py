@@ -167,14 +167,22 @@ def _stream(s) -> int | None:
 
 class Plan:
     """Owns a ``tp_plan_t``; destroyed with the object. Keeps the sizes that
-    the packed calls check their tensors against."""
+    the packed calls and the logit controls check their tensors against; one
+    made without a description does not have them and takes the other calls only."""
+    _SIZES = ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab")
 
-    def __init__(self, handle: int, desc: tp_model_desc):
+    def __init__(self, handle: int, desc: tp_model_desc | None = None):
         self.handle = handle
         info = tp_plan_get_info(self)
         self.tp, self.hkv_shard, self.workspace_bytes = info["tp"], info["hkv_shard"], info["workspace_bytes"]
-        for n in ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab"):
-            setattr(self, n, int(getattr(desc, n)))
+        if desc is not None:
+            for n in self._SIZES:
+                setattr(self, n, int(getattr(desc, n)))
+
+    def __getattr__(self, name):
+        if name in Plan._SIZES:
+            raise ValueError("the plan object was made without the plan's description, which this call needs")
+        raise AttributeError(name)
 
     def __del__(self):
         if self.handle and _lib is not None:

@@ -64,3 +64,22 @@ def test_large_prefill_plans_hold_partial_results_where_other_buffers_lie():
     for tp, n in ((1, 578228224), (2, 645599232), (4, 780341248), (8, 1050873856)):
         p = tb.tp_plan(desc_of(w), tp)
         assert n < p.workspace_bytes < 1.01 * n
+
+
+def test_a_plan_object_around_a_bare_handle():
+    # as it could be made before it kept sizes: every call but the packed ones takes it
+    lay, b, t, kv, n = PLANS[0]
+    made = tb.tp_plan(K.plan_desc(tb, lay, b, t, kv), lay.tp)
+    bare = tb.Plan(made.handle)
+    try:
+        assert tb.tp_plan_get_info(bare) == tb.tp_plan_get_info(made)
+        assert bare.workspace_bytes == made.workspace_bytes
+        assert status(lambda: tb.tp_block_forward(bare, {}, None, A, A, A, 1, 1, B.TP_MODE_DECODE, None, A, n, stream=0)) \
+            == B.TP_ERR_INVALID_ARG
+        caches = ([A] * lay.tp, [A] * lay.tp)
+        with pytest.raises(ValueError, match="description"):
+            tb.tp_attn_packed(bare, A, caches, A, A, 1, 1, 2 * A, A, n, stream=0)
+        with pytest.raises(ValueError, match="description"):
+            tb.tp_logits_process(bare, A, 1, 2 * A, stream=0)
+    finally:
+        bare.handle = None                       # `made` owns it
