@@ -252,14 +252,10 @@ static cudaError_t launch_slices(LogitArgs a, cudaStream_t s) {
     a.slices = (int)(((int64_t)a.V + 3 + SLICE - 1) / SLICE);
     const int64_t grid = (int64_t)a.T * a.slices;
     if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-    const size_t smem = (SLICE + 32 + THREADS) * sizeof(unsigned);
-    const void* fn = reinterpret_cast<const void*>(logits_process_kernel<SLICE, THREADS>);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    constexpr size_t smem = (SLICE + 32 + THREADS) * sizeof(unsigned);
+    static_assert(smem <= 48 * 1024, "what a kernel gets without asking");
     void* args[] = {&a};
-    return launch_pdl(fn, args, (int)grid, smem, s, THREADS);
+    return launch_pdl(reinterpret_cast<const void*>(logits_process_kernel<SLICE, THREADS>), args, (int)grid, smem, s, THREADS);
 }
 
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s) {
