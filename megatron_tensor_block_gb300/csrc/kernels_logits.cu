@@ -67,21 +67,22 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         for (int i = 0; i < AHEAD; ++i) load(group(i), x[i]);
 
     int h0 = 0, hn = 0, b0 = 0, bn = 0, np = 0;
-    auto list = [&](const int* cu, int64_t n, int& begin) {  // the row's entries, none where they do not lie in the list
-        begin = cu[t];
-        const int end = cu[t + 1];
-        return begin >= 0 && end > begin && end <= n ? end - begin : 0;
-    };
+    // entries begin .. end - 1 of a list of n: how many, 0 where they do not lie in it (negative numbers are large ones here)
+    auto within = [](unsigned begin, unsigned end, unsigned n) { return begin <= end && end <= n ? (int)(end - begin) : 0; };
     float rep = 1.f, pres = 0.f, freq = 0.f;
     if (a.tokens) {
-        hn = list(a.cu_tokens, a.n_tokens, h0);
+        h0 = a.cu_tokens[t];
+        hn = within(h0, a.cu_tokens[t + 1], a.n_tokens);
         np = a.n_prompt ? a.n_prompt[t] : 0;
         if (a.repetition) rep = a.repetition[t];
         if (a.presence) pres = a.presence[t];
         if (a.frequency) freq = a.frequency[t];
         if (rep == 1.f && pres == 0.f && freq == 0.f) hn = 0;
     }
-    if (a.bias_ids) bn = list(a.cu_bias, a.n_bias, b0);
+    if (a.bias_ids) {
+        b0 = a.cu_bias[t];
+        bn = within(b0, a.cu_bias[t + 1], a.n_bias);
+    }
     const uint32_t* mask = nullptr;
     if (a.mask) {
         const int m = a.mask_row ? a.mask_row[t] : t;
@@ -91,10 +92,10 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
 
     const int lo = max(v0, 0), hi = (int)min((int64_t)v0 + SLICE, (int64_t)a.V);
     const unsigned span = (unsigned)max(hi - lo, 0);
-    int id = -1;                                            // the thread's entry of a short bias list
     float bias = 0.f, biased = 0.f;                         // its bias and its logit, read ahead of the counting
     if (bn && bn <= THREADS && tid < bn) {
-        s_ids[tid] = id = a.bias_ids[(int64_t)b0 + tid];
+        const int id = a.bias_ids[(int64_t)b0 + tid];           // the thread's entry of a short bias list
+        s_ids[tid] = id;
         if (id >= lo && id < hi) {
             bias = a.bias_values[(int64_t)b0 + tid];
             biased = a.x[row0 + id];
@@ -227,6 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1536 / THREADS) logits_process_kernel
         if (!mask || mask[v >> 5] >> (v & 31) & 1u) a.y[row0 + v] += a.bias_values[(int64_t)b0 + entry];
     };
     if (bn <= THREADS) {
+        const int id = tid < bn ? s_ids[tid] : -1;
         if (id >= lo && id < hi) {
             bool last = true;
             for (int j = tid + 1; j < bn; ++j) last &= s_ids[j] != id;

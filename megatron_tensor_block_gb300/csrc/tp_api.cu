@@ -1399,8 +1399,8 @@ extern "C" tp_status tp_logits_process(tp_plan_t plan, const float* logits, int3
     a.mask_row = c->mask_row;
     a.mask_rows = c->mask_rows;
     a.mask_words = (int)((V + 31) / 32);
-    a.n_tokens = c->n_tokens;
-    a.n_bias = c->n_bias;
+    a.n_tokens = (int)std::min<int64_t>(c->n_tokens, INT32_MAX);
+    a.n_bias = (int)std::min<int64_t>(c->n_bias, INT32_MAX);
     TP_CUDA(launch_logits(a, static_cast<cudaStream_t>(stream)), who);
     return ok();
 }

@@ -397,7 +397,7 @@ struct LogitArgs {
     const uint32_t* mask;
     const int* mask_row;
     int mask_rows, mask_words;
-    int64_t n_tokens, n_bias;
+    int n_tokens, n_bias;                 // entries of the lists, or INT32_MAX where there are more
 };
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
