@@ -429,13 +429,21 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
 // The items' ranges of blocks are walked in the same order by every role; all
 // waits are bounded.
 //
+// P is held in bf16 because a product's operands are of one type and V is bf16:
+// float32 weights would need V widened in shared memory and products of tf32, at
+// half the rate that bounds the kernel. A weight is off by at most 2^-8 of
+// itself, with either sign; over the listed calls the results are 0.0019 to
+// 0.0023 of their norm off, and 0.0016 to 0.0017, which is their own rounding to
+// bf16, with float32 weights. Sums, maxima and O stay float32.
+//
 // Bound by the tensor cores: 256 rows x 128 keys are 2048 cycles of products for
-// d = 128 (2053 measured, products alone) and 1024 for d = 64, where the 32768
-// exponentials, at 4 cycles for 32 of a quarter of the SM, take as long. Causal
-// prompts of 32 heads: 8192 tokens 342 us, 1.61 PFLOP/s (d = 64: 286 us, 0.96),
-// 16384 tokens 1350 us, 1.63 PFLOP/s of 1.88 measured for a library product; the
-// block takes about 2500 cycles, and the power limit takes its share of the
-// clock. For short prompts an item's beginning and end count: the first 10 to 14
+// d = 128 (2053 measured, products alone). Causal prompts of 32 heads: 8192
+// tokens 342 us, 1.61 PFLOP/s, 16384 tokens 1350 to 1380 us, 1.6 PFLOP/s of 1.88
+// measured for a library product; the block takes about 2500 cycles, and the
+// power limit takes its share of the clock. For d = 64 the products take 1024
+// cycles and the 32768 exponentials, at 4 cycles for 32 of a quarter of the SM,
+// as long, but 8192 tokens take 290 us, 0.95 PFLOP/s: the chain of maximum,
+// exponentials and hand-over bounds it, with each unit at half its rate. For short prompts an item's beginning and end count: the first 10 to 14
 // us with cold code, each later one 3 to 6 (16 prompts behind 2048 keys: 56 us
 // for 15 us of products).
 //

@@ -15,7 +15,7 @@
 // biased entries follow.
 //
 // 256 rows x 151936 with histories of up to 8192 tokens, masks and biases take
-// 72 to 75 us, 4.3 TB/s; without histories 60, the bare copy 47. The history's
+// 76 us, 4.2 TB/s; without histories 60, the bare copy 47. The history's
 // loads, its atomics and the penalties are about 5 us each: a CTA spends them
 // one after the other, and only the six on an SM cover one another. Every slice
 // of a row counts its whole history: that is why slices are not shorter, and
