@@ -443,9 +443,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const RaggedAtt
 // power limit takes its share of the clock. For d = 64 the products take 1024
 // cycles and the 32768 exponentials, at 4 cycles for 32 of a quarter of the SM,
 // as long, but 8192 tokens take 290 us, 0.95 PFLOP/s: the chain of maximum,
-// exponentials and hand-over bounds it, with each unit at half its rate. For short prompts an item's beginning and end count: the first 10 to 14
-// us with cold code, each later one 3 to 6 (16 prompts behind 2048 keys: 56 us
-// for 15 us of products).
+// exponentials and hand-over bounds it, with each unit at half its rate. For
+// short prompts an item's beginning and end count: the first 10 to 14 us with
+// cold code, each later one 3 to 6 (16 prompts behind 2048 keys: 56 us for 15 us
+// of products).
 //
 // Taken against (8192 tokens): the scores read twice, once for the maximum, once
 // for the weights, so that they need no registers: 400 for 357 us; the products
