@@ -176,7 +176,9 @@ class Model:
         As the workspace, the buffer between the layers is the model's: its
         calls must not overlap on the GPU."""
         n, cur, B_ = len(self.layers), x, pos.numel()
-        tmp = self.tmp[:x.shape[0]] if n > 1 else None
+        tmp = None
+        if n > 1:                                       # (more rows than the plan has: the first layer's call refuses them)
+            tmp = self.tmp[:x.shape[0]] if x.shape[0] <= self.tmp.shape[0] else y
         for i, L in enumerate(self.layers):
             out = y if (n - 1 - i) % 2 == 0 else tmp
             B.tp_block_forward_packed(self.plan, L.shards, (self.caches[i].k, self.caches[i].v), cur, out, cu, pos, B_,

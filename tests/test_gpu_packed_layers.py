@@ -72,3 +72,17 @@ def test_layers_on_another_stream_beside_work_of_the_current_one(gpu_lib, as_add
     torch.cuda.synchronize()
     assert m.ws.status() == 0
     assert P.err(y.double().cpu().numpy(), ref) <= TOL
+
+
+@pytest.mark.parametrize("layers", [1, 2, 3])
+def test_more_rows_than_the_plan_has_are_refused_by_every_number_of_layers(gpu_lib, layers):
+    import torch
+    from megatron_tensor_block_gb300.runtime import Model
+    w = synth.scaled(BLOCKS["llama_tp2"], n_layers=layers, seed=44)
+    m = Model(synth.make_inputs(w, with_head=False))
+    x = torch.zeros(w.tokens + 1, w.hidden, device="cuda")
+    y = torch.full_like(x, 7.0)
+    cu = torch.tensor([0, w.tokens + 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(gpu_lib.TpError, match="TP_ERR_SHAPE"):
+        m.forward_packed(x, y, cu, torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert (y == 7.0).all() and m.ws.status() == 0
