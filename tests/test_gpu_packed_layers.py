@@ -86,3 +86,45 @@ def test_more_rows_than_the_plan_has_are_refused_by_every_number_of_layers(gpu_l
     with pytest.raises(gpu_lib.TpError, match="TP_ERR_SHAPE"):
         m.forward_packed(x, y, cu, torch.zeros(1, dtype=torch.int32, device="cuda"))
     assert (y == 7.0).all() and m.ws.status() == 0
+
+
+@pytest.mark.parametrize("prefix", [0, 130])
+def test_a_captured_pass_replays_with_other_lengths_in_a_padded_batch(gpu_lib, prefix):
+    # rows behind the last sequence hold NaN: they reach nothing and stay as they are
+    import torch
+    w, inputs, m, pre, _ = setup(2, prefix)
+    x = torch.from_numpy(np.ascontiguousarray(np.asarray(inputs["x"])[:90])).to("cuda")
+    y = torch.full_like(x, 7.0)
+    cu = torch.tensor([0, 40, 60, 70, 80], dtype=torch.int32, device="cuda")
+    pos = torch.zeros(4, dtype=torch.int32, device="cuda")
+    caches = [[t.clone() for t in c.k + c.v] for c in m.caches]
+
+    def restore():
+        for c, old in zip(m.caches, caches):
+            for t, o in zip(c.k + c.v, old):
+                t.copy_(o)
+    m.forward_packed(x, y, cu, pos, pre, prefix, prefix)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.forward_packed(x, y, cu, pos, pre, prefix, prefix)
+    for new, cached in (([40, 0, 1, 23], [20, 5, 17, 0]), ([1, 1, 1, 1], [89, 0, 63, 64]), ([0, 0, 0, 70], [0, 0, 0, 90]), ([0] * 4, [0] * 4)):
+        n = sum(new)
+        cu.copy_(torch.from_numpy(np.cumsum([0] + new).astype(np.int32)))
+        pos.copy_(torch.tensor(cached, dtype=torch.int32))
+        x.copy_(torch.from_numpy(np.ascontiguousarray(np.asarray(inputs["x"])[:90])))
+        x[n:] = float("nan")
+        outs = []
+        for run in (g.replay, lambda: m.forward_packed(x, y, cu, pos, pre, prefix, prefix),
+                    lambda: m.forward_packed(x[:n].contiguous(), y[:n], cu, pos, pre, prefix, prefix)):
+            if n == 0 and len(outs) == 2:
+                break
+            restore()
+            y.fill_(7.0)
+            run()
+            outs.append(y.clone())
+        assert m.ws.status() == 0
+        assert torch.isfinite(outs[0]).all() and (outs[0][n:] == 7.0).all()
+        assert torch.equal(outs[0], outs[1])
+        if n:                                           # without the rows behind: other parts, so equal to a rounding
+            assert P.err(outs[2][:n].double().cpu().numpy(), outs[0][:n].double().cpu().numpy()) <= TOL
