@@ -556,6 +556,153 @@ tp_status tp_block_forward_packed(tp_plan_t plan, const tp_shard_set* w, const t
                                   int32_t B, int32_t T, void* workspace, size_t workspace_bytes,
                                   void* stream);
 
+/* ------------------------------------- rotary embedding, 8-bit paged cache */
+
+typedef enum tp_rope_layout {
+    TP_ROPE_HALF = 0,         /* a rotated head's features i and i + rot_dim / 2 are a pair */
+    TP_ROPE_INTERLEAVED = 1   /* features 2 i and 2 i + 1 */
+} tp_rope_layout;
+
+typedef enum tp_rope_scaling {
+    TP_ROPE_NONE = 0,
+    TP_ROPE_LINEAR = 1,       /* every frequency divided by factor */
+    TP_ROPE_WAVELENGTH = 2,   /* long waves divided, short ones kept, a line between */
+    TP_ROPE_RAMP = 3          /* a ramp over the pairs' indices, and a factor on the result */
+} tp_rope_scaling;
+
+/* A rotary embedding: features of pair i of the first rot_dim of a head turn
+ *   (a, b) -> m (a cos(p f_i) - b sin(p f_i), a sin(p f_i) + b cos(p f_i))
+ * at position p; the others stay. With g_i = theta^(-2 i / rot_dim):
+ *   NONE        f_i = g_i
+ *   LINEAR      f_i = g_i / factor
+ *   WAVELENGTH  u = clamp((original g_i / (2 pi) - low) / (high - low), 0, 1),
+ *               f_i = (1 - u) g_i / factor + u g_i
+ *   RAMP        c(x) = rot_dim ln(original / (2 pi x)) / (2 ln theta),
+ *               first = max(floor(c(high)), 0), last = min(ceil(c(low)), rot_dim - 1),
+ *               u = clamp((i - first) / max(last - first, 0.001), 0, 1),
+ *               f_i = (1 - u) g_i + u g_i / factor.
+ * The angle p f_i is taken modulo a turn from a 64-bit fraction, so positions
+ * of any size are as good as small ones; the rotation is float32. */
+typedef struct tp_rope {
+    int64_t rot_dim;          /* rotated features of a head, a multiple of 16; 0: head_dim */
+    int32_t layout;           /* tp_rope_layout */
+    int32_t scaling;          /* tp_rope_scaling */
+    double theta;             /* base, at least 1 (RAMP: above 1); 0: the plan's rope_theta */
+    double factor;            /* of the scalings, at least 1 */
+    double low, high;         /* WAVELENGTH and RAMP: turns over `original` positions, 0 < low < high */
+    int64_t original;         /* ... which is the length trained on */
+    double attn_factor;       /* m; 0: 1, or for RAMP 0.1 ln(factor) + 1 */
+} tp_rope;
+
+/* Token rows of every shard: row t of shard r begins shard_stride r +
+ * token_stride t elements after p, its heads lie d elements apart (so rows may
+ * be pieces of a fused projection's). Strides are multiples of 16 bytes. */
+typedef struct tp_rows {
+    const void* p;
+    int64_t token_stride, shard_stride;
+} tp_rows;
+
+/* Rotates the query and key rows of a packed batch: token row t of sequence b
+ * is at position pos[b] + t - cu[b]. q: rows of Hq' heads, q_out
+ * [tp][T][Hq'][d]; k: rows of Hkv' heads, k_out [tp][T][Hkv'][d]; all in the
+ * plan's dtype, 16-byte aligned; q or k may be NULL, with its output. An output
+ * may be its input's own buffer (of the same strides), and overlaps no input
+ * otherwise. Rows cu[B]..T-1 of the outputs are left as they are. A malformed
+ * cu records TP_ERR_SHAPE in *device_status (nullable, DEVICE int32, kept
+ * unless it is 0) and nothing is written. One launch, no allocation.
+ * Errors: TP_ERR_NULL (both q and k NULL; an input without its output),
+ * TP_ERR_INVALID_ARG (no attention block, a rope outside the ranges above,
+ * overlap), TP_ERR_SHAPE (B outside 1..max_batch, T outside 1..max_tokens,
+ * strides shorter than a row of heads), TP_ERR_ALIGN, TP_ERR_UNSUPPORTED,
+ * TP_ERR_CUDA. */
+tp_status tp_rope_packed(tp_plan_t plan, const tp_rope* rope, const tp_rows* q, const tp_rows* k, const int32_t* cu,
+                         const int32_t* pos, int32_t B, int32_t T, void* q_out, void* k_out, int32_t* device_status,
+                         void* stream);
+
+/* Per-shard KV caches in pages of 8-bit values, an alternative to tp_kv_set
+ * for tp_kv_append_paged and tp_attn_paged: token j of sequence b lies in slot
+ * j % page of pool page pages[b][j / page]. A stored value is e4m3 (four
+ * significant bits; finite ones are at most 448) times its page's and head's
+ * scale. Scales are positive powers of two where tp_kv_append_paged has written
+ * them; tp_attn_paged takes any positive normal ones. */
+typedef struct tp_paged_kv {
+    void* k[TP_MAX_SHARDS];         /* [n_pages][Hkv'][page][d] e4m3, keys after the rotary embedding */
+    void* v[TP_MAX_SHARDS];
+    float* k_scale[TP_MAX_SHARDS];  /* [n_pages][Hkv'] */
+    float* v_scale[TP_MAX_SHARDS];
+    const int32_t* pages;           /* DEVICE [B][width] */
+    int64_t n_pages;
+    int32_t page;                   /* tokens of a page: 16, 32, 64 or 128 */
+    int32_t width;                  /* pages of a sequence at most: it holds width * page tokens */
+} tp_paged_kv;
+
+/* Appends a packed batch's new keys and values to the pages, the rotation
+ * (rope; NULL: keys are rotated already) applied on the way, and rotates the
+ * batch's queries too where q is given (as tp_rope_packed would; q and q_out
+ * may be NULL; they need rope). k and v: rows of Hkv' heads, bf16. Token row t
+ * of sequence b goes to position p = pos[b] + t - cu[b].
+ * The scale of every page and head that receives tokens becomes
+ *   s = max(s_before, 2^e),  or 2^e where slot 0 is among the new ones,
+ * with e the least integer from -60 on with c max|x| <= 448 2^e over the finite
+ * new values x of the page and head (for keys those before the rotation, with
+ * c = sqrt(2) max(1, m), or 1 without rope; for values c = 1): no rounding of a
+ * sine decides a scale. Values that the page holds already are brought to a
+ * larger s, which rounds them again only below 2^-6 s. Stored is x / s rounded
+ * to the nearest e4m3, ties to even, from the float32 rotation without a
+ * rounding between; values that are not finite are stored as NaN. Slots that no
+ * token of the call falls into keep their value.
+ * Every page that receives tokens belongs to one sequence (a page that several
+ * sequences write has undefined contents). Rows at positions outside
+ * 0..width*page-1 or in a page whose id is outside 0..n_pages-1 append nothing
+ * and record TP_ERR_CAPACITY in *device_status (nullable, DEVICE int32, kept
+ * unless it is 0); a malformed cu records TP_ERR_SHAPE, and nothing is
+ * written. Deterministic; one launch, no allocation: the call may be captured.
+ * Errors: TP_ERR_NULL, TP_ERR_INVALID_ARG (no attention block, rope, q without
+ * rope, page size, overlap of q_out), TP_ERR_SHAPE (B, T, n_pages, width,
+ * strides), TP_ERR_ALIGN, TP_ERR_UNSUPPORTED (not a bf16 plan), TP_ERR_CUDA. */
+tp_status tp_kv_append_paged(tp_plan_t plan, const tp_rope* rope, const tp_rows* q, const tp_rows* k, const tp_rows* v,
+                             const tp_paged_kv* kv, const int32_t* cu, const int32_t* pos, int32_t B, int32_t T, void* q_out,
+                             int32_t* device_status, void* stream);
+
+/* Bytes of the workspace of tp_attn_paged for a plan (its own, apart from
+ * tp_plan_info.workspace_bytes), into *bytes (host). Errors: TP_ERR_NULL,
+ * TP_ERR_INVALID_ARG (no attention block), TP_ERR_UNSUPPORTED (not a bf16
+ * plan). */
+tp_status tp_paged_workspace_bytes(tp_plan_t plan, int64_t* bytes);
+
+/* Zeroes the control words at the start of a paged workspace. Call once after
+ * allocating it, and after a TP_ERR_TIMEOUT. tp_get_device_status reads its
+ * status word. Errors: as tp_paged_workspace_bytes, TP_ERR_CAPACITY,
+ * TP_ERR_ALIGN, TP_ERR_CUDA. */
+tp_status tp_paged_workspace_init(tp_plan_t plan, void* workspace, size_t bytes, void* stream);
+
+/* tp_attn_packed over 8-bit pages: causal grouped attention of every token row
+ * over positions 0..p of its sequence's pages (the new tokens' keys and values
+ * are there already). q and out are bf16 [tp][T][Hq'][d], 16-byte aligned, not
+ * overlapping. max_new: no sequence has more new tokens than this (1: a decode
+ * step), 0 where it is not known; the work that a bound rules out is not
+ * launched, and a sequence with more records TP_ERR_SHAPE and keeps its rows of
+ * out as they are. The plan's max_kv does not matter.
+ * Rows at positions outside 0..width*page-1 are written as zeros and recorded
+ * as TP_ERR_CAPACITY in the workspace's status word. Keys in a page whose id is
+ * outside 0..n_pages-1 are not seen and recorded likewise; a row that sees no
+ * key is zeros. Rows cu[B]..T-1 of out are left as they are; a malformed cu
+ * records TP_ERR_SHAPE, and out is left as it is. NaN among the values that a
+ * row sees (and infinities of q) go the way of the formula; what it does not
+ * see never reaches it. Scores, sums and outputs accumulate in float32; the
+ * softmax's weights are rounded to fp16 for the product with the values, out
+ * once from float32. Deterministic. Every wait on the device is bounded; one
+ * that runs out records TP_ERR_TIMEOUT, and out is then undefined. No
+ * allocation, no synchronisation: the call may be captured; calls on one
+ * workspace must not overlap on the GPU.
+ * Errors: TP_ERR_NULL, TP_ERR_INVALID_ARG (no attention block, page size, out
+ * overlaps q), TP_ERR_SHAPE (B outside 1..max_batch, T outside 1..max_tokens,
+ * max_new < 0, n_pages, width), TP_ERR_CAPACITY (workspace too small),
+ * TP_ERR_ALIGN, TP_ERR_UNSUPPORTED (not a bf16 plan), TP_ERR_CUDA. */
+tp_status tp_attn_paged(tp_plan_t plan, const void* q, const tp_paged_kv* kv, const int32_t* cu, const int32_t* pos,
+                        int32_t B, int32_t T, int32_t max_new, void* out, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Standalone rank-order reduction ([RT] Collective backend abstraction,
  * copy-and-reduce; [MG] Local TP: the add after the copies):
  *   out[m, :] = residual[m, :] + (((p_0 + p_1) + p_2) + ... + p_{tp-1})[m, :] + bias

@@ -34,6 +34,8 @@ TP_F32, TP_BF16 = 0, 1
 TP_MODE_DECODE, TP_MODE_PREFILL, TP_MODE_MOE_FFN = 0, 1, 2
 (TP_PARAM_REPLICATED, TP_PARAM_COLWISE, TP_PARAM_ROWWISE, TP_PARAM_FUSED_QKV, TP_PARAM_FUSED_GATE_UP,
  TP_PARAM_PACKED_COLWISE, TP_PARAM_VOCAB_PARALLEL) = range(7)
+TP_ROPE_HALF, TP_ROPE_INTERLEAVED = 0, 1
+TP_ROPE_NONE, TP_ROPE_LINEAR, TP_ROPE_WAVELENGTH, TP_ROPE_RAMP = range(4)
 
 _P8 = C.c_void_p * TP_MAX_SHARDS
 
@@ -75,6 +77,22 @@ class tp_logit_controls(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in (
         "tokens", "cu_tokens", "n_prompt", "repetition", "presence", "frequency", "bias_ids", "bias_values", "cu_bias",
         "mask", "mask_row")] + [("mask_rows", C.c_int32), ("reserved0", C.c_int32), ("n_tokens", C.c_int64), ("n_bias", C.c_int64)]
+
+
+class tp_rope(C.Structure):
+    """A rotary embedding; fields not given are 0 (``rot_dim`` 0: the whole head, ``theta`` 0: the plan's)."""
+    _fields_ = [("rot_dim", C.c_int64), ("layout", C.c_int32), ("scaling", C.c_int32), ("theta", C.c_double),
+                ("factor", C.c_double), ("low", C.c_double), ("high", C.c_double), ("original", C.c_int64),
+                ("attn_factor", C.c_double)]
+
+
+class tp_rows(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("token_stride", C.c_int64), ("shard_stride", C.c_int64)]
+
+
+class tp_paged_kv(C.Structure):
+    _fields_ = [("k", _P8), ("v", _P8), ("k_scale", _P8), ("v_scale", _P8), ("pages", C.c_void_p), ("n_pages", C.c_int64),
+                ("page", C.c_int32), ("width", C.c_int32)]
 
 
 class TpError(RuntimeError):
@@ -125,6 +143,12 @@ def load(path: str | None = None) -> C.CDLL:
         "tp_block_forward_packed": (I32, [P, C.POINTER(tp_shard_set), C.POINTER(tp_kv_set), C.POINTER(tp_kv_set), I64,
                                           I64, VP, VP, VP, VP, I32, I32, VP, C.c_size_t, VP]),
         "tp_logits_process": (I32, [P, VP, I32, C.POINTER(tp_logit_controls), VP, VP]),
+        "tp_rope_packed": (I32, [P, C.POINTER(tp_rope), C.POINTER(tp_rows), C.POINTER(tp_rows), VP, VP, I32, I32, VP, VP, VP, VP]),
+        "tp_kv_append_paged": (I32, [P, C.POINTER(tp_rope), C.POINTER(tp_rows), C.POINTER(tp_rows), C.POINTER(tp_rows),
+                                     C.POINTER(tp_paged_kv), VP, VP, I32, I32, VP, VP, VP]),
+        "tp_paged_workspace_bytes": (I32, [P, C.POINTER(I64)]),
+        "tp_paged_workspace_init": (I32, [P, VP, C.c_size_t, VP]),
+        "tp_attn_paged": (I32, [P, VP, C.POINTER(tp_paged_kv), VP, VP, I32, I32, I32, VP, VP, C.c_size_t, VP]),
         "tp_get_device_status": (I32, [VP, C.POINTER(I32), VP]),
         "tp_gemm_bf16": (I32, [VP, VP, VP, I64, I64, I64, VP, VP]),
         "tp_gemm_bf16_kn": (I32, [VP, VP, VP, I64, I64, I64, VP, VP]),
@@ -169,7 +193,7 @@ class Plan:
     """Owns a ``tp_plan_t``; destroyed with the object. Keeps the sizes that
     the packed calls and the logit controls check their tensors against; one
     made without a description does not have them and takes the other calls only."""
-    _SIZES = ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab")
+    _SIZES = ("hidden", "n_heads", "head_dim", "max_batch", "max_kv", "org_vocab", "dtype")
 
     def __init__(self, handle: int, desc: tp_model_desc | None = None):
         self.handle = handle
@@ -415,6 +439,131 @@ def tp_block_forward_packed(plan: Plan, shards: dict, kv: tuple, x, y, cu, pos, 
                                           _checked(x, "x", _Torch.f32, n, dev), _checked(y, "y", _Torch.f32, n, dev),
                                           _checked(cu, "cu", _Torch.i32, B + 1, dev), _checked(pos, "pos", _Torch.i32, B, dev), B, T,
                                           _checked(workspace, "workspace", _Torch.u8, nbytes, dev), nbytes, _Torch.stream(stream, dev)))
+
+
+def _rows(plan: Plan, t, name: str, heads: int, T: int, dtype, device: int):
+    """``tp_rows`` of a tensor ``[tp, >= T, heads, d]`` whose heads are contiguous; an address is that of a contiguous
+    ``[tp, T, heads, d]``."""
+    if t is None:
+        return None
+    d = plan.head_dim
+    if type(t) is int:
+        return tp_rows(t, heads * d, T * heads * d)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != plan.tp or shape[1] < T or shape[2] != heads or shape[3] != d:
+        raise ValueError(f"{name}: {tuple(shape)}, expected ({plan.tp}, at least {T}, {heads}, {d})")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+    shard, token, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
+        raise ValueError(f"{name}: the heads of a row are not contiguous")
+    return tp_rows(t.data_ptr(), token, shard)
+
+
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
+def tp_rope_packed(plan: Plan, rope: tp_rope, cu, pos, B: int, T: int, q=None, q_out=None, k=None, k_out=None, device_status=None,
+                   stream=None) -> None:
+    """Rotates the rows ``q`` ``[tp, T, Hq', d]`` and ``k`` ``[tp, T, Hkv', d]`` of a packed batch (either may be left out) into
+    contiguous ``q_out`` and ``k_out``, which may be the inputs themselves."""
+    dev = _Torch.device()
+    dt, hq, hkv, d = _Torch.bf16 if plan.dtype == TP_BF16 else _Torch.f32, plan.n_heads // plan.tp, plan.hkv_shard, plan.head_dim
+    _check(load().tp_rope_packed(plan.handle, _ref(rope), _ref(_rows(plan, q, "q", hq, T, dt, dev)),
+                                 _ref(_rows(plan, k, "k", hkv, T, dt, dev)), _checked(cu, "cu", _Torch.i32, B + 1, dev),
+                                 _checked(pos, "pos", _Torch.i32, B, dev), B, T, _checked(q_out, "q_out", dt, plan.tp * T * hq * d, dev),
+                                 _checked(k_out, "k_out", dt, plan.tp * T * hkv * d, dev),
+                                 _checked(device_status, "device_status", _Torch.i32, 1, dev), _Torch.stream(stream, dev)))
+
+
+class PagedKV:
+    """8-bit paged caches: per shard ``k`` and ``v`` ``[n_pages, Hkv', page, d]`` of ``torch.float8_e4m3fn`` (or its bytes as
+    uint8), ``k_scale`` and ``v_scale`` float32 ``[n_pages, Hkv']``, and the page table ``pages`` int32 ``[B, width]``. Checked
+    here once; keeps the tensors alive. ``at`` makes the same caches with another table."""
+
+    def __init__(self, plan: Plan, k: list, v: list, k_scale: list, v_scale: list, pages):
+        import torch
+        dev = _Torch.device()
+        self.tensors, self.device = (list(k), list(v), list(k_scale), list(v_scale)), dev
+        shape = tuple(k[0].shape) if k else ()
+        if len(shape) != 4 or shape[1] != plan.hkv_shard or shape[3] != plan.head_dim:
+            raise ValueError(f"k: {shape}, expected (n_pages, {plan.hkv_shard}, page, {plan.head_dim})")
+        for name, ts, of, types in (("k", k, shape, (torch.float8_e4m3fn, torch.uint8)), ("v", v, shape, (torch.float8_e4m3fn, torch.uint8)),
+                                    ("k_scale", k_scale, shape[:2], (torch.float32,)), ("v_scale", v_scale, shape[:2], (torch.float32,))):
+            if len(ts) != plan.tp:
+                raise ValueError(f"{name}: expected a tensor for each of {plan.tp} shards")
+            for t in ts:
+                if t.dtype not in types:
+                    raise TypeError(f"{name}: {t.dtype}, expected {types[0]}")
+                if tuple(t.shape) != of or not t.is_contiguous():
+                    raise ValueError(f"{name}: {tuple(t.shape)}, expected contiguous {of}")
+                if t.get_device() != dev:
+                    raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+        self.page, self.n_pages = shape[2], shape[0]
+        self._ptrs = [_P8(*[t.data_ptr() for t in ts]) for ts in self.tensors]
+        self._table(pages)
+
+    def _table(self, pages) -> None:
+        if pages.dim() != 2:
+            raise ValueError(f"pages: {tuple(pages.shape)}, expected (sequences, width)")
+        self.pages, self.sequences = pages, pages.shape[0]
+        self.struct = tp_paged_kv(*self._ptrs, _checked(pages, "pages", _Torch.i32, 1, self.device), self.n_pages, self.page,
+                                  pages.shape[1])
+
+    def at(self, pages) -> "PagedKV":
+        """These caches with another page table."""
+        new = object.__new__(PagedKV)
+        new.__dict__.update(self.__dict__)
+        new._table(pages)
+        return new
+
+
+def _paged(kv, B: int, device: int):
+    if isinstance(kv, tp_paged_kv) or kv is None:
+        return _ref(kv)
+    if kv.sequences < B:
+        raise ValueError(f"pages: {kv.sequences} sequences, expected at least {B}")
+    if kv.device != device:
+        raise ValueError("kv: not on the current CUDA device")
+    return C.byref(kv.struct)
+
+
+def tp_kv_append_paged(plan: Plan, rope, k, v, kv, cu, pos, B: int, T: int, q=None, q_out=None, device_status=None,
+                       stream=None) -> None:
+    """Appends a packed batch's ``k`` (rotated by ``rope`` on the way; None: rotated already) and ``v`` ``[tp, T, Hkv', d]`` to the
+    pages of ``kv`` (a :class:`PagedKV`), and rotates ``q`` ``[tp, T, Hq', d]`` into ``q_out`` where it is given."""
+    dev, bf16, hq, hkv = _Torch.device(), _Torch.bf16, plan.n_heads // plan.tp, plan.hkv_shard
+    _check(load().tp_kv_append_paged(plan.handle, _ref(rope), _ref(_rows(plan, q, "q", hq, T, bf16, dev)),
+                                     _ref(_rows(plan, k, "k", hkv, T, bf16, dev)), _ref(_rows(plan, v, "v", hkv, T, bf16, dev)),
+                                     _paged(kv, B, dev), _checked(cu, "cu", _Torch.i32, B + 1, dev),
+                                     _checked(pos, "pos", _Torch.i32, B, dev), B, T,
+                                     _checked(q_out, "q_out", bf16, plan.tp * T * hq * plan.head_dim, dev),
+                                     _checked(device_status, "device_status", _Torch.i32, 1, dev), _Torch.stream(stream, dev)))
+
+
+def tp_paged_workspace_bytes(plan: Plan) -> int:
+    n = C.c_int64()
+    _check(load().tp_paged_workspace_bytes(plan.handle, C.byref(n)))
+    return n.value
+
+
+def tp_paged_workspace_init(plan: Plan, workspace, nbytes: int, stream=None) -> None:
+    dev = _Torch.device()
+    _check(load().tp_paged_workspace_init(plan.handle, _checked(workspace, "workspace", _Torch.u8, nbytes, dev), nbytes,
+                                          _Torch.stream(stream, dev)))
+
+
+def tp_attn_paged(plan: Plan, q, kv, cu, pos, B: int, T: int, out, workspace, nbytes: int, max_new: int = 0, stream=None) -> None:
+    """``tp_attn_packed`` over the 8-bit pages of ``kv`` (a :class:`PagedKV`); ``max_new``: no sequence has more new tokens than
+    this (0: not known). ``workspace`` is one of ``tp_paged_workspace_bytes``, set up by ``tp_paged_workspace_init``."""
+    n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
+    _check(load().tp_attn_paged(plan.handle, _checked(q, "q", _Torch.bf16, n, dev), _paged(kv, B, dev),
+                                _checked(cu, "cu", _Torch.i32, B + 1, dev), _checked(pos, "pos", _Torch.i32, B, dev), B, T, max_new,
+                                _checked(out, "out", _Torch.bf16, n, dev), _checked(workspace, "workspace", _Torch.u8, nbytes, dev),
+                                nbytes, _Torch.stream(stream, dev)))
 
 
 def tp_logits_process(plan: Plan, logits, T: int, out, tokens=None, cu_tokens=None, n_prompt=None, repetition=None,

@@ -1348,6 +1348,274 @@ extern "C" tp_status tp_block_forward_packed(tp_plan_t plan, const tp_shard_set*
     return forward_prefill(plan, w, kv, x, y, pos, B, 0, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream), &a);
 }
 
+// ---------------------------------------------------------------- rotary embedding, 8-bit paged cache
+
+// Frequencies as 64-bit fractions of a turn per position, so that the kernels
+// take an angle modulo a turn by an integer product.
+static tp_status rope_table(const char* who, tp_plan_t plan, const tp_rope* rope, RopeTable& t) {
+    const int64_t d = plan->d.head_dim, rot = rope->rot_dim ? rope->rot_dim : d;
+    const double theta = rope->theta != 0 ? rope->theta : plan->d.rope_theta, f = rope->factor;
+    if (rope->layout != TP_ROPE_HALF && rope->layout != TP_ROPE_INTERLEAVED)
+        return fail(TP_ERR_INVALID_ARG, "%s: unknown rotary layout %d", who, rope->layout);
+    if (rope->scaling < TP_ROPE_NONE || rope->scaling > TP_ROPE_RAMP)
+        return fail(TP_ERR_INVALID_ARG, "%s: unknown rotary scaling %d", who, rope->scaling);
+    if (rot < 16 || rot > d || rot % 16)
+        return fail(TP_ERR_INVALID_ARG, "%s: rot_dim=%lld is not a multiple of 16 in 16..head_dim", who, (long long)rot);
+    if (!(theta >= 1) || !std::isfinite(theta) || (rope->scaling == TP_ROPE_RAMP && !(theta > 1)))
+        return fail(TP_ERR_INVALID_ARG, "%s: theta below 1", who);
+    if (rope->scaling != TP_ROPE_NONE && (!(f >= 1) || !std::isfinite(f)))
+        return fail(TP_ERR_INVALID_ARG, "%s: factor below 1", who);
+    const bool ends = rope->scaling == TP_ROPE_WAVELENGTH || rope->scaling == TP_ROPE_RAMP;
+    if (ends && (!(rope->low > 0) || !(rope->high > rope->low) || !std::isfinite(rope->high) || rope->original < 1))
+        return fail(TP_ERR_INVALID_ARG, "%s: the scaling needs 0 < low < high and original >= 1", who);
+    double by = rope->attn_factor;
+    if (!(by >= 0) || by > 1e6) return fail(TP_ERR_INVALID_ARG, "%s: attn_factor outside 0..1e6", who);
+    if (by == 0) by = rope->scaling == TP_ROPE_RAMP ? 0.1 * std::log(f) + 1 : 1;
+    const double two_pi = 6.283185307179586476925286766559;
+    double first = 0, last = 0;
+    if (rope->scaling == TP_ROPE_RAMP) {
+        auto pair = [&](double turns) { return rot * std::log((double)rope->original / (two_pi * turns)) / (2 * std::log(theta)); };
+        first = std::max(std::floor(pair(rope->high)), 0.0);
+        last = std::min(std::ceil(pair(rope->low)), (double)rot - 1);
+    }
+    t = RopeTable{};
+    for (int64_t i = 0; i < rot / 2; ++i) {
+        double g = std::pow(theta, -2.0 * (double)i / (double)rot);
+        if (rope->scaling == TP_ROPE_LINEAR) g /= f;
+        if (rope->scaling == TP_ROPE_WAVELENGTH) {
+            const double u = std::min(1.0, std::max(0.0, ((double)rope->original * g / two_pi - rope->low) / (rope->high - rope->low)));
+            g = (1 - u) * g / f + u * g;
+        }
+        if (rope->scaling == TP_ROPE_RAMP) {
+            const double u = std::min(1.0, std::max(0.0, ((double)i - first) / std::max(last - first, 0.001)));
+            g = (1 - u) * g + u * g / f;
+        }
+        t.turn[i] = (uint64_t)std::nearbyint(std::ldexp(g / two_pi, 64));        // g <= 1: below a sixth of a turn
+    }
+    t.by = (float)by;
+    t.rot = (int)rot;
+    t.layout = rope->layout;
+    return TP_OK;
+}
+
+struct Span {
+    uintptr_t a, b;
+    Span(const void* p, int64_t bytes) : a(reinterpret_cast<uintptr_t>(p)), b(a + (uintptr_t)bytes) {}
+    bool meets(const Span& o) const { return a < o.b && o.a < b; }
+};
+
+// The checks that the paged calls and tp_rope_packed share.
+static tp_status batch_args(const char* who, tp_plan_t plan, const int32_t* cu, const int32_t* pos, int32_t B, int32_t T) {
+    if (!plan || !cu || !pos) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if (!plan->dense) return fail(TP_ERR_INVALID_ARG, "%s: the plan has no attention block", who);
+    if (B < 1 || B > plan->d.max_batch || T < 1 || T > plan->d.max_tokens)
+        return fail(TP_ERR_SHAPE, "%s: B=%d or T=%d outside 1..max_batch, 1..max_tokens of the plan", who, B, T);
+    if ((reinterpret_cast<uintptr_t>(cu) | reinterpret_cast<uintptr_t>(pos)) & 3)
+        return fail(TP_ERR_ALIGN, "%s: cu and pos must be 4-byte aligned", who);
+    return TP_OK;
+}
+
+// Rows of `heads` heads of every shard: their strides, and the bytes that they span.
+static tp_status rows_args(const char* who, const char* name, tp_plan_t plan, const tp_rows* x, int32_t T, int64_t heads,
+                           TokenRows& r, int64_t& span) {
+    const int64_t row = heads * plan->d.head_dim, es = (int64_t)plan->esz, N = plan->N, far = INT64_MAX / 64;
+    if (!x->p) return fail(TP_ERR_NULL, "%s: %s is NULL", who, name);
+    if (x->token_stride < (T > 1 ? row : 0) || x->shard_stride < 0 || x->token_stride > far / T || x->shard_stride > far / N)
+        return fail(TP_ERR_SHAPE, "%s: strides of %s shorter than a row of %lld elements, or beyond the address space", who, name,
+                    (long long)row);
+    // (shards may interleave, as pieces of a fused row do)
+    if (N > 1 && x->shard_stride < row) return fail(TP_ERR_SHAPE, "%s: shards of %s overlap", who, name);
+    if (!aligned16(x->p) || (T > 1 && (x->token_stride * es) % 16) || (N > 1 && (x->shard_stride * es) % 16))
+        return fail(TP_ERR_ALIGN, "%s: %s and its strides must be multiples of 16 bytes", who, name);
+    r = TokenRows{x->p, x->token_stride, x->shard_stride};
+    span = (row + (T - 1) * x->token_stride + (N - 1) * x->shard_stride) * es;
+    return TP_OK;
+}
+
+static tp_status rotated_output(const char* who, const char* name, tp_plan_t plan, const TokenRows& x, int64_t span, const void* out,
+                                int32_t T, int64_t heads) {
+    if (!out) return fail(TP_ERR_NULL, "%s: %s without its output", who, name);
+    if (!aligned16(out)) return fail(TP_ERR_ALIGN, "%s: the output of %s must be 16-byte aligned", who, name);
+    const int64_t row = heads * plan->d.head_dim;
+    const bool same = out == x.p && (T == 1 || x.token == row) && (plan->N == 1 || x.shard == row * T);
+    if (!same && Span(out, row * T * plan->N * (int64_t)plan->esz).meets(Span(x.p, span)))
+        return fail(TP_ERR_INVALID_ARG, "%s: the output of %s overlaps it without being the same buffer", who, name);
+    return TP_OK;
+}
+
+extern "C" tp_status tp_rope_packed(tp_plan_t plan, const tp_rope* rope, const tp_rows* q, const tp_rows* k, const int32_t* cu,
+                                    const int32_t* pos, int32_t B, int32_t T, void* q_out, void* k_out, int32_t* device_status,
+                                    void* stream) {
+    const char* who = "tp_rope_packed";
+    tp_status st = batch_args(who, plan, cu, pos, B, T);
+    if (st) return st;
+    if (!rope || (!q && !k)) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if ((!q && q_out) || (!k && k_out)) return fail(TP_ERR_NULL, "%s: an output without its input", who);
+    RopeArgs a{};
+    if ((st = rope_table(who, plan, rope, a.rope))) return st;
+    const int64_t hq = plan->info.hq_shard, hkv = plan->info.hkv_shard, d = plan->d.head_dim, es = (int64_t)plan->esz;
+    int64_t q_span = 0, k_span = 0;
+    if (q && ((st = rows_args(who, "q", plan, q, T, hq, a.q, q_span)) || (st = rotated_output(who, "q", plan, a.q, q_span, q_out, T, hq))))
+        return st;
+    if (k && ((st = rows_args(who, "k", plan, k, T, hkv, a.k, k_span)) || (st = rotated_output(who, "k", plan, a.k, k_span, k_out, T, hkv))))
+        return st;
+    if (q && k) {
+        const Span qo(q_out, hq * d * T * plan->N * es), ko(k_out, hkv * d * T * plan->N * es);
+        if (qo.meets(ko) || qo.meets(Span(k->p, k_span)) || ko.meets(Span(q->p, q_span)))
+            return fail(TP_ERR_INVALID_ARG, "%s: an output overlaps the other's tensors", who);
+    }
+    if (reinterpret_cast<uintptr_t>(device_status) & 3) return fail(TP_ERR_ALIGN, "%s: device_status must be 4-byte aligned", who);
+    if ((st = check_device())) return st;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.cu = cu;
+    a.pos = pos;
+    a.N = plan->N;
+    a.B = B;
+    a.T = T;
+    a.hq_s = (int)hq;
+    a.hkv_s = (int)hkv;
+    a.d = (int)d;
+    a.status = device_status;
+    TP_CUDA(launch_rope(a, plan->d.dtype, static_cast<cudaStream_t>(stream)), who);
+    return ok();
+}
+
+static tp_status paged_args(const char* who, tp_plan_t plan, const tp_paged_kv* kv, PagedCache& c) {
+    if (!kv || !kv->pages) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if (plan->d.dtype != TP_BF16) return fail(TP_ERR_UNSUPPORTED, "%s runs on bf16 plans", who);
+    if (kv->page != 16 && kv->page != 32 && kv->page != 64 && kv->page != 128)
+        return fail(TP_ERR_INVALID_ARG, "%s: pages of %d tokens; 16, 32, 64 and 128 are served", who, kv->page);
+    const int64_t hkv = plan->info.hkv_shard;
+    if (kv->n_pages < 1 || kv->n_pages > INT32_MAX / (hkv * kv->page) || kv->width < 1 || kv->width > (INT32_MAX - 1024) / kv->page)
+        return fail(TP_ERR_SHAPE, "%s: n_pages=%lld or width=%d out of range", who, (long long)kv->n_pages, kv->width);
+    c = PagedCache{};
+    for (int r = 0; r < plan->N; ++r) {
+        if (!kv->k[r] || !kv->v[r] || !kv->k_scale[r] || !kv->v_scale[r])
+            return fail(TP_ERR_NULL, "%s: a pool or scale pointer of shard %d is NULL", who, r);
+        if (!aligned16(kv->k[r]) || !aligned16(kv->v[r]))
+            return fail(TP_ERR_ALIGN, "%s: a pool of shard %d is not 16-byte aligned", who, r);
+        if ((reinterpret_cast<uintptr_t>(kv->k_scale[r]) | reinterpret_cast<uintptr_t>(kv->v_scale[r])) & 3)
+            return fail(TP_ERR_ALIGN, "%s: scales of shard %d must be 4-byte aligned", who, r);
+        c.k[r] = static_cast<uint8_t*>(kv->k[r]);
+        c.v[r] = static_cast<uint8_t*>(kv->v[r]);
+        c.ks[r] = kv->k_scale[r];
+        c.vs[r] = kv->v_scale[r];
+    }
+    if (reinterpret_cast<uintptr_t>(kv->pages) & 3) return fail(TP_ERR_ALIGN, "%s: pages must be 4-byte aligned", who);
+    c.pages = kv->pages;
+    c.n_pages = (int)kv->n_pages;
+    c.page = kv->page;
+    c.width = kv->width;
+    return TP_OK;
+}
+
+extern "C" tp_status tp_kv_append_paged(tp_plan_t plan, const tp_rope* rope, const tp_rows* q, const tp_rows* k, const tp_rows* v,
+                                        const tp_paged_kv* kv, const int32_t* cu, const int32_t* pos, int32_t B, int32_t T,
+                                        void* q_out, int32_t* device_status, void* stream) {
+    const char* who = "tp_kv_append_paged";
+    tp_status st = batch_args(who, plan, cu, pos, B, T);
+    if (st) return st;
+    if (!k || !v) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if (!q && q_out) return fail(TP_ERR_NULL, "%s: an output without its input", who);
+    if (q && !rope) return fail(TP_ERR_INVALID_ARG, "%s: q is given to be rotated, without a rope", who);
+    AppendArgs a{};
+    if ((st = paged_args(who, plan, kv, a.c))) return st;
+    if (rope && (st = rope_table(who, plan, rope, a.r.rope))) return st;
+    const int64_t hq = plan->info.hq_shard, hkv = plan->info.hkv_shard, d = plan->d.head_dim;
+    int64_t q_span = 0, k_span = 0, v_span = 0;
+    if ((st = rows_args(who, "k", plan, k, T, hkv, a.r.k, k_span)) || (st = rows_args(who, "v", plan, v, T, hkv, a.v, v_span))) return st;
+    if (q && ((st = rows_args(who, "q", plan, q, T, hq, a.r.q, q_span)) || (st = rotated_output(who, "q", plan, a.r.q, q_span, q_out, T, hq))))
+        return st;
+    if (q) {
+        const Span qo(q_out, hq * d * T * plan->N * 2);
+        if (qo.meets(Span(k->p, k_span)) || qo.meets(Span(v->p, v_span)))
+            return fail(TP_ERR_INVALID_ARG, "%s: q_out overlaps k or v", who);
+    }
+    if (reinterpret_cast<uintptr_t>(device_status) & 3) return fail(TP_ERR_ALIGN, "%s: device_status must be 4-byte aligned", who);
+    if ((st = check_device())) return st;
+    a.k_growth = rope ? std::sqrt(2.0) * std::max(1.0, (double)a.r.rope.by) : 1.0;
+    a.r.q_out = q_out;
+    a.r.cu = cu;
+    a.r.pos = pos;
+    a.r.N = plan->N;
+    a.r.B = B;
+    a.r.T = T;
+    a.r.hq_s = (int)hq;
+    a.r.hkv_s = (int)hkv;
+    a.r.d = (int)d;
+    a.r.status = device_status;
+    TP_CUDA(launch_append(a, static_cast<cudaStream_t>(stream)), who);
+    return ok();
+}
+
+static tp_status paged_plan(const char* who, tp_plan_t plan, size_t& bytes) {
+    if (!plan) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if (!plan->dense) return fail(TP_ERR_INVALID_ARG, "%s: the plan has no attention block", who);
+    if (plan->d.dtype != TP_BF16) return fail(TP_ERR_UNSUPPORTED, "%s: bf16 plans have a paged workspace", who);
+    bytes = paged_workspace(plan->d.max_tokens, (int)(plan->d.n_heads / plan->d.n_kv_heads), (int)plan->d.head_dim);
+    return TP_OK;
+}
+
+extern "C" tp_status tp_paged_workspace_bytes(tp_plan_t plan, int64_t* bytes) {
+    if (!bytes) return fail(TP_ERR_NULL, "tp_paged_workspace_bytes: NULL argument");
+    size_t n = 0;
+    tp_status st = paged_plan("tp_paged_workspace_bytes", plan, n);
+    if (st) return st;
+    *bytes = (int64_t)n;
+    return ok();
+}
+
+extern "C" tp_status tp_paged_workspace_init(tp_plan_t plan, void* workspace, size_t bytes, void* stream) {
+    const char* who = "tp_paged_workspace_init";
+    size_t n = 0;
+    tp_status st = paged_plan(who, plan, n);
+    if (st) return st;
+    if (!workspace) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    if (bytes < n) return fail(TP_ERR_CAPACITY, "%s: workspace %zu bytes < required %zu", who, bytes, n);
+    if (!aligned16(workspace)) return fail(TP_ERR_ALIGN, "%s: workspace must be 16-byte aligned", who);
+    if ((st = check_device())) return st;
+    TP_CUDA(cudaMemsetAsync(workspace, 0, kPagedCtrl, static_cast<cudaStream_t>(stream)), who);
+    return ok();
+}
+
+extern "C" tp_status tp_attn_paged(tp_plan_t plan, const void* q, const tp_paged_kv* kv, const int32_t* cu, const int32_t* pos,
+                                   int32_t B, int32_t T, int32_t max_new, void* out, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    const char* who = "tp_attn_paged";
+    tp_status st = batch_args(who, plan, cu, pos, B, T);
+    if (st) return st;
+    if (!q || !out || !workspace) return fail(TP_ERR_NULL, "%s: NULL argument", who);
+    PagedAttnArgs a{};
+    if ((st = paged_args(who, plan, kv, a.c))) return st;
+    if (max_new < 0) return fail(TP_ERR_SHAPE, "%s: max_new=%d below 0", who, max_new);
+    size_t need = 0;
+    if ((st = paged_plan(who, plan, need))) return st;
+    if (workspace_bytes < need)
+        return fail(TP_ERR_CAPACITY, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, need);
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+        return fail(TP_ERR_ALIGN, "%s: q, out and workspace must be 16-byte aligned", who);
+    const int64_t bytes = (int64_t)T * plan->d.n_heads * plan->d.head_dim * 2;
+    if (Span(q, bytes).meets(Span(out, bytes))) return fail(TP_ERR_INVALID_ARG, "%s: out must not overlap q", who);
+    if ((st = check_device())) return st;
+    a.q = q;
+    a.out = out;
+    a.cu = cu;
+    a.pos = pos;
+    a.N = plan->N;
+    a.B = B;
+    a.T = T;
+    a.hq_s = (int)plan->info.hq_shard;
+    a.hkv_s = (int)plan->info.hkv_shard;
+    a.d = (int)plan->d.head_dim;
+    a.max_new = max_new && max_new < T ? max_new : T;
+    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)plan->d.head_dim));
+    a.ws = static_cast<char*>(workspace);
+    a.status = static_cast<int*>(workspace);
+    TP_CUDA(launch_attn_paged(a, static_cast<cudaStream_t>(stream)), who);
+    return ok();
+}
+
 // ---------------------------------------------------------------- logits
 
 extern "C" tp_status tp_logits_process(tp_plan_t plan, const float* logits, int32_t T, const tp_logit_controls* c,

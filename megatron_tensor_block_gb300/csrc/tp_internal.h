@@ -401,6 +401,58 @@ struct LogitArgs {
 };
 cudaError_t launch_logits(const LogitArgs& a, cudaStream_t s);
 
+// Rotary embeddings and 8-bit pages (kernels_paged.cu, kernels_paged_attn.cu).
+struct RopeTable {
+    uint64_t turn[64];                    // per pair: turns per position, in 2^-64
+    float by;                             // on the rotated features
+    int rot, layout;                      // rot = 0: nothing is rotated
+};
+struct TokenRows {
+    const void* p;
+    int64_t token, shard;                 // strides in elements
+};
+struct RopeArgs {
+    RopeTable rope;
+    TokenRows q, k;                       // p NULL: none
+    void* q_out;
+    void* k_out;
+    const int* cu;
+    const int* pos;
+    int N, B, T, hq_s, hkv_s, d;
+    int* status;
+};
+struct PagedCache {
+    uint8_t* k[TP_MAX_SHARDS];            // [n_pages][hkv_s][page][d]
+    uint8_t* v[TP_MAX_SHARDS];
+    float* ks[TP_MAX_SHARDS];             // [n_pages][hkv_s]
+    float* vs[TP_MAX_SHARDS];
+    const int* pages;                     // [B][width]
+    int n_pages, page, width;
+};
+struct AppendArgs {
+    RopeArgs r;                           // q, q_out and the batch; k unrotated
+    TokenRows v;
+    PagedCache c;
+    double k_growth;                      // how far a key's rotation can exceed its largest feature
+};
+struct PagedAttnArgs {
+    const void* q;                        // [N][T][hq_s][d] bf16
+    void* out;
+    PagedCache c;
+    const int* cu;
+    const int* pos;
+    int N, B, T, hq_s, hkv_s, d, max_new;
+    float scale_log2;                     // log2(e) / sqrt(d)
+    int* status;                          // first word of the workspace
+    char* ws;
+};
+// Bytes of a paged workspace for calls of at most max_tokens rows.
+size_t paged_workspace(int64_t max_tokens, int group, int d);
+constexpr size_t kPagedCtrl = 4096;       // control words at its start, zero between calls but for the status
+cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s);
+
 // launchers (return the launch's cudaError_t)
 cudaError_t launch_gemv(const GemvParams& p, int epi, int dtype, cudaStream_t s);
 void set_pdl(bool on);   // programmatic dependent launch between the kernels of a call (default on)
