@@ -2,33 +2,783 @@
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
 //
-// A warp per query row and head walks the keys, 32 at a time: a lane has a key
-// for the scores and d / 32 features for the sums.
+// in one pass over the keys with a running m and sum.
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
+#include "stream.cuh"
 #include "tp_internal.h"
 
 namespace tpk {
 
-__device__ __forceinline__ float from_e4m3(uint8_t x) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)x));
-    float f;
-    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(h));
-    return f;
+// ---------------------------------------------------------------------------
+// Sequences of at most 16 query rows per KV head (rows: new tokens x heads of
+// the group): single tokens and a few drafted ones. Bound by the bytes of the
+// pages, so the design keeps many of them on the way and gives every SM the
+// same number.
+//
+// All the batch's chunks of 32 keys, sequence by sequence and head by head, are
+// one list, cut into equal runs for the CTAs (one per SM) and each of those for
+// its eight warps. Every CTA finds its place from the offsets and lengths by
+// itself. A warp works alone: its own ring of stages in shared memory, filled
+// by its own TMA copies, no barrier with another warp until its run ends. What
+// it has of a head that others have a part of is joined behind that, first in
+// shared memory, then through the workspace by the CTA that comes last.
+//
+// Keys are the rows of the products: S^T = K Q^T (16 keys x 8 query rows) as
+// e4m3 x e4m3, with q, scaled by a power of two for each row, in two e4m3
+// terms: eight significant bits together, all that bf16 has (for elements above
+// 2^-10 of a row's largest; the others are off by 2^-18 of it). So a key's
+// bytes go from its page to the tensor cores as they are. O^T = V^T P^T as
+// fp16 x fp16: ldmatrix transposes pairs of bytes, one conversion makes two fp16
+// of them (exactly), and the weights' rounding to fp16 is 2^-11. The scale of a
+// page's keys goes into the scores, that of its values, relative to the largest
+// so far, into the weights.
+// ---------------------------------------------------------------------------
+
+constexpr int kPnWarps = 8, kPnThreads = 32 * kPnWarps;
+constexpr int kPnKeys = 32;               // keys of a chunk
+constexpr int kPnRows = 16;               // query rows of a sequence and KV head at most
+constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
+
+template <int D>
+struct PnShape {
+    static constexpr int TILE = kPnKeys * D;                        // bytes of a chunk's K or V
+    static constexpr int STAGES = D == 128 ? 2 : 4;
+    static constexpr int SLOT = kPnRows * D * 4 + kPnRows * 8;       // a piece of a head: O, then (m, l)
+    static constexpr int RING = kPnWarps * STAGES * 2 * TILE;
+    static constexpr int HEAD = 4096;
+    static constexpr int SMEM = HEAD + RING + kPnWarps * SLOT;
+    static_assert(STAGES * 2 * TILE >= SLOT, "a warp's ring holds its last piece");
+};
+
+struct PnArgs {
+    CUtensorMap tk[TP_MAX_SHARDS], tv[TP_MAX_SHARDS];   // pools as [n_pages hkv_s][page][D] bytes, boxes of up to 32 keys
+    const float* ks[TP_MAX_SHARDS];
+    const float* vs[TP_MAX_SHARDS];
+    const bf16* q;
+    bf16* out;
+    const int* cu;
+    const int* pos;
+    const int* pages;
+    float* part_o;                        // [kSMs][2][kPnRows][D]
+    float2* part_ml;                      // [kSMs][2][kPnRows]
+    unsigned* joined;                     // [kSMs] pieces of the head that begins in this CTA and ends in another
+    int* status;
+    int N, B, T, hq_s, hkv_s, G, bits, width, n_pages, max_new, cap;
+    float scale_log2;
+};
+
+struct PnPiece {                          // of a head of a sequence
+    int64_t start;                        // the head's first chunk in the batch's list
+    int b, h, x0, x1, nch;                // chunks x0 .. x1 - 1 of nch; x1 = 0: none
+};
+
+// Chunks of a sequence for each head: none where it is not this kernel's.
+__device__ __forceinline__ int pn_chunks(const PnArgs& a, int b, int& c0, int& n, int& pos) {
+    c0 = __ldg(a.cu + b);
+    n = __ldg(a.cu + b + 1) - c0;
+    pos = __ldg(a.pos + b);
+    if (n <= 0 || n > a.max_new || n * a.G > kPnRows) return 0;
+    const int64_t end = (int64_t)pos + n;
+    const int kend = (int)(end < 0 ? 0 : end > a.cap ? a.cap : end);
+    return max(1, (kend + kPnKeys - 1) / kPnKeys);
 }
+
+// A place in the batch's list of chunks.
+struct PnCursor {
+    int b, h, c, nch, c0, n, pos;
+    __device__ __forceinline__ void begin(const PnArgs& a, int64_t in_sequence) {
+        nch = pn_chunks(a, b, c0, n, pos);
+        h = (int)(in_sequence / nch);
+        c = (int)(in_sequence - (int64_t)h * nch);
+    }
+    __device__ __forceinline__ void next(const PnArgs& a) {
+        if (++c < nch) return;
+        c = 0;
+        if (++h < a.N * a.hkv_s) return;
+        h = 0;
+        do {
+            ++b;
+            nch = b < a.B ? pn_chunks(a, b, c0, n, pos) : 1;
+        } while (nch == 0);
+    }
+    __device__ __forceinline__ int kend(const PnArgs& a) const {
+        const int64_t end = (int64_t)pos + n;
+        return (int)(end < 0 ? 0 : end > a.cap ? a.cap : end);
+    }
+};
+
+__device__ __forceinline__ void mma_e4m3_16832(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint16_t x) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+    return r;
+}
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
+    float2 r;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Four values, scaled, in two e4m3 terms each. What is not finite becomes NaN.
+__device__ __forceinline__ void two_terms(uint2 x, float by, uint32_t& hi, uint32_t& lo) {
+    const float2 p = unpack_bf16x2(x.x), q = unpack_bf16x2(x.y);
+    float f[4] = {p.x * by, p.y * by, q.x * by, q.y * by};
+    uint16_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        h[i] = to_e4m3x2(f[2 * i], f[2 * i + 1]);
+        const float2 back = f16x2_to_float2(e4m3_to_f16x2(h[i]));
+        l[i] = to_e4m3x2(f[2 * i] - back.x, f[2 * i + 1] - back.y);
+        if (!(fabsf(f[2 * i]) < INFINITY)) h[i] |= 0x7f;
+        if (!(fabsf(f[2 * i + 1]) < INFINITY)) h[i] |= 0x7f00;
+    }
+    hi = (uint32_t)h[0] | (uint32_t)h[1] << 16;
+    lo = (uint32_t)l[0] | (uint32_t)l[1] << 16;
+}
+
+// The power of two that brings a row's largest magnitude to 128 .. 256.
+__device__ __forceinline__ float row_scale(float most) {
+    const int e = (int)(__float_as_uint(most) >> 23);               // biased; 0: zero or subnormal, 255: infinite
+    const int k = min(254, 127 + 7 + 127 - e);
+    return most > 0.f ? __uint_as_float((uint32_t)k << 23) : 1.f;
+}
+
+template <int D>
+struct PnWarp {
+    const PnArgs& a;
+    unsigned char* ring;                  // the warp's stages: K, then V
+    uint64_t* kfull;
+    uint64_t* vfull;
+    float* scales;                        // [STAGES][4]: of K for both halves of the chunk, of V
+    int* valid;                           // [STAGES] halves whose page is there
+    volatile int* abort;
+    int lane;
+    PnCursor ahead;                       // the next chunk to be loaded
+    int64_t to_load;                      // chunks not loaded yet
+    uint32_t loads, done;                 // chunks loaded, worked on
+    int tile, off, mask, shard;           // of the chunk whose keys were loaded last
+
+    static constexpr int TILE = PnShape<D>::TILE, S = PnShape<D>::STAGES;
+
+    // 16-byte unit u of row r of a tile, as the copies' swizzle puts it
+    __device__ __forceinline__ static uint32_t at(int r, int u) {
+        if constexpr (D == 128) return r * 128 + ((u ^ (r & 7)) << 4);
+        return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+    }
+
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, a.status));
+    }
+
+    // Starts the copies of the next chunk's keys and scales; load_v: of its values.
+    __device__ __forceinline__ void load_k() {
+        const int s = loads % S, key = kPnKeys * ahead.c + 16 * (lane & 1), page = 1 << a.bits;
+        shard = ahead.h / a.hkv_s;
+        const int kv = ahead.h - shard * a.hkv_s;
+        bool there = false;
+        if (lane < 4 && key < ahead.kend(a)) {
+            const int pid = __ldg(a.pages + (int64_t)ahead.b * a.width + (key >> a.bits));
+            there = pid >= 0 && pid < a.n_pages;
+            if (!there) set_status(a.status, TP_ERR_CAPACITY);
+            tile = pid * a.hkv_s + kv;
+        }
+        mask = __ballot_sync(0xffffffffu, there) & 3;
+        off = key & (page - 1);
+        if (lane < 4) {
+            if (there) {
+                const float* src = (lane < 2 ? a.ks[shard] : a.vs[shard]) + tile;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(scales + 4 * s + lane)), "l"(src) : "memory");
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(kfull + s)) : "memory");
+        }
+        if (lane == 0) valid[s] = mask;
+        copies(&a.tk[shard], ring + s * 2 * TILE, kfull + s);
+    }
+    __device__ __forceinline__ void load_v() {
+        const int s = loads % S;
+        copies(&a.tv[shard], ring + s * 2 * TILE + TILE, vfull + s);
+        ++loads;
+        if (--to_load > 0) ahead.next(a);
+    }
+    __device__ __forceinline__ void copies(const CUtensorMap* m, unsigned char* dst, uint64_t* bar) {
+        const bool two = a.bits == 4;                       // pages of 16: a box for each half
+        const int boxes = two ? __popc(mask) : mask & 1;
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * (two ? TILE / 2 : TILE));
+        __syncwarp();
+        if (lane < (two ? 2 : 1) && (mask >> lane & 1)) tma_load_3d_keep(dst + lane * (TILE / 2), m, 0, off, tile, bar);
+    }
+
+    // The values of a chunk that some row does not see whole: what is not finite counts for the rows that see it (their sums
+    // become NaN), and is taken out; so are the rows behind the last key. first: the chunk's first key.
+    template <int NT>
+    __device__ __forceinline__ void clean(unsigned char* v, int first, int kend, int there, const int (&lim)[NT][2], float (&o)[NT][D / 16][4]) {
+        const bool gone = first + lane >= kend || !(there >> (lane >> 4) & 1);
+        int found = 0;
+        auto bad4 = [](uint32_t x) { return __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu); };
+#pragma unroll 1
+        for (int u = 0; u < D / 16; ++u) {
+            uint4* p = reinterpret_cast<uint4*>(v + at(lane, u));
+            if (gone) *p = make_uint4(0, 0, 0, 0);
+            else {
+                const uint4 x = *p;
+                found |= (bad4(x.x) | bad4(x.y) | bad4(x.z) | bad4(x.w)) != 0;
+            }
+        }
+        const unsigned rows = __ballot_sync(0xffffffffu, found);
+        if (rows) {
+            const int g = lane >> 2;
+            for (int k = 0; k < kPnKeys; ++k) {
+                if (!(rows >> k & 1)) continue;
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    const unsigned char* p = v + at(k, mt) + 2 * g;
+                    const bool n0 = (p[0] & 0x7f) == 0x7f, n1 = (p[1] & 0x7f) == 0x7f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (n0 && first + k <= lim[nt][i]) o[nt][mt][i] = NAN;
+                            if (n1 && first + k <= lim[nt][i]) o[nt][mt][2 + i] = NAN;
+                        }
+                }
+            }
+            __syncwarp();
+            if (found)
+#pragma unroll 1
+                for (int u = 0; u < D / 16; ++u) {
+                    uint4* p = reinterpret_cast<uint4*>(v + at(lane, u));
+                    const uint4 x = *p;
+                    *p = make_uint4(x.x & ~bad4(x.x), x.y & ~bad4(x.y), x.z & ~bad4(x.z), x.w & ~bad4(x.w));
+                }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+    }
+
+    // Chunks w.x0 .. w.x1 - 1 of a head of the sequence at cur. Where that is all of them the result goes to out, else to
+    // slot (O [rows][D], then (m, l)).
+    template <int NT>
+    __device__ __forceinline__ bool head(const PnCursor& cur, const PnPiece& w, float* slot) {
+        const int g = lane >> 2, t = lane & 3, rows = cur.n * a.G, kend = cur.kend(a);
+        const int r = w.h / a.hkv_s, kvh = w.h - r * a.hkv_s;
+        // the queries: rows 8 nt + g as columns of the products
+        uint32_t qh[NT][D / 32][2], ql[NT][D / 32][2];
+        float factor[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = 8 * nt + g, i = row / a.G;
+            const bf16* src = a.q + (((int64_t)r * a.T + cur.c0 + i) * a.hq_s + kvh * a.G + (row - i * a.G)) * D + 4 * t;
+            uint2 x[D / 32][2];
+            float most = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[ks][j] = row < rows ? *reinterpret_cast<const uint2*>(src + 32 * ks + 16 * j) : make_uint2(0, 0);
+                    const float2 f = unpack_bf16x2(x[ks][j].x), f2 = unpack_bf16x2(x[ks][j].y);
+                    most = fmaxf(fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f2.x), fabsf(f2.y)));
+                }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const float by = row_scale(most), back = a.scale_log2 / by;
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) two_terms(x[ks][j], by, qh[nt][ks][j], ql[nt][ks][j]);
+#pragma unroll
+            for (int i2 = 0; i2 < 2; ++i2) {
+                const int mine = 8 * nt + 2 * t + i2, tok = mine / a.G;        // the lane's rows of S^T and O^T
+                factor[nt][i2] = __shfl_sync(0xffffffffu, back, (2 * t + i2) * 4);
+                const int64_t p = (int64_t)cur.pos + tok;
+                lim[nt][i2] = mine < rows && p >= 0 && p < a.cap ? (int)p : -1;
+            }
+        }
+        float o[NT][D / 16][4] = {}, m[NT][2], l[NT][2], ref = 0.f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+
+        for (int c = w.x0; c < w.x1; ++c, ++done) {
+            const int s = done % S;
+            const uint32_t par = (done / S) & 1;
+            unsigned char* kt = ring + s * 2 * TILE;
+            if (!wait(kfull + s, par)) return false;
+            float sc[NT][2][4], sl[NT][2][4];
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc[nt][kk][i] = sl[nt][kk][i] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks) {
+                    uint32_t x[4];
+                    // matrices: keys 0-7 and 8-15 of the first sixteen bytes, then of the others
+                    ldsm4(x, smem_u32(kt + at(16 * kk + (lane & 15), 2 * ks + (lane >> 4))));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_e4m3_16832(sc[nt][kk], x, qh[nt][ks][0], qh[nt][ks][1]);
+                        mma_e4m3_16832(sl[nt][kk], x, ql[nt][ks][0], ql[nt][ks][1]);
+                    }
+                }
+            }
+            const int there = *(volatile int*)(valid + s);
+            const float4 pg = *reinterpret_cast<const float4*>(scales + 4 * s);
+            const float pk[2] = {pg.x, pg.y}, pv[2] = {pg.z, pg.w};
+            __syncwarp();
+            if (to_load > 0) load_k();
+
+            const int first = kPnKeys * c;
+            const bool whole = first + kPnKeys <= cur.pos + 1 && there == 3;   // every row sees every key
+            float top[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int kk = j >> 1, e = i + 2 * (j & 1);
+                        x[j] = (sc[nt][kk][e] + sl[nt][kk][e]) * (factor[nt][i] * pk[kk]);
+                        if (!whole) {
+                            const int key = first + 16 * kk + 8 * (j & 1) + g;
+                            if (key > lim[nt][i] || !(there >> kk & 1)) x[j] = -INFINITY;
+                        }
+                        sc[nt][kk][e] = x[j];
+                    }
+                    float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                    y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                    top[nt][i] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                }
+            // the largest scale of values so far, and a moved maximum, scale the sums
+            float most_v = ref;
+            if (there & 1) most_v = fmaxf(most_v, pv[0]);
+            if (there & 2) most_v = fmaxf(most_v, pv[1]);
+            bool moved = most_v > ref;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) moved |= top[nt][0] > m[nt][0] + kPnRescale || top[nt][1] > m[nt][1] + kPnRescale;
+            if (__any_sync(0xffffffffu, moved)) {
+                const float down = most_v > ref ? ref / most_v : 1.f;
+                ref = most_v;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const bool grow = top[nt][i] > m[nt][i] + kPnRescale;
+                        const float f = grow ? ex2_approx(m[nt][i] - top[nt][i]) : 1.f;      // 0 when m is -inf
+                        if (grow) m[nt][i] = top[nt][i];
+                        l[nt][i] *= f;
+#pragma unroll
+                        for (int mt = 0; mt < D / 16; ++mt) {
+                            o[nt][mt][i] *= f * down;
+                            o[nt][mt][2 + i] *= f * down;
+                        }
+                    }
+            }
+            const float up = ref > 0.f ? 1.f / ref : 0.f;
+            uint32_t pb[NT][2][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const float by = there >> kk & 1 ? pv[kk] * up : 0.f;
+                    float p[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[e] = ex2_approx(sc[nt][kk][e] - (e & 1 ? m1 : m0));
+                        l[nt][e & 1] += p[e];
+                        p[e] *= by;
+                    }
+                    pb[nt][kk][0] = movmatrix(pack_f16x2(p[0], p[1]));
+                    pb[nt][kk][1] = movmatrix(pack_f16x2(p[2], p[3]));
+                }
+            }
+            if (!wait(vfull + s, par)) return false;
+            unsigned char* vt = kt + TILE;
+            if (!whole) clean<NT>(vt, first, kend, there, lim, o);
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                for (int mt = 0; mt < D / 16; mt += 2) {
+                    uint32_t x[4];
+                    // matrices: keys 0-7 and 8-15 of sixteen features, then of the next sixteen
+                    ldsm4_t(x, smem_u32(vt + at(16 * kk + (lane & 15), mt + (lane >> 4))));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t y0 = __byte_perm(x[2 * j], 0, 0x3120), y1 = __byte_perm(x[2 * j + 1], 0, 0x3120);
+                        const uint32_t a0 = e4m3_to_f16x2((uint16_t)y0), a1 = e4m3_to_f16x2((uint16_t)(y0 >> 16));
+                        const uint32_t a2 = e4m3_to_f16x2((uint16_t)y1), a3 = e4m3_to_f16x2((uint16_t)(y1 >> 16));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][mt + j], a0, a1, a2, a3, pb[nt][kk][0], pb[nt][kk][1]);
+                    }
+                }
+            __syncwarp();
+            if (to_load > 0) load_v();
+        }
+
+        const bool all = w.x0 == 0 && w.x1 == w.nch;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float x = l[nt][i];
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                const int row = 8 * nt + 2 * t + i;
+                if (row >= rows) continue;
+                if (all) {
+                    const int tok = row / a.G;
+                    const int64_t p = (int64_t)cur.pos + tok;
+                    const bool none = x == 0.f || p < 0 || p >= a.cap;      // no key seen, no such place: zeros
+                    const float f = ref / x;
+                    bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + 2 * g;
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt)
+                        *reinterpret_cast<uint32_t*>(dst + 16 * mt) =
+                            none ? 0u : pack_bf16x2(o[nt][mt][i] * f, o[nt][mt][2 + i] * f);
+                } else {
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt)
+                        *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i] * ref, o[nt][mt][2 + i] * ref);
+                    if (g == 0) reinterpret_cast<float2*>(slot + kPnRows * D)[row] = make_float2(m[nt][i], x);
+                }
+            }
+        return true;
+    }
+};
+
+// One warp: a row's pieces joined, o = sum_i 2^(m_i - m) O_i and l likewise;
+// `get(i, ml, x)` reads piece i: (m, l), and the lane's D / 32 elements of O.
+template <int D, typename Get>
+__device__ __forceinline__ float2 pn_join(int n, Get get, float (&o)[D / 32]) {
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+        float2 ml;
+        float x[D / 32];
+        get(i, ml, x);
+        const float top = fmaxf(m, ml.x);
+        const float a = m == -INFINITY ? 0.f : ex2_approx(m - top), b = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+        m = top;
+        l = l * a + ml.y * b;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) o[k] = o[k] * a + x[k] * b;
+    }
+    return make_float2(m, l);
+}
+
+template <int D>
+__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int c0, int row, int lane, float l, const float (&o)[D / 32]) {
+    const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, tok = row / a.G;
+    const int64_t at = (int64_t)__ldg(a.pos + p.b) + tok;
+    const bool none = l == 0.f || at < 0 || at >= a.cap;
+    bf16* dst = a.out + (((int64_t)r * a.T + c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + lane * (D / 32);
+    const float f = 1.f / l;
+    uint32_t y[D / 64];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
+    if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = y[0];
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_constant__ PnArgs a) {
+    using Sh = PnShape<D>;
+    constexpr int S = Sh::STAGES, E = D / 32;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    // head: barriers, scales, masks, pieces
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                                    // [warps][2][S]
+    float* scales = reinterpret_cast<float*>(smem + 512);                                  // [warps][S][4]
+    int* valid = reinterpret_cast<int*>(smem + 1024);                                      // [warps][S]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 1152);
+    int* s_last = reinterpret_cast<int*>(smem + 1156);                                     // [2]
+    int* s_runs = reinterpret_cast<int*>(smem + 1164);
+    int64_t* s_warp = reinterpret_cast<int64_t*>(smem + 1168);                             // [warps + 1]
+    int64_t* s_at = reinterpret_cast<int64_t*>(smem + 1248);                               // [warps] place in the sequence
+    int* s_seq = reinterpret_cast<int*>(smem + 1312);                                      // [warps]
+    PnPiece* pieces = reinterpret_cast<PnPiece*>(smem + 1344);                             // [warps][2]
+    PnPiece* runs = pieces + 2 * kPnWarps;                                                 // [2 warps]
+    int* run_from = reinterpret_cast<int*>(runs + 2 * kPnWarps);                           // [2 warps] first piece of the run, and behind the last
+    static_assert(1344 + 4 * kPnWarps * sizeof(PnPiece) + 2 * 2 * kPnWarps * 4 <= Sh::HEAD, "the head's words");
+    static_assert(kPnWarps * 2 * S * 8 <= 512 && kPnWarps * S * 16 <= 512 && kPnWarps * S * 4 <= 128, "the head's words");
+    unsigned char* ring0 = smem + Sh::HEAD;
+    unsigned char* slots = ring0 + Sh::RING;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kPnWarps * 2 * S; ++i) mbar_init(bars + i, (i / S) & 1 ? 1 : 5);
+        *abort_flag = (smem_u32(ring0) & 1023u) ? 1 : 0;
+        if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
+        fence_mbar_init();
+    }
+    if (tid < 2 * kPnWarps) pieces[tid].x1 = 0;
+    pdl_trigger();
+    pdl_wait();
+
+    // ---- the CTA's and its warps' place in the list of chunks
+    const int heads = a.N * a.hkv_s;
+    int bad = 0;
+    int64_t sum = 0;
+    for (int b = tid; b < a.B; b += kPnThreads) {
+        int c0, n, pos;
+        sum += (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
+        bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
+        if (blockIdx.x == 0 && n > 0) {
+            if (n > a.max_new) set_status(a.status, TP_ERR_SHAPE);
+            else if (pos < 0 || (int64_t)pos + n > a.cap) set_status(a.status, TP_ERR_CAPACITY);
+        }
+    }
+    auto warp_sum64 = [&](int64_t x) {
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
+    sum = warp_sum64(sum);
+    if (lane == 0) s_warp[warp] = sum;
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
+        return;
+    }
+    int64_t total = 0;
+    for (int i = 0; i < kPnWarps; ++i) total += s_warp[i];
+    // a chunk for each warp at least: fewer CTAs then have fewer pieces to join
+    const int ctas = (int)min((int64_t)gridDim.x, (total + kPnWarps - 1) / kPnWarps);
+    if ((int)blockIdx.x >= ctas) return;
+    const int64_t from = total * blockIdx.x / ctas, upto = total * (blockIdx.x + 1) / ctas;
+    auto warp_from = [&](int w) { return from + (upto - from) * w / kPnWarps; };
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPnThreads) {
+        const int b = b0 + tid;
+        int c0, n, pos;
+        const int64_t mine = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
+        int64_t x = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += v;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        int64_t before = base + x - mine;
+        for (int i = 0; i < kPnWarps; ++i) {
+            if (i < warp) before += s_warp[i];
+            base += s_warp[i];
+        }
+        if (mine)
+            for (int w = 0; w < kPnWarps; ++w) {
+                const int64_t at = warp_from(w);
+                if (at >= before && at < before + mine) {
+                    s_seq[w] = b;
+                    s_at[w] = at - before;
+                }
+            }
+    }
+    __syncthreads();
+
+    // ---- a warp's run
+    const int64_t w0 = warp_from(warp), w1 = warp_from(warp + 1);
+    bool ok = !*abort_flag;
+    if (w1 > w0) {
+        PnWarp<D> x{a, ring0 + warp * S * 2 * Sh::TILE, bars + warp * 2 * S, bars + warp * 2 * S + S, scales + warp * S * 4, valid + warp * S,
+                    abort_flag, lane, {}, w1 - w0, 0, 0, 0, 0, 0, 0};
+        x.ahead.b = s_seq[warp];
+        x.ahead.begin(a, s_at[warp]);
+        PnCursor cur = x.ahead;
+        for (int i = 0; ok && i < S && x.to_load > 0; ++i) {
+            x.load_k();
+            x.load_v();
+        }
+        int64_t at = w0;
+        while (ok && at < w1) {
+            PnPiece p;
+            p.start = at - cur.c;
+            p.b = cur.b;
+            p.h = cur.h;
+            p.x0 = cur.c;
+            p.nch = cur.nch;
+            p.x1 = (int)min((int64_t)cur.nch, cur.c + (w1 - at));
+            const int second = p.x0 == 0;
+            float* slot = reinterpret_cast<float*>(second ? ring0 + warp * S * 2 * Sh::TILE : slots + warp * Sh::SLOT);
+            if (cur.n * a.G <= 8) ok = x.template head<1>(cur, p, slot);
+            else ok = x.template head<2>(cur, p, slot);
+            if (!ok) break;
+            if (lane == 0 && !(p.x0 == 0 && p.x1 == p.nch)) pieces[2 * warp + second] = p;
+            at += p.x1 - p.x0;
+            if (at < w1) {
+                cur.c = cur.nch - 1;
+                cur.next(a);
+            }
+        }
+        if (!ok && lane == 0) {                      // no copy may still be landing when the CTA exits
+            volatile int no_abort = 0;
+            for (uint32_t k = x.loads > S ? x.loads - S : 0; k < x.loads + 1; ++k) {
+                if (k < x.loads) mbar_wait(x.vfull + k % S, (k / S) & 1, &no_abort, nullptr);
+                if (k < x.loads || x.to_load > 0) mbar_wait(x.kfull + k % S, (k / S) & 1, &no_abort, nullptr);
+            }
+        }
+    }
+    if (__syncthreads_or(!ok)) return;
+
+    // ---- pieces of a head, in this CTA
+    if (tid == 0) {
+        int n = 0;
+        for (int i = 0; i < 2 * kPnWarps; ++i) {
+            const PnPiece p = pieces[i];
+            if (p.x1 == 0) continue;
+            if (n && runs[n - 1].start == p.start) {
+                runs[n - 1].x1 = p.x1;
+                run_from[2 * n - 1] = i + 1;
+            } else {
+                runs[n] = p;
+                run_from[2 * n] = i;
+                run_from[2 * n + 1] = i + 1;
+                ++n;
+            }
+        }
+        *s_runs = n;
+    }
+    __syncthreads();
+    const int n_runs = *s_runs;
+    if (n_runs == 0) return;
+    for (int u = warp; u < n_runs * kPnRows; u += kPnWarps) {
+        const int k = u / kPnRows, row = u - k * kPnRows;
+        const PnPiece p = runs[k];
+        const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
+        if (row >= rows) continue;
+        const int i0 = run_from[2 * k], i1 = run_from[2 * k + 1];
+        float o[E];
+        float m = -INFINITY, l = 0.f;
+        {
+            int n = 0;
+            for (int i = i0; i < i1; ++i) n += pieces[i].x1 != 0;
+            int i = i0;
+            auto get = [&](int, float2& ml, float (&y)[E]) {
+                while (pieces[i].x1 == 0) ++i;
+                const float* slot = reinterpret_cast<const float*>(i & 1 ? ring0 + (i >> 1) * S * 2 * Sh::TILE : slots + (i >> 1) * Sh::SLOT);
+                ++i;
+                ml = reinterpret_cast<const float2*>(slot + kPnRows * D)[row];
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = slot[row * D + lane * E + e];
+            };
+            const float2 r = pn_join<D>(n, get, o);
+            m = r.x;
+            l = r.y;
+        }
+        if (p.x0 == 0 && p.x1 == p.nch) {
+            pn_store<D>(a, p, c0, row, lane, l, o);
+        } else {
+            const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * kPnRows + row;
+            if (lane == 0) a.part_ml[dst] = make_float2(m, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) a.part_o[dst * D + lane * E + e] = o[e];
+        }
+    }
+
+    // ---- pieces of a head in several CTAs: the last of them joins
+    auto cta_of = [&](int64_t c) { return (int)(((c + 1) * ctas - 1) / total); };
+    __threadfence();
+    __syncthreads();
+    if (tid < 2) {
+        int last = -1;
+        const int k = tid == 0 ? 0 : n_runs - 1;            // only the first and the last run can go on elsewhere
+        const PnPiece p = runs[k];
+        if ((tid == 0 || n_runs > 1) && !(p.x0 == 0 && p.x1 == p.nch)) {
+            const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
+            if (atomicAdd(a.joined + first, 1u) == (unsigned)n - 1) {
+                a.joined[first] = 0;
+                __threadfence();
+                last = k;
+            }
+        }
+        s_last[tid] = last;
+    }
+    __syncthreads();
+    for (int j = 0; j < 2; ++j) {
+        const int k = s_last[j];
+        if (k < 0) continue;
+        const PnPiece p = runs[k];
+        const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
+        const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
+        for (int row = warp; row < rows; row += kPnWarps) {
+            float o[E];
+            auto get = [&](int i, float2& ml, float (&y)[E]) {
+                const int64_t src = ((int64_t)(first + i) * 2 + (i == 0)) * kPnRows + row;
+                ml = __ldcg(a.part_ml + src);
+                if constexpr (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + src * D) + lane);
+                    y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + src * D) + lane);
+                    y[0] = v.x, y[1] = v.y;
+                }
+            };
+            const float2 r = pn_join<D>(n, get, o);
+            pn_store<D>(a, p, c0, row, lane, r.y, o);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Every other sequence: a warp per query row and head walks the keys, 32 at a
+// time: a lane has a key for the scores and d / 32 features for the sums.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float from_e4m3(uint8_t x) { return f16x2_to_float2(e4m3_to_f16x2(x)).x; }
 
 template <int D>
 __global__ void __launch_bounds__(128) paged_rows_kernel(const __grid_constant__ PagedAttnArgs p) {
     __shared__ float sq[4][D];
     int bad = 0;
+    pdl_wait();
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) {
         const int a = p.cu[i], b = p.cu[i + 1];
         bad |= b < a || a < 0 || b > p.T || (i == 0 && a != 0);
     }
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, TP_ERR_SHAPE);
-        return;
-    }
+    if (__syncthreads_or(bad)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * 4 + warp, heads = (int64_t)p.N * p.hq_s;
     const int t = (int)(unit / heads), hh = (int)(unit - t * heads), r = hh / p.hq_s, h = hh - r * p.hq_s;
@@ -39,14 +789,11 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(const __grid_constant__
         if (p.cu[m] <= t) lo = b = m;
         else hi = m;
     }
-    if (p.cu[b + 1] - p.cu[b] > p.max_new) {
-        if (lane == 0) set_status(p.status, TP_ERR_SHAPE);
-        return;
-    }
+    const int n_new = p.cu[b + 1] - p.cu[b];
+    if (n_new > p.max_new || n_new * (p.hq_s / p.hkv_s) <= kPnRows) return;
     const int64_t pos = (int64_t)p.pos[b] + (t - p.cu[b]), cap = (int64_t)p.c.width * p.c.page;
     bf16* out = static_cast<bf16*>(p.out) + (((int64_t)r * p.T + t) * p.hq_s + h) * D;
     if (pos < 0 || pos >= cap) {
-        if (lane == 0) set_status(p.status, TP_ERR_CAPACITY);
         for (int i = lane; i < D; i += 32) out[i] = __float2bfloat16_rn(0.f);
         return;
     }
@@ -87,14 +834,87 @@ __global__ void __launch_bounds__(128) paged_rows_kernel(const __grid_constant__
     for (int x = 0; x < D / 32; ++x) out[lane + 32 * x] = __float2bfloat16_rn(any ? o[x] / l : 0.f);
 }
 
-size_t paged_workspace(int64_t max_tokens, int group, int d) { return kPagedCtrl; }
+// ---------------------------------------------------------------------------
+
+namespace {
+// Bytes [tiles][page][d], boxes of `rows` keys of a tile, swizzled over their rows' width.
+cudaError_t page_map(const void* base, int64_t d, int64_t page, int64_t tiles, int rows, CUtensorMap* out) {
+    static std::mutex mu;
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!encode) {
+            cudaDriverEntryPointQueryResult q;
+            cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", reinterpret_cast<void**>(&encode), 12000,
+                                                             cudaEnableDefault, &q);
+            if (e != cudaSuccess || !encode) return e != cudaSuccess ? e : cudaErrorNotSupported;
+        }
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)tiles};
+    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)(page * d)};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)rows, 1u};
+    cuuint32_t step[3] = {1u, 1u, 1u};
+    const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr size_t kPnMl = (size_t)kSMs * 2 * kPnRows * sizeof(float2);
+size_t pn_part(int d) { return (size_t)kSMs * 2 * kPnRows * d * sizeof(float); }
+}  // namespace
+
+size_t paged_workspace(int64_t, int, int d) { return kPagedCtrl + kPnMl + pn_part(d); }
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
+    const int G = p.hq_s / p.hkv_s;
+    const bool d128 = p.d == 128;
+    {
+        PnArgs a;
+        memset(&a, 0, sizeof a);
+        for (int r = 0; r < p.N; ++r) {
+            const int64_t tiles = (int64_t)p.c.n_pages * p.hkv_s;
+            const int rows = p.c.page < kPnKeys ? p.c.page : kPnKeys;
+            cudaError_t e = page_map(p.c.k[r], p.d, p.c.page, tiles, rows, &a.tk[r]);
+            if (e == cudaSuccess) e = page_map(p.c.v[r], p.d, p.c.page, tiles, rows, &a.tv[r]);
+            if (e != cudaSuccess) return e;
+            a.ks[r] = p.c.ks[r];
+            a.vs[r] = p.c.vs[r];
+        }
+        a.q = static_cast<const bf16*>(p.q);
+        a.out = static_cast<bf16*>(p.out);
+        a.cu = p.cu;
+        a.pos = p.pos;
+        a.pages = p.c.pages;
+        a.joined = reinterpret_cast<unsigned*>(p.ws + 256);
+        a.part_ml = reinterpret_cast<float2*>(p.ws + kPagedCtrl);
+        a.part_o = reinterpret_cast<float*>(p.ws + kPagedCtrl + kPnMl);
+        a.status = p.status;
+        a.N = p.N;
+        a.B = p.B;
+        a.T = p.T;
+        a.hq_s = p.hq_s;
+        a.hkv_s = p.hkv_s;
+        a.G = G;
+        a.bits = 31 - __builtin_clz((unsigned)p.c.page);
+        a.width = p.c.width;
+        a.n_pages = p.c.n_pages;
+        a.max_new = p.max_new;
+        a.cap = p.c.width * p.c.page;
+        a.scale_log2 = p.scale_log2;
+        void* args[] = {&a};
+        const void* fn = d128 ? reinterpret_cast<const void*>(paged_few_kernel<128>) : reinterpret_cast<const void*>(paged_few_kernel<64>);
+        const int smem = d128 ? PnShape<128>::SMEM : PnShape<64>::SMEM;
+        cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kPnThreads);
+        if (e != cudaSuccess) return e;
+    }
+    if ((int64_t)p.max_new * G <= kPnRows) return cudaSuccess;
     PagedAttnArgs a = p;
+    void* args[] = {&a};
     const int64_t units = (int64_t)a.T * a.N * a.hq_s;
-    if (a.d == 128) paged_rows_kernel<128><<<(unsigned)((units + 3) / 4), 128, 0, s>>>(a);
-    else paged_rows_kernel<64><<<(unsigned)((units + 3) / 4), 128, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(d128 ? reinterpret_cast<const void*>(paged_rows_kernel<128>) : reinterpret_cast<const void*>(paged_rows_kernel<64>), args,
+                      (int)((units + 3) / 4), 0, s, 128);
 }
 
 }  // namespace tpk
