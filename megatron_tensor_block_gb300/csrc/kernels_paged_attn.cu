@@ -23,37 +23,54 @@ namespace tpk {
 //
 // All the batch's chunks of 32 keys, sequence by sequence and head by head, are
 // one list, cut into equal runs for the CTAs (one per SM) and each of those for
-// its eight warps. Every CTA finds its place from the offsets and lengths by
-// itself. A warp works alone: its own ring of stages in shared memory, filled
-// by its own TMA copies, no barrier with another warp until its run ends. What
-// it has of a head that others have a part of is joined behind that, first in
-// shared memory, then through the workspace by the CTA that comes last.
+// its warps. Every CTA finds its place from the offsets and lengths by itself.
+// A warp works alone: its own ring of stages in shared memory, no barrier with
+// another warp but the one that copies until its run ends. What it has of a
+// head that others have a part of is joined behind that, first in shared
+// memory, then through the workspace by the CTA that comes last. One more warp
+// copies, a lane for each of the others: their page tables, scales, TMA boxes.
 //
-// Keys are the rows of the products: S^T = K Q^T (16 keys x 8 query rows) as
-// e4m3 x e4m3, with q, scaled by a power of two for each row, in two e4m3
-// terms: eight significant bits together, all that bf16 has (for elements above
-// 2^-10 of a row's largest; the others are off by 2^-18 of it). So a key's
-// bytes go from its page to the tensor cores as they are. O^T = V^T P^T as
-// fp16 x fp16: ldmatrix transposes pairs of bytes, one conversion makes two fp16
-// of them (exactly), and the weights' rounding to fp16 is 2^-11. The scale of a
-// page's keys goes into the scores, that of its values, relative to the largest
-// so far, into the weights.
+// Keys are the rows of the products, S^T = K Q^T and O^T = V^T P^T (16 x 8
+// query rows), as fp16 x fp16: one conversion makes two fp16 of two e4m3,
+// exactly; q is brought to fp16 by a power of two for each row, exactly but for
+// elements below 2^-29 of the row's largest; the weights' rounding to fp16 is
+// 2^-11. The scale of a page's keys goes into the scores, that of its values,
+// relative to the largest so far, into the weights. (e4m3 x e4m3 products of q
+// in two terms, without conversions of K here: decode of 64 68 us where this
+// took 63.)
 // ---------------------------------------------------------------------------
 
-constexpr int kPnWarps = 8, kPnThreads = 32 * kPnWarps;
 constexpr int kPnKeys = 32;               // keys of a chunk
 constexpr int kPnRows = 16;               // query rows of a sequence and KV head at most
 constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
 
-template <int D>
+struct PnPiece {                          // of a head of a sequence
+    int64_t start;                        // the head's first chunk in the batch's list
+    int b, h, x0, x1, nch;                // chunks x0 .. x1 - 1 of nch; x1 = 0: none
+};
+
+// Fifteen warps and the copying one where no sequence has more than 8 rows, else seven with twice the registers.
+template <int D, int W>
 struct PnShape {
+    static constexpr int ROWS = W == 15 ? 8 : 16;
     static constexpr int TILE = kPnKeys * D;                        // bytes of a chunk's K or V
-    static constexpr int STAGES = D == 128 ? 2 : 4;
-    static constexpr int SLOT = kPnRows * D * 4 + kPnRows * 8;       // a piece of a head: O, then (m, l)
-    static constexpr int RING = kPnWarps * STAGES * 2 * TILE;
-    static constexpr int HEAD = 4096;
-    static constexpr int SMEM = HEAD + RING + kPnWarps * SLOT;
-    static_assert(STAGES * 2 * TILE >= SLOT, "a warp's ring holds its last piece");
+    static constexpr int STAGES = (D == 128 ? 1 : 2) * (W == 15 ? 1 : 2);
+    static constexpr int SLOT = ROWS * D * 4 + ROWS * 8;             // a piece of a head: O, then (m, l)
+    static constexpr int RING = STAGES * 2 * TILE;                  // of a warp
+    static constexpr int THREADS = 32 * (W + 1);
+    struct Head {
+        uint64_t kfull[W][STAGES], kempty[W][STAGES], vfull[W][STAGES], vempty[W][STAGES];
+        float scales[W][STAGES][4];                                 // of K for both halves of the chunk, of V
+        int64_t sums[W + 1], at[W];                                 // a warp's place in its first sequence
+        PnPiece pieces[2 * W], runs[2 * W];
+        int run[2 * W][2];                                          // first piece of the run, and behind the last
+        int valid[W][STAGES];                                       // halves whose page is there
+        int seq[W], last[2], n_runs, abort;
+    };
+    static constexpr int HEAD = ((int)sizeof(Head) + 1023) & ~1023;
+    static constexpr int SMEM = HEAD + W * (RING + SLOT);
+    static_assert(RING >= SLOT, "a warp's ring holds its last piece");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 struct PnArgs {
@@ -65,17 +82,12 @@ struct PnArgs {
     const int* cu;
     const int* pos;
     const int* pages;
-    float* part_o;                        // [kSMs][2][kPnRows][D]
-    float2* part_ml;                      // [kSMs][2][kPnRows]
+    float* part_o;                        // [kSMs][2][rows][D]
+    float2* part_ml;                      // [kSMs][2][rows]
     unsigned* joined;                     // [kSMs] pieces of the head that begins in this CTA and ends in another
     int* status;
     int N, B, T, hq_s, hkv_s, G, bits, width, n_pages, max_new, cap;
     float scale_log2;
-};
-
-struct PnPiece {                          // of a head of a sequence
-    int64_t start;                        // the head's first chunk in the batch's list
-    int b, h, x0, x1, nch;                // chunks x0 .. x1 - 1 of nch; x1 = 0: none
 };
 
 // Chunks of a sequence for each head: none where it is not this kernel's.
@@ -83,7 +95,7 @@ __device__ __forceinline__ int pn_chunks(const PnArgs& a, int b, int& c0, int& n
     c0 = __ldg(a.cu + b);
     n = __ldg(a.cu + b + 1) - c0;
     pos = __ldg(a.pos + b);
-    if (n <= 0 || n > a.max_new || n * a.G > kPnRows) return 0;
+    if (n <= 0 || n > a.max_new || (int64_t)n * a.G > kPnRows) return 0;
     const int64_t end = (int64_t)pos + n;
     const int kend = (int)(end < 0 ? 0 : end > a.cap ? a.cap : end);
     return max(1, (kend + kPnKeys - 1) / kPnKeys);
@@ -113,12 +125,6 @@ struct PnCursor {
     }
 };
 
-__device__ __forceinline__ void mma_e4m3_16832(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
     asm volatile(
@@ -154,99 +160,129 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
     asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(x));
     return r;
 }
-__device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// Four values, scaled, in two e4m3 terms each. What is not finite becomes NaN.
-__device__ __forceinline__ void two_terms(uint2 x, float by, uint32_t& hi, uint32_t& lo) {
-    const float2 p = unpack_bf16x2(x.x), q = unpack_bf16x2(x.y);
-    float f[4] = {p.x * by, p.y * by, q.x * by, q.y * by};
-    uint16_t h[2], l[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        h[i] = to_e4m3x2(f[2 * i], f[2 * i + 1]);
-        const float2 back = f16x2_to_float2(e4m3_to_f16x2(h[i]));
-        l[i] = to_e4m3x2(f[2 * i] - back.x, f[2 * i + 1] - back.y);
-        if (!(fabsf(f[2 * i]) < INFINITY)) h[i] |= 0x7f;
-        if (!(fabsf(f[2 * i + 1]) < INFINITY)) h[i] |= 0x7f00;
-    }
-    hi = (uint32_t)h[0] | (uint32_t)h[1] << 16;
-    lo = (uint32_t)l[0] | (uint32_t)l[1] << 16;
-}
-
-// The power of two that brings a row's largest magnitude to 128 .. 256.
+// The power of two that brings a row's largest magnitude to 2^14 .. 2^15.
 __device__ __forceinline__ float row_scale(float most) {
     const int e = (int)(__float_as_uint(most) >> 23);               // biased; 0: zero or subnormal, 255: infinite
-    const int k = min(254, 127 + 7 + 127 - e);
+    const int k = min(254, 127 + 14 + 127 - e);
     return most > 0.f ? __uint_as_float((uint32_t)k << 23) : 1.f;
 }
 
+// 16-byte unit u of row r of a tile, as the copies' swizzle puts it.
 template <int D>
-struct PnWarp {
-    const PnArgs& a;
-    unsigned char* ring;                  // the warp's stages: K, then V
-    uint64_t* kfull;
-    uint64_t* vfull;
-    float* scales;                        // [STAGES][4]: of K for both halves of the chunk, of V
-    int* valid;                           // [STAGES] halves whose page is there
-    volatile int* abort;
-    int lane;
-    PnCursor ahead;                       // the next chunk to be loaded
-    int64_t to_load;                      // chunks not loaded yet
-    uint32_t loads, done;                 // chunks loaded, worked on
-    int tile, off, mask, shard;           // of the chunk whose keys were loaded last
+__device__ __forceinline__ uint32_t pn_unit(int r, int u) {
+    if constexpr (D == 128) return r * 128 + ((u ^ (r & 7)) << 4);
+    return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
 
-    static constexpr int TILE = PnShape<D>::TILE, S = PnShape<D>::STAGES;
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 
-    // 16-byte unit u of row r of a tile, as the copies' swizzle puts it
-    __device__ __forceinline__ static uint32_t at(int r, int u) {
-        if constexpr (D == 128) return r * 128 + ((u ^ (r & 7)) << 4);
-        return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+// The copying warp: lane w starts the copies of warp w's chunks as its stages become free.
+template <int D, int W>
+__device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int lane, int64_t todo,
+                                          int64_t in_sequence) {
+    using Sh = PnShape<D, W>;
+    constexpr int S = Sh::STAGES, TILE = Sh::TILE;
+    const int w = min(lane, W - 1), page = 1 << a.bits;
+    PnCursor at = {};
+    if (todo > 0) {
+        at.b = hd.seq[w];
+        at.begin(a, in_sequence);
     }
+    unsigned char* ring = rings + w * Sh::RING;
+    uint32_t loads = 0;
+    bool values = false;                                    // next are the values of the chunk whose keys are on the way
+    int id0 = 0, id1 = 0, mask = 0, off = 0, shard = 0, tile0 = 0, tile1 = 0;
+    uint64_t since = global_ns();
+    auto copies = [&](const CUtensorMap* m, unsigned char* dst, uint64_t* bar) {
+        if (a.bits == 4) {                                  // pages of 16: a box for each half
+            mbar_arrive_expect_tx(bar, __popc(mask) * (TILE / 2));
+            if (mask & 1) tma_load_3d_keep(dst, m, 0, 0, tile0, bar);
+            if (mask & 2) tma_load_3d_keep(dst + TILE / 2, m, 0, 0, tile1, bar);
+        } else {
+            mbar_arrive_expect_tx(bar, (mask & 1) * TILE);
+            if (mask & 1) tma_load_3d_keep(dst, m, 0, off, tile0, bar);
+        }
+    };
+    while (__any_sync(0xffffffffu, todo > 0)) {
+        const int s = loads % S;
+        const bool go = todo > 0 && mbar_test(values ? &hd.vempty[w][s] : &hd.kempty[w][s], ((loads / S) & 1) ^ 1);
+        if (go && !values) {
+            const int key = kPnKeys * at.c, kend = at.kend(a);
+            shard = at.h / a.hkv_s;
+            const int kv = at.h - shard * a.hkv_s;
+            const int* row = a.pages + (int64_t)at.b * a.width;
+            const bool in0 = key < kend, in1 = key + 16 < kend;
+            id0 = in0 ? __ldg(row + (key >> a.bits)) : -1;
+            id1 = in1 ? (a.bits == 4 ? __ldg(row + (key >> 4) + 1) : id0) : -1;
+            mask = (id0 >= 0 && id0 < a.n_pages) | (id1 >= 0 && id1 < a.n_pages) << 1;
+            if ((in0 && !(mask & 1)) || (in1 && !(mask & 2))) set_status(a.status, TP_ERR_CAPACITY);
+            off = key & (page - 1);
+            tile0 = id0 * a.hkv_s + kv;
+            tile1 = id1 * a.hkv_s + kv;
+            const uint32_t to = smem_u32(&hd.scales[w][s][0]);
+            auto scale = [&](int i, const float* src) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * i), "l"(src) : "memory");
+            };
+            if (mask & 1) scale(0, a.ks[shard] + tile0), scale(2, a.vs[shard] + tile0);
+            if (mask & 2) scale(1, a.ks[shard] + tile1), scale(3, a.vs[shard] + tile1);
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&hd.kfull[w][s])) : "memory");
+            hd.valid[w][s] = mask;
+            copies(&a.tk[shard], ring + s * 2 * TILE, &hd.kfull[w][s]);
+        }
+        if (go && values) {
+            copies(&a.tv[shard], ring + s * 2 * TILE + TILE, &hd.vfull[w][s]);
+            ++loads;
+            if (--todo > 0) at.next(a);
+        }
+        if (go) values = !values;
+        if (__any_sync(0xffffffffu, go)) {
+            since = global_ns();
+        } else {
+            if (*(volatile int*)&hd.abort) break;
+            if (global_ns() - since > 2 * kWaitLimitNs) {   // (the warps' own waits run out first)
+                *(volatile int*)&hd.abort = 1;
+                set_status(a.status, TP_ERR_TIMEOUT);
+                break;
+            }
+            __nanosleep(32);
+        }
+    }
+    // no copy may still be landing when the CTA exits
+    if (lane < W && *(volatile int*)&hd.abort) {
+        volatile int no_abort = 0;
+        for (uint32_t k = loads > S ? loads - S : 0; k < loads; ++k) {
+            mbar_wait(&hd.kfull[w][k % S], (k / S) & 1, &no_abort, nullptr);
+            mbar_wait(&hd.vfull[w][k % S], (k / S) & 1, &no_abort, nullptr);
+        }
+        if (values) mbar_wait(&hd.kfull[w][loads % S], (loads / S) & 1, &no_abort, nullptr);
+    }
+}
+
+template <int D, int W>
+struct PnWarp {
+    using Sh = PnShape<D, W>;
+    const PnArgs& a;
+    typename Sh::Head& hd;
+    unsigned char* ring;                  // the warp's stages: K, then V
+    int warp, lane;
+    uint32_t done;                        // chunks worked on
+
+    static constexpr int TILE = Sh::TILE, S = Sh::STAGES;
 
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, a.status));
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, &hd.abort, a.status));
     }
-
-    // Starts the copies of the next chunk's keys and scales; load_v: of its values.
-    __device__ __forceinline__ void load_k() {
-        const int s = loads % S, key = kPnKeys * ahead.c + 16 * (lane & 1), page = 1 << a.bits;
-        shard = ahead.h / a.hkv_s;
-        const int kv = ahead.h - shard * a.hkv_s;
-        bool there = false;
-        if (lane < 4 && key < ahead.kend(a)) {
-            const int pid = __ldg(a.pages + (int64_t)ahead.b * a.width + (key >> a.bits));
-            there = pid >= 0 && pid < a.n_pages;
-            if (!there) set_status(a.status, TP_ERR_CAPACITY);
-            tile = pid * a.hkv_s + kv;
-        }
-        mask = __ballot_sync(0xffffffffu, there) & 3;
-        off = key & (page - 1);
-        if (lane < 4) {
-            if (there) {
-                const float* src = (lane < 2 ? a.ks[shard] : a.vs[shard]) + tile;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(scales + 4 * s + lane)), "l"(src) : "memory");
-            }
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(kfull + s)) : "memory");
-        }
-        if (lane == 0) valid[s] = mask;
-        copies(&a.tk[shard], ring + s * 2 * TILE, kfull + s);
-    }
-    __device__ __forceinline__ void load_v() {
-        const int s = loads % S;
-        copies(&a.tv[shard], ring + s * 2 * TILE + TILE, vfull + s);
-        ++loads;
-        if (--to_load > 0) ahead.next(a);
-    }
-    __device__ __forceinline__ void copies(const CUtensorMap* m, unsigned char* dst, uint64_t* bar) {
-        const bool two = a.bits == 4;                       // pages of 16: a box for each half
-        const int boxes = two ? __popc(mask) : mask & 1;
-        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * (two ? TILE / 2 : TILE));
+    __device__ __forceinline__ void release(uint64_t* bar) {
         __syncwarp();
-        if (lane < (two ? 2 : 1) && (mask >> lane & 1)) tma_load_3d_keep(dst + lane * (TILE / 2), m, 0, off, tile, bar);
+        if (lane == 0) mbar_arrive(bar);
     }
 
     // The values of a chunk that some row does not see whole: what is not finite counts for the rows that see it (their sums
@@ -258,7 +294,7 @@ struct PnWarp {
         auto bad4 = [](uint32_t x) { return __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu); };
 #pragma unroll 1
         for (int u = 0; u < D / 16; ++u) {
-            uint4* p = reinterpret_cast<uint4*>(v + at(lane, u));
+            uint4* p = reinterpret_cast<uint4*>(v + pn_unit<D>(lane, u));
             if (gone) *p = make_uint4(0, 0, 0, 0);
             else {
                 const uint4 x = *p;
@@ -272,7 +308,7 @@ struct PnWarp {
                 if (!(rows >> k & 1)) continue;
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) {
-                    const unsigned char* p = v + at(k, mt) + 2 * g;
+                    const unsigned char* p = v + pn_unit<D>(k, mt) + 2 * g;
                     const bool n0 = (p[0] & 0x7f) == 0x7f, n1 = (p[1] & 0x7f) == 0x7f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -287,7 +323,7 @@ struct PnWarp {
             if (found)
 #pragma unroll 1
                 for (int u = 0; u < D / 16; ++u) {
-                    uint4* p = reinterpret_cast<uint4*>(v + at(lane, u));
+                    uint4* p = reinterpret_cast<uint4*>(v + pn_unit<D>(lane, u));
                     const uint4 x = *p;
                     *p = make_uint4(x.x & ~bad4(x.x), x.y & ~bad4(x.y), x.z & ~bad4(x.z), x.w & ~bad4(x.w));
                 }
@@ -303,30 +339,30 @@ struct PnWarp {
         const int g = lane >> 2, t = lane & 3, rows = cur.n * a.G, kend = cur.kend(a);
         const int r = w.h / a.hkv_s, kvh = w.h - r * a.hkv_s;
         // the queries: rows 8 nt + g as columns of the products
-        uint32_t qh[NT][D / 32][2], ql[NT][D / 32][2];
+        uint32_t qf[NT][D / 16][2];
         float factor[NT][2];
         int lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = 8 * nt + g, i = row / a.G;
             const bf16* src = a.q + (((int64_t)r * a.T + cur.c0 + i) * a.hq_s + kvh * a.G + (row - i * a.G)) * D + 4 * t;
-            uint2 x[D / 32][2];
+            uint2 x[D / 16];
             float most = 0.f;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    x[ks][j] = row < rows ? *reinterpret_cast<const uint2*>(src + 32 * ks + 16 * j) : make_uint2(0, 0);
-                    const float2 f = unpack_bf16x2(x[ks][j].x), f2 = unpack_bf16x2(x[ks][j].y);
-                    most = fmaxf(fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f2.x), fabsf(f2.y)));
-                }
+            for (int ks = 0; ks < D / 16; ++ks) {
+                x[ks] = row < rows ? *reinterpret_cast<const uint2*>(src + 16 * ks) : make_uint2(0, 0);
+                const float2 f = unpack_bf16x2(x[ks].x), f2 = unpack_bf16x2(x[ks].y);
+                most = fmaxf(fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f2.x), fabsf(f2.y)));
+            }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const float by = row_scale(most), back = a.scale_log2 / by;
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) two_terms(x[ks][j], by, qh[nt][ks][j], ql[nt][ks][j]);
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const float2 f = unpack_bf16x2(x[ks].x), f2 = unpack_bf16x2(x[ks].y);
+                qf[nt][ks][0] = pack_f16x2(f.x * by, f.y * by);
+                qf[nt][ks][1] = pack_f16x2(f2.x * by, f2.y * by);
+            }
 #pragma unroll
             for (int i2 = 0; i2 < 2; ++i2) {
                 const int mine = 8 * nt + 2 * t + i2, tok = mine / a.G;        // the lane's rows of S^T and O^T
@@ -339,12 +375,15 @@ struct PnWarp {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
 
+        // the lane's row of a half's sixteen, and its first or second unit of two; units 2 i on: bits of the address exchanged
+        const uint32_t unit = pn_unit<D>(lane & 15, lane >> 4);
         for (int c = w.x0; c < w.x1; ++c, ++done) {
             const int s = done % S;
             const uint32_t par = (done / S) & 1;
             unsigned char* kt = ring + s * 2 * TILE;
-            if (!wait(kfull + s, par)) return false;
-            float sc[NT][2][4], sl[NT][2][4];
+            const uint32_t at = smem_u32(kt) + unit;
+            if (!wait(&hd.kfull[warp][s], par)) return false;
+            float sc[NT][2][4], sl[NT][2][4];                       // two sums each: shorter chains
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
@@ -352,22 +391,25 @@ struct PnWarp {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) sc[nt][kk][i] = sl[nt][kk][i] = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ++ks) {
+                for (int ks = 0; ks < D / 16; ks += 2) {
                     uint32_t x[4];
-                    // matrices: keys 0-7 and 8-15 of the first sixteen bytes, then of the others
-                    ldsm4(x, smem_u32(kt + at(16 * kk + (lane & 15), 2 * ks + (lane >> 4))));
+                    // matrices: keys 0-7 and 8-15 of sixteen features, then of the next sixteen. A lane's four bytes are
+                    // elements 2 t, 2 t + 1 and 2 t + 8, 2 t + 9 of the products' sum, as q is laid out too.
+                    ldsm4(x, (at ^ (ks << 4)) + 16 * kk * D);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_e4m3_16832(sc[nt][kk], x, qh[nt][ks][0], qh[nt][ks][1]);
-                        mma_e4m3_16832(sl[nt][kk], x, ql[nt][ks][0], ql[nt][ks][1]);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t a0 = e4m3_to_f16x2((uint16_t)x[2 * j]), a2 = e4m3_to_f16x2((uint16_t)(x[2 * j] >> 16));
+                        const uint32_t a1 = e4m3_to_f16x2((uint16_t)x[2 * j + 1]), a3 = e4m3_to_f16x2((uint16_t)(x[2 * j + 1] >> 16));
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16_16816(j ? sl[nt][kk] : sc[nt][kk], a0, a1, a2, a3, qf[nt][ks + j][0], qf[nt][ks + j][1]);
                     }
                 }
             }
-            const int there = *(volatile int*)(valid + s);
-            const float4 pg = *reinterpret_cast<const float4*>(scales + 4 * s);
+            const int there = *(volatile int*)&hd.valid[warp][s];
+            const float4 pg = *reinterpret_cast<const float4*>(&hd.scales[warp][s][0]);
             const float pk[2] = {pg.x, pg.y}, pv[2] = {pg.z, pg.w};
-            __syncwarp();
-            if (to_load > 0) load_k();
+            release(&hd.kempty[warp][s]);
 
             const int first = kPnKeys * c;
             const bool whole = first + kPnKeys <= cur.pos + 1 && there == 3;   // every row sees every key
@@ -436,16 +478,15 @@ struct PnWarp {
                     pb[nt][kk][1] = movmatrix(pack_f16x2(p[2], p[3]));
                 }
             }
-            if (!wait(vfull + s, par)) return false;
-            unsigned char* vt = kt + TILE;
-            if (!whole) clean<NT>(vt, first, kend, there, lim, o);
+            if (!wait(&hd.vfull[warp][s], par)) return false;
+            if (!whole) clean<NT>(kt + TILE, first, kend, there, lim, o);
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
                 for (int mt = 0; mt < D / 16; mt += 2) {
                     uint32_t x[4];
                     // matrices: keys 0-7 and 8-15 of sixteen features, then of the next sixteen
-                    ldsm4_t(x, smem_u32(vt + at(16 * kk + (lane & 15), mt + (lane >> 4))));
+                    ldsm4_t(x, (at ^ (mt << 4)) + TILE + 16 * kk * D);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t y0 = __byte_perm(x[2 * j], 0, 0x3120), y1 = __byte_perm(x[2 * j + 1], 0, 0x3120);
@@ -455,8 +496,7 @@ struct PnWarp {
                         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][mt + j], a0, a1, a2, a3, pb[nt][kk][0], pb[nt][kk][1]);
                     }
                 }
-            __syncwarp();
-            if (to_load > 0) load_v();
+            release(&hd.vempty[warp][s]);
         }
 
         const bool all = w.x0 == 0 && w.x1 == w.nch;
@@ -484,7 +524,7 @@ struct PnWarp {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i] * ref, o[nt][mt][2 + i] * ref);
-                    if (g == 0) reinterpret_cast<float2*>(slot + kPnRows * D)[row] = make_float2(m[nt][i], x);
+                    if (g == 0) reinterpret_cast<float2*>(slot + Sh::ROWS * D)[row] = make_float2(m[nt][i], x);
                 }
             }
         return true;
@@ -527,36 +567,27 @@ __device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int 
     else *reinterpret_cast<uint32_t*>(dst) = y[0];
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_constant__ PnArgs a) {
-    using Sh = PnShape<D>;
-    constexpr int S = Sh::STAGES, E = D / 32;
+template <int D, int W>
+__global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(const __grid_constant__ PnArgs a) {
+    using Sh = PnShape<D, W>;
+    constexpr int S = Sh::STAGES, E = D / 32, THREADS = Sh::THREADS, WARPS = W + 1;
     extern __shared__ __align__(1024) unsigned char smem[];
-    // head: barriers, scales, masks, pieces
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem);                                    // [warps][2][S]
-    float* scales = reinterpret_cast<float*>(smem + 512);                                  // [warps][S][4]
-    int* valid = reinterpret_cast<int*>(smem + 1024);                                      // [warps][S]
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + 1152);
-    int* s_last = reinterpret_cast<int*>(smem + 1156);                                     // [2]
-    int* s_runs = reinterpret_cast<int*>(smem + 1164);
-    int64_t* s_warp = reinterpret_cast<int64_t*>(smem + 1168);                             // [warps + 1]
-    int64_t* s_at = reinterpret_cast<int64_t*>(smem + 1248);                               // [warps] place in the sequence
-    int* s_seq = reinterpret_cast<int*>(smem + 1312);                                      // [warps]
-    PnPiece* pieces = reinterpret_cast<PnPiece*>(smem + 1344);                             // [warps][2]
-    PnPiece* runs = pieces + 2 * kPnWarps;                                                 // [2 warps]
-    int* run_from = reinterpret_cast<int*>(runs + 2 * kPnWarps);                           // [2 warps] first piece of the run, and behind the last
-    static_assert(1344 + 4 * kPnWarps * sizeof(PnPiece) + 2 * 2 * kPnWarps * 4 <= Sh::HEAD, "the head's words");
-    static_assert(kPnWarps * 2 * S * 8 <= 512 && kPnWarps * S * 16 <= 512 && kPnWarps * S * 4 <= 128, "the head's words");
-    unsigned char* ring0 = smem + Sh::HEAD;
-    unsigned char* slots = ring0 + Sh::RING;
+    typename Sh::Head& hd = *reinterpret_cast<typename Sh::Head*>(smem);
+    unsigned char* rings = smem + Sh::HEAD;
+    unsigned char* slots = rings + W * Sh::RING;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
-        for (int i = 0; i < kPnWarps * 2 * S; ++i) mbar_init(bars + i, (i / S) & 1 ? 1 : 5);
-        *abort_flag = (smem_u32(ring0) & 1023u) ? 1 : 0;
-        if (*abort_flag) set_status(a.status, TP_ERR_ALIGN);
+        for (int i = 0; i < W * S; ++i) {
+            mbar_init(&hd.kfull[0][0] + i, 2);               // the copies, and the scales
+            mbar_init(&hd.kempty[0][0] + i, 1);
+            mbar_init(&hd.vfull[0][0] + i, 1);
+            mbar_init(&hd.vempty[0][0] + i, 1);
+        }
+        hd.abort = (smem_u32(rings) & 1023u) ? 1 : 0;
+        if (hd.abort) set_status(a.status, TP_ERR_ALIGN);
         fence_mbar_init();
     }
-    if (tid < 2 * kPnWarps) pieces[tid].x1 = 0;
+    if (tid < 2 * W) hd.pieces[tid].x1 = 0;
     pdl_trigger();
     pdl_wait();
 
@@ -564,7 +595,7 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
     const int heads = a.N * a.hkv_s;
     int bad = 0;
     int64_t sum = 0;
-    for (int b = tid; b < a.B; b += kPnThreads) {
+    for (int b = tid; b < a.B; b += THREADS) {
         int c0, n, pos;
         sum += (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
@@ -578,20 +609,20 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
         return x;
     };
     sum = warp_sum64(sum);
-    if (lane == 0) s_warp[warp] = sum;
+    if (lane == 0) hd.sums[warp] = sum;
     if (__syncthreads_or(bad)) {
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
         return;
     }
     int64_t total = 0;
-    for (int i = 0; i < kPnWarps; ++i) total += s_warp[i];
+    for (int i = 0; i < WARPS; ++i) total += hd.sums[i];
     // a chunk for each warp at least: fewer CTAs then have fewer pieces to join
-    const int ctas = (int)min((int64_t)gridDim.x, (total + kPnWarps - 1) / kPnWarps);
+    const int ctas = (int)min((int64_t)gridDim.x, (total + W - 1) / W);
     if ((int)blockIdx.x >= ctas) return;
     const int64_t from = total * blockIdx.x / ctas, upto = total * (blockIdx.x + 1) / ctas;
-    auto warp_from = [&](int w) { return from + (upto - from) * w / kPnWarps; };
+    auto warp_from = [&](int w) { return from + (upto - from) * w / W; };
     int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kPnThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
         const int b = b0 + tid;
         int c0, n, pos;
         const int64_t mine = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
@@ -601,36 +632,37 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
             if (lane >= o) x += v;
         }
         __syncthreads();
-        if (lane == 31) s_warp[warp] = x;
+        if (lane == 31) hd.sums[warp] = x;
         __syncthreads();
         int64_t before = base + x - mine;
-        for (int i = 0; i < kPnWarps; ++i) {
-            if (i < warp) before += s_warp[i];
-            base += s_warp[i];
+        for (int i = 0; i < WARPS; ++i) {
+            if (i < warp) before += hd.sums[i];
+            base += hd.sums[i];
         }
         if (mine)
-            for (int w = 0; w < kPnWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const int64_t at = warp_from(w);
                 if (at >= before && at < before + mine) {
-                    s_seq[w] = b;
-                    s_at[w] = at - before;
+                    hd.seq[w] = b;
+                    hd.at[w] = at - before;
                 }
             }
     }
     __syncthreads();
 
     // ---- a warp's run
-    const int64_t w0 = warp_from(warp), w1 = warp_from(warp + 1);
-    bool ok = !*abort_flag;
-    if (w1 > w0) {
-        PnWarp<D> x{a, ring0 + warp * S * 2 * Sh::TILE, bars + warp * 2 * S, bars + warp * 2 * S + S, scales + warp * S * 4, valid + warp * S,
-                    abort_flag, lane, {}, w1 - w0, 0, 0, 0, 0, 0, 0};
-        x.ahead.b = s_seq[warp];
-        x.ahead.begin(a, s_at[warp]);
-        PnCursor cur = x.ahead;
-        for (int i = 0; ok && i < S && x.to_load > 0; ++i) {
-            x.load_k();
-            x.load_v();
+    bool ok = !*(volatile int*)&hd.abort;
+    if (warp == W) {
+        const int w = min(lane, W - 1);
+        const int64_t todo = lane < W && ok ? warp_from(w + 1) - warp_from(w) : 0;
+        pn_copies<D, W>(a, hd, rings, lane, todo, todo ? hd.at[w] : 0);
+    } else {
+        const int64_t w0 = warp_from(warp), w1 = warp_from(warp + 1);
+        PnWarp<D, W> x{a, hd, rings + warp * Sh::RING, warp, lane, 0};
+        PnCursor cur = {};
+        if (w1 > w0) {
+            cur.b = hd.seq[warp];
+            cur.begin(a, hd.at[warp]);
         }
         int64_t at = w0;
         while (ok && at < w1) {
@@ -642,65 +674,58 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
             p.nch = cur.nch;
             p.x1 = (int)min((int64_t)cur.nch, cur.c + (w1 - at));
             const int second = p.x0 == 0;
-            float* slot = reinterpret_cast<float*>(second ? ring0 + warp * S * 2 * Sh::TILE : slots + warp * Sh::SLOT);
-            if (cur.n * a.G <= 8) ok = x.template head<1>(cur, p, slot);
-            else ok = x.template head<2>(cur, p, slot);
+            float* slot = reinterpret_cast<float*>(second ? rings + warp * Sh::RING : slots + warp * Sh::SLOT);
+            if (Sh::ROWS == 8 || cur.n * a.G <= 8) ok = x.template head<1>(cur, p, slot);
+            else ok = x.template head<Sh::ROWS / 8>(cur, p, slot);
             if (!ok) break;
-            if (lane == 0 && !(p.x0 == 0 && p.x1 == p.nch)) pieces[2 * warp + second] = p;
+            if (lane == 0 && !(p.x0 == 0 && p.x1 == p.nch)) hd.pieces[2 * warp + second] = p;
             at += p.x1 - p.x0;
             if (at < w1) {
                 cur.c = cur.nch - 1;
                 cur.next(a);
             }
         }
-        if (!ok && lane == 0) {                      // no copy may still be landing when the CTA exits
-            volatile int no_abort = 0;
-            for (uint32_t k = x.loads > S ? x.loads - S : 0; k < x.loads + 1; ++k) {
-                if (k < x.loads) mbar_wait(x.vfull + k % S, (k / S) & 1, &no_abort, nullptr);
-                if (k < x.loads || x.to_load > 0) mbar_wait(x.kfull + k % S, (k / S) & 1, &no_abort, nullptr);
-            }
-        }
     }
-    if (__syncthreads_or(!ok)) return;
+    if (__syncthreads_or(!ok || *(volatile int*)&hd.abort)) return;
 
     // ---- pieces of a head, in this CTA
     if (tid == 0) {
         int n = 0;
-        for (int i = 0; i < 2 * kPnWarps; ++i) {
-            const PnPiece p = pieces[i];
+        for (int i = 0; i < 2 * W; ++i) {
+            const PnPiece p = hd.pieces[i];
             if (p.x1 == 0) continue;
-            if (n && runs[n - 1].start == p.start) {
-                runs[n - 1].x1 = p.x1;
-                run_from[2 * n - 1] = i + 1;
+            if (n && hd.runs[n - 1].start == p.start) {
+                hd.runs[n - 1].x1 = p.x1;
+                hd.run[n - 1][1] = i + 1;
             } else {
-                runs[n] = p;
-                run_from[2 * n] = i;
-                run_from[2 * n + 1] = i + 1;
+                hd.runs[n] = p;
+                hd.run[n][0] = i;
+                hd.run[n][1] = i + 1;
                 ++n;
             }
         }
-        *s_runs = n;
+        hd.n_runs = n;
     }
     __syncthreads();
-    const int n_runs = *s_runs;
+    const int n_runs = hd.n_runs;
     if (n_runs == 0) return;
-    for (int u = warp; u < n_runs * kPnRows; u += kPnWarps) {
-        const int k = u / kPnRows, row = u - k * kPnRows;
-        const PnPiece p = runs[k];
+    for (int u = warp; u < n_runs * Sh::ROWS; u += WARPS) {
+        const int k = u / Sh::ROWS, row = u - k * Sh::ROWS;
+        const PnPiece p = hd.runs[k];
         const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
         if (row >= rows) continue;
-        const int i0 = run_from[2 * k], i1 = run_from[2 * k + 1];
+        const int i0 = hd.run[k][0], i1 = hd.run[k][1];
         float o[E];
         float m = -INFINITY, l = 0.f;
         {
             int n = 0;
-            for (int i = i0; i < i1; ++i) n += pieces[i].x1 != 0;
+            for (int i = i0; i < i1; ++i) n += hd.pieces[i].x1 != 0;
             int i = i0;
             auto get = [&](int, float2& ml, float (&y)[E]) {
-                while (pieces[i].x1 == 0) ++i;
-                const float* slot = reinterpret_cast<const float*>(i & 1 ? ring0 + (i >> 1) * S * 2 * Sh::TILE : slots + (i >> 1) * Sh::SLOT);
+                while (hd.pieces[i].x1 == 0) ++i;
+                const float* slot = reinterpret_cast<const float*>(i & 1 ? rings + (i >> 1) * Sh::RING : slots + (i >> 1) * Sh::SLOT);
                 ++i;
-                ml = reinterpret_cast<const float2*>(slot + kPnRows * D)[row];
+                ml = reinterpret_cast<const float2*>(slot + Sh::ROWS * D)[row];
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[e] = slot[row * D + lane * E + e];
             };
@@ -711,7 +736,7 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
         if (p.x0 == 0 && p.x1 == p.nch) {
             pn_store<D>(a, p, c0, row, lane, l, o);
         } else {
-            const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * kPnRows + row;
+            const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * Sh::ROWS + row;
             if (lane == 0) a.part_ml[dst] = make_float2(m, l);
 #pragma unroll
             for (int e = 0; e < E; ++e) a.part_o[dst * D + lane * E + e] = o[e];
@@ -725,7 +750,7 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
     if (tid < 2) {
         int last = -1;
         const int k = tid == 0 ? 0 : n_runs - 1;            // only the first and the last run can go on elsewhere
-        const PnPiece p = runs[k];
+        const PnPiece p = hd.runs[k];
         if ((tid == 0 || n_runs > 1) && !(p.x0 == 0 && p.x1 == p.nch)) {
             const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
             if (atomicAdd(a.joined + first, 1u) == (unsigned)n - 1) {
@@ -734,19 +759,19 @@ __global__ void __launch_bounds__(kPnThreads, 1) paged_few_kernel(const __grid_c
                 last = k;
             }
         }
-        s_last[tid] = last;
+        hd.last[tid] = last;
     }
     __syncthreads();
     for (int j = 0; j < 2; ++j) {
-        const int k = s_last[j];
+        const int k = hd.last[j];
         if (k < 0) continue;
-        const PnPiece p = runs[k];
+        const PnPiece p = hd.runs[k];
         const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
         const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
-        for (int row = warp; row < rows; row += kPnWarps) {
+        for (int row = warp; row < rows; row += WARPS) {
             float o[E];
             auto get = [&](int i, float2& ml, float (&y)[E]) {
-                const int64_t src = ((int64_t)(first + i) * 2 + (i == 0)) * kPnRows + row;
+                const int64_t src = ((int64_t)(first + i) * 2 + (i == 0)) * Sh::ROWS + row;
                 ml = __ldcg(a.part_ml + src);
                 if constexpr (E == 4) {
                     const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + src * D) + lane);
@@ -903,10 +928,12 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         a.cap = p.c.width * p.c.page;
         a.scale_log2 = p.scale_log2;
         void* args[] = {&a};
-        const void* fn = d128 ? reinterpret_cast<const void*>(paged_few_kernel<128>) : reinterpret_cast<const void*>(paged_few_kernel<64>);
-        const int smem = d128 ? PnShape<128>::SMEM : PnShape<64>::SMEM;
+        const bool eight = (int64_t)p.max_new * G <= 8;
+        const void* fn = d128 ? (eight ? reinterpret_cast<const void*>(paged_few_kernel<128, 15>) : reinterpret_cast<const void*>(paged_few_kernel<128, 7>))
+                              : (eight ? reinterpret_cast<const void*>(paged_few_kernel<64, 15>) : reinterpret_cast<const void*>(paged_few_kernel<64, 7>));
+        const int smem = d128 ? (eight ? PnShape<128, 15>::SMEM : PnShape<128, 7>::SMEM) : (eight ? PnShape<64, 15>::SMEM : PnShape<64, 7>::SMEM);
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kPnThreads);
+        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, eight ? PnShape<64, 15>::THREADS : PnShape<64, 7>::THREADS);
         if (e != cudaSuccess) return e;
     }
     if ((int64_t)p.max_new * G <= kPnRows) return cudaSuccess;
