@@ -46,7 +46,8 @@ constexpr float kPnRescale = 8.f;         // m follows the maximum where that ha
 
 struct PnPiece {                          // of a head of a sequence
     int64_t start;                        // the head's first chunk in the batch's list
-    int b, h, x0, x1, nch;                // chunks x0 .. x1 - 1 of nch; x1 = 0: none
+    int h, x0, x1, nch;                   // chunks x0 .. x1 - 1 of nch; x1 = 0: none
+    int c0, rows, pos;                    // the sequence's first token row, its rows, its first position
 };
 
 // Fifteen warps and the copying one where no sequence has more than 8 rows, else seven with twice the registers.
@@ -61,11 +62,11 @@ struct PnShape {
     struct Head {
         uint64_t kfull[W][STAGES], kempty[W][STAGES], vfull[W][STAGES], vempty[W][STAGES];
         float scales[W][STAGES][4];                                 // of K for both halves of the chunk, of V
-        int64_t sums[W + 1], at[W];                                 // a warp's place in its first sequence
-        PnPiece pieces[2 * W], runs[2 * W];
-        int run[2 * W][2];                                          // first piece of the run, and behind the last
+        int64_t sums[W + 1], firsts[W + 1];
+        int64_t at[W];                                              // a warp's place in its first sequence
+        PnPiece pieces[2 * W];                                      // of warp w: one that began before it, one that goes on behind it
         int valid[W][STAGES];                                       // halves whose page is there
-        int seq[W], last[2], n_runs, abort;
+        int seq[W], last[2], first_cta[2], abort;
     };
     static constexpr int HEAD = ((int)sizeof(Head) + 1023) & ~1023;
     static constexpr int SMEM = HEAD + W * (RING + SLOT);
@@ -201,14 +202,15 @@ __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W
     bool values = false;                                    // next are the values of the chunk whose keys are on the way
     int id0 = 0, id1 = 0, mask = 0, off = 0, shard = 0, tile0 = 0, tile1 = 0;
     uint64_t since = global_ns();
+    const uint64_t once = l2_evict_first_policy();
     auto copies = [&](const CUtensorMap* m, unsigned char* dst, uint64_t* bar) {
         if (a.bits == 4) {                                  // pages of 16: a box for each half
             mbar_arrive_expect_tx(bar, __popc(mask) * (TILE / 2));
-            if (mask & 1) tma_load_3d_keep(dst, m, 0, 0, tile0, bar);
-            if (mask & 2) tma_load_3d_keep(dst + TILE / 2, m, 0, 0, tile1, bar);
+            if (mask & 1) tma_load_3d_hint(dst, m, 0, 0, tile0, bar, once);
+            if (mask & 2) tma_load_3d_hint(dst + TILE / 2, m, 0, 0, tile1, bar, once);
         } else {
             mbar_arrive_expect_tx(bar, (mask & 1) * TILE);
-            if (mask & 1) tma_load_3d_keep(dst, m, 0, off, tile0, bar);
+            if (mask & 1) tma_load_3d_hint(dst, m, 0, off, tile0, bar, once);
         }
     };
     while (__any_sync(0xffffffffu, todo > 0)) {
@@ -531,40 +533,73 @@ struct PnWarp {
     }
 };
 
-// One warp: a row's pieces joined, o = sum_i 2^(m_i - m) O_i and l likewise;
-// `get(i, ml, x)` reads piece i: (m, l), and the lane's D / 32 elements of O.
-template <int D, typename Get>
-__device__ __forceinline__ float2 pn_join(int n, Get get, float (&o)[D / 32]) {
+// One warp: a row's n pieces joined, o = sum_i 2^(m_i - m) O_i and (m, l)
+// likewise, always in the same order. stat(i): (m, l) of piece i, read by lane
+// i; get(i, x): the lane's D / 32 elements of its O. No piece is left out, so
+// that a NaN of one stays.
+template <int D, typename Stat, typename Get>
+__device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, float (&o)[D / 32]) {
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int E = D / 32, AHEAD = 4;
     float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) o[k] = 0.f;
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-        float2 ml;
-        float x[D / 32];
-        get(i, ml, x);
-        const float top = fmaxf(m, ml.x);
-        const float a = m == -INFINITY ? 0.f : ex2_approx(m - top), b = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-        m = top;
-        l = l * a + ml.y * b;
+    for (int k = 0; k < E; ++k) o[k] = 0.f;
+    float x[AHEAD][E];
+    auto load = [&](int i) {                                // on the way while the weights are found
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) o[k] = o[k] * a + x[k] * b;
+        for (int j = 0; j < AHEAD; ++j)
+            if (i + j < n) get(i + j, x[j]);
+    };
+    load(0);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (i0 + lane < n) ml = stat(i0 + lane);
+        const float top = fmaxf(m, warp_max(ml.x)), down = m == -INFINITY ? 0.f : ex2_approx(m - top);
+        const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+        l = l * down + warp_sum(w * ml.y);
+        m = top;
+#pragma unroll
+        for (int k = 0; k < E; ++k) o[k] *= down;
+#pragma unroll 1
+        for (int i = i0; i < min(i0 + 32, n); i += AHEAD) {
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const float f = __shfl_sync(kAll, w, (i + j) & 31);
+                if (i + j < n)
+#pragma unroll
+                    for (int k = 0; k < E; ++k) o[k] = fmaf(f, x[j][k], o[k]);
+            }
+            load(i + AHEAD);
+        }
     }
     return make_float2(m, l);
 }
 
 template <int D>
-__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int c0, int row, int lane, float l, const float (&o)[D / 32]) {
+__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float l, const float (&o)[D / 32]) {
     const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, tok = row / a.G;
-    const int64_t at = (int64_t)__ldg(a.pos + p.b) + tok;
+    const int64_t at = (int64_t)p.pos + tok;
     const bool none = l == 0.f || at < 0 || at >= a.cap;
-    bf16* dst = a.out + (((int64_t)r * a.T + c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + lane * (D / 32);
+    bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + lane * (D / 32);
     const float f = 1.f / l;
     uint32_t y[D / 64];
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
     if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
     else *reinterpret_cast<uint32_t*>(dst) = y[0];
+}
+template <int D>
+__device__ __forceinline__ void pn_read(const float* src, int lane, float (&x)[D / 32], bool global) {
+    if constexpr (D == 128) {
+        const float4* p = reinterpret_cast<const float4*>(src) + lane;
+        const float4 v = global ? __ldcg(p) : *p;
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+        const float2* p = reinterpret_cast<const float2*>(src) + lane;
+        const float2 v = global ? __ldcg(p) : *p;
+        x[0] = v.x, x[1] = v.y;
+    }
 }
 
 template <int D, int W>
@@ -588,65 +623,82 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         fence_mbar_init();
     }
     if (tid < 2 * W) hd.pieces[tid].x1 = 0;
+    if (tid < 2 * a.N) {
+        const CUtensorMap* m = tid < a.N ? &a.tk[tid] : &a.tv[tid - a.N];
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+    }
     pdl_trigger();
     pdl_wait();
 
     // ---- the CTA's and its warps' place in the list of chunks
     const int heads = a.N * a.hkv_s;
     int bad = 0;
-    int64_t sum = 0;
+    int64_t sum = 0, own = 0;                               // chunks of the thread's sequences, of the first of them
     for (int b = tid; b < a.B; b += THREADS) {
         int c0, n, pos;
-        sum += (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
+        const int64_t x = (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
+        if (b == tid) own = x;
+        sum += x;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
         if (blockIdx.x == 0 && n > 0) {
             if (n > a.max_new) set_status(a.status, TP_ERR_SHAPE);
             else if (pos < 0 || (int64_t)pos + n > a.cap) set_status(a.status, TP_ERR_CAPACITY);
         }
     }
-    auto warp_sum64 = [&](int64_t x) {
-        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        return x;
-    };
-    sum = warp_sum64(sum);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    int64_t upto_own = own;                                 // ... of those of the warp up to it
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto_own, o);
+        if (lane >= o) upto_own += v;
+    }
     if (lane == 0) hd.sums[warp] = sum;
+    if (lane == 31) hd.firsts[warp] = upto_own;
     if (__syncthreads_or(bad)) {
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
         return;
     }
-    int64_t total = 0;
-    for (int i = 0; i < WARPS; ++i) total += hd.sums[i];
+    int64_t total = 0, base = 0, before_own = upto_own - own;
+    for (int i = 0; i < WARPS; ++i) {
+        total += hd.sums[i];
+        if (i < warp) before_own += hd.firsts[i];
+        base += hd.firsts[i];
+    }
     // a chunk for each warp at least: fewer CTAs then have fewer pieces to join
     const int ctas = (int)min((int64_t)gridDim.x, (total + W - 1) / W);
     if ((int)blockIdx.x >= ctas) return;
     const int64_t from = total * blockIdx.x / ctas, upto = total * (blockIdx.x + 1) / ctas;
-    auto warp_from = [&](int w) { return from + (upto - from) * w / W; };
-    int64_t base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    // (a run for the first warps only where there are fewer chunks: the pieces of a head lie in warps next to one another)
+    const int busy = (int)min((int64_t)W, upto - from);
+    auto warp_from = [&](int w) { return from + (upto - from) * min(w, busy) / busy; };
+    auto place = [&](int b, int64_t before, int64_t n) {     // whose run begins in sequence b
+        if (!n || before >= upto || before + n <= from) return;
+        for (int w = 0; w < W; ++w) {
+            const int64_t at = warp_from(w);
+            if (at >= before && at < before + n) {
+                hd.seq[w] = b;
+                hd.at[w] = at - before;
+            }
+        }
+    };
+    place(tid, before_own, own);
+    for (int b0 = THREADS; b0 < a.B; b0 += THREADS) {
         const int b = b0 + tid;
         int c0, n, pos;
-        const int64_t mine = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
-        int64_t x = mine;
+        const int64_t x = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
+        int64_t y = x;
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += v;
+            const int64_t v = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += v;
         }
         __syncthreads();
-        if (lane == 31) hd.sums[warp] = x;
+        if (lane == 31) hd.firsts[warp] = y;
         __syncthreads();
-        int64_t before = base + x - mine;
+        int64_t before = base + y - x;
         for (int i = 0; i < WARPS; ++i) {
-            if (i < warp) before += hd.sums[i];
-            base += hd.sums[i];
+            if (i < warp) before += hd.firsts[i];
+            base += hd.firsts[i];
         }
-        if (mine)
-            for (int w = 0; w < W; ++w) {
-                const int64_t at = warp_from(w);
-                if (at >= before && at < before + mine) {
-                    hd.seq[w] = b;
-                    hd.at[w] = at - before;
-                }
-            }
+        place(b, before, x);
     }
     __syncthreads();
 
@@ -668,8 +720,10 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         while (ok && at < w1) {
             PnPiece p;
             p.start = at - cur.c;
-            p.b = cur.b;
             p.h = cur.h;
+            p.c0 = cur.c0;
+            p.rows = cur.n * a.G;
+            p.pos = cur.pos;
             p.x0 = cur.c;
             p.nch = cur.nch;
             p.x1 = (int)min((int64_t)cur.nch, cur.c + (w1 - at));
@@ -688,101 +742,85 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     }
     if (__syncthreads_or(!ok || *(volatile int*)&hd.abort)) return;
 
-    // ---- pieces of a head, in this CTA
-    if (tid == 0) {
-        int n = 0;
-        for (int i = 0; i < 2 * W; ++i) {
-            const PnPiece p = hd.pieces[i];
-            if (p.x1 == 0) continue;
-            if (n && hd.runs[n - 1].start == p.start) {
-                hd.runs[n - 1].x1 = p.x1;
-                hd.run[n - 1][1] = i + 1;
-            } else {
-                hd.runs[n] = p;
-                hd.run[n][0] = i;
-                hd.run[n][1] = i + 1;
-                ++n;
-            }
-        }
-        hd.n_runs = n;
-    }
-    __syncthreads();
-    const int n_runs = hd.n_runs;
-    if (n_runs == 0) return;
-    for (int u = warp; u < n_runs * Sh::ROWS; u += WARPS) {
-        const int k = u / Sh::ROWS, row = u - k * Sh::ROWS;
-        const PnPiece p = hd.runs[k];
-        const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
-        if (row >= rows) continue;
-        const int i0 = hd.run[k][0], i1 = hd.run[k][1];
+    // ---- pieces of a head, in this CTA: runs of pieces, which every warp finds by itself, their rows dealt out
+    constexpr unsigned kAll = 0xffffffffu;
+    const PnPiece mine = hd.pieces[min(lane, 2 * W - 1)];
+    const unsigned there = __ballot_sync(kAll, lane < 2 * W && mine.x1 > 0), below = there & ((1u << lane) - 1u);
+    const int before = below ? 31 - __clz(below) : 0;
+    const int64_t its = __shfl_sync(kAll, mine.start, before);
+    const unsigned begins = __ballot_sync(kAll, (there >> lane & 1) && (!below || its != mine.start));
+    auto slot_of = [&](int i) {
+        return reinterpret_cast<const float*>(i & 1 ? rings + (i >> 1) * Sh::RING : slots + (i >> 1) * Sh::SLOT);
+    };
+    auto run_of = [&](int first, unsigned& pieces) {          // the run whose first piece it is
+        const unsigned behind = begins & ~((2u << first) - 1u);
+        pieces = there & ~((1u << first) - 1u) & (behind ? (1u << (__ffs(behind) - 1)) - 1u : kAll);
+        PnPiece p = hd.pieces[first];
+        p.x1 = hd.pieces[31 - __clz(pieces)].x1;
+        return p;
+    };
+    const int stride = (int)min((int64_t)Sh::ROWS, (int64_t)a.max_new * a.G);
+    for (int u = warp; u < __popc(begins) * stride; u += WARPS) {
+        const int k = u / stride, row = u - k * stride;
+        unsigned from_k = begins, pieces;
+        for (int i = 0; i < k; ++i) from_k &= from_k - 1;
+        // piece j of the run lies j places on: only a head's first piece is a warp's second one
+        const int first = __ffs(from_k) - 1;
+        const PnPiece p = run_of(first, pieces);
+        if (row >= p.rows) continue;
+        auto at = [&](int j) { return j ? ((first + 1) & ~1) + 2 * (j - (first & 1)) : first; };
         float o[E];
-        float m = -INFINITY, l = 0.f;
-        {
-            int n = 0;
-            for (int i = i0; i < i1; ++i) n += hd.pieces[i].x1 != 0;
-            int i = i0;
-            auto get = [&](int, float2& ml, float (&y)[E]) {
-                while (hd.pieces[i].x1 == 0) ++i;
-                const float* slot = reinterpret_cast<const float*>(i & 1 ? rings + (i >> 1) * Sh::RING : slots + (i >> 1) * Sh::SLOT);
-                ++i;
-                ml = reinterpret_cast<const float2*>(slot + Sh::ROWS * D)[row];
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = slot[row * D + lane * E + e];
-            };
-            const float2 r = pn_join<D>(n, get, o);
-            m = r.x;
-            l = r.y;
-        }
+        const float2 r = pn_join<D>(
+            __popc(pieces), lane, [&](int j) { return reinterpret_cast<const float2*>(slot_of(at(j)) + Sh::ROWS * D)[row]; },
+            [&](int j, float (&x)[E]) { pn_read<D>(slot_of(at(j)) + row * D, lane, x, false); }, o);
         if (p.x0 == 0 && p.x1 == p.nch) {
-            pn_store<D>(a, p, c0, row, lane, l, o);
+            pn_store<D>(a, p, row, lane, r.y, o);
         } else {
             const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * Sh::ROWS + row;
-            if (lane == 0) a.part_ml[dst] = make_float2(m, l);
-#pragma unroll
-            for (int e = 0; e < E; ++e) a.part_o[dst * D + lane * E + e] = o[e];
+            if (lane == 0) a.part_ml[dst] = r;
+            float* to = a.part_o + dst * D + lane * E;
+            if constexpr (E == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
+            else *reinterpret_cast<float2*>(to) = make_float2(o[0], o[1]);
         }
     }
 
-    // ---- pieces of a head in several CTAs: the last of them joins
+    // ---- pieces of a head in several CTAs: the last of them joins. Only the CTA's first and last run can go on elsewhere.
     auto cta_of = [&](int64_t c) { return (int)(((c + 1) * ctas - 1) / total); };
+    auto end_run = [&](int j, PnPiece& p) {
+        if (begins == 0 || (j && !(begins & (begins - 1)))) return false;
+        unsigned pieces;
+        p = run_of(j ? 31 - __clz(begins) : __ffs(begins) - 1, pieces);
+        return !(p.x0 == 0 && p.x1 == p.nch);
+    };
     __threadfence();
     __syncthreads();
     if (tid < 2) {
-        int last = -1;
-        const int k = tid == 0 ? 0 : n_runs - 1;            // only the first and the last run can go on elsewhere
-        const PnPiece p = hd.runs[k];
-        if ((tid == 0 || n_runs > 1) && !(p.x0 == 0 && p.x1 == p.nch)) {
+        PnPiece p;
+        int last = 0;
+        if (end_run(tid, p)) {
             const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
             if (atomicAdd(a.joined + first, 1u) == (unsigned)n - 1) {
                 a.joined[first] = 0;
                 __threadfence();
-                last = k;
+                last = n;
+                hd.first_cta[tid] = first;
             }
         }
         hd.last[tid] = last;
     }
     __syncthreads();
     for (int j = 0; j < 2; ++j) {
-        const int k = hd.last[j];
-        if (k < 0) continue;
-        const PnPiece p = hd.runs[k];
-        const int first = cta_of(p.start), n = cta_of(p.start + p.nch - 1) - first + 1;
-        const int c0 = __ldg(a.cu + p.b), rows = (__ldg(a.cu + p.b + 1) - c0) * a.G;
-        for (int row = warp; row < rows; row += WARPS) {
+        const int n = hd.last[j], first = hd.first_cta[j];
+        if (!n) continue;
+        PnPiece p;
+        end_run(j, p);
+        auto src = [&](int i) { return ((int64_t)(first + i) * 2 + (i == 0)) * Sh::ROWS; };
+        for (int row = warp; row < p.rows; row += WARPS) {
             float o[E];
-            auto get = [&](int i, float2& ml, float (&y)[E]) {
-                const int64_t src = ((int64_t)(first + i) * 2 + (i == 0)) * Sh::ROWS + row;
-                ml = __ldcg(a.part_ml + src);
-                if constexpr (E == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + src * D) + lane);
-                    y[0] = v.x, y[1] = v.y, y[2] = v.z, y[3] = v.w;
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(a.part_o + src * D) + lane);
-                    y[0] = v.x, y[1] = v.y;
-                }
-            };
-            const float2 r = pn_join<D>(n, get, o);
-            pn_store<D>(a, p, c0, row, lane, r.y, o);
+            const float2 r = pn_join<D>(
+                n, lane, [&](int i) { return __ldcg(a.part_ml + src(i) + row); },
+                [&](int i, float (&x)[E]) { pn_read<D>(a.part_o + (src(i) + row) * D, lane, x, true); }, o);
+            pn_store<D>(a, p, row, lane, r.y, o);
         }
     }
 }
