@@ -669,14 +669,16 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     const int64_t from = total * blockIdx.x / ctas, upto = total * (blockIdx.x + 1) / ctas;
     // (a run for the first warps only where there are fewer chunks: the pieces of a head lie in warps next to one another)
     const int busy = (int)min((int64_t)W, upto - from);
-    auto warp_from = [&](int w) { return from + (upto - from) * min(w, busy) / busy; };
-    auto place = [&](int b, int64_t before, int64_t n) {     // whose run begins in sequence b
-        if (!n || before >= upto || before + n <= from) return;
-        for (int w = 0; w < W; ++w) {
-            const int64_t at = warp_from(w);
-            if (at >= before && at < before + n) {
-                hd.seq[w] = b;
-                hd.at[w] = at - before;
+    // lane w: the beginning of warp w's run
+    const int64_t begin = from + (upto - from) * min(lane, busy) / busy;
+    auto place = [&](int b, int64_t before, int64_t n) {     // whose run begins in one of the warp's sequences
+        for (unsigned left = __ballot_sync(0xffffffffu, n && before < upto && before + n > from); left; left &= left - 1) {
+            const int i = __ffs(left) - 1;
+            const int64_t x = __shfl_sync(0xffffffffu, before, i), y = x + __shfl_sync(0xffffffffu, n, i);
+            const int seq = __shfl_sync(0xffffffffu, b, i);
+            if (lane < W && begin >= x && begin < y) {
+                hd.seq[lane] = seq;
+                hd.at[lane] = begin - x;
             }
         }
     };
@@ -703,13 +705,13 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     __syncthreads();
 
     // ---- a warp's run
+    constexpr unsigned kAll = 0xffffffffu;
     bool ok = !*(volatile int*)&hd.abort;
     if (warp == W) {
-        const int w = min(lane, W - 1);
-        const int64_t todo = lane < W && ok ? warp_from(w + 1) - warp_from(w) : 0;
-        pn_copies<D, W>(a, hd, rings, lane, todo, todo ? hd.at[w] : 0);
+        const int64_t end = __shfl_down_sync(kAll, begin, 1), todo = lane < W && ok ? end - begin : 0;
+        pn_copies<D, W>(a, hd, rings, lane, todo, todo ? hd.at[lane] : 0);
     } else {
-        const int64_t w0 = warp_from(warp), w1 = warp_from(warp + 1);
+        const int64_t w0 = __shfl_sync(kAll, begin, warp), w1 = __shfl_sync(kAll, begin, warp + 1);
         PnWarp<D, W> x{a, hd, rings + warp * Sh::RING, warp, lane, 0};
         PnCursor cur = {};
         if (w1 > w0) {
@@ -743,7 +745,6 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     if (__syncthreads_or(!ok || *(volatile int*)&hd.abort)) return;
 
     // ---- pieces of a head, in this CTA: runs of pieces, which every warp finds by itself, their rows dealt out
-    constexpr unsigned kAll = 0xffffffffu;
     const PnPiece mine = hd.pieces[min(lane, 2 * W - 1)];
     const unsigned there = __ballot_sync(kAll, lane < 2 * W && mine.x1 > 0), below = there & ((1u << lane) - 1u);
     const int before = below ? 31 - __clz(below) : 0;
