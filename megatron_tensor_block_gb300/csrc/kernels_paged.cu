@@ -7,6 +7,7 @@
 // p f is off by whole degrees at p = 10^6). The nearest quarter turn is taken
 // off as an integer, so that sine and cosine are taken of at most an eighth.
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "tp_internal.h"
 
 namespace tpk {
@@ -150,9 +151,7 @@ __global__ void __launch_bounds__(kPgThreads) rope_kernel(const __grid_constant_
 
 // Two float32 values as e4m3, to nearest even; what is not finite as NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    uint32_t x = r;
+    uint32_t x = to_e4m3x2(lo, hi);
     if (!(fabsf(lo) < INFINITY)) x |= 0x7fu;
     if (!(fabsf(hi) < INFINITY)) x |= 0x7f00u;
     return x;
@@ -164,11 +163,8 @@ __device__ __forceinline__ uint32_t requantise4(uint32_t x, float by) {
     uint32_t y = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(x >> (16 * i))));
-        float lo, hi;
-        asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(lo), "=f"(hi) : "r"(h));
-        y |= e4m3x2(lo * by, hi * by) << (16 * i);
+        const float2 f = f16x2_to_float2(e4m3_to_f16x2((uint16_t)(x >> (16 * i))));
+        y |= e4m3x2(f.x * by, f.y * by) << (16 * i);
     }
     return y;
 }

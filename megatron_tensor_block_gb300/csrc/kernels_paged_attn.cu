@@ -10,6 +10,7 @@
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "stream.cuh"
 #include "tp_internal.h"
 
@@ -145,21 +146,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint16_t x) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
-    return r;
-}
-__device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
-    float2 r;
-    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(x));
-    return r;
 }
 // The power of two that brings a row's largest magnitude to 2^14 .. 2^15.
 __device__ __forceinline__ float row_scale(float most) {
