@@ -41,7 +41,7 @@ __device__ __forceinline__ bool mbar_try_at(uint32_t bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
+static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort, int* status) {
     const uint64_t t0 = global_ns();
     while (true) {
         if (mbar_try_at(bar, parity)) return true;
