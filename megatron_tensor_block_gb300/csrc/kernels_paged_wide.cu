@@ -550,12 +550,20 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             const int whole_to = (int)min(warp_max, (int64_t)w.kend - 1);
             float m_use = -INFINITY, l_run = 0.f, factor = 0.f;
             for (int j = 0; j < n; ++j, ++sp) {
-                if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
                 if ((j & 3) == 0 && !(ok = info_wait_in(in + j))) break;
+                if (j == 0) {                               // (what a row is scaled by is there with its first scores)
+                    if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
+                    factor = hd.row[k & 1][t][m];
+                }
+                const PwBlock& x = hd.info[(in + j) % kPwInfos];
+                const float4 f0 = *reinterpret_cast<const float4*>(&x.kf[0]), f1 = *reinterpret_cast<const float4*>(&x.kf[4]);
+                // what the row's scores of sixteen keys each are multiplied by; never 0, so that -inf stays -inf
+                float kf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) kf[i] = fmaxf(kf[i] * factor, 0x1p-126f);
+                if (j && !(ok = wait_in(&hd.s_full[t], sp & 1))) break;
                 if (!idle) {
                     tc_fence_after();
-                    if (j == 0) factor = hd.row[k & 1][t][m];
-                    const PwBlock& x = hd.info[(in + j) % kPwInfos];
                     const int key0 = (w.blk0 + j) * kPwK, mask = x.mask;
                     const float down = x.down;
                     // a block that every row of the warp sees whole needs no mask
@@ -564,14 +572,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     uint32_t v[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
-                    // What a row's scores of two times sixteen keys are multiplied by: never 0, so that -inf stays -inf. Read
-                    // where it is used: there are no registers for all eight beside the scores.
-                    const uint32_t kf_at = smem_u32(&x.kf[0]);
-                    auto factors = [&](int c) {
-                        float2 f;
-                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f.x), "=f"(f.y) : "r"(kf_at + 8 * c));
-                        return make_float2(fmaxf(f.x * factor, 0x1p-126f), fmaxf(f.y * factor, 0x1p-126f));
-                    };
                     tmem_wait_ld();
                     float* e = reinterpret_cast<float*>(&v[0][0]);
                     if (!whole) {
@@ -581,14 +581,13 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     float mq[4];                            // independent chains
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float2 f = factors(c);
                         float y = fmaxf(e[32 * c], e[32 * c + 1]), z = fmaxf(e[32 * c + 16], e[32 * c + 17]);
 #pragma unroll
                         for (int i = 2; i < 16; i += 2) {
                             y = max3(y, e[32 * c + i], e[32 * c + i + 1]);
                             z = max3(z, e[32 * c + 16 + i], e[32 * c + 17 + i]);
                         }
-                        mq[c] = fmaxf(y * f.x, z * f.y);
+                        mq[c] = fmaxf(y * kf[2 * c], z * kf[2 * c + 1]);
                     }
                     const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
                     const bool grow = m_blk > m_use + kPwRescale;
@@ -610,11 +609,10 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     }
                     const float m_sub = m_use == -INFINITY ? 0.f : m_use;            // nothing seen yet: every weight is 0
                     const uint64_t neg2 = f2_pack(-m_sub, -m_sub);
-                    uint64_t sum[2] = {0, 0};
+                    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const float2 f = factors(c);
-                        const uint64_t scale2[2] = {f2_pack(f.x, f.x), f2_pack(f.y, f.y)};
+                        const uint64_t scale2[2] = {f2_pack(kf[2 * c], kf[2 * c]), f2_pack(kf[2 * c + 1], kf[2 * c + 1])};
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
@@ -622,7 +620,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                             f2_unpack(f2_fma(f2_pack(e[32 * c + 2 * i], e[32 * c + 2 * i + 1]), scale2[i / 8], neg2), y, z);
                             y = ex2_approx(y);
                             z = ex2_approx(z);
-                            sum[i & 1] = f2_add(sum[i & 1], f2_pack(y, z));
+                            sum[i & 3] = f2_add(sum[i & 3], f2_pack(y, z));
                             pk[i] = pack_f16x2(y, z);
                         }
                         if (c == 2) {                       // the first 64 keys' products may begin
@@ -634,7 +632,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         tmem_st16(s_col + 16 * c, pk);
                     }
                     float sx, sy;
-                    f2_unpack(f2_add(sum[0], sum[1]), sx, sy);
+                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), sx, sy);
                     l_run = l_run * alpha + (sx + sy);
                     tmem_wait_st();
                     tc_fence_before();
@@ -741,7 +739,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 const bool ragged = (int64_t)key0 + kPwK > (int64_t)w.qpos + 1 || mask != 0xFF;
                 if (j < w.nb0) ref0 = x.ref;
                 ref1 = x.ref;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     const int key = 32 * qd + 8 * i + (lane >> 2), u = lane & 3;
                     const bool gone = ragged && (key0 + key >= w.kend || !(mask >> (key >> 4) & 1));
