@@ -42,27 +42,29 @@ namespace tpk {
 // ---------------------------------------------------------------------------
 
 constexpr int kPnKeys = 32;               // keys of a chunk
-constexpr int kPnRows = 16;               // query rows of a sequence and KV head at most
+constexpr int kPnRows = 16;               // query rows that a warp works on
+constexpr int kPnMost = 32;               // ... of a sequence and KV head that are this kernel's, sixteen at a time
 constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
 
 struct PnPiece {                          // of a head of a sequence
     int64_t start;                        // the head's first chunk in the batch's list
     int h, x0, x1, nch;                   // chunks x0 .. x1 - 1 of nch; x1 = 0: none
-    int c0, rows, pos;                    // the sequence's first token row, its rows, its first position
+    int c0, row0, rows, pos;              // the sequence's first token row, the rows of the head, its first position
 };
 
-// Fifteen warps and the copying one where no sequence has more than 8 rows, else seven with twice the registers.
+// Fifteen warps and the copying one where no sequence has more than 8 rows, else eleven with more registers.
 template <int D, int W>
 struct PnShape {
     static constexpr int ROWS = W == 15 ? 8 : 16;
     static constexpr int TILE = kPnKeys * D;                        // bytes of a chunk's K or V
-    static constexpr int STAGES = (D == 128 ? 1 : 2) * (W == 15 ? 1 : 2);
-    static constexpr int SLOT = ROWS * D * 4 + ROWS * 8;             // a piece of a head: O, then (m, l)
+    static constexpr int STAGES = D == 128 ? 1 : 2;
+    static constexpr int SLOT = ROWS * D * 4;                       // O of a piece of a head
     static constexpr int RING = STAGES * 2 * TILE;                  // of a warp
     static constexpr int THREADS = 32 * (W + 1);
     struct Head {
         uint64_t kfull[W][STAGES], kempty[W][STAGES], vfull[W][STAGES], vempty[W][STAGES];
         float scales[W][STAGES][4];                                 // of K for both halves of the chunk, of V
+        float2 ml[2 * W][ROWS];                                     // (m, l) of the pieces
         int64_t sums[W + 1], firsts[W + 1];
         int64_t at[W];                                              // a warp's place in its first sequence
         PnPiece pieces[2 * W];                                      // of warp w: one that began before it, one that goes on behind it
@@ -97,29 +99,34 @@ __device__ __forceinline__ int pn_chunks(const PnArgs& a, int b, int& c0, int& n
     c0 = __ldg(a.cu + b);
     n = __ldg(a.cu + b + 1) - c0;
     pos = __ldg(a.pos + b);
-    if (n <= 0 || n > a.max_new || (int64_t)n * a.G > kPnRows) return 0;
+    if (n <= 0 || n > a.max_new || (int64_t)n * a.G > kPnMost) return 0;
     const int64_t end = (int64_t)pos + n;
     const int kend = (int)(end < 0 ? 0 : end > a.cap ? a.cap : end);
     return max(1, (kend + kPnKeys - 1) / kPnKeys);
 }
 
-// A place in the batch's list of chunks.
+// A head's query rows are worked on sixteen at a time.
+__device__ __forceinline__ int pn_groups(const PnArgs& a, int n) { return (n * a.G + kPnRows - 1) / kPnRows; }
+
+// A place in the batch's list of chunks: of a sequence, the chunks of every head's groups of rows.
 struct PnCursor {
-    int b, h, c, nch, c0, n, pos;
+    int b, h, c, nch, c0, n, pos, groups; // h: head times groups, and the group
     __device__ __forceinline__ void begin(const PnArgs& a, int64_t in_sequence) {
         nch = pn_chunks(a, b, c0, n, pos);
+        groups = pn_groups(a, n);
         h = (int)(in_sequence / nch);
         c = (int)(in_sequence - (int64_t)h * nch);
     }
     __device__ __forceinline__ void next(const PnArgs& a) {
         if (++c < nch) return;
         c = 0;
-        if (++h < a.N * a.hkv_s) return;
+        if (++h < a.N * a.hkv_s * groups) return;
         h = 0;
         do {
             ++b;
             nch = b < a.B ? pn_chunks(a, b, c0, n, pos) : 1;
         } while (nch == 0);
+        groups = pn_groups(a, n);
     }
     __device__ __forceinline__ int kend(const PnArgs& a) const {
         const int64_t end = (int64_t)pos + n;
@@ -204,8 +211,9 @@ __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W
         const bool go = todo > 0 && mbar_test(values ? &hd.vempty[w][s] : &hd.kempty[w][s], ((loads / S) & 1) ^ 1);
         if (go && !values) {
             const int key = kPnKeys * at.c, kend = at.kend(a);
-            shard = at.h / a.hkv_s;
-            const int kv = at.h - shard * a.hkv_s;
+            const int head = at.h / at.groups;
+            shard = head / a.hkv_s;
+            const int kv = head - shard * a.hkv_s;
             const int* row = a.pages + (int64_t)at.b * a.width;
             const bool in0 = key < kend, in1 = key + 16 < kend;
             id0 = in0 ? __ldg(row + (key >> a.bits)) : -1;
@@ -321,10 +329,10 @@ struct PnWarp {
     }
 
     // Chunks w.x0 .. w.x1 - 1 of a head of the sequence at cur. Where that is all of them the result goes to out, else to
-    // slot (O [rows][D], then (m, l)).
+    // slot (O [rows][D]) and (m, l) beside it.
     template <int NT>
     __device__ __forceinline__ bool head(const PnCursor& cur, const PnPiece& w, float* slot) {
-        const int g = lane >> 2, t = lane & 3, rows = cur.n * a.G, kend = cur.kend(a);
+        const int g = lane >> 2, t = lane & 3, kend = cur.kend(a);
         const int r = w.h / a.hkv_s, kvh = w.h - r * a.hkv_s;
         // the queries: rows 8 nt + g as columns of the products
         uint32_t qf[NT][D / 16][2];
@@ -332,13 +340,14 @@ struct PnWarp {
         int lim[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int row = 8 * nt + g, i = row / a.G;
+            const bool is = 8 * nt + g < w.rows;
+            const int row = w.row0 + 8 * nt + g, i = row / a.G;
             const bf16* src = a.q + (((int64_t)r * a.T + cur.c0 + i) * a.hq_s + kvh * a.G + (row - i * a.G)) * D + 4 * t;
             uint2 x[D / 16];
             float most = 0.f;
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                x[ks] = row < rows ? *reinterpret_cast<const uint2*>(src + 16 * ks) : make_uint2(0, 0);
+                x[ks] = is ? *reinterpret_cast<const uint2*>(src + 16 * ks) : make_uint2(0, 0);
                 const float2 f = unpack_bf16x2(x[ks].x), f2 = unpack_bf16x2(x[ks].y);
                 most = fmaxf(fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f2.x), fabsf(f2.y)));
             }
@@ -353,10 +362,10 @@ struct PnWarp {
             }
 #pragma unroll
             for (int i2 = 0; i2 < 2; ++i2) {
-                const int mine = 8 * nt + 2 * t + i2, tok = mine / a.G;        // the lane's rows of S^T and O^T
+                const int mine = 8 * nt + 2 * t + i2, tok = (w.row0 + mine) / a.G;        // the lane's rows of S^T and O^T
                 factor[nt][i2] = __shfl_sync(0xffffffffu, back, (2 * t + i2) * 4);
                 const int64_t p = (int64_t)cur.pos + tok;
-                lim[nt][i2] = mine < rows && p >= 0 && p < a.cap ? (int)p : -1;
+                lim[nt][i2] = mine < w.rows && p >= 0 && p < a.cap ? (int)p : -1;
             }
         }
         float o[NT][D / 16][4] = {}, m[NT][2], l[NT][2], ref = 0.f;
@@ -371,13 +380,13 @@ struct PnWarp {
             unsigned char* kt = ring + s * 2 * TILE;
             const uint32_t at = smem_u32(kt) + unit;
             if (!wait(&hd.kfull[warp][s], par)) return false;
-            float sc[NT][2][4], sl[NT][2][4];                       // two sums each: shorter chains
+            float sc[NT][2][4], sl[1][2][4];                        // two sums for eight rows: shorter chains
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc[nt][kk][i] = sl[nt][kk][i] = 0.f;
+                    for (int i = 0; i < 4; ++i) sc[nt][kk][i] = sl[0][kk][i] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks += 2) {
                     uint32_t x[4];
@@ -390,7 +399,7 @@ struct PnWarp {
                         const uint32_t a1 = e4m3_to_f16x2((uint16_t)x[2 * j + 1]), a3 = e4m3_to_f16x2((uint16_t)(x[2 * j + 1] >> 16));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
-                            mma_f16_16816(j ? sl[nt][kk] : sc[nt][kk], a0, a1, a2, a3, qf[nt][ks + j][0], qf[nt][ks + j][1]);
+                            mma_f16_16816(NT == 1 && j ? sl[0][kk] : sc[nt][kk], a0, a1, a2, a3, qf[nt][ks + j][0], qf[nt][ks + j][1]);
                     }
                 }
             }
@@ -410,7 +419,7 @@ struct PnWarp {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int kk = j >> 1, e = i + 2 * (j & 1);
-                        x[j] = (sc[nt][kk][e] + sl[nt][kk][e]) * (factor[nt][i] * pk[kk]);
+                        x[j] = (NT == 1 ? sc[nt][kk][e] + sl[0][kk][e] : sc[nt][kk][e]) * (factor[nt][i] * pk[kk]);
                         if (!whole) {
                             const int key = first + 16 * kk + 8 * (j & 1) + g;
                             if (key > lim[nt][i] || !(there >> kk & 1)) x[j] = -INFINITY;
@@ -497,13 +506,13 @@ struct PnWarp {
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
                 const int row = 8 * nt + 2 * t + i;
-                if (row >= rows) continue;
+                if (row >= w.rows) continue;
                 if (all) {
-                    const int tok = row / a.G;
+                    const int of = w.row0 + row, tok = of / a.G;
                     const int64_t p = (int64_t)cur.pos + tok;
                     const bool none = x == 0.f || p < 0 || p >= a.cap;      // no key seen, no such place: zeros
                     const float f = ref / x;
-                    bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + 2 * g;
+                    bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + 2 * g;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<uint32_t*>(dst + 16 * mt) =
@@ -512,7 +521,7 @@ struct PnWarp {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i] * ref, o[nt][mt][2 + i] * ref);
-                    if (g == 0) reinterpret_cast<float2*>(slot + Sh::ROWS * D)[row] = make_float2(m[nt][i], x);
+                    if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(m[nt][i], x);
                 }
             }
         return true;
@@ -564,10 +573,10 @@ __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, f
 
 template <int D>
 __device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float l, const float (&o)[D / 32]) {
-    const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, tok = row / a.G;
+    const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, of = p.row0 + row, tok = of / a.G;
     const int64_t at = (int64_t)p.pos + tok;
     const bool none = l == 0.f || at < 0 || at >= a.cap;
-    bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (row - tok * a.G)) * D + lane * (D / 32);
+    bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + lane * (D / 32);
     const float f = 1.f / l;
     uint32_t y[D / 64];
 #pragma unroll
@@ -622,7 +631,8 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     int64_t sum = 0, own = 0;                               // chunks of the thread's sequences, of the first of them
     for (int b = tid; b < a.B; b += THREADS) {
         int c0, n, pos;
-        const int64_t x = (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
+        int64_t x = (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
+        if (x) x *= pn_groups(a, n);
         if (b == tid) own = x;
         sum += x;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
@@ -672,7 +682,8 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     for (int b0 = THREADS; b0 < a.B; b0 += THREADS) {
         const int b = b0 + tid;
         int c0, n, pos;
-        const int64_t x = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
+        int64_t x = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
+        if (x) x *= pn_groups(a, n);
         int64_t y = x;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, y, o);
@@ -708,16 +719,17 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         while (ok && at < w1) {
             PnPiece p;
             p.start = at - cur.c;
-            p.h = cur.h;
+            p.h = cur.h / cur.groups;
             p.c0 = cur.c0;
-            p.rows = cur.n * a.G;
+            p.row0 = (cur.h - p.h * cur.groups) * kPnRows;
+            p.rows = min(kPnRows, cur.n * a.G - p.row0);
             p.pos = cur.pos;
             p.x0 = cur.c;
             p.nch = cur.nch;
             p.x1 = (int)min((int64_t)cur.nch, cur.c + (w1 - at));
             const int second = p.x0 == 0;
             float* slot = reinterpret_cast<float*>(second ? rings + warp * Sh::RING : slots + warp * Sh::SLOT);
-            if (Sh::ROWS == 8 || cur.n * a.G <= 8) ok = x.template head<1>(cur, p, slot);
+            if (Sh::ROWS == 8 || p.rows <= 8) ok = x.template head<1>(cur, p, slot);
             else ok = x.template head<Sh::ROWS / 8>(cur, p, slot);
             if (!ok) break;
             if (lane == 0 && !(p.x0 == 0 && p.x1 == p.nch)) hd.pieces[2 * warp + second] = p;
@@ -758,7 +770,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         auto at = [&](int j) { return j ? ((first + 1) & ~1) + 2 * (j - (first & 1)) : first; };
         float o[E];
         const float2 r = pn_join<D>(
-            __popc(pieces), lane, [&](int j) { return reinterpret_cast<const float2*>(slot_of(at(j)) + Sh::ROWS * D)[row]; },
+            __popc(pieces), lane, [&](int j) { return hd.ml[at(j)][row]; },
             [&](int j, float (&x)[E]) { pn_read<D>(slot_of(at(j)) + row * D, lane, x, false); }, o);
         if (p.x0 == 0 && p.x1 == p.nch) {
             pn_store<D>(a, p, row, lane, r.y, o);
@@ -842,7 +854,7 @@ size_t pn_part(int d) { return (size_t)kSMs * 2 * kPnRows * d * sizeof(float); }
 }  // namespace
 
 size_t paged_workspace(int64_t max_tokens, int group, int d) {
-    return kPagedCtrl + kPnMl + pn_part(d) + (max_tokens * group <= kPnRows ? 0 : paged_wide_bytes(d));
+    return kPagedCtrl + kPnMl + pn_part(d) + (max_tokens * group <= kPnMost ? 0 : paged_wide_bytes(d));
 }
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
@@ -883,15 +895,15 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         a.scale_log2 = p.scale_log2;
         void* args[] = {&a};
         const bool eight = (int64_t)p.max_new * G <= 8;
-        const void* fn = d128 ? (eight ? reinterpret_cast<const void*>(paged_few_kernel<128, 15>) : reinterpret_cast<const void*>(paged_few_kernel<128, 7>))
-                              : (eight ? reinterpret_cast<const void*>(paged_few_kernel<64, 15>) : reinterpret_cast<const void*>(paged_few_kernel<64, 7>));
-        const int smem = d128 ? (eight ? PnShape<128, 15>::SMEM : PnShape<128, 7>::SMEM) : (eight ? PnShape<64, 15>::SMEM : PnShape<64, 7>::SMEM);
+        const void* fn = d128 ? (eight ? reinterpret_cast<const void*>(paged_few_kernel<128, 15>) : reinterpret_cast<const void*>(paged_few_kernel<128, 11>))
+                              : (eight ? reinterpret_cast<const void*>(paged_few_kernel<64, 15>) : reinterpret_cast<const void*>(paged_few_kernel<64, 11>));
+        const int smem = d128 ? (eight ? PnShape<128, 15>::SMEM : PnShape<128, 11>::SMEM) : (eight ? PnShape<64, 15>::SMEM : PnShape<64, 11>::SMEM);
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, eight ? PnShape<64, 15>::THREADS : PnShape<64, 7>::THREADS);
+        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, eight ? PnShape<64, 15>::THREADS : PnShape<64, 11>::THREADS);
         if (e != cudaSuccess) return e;
     }
-    if ((int64_t)p.max_new * G <= kPnRows) return cudaSuccess;
-    return launch_paged_wide(p, kPnRows, p.ws + kPagedCtrl + kPnMl + pn_part(p.d), s);
+    if ((int64_t)p.max_new * G <= kPnMost) return cudaSuccess;
+    return launch_paged_wide(p, kPnMost, p.ws + kPagedCtrl + kPnMl + pn_part(p.d), s);
 }
 
 }  // namespace tpk
