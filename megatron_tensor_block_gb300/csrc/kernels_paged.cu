@@ -5,7 +5,11 @@
 // 64-bit fraction of a turn per position, and p times it modulo 2^64 is the
 // angle modulo a turn, exact for that f however far p is (a float32 product
 // p f is off by whole degrees at p = 10^6). The nearest quarter turn is taken
-// off as an integer, so that sine and cosine are taken of at most an eighth.
+// off as an integer; sine and cosine of the rest, at most an eighth of a turn,
+// are their Taylor polynomials.
+//
+// A thread has sixteen features (eight pairs) of a token row and keeps their
+// sines and cosines while it goes through heads.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "tp_internal.h"
@@ -13,7 +17,6 @@
 namespace tpk {
 
 constexpr int kPgThreads = 256;
-constexpr int kPgRows = 16;               // token rows whose sines are in shared memory at a time
 
 // Whether cu is not 0 = cu[0] <= cu[1] <= ... <= T (the whole block asks).
 __device__ __forceinline__ bool cu_malformed(const int* cu, int B, int T) {
@@ -38,8 +41,10 @@ __device__ __forceinline__ int sequence_of(const int* cu, int B, int t) {
 
 __device__ __forceinline__ float2 cos_sin(int64_t p, uint64_t turn, float by) {
     const uint64_t x = (uint64_t)p * turn, quarter = (x + (1ull << 61)) >> 62;
-    float s, c;
-    sincospif(__ll2float_rn((int64_t)(x - (quarter << 62))) * 0x1p-63f, &s, &c);
+    // the rest in 2^-62 quarters of a turn, within half of one: radians from its upper 32 bits (2^-32 of a quarter each)
+    const float r = (float)(int)((int64_t)(x - (quarter << 62)) >> 30) * (1.5707963267948966f * 0x1p-32f), r2 = r * r;
+    float s = fmaf(fmaf(fmaf(fmaf(2.7557319e-6f, r2, -1.9841270e-4f), r2, 8.3333333e-3f), r2, -1.6666667e-1f) * r2, r, r);
+    float c = fmaf(fmaf(fmaf(fmaf(fmaf(-2.7557319e-7f, r2, 2.4801587e-5f), r2, -1.3888889e-3f), r2, 4.1666667e-2f), r2, -0.5f), r2, 1.f);
     if (quarter & 1) {
         const float t = c;
         c = -s;
@@ -79,21 +84,25 @@ __device__ __forceinline__ void unit_at(const RopeTable& r, int u, int& a, int& 
     a = half ? 8 * u : 16 * u;
     b = half ? r.rot / 2 + 8 * u : 16 * u + 8;
 }
-// ... turned; cs: the row's cosines and sines.
-__device__ __forceinline__ void turn_unit(const RopeTable& r, int u, const float2* cs, float (&a)[8], float (&b)[8]) {
+// The cosines and sines of unit u at position p.
+__device__ __forceinline__ void unit_turns(const RopeTable& r, int u, int64_t p, float2 (&cs)[8]) {
+    if (16 * u >= r.rot) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = cos_sin(p, r.turn[8 * u + i], r.by);
+}
+__device__ __forceinline__ void turn_unit(const RopeTable& r, int u, const float2 (&cs)[8], float (&a)[8], float (&b)[8]) {
     if (16 * u >= r.rot) return;
     if (r.layout == TP_ROPE_HALF) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 t = cs[8 * u + i];
             const float x = a[i], y = b[i];
-            a[i] = x * t.x - y * t.y;
-            b[i] = x * t.y + y * t.x;
+            a[i] = x * cs[i].x - y * cs[i].y;
+            b[i] = x * cs[i].y + y * cs[i].x;
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float2 t = cs[8 * u + i / 2], v = cs[8 * u + 4 + i / 2];
+            const float2 t = cs[i / 2], v = cs[4 + i / 2];
             float x = a[i], y = a[i + 1];
             a[i] = x * t.x - y * t.y;
             a[i + 1] = x * t.y + y * t.x;
@@ -104,47 +113,42 @@ __device__ __forceinline__ void turn_unit(const RopeTable& r, int u, const float
     }
 }
 
-// One CTA: `rows` token rows of a shard. Bound by the bytes of the rows.
+// Threads of a token row's units and of `split` groups of its heads of all shards, hq of q in each and then hk of k; a group's heads lie
+// `split` apart, so that neighbouring threads have neighbouring memory. Bound by the bytes of the rows.
 template <typename T>
-__global__ void __launch_bounds__(kPgThreads) rope_kernel(const __grid_constant__ RopeArgs p, int rows) {
-    __shared__ float2 cs[kPgRows][64];
-    __shared__ int64_t s_pos[kPgRows];
-    const int tid = threadIdx.x;
+__device__ __forceinline__ void rope_rows(const RopeArgs& p, int hq, int hk, int64_t thread, int split) {
+    const int per = p.d / 16, u = (int)(thread % per);
+    const int64_t rest = thread / per, row = rest / split;
+    if (row >= __ldg(p.cu + p.B)) return;
+    const int t = (int)row, b = sequence_of(p.cu, p.B, t);
+    const int heads = p.N * (hq + hk);
+    int x, y;
+    unit_at(p.rope, u, x, y);
+    float2 cs[8];
+    unit_turns(p.rope, u, (int64_t)__ldg(p.pos + b) + (t - __ldg(p.cu + b)), cs);
+#pragma unroll 2
+    for (int h = (int)(rest % split); h < heads; h += split) {
+        const bool key = h >= p.N * hq;
+        const int i = key ? h - p.N * hq : h, of = key ? hk : hq, r = i / of, head = i - r * of;
+        const TokenRows& from = key ? p.k : p.q;
+        const T* src = static_cast<const T*>(from.p) + r * from.shard + (int64_t)t * from.token + head * p.d;
+        T* dst = static_cast<T*>(key ? p.k_out : p.q_out) + (((int64_t)r * p.T + t) * of + head) * p.d;
+        float f[8], g[8];
+        load8(src + x, f);
+        load8(src + y, g);
+        turn_unit(p.rope, u, cs, f, g);
+        store8(dst + x, f);
+        store8(dst + y, g);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kPgThreads) rope_kernel(const __grid_constant__ RopeArgs p, int split) {
     if (cu_malformed(p.cu, p.B, p.T)) {
-        if (tid == 0 && blockIdx.x == 0) set_status(p.status, TP_ERR_SHAPE);
+        if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, TP_ERR_SHAPE);
         return;
     }
-    const int r = blockIdx.x % p.N, t0 = blockIdx.x / p.N * rows, n = min(rows, __ldg(p.cu + p.B) - t0);
-    if (n <= 0) return;
-    if (tid < n) {
-        const int b = sequence_of(p.cu, p.B, t0 + tid);
-        s_pos[tid] = (int64_t)p.pos[b] + (t0 + tid - p.cu[b]);
-    }
-    __syncthreads();
-    const int half = p.rope.rot / 2;
-    for (int i = tid; i < n * half; i += kPgThreads) {
-        const int t = i / half, j = i - t * half;
-        cs[t][j] = cos_sin(s_pos[t], p.rope.turn[j], p.rope.by);
-    }
-    __syncthreads();
-    const int hq = p.q.p ? p.hq_s : 0, heads = hq + (p.k.p ? p.hkv_s : 0);
-    const int per = p.d / 16, per_row = heads * per;
-    for (int i = tid; i < n * per_row; i += kPgThreads) {
-        const int t = i / per_row, in = i - t * per_row, h = in / per, u = in - h * per;
-        const bool key = h >= hq;
-        const TokenRows& x = key ? p.k : p.q;
-        const int head = key ? h - hq : h, all = key ? p.hkv_s : p.hq_s;
-        const T* src = static_cast<const T*>(x.p) + r * x.shard + (int64_t)(t0 + t) * x.token + head * p.d;
-        T* dst = static_cast<T*>(key ? p.k_out : p.q_out) + (((int64_t)r * p.T + t0 + t) * all + head) * p.d;
-        int at, bt;
-        unit_at(p.rope, u, at, bt);
-        float a[8], b[8];
-        load8(src + at, a);
-        load8(src + bt, b);
-        turn_unit(p.rope, u, cs[t], a, b);
-        store8(dst + at, a);
-        store8(dst + bt, b);
-    }
+    rope_rows<T>(p, p.q.p ? p.hq_s : 0, p.k.p ? p.hkv_s : 0, (int64_t)blockIdx.x * kPgThreads + threadIdx.x, split);
 }
 
 // ---------------------------------------------------------------------------
@@ -157,7 +161,12 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return x;
 }
 __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8]) {
-    return make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+    float none = 0.f;                     // NaN where one of them is not finite, which is rare
+#pragma unroll
+    for (int i = 0; i < 8; ++i) none = fmaf(x[i], 0.f, none);
+    if (none != none) return make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16, e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+    return make_uint2((uint32_t)to_e4m3x2(x[0], x[1]) | (uint32_t)to_e4m3x2(x[2], x[3]) << 16,
+                      (uint32_t)to_e4m3x2(x[4], x[5]) | (uint32_t)to_e4m3x2(x[6], x[7]) << 16);
 }
 __device__ __forceinline__ uint32_t requantise4(uint32_t x, float by) {
     uint32_t y = 0;
@@ -178,22 +187,26 @@ __device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t x) {
 // One CTA: the token rows of one window of a sequence, page-aligned positions
 // of one page, for a shard: first the largest magnitude of every head's new
 // keys and values, hence the scales; then what the page holds is brought to
-// them where they grew; then the new rows, a few at a time with their sines.
+// them where they grew; then the new rows, which are in L1 by then. The
+// queries' rows are CTAs of their own.
 //
 // The windows are found without a pass over the batch: sequence b has those
 // from cu[b] / page + 2 b on, of which it needs no more than there are before
 // the next one's; where there are fewer rows than that, a row that begins a
 // window has it.
-__global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constant__ AppendArgs p, int by_row) {
-    __shared__ float2 cs[kPgRows][64];
+__global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constant__ AppendArgs p, int by_row, int windows, int split) {
     extern __shared__ uint32_t s_max[];                     // [2][hkv_s]: magnitudes of K and V, then 1 / scale
     const RopeArgs& a = p.r;
-    const int tid = threadIdx.x, lane = tid & 31, hkv = a.hkv_s, d = a.d, page = p.c.page, per = d / 16;
+    const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, hkv = a.hkv_s, d = a.d, page = p.c.page, per = d / 16;
     float* s_inv = reinterpret_cast<float*>(s_max);
     float* s_ratio = s_inv + 2 * hkv;                       // [2][hkv_s]: old scale over new one
-    for (int i = tid; i < 2 * hkv; i += kPgThreads) s_max[i] = 0;
+    for (int i = tid; i < 2 * hkv; i += threads) s_max[i] = 0;
     if (cu_malformed(a.cu, a.B, a.T)) {
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
+        return;
+    }
+    if ((int)blockIdx.x >= windows * a.N) {                 // the CTAs behind: queries
+        rope_rows<bf16>(a, a.hq_s, 0, (int64_t)(blockIdx.x - windows * a.N) * threads + tid, split);
         return;
     }
     const int r = blockIdx.x % a.N, slot = blockIdx.x / a.N, used = __ldg(a.cu + a.B), bits = 31 - __clz(page);
@@ -224,131 +237,128 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
     const int n = (int)min((int64_t)(a.cu[b + 1] - t0), (w + 1) * page - first), slot0 = (int)(first - w * page);
     int at = -1;                                                       // page of the pool
     if (w >= 0 && w < p.c.width) at = __ldg(p.c.pages + (int64_t)b * p.c.width + w);
-    const bool there = at >= 0 && at < p.c.n_pages;
-    if (!there && tid == 0) set_status(a.status, TP_ERR_CAPACITY);
-
+    if (at < 0 || at >= p.c.n_pages) {
+        if (tid == 0) set_status(a.status, TP_ERR_CAPACITY);
+        return;
+    }
     auto source = [&](const TokenRows& x, int t, int h) {
         return static_cast<const bf16*>(x.p) + r * x.shard + (int64_t)(t0 + t) * x.token + h * d;
     };
     auto stored = [&](int g) {                                         // head g's page, of K or (from hkv on) of V
         return (g < hkv ? p.c.k[r] : p.c.v[r]) + ((int64_t)at * hkv + (g < hkv ? g : g - hkv)) * page * d;
     };
-    if (there) {
-        const int vecs = d / 8, each = n * vecs, all = 2 * hkv * each; // 16-byte pieces, a head's together
-        for (int i0 = 0; i0 < all; i0 += kPgThreads) {
-            const int i = i0 + tid, g = min(i, all - 1) / each;
-            uint32_t m = 0;
-            if (i < all) {
-                const int in = i - g * each, t = in / vecs, x = in - t * vecs;
-                const uint4 v = *reinterpret_cast<const uint4*>(g < hkv ? source(a.k, t, g) + 8 * x : source(p.v, t, g - hkv) + 8 * x);
-                m = max_finite(max_finite(max_finite(max_finite(0, v.x), v.y), v.z), v.w);
-                m = max(m & 0xFFFFu, m >> 16);
-            }
-            const int g0 = __shfl_sync(0xffffffffu, g, 0);             // a warp's pieces are mostly one head's
-            if (__all_sync(0xffffffffu, g == g0)) {
-                m = __reduce_max_sync(0xffffffffu, m);
-                if (lane == 0) atomicMax(&s_max[g], m);
-            } else {
-                atomicMax(&s_max[g], m);
-            }
+    // units of K and of V: the unit of a row fastest, then the row, then the head
+    const int each = n * per, all = hkv * each;
+    for (int i0 = 0; i0 < all; i0 += threads) {
+        const int i = i0 + tid, h = min(i, all - 1) / each, in = min(i, all - 1) - h * each, t = in / per, u = in - t * per;
+        const uint4* k = reinterpret_cast<const uint4*>(source(a.k, t, h) + 16 * u);
+        const uint4* v = reinterpret_cast<const uint4*>(source(p.v, t, h) + 16 * u);
+        const uint4 x[4] = {k[0], k[1], v[0], v[1]};
+        uint32_t m[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t y = 0;
+#pragma unroll
+            for (int z = 2 * j; z < 2 * j + 2; ++z) y = max_finite(max_finite(max_finite(max_finite(y, x[z].x), x[z].y), x[z].z), x[z].w);
+            m[j] = max(y & 0xFFFFu, y >> 16);
         }
-        __syncthreads();
-        for (int g = tid; g < 2 * hkv; g += kPgThreads) {
-            float* scale = g < hkv ? p.c.ks[r] + (int64_t)at * hkv + g : p.c.vs[r] + (int64_t)at * hkv + g - hkv;
-            const double x = (double)__uint_as_float(s_max[g] << 16) * (g < hkv ? p.k_growth : 1.0) / 448.0;
-            // the least power of two not below x: x's exponent, and one more unless x is a power itself
-            const long long word = __double_as_longlong(x);
-            const int e = max(-60, (int)(word >> 52) - 1023 + ((word & 0xFFFFFFFFFFFFFll) != 0));
-            float s = __uint_as_float((uint32_t)(127 + e) << 23), ratio = 1.f;
-            if (slot0) {
-                const float before = *scale;
-                if (before > s) s = before;
-                ratio = before / s;
-            }
-            *scale = s;
-            s_inv[g] = 1.f / s;
-            s_ratio[g] = ratio;
+        const int h0 = __shfl_sync(0xffffffffu, h, 0);                 // a warp's units are mostly one head's
+        if (__all_sync(0xffffffffu, h == h0)) {
+            m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+            m[1] = __reduce_max_sync(0xffffffffu, m[1]);
+            if (lane < 2) atomicMax(&s_max[lane * hkv + h], lane ? m[1] : m[0]);
+        } else {
+            atomicMax(&s_max[h], m[0]);
+            atomicMax(&s_max[hkv + h], m[1]);
         }
-        __syncthreads();
+    }
+    __syncthreads();
+    bool grown = false;
+    for (int g = tid; g < 2 * hkv; g += threads) {
+        float* scale = g < hkv ? p.c.ks[r] + (int64_t)at * hkv + g : p.c.vs[r] + (int64_t)at * hkv + g - hkv;
+        const double x = (double)__uint_as_float(s_max[g] << 16) * (g < hkv ? p.k_growth : 1.0) / 448.0;
+        // the least power of two not below x: x's exponent, and one more unless x is a power itself
+        const long long word = __double_as_longlong(x);
+        const int e = max(-60, (int)(word >> 52) - 1023 + ((word & 0xFFFFFFFFFFFFFll) != 0));
+        float s = __uint_as_float((uint32_t)(127 + e) << 23), ratio = 1.f;
+        if (slot0) {
+            const float before = *scale;
+            if (before > s) s = before;
+            ratio = before / s;
+        }
+        *scale = s;
+        s_inv[g] = 1.f / s;
+        s_ratio[g] = ratio;
+        grown |= ratio < 1.f;
+    }
+    if (__syncthreads_or(grown)) {
         const int old = slot0 * d / 16;                                // 16-byte pieces of what a head's page holds
         for (int g = 0; g < 2 * hkv; ++g) {
             const float ratio = s_ratio[g];
             if (!(ratio < 1.f)) continue;
             uint4* q = reinterpret_cast<uint4*>(stored(g));
-            for (int i = tid; i < old; i += kPgThreads) {
+            for (int i = tid; i < old; i += threads) {
                 const uint4 v = q[i];
                 q[i] = make_uint4(requantise4(v.x, ratio), requantise4(v.y, ratio), requantise4(v.z, ratio), requantise4(v.w, ratio));
             }
         }
     }
-
-    const int half = a.rope.rot / 2, hq = a.q.p ? a.hq_s : 0, heads = hq + (there ? 2 * hkv : 0), per_row = heads * per;
-    for (int r0 = 0; r0 < n; r0 += kPgRows) {
-        const int rows = min(kPgRows, n - r0);
-        if (half) {
-            __syncthreads();
-            for (int i = tid; i < rows * half; i += kPgThreads) {
-                const int t = i / half, j = i - t * half;
-                cs[t][j] = cos_sin(first + r0 + t, a.rope.turn[j], a.rope.by);
-            }
-            __syncthreads();
-        }
-        for (int i = tid; i < rows * per_row; i += kPgThreads) {
-            const int t = i / per_row, in = i - t * per_row, h = in / per, u = in - h * per;
-            const int g = h - hq;                                      // below 0: a query head
-            const bool val = g >= hkv;
-            const bf16* src = g < 0 ? source(a.q, r0 + t, h) : val ? source(p.v, r0 + t, g - hkv) : source(a.k, r0 + t, g);
-            int x, y;
-            if (val) x = 16 * u, y = x + 8;
-            else unit_at(a.rope, u, x, y);
-            float f[8], f2[8];
-            load8(src + x, f);
-            load8(src + y, f2);
-            if (g >= 0) {                                              // by the scale first, so that no sum overflows
-                const float inv = s_inv[g];
+    for (int i = tid; i < all; i += threads) {
+        const int h = i / each, in = i - h * each, t = in / per, u = in - t * per;
+        const float ki = s_inv[h], vi = s_inv[hkv + h];
+        int x, y;
+        unit_at(a.rope, u, x, y);
+        const bf16* k = source(a.k, t, h);
+        const bf16* v = source(p.v, t, h) + 16 * u;
+        float f[8], g[8], f2[8], g2[8];
+        load8(k + x, f);
+        load8(k + y, g);
+        load8(v, f2);
+        load8(v + 8, g2);
+        float2 cs[8];
+        unit_turns(a.rope, u, first + t, cs);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] *= inv, f2[j] *= inv;
-            }
-            if (!val) turn_unit(a.rope, u, cs[t], f, f2);
-            if (g < 0) {
-                bf16* dst = static_cast<bf16*>(a.q_out) + (((int64_t)r * a.T + t0 + r0 + t) * a.hq_s + h) * d;
-                store8(dst + x, f);
-                store8(dst + y, f2);
-            } else {
-                uint8_t* dst = stored(g) + (slot0 + r0 + t) * d;
-                const uint2 lo = e4m3x8(f), hi = e4m3x8(f2);
-                if (y == x + 8) {
-                    *reinterpret_cast<uint4*>(dst + x) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-                } else {
-                    *reinterpret_cast<uint2*>(dst + x) = lo;
-                    *reinterpret_cast<uint2*>(dst + y) = hi;
-                }
-            }
+        for (int j = 0; j < 8; ++j) f[j] *= ki, g[j] *= ki, f2[j] *= vi, g2[j] *= vi;      // by the scale first, so that no sum overflows
+        turn_unit(a.rope, u, cs, f, g);
+        uint8_t* dst = stored(h) + (slot0 + t) * d;
+        const uint2 lo = e4m3x8(f), hi = e4m3x8(g), lo2 = e4m3x8(f2), hi2 = e4m3x8(g2);
+        if (y == x + 8) {
+            *reinterpret_cast<uint4*>(dst + x) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+            *reinterpret_cast<uint2*>(dst + x) = lo;
+            *reinterpret_cast<uint2*>(dst + y) = hi;
         }
+        *reinterpret_cast<uint4*>(stored(hkv + h) + (slot0 + t) * d + 16 * u) = make_uint4(lo2.x, lo2.y, hi2.x, hi2.y);
     }
 }
 
 // ---------------------------------------------------------------------------
 
+// Groups of a row's heads: as many as give every SM 1024 threads, a head each at most.
+static int rope_split(const RopeArgs& a, int64_t heads) {
+    const int64_t rows = (int64_t)a.T * (a.d / 16), want = ((int64_t)kSMs * 1024 + rows - 1) / rows;
+    return (int)(want < 1 ? 1 : want > heads ? heads : want);
+}
+
 cudaError_t launch_rope(const RopeArgs& p, int dtype, cudaStream_t s) {
     RopeArgs a = p;
-    // rows per CTA: as many as keep 8 CTAs per SM
-    int rows = (int)((int64_t)a.T * a.N / (8 * kSMs));
-    rows = rows < 1 ? 1 : rows > kPgRows ? kPgRows : rows;
-    const int64_t ctas = (((int64_t)a.T + rows - 1) / rows) * a.N;
+    const int split = rope_split(a, (int64_t)a.N * ((a.q.p ? a.hq_s : 0) + (a.k.p ? a.hkv_s : 0)));
+    const int64_t ctas = ((int64_t)a.T * (a.d / 16) * split + kPgThreads - 1) / kPgThreads;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    if (dtype == TP_BF16) rope_kernel<bf16><<<(unsigned)ctas, kPgThreads, 0, s>>>(a, rows);
-    else rope_kernel<float><<<(unsigned)ctas, kPgThreads, 0, s>>>(a, rows);
+    if (dtype == TP_BF16) rope_kernel<bf16><<<(unsigned)ctas, kPgThreads, 0, s>>>(a, split);
+    else rope_kernel<float><<<(unsigned)ctas, kPgThreads, 0, s>>>(a, split);
     return cudaGetLastError();
 }
 
 cudaError_t launch_append(const AppendArgs& p, cudaStream_t s) {
     AppendArgs a = p;
-    const int64_t windows = a.r.T / a.c.page + 2 * (int64_t)a.r.B;
-    const int by_row = a.r.T <= windows;
-    const int64_t ctas = (by_row ? (int64_t)a.r.T : windows) * a.r.N;
+    const int64_t most = a.r.T / a.c.page + 2 * (int64_t)a.r.B;
+    const int by_row = a.r.T <= most;
+    const int64_t windows = by_row ? (int64_t)a.r.T : most;
+    const int threads = by_row ? 64 : kPgThreads, split = a.r.q.p ? rope_split(a.r, (int64_t)a.r.N * a.r.hq_s) : 0;
+    const int64_t ctas = windows * a.r.N + ((int64_t)a.r.T * (a.r.d / 16) * split + threads - 1) / threads;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    append_kernel<<<(unsigned)ctas, kPgThreads, 4 * a.r.hkv_s * sizeof(float), s>>>(a, by_row);
+    append_kernel<<<(unsigned)ctas, threads, 4 * a.r.hkv_s * sizeof(float), s>>>(a, by_row, (int)windows, split);
     return cudaGetLastError();
 }
 
