@@ -10,13 +10,15 @@
 //
 // A thread has sixteen features (eight pairs) of a token row and keeps their
 // sines and cosines while it goes through heads.
+#include <climits>
+
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "tp_internal.h"
 
 namespace tpk {
 
-constexpr int kPgThreads = 256;
+constexpr int kPgThreads = 256, kPgAppend = 128;
 
 // Whether cu is not 0 = cu[0] <= cu[1] <= ... <= T (the whole block asks).
 __device__ __forceinline__ bool cu_malformed(const int* cu, int B, int T) {
@@ -84,11 +86,16 @@ __device__ __forceinline__ void unit_at(const RopeTable& r, int u, int& a, int& 
     a = half ? 8 * u : 16 * u;
     b = half ? r.rot / 2 + 8 * u : 16 * u + 8;
 }
-// The cosines and sines of unit u at position p.
-__device__ __forceinline__ void unit_turns(const RopeTable& r, int u, int64_t p, float2 (&cs)[8]) {
+// The cosines and sines of unit u at position p. The frequencies are read from shared memory: a warp's lanes want different
+// ones, which constant memory gives one after another.
+__device__ __forceinline__ void unit_turns(const RopeTable& r, const uint64_t* turns, int u, int64_t p, float2 (&cs)[8]) {
     if (16 * u >= r.rot) return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = cos_sin(p, r.turn[8 * u + i], r.by);
+    for (int i = 0; i < 8; i += 2) {
+        const ulonglong2 t = *reinterpret_cast<const ulonglong2*>(turns + 8 * u + i);
+        cs[i] = cos_sin(p, t.x, r.by);
+        cs[i + 1] = cos_sin(p, t.y, r.by);
+    }
 }
 __device__ __forceinline__ void turn_unit(const RopeTable& r, int u, const float2 (&cs)[8], float (&a)[8], float (&b)[8]) {
     if (16 * u >= r.rot) return;
@@ -116,16 +123,16 @@ __device__ __forceinline__ void turn_unit(const RopeTable& r, int u, const float
 // Threads of a token row's units and of `split` groups of its heads of all shards, hq of q in each and then hk of k; a group's heads lie
 // `split` apart, so that neighbouring threads have neighbouring memory. Bound by the bytes of the rows.
 template <typename T>
-__device__ __forceinline__ void rope_rows(const RopeArgs& p, int hq, int hk, int64_t thread, int split) {
-    const int per = p.d / 16, u = (int)(thread % per);
-    const int64_t rest = thread / per, row = rest / split;
+__device__ __forceinline__ void rope_rows(const RopeArgs& p, const uint64_t* turns, int hq, int hk, int64_t thread, int split) {
+    const int bits = p.d == 128 ? 3 : 2, u = (int)(thread & ((1 << bits) - 1));
+    const int64_t rest = thread >> bits, row = rest <= INT_MAX ? (int)rest / split : rest / split;
     if (row >= __ldg(p.cu + p.B)) return;
     const int t = (int)row, b = sequence_of(p.cu, p.B, t);
     const int heads = p.N * (hq + hk);
     int x, y;
     unit_at(p.rope, u, x, y);
     float2 cs[8];
-    unit_turns(p.rope, u, (int64_t)__ldg(p.pos + b) + (t - __ldg(p.cu + b)), cs);
+    unit_turns(p.rope, turns, u, (int64_t)__ldg(p.pos + b) + (t - __ldg(p.cu + b)), cs);
 #pragma unroll 2
     for (int h = (int)(rest % split); h < heads; h += split) {
         const bool key = h >= p.N * hq;
@@ -144,11 +151,13 @@ __device__ __forceinline__ void rope_rows(const RopeArgs& p, int hq, int hk, int
 
 template <typename T>
 __global__ void __launch_bounds__(kPgThreads) rope_kernel(const __grid_constant__ RopeArgs p, int split) {
+    __shared__ __align__(16) uint64_t turns[64];
+    if (threadIdx.x < 64) turns[threadIdx.x] = p.rope.turn[threadIdx.x];
     if (cu_malformed(p.cu, p.B, p.T)) {
         if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, TP_ERR_SHAPE);
         return;
     }
-    rope_rows<T>(p, p.q.p ? p.hq_s : 0, p.k.p ? p.hkv_s : 0, (int64_t)blockIdx.x * kPgThreads + threadIdx.x, split);
+    rope_rows<T>(p, turns, p.q.p ? p.hq_s : 0, p.k.p ? p.hkv_s : 0, (int64_t)blockIdx.x * kPgThreads + threadIdx.x, split);
 }
 
 // ---------------------------------------------------------------------------
@@ -194,22 +203,27 @@ __device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t x) {
 // from cu[b] / page + 2 b on, of which it needs no more than there are before
 // the next one's; where there are fewer rows than that, a row that begins a
 // window has it.
-__global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constant__ AppendArgs p, int by_row, int windows, int split) {
+__global__ void __launch_bounds__(kPgAppend, 6) append_kernel(const __grid_constant__ AppendArgs p, int by_row, int windows, int apart, int split) {
+    __shared__ __align__(16) uint64_t turns[64];
     extern __shared__ uint32_t s_max[];                     // [2][hkv_s]: magnitudes of K and V, then 1 / scale
     const RopeArgs& a = p.r;
     const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, hkv = a.hkv_s, d = a.d, page = p.c.page, per = d / 16;
     float* s_inv = reinterpret_cast<float*>(s_max);
     float* s_ratio = s_inv + 2 * hkv;                       // [2][hkv_s]: old scale over new one
     for (int i = tid; i < 2 * hkv; i += threads) s_max[i] = 0;
+    if (tid < 64) turns[tid] = a.rope.turn[tid];
     if (cu_malformed(a.cu, a.B, a.T)) {
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
         return;
     }
-    if ((int)blockIdx.x >= windows * a.N) {                 // the CTAs behind: queries
-        rope_rows<bf16>(a, a.hq_s, 0, (int64_t)(blockIdx.x - windows * a.N) * threads + tid, split);
+    // the CTAs of windows lie among those of queries, every `apart`-th: they wait for memory again and again, the others load it
+    const int turn = blockIdx.x / apart, cta = min(turn, windows * a.N);
+    if (turn * apart != (int)blockIdx.x || turn >= windows * a.N) {
+        const int before = min(windows * a.N, turn + 1);
+        rope_rows<bf16>(a, turns, a.hq_s, 0, (int64_t)((int)blockIdx.x - before) * threads + tid, split);
         return;
     }
-    const int r = blockIdx.x % a.N, slot = blockIdx.x / a.N, used = __ldg(a.cu + a.B), bits = 31 - __clz(page);
+    const int r = cta % a.N, slot = cta / a.N, used = __ldg(a.cu + a.B), bits = 31 - __clz(page);
     int b, t0;
     int64_t w;                                              // the window: positions w page ..
     if (by_row) {
@@ -237,10 +251,8 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
     const int n = (int)min((int64_t)(a.cu[b + 1] - t0), (w + 1) * page - first), slot0 = (int)(first - w * page);
     int at = -1;                                                       // page of the pool
     if (w >= 0 && w < p.c.width) at = __ldg(p.c.pages + (int64_t)b * p.c.width + w);
-    if (at < 0 || at >= p.c.n_pages) {
-        if (tid == 0) set_status(a.status, TP_ERR_CAPACITY);
-        return;
-    }
+    const bool there = at >= 0 && at < p.c.n_pages;
+    auto scale_of = [&](int g) { return g < hkv ? p.c.ks[r] + (int64_t)at * hkv + g : p.c.vs[r] + (int64_t)at * hkv + g - hkv; };
     auto source = [&](const TokenRows& x, int t, int h) {
         return static_cast<const bf16*>(x.p) + r * x.shard + (int64_t)(t0 + t) * x.token + h * d;
     };
@@ -248,9 +260,9 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
         return (g < hkv ? p.c.k[r] : p.c.v[r]) + ((int64_t)at * hkv + (g < hkv ? g : g - hkv)) * page * d;
     };
     // units of K and of V: the unit of a row fastest, then the row, then the head
-    const int each = n * per, all = hkv * each;
+    const int each = n * per, all = hkv * each, unit_bits = d == 128 ? 3 : 2;
     for (int i0 = 0; i0 < all; i0 += threads) {
-        const int i = i0 + tid, h = min(i, all - 1) / each, in = min(i, all - 1) - h * each, t = in / per, u = in - t * per;
+        const int i = i0 + tid, h = min(i, all - 1) / each, in = min(i, all - 1) - h * each, t = in >> unit_bits, u = in & (per - 1);
         const uint4* k = reinterpret_cast<const uint4*>(source(a.k, t, h) + 16 * u);
         const uint4* v = reinterpret_cast<const uint4*>(source(p.v, t, h) + 16 * u);
         const uint4 x[4] = {k[0], k[1], v[0], v[1]};
@@ -272,17 +284,22 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
             atomicMax(&s_max[hkv + h], m[1]);
         }
     }
+    if (!there) {                                                      // (the rows' loads were on the way meanwhile)
+        if (tid == 0) set_status(a.status, TP_ERR_CAPACITY);
+        return;
+    }
+    float held = slot0 && tid < 2 * hkv ? *scale_of(tid) : 0.f;
     __syncthreads();
     bool grown = false;
     for (int g = tid; g < 2 * hkv; g += threads) {
-        float* scale = g < hkv ? p.c.ks[r] + (int64_t)at * hkv + g : p.c.vs[r] + (int64_t)at * hkv + g - hkv;
+        float* scale = scale_of(g);
         const double x = (double)__uint_as_float(s_max[g] << 16) * (g < hkv ? p.k_growth : 1.0) / 448.0;
         // the least power of two not below x: x's exponent, and one more unless x is a power itself
         const long long word = __double_as_longlong(x);
         const int e = max(-60, (int)(word >> 52) - 1023 + ((word & 0xFFFFFFFFFFFFFll) != 0));
         float s = __uint_as_float((uint32_t)(127 + e) << 23), ratio = 1.f;
         if (slot0) {
-            const float before = *scale;
+            const float before = g == tid ? held : *scale;
             if (before > s) s = before;
             ratio = before / s;
         }
@@ -304,7 +321,7 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
         }
     }
     for (int i = tid; i < all; i += threads) {
-        const int h = i / each, in = i - h * each, t = in / per, u = in - t * per;
+        const int h = i / each, in = i - h * each, t = in >> unit_bits, u = in & (per - 1);
         const float ki = s_inv[h], vi = s_inv[hkv + h];
         int x, y;
         unit_at(a.rope, u, x, y);
@@ -316,7 +333,7 @@ __global__ void __launch_bounds__(kPgThreads) append_kernel(const __grid_constan
         load8(v, f2);
         load8(v + 8, g2);
         float2 cs[8];
-        unit_turns(a.rope, u, first + t, cs);
+        unit_turns(a.rope, turns, u, first + t, cs);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] *= ki, g[j] *= ki, f2[j] *= vi, g2[j] *= vi;      // by the scale first, so that no sum overflows
         turn_unit(a.rope, u, cs, f, g);
@@ -355,10 +372,10 @@ cudaError_t launch_append(const AppendArgs& p, cudaStream_t s) {
     const int64_t most = a.r.T / a.c.page + 2 * (int64_t)a.r.B;
     const int by_row = a.r.T <= most;
     const int64_t windows = by_row ? (int64_t)a.r.T : most;
-    const int threads = by_row ? 64 : kPgThreads, split = a.r.q.p ? rope_split(a.r, (int64_t)a.r.N * a.r.hq_s) : 0;
+    const int threads = by_row ? 64 : kPgAppend, split = a.r.q.p ? rope_split(a.r, (int64_t)a.r.N * a.r.hq_s) : 0;
     const int64_t ctas = windows * a.r.N + ((int64_t)a.r.T * (a.r.d / 16) * split + threads - 1) / threads;
     if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    append_kernel<<<(unsigned)ctas, threads, 4 * a.r.hkv_s * sizeof(float), s>>>(a, by_row, (int)windows, split);
+    append_kernel<<<(unsigned)ctas, threads, 4 * a.r.hkv_s * sizeof(float), s>>>(a, by_row, (int)windows, (int)(ctas / (windows * a.r.N)), split);
     return cudaGetLastError();
 }
 
