@@ -649,8 +649,9 @@ typedef struct tp_paged_kv {
  * sine decides a scale. Values that the page holds already are brought to a
  * larger s, which rounds them again only below 2^-6 s. Stored is x / s rounded
  * to the nearest e4m3, ties to even, from the float32 rotation without a
- * rounding between; values that are not finite are stored as NaN. Slots that no
- * token of the call falls into keep their value.
+ * rounding between; values that are not finite are stored as NaN. Slots of the
+ * page that no token of the call falls into keep their values, but where slot 0
+ * is among the new ones: what those behind them hold means nothing then.
  * Every page that receives tokens belongs to one sequence (a page that several
  * sequences write has undefined contents). Rows at positions outside
  * 0..width*page-1 or in a page whose id is outside 0..n_pages-1 append nothing

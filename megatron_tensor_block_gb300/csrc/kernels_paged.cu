@@ -309,12 +309,14 @@ __global__ void __launch_bounds__(kPgAppend, 6) append_kernel(const __grid_const
         grown |= ratio < 1.f;
     }
     if (__syncthreads_or(grown)) {
-        const int old = slot0 * d / 16;                                // 16-byte pieces of what a head's page holds
+        // 16-byte pieces of what a head's page holds before and behind the new rows
+        const int row = d / 16, lo = slot0 * row, hi = (slot0 + n) * row, end = page * row;
         for (int g = 0; g < 2 * hkv; ++g) {
             const float ratio = s_ratio[g];
             if (!(ratio < 1.f)) continue;
             uint4* q = reinterpret_cast<uint4*>(stored(g));
-            for (int i = tid; i < old; i += threads) {
+            for (int i = tid; i < end; i += threads) {
+                if (i >= lo && i < hi) continue;
                 const uint4 v = q[i];
                 q[i] = make_uint4(requantise4(v.x, ratio), requantise4(v.y, ratio), requantise4(v.z, ratio), requantise4(v.w, ratio));
             }

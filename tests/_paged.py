@@ -221,10 +221,9 @@ class Batch:
                     s = 2.0 ** exponent(np.where(np.isfinite(x), np.abs(x), 0).max((1, 3)), growth)
                     if lo > w * page:
                         s = np.maximum(s, scale[:, at])
-                        n = lo - w * page
-                        kept = DECODE[codes[:, at, :, :n]] * (scale[:, at] / s)[..., None, None]
-                        codes[:, at, :, :n] = encode(kept)
-                        value[:, at, :, :n] = DECODE[codes[:, at, :, :n]]
+                        kept = DECODE[codes[:, at]] * (scale[:, at] / s)[..., None, None]
+                        codes[:, at] = encode(kept)
+                        value[:, at] = DECODE[codes[:, at]]
                     scale[:, at] = s
                     slots = slice(lo - w * page, hi - w * page)
                     y = turned[:, rows].transpose(0, 2, 1, 3) / s[..., None, None]

@@ -100,6 +100,7 @@ APPENDS = {
     "prompt_64_128": (L(4, 1, 64, 1), R(layout=1), 128, [400], [127], {}),
     "long": (L(2, 2, 64, 1), R(), 16, [2000], [7], {}),
     "many_short": (L(2, 2, 64, 2), R(), 16, [1, 2, 0, 3] * 30, [(29 * i) % 40 for i in range(120)], {}),
+    "values_behind_the_new": (QWEN, R(), 32, [1, 3, 9], [10, 1, 60], dict(stale=0x35, spread=12)),
     "small_pages_held": (QWEN, R(), 16, [3, 5], [10, 13], dict(spread=20)),
     "attn_factor": (QWEN, R(attn_factor=3.0), 16, [20], [5], {}),
     "far": (L(2, 2, 64, 1), R(theta=1e4), 128, [3], [2 ** 20 + 5], {}),
