@@ -168,16 +168,6 @@ __device__ __forceinline__ uint32_t pn_unit(int r, int u) {
     return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
 // The copying warp: lane w starts the copies of warp w's chunks as its stages become free.
 template <int D, int W>
 __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int lane, int64_t todo,
@@ -826,7 +816,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
 
 // ---------------------------------------------------------------------------
 
-cudaError_t page_map(const void* base, int64_t d, int64_t page, int64_t tiles, int rows, CUtensorMap* out) {
+cudaError_t byte_map(const void* base, int64_t d, int64_t d1, int64_t d2, int b1, int b2, CUtensorMap* out) {
     static std::mutex mu;
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     {
@@ -838,9 +828,9 @@ cudaError_t page_map(const void* base, int64_t d, int64_t page, int64_t tiles, i
             if (e != cudaSuccess || !encode) return e != cudaSuccess ? e : cudaErrorNotSupported;
         }
     }
-    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)tiles};
-    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)(page * d)};
-    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)rows, 1u};
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)d1, (cuuint64_t)d2};
+    cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)(d1 * d)};
+    cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)b1, (cuuint32_t)b2};
     cuuint32_t step[3] = {1u, 1u, 1u};
     const CUresult r = encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, step,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -853,8 +843,8 @@ constexpr size_t kPnMl = (size_t)kSMs * 2 * kPnRows * sizeof(float2);
 size_t pn_part(int d) { return (size_t)kSMs * 2 * kPnRows * d * sizeof(float); }
 }  // namespace
 
-size_t paged_workspace(int64_t max_tokens, int group, int d) {
-    return kPagedCtrl + kPnMl + pn_part(d) + (max_tokens * group <= kPnMost ? 0 : paged_wide_bytes(d));
+size_t paged_workspace(int64_t max_tokens, int heads, int group, int d) {
+    return kPagedCtrl + kPnMl + pn_part(d) + (max_tokens * group <= kPnMost ? 0 : paged_wide_bytes(max_tokens, heads, d));
 }
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
@@ -866,8 +856,8 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         for (int r = 0; r < p.N; ++r) {
             const int64_t tiles = (int64_t)p.c.n_pages * p.hkv_s;
             const int rows = p.c.page < kPnKeys ? p.c.page : kPnKeys;
-            cudaError_t e = page_map(p.c.k[r], p.d, p.c.page, tiles, rows, &a.tk[r]);
-            if (e == cudaSuccess) e = page_map(p.c.v[r], p.d, p.c.page, tiles, rows, &a.tv[r]);
+            cudaError_t e = byte_map(p.c.k[r], p.d, p.c.page, tiles, rows, 1, &a.tk[r]);
+            if (e == cudaSuccess) e = byte_map(p.c.v[r], p.d, p.c.page, tiles, rows, 1, &a.tv[r]);
             if (e != cudaSuccess) return e;
             a.ks[r] = p.c.ks[r];
             a.vs[r] = p.c.vs[r];

@@ -23,9 +23,11 @@
 // CTAs, one per SM, each of which finds its place by itself. Parts of an item
 // that two CTAs share are joined by a kernel behind this one.
 //
-// Warps: 0 copies pages, 1 and 2 issue the products of a tile each, 3 walks the
-// items and reads the page table and scales ahead, 4-11 softmax (four a tile),
-// 12-15 widen values, split the next item's queries, write results.
+// A kernel before this one writes q's terms (done here by the warps that widen
+// values, an item's beginning waited 7 us for them). Warps: 0 copies, 1 and 2
+// issue the products of a tile each, 3 walks the items and reads the page table
+// and scales ahead, 4-11 softmax (four a tile), 12-15 widen values and write
+// results.
 #include <cstring>
 
 #include <cuda.h>
@@ -46,7 +48,7 @@ constexpr int kPwInfos = 12;              // blocks whose pages are read ahead, 
 constexpr int kPwMinCut = 4;              // blocks of the shortest part of an item worth its join
 constexpr int kPwCost = 2;                // what an item's beginning and end take, in blocks
 constexpr float kPwRescale = 8.f;         // m follows the maximum where that has grown by more than this
-constexpr int kPwRegsIo = 88, kPwRegsSoftmax = 160, kPwRegsOut = 104;
+constexpr int kPwRegsIo = 80, kPwRegsSoftmax = 168, kPwRegsOut = 96;
 static_assert(kPwRegsIo + 2 * kPwRegsSoftmax + kPwRegsOut <= 4 * 128, "the launch's registers");
 
 struct __align__(16) PwItem {
@@ -76,7 +78,6 @@ struct PwShape {
         uint64_t info_full[kPwInfos / 4], info_empty[kPwInfos / 4], item_full[kPwQueue], item_empty[kPwQueue], done;
         PwItem queue[kPwQueue];
         PwBlock info[kPwInfos];
-        float row[2][2][kPwM];                          // item's parity, tile: what a row's scores are multiplied by
         float2 stat[2][kPwM];                           // (m, l)
         int64_t sums[kPwThreads / 32], start_at;
         int start_seq, abort;
@@ -88,11 +89,14 @@ struct PwShape {
 };
 
 struct PwArgs {
+    CUtensorMap tq[2];                    // the terms of q as [N T][hq_s][D] bytes, boxes of a tile
     CUtensorMap tk[TP_MAX_SHARDS];        // pools as [n_pages hkv_s][page][D] bytes, boxes of a page
     const uint8_t* v[TP_MAX_SHARDS];
     const float* ks[TP_MAX_SHARDS];
     const float* vs[TP_MAX_SHARDS];
     const bf16* q;
+    uint8_t* q_terms;                     // [2][N][T][hq_s][D]
+    float* q_rows;                        // [N][T][hq_s] what a row's scores are multiplied by
     bf16* out;
     const int* cu;
     const int* pos;
@@ -158,6 +162,16 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
 __device__ __forceinline__ uint32_t e4m3_nan(uint32_t x) { return __vcmpeq4(x & 0x7F7F7F7Fu, 0x7F7F7F7Fu); }
 
 __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -181,7 +195,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&hd.q_full[i], 4);
+            mbar_init(&hd.q_full[i], 1);
             mbar_init(&hd.q_empty[i], 1);
             mbar_init(&hd.s_full[i], 1);
             mbar_init(&hd.p_half[i], 4);
@@ -211,10 +225,12 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
     // ---- the CTA's place in the list of units
     const int heads = a.N * a.hkv_s;
     int bad = 0;
-    int64_t sum = 0;
+    int64_t sum = 0, own = 0;                               // units of the thread's sequences, of the first of them
     for (int b = tid; b < a.B; b += kPwThreads) {
         int c0, n, pos;
-        sum += pw_units(a, b, c0, n, pos) * heads;
+        const int64_t x = pw_units(a, b, c0, n, pos) * heads;
+        if (b == tid) own = x;
+        sum += x;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
     }
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         for (int b0 = 0; b0 < a.B; b0 += kPwThreads) {
             const int b = b0 + tid;
             int c0, n, pos;
-            const int64_t x = b < a.B ? pw_units(a, b, c0, n, pos) * heads : 0;
+            const int64_t x = b0 == 0 ? own : b < a.B ? pw_units(a, b, c0, n, pos) * heads : 0;
             int64_t y = x;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(kAll, y, o);
@@ -298,7 +314,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPwRegsIo));
         if (warp == 0) {
             // ---------------------------------------------------------------- loads
-            uint32_t it = 0, n = 0;
+            uint32_t it = 0, n = 0, nq[2] = {0, 0};         // blocks, entries, Q tiles
             const int page = 1 << a.bits, step = page / 16, box = page * D;
             bool ok = !*abort_flag;
             PwItem w;
@@ -313,6 +329,25 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     if (lane == 0) mbar_arrive_expect_tx(&hd.k_full[s], bytes);
                     __syncwarp();
                     if (is) tma_load_3d_keep(sk + s * Sh::KB + lane * 16 * D, &a.tk[w.r], 0, 0, tile, &hd.k_full[s]);
+                    if (j == 0) {
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (!ok || (t ? w.nb1 : w.nb0) == 0) continue;
+                            if (!(ok = wait_all(&hd.q_empty[t], (nq[t] & 1) ^ 1))) continue;
+                            ++nq[t];
+                            if (lane == 0) {
+                                mbar_arrive_expect_tx(&hd.q_full[t], 2 * a.tpt * a.G * D);
+                                for (int x = 0; x < 2; ++x)
+                                    tma_load_3d_keep(sq + (2 * t + x) * Sh::QT, &a.tq[x], 0, w.kvh * a.G, w.r * a.T + w.t0 + t * a.tpt,
+                                                     &hd.q_full[t]);
+                            }
+                            __syncwarp();
+                        }
+                        if (!ok) {
+                            ++it;                           // (its keys are on the way)
+                            break;
+                        }
+                    }
                     if (!(ok = wait_all(&hd.r_empty[v], ((it / RR) & 1) ^ 1))) {
                         ++it;                               // (its keys are on the way)
                         break;
@@ -325,6 +360,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             }
             volatile int no_abort = 0;                      // no copy may still be landing when the CTA exits
             if (lane == 0) {
+                for (int t = 0; t < 2; ++t)
+                    if (nq[t]) mbar_wait(&hd.q_full[t], (nq[t] - 1) & 1, &no_abort, nullptr);
                 for (uint32_t i = it > RK ? it - RK : 0; i < it; ++i) mbar_wait(&hd.k_full[i % RK], (i / RK) & 1, &no_abort, nullptr);
                 for (uint32_t i = it > RR ? it - RR : 0; i < it; ++i)
                     if (ok || i + 1 < it) mbar_wait(&hd.r_full[i % RR], (i / RR) & 1, &no_abort, nullptr);
@@ -535,7 +572,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         const int t = (warp - 4) >> 2;                      // tile
         const int qd = warp & 3;                            // tensor-memory lane quarter
         const int m = 32 * qd + lane;                       // row of the tile
-        const int tok = m / a.G + t * a.tpt;                // the row's token in the item
+        const int tok0 = m / a.G, tok = tok0 + t * a.tpt;   // the row's token in the item
         const uint32_t lane_off = (uint32_t)(32 * qd) << 16;
         const uint32_t s_col = tmem + lane_off + kPwK * t, o_col = tmem + lane_off + 2 * kPwK + D * t;
         uint32_t sp = 0, ip = 0, in = 0;                    // blocks, items of the tile, entries so far
@@ -548,20 +585,17 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             const int own_max = (int)min((int64_t)w.kend - 1, (int64_t)w.qpos + tok);          // last key the row sees
             const int64_t warp_max = (int64_t)w.qpos + (32 * qd) / a.G + t * a.tpt;            // ... its warp's first row
             const int whole_to = (int)min(warp_max, (int64_t)w.kend - 1);
-            float m_use = -INFINITY, l_run = 0.f, factor = 0.f;
+            float m_use = -INFINITY, l_run = 0.f;
+            const float factor = tok0 < a.tpt && tok < w.ntok ? __ldg(a.q_rows + ((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + m - tok0 * a.G) : 0.f;
             for (int j = 0; j < n; ++j, ++sp) {
                 if ((j & 3) == 0 && !(ok = info_wait_in(in + j))) break;
-                if (j == 0) {                               // (what a row is scaled by is there with its first scores)
-                    if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
-                    factor = hd.row[k & 1][t][m];
-                }
                 const PwBlock& x = hd.info[(in + j) % kPwInfos];
                 const float4 f0 = *reinterpret_cast<const float4*>(&x.kf[0]), f1 = *reinterpret_cast<const float4*>(&x.kf[4]);
                 // what the row's scores of sixteen keys each are multiplied by; never 0, so that -inf stays -inf
                 float kf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) kf[i] = fmaxf(kf[i] * factor, 0x1p-126f);
-                if (j && !(ok = wait_in(&hd.s_full[t], sp & 1))) break;
+                if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
                 if (!idle) {
                     tc_fence_after();
                     const int key0 = (w.blk0 + j) * kPwK, mask = x.mask;
@@ -660,71 +694,15 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             if (lane == 0) mbar_arrive(&hd.st_full[t]);
         }
     } else {
-        // -------------------------------------------------------------------- queries, values, results
+        // -------------------------------------------------------------------- values, results
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPwRegsOut));
         const int qd = warp & 3, m = 32 * qd + lane;
         const int tok0 = m / a.G, g = m - tok0 * a.G;
         const uint32_t o_col = tmem + ((uint32_t)(32 * qd) << 16) + 2 * kPwK;
-        uint32_t nq0 = 0, nq1 = 0, ip0 = 0, ip1 = 0, in = 0, ir = 0;
+        uint32_t ip0 = 0, ip1 = 0, in = 0, ir = 0;
         bool ok = !*abort_flag;
-        // Q of an item's tiles: a row per thread, in two e4m3 terms
-        auto queries = [&](const PwItem& w, int k) {
-#pragma unroll 1
-            for (int t = 0; t < w.nt && ok; ++t) {
-                if ((t ? w.nb1 : w.nb0) == 0) continue;
-                const int tok = tok0 + t * a.tpt;
-                const bool live = tok0 < a.tpt && tok < w.ntok;
-                const uint4* src = reinterpret_cast<const uint4*>(a.q + (((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + g) * D);
-                // (read twice: there are no registers for a row beside the rest)
-                uint32_t most = 0;
-#pragma unroll 4
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    most = __vmaxu2(__vmaxu2(__vmaxu2(most, x.x & 0x7FFF7FFFu), __vmaxu2(x.y & 0x7FFF7FFFu, x.z & 0x7FFF7FFFu)),
-                                    x.w & 0x7FFF7FFFu);
-                }
-                const int e = (int)(max(most & 0xFFFFu, most >> 16) >> 7);           // biased exponent of the largest magnitude
-                // by 2^k to 128 .. 256; a row with infinities or NaN is NaN whatever it is
-                const float by = __uint_as_float((uint32_t)min(252, e ? 127 + 7 + 127 - e : 127) << 23);
-                if (!(ok = wait_in(&hd.q_empty[t], ((t ? nq1 : nq0) & 1) ^ 1))) return;
-                if (t) ++nq1;
-                else ++nq0;
-                unsigned char* dst = sq + 2 * t * Sh::QT;
-#pragma unroll 2
-                for (int u = 0; u < D / 16; ++u) {
-                    uint4 x[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) x[i] = live ? __ldg(src + 2 * u + i) : make_uint4(0, 0, 0, 0);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4& y = x[i / 2];
-                        const float2 p = unpack_bf16x2(i & 1 ? y.z : y.x), q = unpack_bf16x2(i & 1 ? y.w : y.y);
-                        const float f[4] = {p.x * by, p.y * by, q.x * by, q.y * by};
-                        uint32_t h[2], l[2];
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            h[z] = to_e4m3x2(f[2 * z], f[2 * z + 1]);
-                            const float2 back = f16x2_to_float2(e4m3_to_f16x2((uint16_t)h[z]));
-                            l[z] = to_e4m3x2(f[2 * z] - back.x, f[2 * z + 1] - back.y);
-                            if (!(fabsf(f[2 * z]) < INFINITY)) h[z] |= 0x7fu;
-                            if (!(fabsf(f[2 * z + 1]) < INFINITY)) h[z] |= 0x7f00u;
-                        }
-                        hi[i] = h[0] | h[1] << 16;
-                        lo[i] = l[0] | l[1] << 16;
-                    }
-                    *reinterpret_cast<uint4*>(dst + byte_tile_at<D>(m, u)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(dst + Sh::QT + byte_tile_at<D>(m, u)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                }
-                hd.row[k & 1][t][m] = 1.f / by;
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&hd.q_full[t]);
-            }
-        };
         PwItem w;
         bool more = ok && item(0, w, true);
-        if (more) queries(w, 0);
         for (int k = 0; ok && more; ++k) {
             // ---- values of the item's blocks, widened: a lane takes 16 bytes of a key, a warp 8 keys at a time. In a block that
             // some row does not see whole, NaN are taken out, to be put into the rows that see them at the end.
@@ -777,11 +755,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             }
             if (!ok) break;
             in = next_four(in + w.nb);
-            // ---- the next item's queries, before this one's results
-            more = item(k + 1, w, true);
-            if (more) queries(w, k + 1);
-            if (!ok) break;
-            item_read(k, w);
             // ---- results
             const bool part = w.part >= 0;
             const int64_t prow = ((int64_t)blockIdx.x * 2 + (part ? w.part : 0)) * (2 * kPwM);
@@ -891,8 +864,9 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     }
                 }
             }
-            if (ok) item_done(k);
-            if (more) item_read(k + 1, w);
+            if (!ok) break;
+            item_done(k);
+            more = item(k + 1, w, true);
         }
     }
     tc_fence_before();
@@ -905,6 +879,50 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         tmem_dealloc(tmem, 512);
         tmem_relinquish();
     }
+}
+
+// Rows of q in two e4m3 terms, scaled to 128 .. 256 by a power of two each: a lane takes sixteen features. Bound by its bytes.
+template <int D>
+__global__ void __launch_bounds__(256) paged_terms_kernel(const __grid_constant__ PwArgs a) {
+    constexpr int LANES = D / 16;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, rows = (int64_t)a.N * a.T * a.hq_s;
+    const bool is = i < rows * LANES;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q) + 2 * i;
+    uint4 x[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) x[z] = is ? __ldg(src + z) : make_uint4(0, 0, 0, 0);
+    uint32_t most = 0;
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+        most = __vmaxu2(__vmaxu2(__vmaxu2(most, x[z].x & 0x7FFF7FFFu), x[z].y & 0x7FFF7FFFu), __vmaxu2(x[z].z & 0x7FFF7FFFu, x[z].w & 0x7FFF7FFFu));
+    most = max(most & 0xFFFFu, most >> 16);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (!is) return;
+    const int e = (int)(most >> 7);                  // biased exponent of the row's largest magnitude
+    // all of a row with infinities or NaN is NaN
+    const float by = __uint_as_float((uint32_t)(e == 255 ? 255 : min(252, e ? 127 + 7 + 127 - e : 127)) << 23 | (e == 255));
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        const uint4& y = x[v / 2];
+        const float2 p = unpack_bf16x2(v & 1 ? y.z : y.x), q = unpack_bf16x2(v & 1 ? y.w : y.y);
+        const uint32_t f[2] = {pack_f16x2(p.x * by, p.y * by), pack_f16x2(q.x * by, q.y * by)};
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            h[z] = f16x2_to_e4m3x2(f[z]);
+            l[z] = f16x2_to_e4m3x2(sub_f16x2(f[z], e4m3_to_f16x2((uint16_t)h[z])));
+        }
+        hi[v] = h[0] | h[1] << 16;
+        lo[v] = l[0] | l[1] << 16;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(a.q_terms);
+    dst[i] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    dst[rows * LANES + i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if (i % LANES == 0) a.q_rows[i / LANES] = e == 255 ? 1.f : 1.f / by;
 }
 
 // Rows of the items that were cut, a warp each: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts
@@ -962,15 +980,30 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
     }
 }
 
-size_t paged_wide_bytes(int d) {
-    return ((kSMs * sizeof(PagedCut) + 255) & ~(size_t)255) + (size_t)kSMs * 2 * 2 * kPwM * (sizeof(float2) + d * sizeof(float));
+// Cuts, partial (m, l), partial O, q's terms and rows.
+static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+static const size_t kPwCuts = up256(kSMs * sizeof(PagedCut)), kPwMl = (size_t)kSMs * 2 * 2 * kPwM * sizeof(float2);
+static size_t pw_o(int d) { return (size_t)kSMs * 2 * 2 * kPwM * d * sizeof(float); }
+size_t paged_wide_bytes(int64_t tokens, int heads, int d) {
+    return kPwCuts + kPwMl + pw_o(d) + up256((size_t)tokens * heads * d * 2) + up256((size_t)tokens * heads * sizeof(float));
 }
 
 cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStream_t s) {
     PwArgs a;
     memset(&a, 0, sizeof a);
+    a.cuts = reinterpret_cast<PagedCut*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + kPwCuts);
+    a.part_o = reinterpret_cast<float*>(ws + kPwCuts + kPwMl);
+    a.q_terms = reinterpret_cast<uint8_t*>(ws + kPwCuts + kPwMl + pw_o(p.d));
+    const int64_t rows = (int64_t)p.N * p.T * p.hq_s;
+    a.q_rows = reinterpret_cast<float*>(a.q_terms + up256((size_t)rows * p.d * 2));
+    const int G = p.hq_s / p.hkv_s;
+    for (int x = 0; x < 2; ++x) {
+        const cudaError_t e = byte_map(a.q_terms + x * rows * p.d, p.d, p.hq_s, (int64_t)p.N * p.T, G, kPwM / G, &a.tq[x]);
+        if (e != cudaSuccess) return e;
+    }
     for (int r = 0; r < p.N; ++r) {
-        const cudaError_t e = page_map(p.c.k[r], p.d, p.c.page, (int64_t)p.c.n_pages * p.hkv_s, p.c.page, &a.tk[r]);
+        const cudaError_t e = byte_map(p.c.k[r], p.d, p.c.page, (int64_t)p.c.n_pages * p.hkv_s, p.c.page, 1, &a.tk[r]);
         if (e != cudaSuccess) return e;
         a.v[r] = p.c.v[r];
         a.ks[r] = p.c.ks[r];
@@ -981,16 +1014,13 @@ cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStr
     a.cu = p.cu;
     a.pos = p.pos;
     a.pages = p.c.pages;
-    a.cuts = reinterpret_cast<PagedCut*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(ws + ((kSMs * sizeof(PagedCut) + 255) & ~(size_t)255));
-    a.part_o = reinterpret_cast<float*>(a.part_ml + (size_t)kSMs * 2 * 2 * kPwM);
     a.status = p.status;
     a.N = p.N;
     a.B = p.B;
     a.T = p.T;
     a.hq_s = p.hq_s;
     a.hkv_s = p.hkv_s;
-    a.G = p.hq_s / p.hkv_s;
+    a.G = G;
     a.tpt = kPwM / a.G;
     a.bits = 31 - __builtin_clz((unsigned)p.c.page);
     a.width = p.c.width;
@@ -1003,7 +1033,9 @@ cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStr
     const void* fn = d128 ? reinterpret_cast<const void*>(paged_items_kernel<128>) : reinterpret_cast<const void*>(paged_items_kernel<64>);
     const int smem = d128 ? PwShape<128>::SMEM : PwShape<64>::SMEM;
     void* args[] = {&a};
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = launch_pdl(d128 ? reinterpret_cast<const void*>(paged_terms_kernel<128>) : reinterpret_cast<const void*>(paged_terms_kernel<64>), args,
+                               (int)((rows * (p.d / 16) + 255) / 256), 0, s, 256);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kPwThreads);
     if (e != cudaSuccess) return e;
     int slices = 16;

@@ -1553,7 +1553,7 @@ static tp_status paged_plan(const char* who, tp_plan_t plan, size_t& bytes) {
     if (!plan) return fail(TP_ERR_NULL, "%s: NULL argument", who);
     if (!plan->dense) return fail(TP_ERR_INVALID_ARG, "%s: the plan has no attention block", who);
     if (plan->d.dtype != TP_BF16) return fail(TP_ERR_UNSUPPORTED, "%s: bf16 plans have a paged workspace", who);
-    bytes = paged_workspace(plan->d.max_tokens, (int)(plan->d.n_heads / plan->d.n_kv_heads), (int)plan->d.head_dim);
+    bytes = paged_workspace(plan->d.max_tokens, (int)plan->d.n_heads, (int)(plan->d.n_heads / plan->d.n_kv_heads), (int)plan->d.head_dim);
     return TP_OK;
 }
 

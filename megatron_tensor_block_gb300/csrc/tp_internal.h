@@ -450,16 +450,16 @@ struct PagedCut {                         // an item that begins in a CTA and go
     int parts, t0, ntok, h, qpos;         // 0 parts: none
 };
 // Bytes of a paged workspace for calls of at most max_tokens rows.
-size_t paged_workspace(int64_t max_tokens, int group, int d);
+size_t paged_workspace(int64_t max_tokens, int heads, int group, int d);
 constexpr size_t kPagedCtrl = 4096;       // control words at its start, zero between calls but for the status
 cudaError_t launch_rope(const RopeArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t s);
 // Sequences of more than `few` query rows per KV head; bytes of its part of the workspace (kernels_paged_wide.cu).
 cudaError_t launch_paged_wide(const PagedAttnArgs& a, int few, char* ws, cudaStream_t s);
-size_t paged_wide_bytes(int d);
-// Pages' bytes [tiles][page][d] as a tensor map of boxes of `rows` keys, swizzled over their rows' width.
-cudaError_t page_map(const void* base, int64_t d, int64_t page, int64_t tiles, int rows, CUtensorMap* out);
+size_t paged_wide_bytes(int64_t tokens, int heads, int d);
+// Bytes [d2][d1][d] as a tensor map of boxes of b2 x b1 rows, swizzled over the rows' width.
+cudaError_t byte_map(const void* base, int64_t d, int64_t d1, int64_t d2, int b1, int b2, CUtensorMap* out);
 
 // launchers (return the launch's cudaError_t)
 cudaError_t launch_gemv(const GemvParams& p, int epi, int dtype, cudaStream_t s);
