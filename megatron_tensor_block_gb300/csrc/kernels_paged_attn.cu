@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "paged.cuh"
 #include "stream.cuh"
 #include "tp_internal.h"
 
@@ -41,9 +42,6 @@ namespace tpk {
 // took 63.)
 // ---------------------------------------------------------------------------
 
-constexpr int kPnKeys = 32;               // keys of a chunk
-constexpr int kPnRows = 16;               // query rows that a warp works on
-constexpr int kPnMost = 32;               // ... of a sequence and KV head that are this kernel's, sixteen at a time
 constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
 
 struct PnPiece {                          // of a head of a sequence
@@ -69,7 +67,7 @@ struct PnShape {
         int64_t at[W];                                              // a warp's place in its first sequence
         PnPiece pieces[2 * W];                                      // of warp w: one that began before it, one that goes on behind it
         int valid[W][STAGES];                                       // halves whose page is there
-        int seq[W], last[2], first_cta[2], abort;
+        int seq[W], last[2], first_cta[2], many[W + 1], abort;
     };
     static constexpr int HEAD = ((int)sizeof(Head) + 1023) & ~1023;
     static constexpr int SMEM = HEAD + W * (RING + SLOT);
@@ -100,20 +98,15 @@ __device__ __forceinline__ int pn_chunks(const PnArgs& a, int b, int& c0, int& n
     n = __ldg(a.cu + b + 1) - c0;
     pos = __ldg(a.pos + b);
     if (n <= 0 || n > a.max_new || (int64_t)n * a.G > kPnMost) return 0;
-    const int64_t end = (int64_t)pos + n;
-    const int kend = (int)(end < 0 ? 0 : end > a.cap ? a.cap : end);
-    return max(1, (kend + kPnKeys - 1) / kPnKeys);
+    return paged_chunks(n, pos, a.cap);
 }
-
-// A head's query rows are worked on sixteen at a time.
-__device__ __forceinline__ int pn_groups(const PnArgs& a, int n) { return (n * a.G + kPnRows - 1) / kPnRows; }
 
 // A place in the batch's list of chunks: of a sequence, the chunks of every head's groups of rows.
 struct PnCursor {
     int b, h, c, nch, c0, n, pos, groups; // h: head times groups, and the group
     __device__ __forceinline__ void begin(const PnArgs& a, int64_t in_sequence) {
         nch = pn_chunks(a, b, c0, n, pos);
-        groups = pn_groups(a, n);
+        groups = paged_groups(n, a.G);
         h = (int)(in_sequence / nch);
         c = (int)(in_sequence - (int64_t)h * nch);
     }
@@ -126,7 +119,7 @@ struct PnCursor {
             ++b;
             nch = b < a.B ? pn_chunks(a, b, c0, n, pos) : 1;
         } while (nch == 0);
-        groups = pn_groups(a, n);
+        groups = paged_groups(n, a.G);
     }
     __device__ __forceinline__ int kend(const PnArgs& a) const {
         const int64_t end = (int64_t)pos + n;
@@ -617,15 +610,16 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
 
     // ---- the CTA's and its warps' place in the list of chunks
     const int heads = a.N * a.hkv_s;
-    int bad = 0;
+    int bad = 0, many = 0;
     int64_t sum = 0, own = 0;                               // chunks of the thread's sequences, of the first of them
     for (int b = tid; b < a.B; b += THREADS) {
         int c0, n, pos;
         int64_t x = (int64_t)pn_chunks(a, b, c0, n, pos) * heads;
-        if (x) x *= pn_groups(a, n);
+        if (x) x *= paged_groups(n, a.G);
         if (b == tid) own = x;
         sum += x;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
+        many |= n > 0 && (int64_t)n * a.G > kPnMost && n <= a.max_new;
         if (blockIdx.x == 0 && n > 0) {
             if (n > a.max_new) set_status(a.status, TP_ERR_SHAPE);
             else if (pos < 0 || (int64_t)pos + n > a.cap) set_status(a.status, TP_ERR_CAPACITY);
@@ -637,7 +631,8 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         const int64_t v = __shfl_up_sync(0xffffffffu, upto_own, o);
         if (lane >= o) upto_own += v;
     }
-    if (lane == 0) hd.sums[warp] = sum;
+    many = __any_sync(0xffffffffu, many);
+    if (lane == 0) hd.sums[warp] = sum, hd.many[warp] = many;
     if (lane == 31) hd.firsts[warp] = upto_own;
     if (__syncthreads_or(bad)) {
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
@@ -646,9 +641,11 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     int64_t total = 0, base = 0, before_own = upto_own - own;
     for (int i = 0; i < WARPS; ++i) {
         total += hd.sums[i];
+        many |= hd.many[i];
         if (i < warp) before_own += hd.firsts[i];
         base += hd.firsts[i];
     }
+    if (many && total <= kPagedFewBeside) return;        // left to the prompts' kernel
     // a chunk for each warp at least: fewer CTAs then have fewer pieces to join
     const int ctas = (int)min((int64_t)gridDim.x, (total + W - 1) / W);
     if ((int)blockIdx.x >= ctas) return;
@@ -673,7 +670,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         const int b = b0 + tid;
         int c0, n, pos;
         int64_t x = b < a.B ? (int64_t)pn_chunks(a, b, c0, n, pos) * heads : 0;
-        if (x) x *= pn_groups(a, n);
+        if (x) x *= paged_groups(n, a.G);
         int64_t y = x;
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t v = __shfl_up_sync(0xffffffffu, y, o);

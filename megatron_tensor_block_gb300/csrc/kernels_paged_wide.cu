@@ -35,6 +35,7 @@
 #include "attn.cuh"
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "paged.cuh"
 #include "stream.cuh"
 #include "tcgen05.cuh"
 #include "tp_internal.h"
@@ -45,8 +46,8 @@ constexpr int kPwM = 128, kPwK = 128;     // query rows of a tile, keys of a blo
 constexpr int kPwThreads = 512;
 constexpr int kPwQueue = 4;               // items read ahead
 constexpr int kPwInfos = 12;              // blocks whose pages are read ahead, in fours
-constexpr int kPwMinCut = 4;              // blocks of the shortest part of an item worth its join
-constexpr int kPwCost = 2;                // what an item's beginning and end take, in blocks
+constexpr int kPwMinCut = 2;              // blocks of the shortest part of an item worth its join
+constexpr int kPwCost = 3;                // what an item's beginning and end take, in blocks
 constexpr float kPwRescale = 8.f;         // m follows the maximum where that has grown by more than this
 constexpr int kPwRegsIo = 80, kPwRegsSoftmax = 168, kPwRegsOut = 96;
 static_assert(kPwRegsIo + 2 * kPwRegsSoftmax + kPwRegsOut <= 4 * 128, "the launch's registers");
@@ -79,7 +80,7 @@ struct PwShape {
         PwItem queue[kPwQueue];
         PwBlock info[kPwInfos];
         float2 stat[2][kPwM];                           // (m, l)
-        int64_t sums[kPwThreads / 32], start_at;
+        int64_t sums[3][kPwThreads / 32], start_at;
         int start_seq, abort;
         uint32_t tmem;
     };
@@ -113,12 +114,12 @@ __device__ __forceinline__ int pw_blocks(const PwArgs& a, int pos, int tokens) {
     const int64_t e = (int64_t)pos + tokens;
     return (int)(((e < 0 ? 0 : e > a.cap ? a.cap : e) + kPwK - 1) / kPwK);
 }
-// Units of a sequence for each head: its items' blocks, and what items take besides; 0 where it is not this kernel's.
-__device__ __forceinline__ int64_t pw_units(const PwArgs& a, int b, int& c0, int& n, int& pos) {
+// Units of a sequence for each head: its items' blocks, and what items take besides; 0 where it has `few` rows or fewer.
+__device__ __forceinline__ int64_t pw_units(const PwArgs& a, int few, int b, int& c0, int& n, int& pos) {
     c0 = __ldg(a.cu + b);
     n = __ldg(a.cu + b + 1) - c0;
     pos = __ldg(a.pos + b);
-    if (n <= 0 || n > a.max_new || (int64_t)n * a.G <= a.few) return 0;
+    if (n <= 0 || n > a.max_new || (int64_t)n * a.G <= few) return 0;
     const int per = 2 * a.tpt;
     int64_t sum = 0;
     for (int i = 0; i < n; i += per) sum += pw_blocks(a, pos, min(n, i + per)) + kPwCost;
@@ -225,24 +226,34 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
     // ---- the CTA's place in the list of units
     const int heads = a.N * a.hkv_s;
     int bad = 0;
-    int64_t sum = 0, own = 0;                               // units of the thread's sequences, of the first of them
+    int64_t sum[3] = {0, 0, 0}, own = 0, own_few = 0;       // units of the thread's sequences of many rows, and of few; the latter's chunks
     for (int b = tid; b < a.B; b += kPwThreads) {
         int c0, n, pos;
-        const int64_t x = pw_units(a, b, c0, n, pos) * heads;
-        if (b == tid) own = x;
-        sum += x;
+        const int64_t x = pw_units(a, 0, b, c0, n, pos) * heads;
+        const bool few = (int64_t)n * a.G <= a.few;
+        if (b == tid) own = few ? 0 : x, own_few = few ? x : 0;
+        sum[0] += few ? 0 : x;
+        sum[1] += few ? x : 0;
+        if (few && x) sum[2] += paged_few_chunks(n, pos, a.G, a.cap) * heads;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
     }
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) hd.sums[warp] = sum;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        for (int o = 16; o; o >>= 1) sum[i] += __shfl_xor_sync(kAll, sum[i], o);
+        if (lane == 0) hd.sums[i][warp] = sum[i];
+    }
     if (tid == 0) a.cuts[blockIdx.x].parts = 0;
     tc_fence_before();
     const bool malformed = __syncthreads_or(bad);
     tc_fence_after();
     const uint32_t tmem = uniform(hd.tmem);
-    int64_t total = 0;
+    int64_t total = 0, total_few = 0, chunks = 0;
     if (!malformed)
-        for (int i = 0; i < WARPS; ++i) total += hd.sums[i];
+        for (int i = 0; i < WARPS; ++i) total += hd.sums[0][i], total_few += hd.sums[1][i], chunks += hd.sums[2][i];
+    // the sequences of few rows too, where the other kernel has left them
+    const bool take = total > 0 && chunks <= kPagedFewBeside;
+    const int few = take ? 0 : a.few;
+    if (take) total += total_few, own += own_few;
     // parts of a few blocks at least: as few CTAs as that takes
     const int ctas = (int)min((int64_t)gridDim.x, (total + kPwMinCut + kPwCost - 1) / (kPwMinCut + kPwCost));
     const bool mine = (int)blockIdx.x < ctas;
@@ -252,19 +263,19 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         for (int b0 = 0; b0 < a.B; b0 += kPwThreads) {
             const int b = b0 + tid;
             int c0, n, pos;
-            const int64_t x = b0 == 0 ? own : b < a.B ? pw_units(a, b, c0, n, pos) * heads : 0;
+            const int64_t x = b0 == 0 ? own : b < a.B ? pw_units(a, few, b, c0, n, pos) * heads : 0;
             int64_t y = x;
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t v = __shfl_up_sync(kAll, y, o);
                 if (lane >= o) y += v;
             }
             __syncthreads();
-            if (lane == 31) hd.sums[warp] = y;
+            if (lane == 31) hd.sums[0][warp] = y;
             __syncthreads();
             int64_t before = base + y - x;
             for (int i = 0; i < WARPS; ++i) {
-                if (i < warp) before += hd.sums[i];
-                base += hd.sums[i];
+                if (i < warp) before += hd.sums[0][i];
+                base += hd.sums[0][i];
             }
             if (from >= before && from < before + x) {
                 hd.start_seq = b;
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             };
             if (mine && ok) {
                 int b = hd.start_seq, c0, len, pos;
-                int64_t units = pw_units(a, b, c0, len, pos), at = hd.start_at;      // of the sequence for each head; the item's place
+                int64_t units = pw_units(a, few, b, c0, len, pos), at = hd.start_at;      // of the sequence for each head; the item's place
                 int h = (int)((from - at) / units), i = 0;
                 at += h * units;
                 const int per = 2 * a.tpt;
@@ -553,7 +564,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         if (++h == heads) {
                             h = 0;
                             do {
-                                units = ++b < a.B ? pw_units(a, b, c0, len, pos) : 1;
+                                units = ++b < a.B ? pw_units(a, few, b, c0, len, pos) : 1;
                             } while (units == 0);
                             if (b >= a.B) break;
                         }
@@ -642,6 +653,14 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         }
                     }
                     const float m_sub = m_use == -INFINITY ? 0.f : m_use;            // nothing seen yet: every weight is 0
+                    // e kf - m in one rounding is not 0 for the largest, but off by half a step of m: of scores so large that this
+                    // counts the products are rounded first
+                    if (__any_sync(kAll, fabsf(m_sub) > 0x1p17f)) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i) e[i] *= kf[i / 16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) kf[i] = 1.f;
+                    }
                     const uint64_t neg2 = f2_pack(-m_sub, -m_sub);
                     uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll

@@ -1,0 +1,30 @@
+// What the two kernels of the attention over pages agree on: which of them has
+// a batch's sequences of few query rows.
+#pragma once
+
+#include "common.cuh"
+
+namespace tpk {
+
+constexpr int kPnKeys = 32;               // keys of a chunk
+constexpr int kPnRows = 16;               // query rows that a warp works on
+constexpr int kPnMost = 32;               // ... of a sequence and KV head that are few, sixteen at a time
+// Chunks of such sequences beside prompts that go with these: so few that their own kernel, which the prompts' has to wait
+// for, would leave most of the machine idle. Single tokens behind 1000 keys and a prompt of 512, 8 KV heads of 128, with
+// the prompt and apart: 8 tokens (2048 chunks) 33.3 and 41.4 us, 16 (4096) 38.4 and 44.1, 32 (8192) 56.9 and 50.2, 64 89.5
+// and 63.8.
+constexpr int64_t kPagedFewBeside = 5000;
+
+// A head's query rows are worked on sixteen at a time.
+__device__ __forceinline__ int paged_groups(int n, int G) { return (n * G + kPnRows - 1) / kPnRows; }
+// Chunks of keys of a sequence (n new tokens from position pos on, pages for cap) for each head.
+__device__ __forceinline__ int paged_chunks(int n, int pos, int cap) {
+    const int64_t end = (int64_t)pos + n;
+    const int kend = (int)(end < 0 ? 0 : end > cap ? cap : end);
+    return max(1, (kend + kPnKeys - 1) / kPnKeys);
+}
+__device__ __forceinline__ int64_t paged_few_chunks(int n, int pos, int G, int cap) {
+    return (int64_t)paged_chunks(n, pos, cap) * paged_groups(n, G);
+}
+
+}  // namespace tpk

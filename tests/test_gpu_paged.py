@@ -211,6 +211,11 @@ ATTENDS = {
     "sharp": (L(8, 2, 128, 1), 16, [200, 1, 3], [300, 700, 100], dict(sharp=12.0), 0),
     "unlike_scales": (L(8, 2, 128, 1), 16, [200, 1, 3], [300, 700, 100], dict(spread=12, sharp=0.01), 0),
     "far_apart_scales": (L(8, 2, 64, 1), 16, [60, 1, 3], [300, 700, 100], dict(spread=25, sharp=1e-6), 0),
+    # a few single tokens that go with a prompt, and more that do not
+    "few_beside_a_prompt": (L(32, 8, 64, 2), 64, [1, 600, 2, 0, 4, 1], [700, 5, 129, 3, 1000, 0], {}, 0),
+    "many_beside_a_prompt": (L(8, 8, 64, 1), 16, [1] * 40 + [70], [600] * 40 + [10], {}, 0),
+    "groups_of_rows": (L(8, 1, 64, 1), 16, [3, 4, 1, 2], [100, 31, 70, 256], {}, 4),
+    "groups_of_rows_128": (L(6, 2, 128, 2), 32, [10, 3, 6, 1], [100, 31, 700, 256], {}, 10),
     "rows_behind": (QWEN, 16, [3, 60], [10, 0], dict(extra_rows=77), 0),
     "rows_behind_decode": (QWEN, 16, [1, 1], [10, 0], dict(extra_rows=5), 1),
     "all_empty": (QWEN, 16, [0, 0], [3, 0], dict(extra_rows=9), 0),
@@ -286,3 +291,156 @@ def test_pages_outside_the_pool_are_not_seen(gpu_lib, new):
                     want = w @ v[h // b.lay.group][seen] / w.sum()
                     most = np.abs(v[h // b.lay.group][seen]).max()
                     assert (np.abs(got[r, t, h] - want) <= 2.0 ** -7 * most).all()
+
+
+def formula(b, r, s, i, h, v=None):
+    """Attention of one row in float64, NaN and all."""
+    p = b.cached[s] + i
+    k = b.keys("k", s, r, p + 1)[h // b.lay.group]
+    v = b.keys("v", s, r, p + 1)[h // b.lay.group]
+    with np.errstate(invalid="ignore", over="ignore"):
+        x = k @ b.q[r, b.cu[s] + i, h] / np.sqrt(b.lay.d)
+        w = np.exp(x - x.max())
+        return w @ v / w.sum(), np.abs(v).max()
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [4, 2, 3], [9, 40, 150]], ids=["decode", "few", "prompts"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_reaches_the_rows_that_see_it(gpu_lib, new, d):
+    """NaN in a key: every row that sees it, whole. In a value: that feature. In a query: its row. Not elsewhere, and not from
+    slots that a row does not see."""
+    lay = L(8, 4, d, 2)
+    b = K.Batch(lay, new, [40, 130, 5], 16)
+    spots = []                                              # (which, shard, kv head, sequence, position, feature)
+    for s, n in enumerate(new):
+        last = b.cached[s] + n - 1
+        spots += [("v", 0, 1, s, last, 3), ("v", 1, 0, s, max(0, last - n // 2), d - 1), ("k", 1, 1, s, last, 0)]
+    spots += [("v", 0, 0, 1, 7, 0), ("k", 0, 1, 0, 11, 2)]
+    for which, r, kv, s, p, i in spots:
+        b.codes[which][r, b.table[s, p // 16], kv, p % 16, i] = 0xFF if i % 2 else 0x7F
+    b.q[0, b.cu[1], 2, 5], b.q[1, b.cu[2], 0, 1] = np.inf, np.nan
+    dev = K.OnDevice(gpu_lib, b)
+    dev.attend()
+    assert dev.status() == 0
+    got = dev.got()
+    for r in range(2):
+        for s, n in enumerate(new):
+            for i in range(n):
+                for h in range(lay.hq):
+                    want, most = formula(b, r, s, i, h)
+                    if not np.isfinite(b.q[r, b.cu[s] + i, h]).all():
+                        want = np.full(d, np.nan)
+                    g = got[r, b.cu[s] + i, h]
+                    assert (np.isnan(g) == np.isnan(want)).all(), (r, s, i, h, np.argwhere(np.isnan(g) != np.isnan(want))[:4])
+                    most = np.nanmax(np.abs(b.keys("v", s, r, b.cached[s] + i + 1)))
+                    ok = np.isfinite(want)
+                    assert (np.abs(g - want)[ok] <= 2.0 ** -7 * most).all()
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [70, 33]], ids=["decode", "few", "prompts"])
+def test_extremes(gpu_lib, new):
+    """Zeros, the largest values with the largest scales, and queries of unlike sizes."""
+    b = K.Batch(L(8, 2, 64, 1), new, [100, 31], 16, spread=0)
+    b.q[0, :, 0], b.q[0, :, 1], b.q[0, :, 2] = 0.0, K.bf16(b.q[0, :, 1] * 1e30), K.bf16(b.q[0, :, 2] * 1e-30)
+    b.scale["v"][0, :, 1] = 2.0 ** 110
+    b.scale["v"][0, :, 0] = 2.0 ** -60
+    b.scale["k"][0, :, 0] = 2.0 ** -60
+    d = K.OnDevice(gpu_lib, b)
+    d.attend()
+    assert d.status() == 0
+    K.check(d.got(), b)
+
+
+def test_two_streams_with_workspaces_of_their_own(gpu_lib):
+    import torch
+    batches = [attend_batch("mixed"), attend_batch("decode"), attend_batch("prompts_cached")]
+    devs = [K.OnDevice(gpu_lib, b, m) for b, m in batches]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in devs]
+    for _ in range(5):
+        for d, s in zip(devs, streams):
+            d.attend(s)
+    torch.cuda.synchronize()
+    for d in devs:
+        assert d.status() == 0
+        K.check(d.got(), d.b)
+
+
+@pytest.mark.parametrize("name,max_new", [("decode", 1), ("mixed", 0), ("few_tokens", 4)])
+def test_captured_calls_replay_with_other_lengths(gpu_lib, name, max_new):
+    """Append and attend in one graph, two graphs on one workspace; the replays follow what the offsets, positions, table and
+    rows hold by then."""
+    import torch
+    b, _ = attend_batch(name)
+    d = K.OnDevice(gpu_lib, b, max_new)
+    rope = R(theta=1e4)
+    q_out = torch.empty_like(d.q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                d.append(rope, q=d.q, q_out=q_out, stream=side)
+                gpu_lib.tp_attn_paged(d.plan, q_out, d.kv, d.cu, d.pos, b.B, b.T, d.out, d.ws, d.nbytes, max_new, side)
+            graphs.append(g)
+    torch.cuda.synchronize()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    first = d.out.clone()
+    # the sequences in another order, shorter by what the last have more
+    order = list(range(b.B))[::-1]
+    new, cached = [b.new[i] for i in order], [b.cached[i] for i in order]
+    d.cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32))
+    d.pos.copy_(torch.tensor(cached, dtype=torch.int32))
+    d.table.copy_(d.table.flip(0).clone())
+    rows = torch.cat([torch.arange(int(b.cu[i]), int(b.cu[i]) + b.new[i]) for i in order] + [torch.arange(b.used, b.T)]).cuda()
+    for x in (d.q, d.new_k, d.new_v):
+        x.copy_(x[:, rows].clone())
+    graphs[1].replay()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert d.word.item() == 0 and d.status() == 0
+    # the same values, summed up in another order where parts fall differently
+    got, want = d.out[:, :b.used].float(), first[:, rows[:b.used]].float()
+    assert (got - want).abs().max() <= 2.0 ** -7 * want.abs().max()
+
+
+def test_chunks_then_single_tokens(gpu_lib):
+    """As a server runs them: prompts appended and attended to in chunks, then token by token; every step against float64 over
+    the rotated keys and values that the steps before have stored."""
+    import torch
+    lay, rope, page = L(8, 2, 128, 2), WAVES, 32
+    steps = [[50, 7, 33], [30, 0, 1], [1, 1, 1], [2, 1, 0], [1, 3, 1], [1, 1, 1]]
+    total = [sum(s[i] for s in steps) for i in range(3)]
+    base = K.Batch(lay, total, [0, 0, 0], page)
+    base.codes = {n: np.full_like(base.codes[n], 0x7F) for n in "kv"}
+    dev = K.OnDevice(gpu_lib, base)
+    fed = [0, 0, 0]
+    for step, new in enumerate(steps):
+        T = sum(new)
+        rows = np.concatenate([base.cu[i] + fed[i] + np.arange(n) for i, n in enumerate(new)]).astype(int)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32).cuda()
+        pos = torch.tensor(fed, dtype=torch.int32).cuda()
+        q, k, v = (x[:, rows].contiguous() for x in (dev.q, dev.new_k, dev.new_v))
+        q_out, out = torch.empty_like(q), torch.empty_like(q)
+        gpu_lib.tp_kv_append_paged(dev.plan, gpu_lib.tp_rope(**rope), k, v, dev.kv, cu, pos, 3, T, q=q, q_out=q_out,
+                                   device_status=dev.word)
+        gpu_lib.tp_attn_paged(dev.plan, q_out, dev.kv, cu, pos, 3, T, out, dev.ws, dev.nbytes, max(new))
+        now = K.Batch(lay, new, fed, page, width=base.width)
+        now.n_pages, now.table = base.n_pages, base.table
+        now.q = q_out.double().cpu().numpy()
+        now.codes = {n: np.stack([x.cpu().numpy() for x in dev.pool[n]]) for n in "kv"}
+        now.scale = {n: np.stack([x.cpu().numpy().astype(np.float64) for x in dev.scale[n]]) for n in "kv"}
+        K.check(out.double().cpu().numpy(), now)
+        # what is stored stands for the rotated keys: four significant bits, brought to a larger scale at most a few times
+        for i, n in enumerate(new):
+            fed[i] += n
+            for r in range(2):
+                at = slice(int(base.cu[i]), int(base.cu[i]) + fed[i])
+                want = K.rotate(base.new_k[r, at][None], np.arange(fed[i]), rope, 5e5)[0][0].transpose(1, 0, 2)
+                got = now.keys("k", i, r, fed[i])
+                e = np.repeat(now.scale["k"][r, now.table[i, :-(-fed[i] // page)]].T, page, 1)[:, :fed[i], None]
+                assert (np.abs(got - want) <= 2.0 ** -4 * np.abs(want) * 1.01 + 2.0 ** -9 * e).all()
+    assert dev.word.item() == 0 and dev.status() == 0
