@@ -606,13 +606,16 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 float kf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) kf[i] = fmaxf(kf[i] * factor, 0x1p-126f);
+                // S is below 2^24: the scores are below 2^17 but for such factors
+                const bool large = __any_sync(kAll, max3(max3(kf[0], kf[1], kf[2]), max3(kf[3], kf[4], kf[5]), fmaxf(kf[6], kf[7])) > 0x1p-7f);
                 if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
                 if (!idle) {
                     tc_fence_after();
                     const int key0 = (w.blk0 + j) * kPwK, mask = x.mask;
                     const float down = x.down;
-                    // a block that every row of the warp sees whole needs no mask
-                    const bool whole = key0 + kPwK - 1 <= whole_to && mask == 0xFF;
+                    // A block that every row of the warp sees whole needs no mask. (And below, s kf - m in one rounding is off by half
+                    // a step of m for the largest: scores so large that this counts are rounded before.)
+                    const bool whole = key0 + kPwK - 1 <= whole_to && mask == 0xFF && !large;
                     const int hi = own_max - key0;          // last key of the block the row sees
                     uint32_t v[4][32];
 #pragma unroll
@@ -621,7 +624,9 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     float* e = reinterpret_cast<float*>(&v[0][0]);
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 128; ++i) e[i] = i <= hi && (mask >> (i / 16) & 1) ? e[i] : -INFINITY;
+                        for (int i = 0; i < 128; ++i) e[i] = i <= hi && (mask >> (i / 16) & 1) ? e[i] * kf[i / 16] : -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) kf[i] = 1.f;
                     }
                     float mq[4];                            // independent chains
 #pragma unroll
@@ -653,14 +658,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         }
                     }
                     const float m_sub = m_use == -INFINITY ? 0.f : m_use;            // nothing seen yet: every weight is 0
-                    // e kf - m in one rounding is not 0 for the largest, but off by half a step of m: of scores so large that this
-                    // counts the products are rounded first
-                    if (__any_sync(kAll, fabsf(m_sub) > 0x1p17f)) {
-#pragma unroll
-                        for (int i = 0; i < 128; ++i) e[i] *= kf[i / 16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) kf[i] = 1.f;
-                    }
                     const uint64_t neg2 = f2_pack(-m_sub, -m_sub);
                     uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
