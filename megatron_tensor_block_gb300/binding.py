@@ -451,9 +451,11 @@ def _rows(plan: Plan, t, name: str, heads: int, T: int, dtype, device: int):
         return tp_rows(t, heads * d, T * heads * d)
     if t.dtype is not dtype:
         raise TypeError(f"{name}: {t.dtype}, expected {dtype}")
-    shape = t.shape
-    if len(shape) != 4 or shape[0] != plan.tp or shape[1] < T or shape[2] != heads or shape[3] != d:
-        raise ValueError(f"{name}: {tuple(shape)}, expected ({plan.tp}, at least {T}, {heads}, {d})")
+    if t.dim() != 4:
+        raise ValueError(f"{name}: {tuple(t.shape)}, expected ({plan.tp}, at least {T}, {heads}, {d})")
+    shards, rows, many, features = t.shape
+    if features != d or many != heads or shards != plan.tp or rows < T:
+        raise ValueError(f"{name}: {tuple(t.shape)}, expected ({plan.tp}, at least {T}, {heads}, {d})")
     if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     shard, token, head, one = t.stride()

@@ -1379,8 +1379,14 @@ static tp_status rope_table(const char* who, tp_plan_t plan, const tp_rope* rope
         last = std::min(std::ceil(pair(rope->low)), (double)rot - 1);
     }
     t = RopeTable{};
+    // theta^(-2 i / rot) as a product of two powers: 16 calls of pow and not 64, which a call's host time would be made of
+    double coarse[8], fine[8];
+    for (int i = 0; i < 8; ++i) {
+        coarse[i] = 8 * i < rot / 2 ? std::pow(theta, -16.0 * i / (double)rot) : 0;
+        fine[i] = i < rot / 2 ? std::pow(theta, -2.0 * i / (double)rot) : 0;
+    }
     for (int64_t i = 0; i < rot / 2; ++i) {
-        double g = std::pow(theta, -2.0 * (double)i / (double)rot);
+        double g = coarse[i / 8] * fine[i % 8];
         if (rope->scaling == TP_ROPE_LINEAR) g /= f;
         if (rope->scaling == TP_ROPE_WAVELENGTH) {
             const double u = std::min(1.0, std::max(0.0, ((double)rope->original * g / two_pi - rope->low) / (rope->high - rope->low)));
@@ -1390,7 +1396,7 @@ static tp_status rope_table(const char* who, tp_plan_t plan, const tp_rope* rope
             const double u = std::min(1.0, std::max(0.0, ((double)i - first) / std::max(last - first, 0.001)));
             g = (1 - u) * g + u * g / f;
         }
-        t.turn[i] = (uint64_t)std::nearbyint(std::ldexp(g / two_pi, 64));        // g <= 1: below a sixth of a turn
+        t.turn[i] = (uint64_t)(g * (18446744073709551616.0 / two_pi) + 0.5);     // g <= 1: below a sixth of a turn
     }
     t.by = (float)by;
     t.rot = (int)rot;

@@ -444,3 +444,25 @@ def test_chunks_then_single_tokens(gpu_lib):
                 e = np.repeat(now.scale["k"][r, now.table[i, :-(-fed[i] // page)]].T, page, 1)[:, :fed[i], None]
                 assert (np.abs(got - want) <= 2.0 ** -4 * np.abs(want) * 1.01 + 2.0 ** -9 * e).all()
     assert dev.word.item() == 0 and dev.status() == 0
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 2]])
+def test_pools_beyond_two_to_the_31(gpu_lib, new):
+    """Pages whose bytes lie more than 2^31 behind a pool's beginning."""
+    import torch
+    b = K.Batch(L(4, 1, 128, 1), new, [130, 60], 128)
+    far = 140000
+    d = K.OnDevice(gpu_lib, b)
+    pool = {n: torch.zeros(far + b.n_pages, 1, 128, 128, dtype=torch.uint8, device="cuda") for n in "kv"}
+    scale = {n: torch.ones(far + b.n_pages, 1, device="cuda") for n in "kv"}
+    for n in "kv":
+        pool[n][far:], scale[n][far:] = d.pool[n][0], d.scale[n][0]
+    d.kv = gpu_lib.PagedKV(d.plan, [pool["k"]], [pool["v"]], [scale["k"]], [scale["v"]], torch.where(d.table >= 0, d.table + far, -1).to(torch.int32))
+    d.attend()
+    assert d.status() == 0
+    K.check(d.got(), b)
+    d.append(R(theta=1e4))
+    for n in "kv":
+        assert (pool[n][:far].view(torch.int64) == 0).all() and (scale[n][:far] == 1).all()
+        d.pool[n], d.scale[n] = [pool[n][far:]], [scale[n][far:]]
+    check_pages(d, b, R(theta=1e4))
