@@ -9,7 +9,11 @@
 // are their Taylor polynomials.
 //
 // A thread has sixteen features (eight pairs) of a token row and keeps their
-// sines and cosines while it goes through heads.
+// sines and cosines while it goes through heads. 16384 tokens of 32 query and 8
+// KV heads of 128: 62 us on the device, 5.4 TB/s (with sines in shared memory
+// for a shard's CTA, made again for every shard, 98; with frequencies from
+// constant memory, which gives a warp's eight one after another, 63, and 49 for
+// 36 in appending).
 #include <climits>
 
 #include "common.cuh"
@@ -197,7 +201,10 @@ __device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t x) {
 // of one page, for a shard: first the largest magnitude of every head's new
 // keys and values, hence the scales; then what the page holds is brought to
 // them where they grew; then the new rows, which are in L1 by then. The
-// queries' rows are CTAs of their own.
+// queries' rows are CTAs of their own. Bound by the chain of a window's loads
+// (offsets, rows and page, scale), some 6 us: 256 single tokens 9.4 us on the
+// device, 24 prompts of 4695 tokens 32, of which their queries alone 14.8. With
+// 256 threads to a window, of which fewer fit on an SM, 36.5.
 //
 // The windows are found without a pass over the batch: sequence b has those
 // from cu[b] / page + 2 b on, of which it needs no more than there are before

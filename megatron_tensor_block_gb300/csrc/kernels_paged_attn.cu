@@ -40,6 +40,12 @@ namespace tpk {
 // relative to the largest so far, into the weights. (e4m3 x e4m3 products of q
 // in two terms, without conversions of K here: decode of 64 68 us where this
 // took 63.)
+//
+// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 342 us
+// on the device, 6.2 TB/s. 64 over 256 to 4095: 55, of which 1.7 pass until every
+// warp has its place and 10 to 12 from the first CTA's last key to the last join.
+// Every warp with copies of its own: 63 us; a copying warp for fifteen others
+// 58.8.
 // ---------------------------------------------------------------------------
 
 constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
