@@ -29,8 +29,8 @@ namespace tpk {
 // A warp works alone: its own ring of stages in shared memory, no barrier with
 // another warp but the one that copies until its run ends. What it has of a
 // head that others have a part of is joined behind that, first in shared
-// memory, then through the workspace by the CTA that comes last. One more warp
-// copies, a lane for each of the others: their page tables, scales, TMA boxes.
+// memory, then through the workspace by the CTA that comes last. One or two more
+// warps copy, a lane for each of the others: page tables, scales, TMA boxes.
 //
 // Keys are the rows of the products, S^T = K Q^T and O^T = V^T P^T (16 x 8
 // query rows), as fp16 x fp16: one conversion makes two fp16 of two e4m3,
@@ -41,11 +41,9 @@ namespace tpk {
 // in two terms, without conversions of K here: decode of 64 68 us where this
 // took 63.)
 //
-// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 342 us
-// on the device, 6.2 TB/s. 64 over 256 to 4095: 55, of which 1.7 pass until every
-// warp has its place and 10 to 12 from the first CTA's last key to the last join.
-// Every warp with copies of its own: 63 us; a copying warp for fifteen others
-// 58.8.
+// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 322 us
+// on the device, 6.6 TB/s. 64 over 256 to 4095: 51, of which 1.7 pass until every
+// warp has its place and 8 to 10 from the first CTA's last key to the last join.
 // ---------------------------------------------------------------------------
 
 constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
@@ -56,24 +54,25 @@ struct PnPiece {                          // of a head of a sequence
     int c0, row0, rows, pos;              // the sequence's first token row, the rows of the head, its first position
 };
 
-// Fifteen warps and the copying one where no sequence has more than 8 rows, else eleven with more registers.
+// Fourteen warps and two that copy where no sequence has more than 8 rows, else eleven with more registers and one.
 template <int D, int W>
 struct PnShape {
-    static constexpr int ROWS = W == 15 ? 8 : 16;
+    static constexpr int ROWS = W == 14 ? 8 : 16;
     static constexpr int TILE = kPnKeys * D;                        // bytes of a chunk's K or V
     static constexpr int STAGES = D == 128 ? 1 : 2;
     static constexpr int SLOT = ROWS * D * 4;                       // O of a piece of a head
     static constexpr int RING = STAGES * 2 * TILE;                  // of a warp
-    static constexpr int THREADS = 32 * (W + 1);
+    static constexpr int COPIES = W == 14 ? 2 : 1;                  // warps that copy: for keys and for values, or half its lanes for either
+    static constexpr int THREADS = 32 * (W + COPIES);
     struct Head {
         uint64_t kfull[W][STAGES], kempty[W][STAGES], vfull[W][STAGES], vempty[W][STAGES];
         float scales[W][STAGES][4];                                 // of K for both halves of the chunk, of V
         float2 ml[2 * W][ROWS];                                     // (m, l) of the pieces
-        int64_t sums[W + 1], firsts[W + 1];
+        int64_t sums[W + COPIES], firsts[W + COPIES];
         int64_t at[W];                                              // a warp's place in its first sequence
         PnPiece pieces[2 * W];                                      // of warp w: one that began before it, one that goes on behind it
         int valid[W][STAGES];                                       // halves whose page is there
-        int seq[W], last[2], first_cta[2], many[W + 1], abort;
+        int seq[W], last[2], first_cta[2], many[W + COPIES], abort;
     };
     static constexpr int HEAD = ((int)sizeof(Head) + 1023) & ~1023;
     static constexpr int SMEM = HEAD + W * (RING + SLOT);
@@ -167,67 +166,62 @@ __device__ __forceinline__ uint32_t pn_unit(int r, int u) {
     return r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
 }
 
-// The copying warp: lane w starts the copies of warp w's chunks as its stages become free.
+// The copies of warp w's chunks, their keys and scales or (V) their values, by one lane, as its stages become free. Each copy is
+// an instruction for each lane, one after another: a warp with the lanes of fifteen others' keys and values was the kernel's
+// limit (128 long contexts 350 us, and 455 in pages of 16; 325 and 364 with a warp for either).
 template <int D, int W>
-__device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int lane, int64_t todo,
+__device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int w, bool V, int64_t todo,
                                           int64_t in_sequence) {
     using Sh = PnShape<D, W>;
     constexpr int S = Sh::STAGES, TILE = Sh::TILE;
-    const int w = min(lane, W - 1), page = 1 << a.bits;
+    const int page = 1 << a.bits;
     PnCursor at = {};
     if (todo > 0) {
         at.b = hd.seq[w];
         at.begin(a, in_sequence);
     }
-    unsigned char* ring = rings + w * Sh::RING;
+    unsigned char* ring = rings + w * Sh::RING + (V ? TILE : 0);
+    uint64_t* full = V ? &hd.vfull[w][0] : &hd.kfull[w][0];
+    uint64_t* empty = V ? &hd.vempty[w][0] : &hd.kempty[w][0];
     uint32_t loads = 0;
-    bool values = false;                                    // next are the values of the chunk whose keys are on the way
-    int id0 = 0, id1 = 0, mask = 0, off = 0, shard = 0, tile0 = 0, tile1 = 0;
     uint64_t since = global_ns();
     const uint64_t once = l2_evict_first_policy();
-    auto copies = [&](const CUtensorMap* m, unsigned char* dst, uint64_t* bar) {
-        if (a.bits == 4) {                                  // pages of 16: a box for each half
-            mbar_arrive_expect_tx(bar, __popc(mask) * (TILE / 2));
-            if (mask & 1) tma_load_3d_hint(dst, m, 0, 0, tile0, bar, once);
-            if (mask & 2) tma_load_3d_hint(dst + TILE / 2, m, 0, 0, tile1, bar, once);
-        } else {
-            mbar_arrive_expect_tx(bar, (mask & 1) * TILE);
-            if (mask & 1) tma_load_3d_hint(dst, m, 0, off, tile0, bar, once);
-        }
-    };
     while (__any_sync(0xffffffffu, todo > 0)) {
         const int s = loads % S;
-        const bool go = todo > 0 && mbar_test(values ? &hd.vempty[w][s] : &hd.kempty[w][s], ((loads / S) & 1) ^ 1);
-        if (go && !values) {
-            const int key = kPnKeys * at.c, kend = at.kend(a);
-            const int head = at.h / at.groups;
-            shard = head / a.hkv_s;
-            const int kv = head - shard * a.hkv_s;
+        const bool go = todo > 0 && mbar_test(empty + s, ((loads / S) & 1) ^ 1);
+        if (go) {
+            const int key = kPnKeys * at.c, kend = at.kend(a), head = at.h / at.groups;
+            const int shard = head / a.hkv_s, kv = head - shard * a.hkv_s;
             const int* row = a.pages + (int64_t)at.b * a.width;
             const bool in0 = key < kend, in1 = key + 16 < kend;
-            id0 = in0 ? __ldg(row + (key >> a.bits)) : -1;
-            id1 = in1 ? (a.bits == 4 ? __ldg(row + (key >> 4) + 1) : id0) : -1;
-            mask = (id0 >= 0 && id0 < a.n_pages) | (id1 >= 0 && id1 < a.n_pages) << 1;
-            if ((in0 && !(mask & 1)) || (in1 && !(mask & 2))) set_status(a.status, TP_ERR_CAPACITY);
-            off = key & (page - 1);
-            tile0 = id0 * a.hkv_s + kv;
-            tile1 = id1 * a.hkv_s + kv;
-            const uint32_t to = smem_u32(&hd.scales[w][s][0]);
-            auto scale = [&](int i, const float* src) {
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * i), "l"(src) : "memory");
-            };
-            if (mask & 1) scale(0, a.ks[shard] + tile0), scale(2, a.vs[shard] + tile0);
-            if (mask & 2) scale(1, a.ks[shard] + tile1), scale(3, a.vs[shard] + tile1);
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&hd.kfull[w][s])) : "memory");
-            hd.valid[w][s] = mask;
-            copies(&a.tk[shard], ring + s * 2 * TILE, &hd.kfull[w][s]);
-        }
-        if (go && values) {
-            copies(&a.tv[shard], ring + s * 2 * TILE + TILE, &hd.vfull[w][s]);
+            const int id0 = in0 ? __ldg(row + (key >> a.bits)) : -1;
+            const int id1 = in1 ? (a.bits == 4 ? __ldg(row + (key >> 4) + 1) : id0) : -1;
+            const int mask = (id0 >= 0 && id0 < a.n_pages) | (id1 >= 0 && id1 < a.n_pages) << 1;
+            const int tile0 = id0 * a.hkv_s + kv, tile1 = id1 * a.hkv_s + kv;
+            if (!V) {
+                if ((in0 && !(mask & 1)) || (in1 && !(mask & 2))) set_status(a.status, TP_ERR_CAPACITY);
+                const uint32_t to = smem_u32(&hd.scales[w][s][0]);
+                auto scale = [&](int i, const float* src) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * i), "l"(src) : "memory");
+                };
+                if (mask & 1) scale(0, a.ks[shard] + tile0), scale(2, a.vs[shard] + tile0);
+                if (mask & 2) scale(1, a.ks[shard] + tile1), scale(3, a.vs[shard] + tile1);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(full + s)) : "memory");
+                hd.valid[w][s] = mask;
+            }
+            const CUtensorMap* m = V ? &a.tv[shard] : &a.tk[shard];
+            unsigned char* dst = ring + s * 2 * TILE;
+            if (a.bits == 4) {                              // pages of 16: a box for each half
+                mbar_arrive_expect_tx(full + s, __popc(mask) * (TILE / 2));
+                if (mask & 1) tma_load_3d_hint(dst, m, 0, 0, tile0, full + s, once);
+                if (mask & 2) tma_load_3d_hint(dst + TILE / 2, m, 0, 0, tile1, full + s, once);
+            } else {
+                mbar_arrive_expect_tx(full + s, (mask & 1) * TILE);
+                if (mask & 1) tma_load_3d_hint(dst, m, 0, key & (page - 1), tile0, full + s, once);
+            }
             ++loads;
             if (--todo > 0) at.next(a);
         }
-        if (go) values = !values;
         if (__any_sync(0xffffffffu, go)) {
             since = global_ns();
         } else {
@@ -241,13 +235,9 @@ __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W
         }
     }
     // no copy may still be landing when the CTA exits
-    if (lane < W && *(volatile int*)&hd.abort) {
+    if (*(volatile int*)&hd.abort) {
         volatile int no_abort = 0;
-        for (uint32_t k = loads > S ? loads - S : 0; k < loads; ++k) {
-            mbar_wait(&hd.kfull[w][k % S], (k / S) & 1, &no_abort, nullptr);
-            mbar_wait(&hd.vfull[w][k % S], (k / S) & 1, &no_abort, nullptr);
-        }
-        if (values) mbar_wait(&hd.kfull[w][loads % S], (loads / S) & 1, &no_abort, nullptr);
+        for (uint32_t k = loads > S ? loads - S : 0; k < loads; ++k) mbar_wait(full + k % S, (k / S) & 1, &no_abort, nullptr);
     }
 }
 
@@ -589,7 +579,7 @@ __device__ __forceinline__ void pn_read(const float* src, int lane, float (&x)[D
 template <int D, int W>
 __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(const __grid_constant__ PnArgs a) {
     using Sh = PnShape<D, W>;
-    constexpr int S = Sh::STAGES, E = D / 32, THREADS = Sh::THREADS, WARPS = W + 1;
+    constexpr int S = Sh::STAGES, E = D / 32, THREADS = Sh::THREADS, WARPS = W + Sh::COPIES;
     extern __shared__ __align__(1024) unsigned char smem[];
     typename Sh::Head& hd = *reinterpret_cast<typename Sh::Head*>(smem);
     unsigned char* rings = smem + Sh::HEAD;
@@ -697,9 +687,12 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     // ---- a warp's run
     constexpr unsigned kAll = 0xffffffffu;
     bool ok = !*(volatile int*)&hd.abort;
-    if (warp == W) {
-        const int64_t end = __shfl_down_sync(kAll, begin, 1), todo = lane < W && ok ? end - begin : 0;
-        pn_copies<D, W>(a, hd, rings, lane, todo, todo ? hd.at[lane] : 0);
+    if (warp >= W) {
+        const int w = lane & 15;
+        const int64_t first = __shfl_sync(kAll, begin, w), end = __shfl_sync(kAll, begin, w + 1);
+        const bool v = Sh::COPIES == 2 ? warp > W : lane >= 16;
+        const int64_t todo = w < W && ok && (Sh::COPIES == 1 || lane < 16) ? end - first : 0;
+        pn_copies<D, W>(a, hd, rings, min(w, W - 1), v, todo, todo ? hd.at[w] : 0);
     } else {
         const int64_t w0 = __shfl_sync(kAll, begin, warp), w1 = __shfl_sync(kAll, begin, warp + 1);
         PnWarp<D, W> x{a, hd, rings + warp * Sh::RING, warp, lane, 0};
@@ -888,11 +881,11 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         a.scale_log2 = p.scale_log2;
         void* args[] = {&a};
         const bool eight = (int64_t)p.max_new * G <= 8;
-        const void* fn = d128 ? (eight ? reinterpret_cast<const void*>(paged_few_kernel<128, 15>) : reinterpret_cast<const void*>(paged_few_kernel<128, 11>))
-                              : (eight ? reinterpret_cast<const void*>(paged_few_kernel<64, 15>) : reinterpret_cast<const void*>(paged_few_kernel<64, 11>));
-        const int smem = d128 ? (eight ? PnShape<128, 15>::SMEM : PnShape<128, 11>::SMEM) : (eight ? PnShape<64, 15>::SMEM : PnShape<64, 11>::SMEM);
+        const void* fn = d128 ? (eight ? reinterpret_cast<const void*>(paged_few_kernel<128, 14>) : reinterpret_cast<const void*>(paged_few_kernel<128, 11>))
+                              : (eight ? reinterpret_cast<const void*>(paged_few_kernel<64, 14>) : reinterpret_cast<const void*>(paged_few_kernel<64, 11>));
+        const int smem = d128 ? (eight ? PnShape<128, 14>::SMEM : PnShape<128, 11>::SMEM) : (eight ? PnShape<64, 14>::SMEM : PnShape<64, 11>::SMEM);
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, eight ? PnShape<64, 15>::THREADS : PnShape<64, 11>::THREADS);
+        if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, eight ? PnShape<64, 14>::THREADS : PnShape<64, 11>::THREADS);
         if (e != cudaSuccess) return e;
     }
     if ((int64_t)p.max_new * G <= kPnMost) return cudaSuccess;

@@ -1063,7 +1063,7 @@ cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStr
     if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess) e = launch_pdl(fn, args, kSMs, smem, s, kPwThreads);
     if (e != cudaSuccess) return e;
-    int slices = 16;
+    int slices = 32;
     void* jargs[] = {&a, &slices};
     return launch_pdl(d128 ? reinterpret_cast<const void*>(paged_join_kernel<128>) : reinterpret_cast<const void*>(paged_join_kernel<64>), jargs,
                       kSMs * slices, 0, s, 128);
