@@ -18,8 +18,8 @@
 namespace tpk {
 
 // ---------------------------------------------------------------------------
-// Sequences of at most 16 query rows per KV head (rows: new tokens x heads of
-// the group): single tokens and a few drafted ones. Bound by the bytes of the
+// Sequences of at most 32 query rows per KV head (rows: new tokens x heads of
+// the group), in groups of 16: single tokens and a few drafted ones. Bound by the bytes of the
 // pages, so the design keeps many of them on the way and gives every SM the
 // same number.
 //
@@ -168,7 +168,7 @@ __device__ __forceinline__ uint32_t pn_unit(int r, int u) {
 
 // The copies of warp w's chunks, their keys and scales or (V) their values, by one lane, as its stages become free. Each copy is
 // an instruction for each lane, one after another: a warp with the lanes of fifteen others' keys and values was the kernel's
-// limit (128 long contexts 350 us, and 455 in pages of 16; 325 and 364 with a warp for either).
+// limit (128 long contexts 350 us, and 455 in pages of 16; 326 and 366 with a warp for either).
 template <int D, int W>
 __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int w, bool V, int64_t todo,
                                           int64_t in_sequence) {
@@ -388,7 +388,7 @@ struct PnWarp {
             release(&hd.kempty[warp][s]);
 
             const int first = kPnKeys * c;
-            const bool whole = first + kPnKeys <= cur.pos + 1 && there == 3;   // every row sees every key
+            const bool whole = first + kPnKeys - 1 <= cur.pos && there == 3;   // every row sees every key
             float top[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
 
     // ---- the CTA's and its warps' place in the list of chunks
     const int heads = a.N * a.hkv_s;
-    int bad = 0, many = 0;
+    int bad = 0, many = 0, off = 0;
     int64_t sum = 0, own = 0;                               // chunks of the thread's sequences, of the first of them
     for (int b = tid; b < a.B; b += THREADS) {
         int c0, n, pos;
@@ -616,10 +616,8 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         sum += x;
         bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
         many |= n > 0 && (int64_t)n * a.G > kPnMost && n <= a.max_new;
-        if (blockIdx.x == 0 && n > 0) {
-            if (n > a.max_new) set_status(a.status, TP_ERR_SHAPE);
-            else if (pos < 0 || (int64_t)pos + n > a.cap) set_status(a.status, TP_ERR_CAPACITY);
-        }
+        if (n > a.max_new) off = TP_ERR_SHAPE;
+        else if (n > 0 && !off && (pos < 0 || (int64_t)pos + n > a.cap)) off = TP_ERR_CAPACITY;
     }
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     int64_t upto_own = own;                                 // ... of those of the warp up to it
@@ -634,6 +632,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         if (tid == 0 && blockIdx.x == 0) set_status(a.status, TP_ERR_SHAPE);
         return;
     }
+    if (blockIdx.x == 0 && off) set_status(a.status, off);
     int64_t total = 0, base = 0, before_own = upto_own - own;
     for (int i = 0; i < WARPS; ++i) {
         total += hd.sums[i];

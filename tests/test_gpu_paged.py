@@ -91,6 +91,7 @@ def test_rope_in_place_and_of_pieces_of_a_fused_row(gpu_lib, name):
 # name -> (layout, rope or None, page, new, cached, other arguments)
 APPENDS = {
     "one_token": (QWEN, R(theta=1e6), 16, [1], [512], {}),
+    "very_many": (L(2, 2, 64, 1), R(), 16, [1, 1, 0, 2] * 320, [(7 * i) % 50 for i in range(1280)], {}),
     "one_token_in_a_page": (QWEN, R(theta=1e6), 16, [1], [519], {}),
     "decode": (LLAMA, WAVES, 64, [1] * 40, [(37 * i) % 200 for i in range(40)], {}),
     "decode_rotated_already": (LLAMA, None, 32, [1] * 9, [0, 1, 31, 32, 33, 63, 64, 5, 100], {}),
@@ -161,10 +162,11 @@ def test_append_outside_the_pages(gpu_lib):
     check_pages(d, b, R())
 
 
+@pytest.mark.parametrize("pos", [5, -7])
 @pytest.mark.parametrize("cu", [[0, 5, 3], [1, 3, 6], [0, 3, 99], [0, -1, 6], [-4, 0, 6]])
-def test_malformed_offsets_write_nothing(gpu_lib, cu):
+def test_malformed_offsets_write_nothing(gpu_lib, cu, pos):
     import torch
-    b = K.Batch(L(2, 2, 64, 1), [3, 3], [5, 16], 16)
+    b = K.Batch(L(2, 2, 64, 1), [3, 3], [pos, 16], 16)
     d = K.OnDevice(gpu_lib, b)
     before = [x.clone() for n in "kv" for x in d.pool[n] + d.scale[n]]
     d.cu.copy_(torch.tensor(cu))
@@ -216,6 +218,9 @@ ATTENDS = {
     "many_beside_a_prompt": (L(8, 8, 64, 1), 16, [1] * 40 + [70], [600] * 40 + [10], {}, 0),
     "groups_of_rows": (L(8, 1, 64, 1), 16, [3, 4, 1, 2], [100, 31, 70, 256], {}, 4),
     "groups_of_rows_128": (L(6, 2, 128, 2), 32, [10, 3, 6, 1], [100, 31, 700, 256], {}, 10),
+    # more sequences than a CTA has threads
+    "very_many": (L(2, 2, 64, 1), 16, [1, 1, 0, 2] * 320, [(7 * i) % 50 for i in range(1280)], {}, 0),
+    "very_many_prompts": (L(2, 2, 64, 1), 16, [33, 1, 40, 0] * 150, [(7 * i) % 50 for i in range(600)], {}, 0),
     "rows_behind": (QWEN, 16, [3, 60], [10, 0], dict(extra_rows=77), 0),
     "rows_behind_decode": (QWEN, 16, [1, 1], [10, 0], dict(extra_rows=5), 1),
     "all_empty": (QWEN, 16, [0, 0], [3, 0], dict(extra_rows=9), 0),
