@@ -652,8 +652,8 @@ typedef struct tp_paged_kv {
  * rounding between; values that are not finite are stored as NaN. Slots of the
  * page that no token of the call falls into keep their values, but where slot 0
  * is among the new ones: what those behind them hold means nothing then.
- * Every page that receives tokens belongs to one sequence (a page that several
- * sequences write has undefined contents). Rows at positions outside
+ * Every page that receives tokens belongs to one place of one sequence (a page
+ * that several places write has undefined contents). Rows at positions outside
  * 0..width*page-1 or in a page whose id is outside 0..n_pages-1 append nothing
  * and record TP_ERR_CAPACITY in *device_status (nullable, DEVICE int32, kept
  * unless it is 0); a malformed cu records TP_ERR_SHAPE, and nothing is
