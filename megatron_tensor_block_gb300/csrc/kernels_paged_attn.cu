@@ -234,11 +234,9 @@ __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W
             __nanosleep(32);
         }
     }
-    // no copy may still be landing when the CTA exits
-    if (*(volatile int*)&hd.abort) {
-        volatile int no_abort = 0;
-        for (uint32_t k = loads > S ? loads - S : 0; k < loads; ++k) mbar_wait(full + k % S, (k / S) & 1, &no_abort, nullptr);
-    }
+    // no copy may still be landing when the CTA exits, be it that another warp's wait runs out behind the last copy here
+    volatile int no_abort = 0;
+    for (uint32_t k = loads > S ? loads - S : 0; k < loads; ++k) mbar_wait(full + k % S, (k / S) & 1, &no_abort, nullptr);
 }
 
 template <int D, int W>
