@@ -334,21 +334,22 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPwRegsIo));
         if (warp == 0) {
             // ---------------------------------------------------------------- loads
-            uint32_t it = 0, n = 0, nq[2] = {0, 0};         // blocks, entries, Q tiles
+            uint32_t it = 0, iv = 0, n = 0, nq[2] = {0, 0}; // blocks of K and V, entries, Q tiles
             const int page = 1 << a.bits, step = page / 16, box = page * D;
             bool ok = !*abort_flag;
             PwItem w;
             for (int k = 0; ok && item(k, w); ++k, n = next_four(n)) {
-                for (int j = 0; j < w.nb; ++j, ++it, ++n) {
+                for (int j = 0; j < w.nb; ++j, ++n) {
                     if ((j & 3) == 0 && !(ok = info_wait(n))) break;
                     const int tile = hd.info[n % kPwInfos].tile[lane & 7];
                     const bool is = lane < 8 && lane % step == 0 && tile >= 0;
                     const uint32_t bytes = __popc(__ballot_sync(kAll, is)) * box;
-                    const int s = it % RK, v = it % RR;
+                    const int s = it % RK, v = iv % RR;
                     if (!(ok = wait_all(&hd.k_empty[s], ((it / RK) & 1) ^ 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&hd.k_full[s], bytes);
                     __syncwarp();
                     if (is) tma_load_3d_keep(sk + s * Sh::KB + lane * 16 * D, &a.tk[w.r], 0, 0, tile, &hd.k_full[s]);
+                    ++it;
                     if (j == 0) {
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
@@ -363,18 +364,13 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                             }
                             __syncwarp();
                         }
-                        if (!ok) {
-                            ++it;                           // (its keys are on the way)
-                            break;
-                        }
+                        if (!ok) break;
                     }
-                    if (!(ok = wait_all(&hd.r_empty[v], ((it / RR) & 1) ^ 1))) {
-                        ++it;                               // (its keys are on the way)
-                        break;
-                    }
+                    if (!(ok = wait_all(&hd.r_empty[v], ((iv / RR) & 1) ^ 1))) break;
                     if (lane == 0) mbar_arrive_expect_tx(&hd.r_full[v], bytes);
                     __syncwarp();
                     if (is) bulk_copy(sr + v * Sh::KB + lane * 16 * D, a.v[w.r] + (int64_t)tile * box, box, &hd.r_full[v]);
+                    ++iv;
                     if ((j & 3) == 3 || j == w.nb - 1) info_done(n);
                 }
             }
@@ -383,8 +379,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 for (int t = 0; t < 2; ++t)
                     if (nq[t]) mbar_wait(&hd.q_full[t], (nq[t] - 1) & 1, &no_abort, nullptr);
                 for (uint32_t i = it > RK ? it - RK : 0; i < it; ++i) mbar_wait(&hd.k_full[i % RK], (i / RK) & 1, &no_abort, nullptr);
-                for (uint32_t i = it > RR ? it - RR : 0; i < it; ++i)
-                    if (ok || i + 1 < it) mbar_wait(&hd.r_full[i % RR], (i / RR) & 1, &no_abort, nullptr);
+                for (uint32_t i = iv > RR ? iv - RR : 0; i < iv; ++i) mbar_wait(&hd.r_full[i % RR], (i / RR) & 1, &no_abort, nullptr);
             }
         } else if (warp < 3) {
             // ---------------------------------------------------------------- products
