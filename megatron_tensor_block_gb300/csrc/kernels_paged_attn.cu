@@ -41,8 +41,8 @@ namespace tpk {
 // in two terms, without conversions of K here: decode of 64 68 us where this
 // took 63.)
 //
-// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 322 us
-// on the device, 6.6 TB/s. 64 over 256 to 4095: 51, of which 1.7 pass until every
+// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 326 us
+// on the device, 6.5 TB/s. 64 over 256 to 4095: 51 to 53, of which 1.7 pass until every
 // warp has its place and 8 to 10 from the first CTA's last key to the last join.
 // ---------------------------------------------------------------------------
 
