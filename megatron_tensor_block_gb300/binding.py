@@ -484,12 +484,14 @@ def tp_rope_packed(plan: Plan, rope: tp_rope, cu, pos, B: int, T: int, q=None, q
 class PagedKV:
     """8-bit paged caches: per shard ``k`` and ``v`` ``[n_pages, Hkv', page, d]`` of ``torch.float8_e4m3fn`` (or its bytes as
     uint8), ``k_scale`` and ``v_scale`` float32 ``[n_pages, Hkv']``, and the page table ``pages`` int32 ``[B, width]``. Checked
-    here once; keeps the tensors alive. ``at`` makes the same caches with another table."""
+    here once; keeps the tensors alive. Serves every plan of as many shards, KV heads per shard and features per head.
+    ``at`` makes the same caches with another table."""
 
     def __init__(self, plan: Plan, k: list, v: list, k_scale: list, v_scale: list, pages):
         import torch
         dev = _Torch.device()
         self.tensors, self.device = (list(k), list(v), list(k_scale), list(v_scale)), dev
+        self.heads = (plan.tp, plan.hkv_shard, plan.head_dim)
         shape = tuple(k[0].shape) if k else ()
         if len(shape) != 4 or shape[1] != plan.hkv_shard or shape[3] != plan.head_dim:
             raise ValueError(f"k: {shape}, expected (n_pages, {plan.hkv_shard}, page, {plan.head_dim})")
@@ -523,9 +525,12 @@ class PagedKV:
         return new
 
 
-def _paged(kv, B: int, device: int):
+def _paged(plan: Plan, kv, B: int, device: int):
     if isinstance(kv, tp_paged_kv) or kv is None:
         return _ref(kv)
+    want = (plan.tp, plan.hkv_shard, plan.head_dim)
+    if kv.heads != want:
+        raise ValueError(f"kv: caches of (shards, KV heads per shard, head_dim) = {kv.heads}, expected the plan's {want}")
     if kv.sequences < B:
         raise ValueError(f"pages: {kv.sequences} sequences, expected at least {B}")
     if kv.device != device:
@@ -540,7 +545,7 @@ def tp_kv_append_paged(plan: Plan, rope, k, v, kv, cu, pos, B: int, T: int, q=No
     dev, bf16, hq, hkv = _Torch.device(), _Torch.bf16, plan.n_heads // plan.tp, plan.hkv_shard
     _check(load().tp_kv_append_paged(plan.handle, _ref(rope), _ref(_rows(plan, q, "q", hq, T, bf16, dev)),
                                      _ref(_rows(plan, k, "k", hkv, T, bf16, dev)), _ref(_rows(plan, v, "v", hkv, T, bf16, dev)),
-                                     _paged(kv, B, dev), _checked(cu, "cu", _Torch.i32, B + 1, dev),
+                                     _paged(plan, kv, B, dev), _checked(cu, "cu", _Torch.i32, B + 1, dev),
                                      _checked(pos, "pos", _Torch.i32, B, dev), B, T,
                                      _checked(q_out, "q_out", bf16, plan.tp * T * hq * plan.head_dim, dev),
                                      _checked(device_status, "device_status", _Torch.i32, 1, dev), _Torch.stream(stream, dev)))
@@ -562,7 +567,7 @@ def tp_attn_paged(plan: Plan, q, kv, cu, pos, B: int, T: int, out, workspace, nb
     """``tp_attn_packed`` over the 8-bit pages of ``kv`` (a :class:`PagedKV`); ``max_new``: no sequence has more new tokens than
     this (0: not known). ``workspace`` is one of ``tp_paged_workspace_bytes``, set up by ``tp_paged_workspace_init``."""
     n, dev = T * plan.n_heads * plan.head_dim, _Torch.device()
-    _check(load().tp_attn_paged(plan.handle, _checked(q, "q", _Torch.bf16, n, dev), _paged(kv, B, dev),
+    _check(load().tp_attn_paged(plan.handle, _checked(q, "q", _Torch.bf16, n, dev), _paged(plan, kv, B, dev),
                                 _checked(cu, "cu", _Torch.i32, B + 1, dev), _checked(pos, "pos", _Torch.i32, B, dev), B, T, max_new,
                                 _checked(out, "out", _Torch.bf16, n, dev), _checked(workspace, "workspace", _Torch.u8, nbytes, dev),
                                 nbytes, _Torch.stream(stream, dev)))
