@@ -18,6 +18,7 @@
 
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "paged.cuh"
 #include "tp_internal.h"
 
 namespace tpk {
@@ -27,10 +28,7 @@ constexpr int kPgThreads = 256, kPgAppend = 128;
 // Whether cu is not 0 = cu[0] <= cu[1] <= ... <= T (the whole block asks).
 __device__ __forceinline__ bool cu_malformed(const int* cu, int B, int T) {
     int bad = 0;
-    for (int i = threadIdx.x; i < B; i += blockDim.x) {
-        const int a = cu[i], b = cu[i + 1];
-        bad |= b < a || a < 0 || b > T || (i == 0 && a != 0);
-    }
+    for (int i = threadIdx.x; i < B; i += blockDim.x) bad |= cu_bad(cu, i, T);
     return __syncthreads_or(bad);
 }
 

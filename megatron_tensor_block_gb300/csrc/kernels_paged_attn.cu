@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         if (x) x *= paged_groups(n, a.G);
         if (b == tid) own = x;
         sum += x;
-        bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
+        bad |= cu_bad(a.cu, b, a.T);
         many |= n > 0 && (int64_t)n * a.G > kPnMost && n <= a.max_new;
         if (n > a.max_new) off = TP_ERR_SHAPE;
         else if (n > 0 && !off && (pos < 0 || (int64_t)pos + n > a.cap)) off = TP_ERR_CAPACITY;

@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         sum[0] += few ? 0 : x;
         sum[1] += few ? x : 0;
         if (few && x) sum[2] += paged_few_chunks(n, pos, a.G, a.cap) * heads;
-        bad |= n < 0 || c0 < 0 || c0 + n > a.T || (b == 0 && c0 != 0);
+        bad |= cu_bad(a.cu, b, a.T);
     }
 #pragma unroll
     for (int i = 0; i < 3; ++i) {

@@ -1,10 +1,17 @@
-// What the two kernels of the attention over pages agree on: which of them has
-// a batch's sequences of few query rows.
+// What the kernels around pages share: the check of a batch's offsets; which of
+// the attention's two has a batch's sequences of few query rows.
 #pragma once
 
 #include "common.cuh"
 
 namespace tpk {
+
+// Whether the offsets of sequence b are not 0 = cu[0] <= cu[1] <= ... <= T. (Their difference is good behind this only: it can
+// wrap around.)
+__device__ __forceinline__ bool cu_bad(const int* cu, int b, int T) {
+    const int from = cu[b], to = cu[b + 1];
+    return to < from || from < 0 || to > T || (b == 0 && from != 0);
+}
 
 constexpr int kPnKeys = 32;               // keys of a chunk
 constexpr int kPnRows = 16;               // query rows that a warp works on
