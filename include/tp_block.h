@@ -591,7 +591,7 @@ typedef struct tp_rope {
     double factor;            /* of the scalings, at least 1 */
     double low, high;         /* WAVELENGTH and RAMP: turns over `original` positions, 0 < low < high */
     int64_t original;         /* ... which is the length trained on */
-    double attn_factor;       /* m; 0: 1, or for RAMP 0.1 ln(factor) + 1 */
+    double attn_factor;       /* m, at most 1e6; 0: 1, or for RAMP 0.1 ln(factor) + 1 */
 } tp_rope;
 
 /* Token rows of every shard: row t of shard r begins shard_stride r +
@@ -643,10 +643,12 @@ typedef struct tp_paged_kv {
  * of sequence b goes to position p = pos[b] + t - cu[b].
  * The scale of every page and head that receives tokens becomes
  *   s = max(s_before, 2^e),  or 2^e where slot 0 is among the new ones,
- * with e the least integer from -60 on with c max|x| <= 448 2^e over the finite
+ * with e the least integer of -60..127 with c max|x| <= 448 2^e over the finite
  * new values x of the page and head (for keys those before the rotation, with
  * c = sqrt(2) max(1, m), or 1 without rope; for values c = 1): no rounding of a
- * sine decides a scale. Values that the page holds already are brought to a
+ * sine decides a scale. (Where none is large enough, which takes m above 158 and
+ * keys near bf16's largest, e is 127 and what lies beyond 448 2^127 is stored as
+ * that.) Values that the page holds already are brought to a
  * larger s, which rounds them again only below 2^-6 s. Stored is x / s rounded
  * to the nearest e4m3, ties to even, from the float32 rotation without a
  * rounding between; values that are not finite are stored as NaN. Slots of the

@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(kPgAppend, 6) append_kernel(const __grid_const
         const double x = (double)__uint_as_float(s_max[g] << 16) * (g < hkv ? p.k_growth : 1.0) / 448.0;
         // the least power of two not below x: x's exponent, and one more unless x is a power itself
         const long long word = __double_as_longlong(x);
-        const int e = max(-60, (int)(word >> 52) - 1023 + ((word & 0xFFFFFFFFFFFFFll) != 0));
+        // (127 at most, which is float32's end: only factors of the rotation above 158 ask for more)
+        const int e = min(127, max(-60, (int)(word >> 52) - 1023 + ((word & 0xFFFFFFFFFFFFFll) != 0)));
         float s = __uint_as_float((uint32_t)(127 + e) << 23), ratio = 1.f;
         if (slot0) {
             const float before = g == tid ? held : *scale;
