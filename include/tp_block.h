@@ -691,7 +691,8 @@ tp_status tp_paged_workspace_init(tp_plan_t plan, void* workspace, size_t bytes,
  * outside 0..n_pages-1 are not seen and recorded likewise; a row that sees no
  * key is zeros. Rows cu[B]..T-1 of out are left as they are; a malformed cu
  * records TP_ERR_SHAPE, and out is left as it is. NaN among the values that a
- * row sees (and infinities of q) go the way of the formula; what it does not
+ * row sees (and infinities of q) go the way of the formula (a row whose scores
+ * are all -inf, be it that they lie beyond float32, is NaN); what it does not
  * see never reaches it. Scores, sums and outputs accumulate in float32; the
  * softmax's weights are rounded to fp16 for the product with the values, out
  * once from float32. Deterministic. Every wait on the device is bounded; one

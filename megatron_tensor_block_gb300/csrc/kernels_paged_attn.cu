@@ -3,6 +3,7 @@
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
 //
 // in one pass over the keys with a running m and sum.
+#include <cfloat>
 #include <cstring>
 #include <mutex>
 
@@ -305,6 +306,16 @@ struct PnWarp {
         __syncwarp();
     }
 
+    // Whether there is a key up to lim in chunks w.x0 .. w.x1 - 1 (asked for rows without weights only).
+    __device__ __forceinline__ bool sees(const PnCursor& cur, const PnPiece& w, int lim) const {
+        const int end = (int)min((int64_t)lim + 1, (int64_t)kPnKeys * w.x1);
+        for (int key = kPnKeys * w.x0; key < end; key += 16) {
+            const int id = __ldg(a.pages + (int64_t)cur.b * a.width + (key >> a.bits));
+            if (id >= 0 && id < a.n_pages) return true;
+        }
+        return false;
+    }
+
     // Chunks w.x0 .. w.x1 - 1 of a head of the sequence at cur. Where that is all of them the result goes to out, else to
     // slot (O [rows][D]) and (m, l) beside it.
     template <int NT>
@@ -484,11 +495,11 @@ struct PnWarp {
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
                 const int row = 8 * nt + 2 * t + i;
                 if (row >= w.rows) continue;
+                const int of = w.row0 + row, tok = of / a.G;
+                const int64_t p = (int64_t)cur.pos + tok;
+                const bool none = p < 0 || p >= a.cap || (x == 0.f && !sees(cur, w, (int)p));      // no such place, no key seen: zeros
                 if (all) {
-                    const int of = w.row0 + row, tok = of / a.G;
-                    const int64_t p = (int64_t)cur.pos + tok;
-                    const bool none = x == 0.f || p < 0 || p >= a.cap;      // no key seen, no such place: zeros
-                    const float f = ref / x;
+                    const float f = ref / x;                        // (scores all -inf: 0 / 0)
                     bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + 2 * g;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
@@ -498,7 +509,8 @@ struct PnWarp {
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i] * ref, o[nt][mt][2 + i] * ref);
-                    if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(m[nt][i], x);
+                    // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
+                    if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(none ? -INFINITY : fmaxf(m[nt][i], -FLT_MAX), x);
                 }
             }
         return true;
@@ -508,7 +520,7 @@ struct PnWarp {
 // One warp: a row's n pieces joined, o = sum_i 2^(m_i - m) O_i and (m, l)
 // likewise, always in the same order. stat(i): (m, l) of piece i, read by lane
 // i; get(i, x): the lane's D / 32 elements of its O. No piece is left out, so
-// that a NaN of one stays.
+// that a NaN of one stays. m is -inf where no piece has seen a key.
 template <int D, typename Stat, typename Get>
 __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, float (&o)[D / 32]) {
     constexpr unsigned kAll = 0xffffffffu;
@@ -549,12 +561,12 @@ __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, f
 }
 
 template <int D>
-__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float l, const float (&o)[D / 32]) {
+__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float2 ml, const float (&o)[D / 32]) {
     const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, of = p.row0 + row, tok = of / a.G;
     const int64_t at = (int64_t)p.pos + tok;
-    const bool none = l == 0.f || at < 0 || at >= a.cap;
+    const bool none = ml.x == -INFINITY || at < 0 || at >= a.cap;
     bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + lane * (D / 32);
-    const float f = 1.f / l;
+    const float f = 1.f / ml.y;
     uint32_t y[D / 64];
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
@@ -756,7 +768,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
             __popc(pieces), lane, [&](int j) { return hd.ml[at(j)][row]; },
             [&](int j, float (&x)[E]) { pn_read<D>(slot_of(at(j)) + row * D, lane, x, false); }, o);
         if (p.x0 == 0 && p.x1 == p.nch) {
-            pn_store<D>(a, p, row, lane, r.y, o);
+            pn_store<D>(a, p, row, lane, r, o);
         } else {
             const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * Sh::ROWS + row;
             if (lane == 0) a.part_ml[dst] = r;
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
             const float2 r = pn_join<D>(
                 n, lane, [&](int i) { return __ldcg(a.part_ml + src(i) + row); },
                 [&](int i, float (&x)[E]) { pn_read<D>(a.part_o + (src(i) + row) * D, lane, x, true); }, o);
-            pn_store<D>(a, p, row, lane, r.y, o);
+            pn_store<D>(a, p, row, lane, r, o);
         }
     }
 }

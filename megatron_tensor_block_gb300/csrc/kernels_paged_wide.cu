@@ -37,6 +37,7 @@
 // issue the products of a tile each, 3 walks the items and reads the page table
 // and scales ahead, 4-11 softmax (four a tile), 12-15 widen values and write
 // results.
+#include <cfloat>
 #include <cstring>
 
 #include <cuda.h>
@@ -601,6 +602,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             const int64_t warp_max = (int64_t)w.qpos + (32 * qd) / a.G + t * a.tpt;            // ... its warp's first row
             const int whole_to = (int)min(warp_max, (int64_t)w.kend - 1);
             float m_use = -INFINITY, l_run = 0.f;
+            bool seen = false;                              // the row has seen a key
             const float factor = tok0 < a.tpt && tok < w.ntok ? __ldg(a.q_rows + ((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + m - tok0 * a.G) : 0.f;
             for (int j = 0; j < n; ++j, ++sp) {
                 if ((j & 3) == 0 && !(ok = info_wait_in(in + j))) break;
@@ -621,6 +623,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     // a step of m for the largest: scores so large that this counts are rounded before.)
                     const bool whole = key0 + kPwK - 1 <= whole_to && mask == 0xFF && !large;
                     const int hi = own_max - key0;          // last key of the block the row sees
+                    seen |= whole || (hi >= 0 && (mask & ((2 << (min(hi, kPwK - 1) >> 4)) - 1)) != 0);
                     uint32_t v[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
@@ -708,7 +711,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             in = next_four(in + w.nb);
             if (!n) continue;
             if (!(ok = wait_in(&hd.st_empty[t], (ip & 1) ^ 1))) break;
-            hd.stat[t][m] = make_float2(m_use, l_run);
+            // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
+            hd.stat[t][m] = make_float2(seen ? fmaxf(m_use, -FLT_MAX) : -INFINITY, l_run);
             ++ip;
             __syncwarp();
             if (lane == 0) mbar_arrive(&hd.st_full[t]);
@@ -799,7 +803,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 // (the item's last product, of the tile with most blocks, follows what all four warps have found)
                 poison |= *reinterpret_cast<volatile int*>(&hd.queue[k % kPwQueue].poison);
                 const float ref = t ? ref1 : ref0;
-                const bool zero = !n || (!part && (ml.y == 0.f || pos < 0 || pos >= a.cap));
+                const bool zero = !n || (!part && (ml.x == -INFINITY || pos < 0 || pos >= a.cap));
                 const float f = zero ? 0.f : part ? ref : ref / ml.y;
                 if (part && live) a.part_ml[prow + t * kPwM + m] = ml;
                 const unsigned store = __ballot_sync(kAll, live) >> (lane & 28);
@@ -946,7 +950,7 @@ __global__ void __launch_bounds__(256) paged_terms_kernel(const __grid_constant_
 }
 
 // Rows of the items that were cut, a warp each: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts
-// in their order. No part is left out, so that a NaN of one stays.
+// in their order. No part is left out, so that a NaN of one stays. m is -inf where no part has seen a key.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PwArgs a, int slices) {
     constexpr int E = D / 32, AHEAD = 4;             // elements per lane, parts loaded together
@@ -989,7 +993,7 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
             }
         }
         const int64_t pos = (int64_t)c.qpos + tok;
-        const bool none = l == 0.f || pos < 0 || pos >= a.cap;
+        const bool none = top == -INFINITY || pos < 0 || pos >= a.cap;
         const float inv = 1.f / l;
         uint32_t y[E / 2];
 #pragma unroll
