@@ -90,7 +90,7 @@ struct PnArgs {
     const int* cu;
     const int* pos;
     const int* pages;
-    float* part_o;                        // [kSMs][2][rows][D]
+    float* part_o;                        // [kSMs][2][rows][D], as the pieces in shared memory
     float2* part_ml;                      // [kSMs][2][rows]
     unsigned* joined;                     // [kSMs] pieces of the head that begins in this CTA and ends in another
     int* status;
@@ -317,7 +317,7 @@ struct PnWarp {
     }
 
     // Chunks w.x0 .. w.x1 - 1 of a head of the sequence at cur. Where that is all of them the result goes to out, else to
-    // slot (O [rows][D]) and (m, l) beside it.
+    // slot (O / l [rows][D], times kPagedPart) and (m, l) beside it.
     template <int NT>
     __device__ __forceinline__ bool head(const PnCursor& cur, const PnPiece& w, float* slot) {
         const int g = lane >> 2, t = lane & 3, kend = cur.kend(a);
@@ -506,9 +506,11 @@ struct PnWarp {
                         *reinterpret_cast<uint32_t*>(dst + 16 * mt) =
                             none ? 0u : pack_bf16x2(o[nt][mt][i] * f, o[nt][mt][2 + i] * f);
                 } else {
+                    const float f = x == 0.f ? 0.f : ref / x;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
-                        *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i] * ref, o[nt][mt][2 + i] * ref);
+                        *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) =
+                            make_float2(o[nt][mt][i] * f * kPagedPart, o[nt][mt][2 + i] * f * kPagedPart);
                     // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
                     if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(none ? -INFINITY : fmaxf(m[nt][i], -FLT_MAX), x);
                 }
@@ -517,10 +519,11 @@ struct PnWarp {
     }
 };
 
-// One warp: a row's n pieces joined, o = sum_i 2^(m_i - m) O_i and (m, l)
-// likewise, always in the same order. stat(i): (m, l) of piece i, read by lane
-// i; get(i, x): the lane's D / 32 elements of its O. No piece is left out, so
-// that a NaN of one stays. m is -inf where no piece has seen a key.
+// One warp: a row's n pieces joined, l = sum_i 2^(m_i - m) l_i and the mean
+// o = sum_i 2^(m_i - m) l_i / l o_i, which is as large as its pieces at most,
+// always in the same order. stat(i): (m, l) of piece i, read by lane i; get(i, x):
+// the lane's D / 32 elements of its o. No piece is left out, so that a NaN of one
+// stays. m is -inf where no piece has seen a key.
 template <int D, typename Stat, typename Get>
 __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, float (&o)[D / 32]) {
     constexpr unsigned kAll = 0xffffffffu;
@@ -540,11 +543,13 @@ __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, f
         float2 ml = make_float2(-INFINITY, 0.f);
         if (i0 + lane < n) ml = stat(i0 + lane);
         const float top = fmaxf(m, warp_max(ml.x)), down = m == -INFINITY ? 0.f : ex2_approx(m - top);
-        const float w = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-        l = l * down + warp_sum(w * ml.y);
+        float w = (ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top)) * ml.y;
+        const float sum = l * down + warp_sum(w), inv = sum == 0.f ? 0.f : 1.f / sum, keep = l * down * inv;
+        w *= inv;
+        l = sum;
         m = top;
 #pragma unroll
-        for (int k = 0; k < E; ++k) o[k] *= down;
+        for (int k = 0; k < E; ++k) o[k] *= keep;
 #pragma unroll 1
         for (int i = i0; i < min(i0 + 32, n); i += AHEAD) {
 #pragma unroll
@@ -566,7 +571,7 @@ __device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int 
     const int64_t at = (int64_t)p.pos + tok;
     const bool none = ml.x == -INFINITY || at < 0 || at >= a.cap;
     bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + lane * (D / 32);
-    const float f = 1.f / ml.y;
+    const float f = ml.y == 0.f ? NAN : 1.f / kPagedPart;
     uint32_t y[D / 64];
 #pragma unroll
     for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);

@@ -112,7 +112,7 @@ struct PwArgs {
     const int* cu;
     const int* pos;
     const int* pages;
-    float* part_o;                        // [kSMs][2][256][D]
+    float* part_o;                        // [kSMs][2][256][D] O / l, times kPagedPart
     float2* part_ml;                      // [kSMs][2][256]
     PagedCut* cuts;                       // [kSMs]
     int* status;
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 poison |= *reinterpret_cast<volatile int*>(&hd.queue[k % kPwQueue].poison);
                 const float ref = t ? ref1 : ref0;
                 const bool zero = !n || (!part && (ml.x == -INFINITY || pos < 0 || pos >= a.cap));
-                const float f = zero ? 0.f : part ? ref : ref / ml.y;
+                const float f = zero || (part && ml.y == 0.f) ? 0.f : ref / ml.y * (part ? kPagedPart : 1.f);
                 if (part && live) a.part_ml[prow + t * kPwM + m] = ml;
                 const unsigned store = __ballot_sync(kAll, live) >> (lane & 28);
                 const unsigned zeros = __ballot_sync(kAll, zero) >> (lane & 28);
@@ -949,8 +949,8 @@ __global__ void __launch_bounds__(256) paged_terms_kernel(const __grid_constant_
     if (i % LANES == 0) a.q_rows[i / LANES] = e == 255 ? 1.f : 1.f / by;
 }
 
-// Rows of the items that were cut, a warp each: m = max m_i, o = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the parts
-// in their order. No part is left out, so that a NaN of one stays. m is -inf where no part has seen a key.
+// Rows of the items that were cut, a warp each: m = max m_i, l = sum_i 2^(m_i - m) l_i and the mean o = sum_i 2^(m_i - m) l_i / l o_i
+// over the parts in their order, which is as large as its parts at most. No part is left out, so that a NaN of one stays. m is -inf where no part has seen a key.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PwArgs a, int slices) {
     constexpr int E = D / 32, AHEAD = 4;             // elements per lane, parts loaded together
@@ -985,16 +985,18 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
             for (int i = 0; i < AHEAD; ++i) {
                 if (i0 + i >= c.parts) break;
                 const float m2 = fmaxf(top, ml[i].x);
-                const float f = top == -INFINITY ? 0.f : ex2_approx(top - m2), w = ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - m2);
+                const float f = l * (top == -INFINITY ? 0.f : ex2_approx(top - m2));
+                const float w = ml[i].y * (ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - m2));
                 top = m2;
-                l = l * f + ml[i].y * w;
+                l = f + w;
+                const float inv = l == 0.f ? 0.f : 1.f / l, keep = f * inv, add = w * inv;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * f + x[i][e] * w;
+                for (int e = 0; e < E; ++e) o[e] = o[e] * keep + x[i][e] * add;
             }
         }
         const int64_t pos = (int64_t)c.qpos + tok;
         const bool none = top == -INFINITY || pos < 0 || pos >= a.cap;
-        const float inv = 1.f / l;
+        const float inv = l == 0.f ? NAN : 1.f / kPagedPart;
         uint32_t y[E / 2];
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) y[e] = none ? 0u : pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);

@@ -21,6 +21,9 @@ constexpr int kPnMost = 32;               // ... of a sequence and KV head that 
 // the prompt and apart: 8 tokens (2048 chunks) 33.3 and 41.4 us, 16 (4096) 38.4 and 44.1, 32 (8192) 56.9 and 50.2, 64 89.5
 // and 63.8.
 constexpr int64_t kPagedFewBeside = 5000;
+// Parts of a row are kept divided by their own sums of weights and times this, so that they are finite whatever the values
+// are (448 times a scale below 2^128 at most): a row in parts is finite where one in one piece is.
+constexpr float kPagedPart = 0x1p-9f;
 
 // A head's query rows are worked on sixteen at a time.
 __device__ __forceinline__ int paged_groups(int n, int G) { return (n * G + kPnRows - 1) / kPnRows; }
