@@ -693,9 +693,14 @@ tp_status tp_paged_workspace_init(tp_plan_t plan, void* workspace, size_t bytes,
  * records TP_ERR_SHAPE, and out is left as it is. NaN among the values that a
  * row sees (and infinities of q) go the way of the formula (a row whose scores
  * are all -inf, be it that they lie beyond float32, is NaN); what it does not
- * see never reaches it. Scores, sums and outputs accumulate in float32; the
- * softmax's weights are rounded to fp16 for the product with the values, out
- * once from float32. Deterministic. Every wait on the device is bounded; one
+ * see never reaches it, scales of values among it. Scores, sums and outputs
+ * accumulate in float32. For the product with the stored values the softmax's
+ * weights, times the scales of the values' pages, are rounded to fp16, relative to
+ * the row's largest such product: by 2^-11 of themselves, and those below 2^-14 of
+ * the largest by 2^-25 of it. Queries of sequences with more than 32 rows per KV
+ * head (or beside such) are held in two e4m3 terms: elements below 2^-10 of a
+ * row's largest are off by 2^-18 of it. out is rounded once from float32.
+ * Deterministic. Every wait on the device is bounded; one
  * that runs out records TP_ERR_TIMEOUT, and out is then undefined. No
  * allocation, no synchronisation: the call may be captured; calls on one
  * workspace must not overlap on the GPU.

@@ -22,6 +22,12 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
     return r;
 }
 
+// log2 of a positive normal number, to 2^-22 beside its exponent.
+__device__ __forceinline__ float log2_of(float x) {
+    const int bits = __float_as_int(x);
+    return (float)((bits >> 23) - 127) + __log2f(__int_as_float((bits & 0x007FFFFF) | 0x3F800000));
+}
+
 // Two float32 values as e4m3, to nearest even, beyond 448 as 448 (infinities too).
 __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {
     uint16_t r;

@@ -37,8 +37,8 @@ namespace tpk {
 // query rows), as fp16 x fp16: one conversion makes two fp16 of two e4m3,
 // exactly; q is brought to fp16 by a power of two for each row, exactly but for
 // elements below 2^-29 of the row's largest; the weights' rounding to fp16 is
-// 2^-11. The scale of a page's keys goes into the scores, that of its values,
-// relative to the largest so far, into the weights. (e4m3 x e4m3 products of q
+// 2^-11. The scale of a page's keys goes into the scores, that of its values into
+// the weights, relative to the row's largest weight times scale. (e4m3 x e4m3 products of q
 // in two terms, without conversions of K here: decode of 64 68 us where this
 // took 63.)
 //
@@ -47,7 +47,7 @@ namespace tpk {
 // warp has its place and 8 to 10 from the first CTA's last key to the last join.
 // ---------------------------------------------------------------------------
 
-constexpr float kPnRescale = 8.f;         // m follows the maximum where that has grown by more than this
+constexpr float kPnRescale = 8.f;         // m and m + u follow their maxima where these have grown by more than this
 
 struct PnPiece {                          // of a head of a sequence
     int64_t start;                        // the head's first chunk in the batch's list
@@ -356,9 +356,11 @@ struct PnWarp {
                 lim[nt][i2] = mine < w.rows && p >= 0 && p < a.cap ? (int)p : -1;
             }
         }
-        float o[NT][D / 16][4] = {}, m[NT][2], l[NT][2], ref = 0.f;
+        float o[NT][D / 16][4] = {}, m[NT][2], u[NT][2], l[NT][2];  // o holds O 2^-(m + u), l the sum of weights 2^(s - m)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) m[nt][i] = u[nt][i] = -INFINITY, l[nt][i] = 0.f;
 
         // the lane's row of a half's sixteen, and its first or second unit of two; units 2 i on: bits of the address exchanged
         const uint32_t unit = pn_unit<D>(lane & 15, lane >> 4);
@@ -393,7 +395,10 @@ struct PnWarp {
             }
             const int there = *(volatile int*)&hd.valid[warp][s];
             const float4 pg = *reinterpret_cast<const float4*>(&hd.scales[warp][s][0]);
-            const float pk[2] = {pg.x, pg.y}, pv[2] = {pg.z, pg.w};
+            const float pk[2] = {pg.x, pg.y};
+            // of the values (a half that is not there: as the other, for its weights are 0)
+            const float pv1 = there & 2 ? pg.w : there & 1 ? pg.z : 1.f, pv0 = there & 1 ? pg.z : pv1;
+            const float lv[2] = {log2_of(pv0), log2_of(pv1)};
             release(&hd.kempty[warp][s]);
 
             const int first = kPnKeys * c;
@@ -419,45 +424,61 @@ struct PnWarp {
                     y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                     top[nt][i] = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
                 }
-            // the largest scale of values so far, and a moved maximum, scale the sums
-            float most_v = ref;
-            if (there & 1) most_v = fmaxf(most_v, pv[0]);
-            if (there & 2) most_v = fmaxf(most_v, pv[1]);
-            bool moved = most_v > ref;
+            // A row's m follows the largest score, and m + u the largest of score and scale together, each where that has grown by
+            // more than kPnRescale: only what the row sees counts, by its weight.
+            bool moved = false;
+            float m1[NT][2], u1[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) moved |= top[nt][0] > m[nt][0] + kPnRescale || top[nt][1] > m[nt][1] + kPnRescale;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool grow = top[nt][i] > m[nt][i] + kPnRescale;
+                    m1[nt][i] = grow ? top[nt][i] : m[nt][i];
+                    u1[nt][i] = grow ? u[nt][i] + (m[nt][i] - m1[nt][i]) : u[nt][i];
+                    const float m0 = m1[nt][i] == -INFINITY ? 0.f : m1[nt][i];
+                    float rise = (top[nt][i] - m0) + lv[0];
+                    if (pv0 != pv1) {
+                        rise = fmaxf((fmaxf(sc[nt][0][i], sc[nt][0][i + 2]) - m0) + lv[0], (fmaxf(sc[nt][1][i], sc[nt][1][i + 2]) - m0) + lv[1]);
+                        rise = fmaxf(rise, __shfl_xor_sync(0xffffffffu, rise, 4));
+                        rise = fmaxf(rise, __shfl_xor_sync(0xffffffffu, rise, 8));
+                        rise = fmaxf(rise, __shfl_xor_sync(0xffffffffu, rise, 16));
+                    }
+                    const bool up = rise > u1[nt][i] + kPnRescale;
+                    if (up) u1[nt][i] = rise;
+                    moved |= grow || up;
+                }
             if (__any_sync(0xffffffffu, moved)) {
-                const float down = most_v > ref ? ref / most_v : 1.f;
-                ref = most_v;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const bool grow = top[nt][i] > m[nt][i] + kPnRescale;
-                        const float f = grow ? ex2_approx(m[nt][i] - top[nt][i]) : 1.f;      // 0 when m is -inf
-                        if (grow) m[nt][i] = top[nt][i];
-                        l[nt][i] *= f;
+                        const bool is = m1[nt][i] != m[nt][i] || u1[nt][i] != u[nt][i];
+                        const float down = is ? m[nt][i] - m1[nt][i] : 0.f;                  // -inf at first
+                        const float f = is ? ex2_approx(down + (u[nt][i] - u1[nt][i])) : 1.f;
+                        if (is) l[nt][i] *= ex2_approx(down);
+                        m[nt][i] = m1[nt][i];
+                        u[nt][i] = u1[nt][i];
 #pragma unroll
                         for (int mt = 0; mt < D / 16; ++mt) {
-                            o[nt][mt][i] *= f * down;
-                            o[nt][mt][2 + i] *= f * down;
+                            o[nt][mt][i] *= f;
+                            o[nt][mt][2 + i] *= f;
                         }
                     }
             }
-            const float up = ref > 0.f ? 1.f / ref : 0.f;
             uint32_t pb[NT][2][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    const float by = there >> kk & 1 ? pv[kk] * up : 0.f;
+                    // (where nothing has been seen u is -inf, and for keys without weight it can be far below: 0 times a finite factor)
+                    const float by[2] = {ex2_approx(fminf(lv[kk] - u[nt][0], 126.f)), ex2_approx(fminf(lv[kk] - u[nt][1], 126.f))};
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2_approx(sc[nt][kk][e] - (e & 1 ? m1 : m0));
+                        p[e] = ex2_approx(sc[nt][kk][e] - (e & 1 ? b1 : b0));
                         l[nt][e & 1] += p[e];
-                        p[e] *= by;
+                        p[e] *= by[e & 1];
                     }
                     pb[nt][kk][0] = movmatrix(pack_f16x2(p[0], p[1]));
                     pb[nt][kk][1] = movmatrix(pack_f16x2(p[2], p[3]));
@@ -498,19 +519,19 @@ struct PnWarp {
                 const int of = w.row0 + row, tok = of / a.G;
                 const int64_t p = (int64_t)cur.pos + tok;
                 const bool none = p < 0 || p >= a.cap || (x == 0.f && !sees(cur, w, (int)p));      // no such place, no key seen: zeros
+                const float half = ex2_approx(0.5f * u[nt][i]), f = x == 0.f && !all ? 0.f : half / x;      // (scores all -inf: 0 / 0)
                 if (all) {
-                    const float f = ref / x;                        // (scores all -inf: 0 / 0)
                     bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + 2 * g;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<uint32_t*>(dst + 16 * mt) =
-                            none ? 0u : pack_bf16x2(o[nt][mt][i] * f, o[nt][mt][2 + i] * f);
+                            none ? 0u : pack_bf16x2(o[nt][mt][i] * f * half, o[nt][mt][2 + i] * f * half);
                 } else {
-                    const float f = x == 0.f ? 0.f : ref / x;
+                    const float part = half * kPagedPart;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) =
-                            make_float2(o[nt][mt][i] * f * kPagedPart, o[nt][mt][2 + i] * f * kPagedPart);
+                            make_float2(o[nt][mt][i] * f * part, o[nt][mt][2 + i] * f * part);
                     // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
                     if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(none ? -INFINITY : fmaxf(m[nt][i], -FLT_MAX), x);
                 }

@@ -1,5 +1,6 @@
-// Attention over 8-bit pages of sequences that bring more than 16 query rows
-// per KV head: prompts, and chunks of them.
+// Attention over 8-bit pages of sequences that bring more than 32 query rows
+// per KV head: prompts, and chunks of them; and the few of fewer rows beside
+// them.
 //
 //   o = sum_j w_j v_j / sum_j w_j,  w_j = 2^(s_j - m),  s_j = q . k_j log2(e) / sqrt(d)
 //
@@ -13,20 +14,23 @@
 //   two e4m3 terms, which together have all of bf16's eight significant bits
 //   (elements below 2^-10 of a row's largest are off by 2^-18 of it): twice the
 //   products at twice the rate of 16-bit ones.
-// - O += P V as fp16 x fp16: four warps widen a block's values to fp16 (exactly),
-//   times their page's scale over the largest of the item so far, and store them
-//   as the tensor cores read them; P keeps 11 bits. (P in two e4m3 terms would
-//   double what the softmax warps do, which is most of what there is besides the
-//   products.)
+// - O += P V as fp16 x fp16: four warps widen a block's values to fp16, exactly,
+//   and store them as the tensor cores read them; P is a weight times its page's
+//   scale, relative to the row's largest such, and keeps 11 bits: the scale's
+//   logarithm goes into the exponent. (P in two e4m3 terms would double what the
+//   softmax warps do, which is most of what there is besides the products.)
 //
 // Bound by a tile's chain: its products, the softmax of 128 scores per thread,
 // the hand-over, while the other tile's products take their turn. A block of
-// 256 rows takes 3100 to 3200 cycles, 2048 of them products: a chunk of 512
-// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 182 us, 1.39
+// 256 rows takes 3200 to 3300 cycles, 2048 of them products: a chunk of 512
+// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 188 us, 1.35
 // PFLOP/s. Short prompts pay 3 us for an item's beginning and end beside 1.6 for
-// a block (12 of up to 2048 tokens 62 us). Taken against: factors of a block read
-// where they are used (chunk 216 us, 190 with them in registers before its scores
-// are there), parts of four blocks at least (prompts 75 us, 72 with two).
+// a block (12 of up to 2048 tokens 65 us). Scales of values as factors of what is
+// widened, over the item's largest so far, took 182 and 62 us, but lost bits of
+// the values beside a page of a larger scale that a row does not see or that has
+// no weight. Taken against: factors of a block read behind its scores without a
+// group's lead (200 us), parts of four blocks at least (prompts 75 us where two
+// took 72).
 //
 // The batch's blocks are one list, item by item, cut into equal runs for the
 // CTAs, one per SM, each of which finds its place by itself. Parts of an item
@@ -58,8 +62,11 @@ constexpr int kPwQueue = 4;               // items read ahead
 constexpr int kPwInfos = 12;              // blocks whose pages are read ahead, in fours
 constexpr int kPwMinCut = 2;              // blocks of the shortest part of an item worth its join
 constexpr int kPwCost = 3;                // what an item's beginning and end take, in blocks
-constexpr float kPwRescale = 8.f;         // m follows the maximum where that has grown by more than this
-constexpr int kPwRegsIo = 80, kPwRegsSoftmax = 168, kPwRegsOut = 96;
+constexpr float kPwRescale = 8.f;         // m and m + u follow their maxima where these have grown by more than this
+constexpr float kPwFar = 40.f;            // binary orders between scales of values that one sum of weights is taken over
+// Registers of the first four warps, the softmax's, and those that widen values: with 72, 168, 104 a chunk of 512 behind 30001 keys
+// takes 192 us, with these 188; with 80, 168, 96 the last have some of theirs in memory.
+constexpr int kPwRegsIo = 64, kPwRegsSoftmax = 168, kPwRegsOut = 112;
 static_assert(kPwRegsIo + 2 * kPwRegsSoftmax + kPwRegsOut <= 4 * 128, "the launch's registers");
 
 struct __align__(16) PwItem {
@@ -70,10 +77,10 @@ struct __align__(16) PwItem {
 };
 struct __align__(16) PwBlock {
     int tile[8];                          // per 16 keys: page and head, or -1: no key of it is seen
-    float kf[8];                          // scale of its keys, times log2(e) / sqrt(d)
-    uint32_t vw[8];                       // scale of its values over the item's largest so far, fp16 twice
-    float down, ref;                      // the largest before over it; it
-    int mask, reserved;                   // bit i: the 16 keys are there
+    float4 kl[4];                         // of two each: scale of the keys, times log2(e) / sqrt(d); log2 of the scale of the values
+    float iv[8];                          // 2^(unit - that log2)
+    float unit, lv_top;                   // that of the first page there of the item's part, a whole number; the block's largest lv
+    int mask, far;                        // bit i: the 16 keys are there; their lv is more than kPwFar from unit (bit 8: of any so far)
 };
 
 template <int D>
@@ -90,6 +97,7 @@ struct PwShape {
         PwItem queue[kPwQueue];
         PwBlock info[kPwInfos];
         float2 stat[2][kPwM];                           // (m, l)
+        float unit[2][kPwM];                            // u: O is in units of 2^(m + u)
         int64_t sums[3][kPwThreads / 32], start_at;
         int start_seq, abort;
         uint32_t tmem;
@@ -167,11 +175,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                  "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
 }
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -516,46 +519,48 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         publish(w);
                         if (!ok) break;
                         // pages of four blocks at a time: eight lanes for a block's sixteen keys each
-                        float ref = 0.f;
+                        float unit = 0.f;
+                        bool any = false, wild = false;
                         for (int j = 0; j < w.nb; j += 4, n += 4) {
                             const int jj = j + (lane >> 3), g = lane & 7;
                             const int64_t key = (int64_t)(w.blk0 + jj) * kPwK + 16 * g;
                             int tile = -1;
-                            float ks = 0.f, vs = 0.f;
+                            float ks = 0.f, lv = 0.f;
                             if (jj < w.nb && key < w.kend) {
                                 const int id = __ldg(a.pages + (int64_t)b * a.width + (int)(key >> a.bits));
                                 if (id >= 0 && id < a.n_pages) {
                                     tile = id * a.hkv_s + w.kvh;
                                     ks = __ldg(a.ks[w.r] + tile);
-                                    vs = __ldg(a.vs[w.r] + tile);
+                                    lv = log2_of(__ldg(a.vs[w.r] + tile));
                                 } else {
                                     set_status(a.status, TP_ERR_CAPACITY);
                                 }
                             }
                             __syncwarp();
-                            float most = vs;                // of the block, then of those before it too
-                            for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, o));
-                            for (int o = 8; o < 32; o <<= 1) {
-                                const float y = __shfl_up_sync(kAll, most, o);
-                                if (lane >= o) most = fmaxf(most, y);
-                            }
-                            most = fmaxf(most, ref);
-                            float before = __shfl_up_sync(kAll, most, 8);
-                            if (lane < 8) before = ref;
-                            ref = __shfl_sync(kAll, most, 31);
                             const unsigned there = __ballot_sync(kAll, tile >= 0);
+                            if (!any && there) {
+                                unit = floorf(__shfl_sync(kAll, lv, __ffs(there) - 1));
+                                any = true;
+                            }
+                            float lv_top = tile >= 0 ? lv : -INFINITY;
+                            for (int o = 4; o; o >>= 1) lv_top = fmaxf(lv_top, __shfl_xor_sync(kAll, lv_top, o));
+                            const unsigned far = __ballot_sync(kAll, tile >= 0 && fabsf(lv - unit) > kPwFar);
+                            const unsigned upto_block = (2u << (lane | 7)) - 1u;     // (bit 31: all)
                             const int four = n / 4 % (kPwInfos / 4);
                             if (!(ok = wait_all(&hd.info_empty[four], ((n / kPwInfos) & 1) ^ 1))) break;
                             PwBlock& x = hd.info[(n + (lane >> 3)) % kPwInfos];
                             x.tile[g] = tile;
-                            x.kf[g] = ks * a.scale_log2;
-                            const float wv = most > 0.f ? vs / most : 0.f;
-                            x.vw[g] = pack_f16x2(wv, wv);
+                            float* kl = reinterpret_cast<float*>(&x.kl[g >> 1]) + (g & 1);
+                            kl[0] = ks * a.scale_log2;
+                            kl[2] = lv;
+                            x.iv[g] = tile >= 0 ? ex2_approx(fminf(unit - lv, 126.f)) : 1.f;
                             if (g == 0) {
-                                x.down = most > before ? before / most : 1.f;
-                                x.ref = most;
+                                x.unit = unit;
+                                x.lv_top = lv_top;
                                 x.mask = (int)(there >> (lane & 24) & 0xFFu);
+                                x.far = (int)(far >> (lane & 24) & 0xFFu) | (wild || (far & upto_block) ? 0x100 : 0);
                             }
+                            wild |= far != 0;
                             __syncwarp();
                             if (lane == 0) mbar_arrive(&hd.info_full[four]);
                         }
@@ -601,85 +606,129 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             const int own_max = (int)min((int64_t)w.kend - 1, (int64_t)w.qpos + tok);          // last key the row sees
             const int64_t warp_max = (int64_t)w.qpos + (32 * qd) / a.G + t * a.tpt;            // ... its warp's first row
             const int whole_to = (int)min(warp_max, (int64_t)w.kend - 1);
-            float m_use = -INFINITY, l_run = 0.f;
-            bool seen = false;                              // the row has seen a key
+            // O is held in units of 2^(m + u), the sum of the weights 2^(s - m) in l. Both m and u are whole numbers.
+            float m_use = -INFINITY, u_use = -INFINITY, l_run = 0.f;
+            bool far = false, lost = false;                 // the row has seen a page far from the unit; keys, but no score above -inf
             const float factor = tok0 < a.tpt && tok < w.ntok ? __ldg(a.q_rows + ((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + m - tok0 * a.G) : 0.f;
             for (int j = 0; j < n; ++j, ++sp) {
                 if ((j & 3) == 0 && !(ok = info_wait_in(in + j))) break;
                 const PwBlock& x = hd.info[(in + j) % kPwInfos];
-                const float4 f0 = *reinterpret_cast<const float4*>(&x.kf[0]), f1 = *reinterpret_cast<const float4*>(&x.kf[4]);
-                // what the row's scores of sixteen keys each are multiplied by; never 0, so that -inf stays -inf
-                float kf[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                // what the row's scores of sixteen keys each are multiplied by
+                float kf[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) kf[i] = fmaxf(kf[i] * factor, 0x1p-126f);
-                // S is below 2^24: the scores are below 2^17 but for such factors
+                for (int i = 0; i < 4; ++i) {
+                    const float2 k = *reinterpret_cast<const float2*>(&x.kl[i]);
+                    kf[2 * i] = k.x * factor;
+                    kf[2 * i + 1] = k.y * factor;
+                }
+                const int key0 = (w.blk0 + j) * kPwK;
+                // A block that every row of the warp sees whole needs no mask. (And below, s kf - m in one rounding is off by half
+                // a step of m for the largest: scores so large that this counts are rounded before. S is below 2^24: the scores are
+                // below 2^17 but for such factors.)
                 const bool large = __any_sync(kAll, max3(max3(kf[0], kf[1], kf[2]), max3(kf[3], kf[4], kf[5]), fmaxf(kf[6], kf[7])) > 0x1p-7f);
+                const bool whole = key0 + kPwK - 1 <= whole_to && x.mask == 0xFF && !large && !x.far;
                 if (!(ok = wait_in(&hd.s_full[t], sp & 1))) break;
                 if (!idle) {
                     tc_fence_after();
-                    const int key0 = (w.blk0 + j) * kPwK, mask = x.mask;
-                    const float down = x.down;
-                    // A block that every row of the warp sees whole needs no mask. (And below, s kf - m in one rounding is off by half
-                    // a step of m for the largest: scores so large that this counts are rounded before.)
-                    const bool whole = key0 + kPwK - 1 <= whole_to && mask == 0xFF && !large;
-                    const int hi = own_max - key0;          // last key of the block the row sees
-                    seen |= whole || (hi >= 0 && (mask & ((2 << (min(hi, kPwK - 1) >> 4)) - 1)) != 0);
                     uint32_t v[4][32];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, v[c]);
+                    float4 kl = x.kl[0];                    // of the first two sixteens
+                    const float lv_top = x.lv_top;
                     tmem_wait_ld();
                     float* e = reinterpret_cast<float*>(&v[0][0]);
                     if (!whole) {
+                        const int hi = own_max - key0, mask = x.mask;                // hi: last key of the block the row sees
 #pragma unroll
                         for (int i = 0; i < 128; ++i) e[i] = i <= hi && (mask >> (i / 16) & 1) ? e[i] * kf[i / 16] : -INFINITY;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) kf[i] = 1.f;
                     }
+                    auto top_of = [&](int c) {              // of sixteen keys
+                        float y = fmaxf(e[16 * c], e[16 * c + 1]);
+#pragma unroll
+                        for (int i = 2; i < 16; i += 2) y = max3(y, e[16 * c + i], e[16 * c + i + 1]);
+                        return y * kf[c];
+                    };
                     float mq[4];                            // independent chains
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float y = fmaxf(e[32 * c], e[32 * c + 1]), z = fmaxf(e[32 * c + 16], e[32 * c + 17]);
-#pragma unroll
-                        for (int i = 2; i < 16; i += 2) {
-                            y = max3(y, e[32 * c + i], e[32 * c + i + 1]);
-                            z = max3(z, e[32 * c + 16 + i], e[32 * c + 17 + i]);
-                        }
-                        mq[c] = fmaxf(y * kf[2 * c], z * kf[2 * c + 1]);
-                    }
+                    for (int c = 0; c < 4; ++c) mq[c] = fmaxf(top_of(2 * c), top_of(2 * c + 1));
                     const float m_blk = fmaxf(fmaxf(mq[0], mq[1]), fmaxf(mq[2], mq[3]));
-                    const bool grow = m_blk > m_use + kPwRescale;
-                    const float alpha = grow ? ex2_approx(m_use - m_blk) : 1.f;      // 0 when m_use is -inf
-                    if (grow) m_use = m_blk;
-                    // O holds the blocks before this one (their products precede this S in the order of issue); rescale it
-                    // where the row's m moved, or the largest scale of values
-                    if (j > 0 && __any_sync(kAll, grow || down != 1.f)) {
-                        const float by = alpha * down;
-#pragma unroll 1
-                        for (int c = 0; c < D / 8; ++c) {
-                            uint32_t o[8];
-                            tmem_ld8(o_col + 8 * c, o);
-                            tmem_wait_ld();
+                    if (!whole) {
+                        const int hi = own_max - key0, sees = hi < 0 ? 0 : x.mask & ((2 << (min(hi, kPwK - 1) >> 4)) - 1);
+                        lost |= sees && m_blk == -INFINITY;
+                        far |= (sees & x.far) != 0;
+                    }
+                    // m follows the largest score, m + u the largest of score and scale together that the row sees: what it does not
+                    // see never reaches it. Mostly neither moves, which the largest scale of the block shows (seen or not).
+                    float m_sub = m_use == -INFINITY ? 0.f : m_use;                  // nothing seen yet: every weight is 0
+                    // (A row of NaN only is NaN as it is.)
+                    if (__any_sync(kAll, m_blk > m_use + kPwRescale || (m_blk - m_sub) + lv_top > u_use + kPwRescale)) {
+                        const bool grow = m_blk > m_use + kPwRescale;
+                        const float m_new = grow ? floorf(m_blk) : m_use;
+                        m_sub = m_new == -INFINITY ? 0.f : m_new;
+                        float rise = -INFINITY, u_new = grow ? u_use + (m_use - m_new) : u_use;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
-                            tmem_st8(o_col + 8 * c, o);
+                        for (int c = 0; c < 8; ++c) rise = fmaxf(rise, (top_of(c) - m_sub) + (c & 1 ? x.kl[c / 2].w : x.kl[c / 2].z));
+                        if (rise > u_new + kPwRescale) u_new = floorf(rise);
+                        const float by = m_new != m_use || u_new != u_use ? ex2_approx((m_use - m_new) + (u_use - u_new)) : 1.f;
+                        if (grow) l_run *= ex2_approx(m_use - m_new);                // 0 when m_use is -inf
+                        m_use = m_new;
+                        u_use = u_new;
+                        // O holds the blocks before this one (their products precede this S in the order of issue); rescale it
+                        // where a row's unit moved
+                        if (j > 0 && __any_sync(kAll, by != 1.f)) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 8; ++c) {
+                                uint32_t o[8];
+                                tmem_ld8(o_col + 8 * c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+                                tmem_st8(o_col + 8 * c, o);
+                            }
                         }
                     }
-                    const float m_sub = m_use == -INFINITY ? 0.f : m_use;            // nothing seen yet: every weight is 0
-                    const uint64_t neg2 = f2_pack(-m_sub, -m_sub);
-                    uint64_t sum[4] = {0, 0, 0, 0};
+                    const float u_sub = u_use == -INFINITY ? 0.f : u_use;
+                    float base = -(m_sub + u_sub);
+                    if (!whole) {                           // the scores themselves are there, in float32
+                        base = -u_sub;
+                        const uint64_t less = f2_pack(-m_sub, -m_sub);
+#pragma unroll
+                        for (int i = 0; i < 128; i += 2) f2_unpack(f2_add(f2_pack(e[i], e[i + 1]), less), e[i], e[i + 1]);
+                        // The sum below is taken of weights times scales, each divided by its scale again: too far apart for float32
+                        // where the scales are.
+                        if (x.far) {
+                            float sum = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 128; ++i) sum += ex2_approx(e[i]);
+                            if (far) l_run += sum;
+                        }
+                    }
+                    uint64_t total = 0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const uint64_t scale2[2] = {f2_pack(kf[2 * c], kf[2 * c]), f2_pack(kf[2 * c + 1], kf[2 * c + 1])};
+                        uint64_t scale2[2], add2[2], sum[2] = {0, 0};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {       // (read again: registers)
+                            const float k = whole ? (i ? kl.y : kl.x) * factor : 1.f, add = (i ? kl.w : kl.z) + base;
+                            scale2[i] = f2_pack(k, k);
+                            add2[i] = f2_pack(add, add);
+                        }
+                        const float2 back = *reinterpret_cast<const float2*>(&x.iv[2 * c]);
+                        if (c < 3) kl = x.kl[c + 1];
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float y, z;
-                            f2_unpack(f2_fma(f2_pack(e[32 * c + 2 * i], e[32 * c + 2 * i + 1]), scale2[i / 8], neg2), y, z);
+                            f2_unpack(f2_fma(f2_pack(e[32 * c + 2 * i], e[32 * c + 2 * i + 1]), scale2[i / 8], add2[i / 8]), y, z);
                             y = ex2_approx(y);
                             z = ex2_approx(z);
-                            sum[i & 3] = f2_add(sum[i & 3], f2_pack(y, z));
+                            sum[i / 8] = f2_add(sum[i / 8], f2_pack(y, z));
                             pk[i] = pack_f16x2(y, z);
                         }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) total = f2_fma(sum[i], i ? f2_pack(back.y, back.y) : f2_pack(back.x, back.x), total);
                         if (c == 2) {                       // the first 64 keys' products may begin
                             tmem_wait_st();
                             tc_fence_before();
@@ -689,16 +738,19 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         tmem_st16(s_col + 16 * c, pk);
                     }
                     float sx, sy;
-                    f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), sx, sy);
-                    l_run = l_run * alpha + (sx + sy);
+                    f2_unpack(total, sx, sy);
+                    if (!far) l_run += (sx + sy) * ex2_approx((u_use == -INFINITY ? 0.f : u_use) - x.unit);
                     tmem_wait_st();
                     tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&hd.p_full[t]);
                 } else {
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&hd.p_half[t]);
+                    if (lane == 0) {
+                        mbar_arrive(&hd.p_half[t]);
+                        mbar_arrive(&hd.p_full[t]);
+                    }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&hd.p_full[t]);
                 if ((j & 3) == 3 || j == w.nb - 1) info_done(in + j);
             }
             if (!ok) break;
@@ -712,7 +764,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             if (!n) continue;
             if (!(ok = wait_in(&hd.st_empty[t], (ip & 1) ^ 1))) break;
             // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
-            hd.stat[t][m] = make_float2(seen ? fmaxf(m_use, -FLT_MAX) : -INFINITY, l_run);
+            hd.stat[t][m] = make_float2(l_run == 0.f && !lost ? -INFINITY : fmaxf(m_use, -FLT_MAX), l_run);
+            hd.unit[t][m] = u_use;
             ++ip;
             __syncwarp();
             if (lane == 0) mbar_arrive(&hd.st_full[t]);
@@ -730,7 +783,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
         for (int k = 0; ok && more; ++k) {
             // ---- values of the item's blocks, widened: a lane takes 16 bytes of a key, a warp 8 keys at a time. In a block that
             // some row does not see whole, NaN are taken out, to be put into the rows that see them at the end.
-            float ref0 = 0.f, ref1 = 0.f;
             int found = 0;
             for (int j = 0; j < w.nb; ++j, ++ir) {
                 if ((j & 3) == 0 && !(ok = info_wait_in(in + j))) break;
@@ -739,13 +791,10 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 const PwBlock& x = hd.info[(in + j) % kPwInfos];
                 const int key0 = (w.blk0 + j) * kPwK, mask = x.mask;
                 const bool ragged = (int64_t)key0 + kPwK > (int64_t)w.qpos + 1 || mask != 0xFF;
-                if (j < w.nb0) ref0 = x.ref;
-                ref1 = x.ref;
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     const int key = 32 * qd + 8 * i + (lane >> 2), u = lane & 3;
                     const bool gone = ragged && (key0 + key >= w.kend || !(mask >> (key >> 4) & 1));
-                    const uint32_t by = x.vw[key >> 4];
 #pragma unroll
                     for (int c0 = 0; c0 < Sh::NKB; ++c0) {
                         const int c = D == 128 ? c0 ^ (key & 1) : 0;                 // (halves of neighbours on other banks)
@@ -760,8 +809,8 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         uint32_t o[8];
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
-                            o[2 * z] = mul_f16x2(e4m3_to_f16x2((uint16_t)in4[z]), by);
-                            o[2 * z + 1] = mul_f16x2(e4m3_to_f16x2((uint16_t)(in4[z] >> 16)), by);
+                            o[2 * z] = e4m3_to_f16x2((uint16_t)in4[z]);
+                            o[2 * z + 1] = e4m3_to_f16x2((uint16_t)(in4[z] >> 16));
                         }
                         unsigned char* to = sv + d * Sh::VB + c * (kPwK * 128) + key * 128;
                         *reinterpret_cast<uint4*>(to + (((2 * u) ^ (key & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -792,6 +841,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 const bool live = tok0 < a.tpt && tok < w.ntok;
                 const int64_t pos = (int64_t)w.qpos + tok;
                 float2 ml = make_float2(-INFINITY, 0.f);
+                float half = 0.f;
                 if (n) {
                     const uint32_t ph = (t ? ip1 : ip0) & 1;
                     if (!(ok = wait_in(&hd.st_full[t], ph) && wait_in(&hd.o_full[t], ph))) break;
@@ -799,12 +849,13 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     else ++ip0;
                     tc_fence_after();
                     ml = hd.stat[t][m];
+                    half = ex2_approx(0.5f * hd.unit[t][m]);
                 }
                 // (the item's last product, of the tile with most blocks, follows what all four warps have found)
                 poison |= *reinterpret_cast<volatile int*>(&hd.queue[k % kPwQueue].poison);
-                const float ref = t ? ref1 : ref0;
                 const bool zero = !n || (!part && (ml.x == -INFINITY || pos < 0 || pos >= a.cap));
-                const float f = zero || (part && ml.y == 0.f) ? 0.f : ref / ml.y * (part ? kPagedPart : 1.f);
+                const float f = zero || (part && ml.y == 0.f) ? 0.f : half / ml.y;             // (scores all -inf: 0 / 0)
+                if (part) half *= kPagedPart;
                 if (part && live) a.part_ml[prow + t * kPwM + m] = ml;
                 const unsigned store = __ballot_sync(kAll, live) >> (lane & 28);
                 const unsigned zeros = __ballot_sync(kAll, zero) >> (lane & 28);
@@ -823,7 +874,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         if (n) {
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f * half);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) u[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             if (c + 1 < D / 16) tmem_ld16(col + 16 * c + 16, o);
@@ -843,10 +894,10 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                             tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                u[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]) * f, __uint_as_float(o[8 * i + 1]) * f),
-                                                  pack_bf16x2(__uint_as_float(o[8 * i + 2]) * f, __uint_as_float(o[8 * i + 3]) * f),
-                                                  pack_bf16x2(__uint_as_float(o[8 * i + 4]) * f, __uint_as_float(o[8 * i + 5]) * f),
-                                                  pack_bf16x2(__uint_as_float(o[8 * i + 6]) * f, __uint_as_float(o[8 * i + 7]) * f));
+                                u[i] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * i]) * f * half, __uint_as_float(o[8 * i + 1]) * f * half),
+                                                  pack_bf16x2(__uint_as_float(o[8 * i + 2]) * f * half, __uint_as_float(o[8 * i + 3]) * f * half),
+                                                  pack_bf16x2(__uint_as_float(o[8 * i + 4]) * f * half, __uint_as_float(o[8 * i + 5]) * f * half),
+                                                  pack_bf16x2(__uint_as_float(o[8 * i + 6]) * f * half, __uint_as_float(o[8 * i + 7]) * f * half));
                             if (c + 1 < D / 32) tmem_ld32(col + 32 * c + 32, o);
                             transpose4(u, lane);
                         }
