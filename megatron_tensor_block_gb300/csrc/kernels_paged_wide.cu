@@ -923,18 +923,33 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     const int64_t pos = (int64_t)w.qpos + tok;
                     if (tok0 >= a.tpt || tok >= w.ntok || pos < 0 || pos >= a.cap) continue;
                     const int end = (int)min((int64_t)min(w.kend, (w.blk0 + w.nb) * kPwK) - 1, pos), page = 1 << a.bits;
+                    const int* row = a.pages + (int64_t)w.b * a.width;
                     float* po = a.part_o + (prow + t * kPwM + m) * D;
                     bf16* out = a.out + (((int64_t)w.r * a.T + w.t0 + tok) * a.hq_s + w.kvh * a.G + g) * D;
+                    // only blocks that NaN were taken out of, as above
 #pragma unroll 1
-                    for (int key = w.blk0 * kPwK; key <= end; ++key) {
-                        const int id = __ldg(a.pages + (int64_t)w.b * a.width + (key >> a.bits));
-                        if (id < 0 || id >= a.n_pages) continue;
-                        const uint8_t* v = a.v[w.r] + (((int64_t)id * a.hkv_s + w.kvh) * page + (key & (page - 1))) * D;
+                    for (int key0 = w.blk0 * kPwK; key0 <= end; key0 += kPwK) {
+                        bool ragged = (int64_t)key0 + kPwK > (int64_t)w.qpos + 1;
+                        for (int key = key0; !ragged && key < key0 + kPwK; key += page) {
+                            const int id = __ldg(row + (key >> a.bits));
+                            ragged = id < 0 || id >= a.n_pages;
+                        }
+                        if (!ragged) continue;
 #pragma unroll 1
-                        for (int i = 0; i < D; ++i) {
-                            if ((v[i] & 0x7f) != 0x7f) continue;
-                            if (part) po[i] = NAN;
-                            else out[i] = __float2bfloat16_rn(NAN);
+                        for (int key = key0; key < key0 + kPwK && key <= end; ++key) {
+                            const int id = __ldg(row + (key >> a.bits));
+                            if (id < 0 || id >= a.n_pages) continue;
+                            const uint8_t* v = a.v[w.r] + (((int64_t)id * a.hkv_s + w.kvh) * page + (key & (page - 1))) * D;
+#pragma unroll 1
+                            for (int i = 0; i < D; i += 16) {
+                                const uint4 x = *reinterpret_cast<const uint4*>(v + i);
+                                if (!(e4m3_nan(x.x) | e4m3_nan(x.y) | e4m3_nan(x.z) | e4m3_nan(x.w))) continue;
+                                for (int z = i; z < i + 16; ++z) {
+                                    if ((v[z] & 0x7f) != 0x7f) continue;
+                                    if (part) po[z] = NAN;
+                                    else out[z] = __float2bfloat16_rn(NAN);
+                                }
+                            }
                         }
                     }
                 }
