@@ -788,8 +788,10 @@ tp_status tp_profile_phase_stamps(tp_plan_t plan, uint64_t* out, int32_t rows, v
  * every CTA leaves through its abort path (all waits are bounded, so the
  * launch ends within a few seconds). The output and the KV rows at pos are
  * then undefined; call tp_workspace_init on the workspace before its next
- * forward. Off (0) by default; nothing in the library turns it on. No
- * counterpart on the pages.
+ * forward. tp_attn_paged's kernels likewise never get a stage of their ring of
+ * keys back, and give up where they need one again; tp_paged_workspace_init
+ * comes before the next call. Off (0) by default; nothing in the library turns
+ * it on. No counterpart on the pages.
  * Errors: TP_ERR_NULL, TP_ERR_INVALID_ARG (on not 0 or 1). */
 tp_status tp_debug_withhold_arrival(tp_plan_t plan, int32_t on);
 

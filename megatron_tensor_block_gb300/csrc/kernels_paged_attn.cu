@@ -94,7 +94,7 @@ struct PnArgs {
     float2* part_ml;                      // [kSMs][2][rows]
     unsigned* joined;                     // [kSMs] pieces of the head that begins in this CTA and ends in another
     int* status;
-    int N, B, T, hq_s, hkv_s, G, bits, width, n_pages, max_new, cap;
+    int N, B, T, hq_s, hkv_s, G, bits, width, n_pages, max_new, cap, withheld;
     float scale_log2;
 };
 
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
     if (tid == 0) {
         for (int i = 0; i < W * S; ++i) {
             mbar_init(&hd.kfull[0][0] + i, 2);               // the copies, and the scales
-            mbar_init(&hd.kempty[0][0] + i, 1);
+            mbar_init(&hd.kempty[0][0] + i, 1 + a.withheld);
             mbar_init(&hd.vfull[0][0] + i, 1);
             mbar_init(&hd.vempty[0][0] + i, 1);
         }
@@ -912,6 +912,7 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         a.width = p.c.width;
         a.n_pages = p.c.n_pages;
         a.max_new = p.max_new;
+        a.withheld = p.withheld;
         a.cap = p.c.width * p.c.page;
         a.scale_log2 = p.scale_log2;
         void* args[] = {&a};

@@ -124,7 +124,7 @@ struct PwArgs {
     float2* part_ml;                      // [kSMs][2][256]
     PagedCut* cuts;                       // [kSMs]
     int* status;
-    int N, B, T, hq_s, hkv_s, G, tpt, bits, width, n_pages, max_new, cap, few;
+    int N, B, T, hq_s, hkv_s, G, tpt, bits, width, n_pages, max_new, cap, few, withheld;
     float scale_log2;
 };
 
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
             mbar_init(&hd.st_empty[i], 4);
             mbar_init(&hd.turn[i], 1);
         }
-        for (int i = 0; i < RK; ++i) mbar_init(&hd.k_full[i], 1), mbar_init(&hd.k_empty[i], 2);
+        for (int i = 0; i < RK; ++i) mbar_init(&hd.k_full[i], 1), mbar_init(&hd.k_empty[i], 2 + a.withheld);
         for (int i = 0; i < RR; ++i) mbar_init(&hd.r_full[i], 1), mbar_init(&hd.r_empty[i], 4);
         for (int i = 0; i < RV; ++i) mbar_init(&hd.v_full[i], 4), mbar_init(&hd.v_empty[i], 2);
         for (int i = 0; i < kPwInfos / 4; ++i) mbar_init(&hd.info_full[i], 1), mbar_init(&hd.info_empty[i], 13);
@@ -1120,6 +1120,7 @@ cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStr
     a.max_new = p.max_new;
     a.cap = p.c.width * p.c.page;
     a.few = few;
+    a.withheld = p.withheld;
     a.scale_log2 = p.scale_log2;
     const bool d128 = p.d == 128;
     const void* fn = d128 ? reinterpret_cast<const void*>(paged_items_kernel<128>) : reinterpret_cast<const void*>(paged_items_kernel<64>);

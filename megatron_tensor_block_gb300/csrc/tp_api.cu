@@ -1615,6 +1615,7 @@ extern "C" tp_status tp_attn_paged(tp_plan_t plan, const void* q, const tp_paged
     a.hkv_s = (int)plan->info.hkv_shard;
     a.d = (int)plan->d.head_dim;
     a.max_new = max_new && max_new < T ? max_new : T;
+    a.withheld = (int)plan->dbg_bar_extra;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)plan->d.head_dim));
     a.ws = static_cast<char*>(workspace);
     a.status = static_cast<int*>(workspace);

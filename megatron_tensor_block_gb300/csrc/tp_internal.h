@@ -442,6 +442,7 @@ struct PagedAttnArgs {
     const int* cu;
     const int* pos;
     int N, B, T, hq_s, hkv_s, d, max_new;
+    int withheld;                         // test hook: arrivals that a stage of keys waits for in vain
     float scale_log2;                     // log2(e) / sqrt(d)
     int* status;                          // first word of the workspace
     char* ws;
