@@ -38,13 +38,15 @@ namespace tpk {
 // exactly; q is brought to fp16 by a power of two for each row, exactly but for
 // elements below 2^-29 of the row's largest; the weights' rounding to fp16 is
 // 2^-11. The scale of a page's keys goes into the scores, that of its values into
-// the weights, relative to the row's largest weight times scale. (e4m3 x e4m3 products of q
-// in two terms, without conversions of K here: decode of 64 68 us where this
-// took 63.)
+// the weights, relative to the row's largest weight times scale. (e4m3 x e4m3
+// products of q in two terms, without conversions of K here: decode of 64 68 us
+// where this took 63.)
 //
-// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 326 us
-// on the device, 6.5 TB/s. 64 over 256 to 4095: 51 to 53, of which 1.7 pass until every
-// warp has its place and 8 to 10 from the first CTA's last key to the last join.
+// 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 326 to
+// 329 us on the device, 6.5 TB/s. 64 over 256 to 4095: 52 to 54, of which 1.7 pass
+// until every warp has its place and 8 to 10 from the first CTA's last key to the
+// last join. 32 of 1 to 8 tokens over 100 to 4000 keys in pages of 16: 72 (65 in
+// larger ones).
 // ---------------------------------------------------------------------------
 
 constexpr float kPnRescale = 8.f;         // m and m + u follow their maxima where these have grown by more than this
@@ -169,7 +171,7 @@ __device__ __forceinline__ uint32_t pn_unit(int r, int u) {
 
 // The copies of warp w's chunks, their keys and scales or (V) their values, by one lane, as its stages become free. Each copy is
 // an instruction for each lane, one after another: a warp with the lanes of fifteen others' keys and values was the kernel's
-// limit (128 long contexts 350 us, and 455 in pages of 16; 326 and 366 with a warp for either).
+// limit (128 long contexts 350 us, and 455 in pages of 16; 326 and 366 to 370 with a warp for either).
 template <int D, int W>
 __device__ __forceinline__ void pn_copies(const PnArgs& a, typename PnShape<D, W>::Head& hd, unsigned char* rings, int w, bool V, int64_t todo,
                                           int64_t in_sequence) {

@@ -23,12 +23,12 @@
 // Bound by a tile's chain: its products, the softmax of 128 scores per thread,
 // the hand-over, while the other tile's products take their turn. A block of
 // 256 rows takes 3200 to 3300 cycles, 2048 of them products: a chunk of 512
-// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 188 us, 1.35
-// PFLOP/s. Short prompts pay 3 us for an item's beginning and end beside 1.6 for
-// a block (12 of up to 2048 tokens 65 us). Scales of values as factors of what is
-// widened, over the item's largest so far, took 182 and 62 us, but lost bits of
-// the values beside a page of a larger scale that a row does not see or that has
-// no weight. Taken against: factors of a block read behind its scores without a
+// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 188 to 196 us, 1.29 to
+// 1.35 PFLOP/s. Short prompts pay 3 us for an item's beginning and end beside 1.7
+// for a block (12 of up to 2048 tokens 65 to 68 us). Scales of values as factors of
+// what is widened, over the item's largest so far, took 182 and 62 us, but lost
+// bits of the values beside a page of a larger scale that a row does not see or
+// that has no weight. Taken against: factors of a block read behind its scores without a
 // group's lead (200 us), parts of four blocks at least (prompts 75 us where two
 // took 72).
 //

@@ -18,8 +18,11 @@ constexpr int kPnRows = 16;               // query rows that a warp works on
 constexpr int kPnMost = 32;               // ... of a sequence and KV head that are few, sixteen at a time
 // Chunks of such sequences beside prompts that go with these: so few that their own kernel, which the prompts' has to wait
 // for, would leave most of the machine idle. Single tokens behind 1000 keys and a prompt of 512, 8 KV heads of 128, with
-// the prompt and apart: 8 tokens (2048 chunks) 33.3 and 41.4 us, 16 (4096) 38.4 and 44.1, 32 (8192) 56.9 and 50.2, 64 89.5
-// and 63.8.
+// the prompt and apart: 8 tokens (2048 chunks) 37.1 and 43.1 us, 16 (4096) 42.7 and 45.9, 32 (8192) 62.6 and 51.6, 64 99.7
+// and 65.7. Heads of 64: 33.1 and 39.1, 37.1 and 40.5, 53.1 and 44.2, 82.0 and 54.0. A prompt of 4096: 168.7 and 176.7, 178.1
+// and 179.6, 194.9 and 185.4; of 128: 31.1 and 43.2, 36.9 and 45.9, 52.0 and 52.5. Behind 4000 keys (4032 chunks, 8064) 41.0
+// and 46.3, 52.0 and 51.8; but 64 tokens behind 250 keys (4096 chunks) 60.0 and 47.9, since a head of a sequence costs the
+// prompts' kernel three blocks besides its own, which a count of chunks does not see.
 constexpr int64_t kPagedFewBeside = 5000;
 // Parts of a row are kept divided by their own sums of weights and times this, so that they are finite whatever the values
 // are (448 times a scale below 2^128 at most): a row in parts is finite where one in one piece is.
