@@ -70,7 +70,7 @@ struct PnShape {
     struct Head {
         uint64_t kfull[W][STAGES], kempty[W][STAGES], vfull[W][STAGES], vempty[W][STAGES];
         float scales[W][STAGES][4];                                 // of K for both halves of the chunk, of V
-        float2 ml[2 * W][ROWS];                                     // (m, l) of the pieces
+        float4 mlu[2 * W][ROWS];                                    // (m, l, u) of the pieces
         int64_t sums[W + COPIES], firsts[W + COPIES];
         int64_t at[W];                                              // a warp's place in its first sequence
         PnPiece pieces[2 * W];                                      // of warp w: one that began before it, one that goes on behind it
@@ -93,7 +93,7 @@ struct PnArgs {
     const int* pos;
     const int* pages;
     float* part_o;                        // [kSMs][2][rows][D], as the pieces in shared memory
-    float2* part_ml;                      // [kSMs][2][rows]
+    float4* part_mlu;                     // [kSMs][2][rows]
     unsigned* joined;                     // [kSMs] pieces of the head that begins in this CTA and ends in another
     int* status;
     int N, B, T, hq_s, hkv_s, G, bits, width, n_pages, max_new, cap, withheld;
@@ -319,7 +319,7 @@ struct PnWarp {
     }
 
     // Chunks w.x0 .. w.x1 - 1 of a head of the sequence at cur. Where that is all of them the result goes to out, else to
-    // slot (O / l [rows][D], times kPagedPart) and (m, l) beside it.
+    // slot (O [rows][D] in units of 2^(m + u)) and (m, l, u) beside it.
     template <int NT>
     __device__ __forceinline__ bool head(const PnCursor& cur, const PnPiece& w, float* slot) {
         const int g = lane >> 2, t = lane & 3, kend = cur.kend(a);
@@ -471,16 +471,16 @@ struct PnWarp {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+                const float u0 = u[nt][0] == -INFINITY ? 0.f : u[nt][0], u1 = u[nt][1] == -INFINITY ? 0.f : u[nt][1];
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
-                    // (where nothing has been seen u is -inf, and for keys without weight it can be far below: 0 times a finite factor)
-                    const float by[2] = {ex2_approx(fminf(lv[kk] - u[nt][0], 126.f)), ex2_approx(fminf(lv[kk] - u[nt][1], 126.f))};
+                    // (an exponential for either: a weight can be below float32's smallest where its product with the scale counts)
                     float p[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[e] = ex2_approx(sc[nt][kk][e] - (e & 1 ? b1 : b0));
-                        l[nt][e & 1] += p[e];
-                        p[e] *= by[e & 1];
+                        const float y = sc[nt][kk][e] - (e & 1 ? b1 : b0);
+                        l[nt][e & 1] += ex2_approx(y);
+                        p[e] = ex2_approx(y + (lv[kk] - (e & 1 ? u1 : u0)));
                     }
                     pb[nt][kk][0] = movmatrix(pack_f16x2(p[0], p[1]));
                     pb[nt][kk][1] = movmatrix(pack_f16x2(p[2], p[3]));
@@ -521,37 +521,36 @@ struct PnWarp {
                 const int of = w.row0 + row, tok = of / a.G;
                 const int64_t p = (int64_t)cur.pos + tok;
                 const bool none = p < 0 || p >= a.cap || (x == 0.f && !sees(cur, w, (int)p));      // no such place, no key seen: zeros
-                const float half = ex2_approx(0.5f * u[nt][i]), f = x == 0.f && !all ? 0.f : half / x;      // (scores all -inf: 0 / 0)
                 if (all) {
+                    const float half = ex2_approx(0.5f * u[nt][i]), f = half / x;           // (scores all -inf: 0 / 0)
                     bf16* dst = a.out + (((int64_t)r * a.T + cur.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + 2 * g;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
                         *reinterpret_cast<uint32_t*>(dst + 16 * mt) =
                             none ? 0u : pack_bf16x2(o[nt][mt][i] * f * half, o[nt][mt][2 + i] * f * half);
                 } else {
-                    const float part = half * kPagedPart;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt)
-                        *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) =
-                            make_float2(o[nt][mt][i] * f * part, o[nt][mt][2 + i] * f * part);
+                        *reinterpret_cast<float2*>(slot + row * D + 16 * mt + 2 * g) = make_float2(o[nt][mt][i], o[nt][mt][2 + i]);
                     // (a row that saw keys, whose scores were all -inf, has a finite m here: it is not one that saw none)
-                    if (g == 0) hd.ml[2 * warp + (w.x0 == 0)][row] = make_float2(none ? -INFINITY : fmaxf(m[nt][i], -FLT_MAX), x);
+                    if (g == 0) hd.mlu[2 * warp + (w.x0 == 0)][row] = make_float4(none ? -INFINITY : fmaxf(m[nt][i], -FLT_MAX), x, u[nt][i], 0.f);
                 }
             }
         return true;
     }
 };
 
-// One warp: a row's n pieces joined, l = sum_i 2^(m_i - m) l_i and the mean
-// o = sum_i 2^(m_i - m) l_i / l o_i, which is as large as its pieces at most,
-// always in the same order. stat(i): (m, l) of piece i, read by lane i; get(i, x):
-// the lane's D / 32 elements of its o. No piece is left out, so that a NaN of one
+// One warp: a row's n pieces joined, l = sum_i 2^(m_i - m) l_i and, in units of
+// 2^(m + u), o = sum_i 2^(m_i + u_i - m - u) o_i, always in the same order: no
+// piece is as large as its values are, and none is lost whose weights are small
+// but not its values. stat(i): (m, l, u) of piece i, read by lane i; get(i, x): the
+// lane's D / 32 elements of its o. No piece is left out, so that a NaN of one
 // stays. m is -inf where no piece has seen a key.
 template <int D, typename Stat, typename Get>
-__device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, float (&o)[D / 32]) {
+__device__ __forceinline__ float4 pn_join(int n, int lane, Stat stat, Get get, float (&o)[D / 32]) {
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int E = D / 32, AHEAD = 4;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, u = -INFINITY;
 #pragma unroll
     for (int k = 0; k < E; ++k) o[k] = 0.f;
     float x[AHEAD][E];
@@ -563,16 +562,16 @@ __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, f
     load(0);
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += 32) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (i0 + lane < n) ml = stat(i0 + lane);
-        const float top = fmaxf(m, warp_max(ml.x)), down = m == -INFINITY ? 0.f : ex2_approx(m - top);
-        float w = (ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top)) * ml.y;
-        const float sum = l * down + warp_sum(w), inv = sum == 0.f ? 0.f : 1.f / sum, keep = l * down * inv;
-        w *= inv;
-        l = sum;
+        float4 s = make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+        if (i0 + lane < n) s = stat(i0 + lane);
+        const float top = fmaxf(m, warp_max(s.x)), m0 = top == -INFINITY ? 0.f : top;
+        const float was = (m - m0) + u, its = (s.x - m0) + s.z;
+        l = l * ex2_approx(m - m0) + warp_sum(s.y * ex2_approx(s.x - m0));
         m = top;
+        u = fmaxf(was, warp_max(its));
+        const float u0 = u == -INFINITY ? 0.f : u, down = ex2_approx(was - u0), w = ex2_approx(its - u0);
 #pragma unroll
-        for (int k = 0; k < E; ++k) o[k] *= keep;
+        for (int k = 0; k < E; ++k) o[k] *= down;
 #pragma unroll 1
         for (int i = i0; i < min(i0 + 32, n); i += AHEAD) {
 #pragma unroll
@@ -585,19 +584,19 @@ __device__ __forceinline__ float2 pn_join(int n, int lane, Stat stat, Get get, f
             load(i + AHEAD);
         }
     }
-    return make_float2(m, l);
+    return make_float4(m, l, u, 0.f);
 }
 
 template <int D>
-__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float2 ml, const float (&o)[D / 32]) {
+__device__ __forceinline__ void pn_store(const PnArgs& a, const PnPiece& p, int row, int lane, float4 mlu, const float (&o)[D / 32]) {
     const int r = p.h / a.hkv_s, kvh = p.h - r * a.hkv_s, of = p.row0 + row, tok = of / a.G;
     const int64_t at = (int64_t)p.pos + tok;
-    const bool none = ml.x == -INFINITY || at < 0 || at >= a.cap;
+    const bool none = mlu.x == -INFINITY || at < 0 || at >= a.cap;
     bf16* dst = a.out + (((int64_t)r * a.T + p.c0 + tok) * a.hq_s + kvh * a.G + (of - tok * a.G)) * D + lane * (D / 32);
-    const float f = ml.y == 0.f ? NAN : 1.f / kPagedPart;
+    const float half = ex2_approx(0.5f * mlu.z), f = half / mlu.y;          // (scores all -inf: 0 / 0)
     uint32_t y[D / 64];
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f, o[2 * k + 1] * f);
+    for (int k = 0; k < D / 64; ++k) y[k] = none ? 0u : pack_bf16x2(o[2 * k] * f * half, o[2 * k + 1] * f * half);
     if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
     else *reinterpret_cast<uint32_t*>(dst) = y[0];
 }
@@ -792,14 +791,14 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         if (row >= p.rows) continue;
         auto at = [&](int j) { return j ? ((first + 1) & ~1) + 2 * (j - (first & 1)) : first; };
         float o[E];
-        const float2 r = pn_join<D>(
-            __popc(pieces), lane, [&](int j) { return hd.ml[at(j)][row]; },
+        const float4 r = pn_join<D>(
+            __popc(pieces), lane, [&](int j) { return hd.mlu[at(j)][row]; },
             [&](int j, float (&x)[E]) { pn_read<D>(slot_of(at(j)) + row * D, lane, x, false); }, o);
         if (p.x0 == 0 && p.x1 == p.nch) {
             pn_store<D>(a, p, row, lane, r, o);
         } else {
             const int64_t dst = ((int64_t)blockIdx.x * 2 + (p.x0 == 0)) * Sh::ROWS + row;
-            if (lane == 0) a.part_ml[dst] = r;
+            if (lane == 0) a.part_mlu[dst] = r;
             float* to = a.part_o + dst * D + lane * E;
             if constexpr (E == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
             else *reinterpret_cast<float2*>(to) = make_float2(o[0], o[1]);
@@ -839,8 +838,8 @@ __global__ void __launch_bounds__(PnShape<D, W>::THREADS, 1) paged_few_kernel(co
         auto src = [&](int i) { return ((int64_t)(first + i) * 2 + (i == 0)) * Sh::ROWS; };
         for (int row = warp; row < p.rows; row += WARPS) {
             float o[E];
-            const float2 r = pn_join<D>(
-                n, lane, [&](int i) { return __ldcg(a.part_ml + src(i) + row); },
+            const float4 r = pn_join<D>(
+                n, lane, [&](int i) { return __ldcg(a.part_mlu + src(i) + row); },
                 [&](int i, float (&x)[E]) { pn_read<D>(a.part_o + (src(i) + row) * D, lane, x, true); }, o);
             pn_store<D>(a, p, row, lane, r, o);
         }
@@ -872,7 +871,7 @@ cudaError_t byte_map(const void* base, int64_t d, int64_t d1, int64_t d2, int b1
 }
 
 namespace {
-constexpr size_t kPnMl = (size_t)kSMs * 2 * kPnRows * sizeof(float2);
+constexpr size_t kPnMl = (size_t)kSMs * 2 * kPnRows * sizeof(float4);
 size_t pn_part(int d) { return (size_t)kSMs * 2 * kPnRows * d * sizeof(float); }
 }  // namespace
 
@@ -901,7 +900,7 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& p, cudaStream_t s) {
         a.pos = p.pos;
         a.pages = p.c.pages;
         a.joined = reinterpret_cast<unsigned*>(p.ws + 256);
-        a.part_ml = reinterpret_cast<float2*>(p.ws + kPagedCtrl);
+        a.part_mlu = reinterpret_cast<float4*>(p.ws + kPagedCtrl);
         a.part_o = reinterpret_cast<float*>(p.ws + kPagedCtrl + kPnMl);
         a.status = p.status;
         a.N = p.N;

@@ -120,8 +120,8 @@ struct PwArgs {
     const int* cu;
     const int* pos;
     const int* pages;
-    float* part_o;                        // [kSMs][2][256][D] O / l, times kPagedPart
-    float2* part_ml;                      // [kSMs][2][256]
+    float* part_o;                        // [kSMs][2][256][D], in units of 2^(m + u)
+    float4* part_mlu;                     // [kSMs][2][256]
     PagedCut* cuts;                       // [kSMs]
     int* status;
     int N, B, T, hq_s, hkv_s, G, tpt, bits, width, n_pages, max_new, cap, few, withheld;
@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 const bool live = tok0 < a.tpt && tok < w.ntok;
                 const int64_t pos = (int64_t)w.qpos + tok;
                 float2 ml = make_float2(-INFINITY, 0.f);
-                float half = 0.f;
+                float u_row = -INFINITY;
                 if (n) {
                     const uint32_t ph = (t ? ip1 : ip0) & 1;
                     if (!(ok = wait_in(&hd.st_full[t], ph) && wait_in(&hd.o_full[t], ph))) break;
@@ -849,14 +849,13 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                     else ++ip0;
                     tc_fence_after();
                     ml = hd.stat[t][m];
-                    half = ex2_approx(0.5f * hd.unit[t][m]);
+                    u_row = hd.unit[t][m];
                 }
                 // (the item's last product, of the tile with most blocks, follows what all four warps have found)
                 poison |= *reinterpret_cast<volatile int*>(&hd.queue[k % kPwQueue].poison);
                 const bool zero = !n || (!part && (ml.x == -INFINITY || pos < 0 || pos >= a.cap));
-                const float f = zero || (part && ml.y == 0.f) ? 0.f : half / ml.y;             // (scores all -inf: 0 / 0)
-                if (part) half *= kPagedPart;
-                if (part && live) a.part_ml[prow + t * kPwM + m] = ml;
+                if (part && live) a.part_mlu[prow + t * kPwM + m] = make_float4(ml.x, ml.y, u_row, 0.f);
+                const float half = ex2_approx(0.5f * u_row), f = zero ? 0.f : half / ml.y;     // (scores all -inf: 0 / 0)
                 const unsigned store = __ballot_sync(kAll, live) >> (lane & 28);
                 const unsigned zeros = __ballot_sync(kAll, zero) >> (lane & 28);
                 const int row = part ? (t * kPwM + m) * (D * 4) : (tok * a.hq_s + g) * (D * 2);
@@ -873,8 +872,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                         uint4 u[4] = {};
                         if (n) {
                             tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f * half);
 #pragma unroll
                             for (int i = 0; i < 4; ++i) u[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                             if (c + 1 < D / 16) tmem_ld16(col + 16 * c + 16, o);
@@ -1015,8 +1012,9 @@ __global__ void __launch_bounds__(256) paged_terms_kernel(const __grid_constant_
     if (i % LANES == 0) a.q_rows[i / LANES] = e == 255 ? 1.f : 1.f / by;
 }
 
-// Rows of the items that were cut, a warp each: m = max m_i, l = sum_i 2^(m_i - m) l_i and the mean o = sum_i 2^(m_i - m) l_i / l o_i
-// over the parts in their order, which is as large as its parts at most. No part is left out, so that a NaN of one stays. m is -inf where no part has seen a key.
+// Rows of the items that were cut, a warp each, over the parts in their order: l = sum_i 2^(m_i - m) l_i and, in units of
+// 2^(m + u), o = sum_i 2^(m_i + u_i - m - u) O_i: no part is as large as its values are, and none is lost whose weights are
+// small but not its values. No part is left out, so that a NaN of one stays. m is -inf where no part has seen a key.
 template <int D>
 __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PwArgs a, int slices) {
     constexpr int E = D / 32, AHEAD = 4;             // elements per lane, parts loaded together
@@ -1030,14 +1028,14 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
         const int r = c.h / a.hkv_s, kvh = c.h - r * a.hkv_s;
         // the first part is the second place of the CTA that begins the item, the others the first places of those behind it
         auto place = [&](int i) { return ((int64_t)(cta + i) * 2 + (i == 0)) * (2 * kPwM) + row; };
-        float top = -INFINITY, l = 0.f, o[E] = {};
+        float top = -INFINITY, l = 0.f, u = -INFINITY, o[E] = {};
         for (int i0 = 0; i0 < c.parts; i0 += AHEAD) {
-            float2 ml[AHEAD];
+            float4 s[AHEAD];
             float x[AHEAD][E];
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 if (i0 + i >= c.parts) break;
-                ml[i] = __ldcg(a.part_ml + place(i0 + i));
+                s[i] = __ldcg(a.part_mlu + place(i0 + i));
                 const float* src = a.part_o + place(i0 + i) * D + lane * E;
                 if constexpr (E == 4) {
                     const float4 y = __ldcg(reinterpret_cast<const float4*>(src));
@@ -1050,31 +1048,31 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
 #pragma unroll
             for (int i = 0; i < AHEAD; ++i) {
                 if (i0 + i >= c.parts) break;
-                const float m2 = fmaxf(top, ml[i].x);
-                const float f = l * (top == -INFINITY ? 0.f : ex2_approx(top - m2));
-                const float w = ml[i].y * (ml[i].x == -INFINITY ? 0.f : ex2_approx(ml[i].x - m2));
+                const float m2 = fmaxf(top, s[i].x), m0 = m2 == -INFINITY ? 0.f : m2;
+                const float was = (top - m0) + u, its = (s[i].x - m0) + s[i].z;
+                l = l * ex2_approx(top - m0) + s[i].y * ex2_approx(s[i].x - m0);
                 top = m2;
-                l = f + w;
-                const float inv = l == 0.f ? 0.f : 1.f / l, keep = f * inv, add = w * inv;
+                u = fmaxf(was, its);
+                const float u0 = u == -INFINITY ? 0.f : u, f = ex2_approx(was - u0), w = ex2_approx(its - u0);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = o[e] * keep + x[i][e] * add;
+                for (int e = 0; e < E; ++e) o[e] = o[e] * f + x[i][e] * w;
             }
         }
         const int64_t pos = (int64_t)c.qpos + tok;
         const bool none = top == -INFINITY || pos < 0 || pos >= a.cap;
-        const float inv = l == 0.f ? NAN : 1.f / kPagedPart;
+        const float half = ex2_approx(0.5f * u), f = half / l;             // (scores all -inf: 0 / 0)
         uint32_t y[E / 2];
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) y[e] = none ? 0u : pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+        for (int e = 0; e < E / 2; ++e) y[e] = none ? 0u : pack_bf16x2(o[2 * e] * f * half, o[2 * e + 1] * f * half);
         bf16* dst = a.out + (((int64_t)r * a.T + c.t0 + tok) * a.hq_s + kvh * a.G + (m - tok0 * a.G)) * D + lane * E;
         if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
         else *reinterpret_cast<uint32_t*>(dst) = y[0];
     }
 }
 
-// Cuts, partial (m, l), partial O, q's terms and rows.
+// Cuts, partial (m, l, u), partial O, q's terms and rows.
 static size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-static const size_t kPwCuts = up256(kSMs * sizeof(PagedCut)), kPwMl = (size_t)kSMs * 2 * 2 * kPwM * sizeof(float2);
+static const size_t kPwCuts = up256(kSMs * sizeof(PagedCut)), kPwMl = (size_t)kSMs * 2 * 2 * kPwM * sizeof(float4);
 static size_t pw_o(int d) { return (size_t)kSMs * 2 * 2 * kPwM * d * sizeof(float); }
 size_t paged_wide_bytes(int64_t tokens, int heads, int d) {
     return kPwCuts + kPwMl + pw_o(d) + up256((size_t)tokens * heads * d * 2) + up256((size_t)tokens * heads * sizeof(float));
@@ -1084,7 +1082,7 @@ cudaError_t launch_paged_wide(const PagedAttnArgs& p, int few, char* ws, cudaStr
     PwArgs a;
     memset(&a, 0, sizeof a);
     a.cuts = reinterpret_cast<PagedCut*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(ws + kPwCuts);
+    a.part_mlu = reinterpret_cast<float4*>(ws + kPwCuts);
     a.part_o = reinterpret_cast<float*>(ws + kPwCuts + kPwMl);
     a.q_terms = reinterpret_cast<uint8_t*>(ws + kPwCuts + kPwMl + pw_o(p.d));
     const int64_t rows = (int64_t)p.N * p.T * p.hq_s;

@@ -24,9 +24,6 @@ constexpr int kPnMost = 32;               // ... of a sequence and KV head that 
 // and 46.3, 52.0 and 51.8; but 64 tokens behind 250 keys (4096 chunks) 60.0 and 47.9, since a head of a sequence costs the
 // prompts' kernel three blocks besides its own, which a count of chunks does not see.
 constexpr int64_t kPagedFewBeside = 5000;
-// Parts of a row are kept divided by their own sums of weights and times this, so that they are finite whatever the values
-// are (448 times a scale below 2^128 at most): a row in parts is finite where one in one piece is.
-constexpr float kPagedPart = 0x1p-9f;
 
 // A head's query rows are worked on sixteen at a time.
 __device__ __forceinline__ int paged_groups(int n, int G) { return (n * G + kPnRows - 1) / kPnRows; }
