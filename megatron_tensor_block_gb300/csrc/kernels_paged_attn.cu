@@ -45,7 +45,7 @@ namespace tpk {
 // 128 single tokens over up to 16383 keys, 32 query and 8 KV heads of 128: 326 to
 // 329 us on the device, 6.5 TB/s. 64 over 256 to 4095: 52 to 54, of which 1.7 pass
 // until every warp has its place and 8 to 10 from the first CTA's last key to the
-// last join. 32 of 1 to 8 tokens over 100 to 4000 keys in pages of 16: 72 (65 in
+// last join. 32 of 1 to 8 tokens over 100 to 4000 keys in pages of 16: 71 (65 in
 // larger ones).
 // ---------------------------------------------------------------------------
 

@@ -23,8 +23,8 @@
 // Bound by a tile's chain: its products, the softmax of 128 scores per thread,
 // the hand-over, while the other tile's products take their turn. A block of
 // 256 rows takes 3200 to 3300 cycles, 2048 of them products: a chunk of 512
-// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 188 to 196 us, 1.29 to
-// 1.35 PFLOP/s. Short prompts pay 3 us for an item's beginning and end beside 1.7
+// tokens behind 30001 keys, 32 query and 8 KV heads of 128, 187 to 195 us, 1.3 to
+// 1.36 PFLOP/s. Short prompts pay 3 us for an item's beginning and end beside 1.7
 // for a block (12 of up to 2048 tokens 65 to 68 us). Scales of values as factors of
 // what is widened, over the item's largest so far, took 182 and 62 us, but lost
 // bits of the values beside a page of a larger scale that a row does not see or
@@ -65,8 +65,8 @@ constexpr int kPwCost = 3;                // what an item's beginning and end ta
 constexpr float kPwRescale = 8.f;         // m and m + u follow their maxima where these have grown by more than this
 constexpr float kPwFar = 40.f;            // binary orders between scales of values that one sum of weights is taken over
 // Registers of the first four warps, the softmax's, and those that widen values: with 72, 168, 104 a chunk of 512 behind 30001 keys
-// takes 192 us, with these 188; with 80, 168, 96 the last have some of theirs in memory.
-constexpr int kPwRegsIo = 64, kPwRegsSoftmax = 168, kPwRegsOut = 112;
+// takes 192 us, with 64, 168, 112 189, with these 187; with 80, 168, 96 the last have most of theirs in memory.
+constexpr int kPwRegsIo = 56, kPwRegsSoftmax = 168, kPwRegsOut = 120;
 static_assert(kPwRegsIo + 2 * kPwRegsSoftmax + kPwRegsOut <= 4 * 128, "the launch's registers");
 
 struct __align__(16) PwItem {
@@ -855,7 +855,6 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                 poison |= *reinterpret_cast<volatile int*>(&hd.queue[k % kPwQueue].poison);
                 const bool zero = !n || (!part && (ml.x == -INFINITY || pos < 0 || pos >= a.cap));
                 if (part && live) a.part_mlu[prow + t * kPwM + m] = make_float4(ml.x, ml.y, u_row, 0.f);
-                const float half = ex2_approx(0.5f * u_row), f = zero ? 0.f : half / ml.y;     // (scores all -inf: 0 / 0)
                 const unsigned store = __ballot_sync(kAll, live) >> (lane & 28);
                 const unsigned zeros = __ballot_sync(kAll, zero) >> (lane & 28);
                 const int row = part ? (t * kPwM + m) * (D * 4) : (tok * a.hq_s + g) * (D * 2);
@@ -882,6 +881,7 @@ __global__ void __launch_bounds__(kPwThreads, 1) paged_items_kernel(const __grid
                             if (store >> i & 1) *reinterpret_cast<uint4*>(base + to[i] + 64 * c) = u[i];
                     }
                 } else {
+                    const float half = ex2_approx(0.5f * u_row), f = zero ? 0.f : half / ml.y;       // (scores all -inf: 0 / 0)
                     uint32_t o[32];
                     if (n) tmem_ld32(col, o);
 #pragma unroll 1
